@@ -455,6 +455,107 @@ int spec_verify_run_noalloc(const void *logits, int logits_dtype, int vocab_size
  */
 int spec_verify_noalloc_last_error(uint32_t *err_word);
 
+/*
+ * Row operators: drawing tokens from rows of logits outside a verification, and the
+ * log-probabilities of tokens. They use no context and no scratch memory: the arguments are one
+ * struct, everything a call needs is in it, and calls may overlap on any streams. All pointers
+ * are device pointers of `device` (a CUDA ordinal; the stream belongs to it too), owned by the
+ * caller and valid until the stream reaches the end of the call. No allocation, no host
+ * synchronisation, capturable in a CUDA graph; the first call on a device looks the device up.
+ * Problems visible on the host return a status and launch nothing; 0 rows are SV_OK.
+ *   logits        num_rows rows of vocab_size elements of logits_dtype (SV_F32 / SV_BF16), row r
+ *                 at logits + r * logits_stride elements, logits_stride >= vocab_size; aligned to
+ *                 its elements (rows may start anywhere: a view of every third row, say)
+ *   vocab_size    1 to SV_ROWS_MAX_VOCAB (SV_ECAPACITY above)
+ * A logit that is NaN or -inf is never drawn, kept or listed. Where a row's largest logit L is
+ * +inf, the tokens at +inf share the probability.
+ */
+#define SV_ROWS_MAX_VOCAB 786432
+
+/*
+ * spec_verify_sample: one token of every row. With d_v = (l_v - L) * (1 / T) in binary32 (two
+ * roundings; 1 / T rounded and taken into the normal numbers' range; d = 0 at the maximum) and
+ * the binary32 exp of the conventions above, the weight of token v is the whole number
+ * W_v = rint(2^40 exp(d_v)). Kept are the tokens that
+ *   top_k     are at least the k-th largest logit (ties kept; k < 1 or k >= vocab_size: all),
+ *   top_p     and whose strictly larger tokens of those hold less than P of their W (P < 1,
+ *             taken as at least 1e-6; else all; the comparison in binary64),
+ *   min_p     and whose d_v >= ln M rounded to binary32 (M > 0, taken as at most 1; else all),
+ * the meaning top_k and top_p have in spec_verify_batch. The token is the first kept one, in
+ * index order, at which the running sum of W exceeds u Z (binary64; Z the kept sum; u below 0 or
+ * NaN counts as 0; the last kept token of positive weight where u >= 1). Sums of W are exact, so
+ * tokens follow bit for bit from these definitions. T <= 0 or NaN, or top_k == 1: the first of
+ * the largest logits. A row with nothing to keep gives token -1.
+ *   temperature, top_p, min_p  [num_rows] binary32, top_k [num_rows] int32, each or NULL (T = 1;
+ *                  no constraint)
+ *   uniforms       [num_rows] binary32 in [0, 1): the random numbers
+ *   tokens         [num_rows] int32 (out)
+ *   token_logprob  [num_rows] binary32 (out) or NULL: ln of the drawn token's probability among
+ *                  the kept ones (0 for a greedy row, -inf with token -1)
+ *   probs          row r at probs + r * probs_stride, vocab_size binary32 each (out) or NULL:
+ *                  the distribution drawn from, exp(d_v) 2^40 / Z of kept tokens, 0 elsewhere (a
+ *                  greedy row: 1 at its token); with probs_stride = vocab_size the draft_probs
+ *                  of spec_verify_run
+ */
+typedef struct spec_verify_sample_args {
+    const void *logits;
+    int64_t logits_stride;
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    const float *uniforms;
+    int32_t *tokens;
+    float *token_logprob;
+    float *probs;
+    int64_t probs_stride;
+    int32_t num_rows;
+    int32_t vocab_size;
+    int32_t logits_dtype;
+    int32_t device;
+} spec_verify_sample_args;
+
+int spec_verify_sample(const spec_verify_sample_args *args, void *cuda_stream);
+
+/*
+ * spec_verify_logprobs: of every row the log-probability and rank of one token and the num_top
+ * best tokens, over the whole vocabulary: ln p_v = (l_v - L) / T - ln sum exp((l_v - L) / T).
+ *   temperature    [num_rows] binary32 or NULL (1); a value that is not above 0 counts as 1
+ *   tokens         [num_rows] int32; or, with cu_num_draft, the `sampled` of a verification,
+ *                  [num_reqs, token_stride] int32 with token_stride = max_spec_len_this_batch + 1:
+ *                  row cu_num_draft[i] + i + j is then the row of sampled[i, j]; or NULL (only
+ *                  the best tokens, of every row). A token outside [0, vocab_size) (-1 behind
+ *                  a request's last token) leaves its row out: log-probability -inf, rank 0, ids
+ *                  -1; its logits are not read
+ *   cu_num_draft   [num_reqs + 1] int32 prefix sums of the draft lengths, or NULL
+ *   token_logprob, token_rank  [num_rows] (out), each or NULL: rank = 1 + the number of strictly
+ *                  larger logits
+ *   top_ids int32, top_logprobs binary32  [num_rows, num_top] (out): the largest logits from the
+ *                  first on, lowest index first on ties; -1 and -inf where a row has no more
+ *   num_top        0 to SV_MAX_TOP (SV_ECAPACITY above)
+ */
+#define SV_MAX_TOP 64
+typedef struct spec_verify_logprobs_args {
+    const void *logits;
+    int64_t logits_stride;
+    const float *temperature;
+    const int32_t *tokens;
+    const int32_t *cu_num_draft;
+    float *token_logprob;
+    int32_t *token_rank;
+    int32_t *top_ids;
+    float *top_logprobs;
+    int32_t token_stride;
+    int32_t num_reqs;
+    int32_t num_top;
+    int32_t num_rows;
+    int32_t vocab_size;
+    int32_t logits_dtype;
+    int32_t device;
+} spec_verify_logprobs_args;
+
+int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_stream);
+
 /* Release the context and its device memory. NULL is a no-op. */
 void spec_verify_free(spec_verify_ctx *ctx);
 

@@ -20,7 +20,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
 _INCLUDE = os.path.join(_ROOT, "include")
 _HEADER = os.path.join(_INCLUDE, "spec_verify.h")
-_SOURCES = [os.path.join(_PKG, "csrc", "spec_verify.cu"), os.path.join(_PKG, "csrc", "sv_device.cuh")]
+_UNITS = [os.path.join(_PKG, "csrc", f) for f in ("spec_verify.cu", "sv_rows.cu")]
+_SOURCES = [*_UNITS, os.path.join(_PKG, "csrc", "sv_device.cuh")]
 # SPEC_VERIFY_DEBUG_BOUNDS=1 in the environment selects the checked build (-DSV_DEBUG_BOUNDS): every
 # global load and store of the kernels is checked against the call's arrays, and an access
 # outside them is skipped and reported as SV_ERR_BOUNDS in the error word. For tests only.
@@ -30,12 +31,13 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libspecverify_debug.so")
 LIB_PATH = DEBUG_LIB_PATH if DEBUG_BOUNDS else RELEASE_LIB_PATH
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-shared", "-Xcompiler", "-fPIC", "-I" + _INCLUDE]
+              "-shared", "-Xcompiler", "-fPIC", "--threads", "2", "-I" + _INCLUDE]
 
 SV_OK, SV_EINVAL, SV_ECAPACITY, SV_EDTYPE, SV_ECUDA, SV_EDEVICE = 0, -1, -2, -3, -4, -5
 SV_F32, SV_BF16 = 0, 1
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 1, 2
 SV_MAX_SYNTHETIC = 64
+SV_ROWS_MAX_VOCAB, SV_MAX_TOP = 786432, 64
 
 
 class Batch(ctypes.Structure):
@@ -58,6 +60,32 @@ class Outputs(ctypes.Structure):
     _fields_ = [("sampled", ctypes.c_void_p), ("num_sampled", ctypes.c_void_p),
                 ("num_rejected", ctypes.c_void_p), ("row_max", ctypes.c_void_p),
                 ("row_sumexp", ctypes.c_void_p), ("row_argmax", ctypes.c_void_p)]
+
+
+class SampleArgs(ctypes.Structure):
+    """spec_verify_sample_args of include/spec_verify.h."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+                ("uniforms", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("token_logprob", ctypes.c_void_p), ("probs", ctypes.c_void_p),
+                ("probs_stride", ctypes.c_int64), ("num_rows", ctypes.c_int32),
+                ("vocab_size", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
+
+
+class LogprobsArgs(ctypes.Structure):
+    """spec_verify_logprobs_args of include/spec_verify.h."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("temperature", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("cu_num_draft", ctypes.c_void_p), ("token_logprob", ctypes.c_void_p),
+                ("token_rank", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+                ("top_logprobs", ctypes.c_void_p), ("token_stride", ctypes.c_int32),
+                ("num_reqs", ctypes.c_int32), ("num_top", ctypes.c_int32),
+                ("num_rows", ctypes.c_int32), ("vocab_size", ctypes.c_int32),
+                ("logits_dtype", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
 SV_ERR_BATCH, SV_ERR_COUNTS, SV_ERR_BOUNDS, SV_ERR_SELECT = 1, 2, 4, 8
 KERNELS = ("stats", "verify", "select")  # profiling slots (select: top-k / top-p calls)
 
@@ -95,7 +123,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool | None = None)
         return path
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=_PKG)
     os.close(fd)
-    cmd = [_nvcc(), *NVCC_FLAGS, *(["-DSV_DEBUG_BOUNDS"] if debug else []), "-o", tmp, _SOURCES[0]]
+    cmd = [_nvcc(), *NVCC_FLAGS, *(["-DSV_DEBUG_BOUNDS"] if debug else []), "-o", tmp, *_UNITS]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -169,6 +197,8 @@ def lib():
     L.spec_verify_run_noalloc.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, u64, u32, i32, i32,
                                           i32, vp, vp, vp, vp, vp, vp, vp]
     L.spec_verify_noalloc_last_error.argtypes = [ctypes.POINTER(u32)]
+    L.spec_verify_sample.argtypes = [ctypes.POINTER(SampleArgs), vp]
+    L.spec_verify_logprobs.argtypes = [ctypes.POINTER(LogprobsArgs), vp]
     L.spec_verify_reserve_host_io.argtypes = [vp]
     L.spec_verify_last_error.argtypes = [vp, ctypes.POINTER(u32)]
     L.spec_verify_set_profiling.argtypes = [vp, i32]
@@ -183,6 +213,7 @@ def lib():
               "spec_verify_run_batch", "spec_verify_set_synthetic", "spec_verify_synthetic_rates",
               "spec_verify_shard_stats", "spec_verify_shard_race", "spec_verify_shard_finish",
               "spec_verify_run_host", "spec_verify_run_noalloc", "spec_verify_noalloc_last_error",
+              "spec_verify_sample", "spec_verify_logprobs",
               "spec_verify_reserve_host_io", "spec_verify_last_error", "spec_verify_set_profiling",
               "spec_verify_get_profile", "spec_verify_set_chunks", "spec_verify_launches_per_run"):
         getattr(L, f).restype = i32
@@ -359,6 +390,16 @@ def spec_verify_noalloc_last_error() -> int:
     return w.value
 
 
+def spec_verify_sample(args: SampleArgs, cuda_stream=None) -> None:
+    _check(lib().spec_verify_sample(ctypes.byref(args), _stream_handle(cuda_stream)),
+           "spec_verify_sample")
+
+
+def spec_verify_logprobs(args: LogprobsArgs, cuda_stream=None) -> None:
+    _check(lib().spec_verify_logprobs(ctypes.byref(args), _stream_handle(cuda_stream)),
+           "spec_verify_logprobs")
+
+
 def spec_verify_reserve_host_io(ctx) -> None:
     _check(lib().spec_verify_reserve_host_io(ctx), "spec_verify_reserve_host_io")
 
@@ -395,6 +436,146 @@ def spec_verify_free(ctx) -> None:
 
 def spec_verify_status_string(status: int) -> str:
     return _status_string(status)
+
+
+# ---- row operators -------------------------------------------------------------------------
+
+def _row_matrix(name, t, dtypes, shape, device):
+    """A 2-d device tensor whose rows are contiguous (any row stride), checked."""
+    if t.dim() != 2 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    rows, cols = shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _row_array(name, t, dtype, shape, device):
+    """Address of a contiguous device tensor of this shape (None stays None), checked."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_of(logits):
+    """(dtype code, rows, vocabulary, address, stride) of the logits of a row operator."""
+    import torch
+
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab_size]")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported logits dtype {logits.dtype}")
+    rows, vocab = logits.shape
+    ptr, stride = _row_matrix("logits", logits, (logits.dtype,), (rows, vocab), logits.device)
+    return SV_BF16 if logits.dtype == torch.bfloat16 else SV_F32, rows, vocab, ptr, stride
+
+
+def _row_outputs(out, want, device):
+    """The output tensors (name, dtype, shape): those given, one for each, or new ones."""
+    import torch
+
+    if out is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for _, dtype, shape in want]
+    if len(out) != len(want):
+        raise ValueError("out must hold " + ", ".join(name for name, _, _ in want))
+    return list(out)
+
+
+def sample(logits, uniforms, temperature=None, *, top_k=None, top_p=None, min_p=None,
+           logprob: bool = False, probs: bool = False, out=None, stream=None):
+    """Draw one token of every row of logits ([rows, vocab_size] bfloat16 or float32, rows
+    contiguous) by the given uniform numbers ([rows] float32 in [0, 1)): softmax at the
+    temperature, of the tokens that top_k ([rows] int32), top_p and min_p ([rows] float32) keep,
+    each None for no such constraint; the exact rules stand at spec_verify_sample in
+    include/spec_verify.h. Temperature 0 or top_k 1 takes the largest logit.
+
+    Returns (tokens int32 [rows]), with logprob=True also the tokens' log-probabilities, and with
+    probs=True also the distributions they were drawn from, [rows, vocab_size] float32, which
+    SpecVerify.run takes as draft_probs. out: tensors to write instead of new ones, in that
+    order (the distributions' rows may be further apart than vocab_size). Runs on the logits'
+    device, on `stream` or that device's current stream; no scratch memory, so calls may overlap.
+    """
+    import torch
+
+    dtype, rows, vocab, ptr, stride = _rows_of(logits)
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    want = [("tokens", i32, (rows,))]
+    if logprob:
+        want.append(("logprob", f32, (rows,)))
+    if probs:
+        want.append(("probs", f32, (rows, vocab)))
+    got = _row_outputs(out, want, dev)
+    pp, pstride = _row_matrix("probs", got[-1], (f32,), (rows, vocab), dev) if probs else (None, 0)
+    args = SampleArgs(ptr, stride, _row_array("temperature", temperature, f32, (rows,), dev),
+                      _row_array("top_k", top_k, i32, (rows,), dev),
+                      _row_array("top_p", top_p, f32, (rows,), dev),
+                      _row_array("min_p", min_p, f32, (rows,), dev),
+                      _row_array("uniforms", uniforms, f32, (rows,), dev),
+                      _row_array("tokens", got[0], i32, (rows,), dev),
+                      _row_array("logprob", got[1], f32, (rows,), dev) if logprob else None,
+                      pp, pstride, rows, vocab, dtype, dev.index)
+    spec_verify_sample(args, torch.cuda.current_stream(dev) if stream is None else stream)
+    return tuple(got)
+
+
+def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_draft=None,
+             out=None, stream=None):
+    """Log-probabilities over the whole vocabulary of rows of logits ([rows, vocab_size] bfloat16
+    or float32, rows contiguous), at temperature 1 or the given one ([rows] float32).
+
+    tokens: [rows] int32, or with cu_num_draft ([num_reqs + 1] int32) the `sampled`
+    [num_reqs, max_spec_len + 1] of a verification whose target logits these are. Returns
+    (log-probability float32, rank int32: 1 + the number of larger logits), both [rows], and with
+    num_top also the best tokens and their log-probabilities, [rows, num_top]; only these two
+    where tokens is None. A row whose token is outside the vocabulary (the -1 behind a request's
+    last token) is left out: -inf, 0, -1, -inf. out: tensors to write instead of new ones, in that
+    order. Runs on the logits' device, on `stream` or that device's current stream; no scratch
+    memory, so calls may overlap."""
+    import torch
+
+    dtype, rows, vocab, ptr, stride = _rows_of(logits)
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    if not 0 <= num_top <= SV_MAX_TOP:
+        raise ValueError(f"num_top must be in [0, {SV_MAX_TOP}]")
+    if tokens is None and (num_top == 0 or cu_num_draft is not None):
+        raise ValueError("without tokens, num_top best tokens of every row are all there is")
+    want = [("logprob", f32, (rows,)), ("rank", i32, (rows,))] if tokens is not None else []
+    if num_top:
+        want += [("top_ids", i32, (rows, num_top)), ("top_logprobs", f32, (rows, num_top))]
+    got = _row_outputs(out, want, dev)
+    at = [_row_array(name, t, d, shape, dev) for t, (name, d, shape) in zip(got, want)]
+    if tokens is None:
+        at = [None, None, *at]
+    elif not num_top:
+        at += [None, None]
+    num_reqs = width = 0
+    if cu_num_draft is not None:
+        num_reqs = cu_num_draft.numel() - 1
+        if tokens.dim() != 2 or tokens.shape[0] != num_reqs or num_reqs < 1 or tokens.shape[1] < 1:
+            raise ValueError("with cu_num_draft, tokens must be [num_reqs, max_spec_len + 1]")
+        width = tokens.shape[1]
+    args = LogprobsArgs(ptr, stride, _row_array("temperature", temperature, f32, (rows,), dev),
+                        _row_array("tokens", tokens, i32, (num_reqs, width) if width else (rows,), dev),
+                        _row_array("cu_num_draft", cu_num_draft, i32, (num_reqs + 1,), dev),
+                        *at, width, num_reqs, num_top, rows, vocab, dtype, dev.index)
+    spec_verify_logprobs(args, torch.cuda.current_stream(dev) if stream is None else stream)
+    return tuple(got)
 
 
 # ---- convenience owner ---------------------------------------------------------------------
