@@ -470,7 +470,7 @@ int spec_verify_noalloc_last_error(uint32_t *err_word);
  * A logit that is NaN or -inf is never drawn, kept or listed. Where a row's largest logit L is
  * +inf, the tokens at +inf share the probability.
  */
-#define SV_ROWS_MAX_VOCAB 786432
+#define SV_ROWS_MAX_VOCAB 524288
 
 /*
  * spec_verify_sample: one token of every row. With d_v = (l_v - L) * (1 / T) in binary32 (two

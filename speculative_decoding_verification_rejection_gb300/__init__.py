@@ -37,7 +37,7 @@ SV_OK, SV_EINVAL, SV_ECAPACITY, SV_EDTYPE, SV_ECUDA, SV_EDEVICE = 0, -1, -2, -3,
 SV_F32, SV_BF16 = 0, 1
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 1, 2
 SV_MAX_SYNTHETIC = 64
-SV_ROWS_MAX_VOCAB, SV_MAX_TOP = 786432, 64
+SV_ROWS_MAX_VOCAB, SV_MAX_TOP = 524288, 64
 
 
 class Batch(ctypes.Structure):

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <cstdint>
@@ -23,18 +24,90 @@
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr float kInf = __builtin_huge_valf();
-constexpr unsigned long long kOne = 1ull << 40;  // the weight of a row's largest logit
-
 using u64 = unsigned long long;
 
-__device__ __forceinline__ float elem(const float *p, long long k) { return __ldg(p + k); }
-__device__ __forceinline__ float elem(const uint16_t *p, long long k)
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kList = 1024;       // entries of the leader's candidate list
+constexpr int kStages = 4;        // portions in which a warp waits for its logits
+constexpr int kCutBins = 256;     // bins of the cut search: one for each thread
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kLog2e = 0x1.715476p+0f;
+constexpr int kTopP = 128;        // lane maxima that the cut for top-p alone is to reach
+constexpr u64 kNone64 = ~0ull;
+
+// ---------------------------------------------------------------------------------------
+// thread-block clusters and asynchronous copies
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ unsigned smem_addr(const void *p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ unsigned cluster_rank()
 {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p + k)) << 16);
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
+// Every thread of every CTA of the cluster; what was written before (shared memory of any CTA of
+// the cluster, global memory) is visible after.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive();
+    cluster_wait();
+}
+// Address of p, of this CTA's shared memory, in that of CTA `rank`.
+__device__ __forceinline__ unsigned remote(const void *p, unsigned rank)
+{
+    unsigned a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void put(unsigned a, unsigned v) { asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void put(unsigned a, u64 v) { asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory"); }
+
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+
+// ---------------------------------------------------------------------------------------
+// logits and weights
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ float as_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ float as_float(float f) { return f; }
+template <typename T> struct Low;  // -inf in the logits' type
+template <> struct Low<uint16_t> { static __device__ __forceinline__ uint16_t value() { return 0xFF80u; } };
+template <> struct Low<float> { static __device__ __forceinline__ float value() { return -kInf; } };
+
+// The logits of a 16-byte vector as binary32.
+template <typename T> struct Vec;
+template <> struct Vec<uint16_t> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void get(const uint4 &v, float (&f)[8])
+    {
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void get(const uint4 &v, float (&f)[4])
+    {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+};
 
 // Logits as order-preserving unsigned integers, 0 for what is never kept (NaN and -inf); -0 as +0.
 __device__ __forceinline__ unsigned key_of(float l)
@@ -43,39 +116,75 @@ __device__ __forceinline__ unsigned key_of(float l)
     const unsigned b = __float_as_uint(__fadd_rn(l, 0.0f));
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+__device__ __forceinline__ float of_key(unsigned k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
 
 // 1 / T as a normal number: an infinite T then gives a difference that overflowed a d of -inf, not
 // of 0 times infinity, and a tiny T a finite factor for the differences that are 0.
 __device__ __forceinline__ float inverse(float T) { return fminf(fmaxf(__frcp_rn(T), FLT_MIN), FLT_MAX); }
 
-// d of a logit that is not NaN or -inf: 0 at the maximum (also where that is infinite).
-__device__ __forceinline__ float delta(float l, float L, float inv)
+// d of a logit, L finite (a row with L = +inf is rewritten first); NaN for a NaN.
+__device__ __forceinline__ float delta(float l, float L, float inv) { return __fmul_rn(__fsub_rn(l, L), inv); }
+
+// sv::exp_f32 for d <= 0 where only the weight is wanted: below -32 a weight is 0 anyway, and so
+// is that of a NaN or -inf, which the maximum takes to -32. The same operations otherwise; the
+// factor 2^k goes into the exponent, which stays that of a normal number.
+__device__ __forceinline__ float exp_weight(float d)
 {
-    return l == L ? 0.0f : __fmul_rn(__fsub_rn(l, L), inv);
+    d = fmaxf(d, -32.0f);
+    const float shifter = 0x1.8p+23f;
+    const float ks = __fmaf_rn(d, 0x1.715476p+0f, shifter);
+    const float kf = __fsub_rn(ks, shifter);
+    float r = __fmaf_rn(-kf, 0x1.62e430p-1f, d);
+    r = __fmaf_rn(-kf, -0x1.05c610p-29f, r);
+    float p = 0x1.a01a02p-13f;
+    p = __fmaf_rn(p, r, 0x1.6c16c2p-10f);
+    p = __fmaf_rn(p, r, 0x1.111112p-7f);
+    p = __fmaf_rn(p, r, 0x1.555556p-5f);
+    p = __fmaf_rn(p, r, 0x1.555556p-3f);
+    p = __fmaf_rn(p, r, 0.5f);
+    p = __fmaf_rn(p, r, 1.0f);
+    p = __fmaf_rn(p, r, 1.0f);
+    return __uint_as_float(__float_as_uint(p) + (__float_as_uint(ks) << 23));
 }
 
 __device__ __forceinline__ u64 weight(float t) { return static_cast<u64>(__float2ll_rn(t * 0x1p+40f)); }
 
+// An exact sum of weights in two 32-bit words. Adding 12 to t in [0, 1] rounds it to a multiple of
+// 2^-20, whose count the low mantissa bits then hold; what that left, at most 2^-21, is rounded to
+// a multiple of 2^-40 by adding 1.5 2^-17 in the same way. Together they are rint(t 2^40), ties as
+// rint's. The words add the bit patterns; the constant parts come off at the end. Good for up to
+// 4095 weights.
+struct WeightSum {
+    unsigned a = 0, b = 0;
+    __device__ __forceinline__ void add(float t)
+    {
+        const float x = __fadd_rn(t, 12.0f);
+        const float lo = __fsub_rn(t, __fsub_rn(x, 12.0f));
+        a += __float_as_uint(x);
+        b += __float_as_uint(__fadd_rn(lo, 0x1.8p-17f));
+    }
+    __device__ __forceinline__ u64 total(int n) const  // n: how many were added
+    {
+        const unsigned hi = a - static_cast<unsigned>(n) * __float_as_uint(12.0f);
+        const int lo = static_cast<int>(b - static_cast<unsigned>(n) * __float_as_uint(0x1.8p-17f));
+        return (static_cast<u64>(hi) << 20) + static_cast<u64>(static_cast<long long>(lo));
+    }
+};
+
 // ---------------------------------------------------------------------------------------
-// block reductions (every thread calls them; `box` is shared memory for one value per warp + 1)
+// warp and block reductions (block-wide ones by every thread)
 // ---------------------------------------------------------------------------------------
-template <typename V, typename F>
-__device__ V block_reduce(V v, V *box, F join)
+__device__ __forceinline__ u64 warp_sum(u64 v)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int s = 16; s; s >>= 1) v = join(v, __shfl_xor_sync(0xFFFFFFFFu, v, s));
-    __syncthreads();
-    if (lane == 0) box[warp] = v;
-    __syncthreads();
-    v = box[0];
-    for (int w = 1; w < kWarps; ++w) v = join(v, box[w]);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
     return v;
 }
-
-template <typename V>
-__device__ V block_sum(V v, V *box)
+__device__ __forceinline__ float warp_max(float v)
 {
-    return block_reduce(v, box, [](V a, V b) { return a + b; });
+#pragma unroll
+    for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, s));
+    return v;
 }
 
 // Exclusive prefix sum over the block's threads; *all: the total.
@@ -83,6 +192,7 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 s = v;
+#pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
         const u64 o = __shfl_up_sync(0xFFFFFFFFu, s, k);
         if (lane >= k) s += o;
@@ -91,6 +201,7 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
     if (lane == 31) box[warp] = s;
     __syncthreads();
     u64 before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += box[w];
         total += box[w];
@@ -99,170 +210,659 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
     return before + s - v;
 }
 
+// ---------------------------------------------------------------------------------------
+// a row over a cluster
+// ---------------------------------------------------------------------------------------
+// The 16-byte vectors that hold the row are split evenly over the cluster's CTAs and then over
+// their warps, both in contiguous runs, so that the warps in order hold the row in index order; a
+// lane copies the vectors lane, lane + 32, ... of its warp's run to shared memory and is the
+// one to read them again, so no barrier stands between copy and use. Everything that follows
+// reads shared memory: each logit crosses the memory bus once. What of the first and last vector
+// lies outside the row is -inf; those two are copied element by element.
+struct Shared {
+    unsigned bin[kCutBins];
+    u64 box[kWarps];
+    u64 seg[2][kMaxCluster * kWarps];  // a value of every warp of the cluster (two, used in turn)
+    unsigned count[kMaxCluster];       // candidates of every CTA
+    u64 listed[kMaxCluster];           // their weight
+    unsigned mine;                     // candidates of this CTA
+    unsigned cut;
+    int first, found;
+    u64 below;
+    float d;
+};
+
+struct Split {
+    int per_cta, per_warp;  // vectors
+};
+
+template <typename T>
+struct Row {
+    static constexpr int n = Vec<T>::n;
+    const uint4 *vec;  // this CTA's vectors in shared memory
+    int base;          // index in the row of its first vector's first element (may be negative)
+    int lo, hi;        // this warp's vectors
+    int V;
+    int lane, warp;
+
+    __device__ __forceinline__ float at(int i) const  // element i of the row, one of this CTA's
+    {
+        return as_float(reinterpret_cast<const T *>(vec)[i - base]);
+    }
+    __device__ __forceinline__ int first() const { return max(base, 0); }
+    __device__ __forceinline__ int last(int per_cta) const { return min(base + per_cta * n, V); }
+};
+
+// Starts the copies of this CTA's part of the row at `row`.
+template <typename T>
+__device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp, uint4 *store, unsigned rank)
+{
+    constexpr int n = Vec<T>::n;
+    Row<T> R;
+    R.lane = threadIdx.x & 31;
+    R.warp = threadIdx.x >> 5;
+    R.V = V;
+    R.vec = store;
+    const auto address = reinterpret_cast<uintptr_t>(row);
+    const int off = static_cast<int>((address & 15u) / sizeof(T));
+    const int vectors = (off + V + n - 1) / n;
+    const int v0 = static_cast<int>(rank) * sp.per_cta;
+    const int mine = max(min(sp.per_cta, vectors - v0), 0);
+    R.base = v0 * n - off;
+    R.lo = min(R.warp * sp.per_warp, mine);
+    R.hi = min(R.lo + sp.per_warp, mine);
+    const auto *src = reinterpret_cast<const uint4 *>(address & ~static_cast<uintptr_t>(15)) + v0;
+    const int step = ((R.hi - R.lo + 31) / 32 + kStages - 1) / kStages * 32;
+    int j = R.lo + R.lane;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+        const int end = min(R.lo + (s + 1) * step, R.hi);
+        for (; j < end; j += 32) {
+            const int i = R.base + j * n;
+            if (i >= 0 && i + n <= V) {
+                copy16(store + j, src + j);
+            } else {
+#pragma unroll
+                for (int e = 0; e < n; ++e)
+                    reinterpret_cast<T *>(store + j)[e] = i + e >= 0 && i + e < V ? __ldg(row + i + e) : Low<T>::value();
+            }
+        }
+        copy_commit();
+    }
+    return R;
+}
+
+// Calls f(vector number) for this lane's vectors as they arrive.
+template <typename T, typename F>
+__device__ __forceinline__ void as_they_come(const Row<T> &R, F f)
+{
+    const int step = ((R.hi - R.lo + 31) / 32 + kStages - 1) / kStages * 32;
+    int j = R.lo + R.lane;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+        if (s == 0) copy_wait<kStages - 1>();
+        if (s == 1) copy_wait<kStages - 2>();
+        if (s == 2) copy_wait<kStages - 3>();
+        if (s == 3) copy_wait<0>();
+        const int end = min(R.lo + (s + 1) * step, R.hi);
+        for (; j < end; j += 32) f(j);
+    }
+}
+static_assert(kStages == 4, "as_they_come waits for four portions");
+
+template <typename T>
+__device__ __forceinline__ float lane_max(const Row<T> &R)
+{
+    float m = -kInf;
+    as_they_come(R, [&](int j) {
+        float f[Row<T>::n];
+        Vec<T>::get(R.vec[j], f);
+#pragma unroll
+        for (int e = 0; e < Row<T>::n; ++e) m = fmaxf(m, f[e]);  // (a NaN loses)
+    });
+    return m;
+}
+
+// A cut that at least `want` of the cluster's lane maxima reach, or the lowest finite number where there
+// are not so many: the maxima are counted in kCutBins equal bins from the largest, L, down to the smallest.
+// The tokens at or above it are then few more than the lanes that reach it, as a rule, and hold the
+// `want` largest of the row.
+__device__ float cut_for(const float *peaks, int count, float L, int want, Shared &sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float low = L;
+    for (int i = tid; i < count; i += kThreads) {
+        const float p = peaks[i];
+        if (p > -kInf) low = fminf(low, p);
+    }
+    low = -warp_max(-low);
+    sh.bin[tid] = 0;
+    if (lane == 0) reinterpret_cast<float *>(sh.box)[warp] = low;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) low = fminf(low, reinterpret_cast<float *>(sh.box)[w]);
+    // (a spread that overflows, of masks at the lowest value, gives the scale 0: one bin)
+    const float scale = L > low ? (kCutBins - 1) / (L - low) : 0.0f;
+    for (int i = tid; i < count; i += kThreads) {
+        const float p = peaks[i];
+        if (p > -kInf) atomicAdd(&sh.bin[min(static_cast<int>((L - p) * scale), kCutBins - 1)], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {  // the first bin up to which `want` are counted
+        unsigned c[kCutBins / 32], s = 0;
+#pragma unroll
+        for (int i = 0; i < kCutBins / 32; ++i) s += c[i] = sh.bin[lane * (kCutBins / 32) + i];
+        unsigned upto = s;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const unsigned o = __shfl_up_sync(0xFFFFFFFFu, upto, k);
+            if (lane >= k) upto += o;
+        }
+        const unsigned reach = __ballot_sync(0xFFFFFFFFu, upto >= static_cast<unsigned>(want));
+        if (reach == 0) {
+            if (lane == 0) sh.cut = kCutBins;
+        } else if (lane == __ffs(reach) - 1) {
+            unsigned run = upto - s;
+            int i = 0;
+            while (i < kCutBins / 32 - 1 && (run += c[i]) < static_cast<unsigned>(want)) ++i;
+            sh.cut = lane * (kCutBins / 32) + i;
+        }
+    }
+    __syncthreads();
+    if (sh.cut == kCutBins) return -FLT_MAX;
+    if (sh.cut == kCutBins - 1 || scale == 0.0f) return low;
+    // the lower edge of that bin, moved down by more than the roundings of the bin numbers
+    const float width = (L - low) / (kCutBins - 1);
+    return L - (static_cast<float>(sh.cut) + 1.0f) * width - 4e-6f * fmaxf(fabsf(L), fabsf(low));
+}
+
+// ---------------------------------------------------------------------------------------
+// sampling
+// ---------------------------------------------------------------------------------------
 struct SampleParams {
     long long stride, probs_stride;
     const float *temperature, *top_p, *min_p, *uniforms;
     const int32_t *top_k;
     int32_t *tokens;
     float *logprob, *probs;
-    int V;
+    int V, cluster;
+    Split split;
 };
 
-struct Shared {
-    u64 box[kWarps + 1];
-    u64 bin[256];
-    unsigned cnt[256];
-    int token;
-    unsigned digit;
-    u64 rest;
-    float d;
+// What is kept, besides key_of(l) != 0: l >= tau and d >= low.
+struct Kept {
+    float L, inv, tau, low;
 };
 
-// The largest key such that the keys at least as large hold `need` tokens (kMass false) or the
-// weight `need` (compared in binary64), among keys >= floor: four passes of eight bits.
-template <typename T, bool kMass>
-__device__ unsigned select_key(const T *row, int V, float L, float inv, unsigned floor, double need, Shared &sh)
+// Lanes whose maximum reaches the cut put their tokens at or above it into the leader's list, as
+// (key, ~index), into this CTA's part of it; their number goes to every CTA. Entries past the
+// part's end are only counted.
+template <typename T>
+__device__ __forceinline__ void collect(const Row<T> &R, float peak, float cut, u64 *list, int part, unsigned rank,
+                                        int cluster, Shared &sh)
+{
+    constexpr int n = Row<T>::n;
+    if (threadIdx.x == 0) sh.mine = 0;
+    __syncthreads();
+    if (peak >= cut) {
+        const unsigned to = remote(list + rank * part, 0);
+        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+            float f[n];
+            Vec<T>::get(R.vec[j], f);
+#pragma unroll
+            for (int e = 0; e < n; ++e)
+                if (f[e] >= cut) {
+                    const unsigned at = atomicAdd(&sh.mine, 1u);
+                    const auto index = static_cast<unsigned>(R.base + j * n + e);
+                    if (at < static_cast<unsigned>(part))
+                        put(to + at * 8u, (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index));
+                }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < cluster) put(remote(&sh.count[rank], threadIdx.x), sh.mine);
+}
+
+// The leader's list closed up (parts of `part` entries, count[c] of them used), padded with zeros
+// to a power of two, the largest entry first. Returns the padded length.
+__device__ int close_and_sort(u64 *list, int part, int cluster, const unsigned *count)
 {
     const int tid = threadIdx.x;
-    unsigned prefix = 0;
-    u64 above = 0;  // held by the keys above the current prefix's interval
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        __syncthreads();
-        if (tid < 256) sh.bin[tid] = 0;
-        __syncthreads();
-        for (int v = tid; v < V; v += kThreads) {
-            const float l = elem(row, v);
-            const unsigned key = key_of(l);
-            if (key == 0 || key < floor || (shift < 24 && (key >> (shift + 8)) != prefix)) continue;
-            const u64 w = kMass ? weight(sv::exp_f32(delta(l, L, inv))) : 1ull;
-            if (w) atomicAdd(&sh.bin[(key >> shift) & 255u], w);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            u64 s = above;
-            int b = 255;
-            for (; b > 0; --b) {
-                if (static_cast<double>(s + sh.bin[b]) >= need) break;
-                s += sh.bin[b];
+    int total = 0;
+    u64 mine[kList / kThreads];
+    int at[kList / kThreads];
+#pragma unroll
+    for (int q = 0; q < kList / kThreads; ++q) at[q] = -1;
+    for (int c = 0; c < cluster; ++c) {
+        const int n = static_cast<int>(count[c]);
+#pragma unroll
+        for (int q = 0; q < kList / kThreads; ++q) {
+            const int i = tid + q * kThreads - c * part;
+            if (i >= 0 && i < n) {
+                mine[q] = list[tid + q * kThreads];
+                at[q] = total + i;
             }
-            sh.digit = static_cast<unsigned>(b);
-            sh.rest = s;
         }
-        __syncthreads();
-        prefix = (prefix << 8) | sh.digit;
-        above = sh.rest;
+        total += n;
     }
-    return prefix;
+    int size = 1;
+    while (size < total) size *= 2;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kList / kThreads; ++q)
+        if (at[q] >= 0) list[at[q]] = mine[q];
+    for (int i = total + tid; i < size; i += kThreads) list[i] = 0;
+    __syncthreads();
+    return size;
+}
+
+// Bitonic sort of `size` (a power of two) entries, the largest first.
+__device__ void sort_down(u64 *list, int size)
+{
+    for (int run = 2; run <= size; run *= 2)
+        for (int step = run / 2; step > 0; step /= 2) {
+            for (int p = threadIdx.x; p < size / 2; p += kThreads) {
+                const int i = 2 * p - (p & (step - 1));
+                const u64 a = list[i], b = list[i + step];
+                if ((a < b) == ((i & run) == 0)) {
+                    list[i] = b;
+                    list[i + step] = a;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+// Whether a running sum of weights has passed the uniform number's place in the total.
+struct Target {
+    double at;
+    u64 Z;
+    __device__ __forceinline__ Target(float u, u64 Z_) : at(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(Z_)), Z(Z_) {}
+    __device__ __forceinline__ bool passed(u64 c) const { return static_cast<double>(c) > at || c == Z; }
+};
+
+__device__ __forceinline__ float log_prob(float d, u64 Z)
+{
+    return static_cast<float>(static_cast<double>(d) - log(static_cast<double>(Z) * 0x1p-40));
+}
+
+// The leader's work where its list holds every token that can be kept: the sorted list's weights
+// are summed up, the three constraints cut it off, and what is left is put in index order and
+// summed again for the draw.
+template <typename T>
+__device__ void finish_list(const SampleParams &P, const T *row, long long r, u64 *list, u64 *sums, int part, int k,
+                            float p, u64 Z, float u, const Kept &keep, Shared &sh)
+{
+    const int tid = threadIdx.x;
+    int size = close_and_sort(list, part, P.cluster, sh.count);
+    sort_down(list, size);
+    const int q = (size + kThreads - 1) / kThreads;  // contiguous entries of a thread
+    u64 own = 0, all;
+    auto weight_of = [&](u64 entry) {
+        const auto key = static_cast<unsigned>(entry >> 32);
+        return key ? weight(exp_weight(delta(of_key(key), keep.L, keep.inv))) : 0ull;
+    };
+    for (int i = tid * q; i < min(tid * q + q, size); ++i) own += weight_of(list[i]);
+    u64 run = block_scan(own, sh.box, &all);
+    int valid = size;
+    for (int i = tid * q; i < min(tid * q + q, size); ++i) {
+        run += weight_of(list[i]);
+        sums[i] = run;  // up to and with entry i
+        if (list[i] == 0) valid = min(valid, i);
+    }
+    if (tid == 0) {
+        sh.first = size;
+        sh.found = size;
+    }
+    __syncthreads();
+    atomicMin(&sh.first, valid);
+    __syncthreads();
+    valid = sh.first;
+    int kept = valid;
+    if (k > 0 && k < valid) {
+        const auto kth = static_cast<unsigned>(list[k - 1] >> 32);
+        for (int i = tid; i < valid; i += kThreads)
+            if (static_cast<unsigned>(list[i] >> 32) < kth) atomicMin(&sh.found, i);
+        __syncthreads();
+        kept = min(kept, sh.found);
+        __syncthreads();
+    }
+    const double need = static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(k > 0 ? sums[kept - 1] : Z);
+    for (int i = tid; i < kept; i += kThreads) {
+        const auto key = static_cast<unsigned>(list[i] >> 32);
+        bool out = delta(of_key(key), keep.L, keep.inv) < keep.low;
+        if (p < 1.0f && i > 0 && key != static_cast<unsigned>(list[i - 1] >> 32))
+            out |= !(static_cast<double>(sums[i - 1]) < need);
+        if (out) atomicMin(&sh.found, i);
+    }
+    __syncthreads();
+    kept = min(kept, sh.found);
+    const u64 Zk = sums[kept - 1];
+    if (P.probs) {
+        float *probs = P.probs + r * P.probs_stride;
+        const float z = static_cast<float>(static_cast<double>(Zk) * 0x1p-40);
+        for (int i = tid; i < kept; i += kThreads) {
+            const u64 e = list[i];
+            probs[static_cast<int>(~static_cast<unsigned>(e))] =
+                __fdiv_rn(sv::exp_f32(delta(of_key(static_cast<unsigned>(e >> 32)), keep.L, keep.inv)), z);
+        }
+    }
+    __syncthreads();
+    // index order: (~index, place) the largest first
+    size = 1;
+    while (size < kept) size *= 2;
+    for (int i = tid; i < size; i += kThreads)
+        list[i] = i < kept ? (list[i] << 32) | static_cast<unsigned>(i) : 0;
+    __syncthreads();
+    sort_down(list, size);
+    const int qk = (size + kThreads - 1) / kThreads;
+    auto weight_at = [&](int i) {
+        const auto place = static_cast<unsigned>(list[i]);
+        return sums[place] - (place ? sums[place - 1] : 0);
+    };
+    own = 0;
+    for (int i = tid * qk; i < min(tid * qk + qk, kept); ++i) own += weight_at(i);
+    run = block_scan(own, sh.box, &all);
+    const Target target(u, Zk);
+    for (int i = tid * qk; i < min(tid * qk + qk, kept); ++i) {
+        const u64 next = run + weight_at(i);
+        if (target.passed(next) && !target.passed(run)) {
+            const int token = static_cast<int>(~static_cast<unsigned>(list[i] >> 32));
+            P.tokens[r] = token;
+            const float l = as_float(__ldg(row + token));
+            if (P.logprob) P.logprob[r] = log_prob(l == kInf ? 0.0f : delta(l, keep.L, keep.inv), Zk);
+        }
+        run = next;
+    }
+}
+
+template <typename T, bool kAll>
+__device__ __forceinline__ float kept_weight(float l, const Kept &keep)
+{
+    const float d = delta(l, keep.L, keep.inv);
+    const float t = exp_weight(d);
+    return kAll || (l >= keep.tau && d >= keep.low) ? t : 0.0f;
+}
+
+// This warp's sum of the kept tokens' weights.
+template <typename T, bool kAll>
+__device__ __forceinline__ u64 warp_weight(const Row<T> &R, const Kept &keep)
+{
+    constexpr int n = Row<T>::n;
+    WeightSum s;
+    int count = 0;
+    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        float f[n];
+        Vec<T>::get(R.vec[j], f);
+#pragma unroll
+        for (int e = 0; e < n; ++e) s.add(kept_weight<T, kAll>(f[e], keep));
+        count += n;
+    }
+    return warp_sum(s.total(count));
+}
+
+// A value of every warp to every CTA of the cluster (`turn` alternates between the two buffers:
+// a CTA that writes one again has passed a barrier that the others reach only after reading it).
+struct Exchange {
+    Shared &sh;
+    unsigned rank;
+    int cluster, turn;
+    __device__ __forceinline__ const u64 *all(u64 mine)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        u64 *to = sh.seg[turn & 1];
+        ++turn;
+        if (lane < cluster) put(remote(to + rank * kWarps + warp, lane), mine);
+        cluster_sync();
+        return to;
+    }
+    __device__ u64 sum(u64 mine)
+    {
+        const u64 *v = all(mine);
+        u64 s = 0;
+        for (int i = threadIdx.x & 31; i < cluster * kWarps; i += 32) s += v[i];
+        return warp_sum(s);
+    }
+};
+
+// The largest key such that the keys at least as large, of those from `floor` on, hold `need`
+// tokens or, with kMass, the weight `need`: bit by bit, one pass over the row for each.
+template <typename T, bool kMass>
+__device__ unsigned search_key(const Row<T> &R, const Kept &keep, unsigned floor, double need, Exchange &ex)
+{
+    constexpr int n = Row<T>::n;
+    unsigned found = 0;
+    for (unsigned bit = 0x80000000u; bit; bit >>= 1) {
+        const unsigned trial = max(found | bit, floor);
+        u64 m = 0;
+        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+            float f[n];
+            Vec<T>::get(R.vec[j], f);
+#pragma unroll
+            for (int e = 0; e < n; ++e)
+                if (key_of(f[e]) >= trial) m += kMass ? weight(exp_weight(delta(f[e], keep.L, keep.inv))) : 1ull;
+        }
+        if (static_cast<double>(ex.sum(warp_sum(m))) >= need) found |= bit;
+    }
+    return max(found, floor);
+}
+
+// The draw over the whole row: every warp's sum of kept weights goes to every CTA, the CTA that
+// holds the warp's run on which the uniform number falls finds the token in it, and each
+// writes its part of the distribution.
+template <typename T, bool kAll>
+__device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, float u, const Kept &keep, Exchange &ex)
+{
+    constexpr int n = Row<T>::n;
+    Shared &sh = ex.sh;
+    const int tid = threadIdx.x, lane = tid & 31, warps = P.cluster * kWarps;
+    const u64 *seg = ex.all(warp_weight<T, kAll>(R, keep));
+    constexpr int q = kMaxCluster * kWarps / 32;  // a lane's consecutive runs
+    u64 own = 0;
+#pragma unroll
+    for (int i = 0; i < q; ++i)
+        if (lane * q + i < warps) own += seg[lane * q + i];
+    u64 upto = own;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, k);
+        if (lane >= k) upto += o;
+    }
+    const u64 Z = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const Target target(u, Z);
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, target.passed(upto))) - 1;
+    int s = 0;
+    u64 below = upto - own;
+    if (lane == at) {
+        s = lane * q;
+        while (!target.passed(below + seg[s])) below += seg[s++];
+    }
+    s = __shfl_sync(0xFFFFFFFFu, s, at);
+    below = __shfl_sync(0xFFFFFFFFu, below, at);
+    if (s / kWarps == static_cast<int>(ex.rank)) {
+        const int mine = max(min(P.split.per_cta, (P.V - R.base + n - 1) / n), 0);
+        const int lo = min((s % kWarps) * P.split.per_warp, mine), hi = min(lo + P.split.per_warp, mine);
+        const int each = (hi - lo + kThreads - 1) / kThreads;
+        const int from = min(lo + tid * each, hi), to = min(from + each, hi);
+        u64 sum = 0, all;
+        for (int j = from; j < to; ++j) {
+            float f[n];
+            Vec<T>::get(R.vec[j], f);
+#pragma unroll
+            for (int e = 0; e < n; ++e) sum += weight(kept_weight<T, kAll>(f[e], keep));
+        }
+        u64 run = below + block_scan(sum, sh.box, &all);
+        if (target.passed(run + sum) && !target.passed(run)) {
+            const T *elems = reinterpret_cast<const T *>(R.vec);
+            int i = from * n;
+            float l = as_float(elems[i]);
+            while (!target.passed(run += weight(kept_weight<T, kAll>(l, keep)))) l = as_float(elems[++i]);
+            P.tokens[r] = R.base + i;
+            if (P.logprob) P.logprob[r] = log_prob(delta(l, keep.L, keep.inv), Z);
+        }
+    }
+    if (P.probs) {
+        float *probs = P.probs + r * P.probs_stride;
+        const float z = static_cast<float>(static_cast<double>(Z) * 0x1p-40);
+        for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) {
+            const float l = R.at(i), d = delta(l, keep.L, keep.inv);
+            probs[i] = l >= keep.tau && l > -kInf && d >= keep.low ? __fdiv_rn(sv::exp_f32(d), z) : 0.0f;
+        }
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sv_sample_kernel(const T *logits, SampleParams P)
+__global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits, SampleParams P)
 {
+    extern __shared__ uint4 store[];
     __shared__ Shared sh;
-    const int tid = threadIdx.x, V = P.V;
-    const long long r = blockIdx.x;
+    const int tid = threadIdx.x, cluster = P.cluster;
+    const unsigned rank = cluster_rank();
+    const long long r = blockIdx.x / cluster;
     const T *row = logits + r * P.stride;
-    float *probs = P.probs ? P.probs + r * P.probs_stride : nullptr;
+    u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
+    u64 *sums = list + kList;                           // (the leader's, after the lane maxima)
+    float *peaks = reinterpret_cast<float *>(sums);     // a maximum of every lane of the cluster
+    Row<T> R = start_row(row, P.V, P.split, store, rank);
+    cluster_arrive();  // (waited for before the first write to another CTA: that it runs by then)
+    const int part = kList / cluster;
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
-    const int k = P.top_k ? __ldg(P.top_k + r) : 0;
+    const int k0 = P.top_k ? __ldg(P.top_k + r) : 0;
     const float p = P.top_p ? __ldg(P.top_p + r) : 1.0f;
     const float m = P.min_p ? __ldg(P.min_p + r) : 0.0f;
-    const bool greedy = !(temp > 0.0f) || k == 1;
-    const float inv = greedy ? 1.0f : inverse(temp);
+    const float u = __ldg(P.uniforms + r);
+    const bool greedy = !(temp > 0.0f) || k0 == 1;
+    const int k = k0 >= 1 && k0 < P.V ? k0 : 0;
+    const bool open = !greedy && !k && !(p < 1.0f) && !(m > 0.0f);
+    float *probs = P.probs ? P.probs + r * P.probs_stride : nullptr;
+    if (probs && !open)  // zeros while the logits come; what is kept goes over them
+        for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
 
-    // the largest logit and where it first stands
+    float peak = lane_max(R);
+    cluster_wait();
+    for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
+    cluster_sync();
     float L = -kInf;
-    for (int v = tid; v < V; v += kThreads) L = fmaxf(L, elem(row, v));
-    L = block_reduce(L, reinterpret_cast<float *>(sh.box), [](float a, float b) { return fmaxf(a, b); });
+    for (int c = 0; c < cluster; ++c) L = fmaxf(L, peaks[c * kThreads + tid]);
+    L = warp_max(L);
+    if (R.lane == 0) reinterpret_cast<float *>(sh.box)[R.warp] = L;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) L = fmaxf(L, reinterpret_cast<float *>(sh.box)[w]);
+    __syncthreads();
     if (!(L > -kInf)) {  // nothing to keep
-        if (tid == 0) {
+        if (rank == 0 && tid == 0) {
             P.tokens[r] = -1;
             if (P.logprob) P.logprob[r] = -kInf;
         }
-        if (probs)
-            for (int v = tid; v < V; v += kThreads) probs[v] = 0.0f;
+        if (probs && open)
+            for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
         return;
+    }
+    if (L == kInf) {  // the tokens at +inf share the row: 0 for them, -inf for the others
+        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+            T *e = reinterpret_cast<T *>(store + j);
+            for (int i = 0; i < Row<T>::n; ++i) e[i] = as_float(e[i]) == kInf ? T(0) : Low<T>::value();
+        }
+        peak = peak == kInf ? 0.0f : -kInf;
+        for (int c = 0; c < cluster; ++c) peaks[c * kThreads + tid] = peaks[c * kThreads + tid] == kInf ? 0.0f : -kInf;
+        L = 0.0f;
+        __syncthreads();
     }
     if (greedy) {
-        int best = INT_MAX;
-        for (int v = tid; v < V; v += kThreads)
-            if (elem(row, v) == L) best = min(best, v);
-        best = block_reduce(best, reinterpret_cast<int *>(sh.box), [](int a, int b) { return min(a, b); });
-        if (tid == 0) {
+        if (tid == 0) sh.first = INT_MAX;
+        __syncthreads();
+        if (peak == L) {
+            int best = INT_MAX;
+            for (int j = R.lo + R.lane; j < R.hi && best == INT_MAX; j += 32) {
+                float f[Row<T>::n];
+                Vec<T>::get(R.vec[j], f);
+                for (int e = Row<T>::n - 1; e >= 0; --e)
+                    if (f[e] == L) best = R.base + j * Row<T>::n + e;
+            }
+            atomicMin(&sh.first, best);
+        }
+        __syncthreads();
+        if (tid == 0) put(remote(&sh.count[rank], 0), static_cast<unsigned>(sh.first));
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+            int best = INT_MAX;
+            for (int c = 0; c < cluster; ++c) best = min(best, static_cast<int>(sh.count[c]));
             P.tokens[r] = best;
             if (P.logprob) P.logprob[r] = 0.0f;
+            if (probs) probs[best] = 1.0f;
         }
-        if (probs)
-            for (int v = tid; v < V; v += kThreads) probs[v] = v == best ? 1.0f : 0.0f;
         return;
     }
-    unsigned floor = 1;
-    if (k >= 1 && k < V) {
-        int valid = 0;
-        for (int v = tid; v < V; v += kThreads) valid += key_of(elem(row, v)) != 0;
-        valid = block_sum(valid, reinterpret_cast<int *>(sh.box));
-        if (k < valid) floor = select_key<T, false>(row, V, L, inv, 1, k, sh);
-    }
-    if (p < 1.0f) {
-        u64 z = 0;
-        for (int v = tid; v < V; v += kThreads) {
-            const float l = elem(row, v);
-            if (key_of(l) >= floor) z += weight(sv::exp_f32(delta(l, L, inv)));
-        }
-        z = block_sum(z, sh.box);
-        const double need = static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(z);
-        floor = max(floor, select_key<T, true>(row, V, L, inv, floor, need, sh));
-    }
-    const float low = m > 0.0f ? __double2float_rn(log(static_cast<double>(fminf(m, 1.0f)))) : -kInf;
 
-    auto kept = [&](int v, float &d) -> float {
-        const float l = elem(row, v);
-        if (key_of(l) < floor) return 0.0f;
-        d = delta(l, L, inv);
-        return d >= low ? sv::exp_f32(d) : 0.0f;
-    };
-    float d = 0.0f;
-    u64 Z = 0;
-    for (int v = tid; v < V; v += kThreads) Z += weight(kept(v, d));
-    Z = block_sum(Z, sh.box);
-    const float u = __ldg(P.uniforms + r);
-    const double target = static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(Z);
-    if (tid == 0) sh.token = -1;
-    u64 base = 0;
-    for (int v0 = 0; v0 < V; v0 += kThreads) {
-        const int v = v0 + tid;
-        float dv = 0.0f;
-        const u64 w = v < V ? weight(kept(v, dv)) : 0;
-        u64 all;
-        const u64 upto = base + block_scan(w, sh.box, &all) + w;
-        const bool hit = w && (static_cast<double>(upto) > target || upto == Z) &&
-                         !(static_cast<double>(upto - w) > target);
-        if (hit) {
-            sh.token = v;
-            sh.d = dv;
+    Kept keep{L, inverse(temp), -FLT_MAX, -kInf};
+    if (m > 0.0f) keep.low = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
+    Exchange ex{sh, rank, cluster, 0};
+    if (open) {
+        draw_row<T, true>(P, R, r, u, keep, ex);
+        return;
+    }
+    const bool mass = p < 1.0f && k == 0;  // the top-p set's total is the whole row's
+    if (k <= kList / 2) {
+        float cut;
+        if (k > 0 || mass) cut = cut_for(peaks, cluster * kThreads, L, k > 0 ? k : kTopP, sh);
+        else cut = fmaxf(L + keep.low / keep.inv - 4e-6f * (fabsf(L) + fabsf(keep.low / keep.inv)), -FLT_MAX);
+        collect(R, peak, cut, list, part, rank, cluster, sh);
+        u64 Z = 0;
+        if (mass) Z = ex.sum(warp_weight<T, true>(R, keep));
+        else cluster_sync();
+        int total = 0;
+        bool fits = true;
+        for (int c = 0; c < cluster; ++c) {
+            fits &= sh.count[c] <= static_cast<unsigned>(part);
+            total += static_cast<int>(sh.count[c]);
         }
-        base += all;
-        __syncthreads();
-        if (sh.token >= 0) break;
+        fits &= k <= total || cut == -FLT_MAX;
+        if (fits && mass && cut > -FLT_MAX) {
+            // whether the listed tokens reach P of the whole: the leader sums them up
+            if (rank == 0) {
+                u64 s = 0, all;
+                for (int i = tid; i < kList; i += kThreads) {
+                    const int c = i / part;
+                    if (i - c * part < static_cast<int>(sh.count[c]))
+                        s += weight(exp_weight(delta(of_key(static_cast<unsigned>(list[i] >> 32)), L, keep.inv)));
+                }
+                block_scan(s, sh.box, &all);
+                const double need = static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(Z);
+                if (tid < cluster) put(remote(&sh.cut, tid), static_cast<unsigned>(static_cast<double>(all) >= need));
+            }
+            cluster_sync();
+            fits = sh.cut != 0;
+        }
+        if (fits) {
+            if (rank == 0) finish_list(P, row, r, list, sums, part, k, p, Z, u, keep, sh);
+            return;
+        }
     }
-    if (tid == 0) {
-        P.tokens[r] = sh.token;
-        if (P.logprob)
-            P.logprob[r] = static_cast<float>(static_cast<double>(sh.d) - log(static_cast<double>(Z) * 0x1p-40));
+    unsigned floor = 1;
+    if (k > 0) floor = search_key<T, false>(R, keep, 1, k, ex);
+    if (p < 1.0f) {
+        keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
+        Kept all = keep;
+        all.low = -kInf;
+        const u64 Z = ex.sum(warp_weight<T, false>(R, all));
+        floor = search_key<T, true>(R, keep, floor, static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(Z), ex);
     }
-    if (probs) {
-        const float z = static_cast<float>(static_cast<double>(Z) * 0x1p-40);
-        for (int v = tid; v < V; v += kThreads) probs[v] = __fdiv_rn(kept(v, d), z);
-    }
+    keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
+    draw_row<T, false>(P, R, r, u, keep, ex);
 }
 
+// ---------------------------------------------------------------------------------------
+// log-probabilities
+// ---------------------------------------------------------------------------------------
 struct LogprobParams {
     long long stride;
     const float *temperature;
     const int32_t *tokens, *cu;
-    int token_stride, num_reqs, num_top, V;
+    int token_stride, num_reqs, num_top, V, cluster;
     float *logprob, *top_logprob;
     int32_t *rank, *top_ids;
+    Split split;
 };
 
 // The token wanted of row r: tokens[r], or with prefix sums of the draft lengths the entry of the
@@ -281,63 +881,164 @@ __device__ int row_token(const LogprobParams &P, long long r)
     return j >= 0 && j < P.token_stride ? __ldg(P.tokens + static_cast<long long>(lo) * P.token_stride + j) : -1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sv_logprobs_kernel(const T *logits, LogprobParams P)
+__device__ __forceinline__ u64 pack(float a, float b)
 {
+    return (static_cast<u64>(__float_as_uint(a)) << 32) | __float_as_uint(b);
+}
+
+// Each warp sums 2^((l - m) / T log2 e) over its logits against its own largest, m, and counts the
+// logits above the token's; the leader joins the warps' sums. The best tokens come from the list
+// of those above the cut that num_top lane maxima reach, sorted by the leader.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logits, LogprobParams P)
+{
+    constexpr int n = Row<T>::n;
+    extern __shared__ uint4 store[];
     __shared__ Shared sh;
-    const int tid = threadIdx.x, V = P.V, n = P.num_top;
-    const long long r = blockIdx.x;
+    const int tid = threadIdx.x, cluster = P.cluster, top = P.num_top;
+    const unsigned rank = cluster_rank();
+    const long long r = blockIdx.x / cluster;
     const T *row = logits + r * P.stride;
+    u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
+    float *peaks = reinterpret_cast<float *>(list + kList);
     const int token = P.tokens ? row_token(P, r) : 0;
-    int32_t *ids = n ? P.top_ids + r * n : nullptr;
-    float *best = n ? P.top_logprob + r * n : nullptr;
-    float L = -kInf;
-    const bool wanted = token >= 0 && token < V;
-    if (wanted)
-        for (int v = tid; v < V; v += kThreads) L = fmaxf(L, elem(row, v));
-    L = block_reduce(L, reinterpret_cast<float *>(sh.box), [](float a, float b) { return fmaxf(a, b); });
-    if (!(L > -kInf)) {
+    const bool wanted = token >= 0 && token < P.V;
+    if (!wanted) {
+        if (rank != 0) return;
         if (tid == 0 && P.logprob) P.logprob[r] = -kInf;
-        if (tid == 0 && P.rank) P.rank[r] = wanted ? 1 : 0;
-        for (int i = tid; i < n; i += kThreads) {
-            ids[i] = -1;
-            best[i] = -kInf;
+        if (tid == 0 && P.rank) P.rank[r] = 0;
+        for (int i = tid; i < top; i += kThreads) {
+            P.top_ids[r * top + i] = -1;
+            P.top_logprob[r * top + i] = -kInf;
         }
         return;
     }
+    const Row<T> R = start_row(row, P.V, P.split, store, rank);
+    cluster_arrive();  // (waited for before the first write to another CTA: that it runs by then)
+    const float lt = fmaxf(as_float(__ldg(row + token)), -kInf);  // (NaN as -inf)
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
-    const float lt = fmaxf(elem(row, token), -kInf);  // (NaN as -inf)
-    double s = 0.0;
-    int rank = 0;
-    for (int v = tid; v < V; v += kThreads) {
-        const float l = elem(row, v);
-        if (l > -kInf) s += sv::exp_f32(delta(l, L, inv));
-        rank += l > lt;
-    }
-    s = block_sum(s, reinterpret_cast<double *>(sh.box));
-    rank = block_sum(rank, reinterpret_cast<int *>(sh.box));
-    const double norm = log(s);
-    if (tid == 0) {
-        if (P.logprob)
-            P.logprob[r] = lt > -kInf ? static_cast<float>(static_cast<double>(delta(lt, L, inv)) - norm) : -kInf;
-        if (P.rank) P.rank[r] = rank + 1;
-    }
-    u64 last = ~0ull;  // (key, ~index) of the previous best
-    for (int i = 0; i < n; ++i) {
-        u64 b = 0;
-        for (int v = tid; v < V; v += kThreads) {
-            const unsigned key = key_of(elem(row, v));
-            const u64 c = (static_cast<u64>(key) << 32) | static_cast<unsigned>(~v);
-            if (key && c < last && c > b) b = c;
+    const float scale = fminf(inv * kLog2e, FLT_MAX);
+    const float peak = lane_max(R), top_of_warp = warp_max(peak);
+    float s = 0.0f;
+    unsigned above = 0;
+    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        float f[n];
+        Vec<T>::get(R.vec[j], f);
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            s += sv::ex2_approx(fmaxf((f[e] - top_of_warp) * scale, -200.0f));
+            above += f[e] > lt;
         }
-        b = block_reduce(b, sh.box, [](u64 x, u64 y) { return x > y ? x : y; });
-        last = b;
+    }
+    if (top_of_warp == kInf || top_of_warp == -kInf) {  // the tokens at +inf share the row
+        s = 0.0f;
+        if (top_of_warp == kInf)
+            for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+                float f[n];
+                Vec<T>::get(R.vec[j], f);
+                for (int e = 0; e < n; ++e) s += f[e] == kInf;
+            }
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    cluster_wait();
+    if (R.lane == 0) {
+        put(remote(&sh.seg[0][rank * kWarps + R.warp], 0), pack(top_of_warp, s));
+        put(remote(&sh.seg[1][rank * kWarps + R.warp], 0), static_cast<u64>(above));
+    }
+    if (top > 0)
+        for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
+    cluster_sync();
+    float L = -kInf;
+    double norm = 0.0;
+    if (rank == 0) {
+        u64 rank_sum = 0;
+        for (int i = R.lane; i < cluster * kWarps; i += 32) {
+            L = fmaxf(L, __uint_as_float(static_cast<unsigned>(sh.seg[0][i] >> 32)));
+            rank_sum += sh.seg[1][i];
+        }
+        L = warp_max(L);
+        rank_sum = warp_sum(rank_sum);
+        double sum = 0.0;
+        for (int i = R.lane; i < cluster * kWarps; i += 32) {
+            const float mw = __uint_as_float(static_cast<unsigned>(sh.seg[0][i] >> 32));
+            const float sw = __uint_as_float(static_cast<unsigned>(sh.seg[0][i]));
+            if (mw > -kInf) sum += static_cast<double>(sw) * (mw == L ? 1.0 : exp(static_cast<double>((mw - L) * inv)));
+        }
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+        norm = log(sum);
         if (tid == 0) {
-            const int v = static_cast<int>(~static_cast<unsigned>(b));
-            ids[i] = b ? v : -1;
-            best[i] = b ? static_cast<float>(static_cast<double>(delta(elem(row, v), L, inv)) - norm) : -kInf;
+            const float d = lt == L ? 0.0f : (lt - L) * inv;
+            if (P.logprob) P.logprob[r] = lt > -kInf ? static_cast<float>(static_cast<double>(d) - norm) : -kInf;
+            if (P.rank) P.rank[r] = 1 + static_cast<int>(rank_sum);
         }
+    }
+    if (top == 0) return;
+    L = -kInf;
+    for (int c = 0; c < cluster; ++c) L = fmaxf(L, peaks[c * kThreads + tid]);
+    L = warp_max(L);
+    if (R.lane == 0) reinterpret_cast<float *>(sh.box)[R.warp] = L;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) L = fmaxf(L, reinterpret_cast<float *>(sh.box)[w]);
+    __syncthreads();
+    auto write = [&](int i, u64 entry) {
+        const auto index = static_cast<int>(~static_cast<unsigned>(entry));
+        const float l = entry ? of_key(static_cast<unsigned>(entry >> 32)) : -kInf;
+        const float d = l == L ? 0.0f : (l - L) * inv;
+        P.top_ids[r * top + i] = entry ? index : -1;
+        P.top_logprob[r * top + i] = entry ? static_cast<float>(static_cast<double>(d) - norm) : -kInf;
+    };
+    if (!(L > -kInf)) {
+        if (rank == 0)
+            for (int i = tid; i < top; i += kThreads) write(i, 0);
+        return;
+    }
+    // a row with tokens at +inf: a cut below every finite one, which lists them all or none fit
+    const float cut = L < kInf ? cut_for(peaks, cluster * kThreads, L, top, sh) : -FLT_MAX;
+    const int part = kList / cluster;
+    collect(R, peak, cut, list, part, rank, cluster, sh);
+    cluster_sync();
+    bool fits = true;
+    int total = 0;
+    for (int c = 0; c < cluster; ++c) {
+        fits &= sh.count[c] <= static_cast<unsigned>(part);
+        total += static_cast<int>(sh.count[c]);
+    }
+    if (fits && (total >= top || cut == -FLT_MAX)) {
+        if (rank != 0) return;
+        const int size = close_and_sort(list, part, cluster, sh.count);
+        sort_down(list, size);
+        for (int i = tid; i < top; i += kThreads) write(i, i < size ? list[i] : 0);
+        return;
+    }
+    // more ties than the list holds: one token after the other
+    Exchange ex{sh, rank, cluster, 0};
+    u64 last = kNone64;
+    for (int i = 0; i < top; ++i) {
+        u64 best = 0;
+        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+            float f[n];
+            Vec<T>::get(R.vec[j], f);
+#pragma unroll
+            for (int e = 0; e < n; ++e) {
+                const unsigned key = key_of(f[e]);
+                const u64 c = (static_cast<u64>(key) << 32) | static_cast<unsigned>(~static_cast<unsigned>(R.base + j * n + e));
+                if (key && c < last && c > best) best = c;
+            }
+        }
+#pragma unroll
+        for (int k = 16; k; k >>= 1) {
+            const u64 o = __shfl_xor_sync(0xFFFFFFFFu, best, k);
+            best = o > best ? o : best;
+        }
+        const u64 *v = ex.all(best);
+        for (int c = 0; c < cluster * kWarps; ++c) best = v[c] > best ? v[c] : best;
+        last = best;
+        if (rank == 0 && tid == 0) write(i, best);
     }
 }
 
@@ -375,10 +1076,12 @@ struct DeviceGuard {
 };
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxStore = 232448 - static_cast<int>(sizeof(Shared)) - 1024;  // dynamic shared memory of a CTA
 std::mutex g_rows_mutex;
 bool g_rows_ready[kMaxDevices];
 
-// Whether `dev` is a device the kernels run on; looked up once per device.
+// Whether `dev` is a device the kernels run on, and their limits there; looked up and set once per
+// device. Makes the device current for it.
 int rows_device(int dev)
 {
     if (dev < 0 || dev >= kMaxDevices) return SV_EDEVICE;
@@ -391,8 +1094,65 @@ int rows_device(int dev)
         return SV_EDEVICE;
     }
     if (major != 10 || minor != 3) return SV_EDEVICE;  // built for sm_103a only
+    const DeviceGuard guard(dev);
+    if (!guard.ok) return SV_EDEVICE;
+    for (const void *k : {reinterpret_cast<const void *>(sv_sample_kernel<uint16_t>),
+                          reinterpret_cast<const void *>(sv_sample_kernel<float>),
+                          reinterpret_cast<const void *>(sv_logprobs_kernel<uint16_t>),
+                          reinterpret_cast<const void *>(sv_logprobs_kernel<float>)})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStore) != cudaSuccess ||
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return SV_ECUDA;
+        }
     g_rows_ready[dev] = true;
     return SV_OK;
+}
+
+// How a launch splits its rows: CTAs per row, vectors of 16 bytes per CTA and per warp.
+struct Shape {
+    int cluster;
+    Split split;
+    size_t smem;
+};
+
+Shape shape_of(int rows, int V, int elem_bytes)
+{
+    const int vectors = V / (16 / elem_bytes) + 2;  // (a row may start and end within one)
+    int c = 1;
+    // at most 80 KB of a row in a CTA: two or more CTAs on an SM, one computing while another loads
+    while (c < kMaxCluster && (vectors + c - 1) / c > 80 * 1024 / 16) c *= 2;
+    // few rows: more CTAs for each, down to 8 KB in a CTA
+    while (c < kMaxCluster && 2ll * rows * c <= 152 && vectors / (2 * c) >= 512) c *= 2;
+    Shape s;
+    s.cluster = c;
+    s.split.per_warp = ((vectors + c - 1) / c + kWarps - 1) / kWarps;
+    s.split.per_cta = s.split.per_warp * kWarps;
+    const size_t tail = std::max<size_t>(kList * 8, static_cast<size_t>(c) * kThreads * 4);
+    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + kList * 8 + tail;
+    return s;
+}
+
+template <typename T, typename Params>
+int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, cudaStream_t stream)
+{
+    const Shape s = shape_of(rows, P.V, sizeof(T));
+    if (s.smem > static_cast<size_t>(kMaxStore)) return SV_ECAPACITY;
+    P.cluster = s.cluster;
+    P.split = s.split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows) * static_cast<unsigned>(s.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(s.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), P) == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
 bool misaligned(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -438,12 +1198,8 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
     P.probs = a->probs;
     P.V = a->vocab_size;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    const auto grid = static_cast<unsigned>(a->num_rows);
-    if (a->logits_dtype == SV_BF16)
-        sv_sample_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(static_cast<const uint16_t *>(a->logits), P);
-    else
-        sv_sample_kernel<float><<<grid, kThreads, 0, stream>>>(static_cast<const float *>(a->logits), P);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, stream)
+                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, stream);
 }
 
 extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cuda_stream)
@@ -479,10 +1235,6 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    const auto grid = static_cast<unsigned>(a->num_rows);
-    if (a->logits_dtype == SV_BF16)
-        sv_logprobs_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(static_cast<const uint16_t *>(a->logits), P);
-    else
-        sv_logprobs_kernel<float><<<grid, kThreads, 0, stream>>>(static_cast<const float *>(a->logits), P);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, stream)
+                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, stream);
 }
