@@ -479,12 +479,12 @@ int spec_verify_noalloc_last_error(uint32_t *err_word);
  * W_v = rint(2^40 exp(d_v)). Kept are the tokens that
  *   top_k     are at least the k-th largest logit (ties kept; k < 1 or k >= vocab_size: all),
  *   top_p     and whose strictly larger tokens of those hold less than P of their W (P < 1,
- *             taken as at least 1e-6; else all; the comparison in binary64),
+ *             taken as at least 1e-6; else all),
  *   min_p     and whose d_v >= ln M rounded to binary32 (M > 0, taken as at most 1; else all),
  * the meaning top_k and top_p have in spec_verify_batch. The token is the first kept one, in
- * index order, at which the running sum of W exceeds u Z (binary64; Z the kept sum; u below 0 or
- * NaN counts as 0; the last kept token of positive weight where u >= 1). Sums of W are exact, so
- * tokens follow bit for bit from these definitions. T <= 0 or NaN, or top_k == 1: the first of
+ * index order, at which the running sum of W exceeds u Z (Z the kept sum; u below 0 or NaN counts
+ * as 0; the last kept token of positive weight where u >= 1). Sums of W and the comparisons with
+ * P and u are exact, so tokens follow bit for bit from these definitions. T <= 0 or NaN, or top_k == 1: the first of
  * the largest logits. A row with nothing to keep gives token -1.
  *   temperature, top_p, min_p  [num_rows] binary32, top_k [num_rows] int32, each or NULL (T = 1;
  *                  no constraint)

@@ -26,12 +26,12 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kList = 1024;       // entries of the leader's candidate list
 constexpr int kStages = 4;        // portions in which a warp waits for its logits
-constexpr int kCutBins = 256;     // bins of the cut search: one for each thread
+constexpr int kCutBins = 256;     // bins of the cut search
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr int kTopP = 128;        // lane maxima that the cut for top-p alone is to reach
@@ -51,6 +51,7 @@ __device__ __forceinline__ unsigned cluster_rank()
 // Every thread of every CTA of the cluster; what was written before (shared memory of any CTA of
 // the cluster, global memory) is visible after.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_announce() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
@@ -109,6 +110,103 @@ template <> struct Vec<float> {
     }
 };
 
+// The largest of the logits added and -inf; a NaN loses.
+template <typename T> struct Largest;
+template <> struct Largest<uint16_t> {
+    unsigned a = 0xFF80FF80u, b = 0xFF80FF80u;  // (two chains)
+    static __device__ __forceinline__ unsigned pick(unsigned x, unsigned y)
+    {
+        unsigned r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+        return r;
+    }
+    __device__ __forceinline__ void add(const uint4 &v)
+    {
+        a = pick(pick(a, v.x), v.y);
+        b = pick(pick(b, v.z), v.w);
+    }
+    __device__ __forceinline__ float get() const
+    {
+        const unsigned m = pick(a, b);
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+};
+template <> struct Largest<float> {
+    float a = -kInf, b = -kInf;
+    __device__ __forceinline__ void add(const uint4 &v)
+    {
+        a = fmaxf(fmaxf(a, __uint_as_float(v.x)), __uint_as_float(v.y));
+        b = fmaxf(fmaxf(b, __uint_as_float(v.z)), __uint_as_float(v.w));
+    }
+    __device__ __forceinline__ float get() const { return fmaxf(a, b); }
+};
+
+// How many of the logits added are above a bound. A lane adds at most 64 vectors: the bf16 form
+// counts in bf16, which is exact up to 256 in each half.
+template <typename T> struct Above;
+template <> struct Above<uint16_t> {
+    unsigned bound, count = 0;
+    explicit __device__ __forceinline__ Above(float l) { bound = __float_as_uint(l) >> 16; bound |= bound << 16; }
+    __device__ __forceinline__ void add(const uint4 &v)
+    {
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            unsigned one;
+            asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(one) : "r"(w[i]), "r"(bound));
+            asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(one));
+        }
+    }
+    __device__ __forceinline__ unsigned get() const
+    {
+        return static_cast<unsigned>(__uint_as_float(count << 16) + __uint_as_float(count & 0xFFFF0000u));
+    }
+};
+template <> struct Above<float> {
+    float bound;
+    unsigned count = 0;
+    explicit __device__ __forceinline__ Above(float l) : bound(l) {}
+    __device__ __forceinline__ void add(const uint4 &v)
+    {
+        count += __uint_as_float(v.x) > bound;
+        count += __uint_as_float(v.y) > bound;
+        count += __uint_as_float(v.z) > bound;
+        count += __uint_as_float(v.w) > bound;
+    }
+    __device__ __forceinline__ unsigned get() const { return count; }
+};
+
+// Two binary32 values and the packed operations on them (each rounded as the single one).
+struct Two {
+    u64 v;
+};
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ Two two(float a) { return two(a, a); }
+__device__ __forceinline__ void parts(Two t, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(t.v)); }
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Logits as order-preserving unsigned integers, 0 for what is never kept (NaN and -inf); -0 as +0.
 __device__ __forceinline__ unsigned key_of(float l)
 {
@@ -147,13 +245,35 @@ __device__ __forceinline__ float exp_weight(float d)
     return __uint_as_float(__float_as_uint(p) + (__float_as_uint(ks) << 23));
 }
 
-__device__ __forceinline__ u64 weight(float t) { return static_cast<u64>(__float2ll_rn(t * 0x1p+40f)); }
+__device__ __forceinline__ Two exp_weight(Two d)
+{
+    float a, b;
+    parts(d, a, b);
+    d = two(fmaxf(a, -32.0f), fmaxf(b, -32.0f));
+    const Two ks = fma(d, two(0x1.715476p+0f), two(0x1.8p+23f));
+    const Two kf = ks + two(-0x1.8p+23f);
+    Two r = fma(kf, two(-0x1.62e430p-1f), d);
+    r = fma(kf, two(0x1.05c610p-29f), r);
+    Two p = fma(two(0x1.a01a02p-13f), r, two(0x1.6c16c2p-10f));
+    p = fma(p, r, two(0x1.111112p-7f));
+    p = fma(p, r, two(0x1.555556p-5f));
+    p = fma(p, r, two(0x1.555556p-3f));
+    p = fma(p, r, two(0.5f));
+    p = fma(p, r, two(1.0f));
+    p = fma(p, r, two(1.0f));
+    float pa, pb, ka, kb;
+    parts(p, pa, pb);
+    parts(ks, ka, kb);
+    return two(__uint_as_float(__float_as_uint(pa) + (__float_as_uint(ka) << 23)),
+               __uint_as_float(__float_as_uint(pb) + (__float_as_uint(kb) << 23)));
+}
 
 // An exact sum of weights in two 32-bit words. Adding 12 to t in [0, 1] rounds it to a multiple of
 // 2^-20, whose count the low mantissa bits then hold; what that left, at most 2^-21, is rounded to
 // a multiple of 2^-40 by adding 1.5 2^-17 in the same way. Together they are rint(t 2^40), ties as
 // rint's. The words add the bit patterns; the constant parts come off at the end. Good for up to
-// 4095 weights.
+// 4095 weights. (Nothing here is done in binary64, nor by conversions to 64-bit integers: this
+// part runs those at a sixtieth of the binary32 rate.)
 struct WeightSum {
     unsigned a = 0, b = 0;
     __device__ __forceinline__ void add(float t)
@@ -163,6 +283,16 @@ struct WeightSum {
         a += __float_as_uint(x);
         b += __float_as_uint(__fadd_rn(lo, 0x1.8p-17f));
     }
+    __device__ __forceinline__ void add(Two t)
+    {
+        const Two x = t + two(12.0f);
+        const Two y = fma(x + two(-12.0f), two(-1.0f), t) + two(0x1.8p-17f);
+        float p, q;
+        parts(x, p, q);
+        a += __float_as_uint(p) + __float_as_uint(q);
+        parts(y, p, q);
+        b += __float_as_uint(p) + __float_as_uint(q);
+    }
     __device__ __forceinline__ u64 total(int n) const  // n: how many were added
     {
         const unsigned hi = a - static_cast<unsigned>(n) * __float_as_uint(12.0f);
@@ -170,6 +300,66 @@ struct WeightSum {
         return (static_cast<u64>(hi) << 20) + static_cast<u64>(static_cast<long long>(lo));
     }
 };
+
+__device__ __forceinline__ u64 weight(float t)
+{
+    WeightSum s;
+    s.add(t);
+    return s.total(1);
+}
+
+// floor(f Z), for a binary32 f in [0, 1), exactly; *whole: whether f Z is a whole number.
+__device__ __forceinline__ u64 part_of(float f, u64 Z, bool *whole)
+{
+    const unsigned bits = __float_as_uint(f), exponent = bits >> 23;
+    const unsigned m = (bits & 0x7FFFFFu) | (exponent ? 0x800000u : 0u);
+    const int shift = 150 - static_cast<int>(exponent ? exponent : 1u);  // f = m 2^-shift, shift >= 24
+    const u64 lo = m * Z, hi = __umul64hi(m, Z);
+    if (shift < 64) {
+        *whole = (lo << (64 - shift)) == 0;
+        return (hi << (64 - shift)) | (lo >> shift);
+    }
+    if (shift == 64 || shift >= 128) {
+        *whole = lo == 0 && (shift == 64 || hi == 0);
+        return shift == 64 ? hi : 0;
+    }
+    *whole = lo == 0 && (hi << (128 - shift)) == 0;
+    return hi >> (shift - 64);
+}
+
+// The least weight a top-p set has to reach: ceil(P Z).
+__device__ __forceinline__ u64 share_of(float p, u64 Z)
+{
+    bool whole;
+    const u64 f = part_of(fmaxf(p, 1e-6f), Z, &whole);
+    return f + (whole ? 0 : 1);
+}
+
+// Z 2^-40 as binary32, rounded once (what the shift drops stays behind as a sticky bit).
+__device__ __forceinline__ float as_sum(u64 Z)
+{
+    const int s = max(32 - __clzll(static_cast<long long>(Z)), 0);  // drop so many bits
+    const unsigned top = static_cast<unsigned>(Z >> s) | ((Z & ((1ull << s) - 1)) != 0 ? 1u : 0u);
+    return __fmul_rn(__uint2float_rn(top), __uint_as_float(static_cast<unsigned>(127 + s - 40) << 23));
+}
+
+// d - ln(Z 2^-40): Z 2^-40 = 2^k f, f in [sqrt(1/2), sqrt(2)); k ln 2 in two parts, the first with
+// so few bits that its product with k is exact.
+__device__ __forceinline__ float log_prob(float d, u64 Z)
+{
+    float f = as_sum(Z);
+    int k = static_cast<int>(__float_as_uint(f) >> 23) - 127;
+    f = __uint_as_float(__float_as_uint(f) - (static_cast<unsigned>(k) << 23));
+    if (f > 0x1.6a09e6p+0f) {
+        f *= 0.5f;
+        k += 1;
+    }
+    const float kf = static_cast<float>(k);
+    const float hi = kf * 0x1.62ep-1f, lo = __fmaf_rn(kf, 0x1.0bfbe8p-15f, sv::log_f32(f));
+    const float a = __fsub_rn(d, hi), b = __fsub_rn(a, d);           // a + e = d - hi
+    const float e = __fsub_rn(__fsub_rn(d, __fsub_rn(a, b)), __fadd_rn(hi, b));
+    return __fadd_rn(a, __fsub_rn(e, lo));
+}
 
 // ---------------------------------------------------------------------------------------
 // warp and block reductions (block-wide ones by every thread)
@@ -228,7 +418,6 @@ struct Shared {
     unsigned mine;                     // candidates of this CTA
     unsigned cut;
     int first, found;
-    u64 below;
     float d;
 };
 
@@ -292,35 +481,39 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     return R;
 }
 
-// Calls f(vector number) for this lane's vectors as they arrive.
+// Calls f(first, end) for the portions of this lane's vectors (first, first + 32, ... below end)
+// as they arrive.
 template <typename T, typename F>
-__device__ __forceinline__ void as_they_come(const Row<T> &R, F f)
+__device__ __forceinline__ void by_portions(const Row<T> &R, F f)
 {
     const int step = ((R.hi - R.lo + 31) / 32 + kStages - 1) / kStages * 32;
-    int j = R.lo + R.lane;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
         if (s == 0) copy_wait<kStages - 1>();
         if (s == 1) copy_wait<kStages - 2>();
         if (s == 2) copy_wait<kStages - 3>();
         if (s == 3) copy_wait<0>();
-        const int end = min(R.lo + (s + 1) * step, R.hi);
-        for (; j < end; j += 32) f(j);
+        f(R.lo + s * step + R.lane, min(R.lo + (s + 1) * step, R.hi));
     }
 }
-static_assert(kStages == 4, "as_they_come waits for four portions");
+static_assert(kStages == 4, "by_portions waits for four portions");
+
+// Calls f(vector number) for this lane's vectors as they arrive.
+template <typename T, typename F>
+__device__ __forceinline__ void as_they_come(const Row<T> &R, F f)
+{
+    by_portions(R, [&](int j, int end) {
+#pragma unroll 4
+        for (; j < end; j += 32) f(j);
+    });
+}
 
 template <typename T>
 __device__ __forceinline__ float lane_max(const Row<T> &R)
 {
-    float m = -kInf;
-    as_they_come(R, [&](int j) {
-        float f[Row<T>::n];
-        Vec<T>::get(R.vec[j], f);
-#pragma unroll
-        for (int e = 0; e < Row<T>::n; ++e) m = fmaxf(m, f[e]);  // (a NaN loses)
-    });
-    return m;
+    Largest<T> m;
+    as_they_come(R, [&](int j) { m.add(R.vec[j]); });
+    return m.get();
 }
 
 // A cut that at least `want` of the cluster's lane maxima reach, or the lowest finite number where there
@@ -336,7 +529,7 @@ __device__ float cut_for(const float *peaks, int count, float L, int want, Share
         if (p > -kInf) low = fminf(low, p);
     }
     low = -warp_max(-low);
-    sh.bin[tid] = 0;
+    if (tid < kCutBins) sh.bin[tid] = 0;
     if (lane == 0) reinterpret_cast<float *>(sh.box)[warp] = low;
     __syncthreads();
 #pragma unroll
@@ -475,16 +668,14 @@ __device__ void sort_down(u64 *list, int size)
 
 // Whether a running sum of weights has passed the uniform number's place in the total.
 struct Target {
-    double at;
-    u64 Z;
-    __device__ __forceinline__ Target(float u, u64 Z_) : at(static_cast<double>(u > 0.0f ? u : 0.0f) * static_cast<double>(Z_)), Z(Z_) {}
-    __device__ __forceinline__ bool passed(u64 c) const { return static_cast<double>(c) > at || c == Z; }
+    u64 least;  // the least sum that is above u Z, or Z
+    __device__ __forceinline__ Target(float u, u64 Z)
+    {
+        bool whole;
+        least = u >= 1.0f ? Z : 1 + (u > 0.0f ? part_of(u, Z, &whole) : 0);
+    }
+    __device__ __forceinline__ bool passed(u64 c) const { return c >= least; }
 };
-
-__device__ __forceinline__ float log_prob(float d, u64 Z)
-{
-    return static_cast<float>(static_cast<double>(d) - log(static_cast<double>(Z) * 0x1p-40));
-}
 
 // The leader's work where its list holds every token that can be kept: the sorted list's weights
 // are summed up, the three constraints cut it off, and what is left is put in index order and
@@ -527,12 +718,12 @@ __device__ void finish_list(const SampleParams &P, const T *row, long long r, u6
         kept = min(kept, sh.found);
         __syncthreads();
     }
-    const double need = static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(k > 0 ? sums[kept - 1] : Z);
+    const u64 need = p < 1.0f ? share_of(p, k > 0 ? sums[kept - 1] : Z) : 0;
     for (int i = tid; i < kept; i += kThreads) {
         const auto key = static_cast<unsigned>(list[i] >> 32);
         bool out = delta(of_key(key), keep.L, keep.inv) < keep.low;
         if (p < 1.0f && i > 0 && key != static_cast<unsigned>(list[i - 1] >> 32))
-            out |= !(static_cast<double>(sums[i - 1]) < need);
+            out |= sums[i - 1] >= need;
         if (out) atomicMin(&sh.found, i);
     }
     __syncthreads();
@@ -540,7 +731,7 @@ __device__ void finish_list(const SampleParams &P, const T *row, long long r, u6
     const u64 Zk = sums[kept - 1];
     if (P.probs) {
         float *probs = P.probs + r * P.probs_stride;
-        const float z = static_cast<float>(static_cast<double>(Zk) * 0x1p-40);
+        const float z = as_sum(Zk);
         for (int i = tid; i < kept; i += kThreads) {
             const u64 e = list[i];
             probs[static_cast<int>(~static_cast<unsigned>(e))] =
@@ -576,12 +767,23 @@ __device__ void finish_list(const SampleParams &P, const T *row, long long r, u6
     }
 }
 
-template <typename T, bool kAll>
+template <bool kAll>
 __device__ __forceinline__ float kept_weight(float l, const Kept &keep)
 {
     const float d = delta(l, keep.L, keep.inv);
     const float t = exp_weight(d);
     return kAll || (l >= keep.tau && d >= keep.low) ? t : 0.0f;
+}
+template <bool kAll>
+__device__ __forceinline__ Two kept_weight(float l, float m, const Kept &keep)
+{
+    const Two d = (two(l, m) + two(-keep.L)) * two(keep.inv);
+    const Two t = exp_weight(d);
+    if (kAll) return t;
+    float da, db, a, b;
+    parts(d, da, db);
+    parts(t, a, b);
+    return two(l >= keep.tau && da >= keep.low ? a : 0.0f, m >= keep.tau && db >= keep.low ? b : 0.0f);
 }
 
 // This warp's sum of the kept tokens' weights.
@@ -591,11 +793,12 @@ __device__ __forceinline__ u64 warp_weight(const Row<T> &R, const Kept &keep)
     constexpr int n = Row<T>::n;
     WeightSum s;
     int count = 0;
+#pragma unroll 4
     for (int j = R.lo + R.lane; j < R.hi; j += 32) {
         float f[n];
         Vec<T>::get(R.vec[j], f);
 #pragma unroll
-        for (int e = 0; e < n; ++e) s.add(kept_weight<T, kAll>(f[e], keep));
+        for (int e = 0; e < n; e += 2) s.add(kept_weight<kAll>(f[e], f[e + 1], keep));
         count += n;
     }
     return warp_sum(s.total(count));
@@ -628,7 +831,7 @@ struct Exchange {
 // The largest key such that the keys at least as large, of those from `floor` on, hold `need`
 // tokens or, with kMass, the weight `need`: bit by bit, one pass over the row for each.
 template <typename T, bool kMass>
-__device__ unsigned search_key(const Row<T> &R, const Kept &keep, unsigned floor, double need, Exchange &ex)
+__device__ unsigned search_key(const Row<T> &R, const Kept &keep, unsigned floor, u64 need, Exchange &ex)
 {
     constexpr int n = Row<T>::n;
     unsigned found = 0;
@@ -642,7 +845,7 @@ __device__ unsigned search_key(const Row<T> &R, const Kept &keep, unsigned floor
             for (int e = 0; e < n; ++e)
                 if (key_of(f[e]) >= trial) m += kMass ? weight(exp_weight(delta(f[e], keep.L, keep.inv))) : 1ull;
         }
-        if (static_cast<double>(ex.sum(warp_sum(m))) >= need) found |= bit;
+        if (ex.sum(warp_sum(m)) >= need) found |= bit;
     }
     return max(found, floor);
 }
@@ -689,21 +892,21 @@ __device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, fl
             float f[n];
             Vec<T>::get(R.vec[j], f);
 #pragma unroll
-            for (int e = 0; e < n; ++e) sum += weight(kept_weight<T, kAll>(f[e], keep));
+            for (int e = 0; e < n; ++e) sum += weight(kept_weight<kAll>(f[e], keep));
         }
         u64 run = below + block_scan(sum, sh.box, &all);
         if (target.passed(run + sum) && !target.passed(run)) {
             const T *elems = reinterpret_cast<const T *>(R.vec);
             int i = from * n;
             float l = as_float(elems[i]);
-            while (!target.passed(run += weight(kept_weight<T, kAll>(l, keep)))) l = as_float(elems[++i]);
+            while (!target.passed(run += weight(kept_weight<kAll>(l, keep)))) l = as_float(elems[++i]);
             P.tokens[r] = R.base + i;
             if (P.logprob) P.logprob[r] = log_prob(delta(l, keep.L, keep.inv), Z);
         }
     }
     if (P.probs) {
         float *probs = P.probs + r * P.probs_stride;
-        const float z = static_cast<float>(static_cast<double>(Z) * 0x1p-40);
+        const float z = as_sum(Z);
         for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) {
             const float l = R.at(i), d = delta(l, keep.L, keep.inv);
             probs[i] = l >= keep.tau && l > -kInf && d >= keep.low ? __fdiv_rn(sv::exp_f32(d), z) : 0.0f;
@@ -724,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     u64 *sums = list + kList;                           // (the leader's, after the lane maxima)
     float *peaks = reinterpret_cast<float *>(sums);     // a maximum of every lane of the cluster
     Row<T> R = start_row(row, P.V, P.split, store, rank);
-    cluster_arrive();  // (waited for before the first write to another CTA: that it runs by then)
+    cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
     const int part = kList / cluster;
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const int k0 = P.top_k ? __ldg(P.top_k + r) : 0;
@@ -738,6 +941,8 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     if (probs && !open)  // zeros while the logits come; what is kept goes over them
         for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
 
+    // (in binary64, by one thread, while the logits come)
+    if (m > 0.0f && tid == 0) sh.d = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
     float peak = lane_max(R);
     cluster_wait();
     for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
@@ -796,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     }
 
     Kept keep{L, inverse(temp), -FLT_MAX, -kInf};
-    if (m > 0.0f) keep.low = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
+    if (m > 0.0f) keep.low = sh.d;
     Exchange ex{sh, rank, cluster, 0};
     if (open) {
         draw_row<T, true>(P, R, r, u, keep, ex);
@@ -828,8 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
                         s += weight(exp_weight(delta(of_key(static_cast<unsigned>(list[i] >> 32)), L, keep.inv)));
                 }
                 block_scan(s, sh.box, &all);
-                const double need = static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(Z);
-                if (tid < cluster) put(remote(&sh.cut, tid), static_cast<unsigned>(static_cast<double>(all) >= need));
+                if (tid < cluster) put(remote(&sh.cut, tid), static_cast<unsigned>(all >= share_of(p, Z)));
             }
             cluster_sync();
             fits = sh.cut != 0;
@@ -840,13 +1044,13 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         }
     }
     unsigned floor = 1;
-    if (k > 0) floor = search_key<T, false>(R, keep, 1, k, ex);
+    if (k > 0) floor = search_key<T, false>(R, keep, 1, static_cast<u64>(k), ex);
     if (p < 1.0f) {
         keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
         Kept all = keep;
         all.low = -kInf;
         const u64 Z = ex.sum(warp_weight<T, false>(R, all));
-        floor = search_key<T, true>(R, keep, floor, static_cast<double>(fmaxf(p, 1e-6f)) * static_cast<double>(Z), ex);
+        floor = search_key<T, true>(R, keep, floor, share_of(p, Z), ex);
     }
     keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
     draw_row<T, false>(P, R, r, u, keep, ex);
@@ -914,45 +1118,67 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         return;
     }
     const Row<T> R = start_row(row, P.V, P.split, store, rank);
-    cluster_arrive();  // (waited for before the first write to another CTA: that it runs by then)
+    cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
     const float lt = fmaxf(as_float(__ldg(row + token)), -kInf);  // (NaN as -inf)
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
     const float scale = fminf(inv * kLog2e, FLT_MAX);
-    const float peak = lane_max(R), top_of_warp = warp_max(peak);
-    float s = 0.0f;
-    unsigned above = 0;
-    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-        float f[n];
-        Vec<T>::get(R.vec[j], f);
-#pragma unroll
-        for (int e = 0; e < n; ++e) {
-            s += sv::ex2_approx(fmaxf((f[e] - top_of_warp) * scale, -200.0f));
-            above += f[e] > lt;
+    // every portion of a lane's vectors against the largest so far
+    float peak = -kInf, s = 0.0f;
+    Above<T> above(lt);
+    by_portions(R, [&](int first, int end) {
+        Largest<T> m;
+#pragma unroll 4
+        for (int j = first; j < end; j += 32) m.add(R.vec[j]);
+        const float ref = fmaxf(peak, m.get());
+        if (ref > peak) {
+            if (peak > -kInf) s *= sv::ex2_approx((peak - ref) * scale);
+            peak = ref;
         }
-    }
-    if (top_of_warp == kInf || top_of_warp == -kInf) {  // the tokens at +inf share the row
-        s = 0.0f;
-        if (top_of_warp == kInf)
-            for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        Two sum = two(0.0f);
+#pragma unroll 4
+        for (int j = first; j < end; j += 32) {
+            const uint4 v = R.vec[j];
+            above.add(v);
+            float f[n];
+            Vec<T>::get(v, f);
+#pragma unroll
+            for (int e = 0; e < n; e += 2) {
+                const Two x = (two(f[e], f[e + 1]) + two(-ref)) * two(scale);
+                float a, b;
+                parts(x, a, b);
+                sum = sum + two(sv::ex2_approx(a), sv::ex2_approx(b));
+            }
+        }
+        float a, b;
+        parts(sum, a, b);
+        a += b;
+        if (a != a) {  // a NaN among them, or logits of +inf (those share the row) or -inf alone
+            a = 0.0f;
+            for (int j = first; j < end; j += 32) {
                 float f[n];
                 Vec<T>::get(R.vec[j], f);
-                for (int e = 0; e < n; ++e) s += f[e] == kInf;
+                for (int e = 0; e < n; ++e)
+                    if (f[e] > -kInf) a += f[e] == ref ? 1.0f : sv::ex2_approx((f[e] - ref) * scale);
             }
-    }
+        }
+        s += a;
+    });
+    const float top_of_warp = warp_max(peak);
+    if (peak < top_of_warp && s > 0.0f) s *= sv::ex2_approx((peak - top_of_warp) * scale);
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
-    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    const unsigned larger = __reduce_add_sync(0xFFFFFFFFu, above.get());
     cluster_wait();
     if (R.lane == 0) {
         put(remote(&sh.seg[0][rank * kWarps + R.warp], 0), pack(top_of_warp, s));
-        put(remote(&sh.seg[1][rank * kWarps + R.warp], 0), static_cast<u64>(above));
+        put(remote(&sh.seg[1][rank * kWarps + R.warp], 0), static_cast<u64>(larger));
     }
     if (top > 0)
         for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
     cluster_sync();
     float L = -kInf;
-    double norm = 0.0;
+    float norm = 0.0f;
     if (rank == 0) {
         u64 rank_sum = 0;
         for (int i = R.lane; i < cluster * kWarps; i += 32) {
@@ -961,18 +1187,18 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         }
         L = warp_max(L);
         rank_sum = warp_sum(rank_sum);
-        double sum = 0.0;
+        float sum = 0.0f;
         for (int i = R.lane; i < cluster * kWarps; i += 32) {
             const float mw = __uint_as_float(static_cast<unsigned>(sh.seg[0][i] >> 32));
             const float sw = __uint_as_float(static_cast<unsigned>(sh.seg[0][i]));
-            if (mw > -kInf) sum += static_cast<double>(sw) * (mw == L ? 1.0 : exp(static_cast<double>((mw - L) * inv)));
+            if (mw > -kInf) sum += mw == L ? sw : sw * sv::exp_f32((mw - L) * inv);
         }
 #pragma unroll
         for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
-        norm = log(sum);
+        norm = sv::log_f32(sum);
         if (tid == 0) {
             const float d = lt == L ? 0.0f : (lt - L) * inv;
-            if (P.logprob) P.logprob[r] = lt > -kInf ? static_cast<float>(static_cast<double>(d) - norm) : -kInf;
+            if (P.logprob) P.logprob[r] = lt > -kInf ? d - norm : -kInf;
             if (P.rank) P.rank[r] = 1 + static_cast<int>(rank_sum);
         }
     }
@@ -990,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         const float l = entry ? of_key(static_cast<unsigned>(entry >> 32)) : -kInf;
         const float d = l == L ? 0.0f : (l - L) * inv;
         P.top_ids[r * top + i] = entry ? index : -1;
-        P.top_logprob[r * top + i] = entry ? static_cast<float>(static_cast<double>(d) - norm) : -kInf;
+        P.top_logprob[r * top + i] = entry ? d - norm : -kInf;
     };
     if (!(L > -kInf)) {
         if (rank == 0)
@@ -1116,7 +1342,7 @@ struct Shape {
     size_t smem;
 };
 
-Shape shape_of(int rows, int V, int elem_bytes)
+Shape shape_of(int rows, int V, int elem_bytes, bool lists)
 {
     const int vectors = V / (16 / elem_bytes) + 2;  // (a row may start and end within one)
     int c = 1;
@@ -1129,14 +1355,14 @@ Shape shape_of(int rows, int V, int elem_bytes)
     s.split.per_warp = ((vectors + c - 1) / c + kWarps - 1) / kWarps;
     s.split.per_cta = s.split.per_warp * kWarps;
     const size_t tail = std::max<size_t>(kList * 8, static_cast<size_t>(c) * kThreads * 4);
-    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + kList * 8 + tail;
+    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + (lists ? kList * 8 + tail : 0);
     return s;
 }
 
 template <typename T, typename Params>
-int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, cudaStream_t stream)
+int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, bool lists, cudaStream_t stream)
 {
-    const Shape s = shape_of(rows, P.V, sizeof(T));
+    const Shape s = shape_of(rows, P.V, sizeof(T), lists);
     if (s.smem > static_cast<size_t>(kMaxStore)) return SV_ECAPACITY;
     P.cluster = s.cluster;
     P.split = s.split;
@@ -1198,8 +1424,8 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
     P.probs = a->probs;
     P.V = a->vocab_size;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, stream)
-                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, true, stream)
+                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, true, stream);
 }
 
 extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cuda_stream)
@@ -1235,6 +1461,6 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, stream)
-                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, a->num_top > 0, stream)
+                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, a->num_top > 0, stream);
 }
