@@ -31,10 +31,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kList = 1024;       // entries of the leader's candidate list
 constexpr int kStages = 4;        // portions in which a warp waits for its logits
-constexpr int kCutBins = 256;     // bins of the cut search
+constexpr int kPairs = 256;       // most entries that are compared each with each
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
-constexpr int kTopP = 128;        // lane maxima that the cut for top-p alone is to reach
+constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
 constexpr u64 kNone64 = ~0ull;
 
 // ---------------------------------------------------------------------------------------
@@ -410,13 +410,13 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
 // reads shared memory: each logit crosses the memory bus once. What of the first and last vector
 // lies outside the row is -inf; those two are copied element by element.
 struct Shared {
-    unsigned bin[kCutBins];
     u64 box[kWarps];
     u64 seg[2][kMaxCluster * kWarps];  // a value of every warp of the cluster (two, used in turn)
-    unsigned count[kMaxCluster];       // candidates of every CTA
-    u64 listed[kMaxCluster];           // their weight
-    unsigned mine;                     // candidates of this CTA
-    unsigned cut;
+    u64 listed[kMaxCluster];           // the weight of every CTA's candidates
+    unsigned count[kMaxCluster];       // their number
+    float cut[kMaxCluster], peak[kMaxCluster];
+    int small[kWarps];
+    unsigned mine, fits;
     int first, found;
     float d;
 };
@@ -516,57 +516,36 @@ __device__ __forceinline__ float lane_max(const Row<T> &R)
     return m.get();
 }
 
-// A cut that at least `want` of the cluster's lane maxima reach, or the lowest finite number where there
-// are not so many: the maxima are counted in kCutBins equal bins from the largest, L, down to the smallest.
-// The tokens at or above it are then few more than the lanes that reach it, as a rule, and hold the
-// `want` largest of the row.
-__device__ float cut_for(const float *peaks, int count, float L, int want, Shared &sh)
+// The largest of a value over the block.
+__device__ __forceinline__ float block_max(float v, Shared &sh)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float low = L;
-    for (int i = tid; i < count; i += kThreads) {
-        const float p = peaks[i];
-        if (p > -kInf) low = fminf(low, p);
-    }
-    low = -warp_max(-low);
-    if (tid < kCutBins) sh.bin[tid] = 0;
-    if (lane == 0) reinterpret_cast<float *>(sh.box)[warp] = low;
+    v = warp_max(v);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) low = fminf(low, reinterpret_cast<float *>(sh.box)[w]);
-    // (a spread that overflows, of masks at the lowest value, gives the scale 0: one bin)
-    const float scale = L > low ? (kCutBins - 1) / (L - low) : 0.0f;
-    for (int i = tid; i < count; i += kThreads) {
-        const float p = peaks[i];
-        if (p > -kInf) atomicAdd(&sh.bin[min(static_cast<int>((L - p) * scale), kCutBins - 1)], 1u);
-    }
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float *>(sh.small)[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (warp == 0) {  // the first bin up to which `want` are counted
-        unsigned c[kCutBins / 32], s = 0;
-#pragma unroll
-        for (int i = 0; i < kCutBins / 32; ++i) s += c[i] = sh.bin[lane * (kCutBins / 32) + i];
-        unsigned upto = s;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const unsigned o = __shfl_up_sync(0xFFFFFFFFu, upto, k);
-            if (lane >= k) upto += o;
-        }
-        const unsigned reach = __ballot_sync(0xFFFFFFFFu, upto >= static_cast<unsigned>(want));
-        if (reach == 0) {
-            if (lane == 0) sh.cut = kCutBins;
-        } else if (lane == __ffs(reach) - 1) {
-            unsigned run = upto - s;
-            int i = 0;
-            while (i < kCutBins / 32 - 1 && (run += c[i]) < static_cast<unsigned>(want)) ++i;
-            sh.cut = lane * (kCutBins / 32) + i;
+    return warp_max(reinterpret_cast<float *>(sh.small)[threadIdx.x & (kWarps - 1)]);
+}
+
+// A cut that at least `want` of this CTA's lane maxima reach and at most a quarter more, or what
+// twenty halvings of the span of keys from the least to the largest of them give; the lowest
+// finite number where there are not so many. The CTA's tokens at or above it hold its `want` largest, and are few more than that.
+__device__ float cut_for(float peak, float largest, int want, Shared &sh)
+{
+    const unsigned key = key_of(peak);
+    int reach = __syncthreads_count(key != 0);
+    if (reach < want) return -FLT_MAX;
+    unsigned lo = key_of(-block_max(key ? -peak : -kInf, sh)), hi = key_of(largest);
+    for (int i = 0; i < 20 && lo < hi && reach > want + (want >> 2); ++i) {
+        const unsigned mid = lo + (hi - lo) / 2 + 1;
+        const int c = __syncthreads_count(key >= mid);
+        if (c >= want) {
+            lo = mid;
+            reach = c;
+        } else {
+            hi = mid - 1;
         }
     }
-    __syncthreads();
-    if (sh.cut == kCutBins) return -FLT_MAX;
-    if (sh.cut == kCutBins - 1 || scale == 0.0f) return low;
-    // the lower edge of that bin, moved down by more than the roundings of the bin numbers
-    const float width = (L - low) / (kCutBins - 1);
-    return L - (static_cast<float>(sh.cut) + 1.0f) * width - 4e-6f * fmaxf(fabsf(L), fabsf(low));
+    return of_key(lo);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -587,66 +566,79 @@ struct Kept {
     float L, inv, tau, low;
 };
 
-// Lanes whose maximum reaches the cut put their tokens at or above it into the leader's list, as
-// (key, ~index), into this CTA's part of it; their number goes to every CTA. Entries past the
-// part's end are only counted.
-template <typename T>
+// Lanes whose maximum reaches the cut put their tokens at or above it, as (key, ~index), into this
+// CTA's part of the list, and the CTA sends that to the leader's list and its number, its weight
+// (kMass) and, if it is this CTA's own, the cut to every CTA. Entries past the part's end are only counted.
+template <typename T, bool kMass>
 __device__ __forceinline__ void collect(const Row<T> &R, float peak, float cut, u64 *list, int part, unsigned rank,
-                                        int cluster, Shared &sh)
+                                        int cluster, const Kept &keep, bool tell_cut, Shared &sh)
 {
     constexpr int n = Row<T>::n;
-    if (threadIdx.x == 0) sh.mine = 0;
+    const int tid = threadIdx.x;
+    u64 *mine = list + rank * part;
+    if (tid == 0) sh.mine = 0;
     __syncthreads();
     if (peak >= cut) {
-        const unsigned to = remote(list + rank * part, 0);
+#pragma unroll 2
         for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-            float f[n];
-            Vec<T>::get(R.vec[j], f);
+            const uint4 v = R.vec[j];
+            Largest<T> m;
+            m.add(v);
+            if (m.get() >= cut) {
+                float f[n];
+                Vec<T>::get(v, f);
 #pragma unroll
-            for (int e = 0; e < n; ++e)
-                if (f[e] >= cut) {
-                    const unsigned at = atomicAdd(&sh.mine, 1u);
-                    const auto index = static_cast<unsigned>(R.base + j * n + e);
-                    if (at < static_cast<unsigned>(part))
-                        put(to + at * 8u, (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index));
-                }
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x < cluster) put(remote(&sh.count[rank], threadIdx.x), sh.mine);
-}
-
-// The leader's list closed up (parts of `part` entries, count[c] of them used), padded with zeros
-// to a power of two, the largest entry first. Returns the padded length.
-__device__ int close_and_sort(u64 *list, int part, int cluster, const unsigned *count)
-{
-    const int tid = threadIdx.x;
-    int total = 0;
-    u64 mine[kList / kThreads];
-    int at[kList / kThreads];
-#pragma unroll
-    for (int q = 0; q < kList / kThreads; ++q) at[q] = -1;
-    for (int c = 0; c < cluster; ++c) {
-        const int n = static_cast<int>(count[c]);
-#pragma unroll
-        for (int q = 0; q < kList / kThreads; ++q) {
-            const int i = tid + q * kThreads - c * part;
-            if (i >= 0 && i < n) {
-                mine[q] = list[tid + q * kThreads];
-                at[q] = total + i;
+                for (int e = 0; e < n; ++e)
+                    if (f[e] >= cut) {
+                        const unsigned at = atomicAdd(&sh.mine, 1u);
+                        const auto index = static_cast<unsigned>(R.base + j * n + e);
+                        if (at < static_cast<unsigned>(part))
+                            mine[at] = (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index);
+                    }
             }
         }
-        total += n;
     }
-    int size = 1;
-    while (size < total) size *= 2;
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kList / kThreads; ++q)
-        if (at[q] >= 0) list[at[q]] = mine[q];
-    for (int i = total + tid; i < size; i += kThreads) list[i] = 0;
-    __syncthreads();
-    return size;
+    const int count = static_cast<int>(sh.mine);
+    u64 w = 0;
+    for (int i = tid; i < min(count, part); i += kThreads) {
+        const u64 e = mine[i];
+        if (kMass) w += weight(exp_weight(delta(of_key(static_cast<unsigned>(e >> 32)), keep.L, keep.inv)));
+        if (rank != 0) put(remote(mine + i, 0), e);
+    }
+    if (kMass) {
+        u64 all;
+        block_scan(w, sh.box, &all);
+        if (tid < cluster) put(remote(&sh.listed[rank], tid), all);
+    }
+    if (tid < cluster) {
+        put(remote(&sh.count[rank], tid), static_cast<unsigned>(count));
+        if (tell_cut) put(remote(&sh.cut[rank], tid), __float_as_uint(cut));
+    }
+}
+
+// Whether every CTA's candidates found place; *total: their number.
+__device__ __forceinline__ bool all_listed(const Shared &sh, int cluster, int part, int *total)
+{
+    bool fits = true;
+    int n = 0;
+    for (int c = 0; c < cluster; ++c) {
+        fits &= sh.count[c] <= static_cast<unsigned>(part);
+        n += static_cast<int>(sh.count[c]);
+    }
+    *total = n;
+    return fits;
+}
+
+// Entry i of the leader's list, whose parts are filled from their beginnings; 0 past the end.
+__device__ __forceinline__ u64 listed_entry(const u64 *list, int part, int cluster, const Shared &sh, int i)
+{
+    for (int c = 0; c < cluster; ++c) {
+        const int n = static_cast<int>(sh.count[c]);
+        if (i < n) return list[c * part + i];
+        i -= n;
+    }
+    return 0;
 }
 
 // Bitonic sort of `size` (a power of two) entries, the largest first.
@@ -677,94 +669,220 @@ struct Target {
     __device__ __forceinline__ bool passed(u64 c) const { return c >= least; }
 };
 
-// The leader's work where its list holds every token that can be kept: the sorted list's weights
-// are summed up, the three constraints cut it off, and what is left is put in index order and
-// summed again for the draw.
-template <typename T>
-__device__ void finish_list(const SampleParams &P, const T *row, long long r, u64 *list, u64 *sums, int part, int k,
-                            float p, u64 Z, float u, const Kept &keep, Shared &sh)
+// The d of a listed key: of the row's largest logit 0, also where that is +inf.
+__device__ __forceinline__ float listed_delta(unsigned key, const Kept &keep)
+{
+    const float l = of_key(key);
+    return l == keep.L ? 0.0f : delta(l, keep.L, keep.inv);
+}
+
+// What the leader leaves of a drawn or kept entry.
+struct Drawn {
+    const SampleParams &P;
+    long long r;
+    const Kept &keep;
+    __device__ __forceinline__ void token(u64 entry, u64 Z) const
+    {
+        P.tokens[r] = static_cast<int>(~static_cast<unsigned>(entry));
+        if (P.logprob) P.logprob[r] = log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z);
+    }
+    __device__ __forceinline__ void prob(u64 entry, float z) const
+    {
+        P.probs[r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry))] =
+            __fdiv_rn(sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)), z);
+    }
+};
+
+// The key of the k-th largest of the block's entries (each thread's `mine`, 0 for none; at least k
+// of them), by halving the span from lo, which all of them reach, to hi, the largest, until just k
+// reach it or it is found. Of bf16 logits the upper half of the key says all.
+template <typename T, int kMine>
+__device__ unsigned kth_key(const u64 (&mine)[kMine], int used, int k, unsigned lo, unsigned hi)
+{
+    constexpr int drop = sizeof(T) == 2 ? 16 : 0;
+    lo >>= drop;
+    hi >>= drop;
+    while (lo < hi) {
+        const unsigned mid = lo + (hi - lo) / 2 + 1;
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+            if (q < used) c += __syncthreads_count(static_cast<unsigned>(mine[q] >> 32) >> drop >= mid);
+        if (c == k) return mid << drop;
+        if (c > k) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo << drop;
+}
+
+// The draw from `count` entries of work[0, count) with their weights in wts, at most kPairs of them:
+// what lies above each in value, and then before each in index, is summed over all pairs, several
+// threads to an entry.
+__device__ void draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums, int count, float p, u64 Z, float u,
+                           Shared &sh)
 {
     const int tid = threadIdx.x;
-    int size = close_and_sort(list, part, P.cluster, sh.count);
+    int each = 32;  // threads side by side, one for each entry
+    while (each < count) each *= 2;
+    const int ways = kThreads / each, i = tid & (each - 1), way = tid / each;
+    const int from = way * ((count + ways - 1) / ways), to = min(from + (count + ways - 1) / ways, count);
+    const u64 entry = i < count ? work[i] : 0;
+    const auto key = static_cast<unsigned>(entry >> 32);
+    bool keep = i < count && listed_delta(key, out.keep) >= out.keep.low;
+    if (p < 1.0f) {
+        u64 above = 0;
+        for (int j = from; j < to; ++j)
+            if (static_cast<unsigned>(work[j] >> 32) > key) above += wts[j];
+        part_sums[tid] = above;
+        __syncthreads();
+        above = 0;
+        for (int w = 0; w < ways; ++w) above += part_sums[w * each + i];
+        keep = keep && above < share_of(p, Z);
+        __syncthreads();
+    }
+    const bool first = way == 0;
+    const u64 w = keep ? wts[i] : 0;
+    u64 kept;
+    block_scan(first ? w : 0, sh.box, &kept);  // (its barriers also stand between the uses of wts)
+    if (first && i < count) wts[i] = w;
+    __syncthreads();
+    const auto index = static_cast<unsigned>(~static_cast<unsigned>(entry));
+    u64 upto = 0;
+    for (int j = from; j < to; ++j)
+        if (~static_cast<unsigned>(work[j]) <= index) upto += wts[j];
+    part_sums[tid] = upto;
+    __syncthreads();
+    if (first && keep) {
+        upto = 0;
+        for (int v = 0; v < ways; ++v) upto += part_sums[v * each + i];
+        const Target target(u, kept);
+        if (target.passed(upto) && !target.passed(upto - w)) out.token(entry, kept);
+        if (out.P.probs) out.prob(entry, as_sum(kept));
+    }
+}
+
+// The same for more entries, `size` (a power of two, the rest filled with zeros) of them: sorted by
+// value and summed up, cut off, sorted by index and summed up again.
+__device__ void draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, float p, u64 Z, float u, Shared &sh)
+{
+    const int tid = threadIdx.x;
     sort_down(list, size);
     const int q = (size + kThreads - 1) / kThreads;  // contiguous entries of a thread
     u64 own = 0, all;
     auto weight_of = [&](u64 entry) {
-        const auto key = static_cast<unsigned>(entry >> 32);
-        return key ? weight(exp_weight(delta(of_key(key), keep.L, keep.inv))) : 0ull;
+        return entry ? weight(exp_weight(listed_delta(static_cast<unsigned>(entry >> 32), out.keep))) : 0ull;
     };
     for (int i = tid * q; i < min(tid * q + q, size); ++i) own += weight_of(list[i]);
     u64 run = block_scan(own, sh.box, &all);
-    int valid = size;
     for (int i = tid * q; i < min(tid * q + q, size); ++i) {
         run += weight_of(list[i]);
         sums[i] = run;  // up to and with entry i
-        if (list[i] == 0) valid = min(valid, i);
     }
-    if (tid == 0) {
-        sh.first = size;
-        sh.found = size;
+    if (tid == 0) sh.found = size;
+    __syncthreads();
+    const u64 need = p < 1.0f ? share_of(p, Z) : 0;
+    for (int i = tid; i < size; i += kThreads) {
+        const u64 e = list[i];
+        bool out_of = e == 0 || listed_delta(static_cast<unsigned>(e >> 32), out.keep) < out.keep.low;
+        if (p < 1.0f && i > 0 && static_cast<unsigned>(e >> 32) != static_cast<unsigned>(list[i - 1] >> 32))
+            out_of |= sums[i - 1] >= need;
+        if (out_of) atomicMin(&sh.found, i);
     }
     __syncthreads();
-    atomicMin(&sh.first, valid);
-    __syncthreads();
-    valid = sh.first;
-    int kept = valid;
-    if (k > 0 && k < valid) {
-        const auto kth = static_cast<unsigned>(list[k - 1] >> 32);
-        for (int i = tid; i < valid; i += kThreads)
-            if (static_cast<unsigned>(list[i] >> 32) < kth) atomicMin(&sh.found, i);
-        __syncthreads();
-        kept = min(kept, sh.found);
-        __syncthreads();
-    }
-    const u64 need = p < 1.0f ? share_of(p, k > 0 ? sums[kept - 1] : Z) : 0;
-    for (int i = tid; i < kept; i += kThreads) {
-        const auto key = static_cast<unsigned>(list[i] >> 32);
-        bool out = delta(of_key(key), keep.L, keep.inv) < keep.low;
-        if (p < 1.0f && i > 0 && key != static_cast<unsigned>(list[i - 1] >> 32))
-            out |= sums[i - 1] >= need;
-        if (out) atomicMin(&sh.found, i);
-    }
-    __syncthreads();
-    kept = min(kept, sh.found);
+    const int kept = sh.found;
     const u64 Zk = sums[kept - 1];
-    if (P.probs) {
-        float *probs = P.probs + r * P.probs_stride;
-        const float z = as_sum(Zk);
-        for (int i = tid; i < kept; i += kThreads) {
-            const u64 e = list[i];
-            probs[static_cast<int>(~static_cast<unsigned>(e))] =
-                __fdiv_rn(sv::exp_f32(delta(of_key(static_cast<unsigned>(e >> 32)), keep.L, keep.inv)), z);
-        }
-    }
-    __syncthreads();
-    // index order: (~index, place) the largest first
-    size = 1;
-    while (size < kept) size *= 2;
+    if (out.P.probs)
+        for (int i = tid; i < kept; i += kThreads) out.prob(list[i], as_sum(Zk));
+    // index order: (~index, key), the largest first; the weight follows from the key again
     for (int i = tid; i < size; i += kThreads)
-        list[i] = i < kept ? (list[i] << 32) | static_cast<unsigned>(i) : 0;
+        list[i] = i < kept ? (list[i] << 32) | (list[i] >> 32) : 0;
     __syncthreads();
     sort_down(list, size);
-    const int qk = (size + kThreads - 1) / kThreads;
-    auto weight_at = [&](int i) {
-        const auto place = static_cast<unsigned>(list[i]);
-        return sums[place] - (place ? sums[place - 1] : 0);
-    };
+    auto turned = [&](int i) { return (list[i] << 32) | (list[i] >> 32); };
     own = 0;
-    for (int i = tid * qk; i < min(tid * qk + qk, kept); ++i) own += weight_at(i);
+    for (int i = tid * q; i < min(tid * q + q, kept); ++i) own += weight_of(turned(i));
     run = block_scan(own, sh.box, &all);
     const Target target(u, Zk);
-    for (int i = tid * qk; i < min(tid * qk + qk, kept); ++i) {
-        const u64 next = run + weight_at(i);
-        if (target.passed(next) && !target.passed(run)) {
-            const int token = static_cast<int>(~static_cast<unsigned>(list[i] >> 32));
-            P.tokens[r] = token;
-            const float l = as_float(__ldg(row + token));
-            if (P.logprob) P.logprob[r] = log_prob(l == kInf ? 0.0f : delta(l, keep.L, keep.inv), Zk);
-        }
+    for (int i = tid * q; i < min(tid * q + q, kept); ++i) {
+        const u64 next = run + weight_of(turned(i));
+        if (target.passed(next) && !target.passed(run)) out.token(turned(i), Zk);
         run = next;
     }
+}
+
+// The leader's work on its list of `total` candidates. With k > 0 they hold the row's k largest for
+// sure where every CTA listed its own k largest, and otherwise where k of them reach the largest of
+// the CTAs' cuts (false is returned if not); the row's largest logit is among them in any case.
+template <typename T>
+__device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *sums, int part, int total, int k,
+                            bool sure, float p, u64 Z, float u, Kept &keep, Shared &sh)
+{
+    constexpr int kMine = kList / kThreads;
+    const int tid = threadIdx.x, cluster = P.cluster;
+    u64 mine[kMine];
+    unsigned top = 0;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+        const int i = tid + q * kThreads;
+        mine[q] = i < total ? listed_entry(list, part, cluster, sh, i) : 0;
+        top = max(top, static_cast<unsigned>(mine[q] >> 32));
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((tid & 31) == 0) sh.small[tid >> 5] = static_cast<int>(top);
+    if (tid == 0) sh.mine = 0;
+    __syncthreads();
+    top = __reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(sh.small[tid & (kWarps - 1)]));
+    keep.L = of_key(top);
+    if (k > 0) {
+        float low = kInf, high = -kInf;
+        for (int c = 0; c < cluster; ++c) {
+            low = fminf(low, sh.cut[c]);
+            high = fmaxf(high, sh.cut[c]);
+        }
+        if (!sure && high > -FLT_MAX) {
+            int c = 0;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) c += __syncthreads_count(static_cast<unsigned>(mine[q] >> 32) >= key_of(high));
+            if (c < k) return false;
+        }
+        if (k < total) {
+            const unsigned kth = kth_key<T>(mine, (total + kThreads - 1) / kThreads, k, key_of(low), top);
+#pragma unroll
+            for (int q = 0; q < kMine; ++q)
+                if (static_cast<unsigned>(mine[q] >> 32) < kth) mine[q] = 0;
+        }
+    }
+    // the entries left, in any order, closed up
+    u64 w = 0;
+    u64 *work = list, *wts = sums;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, mine[q] != 0);
+        int at = 0;
+        if ((tid & 31) == 0 && some) at = static_cast<int>(atomicAdd(&sh.mine, __popc(some)));
+        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(some & ((1u << (tid & 31)) - 1));
+        if (mine[q]) {
+            const u64 x = weight(exp_weight(listed_delta(static_cast<unsigned>(mine[q] >> 32), keep)));
+            w += x;
+            work[at] = mine[q];
+            wts[at] = x;
+        }
+    }
+    u64 all;
+    block_scan(w, sh.box, &all);
+    const int count = static_cast<int>(sh.mine);
+    if (k > 0 || P.top_p == nullptr || !(p < 1.0f)) Z = all;
+    const Drawn out{P, r, keep};
+    if (count <= kPairs) {
+        draw_pairs(out, work, wts, sums + kPairs, count, p, Z, u, sh);
+    } else {
+        int size = 1;
+        while (size < count) size *= 2;
+        for (int i = count + tid; i < size; i += kThreads) list[i] = 0;
+        __syncthreads();
+        draw_sorted(out, list, sums, size, p, Z, u, sh);
+    }
+    return true;
 }
 
 template <bool kAll>
@@ -924,8 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     const long long r = blockIdx.x / cluster;
     const T *row = logits + r * P.stride;
     u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
-    u64 *sums = list + kList;                           // (the leader's, after the lane maxima)
-    float *peaks = reinterpret_cast<float *>(sums);     // a maximum of every lane of the cluster
+    u64 *sums = list + kList;
     Row<T> R = start_row(row, P.V, P.split, store, rank);
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
     const int part = kList / cluster;
@@ -940,22 +1057,88 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     float *probs = P.probs ? P.probs + r * P.probs_stride : nullptr;
     if (probs && !open)  // zeros while the logits come; what is kept goes over them
         for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
-
     // (in binary64, by one thread, while the logits come)
     if (m > 0.0f && tid == 0) sh.d = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
     float peak = lane_max(R);
+    const float largest = block_max(peak, sh);
     cluster_wait();
-    for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
+
+    if (greedy) {  // each CTA's first largest, and the first largest of those
+        if (tid == 0) sh.first = INT_MAX;
+        __syncthreads();
+        if (peak == largest && peak > -kInf) {
+            int best = INT_MAX;
+            for (int j = R.lo + R.lane; j < R.hi && best == INT_MAX; j += 32) {
+                float f[Row<T>::n];
+                Vec<T>::get(R.vec[j], f);
+                for (int e = Row<T>::n - 1; e >= 0; --e)
+                    if (f[e] == largest) best = R.base + j * Row<T>::n + e;
+            }
+            atomicMin(&sh.first, best);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            put(remote(&sh.count[rank], 0), static_cast<unsigned>(sh.first));
+            put(remote(&sh.peak[rank], 0), __float_as_uint(largest));
+        }
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+            int best = -1;
+            float L = -kInf;
+            for (int c = 0; c < cluster; ++c)
+                if (sh.peak[c] > L) {
+                    L = sh.peak[c];
+                    best = static_cast<int>(sh.count[c]);
+                }
+            P.tokens[r] = best;
+            if (P.logprob) P.logprob[r] = best < 0 ? -kInf : 0.0f;
+            if (probs && best >= 0) probs[best] = 1.0f;
+        }
+        return;
+    }
+
+    Kept keep{0.0f, inverse(temp), -FLT_MAX, m > 0.0f ? sh.d : -kInf};
+    int total;
+    if (k > 0) {
+        // the k largest: of every CTA at least its own k largest, or as many as find place
+        const int most = part / 8 * 5;
+        const float cut = cut_for(peak, largest, min(k, most), sh);
+        collect<T, false>(R, peak, cut, list, part, rank, cluster, keep, true, sh);
+        cluster_sync();
+        if (all_listed(sh, cluster, part, &total)) {
+            if (total == 0) {  // nothing to keep
+                if (rank == 0 && tid == 0) {
+                    P.tokens[r] = -1;
+                    if (P.logprob) P.logprob[r] = -kInf;
+                }
+                return;
+            }
+            if (k <= most) {
+                if (rank == 0) finish_list<T>(P, r, list, sums, part, total, k, true, p, 0, u, keep, sh);
+                return;
+            }
+            if (rank == 0) {
+                const bool done = finish_list<T>(P, r, list, sums, part, total, k, false, p, 0, u, keep, sh);
+                if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
+            }
+            cluster_sync();
+            if (sh.fits) return;
+        }
+    }
+    // the row's largest logit
+    const bool mass = p < 1.0f && k == 0;  // the top-p set's total is the whole row's
+    const float own_cut = mass ? cut_for(peak, largest, kTopP, sh) : 0.0f;
+    if (tid < cluster) {
+        put(remote(&sh.peak[rank], tid), __float_as_uint(largest));
+        put(remote(&sh.cut[rank], tid), __float_as_uint(own_cut));
+    }
     cluster_sync();
-    float L = -kInf;
-    for (int c = 0; c < cluster; ++c) L = fmaxf(L, peaks[c * kThreads + tid]);
-    L = warp_max(L);
-    if (R.lane == 0) reinterpret_cast<float *>(sh.box)[R.warp] = L;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) L = fmaxf(L, reinterpret_cast<float *>(sh.box)[w]);
-    __syncthreads();
-    if (!(L > -kInf)) {  // nothing to keep
+    float L = -kInf, cut = -FLT_MAX;
+    for (int c = 0; c < cluster; ++c) {
+        L = fmaxf(L, sh.peak[c]);
+        cut = fmaxf(cut, sh.cut[c]);
+    }
+    if (!(L > -kInf)) {
         if (rank == 0 && tid == 0) {
             P.tokens[r] = -1;
             if (P.logprob) P.logprob[r] = -kInf;
@@ -970,76 +1153,34 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
             for (int i = 0; i < Row<T>::n; ++i) e[i] = as_float(e[i]) == kInf ? T(0) : Low<T>::value();
         }
         peak = peak == kInf ? 0.0f : -kInf;
-        for (int c = 0; c < cluster; ++c) peaks[c * kThreads + tid] = peaks[c * kThreads + tid] == kInf ? 0.0f : -kInf;
-        L = 0.0f;
+        L = cut = 0.0f;
         __syncthreads();
     }
-    if (greedy) {
-        if (tid == 0) sh.first = INT_MAX;
-        __syncthreads();
-        if (peak == L) {
-            int best = INT_MAX;
-            for (int j = R.lo + R.lane; j < R.hi && best == INT_MAX; j += 32) {
-                float f[Row<T>::n];
-                Vec<T>::get(R.vec[j], f);
-                for (int e = Row<T>::n - 1; e >= 0; --e)
-                    if (f[e] == L) best = R.base + j * Row<T>::n + e;
-            }
-            atomicMin(&sh.first, best);
-        }
-        __syncthreads();
-        if (tid == 0) put(remote(&sh.count[rank], 0), static_cast<unsigned>(sh.first));
-        cluster_sync();
-        if (rank == 0 && tid == 0) {
-            int best = INT_MAX;
-            for (int c = 0; c < cluster; ++c) best = min(best, static_cast<int>(sh.count[c]));
-            P.tokens[r] = best;
-            if (P.logprob) P.logprob[r] = 0.0f;
-            if (probs) probs[best] = 1.0f;
-        }
-        return;
-    }
-
-    Kept keep{L, inverse(temp), -FLT_MAX, -kInf};
-    if (m > 0.0f) keep.low = sh.d;
+    keep.L = L;
     Exchange ex{sh, rank, cluster, 0};
     if (open) {
         draw_row<T, true>(P, R, r, u, keep, ex);
         return;
     }
-    const bool mass = p < 1.0f && k == 0;  // the top-p set's total is the whole row's
-    if (k <= kList / 2) {
-        float cut;
-        if (k > 0 || mass) cut = cut_for(peaks, cluster * kThreads, L, k > 0 ? k : kTopP, sh);
-        else cut = fmaxf(L + keep.low / keep.inv - 4e-6f * (fabsf(L) + fabsf(keep.low / keep.inv)), -FLT_MAX);
-        collect(R, peak, cut, list, part, rank, cluster, sh);
+    if (k == 0) {
         u64 Z = 0;
-        if (mass) Z = ex.sum(warp_weight<T, true>(R, keep));
-        else cluster_sync();
-        int total = 0;
-        bool fits = true;
-        for (int c = 0; c < cluster; ++c) {
-            fits &= sh.count[c] <= static_cast<unsigned>(part);
-            total += static_cast<int>(sh.count[c]);
-        }
-        fits &= k <= total || cut == -FLT_MAX;
-        if (fits && mass && cut > -FLT_MAX) {
-            // whether the listed tokens reach P of the whole: the leader sums them up
-            if (rank == 0) {
-                u64 s = 0, all;
-                for (int i = tid; i < kList; i += kThreads) {
-                    const int c = i / part;
-                    if (i - c * part < static_cast<int>(sh.count[c]))
-                        s += weight(exp_weight(delta(of_key(static_cast<unsigned>(list[i] >> 32)), L, keep.inv)));
-                }
-                block_scan(s, sh.box, &all);
-                if (tid < cluster) put(remote(&sh.cut, tid), static_cast<unsigned>(all >= share_of(p, Z)));
-            }
+        if (mass) {
+            collect<T, true>(R, peak, cut, list, part, rank, cluster, keep, false, sh);
+            Z = ex.sum(warp_weight<T, true>(R, keep));
+        } else {
+            const float span = keep.low / keep.inv;
+            cut = fmaxf(L + span - 4e-6f * (fabsf(L) + fabsf(span)), -FLT_MAX);
+            collect<T, false>(R, peak, cut, list, part, rank, cluster, keep, false, sh);
             cluster_sync();
-            fits = sh.cut != 0;
+        }
+        bool fits = all_listed(sh, cluster, part, &total);
+        if (fits && mass && cut > -FLT_MAX) {  // do the listed tokens reach P of the whole?
+            u64 listed = 0;
+            for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
+            fits = listed >= share_of(p, Z);
         }
         if (fits) {
-            if (rank == 0) finish_list(P, row, r, list, sums, part, k, p, Z, u, keep, sh);
+            if (rank == 0) finish_list<T>(P, r, list, sums, part, total, 0, true, p, Z, u, keep, sh);
             return;
         }
     }
@@ -1104,7 +1245,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
     const long long r = blockIdx.x / cluster;
     const T *row = logits + r * P.stride;
     u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
-    float *peaks = reinterpret_cast<float *>(list + kList);
+    u64 *work = list + kList;
     const int token = P.tokens ? row_token(P, r) : 0;
     const bool wanted = token >= 0 && token < P.V;
     if (!wanted) {
@@ -1174,8 +1315,12 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         put(remote(&sh.seg[0][rank * kWarps + R.warp], 0), pack(top_of_warp, s));
         put(remote(&sh.seg[1][rank * kWarps + R.warp], 0), static_cast<u64>(larger));
     }
-    if (top > 0)
-        for (int c = 0; c < cluster; ++c) put(remote(peaks + rank * kThreads + tid, c), __float_as_uint(peak));
+    const int part = kList / cluster;
+    if (top > 0) {
+        const float largest = block_max(peak, sh);
+        const float cut = largest > -kInf && largest < kInf ? cut_for(peak, largest, min(top, part / 8 * 5), sh) : -FLT_MAX;
+        collect<T, false>(R, peak, cut, list, part, rank, cluster, Kept{}, true, sh);
+    }
     cluster_sync();
     float L = -kInf;
     float norm = 0.0f;
@@ -1203,14 +1348,6 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         }
     }
     if (top == 0) return;
-    L = -kInf;
-    for (int c = 0; c < cluster; ++c) L = fmaxf(L, peaks[c * kThreads + tid]);
-    L = warp_max(L);
-    if (R.lane == 0) reinterpret_cast<float *>(sh.box)[R.warp] = L;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) L = fmaxf(L, reinterpret_cast<float *>(sh.box)[w]);
-    __syncthreads();
     auto write = [&](int i, u64 entry) {
         const auto index = static_cast<int>(~static_cast<unsigned>(entry));
         const float l = entry ? of_key(static_cast<unsigned>(entry >> 32)) : -kInf;
@@ -1218,30 +1355,44 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         P.top_ids[r * top + i] = entry ? index : -1;
         P.top_logprob[r * top + i] = entry ? d - norm : -kInf;
     };
-    if (!(L > -kInf)) {
-        if (rank == 0)
-            for (int i = tid; i < top; i += kThreads) write(i, 0);
-        return;
-    }
-    // a row with tokens at +inf: a cut below every finite one, which lists them all or none fit
-    const float cut = L < kInf ? cut_for(peaks, cluster * kThreads, L, top, sh) : -FLT_MAX;
-    const int part = kList / cluster;
-    collect(R, peak, cut, list, part, rank, cluster, sh);
-    cluster_sync();
-    bool fits = true;
-    int total = 0;
-    for (int c = 0; c < cluster; ++c) {
-        fits &= sh.count[c] <= static_cast<unsigned>(part);
-        total += static_cast<int>(sh.count[c]);
-    }
-    if (fits && (total >= top || cut == -FLT_MAX)) {
-        if (rank != 0) return;
-        const int size = close_and_sort(list, part, cluster, sh.count);
-        sort_down(list, size);
-        for (int i = tid; i < top; i += kThreads) write(i, i < size ? list[i] : 0);
-        return;
+    int total;
+    if (all_listed(sh, cluster, part, &total)) {
+        const bool sure = top <= part / 8 * 5;  // every CTA listed its own `top` largest
+        if (rank == 0) {
+            // an entry's place is the number of larger ones; past the row's tokens nothing is left
+            bool done = true;
+            float high = -FLT_MAX;
+            for (int c = 0; c < cluster; ++c) high = fmaxf(high, sh.cut[c]);
+            for (int i = total + tid; i < top; i += kThreads) write(i, 0);
+            u64 mine[kList / kThreads];
+#pragma unroll
+            for (int q = 0; q < kList / kThreads; ++q)
+                mine[q] = tid + q * kThreads < total ? listed_entry(list, part, cluster, sh, tid + q * kThreads) : 0;
+#pragma unroll
+            for (int q = 0; q < kList / kThreads; ++q)
+                if (mine[q]) work[tid + q * kThreads] = mine[q];
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < kList / kThreads; ++q)
+                if (mine[q]) {
+                    int place = 0;
+                    for (int j = 0; j < total; ++j) place += work[j] > mine[q];
+                    if (place < top) {
+                        write(place, mine[q]);
+                        done &= of_key(static_cast<unsigned>(mine[q] >> 32)) >= high;
+                    }
+                }
+            if (!sure) {
+                done = __syncthreads_and(done && (total >= top || high == -FLT_MAX));
+                if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
+            }
+        }
+        if (sure) return;
+        cluster_sync();
+        if (sh.fits) return;
     }
     // more ties than the list holds: one token after the other
+    cluster_sync();  // (the leader has read what the warps sent)
     Exchange ex{sh, rank, cluster, 0};
     u64 last = kNone64;
     for (int i = 0; i < top; ++i) {
@@ -1354,8 +1505,7 @@ Shape shape_of(int rows, int V, int elem_bytes, bool lists)
     s.cluster = c;
     s.split.per_warp = ((vectors + c - 1) / c + kWarps - 1) / kWarps;
     s.split.per_cta = s.split.per_warp * kWarps;
-    const size_t tail = std::max<size_t>(kList * 8, static_cast<size_t>(c) * kThreads * 4);
-    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + (lists ? kList * 8 + tail : 0);
+    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + (lists ? 2 * kList * 8 : 0);
     return s;
 }
 
