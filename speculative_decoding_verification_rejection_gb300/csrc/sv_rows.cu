@@ -31,6 +31,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kList = 1024;       // entries of the leader's candidate list
 constexpr int kStages = 4;        // portions in which a warp waits for its logits
+constexpr int kBins = 4096;       // bins of the value histogram, two to a word of `sums`
+constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr int kPairs = 256;       // most entries that are compared each with each
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
@@ -67,6 +69,13 @@ __device__ __forceinline__ unsigned remote(const void *p, unsigned rank)
 }
 __device__ __forceinline__ void put(unsigned a, unsigned v) { asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ void put(unsigned a, u64 v) { asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory"); }
+
+__device__ __forceinline__ uint4 get16(unsigned a)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
 
 __device__ __forceinline__ void copy16(void *dst, const void *src)
 {
@@ -417,6 +426,7 @@ struct Shared {
     float cut[kMaxCluster], peak[kMaxCluster];
     int small[kWarps];
     unsigned mine, fits;
+    float upper, lower;
     int first, found;
     float d;
 };
@@ -946,26 +956,198 @@ struct Exchange {
     }
 };
 
-// The largest key such that the keys at least as large, of those from `floor` on, hold `need`
-// tokens or, with kMass, the weight `need`: bit by bit, one pass over the row for each.
+// How much the tokens from l >= bound on hold: tokens or, with kMass, weight; of those >= keep.tau.
 template <typename T, bool kMass>
-__device__ unsigned search_key(const Row<T> &R, const Kept &keep, unsigned floor, u64 need, Exchange &ex)
+__device__ u64 held_from(const Row<T> &R, const Kept &keep, float bound, Exchange &ex)
 {
     constexpr int n = Row<T>::n;
-    unsigned found = 0;
-    for (unsigned bit = 0x80000000u; bit; bit >>= 1) {
-        const unsigned trial = max(found | bit, floor);
-        u64 m = 0;
-        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-            float f[n];
-            Vec<T>::get(R.vec[j], f);
+    Kept k = keep;
+    k.tau = fmaxf(bound, keep.tau);
+    k.low = -kInf;
+    if (kMass) return ex.sum(warp_weight<T, false>(R, k));
+    int c = 0;
+    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        float f[n];
+        Vec<T>::get(R.vec[j], f);
+#pragma unroll
+        for (int e = 0; e < n; ++e) c += f[e] >= k.tau;
+    }
+    return ex.sum(warp_sum(static_cast<u64>(c)));
+}
+
+// The largest key in [lo, hi] such that the tokens with keys at least as large hold `need`, or 0
+// where those from lo on do not: by halving, one pass over the row for each step.
+template <typename T, bool kMass>
+__device__ unsigned search_key(const Row<T> &R, const Kept &keep, u64 need, unsigned lo, unsigned hi, Exchange &ex)
+{
+    constexpr int drop = sizeof(T) == 2 ? 16 : 0;  // (of bf16 logits the upper half of the key says all)
+    constexpr unsigned least = 0x00800000u;        // the key of the lowest finite number
+    lo >>= drop;
+    hi >>= drop;
+    if (held_from<T, kMass>(R, keep, of_key(max(lo << drop, least)), ex) < need) return 0;
+    while (lo < hi) {
+        const unsigned mid = lo + (hi - lo) / 2 + 1;
+        if (held_from<T, kMass>(R, keep, of_key(max(mid << drop, least)), ex) >= need) lo = mid;
+        else hi = mid - 1;
+    }
+    return max(lo << drop, least);
+}
+
+// The same over all keys, for rows whose kept set is too large for the list: the largest key such
+// that the tokens at least as large, of those >= keep.tau, hold `need`; `all` is what they hold
+// together. A histogram of the tokens by value (kBins bins of (L - l) / T) tells the bin it is in:
+// for counts exactly, for weights by the weights of the bins' middles, so that the neighbouring
+// bins are taken as well. One pass sums up what lies above them and lists what lies in them, and the
+// leader finds the key there. Where the bins hold more than the list, or the guess was wrong, it is
+// found by halving. Returns 0 where all tokens together do not hold `need`.
+template <typename T, bool kMass>
+__device__ unsigned find_key(const Row<T> &R, const Kept &keep, u64 need, u64 all, u64 *list, u64 *sums, int part,
+                             Exchange &ex)
+{
+    constexpr int n = Row<T>::n;
+    Shared &sh = ex.sh;
+    const int tid = threadIdx.x, cluster = ex.cluster;
+    auto *words = reinterpret_cast<unsigned *>(sums);
+    const float scale = keep.inv * (kBins / kSpan);
+    for (int i = tid; i < kBins / 2; i += kThreads) words[i] = 0;
+    __syncthreads();
+    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        float f[n];
+        Vec<T>::get(R.vec[j], f);
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            const float at = (keep.L - f[e]) * scale;
+            if (f[e] >= keep.tau && at < static_cast<float>(kBins)) {
+                const int b = static_cast<int>(at);
+                atomicAdd(words + (b >> 1), 1u << (16 * (b & 1)));  // (a CTA holds fewer than 2^16 tokens)
+            }
+        }
+    }
+    cluster_sync();
+    if (ex.rank == 0) {
+        constexpr int q = kBins / kThreads;  // bins of a thread
+        unsigned c[q] = {};
+        for (int k = 0; k < cluster; ++k)
+#pragma unroll
+            for (int i = 0; i < q / 8; ++i) {
+                const uint4 v = get16(remote(words + tid * (q / 2) + 4 * i, k));
+                const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    c[8 * i + 2 * e] += w[e] & 0xFFFFu;
+                    c[8 * i + 2 * e + 1] += w[e] >> 16;
+                }
+            }
+        u64 own = 0, total;
+        auto held = [&](int i) -> u64 {
+            if (!kMass) return c[i];
+            const float middle = (static_cast<float>(tid * q + i) + 0.5f) * (kSpan / kBins);
+            return static_cast<u64>(c[i]) * static_cast<unsigned>(0x1p+31f * sv::ex2_approx(-middle * kLog2e));
+        };
+#pragma unroll
+        for (int i = 0; i < q; ++i) own += held(i);
+        u64 run = block_scan(own, sh.box, &total);
+        const u64 want = kMass ? static_cast<u64>(as_sum(need) / as_sum(all) * __ull2float_rn(total)) : need;
+        if (tid == 0) sh.first = kBins;
+        __syncthreads();
+        if (run + own >= want && run < want) {
+#pragma unroll
+            for (int i = 0; i < q; ++i) {
+                run += held(i);
+                if (run >= want) atomicMin(&sh.first, tid * q + i);
+            }
+        }
+        __syncthreads();
+        const int b = sh.first, around = kMass ? 1 : 0;
+        const float width = kSpan / kBins / keep.inv, slack = 4e-6f * fmaxf(fabsf(keep.L), kSpan / keep.inv);
+        // (a row beyond the last bin: everything, which the halving then has to do)
+        const float upper = b - around <= 0 ? keep.L : keep.L - static_cast<float>(b - around) * width + slack;
+        const float lower = b >= kBins - 2 ? -FLT_MAX : keep.L - static_cast<float>(b + around + 1) * width - slack;
+        if (tid < cluster) {
+            put(remote(&sh.upper, tid), __float_as_uint(upper));
+            put(remote(&sh.lower, tid), __float_as_uint(fmaxf(lower, -FLT_MAX)));
+        }
+    }
+    cluster_sync();
+    const float upper = sh.upper, lower = fmaxf(sh.lower, keep.tau);
+    if (tid == 0) sh.mine = 0;
+    __syncthreads();
+    u64 *mine = list + ex.rank * part;
+    WeightSum above;
+    int count = 0;
+#pragma unroll 2
+    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
+        float f[n];
+        Vec<T>::get(R.vec[j], f);
+        bool within = false;
+#pragma unroll
+        for (int e = 0; e < n; e += 2) {
+            if (kMass) {
+                float a, b;
+                parts(kept_weight<true>(f[e], f[e + 1], keep), a, b);
+                above.add(two(f[e] > upper ? a : 0.0f, f[e + 1] > upper ? b : 0.0f));
+            } else {
+                count += f[e] > upper;
+                count += f[e + 1] > upper;
+            }
+            within |= (f[e] >= lower && f[e] <= upper) || (f[e + 1] >= lower && f[e + 1] <= upper);
+        }
+        if (kMass) count += n;
+        if (within)
 #pragma unroll
             for (int e = 0; e < n; ++e)
-                if (key_of(f[e]) >= trial) m += kMass ? weight(exp_weight(delta(f[e], keep.L, keep.inv))) : 1ull;
-        }
-        if (ex.sum(warp_sum(m)) >= need) found |= bit;
+                if (f[e] >= lower && f[e] <= upper) {
+                    const unsigned at = atomicAdd(&sh.mine, 1u);
+                    if (at < static_cast<unsigned>(part)) mine[at] = static_cast<u64>(key_of(f[e])) << 32;
+                }
     }
-    return max(found, floor);
+    const u64 over_all = warp_sum(kMass ? above.total(count) : static_cast<u64>(count));
+    __syncthreads();
+    const int listed = static_cast<int>(sh.mine);
+    if (ex.rank != 0)
+        for (int i = tid; i < min(listed, part); i += kThreads) put(remote(mine + i, 0), mine[i]);
+    if (tid < cluster) put(remote(&sh.count[ex.rank], tid), static_cast<unsigned>(listed));
+    const u64 over = ex.sum(over_all);
+    int total;
+    unsigned found = 0;
+    if (over < need) {
+        if (all_listed(sh, cluster, part, &total)) {
+            if (ex.rank == 0) {
+                constexpr int kMine = kList / kThreads, drop = sizeof(T) == 2 ? 16 : 0;
+                unsigned key[kMine];
+                u64 w[kMine];
+#pragma unroll
+                for (int q = 0; q < kMine; ++q) {
+                    const int i = tid + q * kThreads;
+                    key[q] = i < total ? static_cast<unsigned>(listed_entry(list, part, cluster, sh, i) >> 32) : 0;
+                    w[q] = key[q] == 0 ? 0 : kMass ? weight(exp_weight(delta(of_key(key[q]), keep.L, keep.inv))) : 1;
+                }
+                auto from = [&](unsigned bound) {
+                    u64 m = 0, sum;
+#pragma unroll
+                    for (int q = 0; q < kMine; ++q) m += key[q] >> drop >= bound ? w[q] : 0;
+                    block_scan(m, sh.box, &sum);
+                    return over + sum;
+                };
+                unsigned lo = key_of(lower) >> drop, hi = key_of(upper) >> drop;
+                if (from(lo) >= need) {
+                    while (lo < hi) {
+                        const unsigned mid = lo + (hi - lo) / 2 + 1;
+                        if (from(mid) >= need) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    found = max(lo << drop, 1u);
+                }
+                if (tid < cluster) put(remote(&sh.fits, tid), found);
+            }
+            cluster_sync();
+            found = sh.fits;
+        } else {
+            found = search_key<T, kMass>(R, keep, need, key_of(lower), key_of(upper), ex);
+        }
+    }
+    if (found == 0) found = search_key<T, kMass>(R, keep, need, 0, key_of(keep.L), ex);
+    return found;
 }
 
 // The draw over the whole row: every warp's sum of kept weights goes to every CTA, the CTA that
@@ -1162,8 +1344,8 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         draw_row<T, true>(P, R, r, u, keep, ex);
         return;
     }
+    u64 Z = 0;
     if (k == 0) {
-        u64 Z = 0;
         if (mass) {
             collect<T, true>(R, peak, cut, list, part, rank, cluster, keep, false, sh);
             Z = ex.sum(warp_weight<T, true>(R, keep));
@@ -1184,16 +1366,14 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
             return;
         }
     }
-    unsigned floor = 1;
-    if (k > 0) floor = search_key<T, false>(R, keep, 1, static_cast<u64>(k), ex);
-    if (p < 1.0f) {
-        keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
-        Kept all = keep;
-        all.low = -kInf;
-        const u64 Z = ex.sum(warp_weight<T, false>(R, all));
-        floor = search_key<T, true>(R, keep, floor, share_of(p, Z), ex);
+    if (k > 0) {
+        const unsigned key = find_key<T, false>(R, keep, static_cast<u64>(k), 0, list, sums, part, ex);
+        if (key) keep.tau = of_key(key);
     }
-    keep.tau = floor > 1 ? of_key(floor) : -FLT_MAX;
+    if (p < 1.0f) {
+        if (!mass) Z = held_from<T, true>(R, keep, -FLT_MAX, ex);
+        keep.tau = of_key(find_key<T, true>(R, keep, share_of(p, Z), Z, list, sums, part, ex));
+    }
     draw_row<T, false>(P, R, r, u, keep, ex);
 }
 
