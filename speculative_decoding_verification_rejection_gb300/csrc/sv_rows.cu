@@ -17,6 +17,7 @@
 #include <cfloat>
 #include <climits>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "spec_verify.h"
@@ -28,16 +29,18 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
+constexpr int kAhead = 8;         // vectors a lane reads before it uses the first
+constexpr int kGroups = 8;        // groups of a lane's vectors whose maxima are kept
 constexpr int kList = 1024;       // entries of the leader's candidate list
-constexpr int kStages = 4;        // portions in which a warp waits for its logits
-constexpr int kBins = 4096;       // bins of the value histogram, two to a word of `sums`
-constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
+constexpr int kHits = 2048;       // groups a CTA looks through for candidates
 constexpr int kPairs = 256;       // most entries that are compared each with each
+constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
+constexpr int kWideList = 2048;   // the same of a bracket's tokens
+constexpr int kBins = 8192;       // bins of the value histogram, two to a word
+constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
-constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
-constexpr u64 kNone64 = ~0ull;
 
 // ---------------------------------------------------------------------------------------
 // thread-block clusters and asynchronous copies
@@ -77,22 +80,20 @@ __device__ __forceinline__ uint4 get16(unsigned a)
     return v;
 }
 
-__device__ __forceinline__ void copy16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
-
 // ---------------------------------------------------------------------------------------
 // logits and weights
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ float as_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ float as_float(float f) { return f; }
 template <typename T> struct Low;  // -inf in the logits' type
-template <> struct Low<uint16_t> { static __device__ __forceinline__ uint16_t value() { return 0xFF80u; } };
-template <> struct Low<float> { static __device__ __forceinline__ float value() { return -kInf; } };
+template <> struct Low<uint16_t> {
+    static constexpr unsigned word = 0xFF80FF80u;
+    static __device__ __forceinline__ uint16_t value() { return 0xFF80u; }
+};
+template <> struct Low<float> {
+    static constexpr unsigned word = 0xFF800000u;
+    static __device__ __forceinline__ float value() { return -kInf; }
+};
 
 // The logits of a 16-byte vector as binary32.
 template <typename T> struct Vec;
@@ -150,11 +151,11 @@ template <> struct Largest<float> {
     __device__ __forceinline__ float get() const { return fmaxf(a, b); }
 };
 
-// How many of the logits added are above a bound. A lane adds at most 64 vectors: the bf16 form
-// counts in bf16, which is exact up to 256 in each half.
+// How many of the logits added are above a bound. The bf16 form counts in bf16, which is exact up to
+// 256 in each half: flush() at the latest after 64 vectors.
 template <typename T> struct Above;
 template <> struct Above<uint16_t> {
-    unsigned bound, count = 0;
+    unsigned bound, part = 0, count = 0;
     explicit __device__ __forceinline__ Above(float l) { bound = __float_as_uint(l) >> 16; bound |= bound << 16; }
     __device__ __forceinline__ void add(const uint4 &v)
     {
@@ -163,13 +164,15 @@ template <> struct Above<uint16_t> {
         for (int i = 0; i < 4; ++i) {
             unsigned one;
             asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(one) : "r"(w[i]), "r"(bound));
-            asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(one));
+            asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(part) : "r"(one));
         }
     }
-    __device__ __forceinline__ unsigned get() const
+    __device__ __forceinline__ void flush()
     {
-        return static_cast<unsigned>(__uint_as_float(count << 16) + __uint_as_float(count & 0xFFFF0000u));
+        count += static_cast<unsigned>(__uint_as_float(part << 16) + __uint_as_float(part & 0xFFFF0000u));
+        part = 0;
     }
+    __device__ __forceinline__ unsigned get() const { return count; }
 };
 template <> struct Above<float> {
     float bound;
@@ -182,6 +185,7 @@ template <> struct Above<float> {
         count += __uint_as_float(v.z) > bound;
         count += __uint_as_float(v.w) > bound;
     }
+    __device__ __forceinline__ void flush() {}
     __device__ __forceinline__ unsigned get() const { return count; }
 };
 
@@ -214,6 +218,19 @@ __device__ __forceinline__ Two fma(Two a, Two b, Two c)
     Two r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
+}
+
+// A vector of a row whose largest logit is +inf: 0 for the tokens at +inf, which share the row, and
+// -inf for the others.
+template <typename T>
+__device__ __forceinline__ uint4 only_inf(uint4 v)
+{
+    T e[Vec<T>::n];
+    memcpy(e, &v, 16);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n; ++i) e[i] = as_float(e[i]) == kInf ? T(0) : Low<T>::value();
+    memcpy(&v, e, 16);
+    return v;
 }
 
 // Logits as order-preserving unsigned integers, 0 for what is never kept (NaN and -inf); -0 as +0.
@@ -275,6 +292,29 @@ __device__ __forceinline__ Two exp_weight(Two d)
     parts(ks, ka, kb);
     return two(__uint_as_float(__float_as_uint(pa) + (__float_as_uint(ka) << 23)),
                __uint_as_float(__float_as_uint(pb) + (__float_as_uint(kb) << 23)));
+}
+
+// sv::exp_f32 of two d <= 0.
+__device__ __forceinline__ Two exp_two(Two d)
+{
+    float da, db, a, b;
+    parts(d, da, db);
+    const Two x = two(fmaxf(da, -87.0f), fmaxf(db, -87.0f));
+    const Two ks = fma(x, two(0x1.715476p+0f), two(0x1.8p+23f));
+    const Two kf = ks + two(-0x1.8p+23f);
+    Two r = fma(kf, two(-0x1.62e430p-1f), x);
+    r = fma(kf, two(0x1.05c610p-29f), r);
+    Two p = fma(two(0x1.a01a02p-13f), r, two(0x1.6c16c2p-10f));
+    p = fma(p, r, two(0x1.111112p-7f));
+    p = fma(p, r, two(0x1.555556p-5f));
+    p = fma(p, r, two(0x1.555556p-3f));
+    p = fma(p, r, two(0.5f));
+    p = fma(p, r, two(1.0f));
+    p = fma(p, r, two(1.0f));
+    parts(ks, a, b);
+    p = p * two(__uint_as_float((__float_as_uint(a) + 127u) << 23), __uint_as_float((__float_as_uint(b) + 127u) << 23));
+    parts(p, a, b);
+    return two(da >= -87.0f ? a : 0.0f, db >= -87.0f ? b : 0.0f);
 }
 
 // An exact sum of weights in two 32-bit words. Adding 12 to t in [0, 1] rounds it to a multiple of
@@ -352,6 +392,15 @@ __device__ __forceinline__ float as_sum(u64 Z)
     return __fmul_rn(__uint2float_rn(top), __uint_as_float(static_cast<unsigned>(127 + s - 40) << 23));
 }
 
+// 2^40 / Z as binary32, to half a unit: a reciprocal and one correction by what it leaves of Z.
+__device__ __forceinline__ float inverse_sum(u64 Z)
+{
+    const float z = as_sum(Z);
+    const float rest = __ll2float_rn(static_cast<long long>(Z - __float2ull_rn(z * 0x1p+40f))) * 0x1p-40f;
+    const float r = __frcp_rn(z);
+    return __fmaf_rn(r, __fmaf_rn(-r, rest, __fmaf_rn(-r, z, 1.0f)), r);
+}
+
 // d - ln(Z 2^-40): Z 2^-40 = 2^k f, f in [sqrt(1/2), sqrt(2)); k ln 2 in two parts, the first with
 // so few bits that its product with k is exact.
 __device__ __forceinline__ float log_prob(float d, u64 Z)
@@ -414,116 +463,204 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
 // ---------------------------------------------------------------------------------------
 // The 16-byte vectors that hold the row are split evenly over the cluster's CTAs and then over
 // their warps, both in contiguous runs, so that the warps in order hold the row in index order; a
-// lane copies the vectors lane, lane + 32, ... of its warp's run to shared memory and is the
-// one to read them again, so no barrier stands between copy and use. Everything that follows
-// reads shared memory: each logit crosses the memory bus once. What of the first and last vector
-// lies outside the row is -inf; those two are copied element by element.
+// lane has the vectors lane, lane + 32, ... of its warp's run. Every pass reads them from global
+// memory: the first one from HBM, those after it from the L2 cache, which holds all rows in work.
+// (Rows copied to shared memory once were as fast where few are in work and slower where many
+// are, since then the 227 KB of an SM bounds how many: 64 rows of 151936 bf16 logits 18 against 20 us,
+// 1024 rows with top-k 157 against 108.) What of the first and last vector lies outside the row is
+// -inf.
 struct Shared {
     u64 box[kWarps];
     u64 seg[2][kMaxCluster * kWarps];  // a value of every warp of the cluster (two, used in turn)
+    u64 runs[kMaxCluster * kWarps];    // kept weight of every warp's run
     u64 listed[kMaxCluster];           // the weight of every CTA's candidates
     unsigned count[kMaxCluster];       // their number
     float cut[kMaxCluster], peak[kMaxCluster];
     int small[kWarps];
-    unsigned mine, fits;
-    float upper, lower;
+    unsigned mine, hits, fits;
+    float upper, lower, from, width;
+    unsigned again;
+    u64 below;
+    u64 kept;
+    int run;
+    unsigned tau;
     int first, found;
     float d;
+    uint4 edge[2];  // the row's first and last vector, if they are not wholly in it
 };
 
 struct Split {
     int per_cta, per_warp;  // vectors
 };
 
+// The parts of a CTA's dynamic shared memory.
+struct Room {
+    u64 *list;                // [kList] candidates; with `work` behind it, [kWideList]
+    u64 *work;                // [kList] weights or sums
+    float *peaks;             // [kGroups][kThreads] maxima of the lanes' groups; the histogram
+    unsigned *hits;           // [kHits]
+    static constexpr size_t bytes = 2 * kList * 8 + kGroups * kThreads * 4 + kHits * 4;
+    explicit __device__ __forceinline__ Room(void *p)
+        : list(static_cast<u64 *>(p)), work(list + kList), peaks(reinterpret_cast<float *>(work + kList)),
+          hits(reinterpret_cast<unsigned *>(peaks + kGroups * kThreads)) {}
+};
+static_assert(kBins / 2 == kGroups * kThreads && kWideList == 2 * kList, "what shares a room");
+
 template <typename T>
 struct Row {
     static constexpr int n = Vec<T>::n;
-    const uint4 *vec;  // this CTA's vectors in shared memory
-    int base;          // index in the row of its first vector's first element (may be negative)
-    int lo, hi;        // this warp's vectors
+    using Elem = T;
+    const uint4 *vec;     // this CTA's vectors
+    const uint4 *edge;    // in place of the vectors `front` and `back`
+    const T *row;
+    int base;             // index in the row of its first vector's first element (may be negative)
+    int lo, hi;           // this warp's vectors
+    int front, back;      // -1 where there is none
+    int mine, per_warp;   // vectors of this CTA, and of its warps but the last
     int V;
     int lane, warp;
+    bool inf;             // read through only_inf()
 
-    __device__ __forceinline__ float at(int i) const  // element i of the row, one of this CTA's
+    static __device__ __forceinline__ uint4 read(const uint4 *p)
     {
-        return as_float(reinterpret_cast<const T *>(vec)[i - base]);
+        uint4 v;
+        asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+        return v;
+    }
+    __device__ __forceinline__ uint4 get(int j) const
+    {
+        uint4 v;
+        if (j == front) v = edge[0];
+        else if (j == back) v = edge[1];
+        else v = read(vec + j);
+        return inf ? only_inf<T>(v) : v;
+    }
+    // Vectors j, j + 32, ... of this lane, k of them, those past the run's end all -inf. Returns how
+    // many are not past the end for some lane of the warp.
+    template <int k>
+    __device__ __forceinline__ int load(int j, uint4 (&v)[k]) const
+    {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {  // the reads first, then the rare vectors that are something else
+            const int a = j + 32 * i;
+            v[i] = make_uint4(Low<T>::word, Low<T>::word, Low<T>::word, Low<T>::word);
+            if (a < hi && a != front && a != back) v[i] = read(vec + a);
+        }
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+            const int a = j + 32 * i;
+            if (a < hi && (a == front || a == back)) v[i] = edge[a != front];
+        }
+        if (inf) {
+#pragma unroll
+            for (int i = 0; i < k; ++i) v[i] = only_inf<T>(v[i]);
+        }
+        return min((hi - (j - lane) + 31) / 32, k);
+    }
+    // Calls f(v, m, c) for this lane's vectors, k at a time: v[0, m) of the c-th time.
+    template <int k, typename F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        int c = 0;
+        for (int j = lo + lane; j - lane < hi; j += 32 * k, ++c) {
+            uint4 v[k];
+            const int m = load<k>(j, v);
+            f(v, m, c);
+        }
+    }
+    __device__ __forceinline__ float at(int i) const  // element i of the row; -inf outside
+    {
+        const float l = i >= 0 && i < V ? as_float(__ldg(row + i)) : -kInf;
+        return !inf ? l : l == kInf ? 0.0f : -kInf;
     }
     __device__ __forceinline__ int first() const { return max(base, 0); }
-    __device__ __forceinline__ int last(int per_cta) const { return min(base + per_cta * n, V); }
+    __device__ __forceinline__ int last() const { return min(base + mine * n, V); }
 };
 
-// Starts the copies of this CTA's part of the row at `row`.
+// This CTA's part of the row at `row`.
 template <typename T>
-__device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp, uint4 *store, unsigned rank)
+__device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp, unsigned rank, Shared &sh)
 {
     constexpr int n = Vec<T>::n;
     Row<T> R;
     R.lane = threadIdx.x & 31;
     R.warp = threadIdx.x >> 5;
     R.V = V;
-    R.vec = store;
+    R.row = row;
+    R.inf = false;
     const auto address = reinterpret_cast<uintptr_t>(row);
     const int off = static_cast<int>((address & 15u) / sizeof(T));
     const int vectors = (off + V + n - 1) / n;
     const int v0 = static_cast<int>(rank) * sp.per_cta;
-    const int mine = max(min(sp.per_cta, vectors - v0), 0);
+    R.mine = max(min(sp.per_cta, vectors - v0), 0);
+    R.per_warp = sp.per_warp;
     R.base = v0 * n - off;
-    R.lo = min(R.warp * sp.per_warp, mine);
-    R.hi = min(R.lo + sp.per_warp, mine);
-    const auto *src = reinterpret_cast<const uint4 *>(address & ~static_cast<uintptr_t>(15)) + v0;
-    const int step = ((R.hi - R.lo + 31) / 32 + kStages - 1) / kStages * 32;
-    int j = R.lo + R.lane;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-        const int end = min(R.lo + (s + 1) * step, R.hi);
-        for (; j < end; j += 32) {
-            const int i = R.base + j * n;
-            if (i >= 0 && i + n <= V) {
-                copy16(store + j, src + j);
-            } else {
-#pragma unroll
-                for (int e = 0; e < n; ++e)
-                    reinterpret_cast<T *>(store + j)[e] = i + e >= 0 && i + e < V ? __ldg(row + i + e) : Low<T>::value();
-            }
-        }
-        copy_commit();
+    R.lo = min(R.warp * sp.per_warp, R.mine);
+    R.hi = min(R.lo + sp.per_warp, R.mine);
+    R.vec = reinterpret_cast<const uint4 *>(address & ~static_cast<uintptr_t>(15)) + v0;
+    R.edge = sh.edge;
+    R.front = off != 0 && rank == 0 ? 0 : -1;
+    R.back = (off + V) % n != 0 && vectors - 1 - v0 < R.mine ? vectors - 1 - v0 : -1;
+    if (threadIdx.x < 2 * n) {
+        const int k = threadIdx.x / n, e = threadIdx.x % n, i = (k == 0 ? 0 : vectors - 1) * n - off + e;
+        reinterpret_cast<T *>(&sh.edge[k])[e] = i >= 0 && i < V ? __ldg(row + i) : Low<T>::value();
     }
+    __syncthreads();
     return R;
 }
 
-// Calls f(first, end) for the portions of this lane's vectors (first, first + 32, ... below end)
-// as they arrive.
-template <typename T, typename F>
-__device__ __forceinline__ void by_portions(const Row<T> &R, F f)
-{
-    const int step = ((R.hi - R.lo + 31) / 32 + kStages - 1) / kStages * 32;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-        if (s == 0) copy_wait<kStages - 1>();
-        if (s == 1) copy_wait<kStages - 2>();
-        if (s == 2) copy_wait<kStages - 3>();
-        if (s == 3) copy_wait<0>();
-        f(R.lo + s * step + R.lane, min(R.lo + (s + 1) * step, R.hi));
-    }
-}
-static_assert(kStages == 4, "by_portions waits for four portions");
-
-// Calls f(vector number) for this lane's vectors as they arrive.
-template <typename T, typename F>
-__device__ __forceinline__ void as_they_come(const Row<T> &R, F f)
-{
-    by_portions(R, [&](int j, int end) {
-#pragma unroll 4
-        for (; j < end; j += 32) f(j);
-    });
-}
-
+// The largest of this lane's logits, and of each group of them (times c of kAhead vectors with the
+// same c mod kGroups) into `peaks`.
 template <typename T>
-__device__ __forceinline__ float lane_max(const Row<T> &R)
+__device__ __forceinline__ float lane_max(const Row<T> &R, float *peaks)
 {
-    Largest<T> m;
-    as_they_come(R, [&](int j) { m.add(R.vec[j]); });
-    return m.get();
+    float all = -kInf;
+    R.template each<kAhead>([&](uint4 (&v)[kAhead], int, int c) {
+        Largest<T> m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) m.add(v[i]);
+        float *at = peaks + (c % kGroups) * kThreads + threadIdx.x;
+        const float own = m.get();
+        *at = c < kGroups ? own : fmaxf(*at, own);
+        all = fmaxf(all, own);
+    });
+    return all;
+}
+
+// Sum of 2^((l - ref) scale) over v[0, m), in binary32, ref the largest logit or more; a NaN and -inf
+// add nothing, and where ref is +inf each logit of +inf adds 1.
+template <typename T, int k>
+__device__ __forceinline__ float fast_sum(const uint4 (&v)[k], int m, float ref, float scale)
+{
+    constexpr int n = Vec<T>::n;
+    Two sum = two(0.0f);
+#pragma unroll
+    for (int i = 0; i < k; ++i) {
+        if (i >= m) continue;
+        float f[n];
+        Vec<T>::get(v[i], f);
+#pragma unroll
+        for (int e = 0; e < n; e += 2) {
+            const Two x = (two(f[e], f[e + 1]) + two(-ref)) * two(scale);
+            float a, b;
+            parts(x, a, b);
+            sum = sum + two(sv::ex2_approx(a), sv::ex2_approx(b));
+        }
+    }
+    float a, b;
+    parts(sum, a, b);
+    a += b;
+    if (a != a) {  // a NaN, or infinities on both sides of a difference
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+            float f[n];
+            Vec<T>::get(v[i], f);
+            for (int e = 0; e < n; ++e)
+                if (f[e] > -kInf) a += f[e] == ref ? 1.0f : sv::ex2_approx((f[e] - ref) * scale);
+        }
+    }
+    return a;
 }
 
 // The largest of a value over the block.
@@ -571,45 +708,65 @@ struct SampleParams {
     Split split;
 };
 
+// The row's weight by fast_sum is off by less than one part in kSure: the 2^x by 2^-22, its argument,
+// at most 42, by three roundings (42 3 2^-24 ln 2 = 2^-17.5), a chain of at most 32 + 16 additions by
+// as many, the joining of lanes and warps by a dozen more, the weights' own exp by 2^-23 and their
+// rounding to 2^-40 by V 2^-41: together below 2^-16.
+constexpr u64 kSure = 1 << 16;
+
 // What is kept, besides key_of(l) != 0: l >= tau and d >= low.
 struct Kept {
     float L, inv, tau, low;
 };
 
-// Lanes whose maximum reaches the cut put their tokens at or above it, as (key, ~index), into this
-// CTA's part of the list, and the CTA sends that to the leader's list and its number, its weight
-// (kMass) and, if it is this CTA's own, the cut to every CTA. Entries past the part's end are only counted.
-template <typename T, bool kMass>
-__device__ __forceinline__ void collect(const Row<T> &R, float peak, float cut, u64 *list, int part, unsigned rank,
-                                        int cluster, const Kept &keep, bool tell_cut, Shared &sh)
+// The CTA's tokens at or above the cut, as (key, ~index), into its part of the list: the groups whose
+// maximum reaches the cut are put down, and their vectors then read by all threads side by side, so
+// that the wait for the cache is one and not one for each group. The CTA sends its part to the
+// leader's list and its number, its weight (kMass) and, if it is this CTA's own, the cut to every CTA.
+// Entries past the part's end are only counted, and groups past kHits make the part count as full.
+template <bool kMass, typename T>
+__device__ __forceinline__ void collect(const Row<T> &R, float cut, const Room &room, int part, unsigned rank, int cluster,
+                                        const Kept &keep, bool tell_cut, Shared &sh)
 {
     constexpr int n = Row<T>::n;
     const int tid = threadIdx.x;
-    u64 *mine = list + rank * part;
-    if (tid == 0) sh.mine = 0;
+    u64 *mine = room.list + rank * part;
+    if (tid == 0) sh.mine = sh.hits = 0;
     __syncthreads();
-    if (peak >= cut) {
-#pragma unroll 2
-        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-            const uint4 v = R.vec[j];
-            Largest<T> m;
-            m.add(v);
-            if (m.get() >= cut) {
-                float f[n];
-                Vec<T>::get(v, f);
+    const int times = (R.hi - R.lo + 32 * kAhead - 1) / (32 * kAhead);
+    for (int g = 0; g < min(times, kGroups); ++g)
+        if (room.peaks[g * kThreads + tid] >= cut) {
+            const unsigned at = atomicAdd(&sh.hits, 1u);
+            if (at < kHits) room.hits[at] = static_cast<unsigned>(g * kThreads + tid);
+        }
+    __syncthreads();
+    const int rounds = (R.per_warp + 32 * kAhead * kGroups - 1) / (32 * kAhead * kGroups);
+    const int slots = rounds * kAhead, total = min(static_cast<int>(sh.hits), kHits) * slots;
+    for (int i = tid; i < total; i += kThreads) {
+        const int slot = i % slots;
+        const auto hit = static_cast<int>(room.hits[i / slots]);
+        const int owner = hit % kThreads, time = hit / kThreads + slot / kAhead * kGroups;
+        const int lo = min((owner >> 5) * R.per_warp, R.mine), hi = min(lo + R.per_warp, R.mine);
+        const int j = lo + (owner & 31) + 32 * (time * kAhead + slot % kAhead);
+        if (j >= hi) continue;
+        const uint4 v = R.get(j);
+        Largest<T> m;
+        m.add(v);
+        if (m.get() >= cut) {
+            float f[n];
+            Vec<T>::get(v, f);
 #pragma unroll
-                for (int e = 0; e < n; ++e)
-                    if (f[e] >= cut) {
-                        const unsigned at = atomicAdd(&sh.mine, 1u);
-                        const auto index = static_cast<unsigned>(R.base + j * n + e);
-                        if (at < static_cast<unsigned>(part))
-                            mine[at] = (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index);
-                    }
-            }
+            for (int e = 0; e < n; ++e)
+                if (f[e] >= cut) {
+                    const unsigned at = atomicAdd(&sh.mine, 1u);
+                    const auto index = static_cast<unsigned>(R.base + j * n + e);
+                    if (at < static_cast<unsigned>(part))
+                        mine[at] = (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index);
+                }
         }
     }
     __syncthreads();
-    const int count = static_cast<int>(sh.mine);
+    const int count = sh.hits > kHits ? part + 1 : static_cast<int>(sh.mine);
     u64 w = 0;
     for (int i = tid; i < min(count, part); i += kThreads) {
         const u64 e = mine[i];
@@ -696,10 +853,10 @@ struct Drawn {
         P.tokens[r] = static_cast<int>(~static_cast<unsigned>(entry));
         if (P.logprob) P.logprob[r] = log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z);
     }
-    __device__ __forceinline__ void prob(u64 entry, float z) const
+    __device__ __forceinline__ void prob(u64 entry, float scale) const
     {
         P.probs[r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry))] =
-            __fdiv_rn(sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)), z);
+            sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)) * scale;
     }
 };
 
@@ -725,10 +882,18 @@ __device__ unsigned kth_key(const u64 (&mine)[kMine], int used, int k, unsigned 
     return lo << drop;
 }
 
+// The share of the weight that a top-p set has to reach: somewhere in [least, most], the same where
+// the whole is known exactly. A token is in the set if what lies above it is below that; false comes
+// back from a draw that cannot tell for some token.
+struct Share {
+    bool on;
+    u64 least, most;
+};
+
 // The draw from `count` entries of work[0, count) with their weights in wts, at most kPairs of them:
 // what lies above each in value, and then before each in index, is summed over all pairs, several
 // threads to an entry.
-__device__ void draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums, int count, float p, u64 Z, float u,
+__device__ bool draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums, int count, const Share &share, float u,
                            Shared &sh)
 {
     const int tid = threadIdx.x;
@@ -739,7 +904,7 @@ __device__ void draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums
     const u64 entry = i < count ? work[i] : 0;
     const auto key = static_cast<unsigned>(entry >> 32);
     bool keep = i < count && listed_delta(key, out.keep) >= out.keep.low;
-    if (p < 1.0f) {
+    if (share.on) {
         u64 above = 0;
         for (int j = from; j < to; ++j)
             if (static_cast<unsigned>(work[j] >> 32) > key) above += wts[j];
@@ -747,8 +912,8 @@ __device__ void draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums
         __syncthreads();
         above = 0;
         for (int w = 0; w < ways; ++w) above += part_sums[w * each + i];
-        keep = keep && above < share_of(p, Z);
-        __syncthreads();
+        if (__syncthreads_or(i < count && above >= share.least && above < share.most)) return false;
+        keep = keep && above < share.least;
     }
     const bool first = way == 0;
     const u64 w = keep ? wts[i] : 0;
@@ -767,13 +932,14 @@ __device__ void draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums
         for (int v = 0; v < ways; ++v) upto += part_sums[v * each + i];
         const Target target(u, kept);
         if (target.passed(upto) && !target.passed(upto - w)) out.token(entry, kept);
-        if (out.P.probs) out.prob(entry, as_sum(kept));
+        if (out.P.probs) out.prob(entry, inverse_sum(kept));
     }
+    return true;
 }
 
 // The same for more entries, `size` (a power of two, the rest filled with zeros) of them: sorted by
 // value and summed up, cut off, sorted by index and summed up again.
-__device__ void draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, float p, u64 Z, float u, Shared &sh)
+__device__ bool draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, const Share &share, float u, Shared &sh)
 {
     const int tid = threadIdx.x;
     sort_down(list, size);
@@ -790,19 +956,21 @@ __device__ void draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, fl
     }
     if (tid == 0) sh.found = size;
     __syncthreads();
-    const u64 need = p < 1.0f ? share_of(p, Z) : 0;
+    bool unsure = false;
     for (int i = tid; i < size; i += kThreads) {
         const u64 e = list[i];
         bool out_of = e == 0 || listed_delta(static_cast<unsigned>(e >> 32), out.keep) < out.keep.low;
-        if (p < 1.0f && i > 0 && static_cast<unsigned>(e >> 32) != static_cast<unsigned>(list[i - 1] >> 32))
-            out_of |= sums[i - 1] >= need;
+        if (share.on && i > 0 && static_cast<unsigned>(e >> 32) != static_cast<unsigned>(list[i - 1] >> 32)) {
+            out_of |= sums[i - 1] >= share.least;
+            unsure |= sums[i - 1] >= share.least && sums[i - 1] < share.most;
+        }
         if (out_of) atomicMin(&sh.found, i);
     }
-    __syncthreads();
+    if (__syncthreads_or(unsure)) return false;
     const int kept = sh.found;
     const u64 Zk = sums[kept - 1];
     if (out.P.probs)
-        for (int i = tid; i < kept; i += kThreads) out.prob(list[i], as_sum(Zk));
+        for (int i = tid; i < kept; i += kThreads) out.prob(list[i], inverse_sum(Zk));
     // index order: (~index, key), the largest first; the weight follows from the key again
     for (int i = tid; i < size; i += kThreads)
         list[i] = i < kept ? (list[i] << 32) | (list[i] >> 32) : 0;
@@ -818,14 +986,16 @@ __device__ void draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, fl
         if (target.passed(next) && !target.passed(run)) out.token(turned(i), Zk);
         run = next;
     }
+    return true;
 }
 
 // The leader's work on its list of `total` candidates. With k > 0 they hold the row's k largest for
 // sure where every CTA listed its own k largest, and otherwise where k of them reach the largest of
 // the CTAs' cuts (false is returned if not); the row's largest logit is among them in any case.
+// Without k, `share` is the top-p set's share of the whole row.
 template <typename T>
 __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *sums, int part, int total, int k,
-                            bool sure, float p, u64 Z, float u, Kept &keep, Shared &sh)
+                            bool sure, float p, Share share, float u, Kept &keep, Shared &sh)
 {
     constexpr int kMine = kList / kThreads;
     const int tid = threadIdx.x, cluster = P.cluster;
@@ -881,18 +1051,17 @@ __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *
     u64 all;
     block_scan(w, sh.box, &all);
     const int count = static_cast<int>(sh.mine);
-    if (k > 0 || P.top_p == nullptr || !(p < 1.0f)) Z = all;
-    const Drawn out{P, r, keep};
-    if (count <= kPairs) {
-        draw_pairs(out, work, wts, sums + kPairs, count, p, Z, u, sh);
-    } else {
-        int size = 1;
-        while (size < count) size *= 2;
-        for (int i = count + tid; i < size; i += kThreads) list[i] = 0;
-        __syncthreads();
-        draw_sorted(out, list, sums, size, p, Z, u, sh);
+    if (k > 0 && p < 1.0f) {
+        share.on = true;
+        share.least = share.most = share_of(p, all);
     }
-    return true;
+    const Drawn out{P, r, keep};
+    if (count <= kPairs) return draw_pairs(out, work, wts, sums + kPairs, count, share, u, sh);
+    int size = 1;
+    while (size < count) size *= 2;
+    for (int i = count + tid; i < size; i += kThreads) list[i] = 0;
+    __syncthreads();
+    return draw_sorted(out, list, sums, size, share, u, sh);
 }
 
 template <bool kAll>
@@ -915,20 +1084,23 @@ __device__ __forceinline__ Two kept_weight(float l, float m, const Kept &keep)
 }
 
 // This warp's sum of the kept tokens' weights.
-template <typename T, bool kAll>
-__device__ __forceinline__ u64 warp_weight(const Row<T> &R, const Kept &keep)
+template <bool kAll, typename RowT>
+__device__ __forceinline__ u64 warp_weight(const RowT &R, const Kept &keep)
 {
-    constexpr int n = Row<T>::n;
+    constexpr int n = RowT::n, k = 4;
     WeightSum s;
     int count = 0;
-#pragma unroll 4
-    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-        float f[n];
-        Vec<T>::get(R.vec[j], f);
+    R.template each<k>([&](uint4 (&v)[k], int m, int) {
 #pragma unroll
-        for (int e = 0; e < n; e += 2) s.add(kept_weight<kAll>(f[e], f[e + 1], keep));
-        count += n;
-    }
+        for (int i = 0; i < k; ++i)
+            if (i < m) {
+                float f[n];
+                Vec<typename RowT::Elem>::get(v[i], f);
+#pragma unroll
+                for (int e = 0; e < n; e += 2) s.add(kept_weight<kAll>(f[e], f[e + 1], keep));
+            }
+        count += n * m;
+    });
     return warp_sum(s.total(count));
 }
 
@@ -957,210 +1129,294 @@ struct Exchange {
 };
 
 // How much the tokens from l >= bound on hold: tokens or, with kMass, weight; of those >= keep.tau.
-template <typename T, bool kMass>
-__device__ u64 held_from(const Row<T> &R, const Kept &keep, float bound, Exchange &ex)
+template <bool kMass, typename RowT>
+__device__ u64 held_from(const RowT &R, const Kept &keep, float bound, Exchange &ex)
 {
-    constexpr int n = Row<T>::n;
-    Kept k = keep;
-    k.tau = fmaxf(bound, keep.tau);
-    k.low = -kInf;
-    if (kMass) return ex.sum(warp_weight<T, false>(R, k));
+    constexpr int n = RowT::n, k = 4;
+    Kept from = keep;
+    from.tau = fmaxf(bound, keep.tau);
+    from.low = -kInf;
+    if (kMass) return ex.sum(warp_weight<false>(R, from));
     int c = 0;
-    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-        float f[n];
-        Vec<T>::get(R.vec[j], f);
+    R.template each<k>([&](uint4 (&v)[k], int, int) {
 #pragma unroll
-        for (int e = 0; e < n; ++e) c += f[e] >= k.tau;
-    }
+        for (int i = 0; i < k; ++i) {
+            float f[n];
+            Vec<typename RowT::Elem>::get(v[i], f);
+#pragma unroll
+            for (int e = 0; e < n; ++e) c += f[e] >= from.tau;
+        }
+    });
     return ex.sum(warp_sum(static_cast<u64>(c)));
 }
 
 // The largest key in [lo, hi] such that the tokens with keys at least as large hold `need`, or 0
 // where those from lo on do not: by halving, one pass over the row for each step.
-template <typename T, bool kMass>
-__device__ unsigned search_key(const Row<T> &R, const Kept &keep, u64 need, unsigned lo, unsigned hi, Exchange &ex)
+template <bool kMass, typename RowT>
+__device__ unsigned search_key(const RowT &R, const Kept &keep, u64 need, unsigned lo, unsigned hi, Exchange &ex)
 {
-    constexpr int drop = sizeof(T) == 2 ? 16 : 0;  // (of bf16 logits the upper half of the key says all)
+    constexpr int drop = RowT::n == 8 ? 16 : 0;  // (of bf16 logits the upper half of the key says all)
     constexpr unsigned least = 0x00800000u;        // the key of the lowest finite number
     lo >>= drop;
     hi >>= drop;
-    if (held_from<T, kMass>(R, keep, of_key(max(lo << drop, least)), ex) < need) return 0;
+    if (held_from<kMass>(R, keep, of_key(max(lo << drop, least)), ex) < need) return 0;
     while (lo < hi) {
         const unsigned mid = lo + (hi - lo) / 2 + 1;
-        if (held_from<T, kMass>(R, keep, of_key(max(mid << drop, least)), ex) >= need) lo = mid;
+        if (held_from<kMass>(R, keep, of_key(max(mid << drop, least)), ex) >= need) lo = mid;
         else hi = mid - 1;
     }
     return max(lo << drop, least);
 }
 
-// The same over all keys, for rows whose kept set is too large for the list: the largest key such
-// that the tokens at least as large, of those >= keep.tau, hold `need`; `all` is what they hold
-// together. A histogram of the tokens by value (kBins bins of (L - l) / T) tells the bin it is in:
-// for counts exactly, for weights by the weights of the bins' middles, so that the neighbouring
-// bins are taken as well. One pass sums up what lies above them and lists what lies in them, and the
-// leader finds the key there. Where the bins hold more than the list, or the guess was wrong, it is
-// found by halving. Returns 0 where all tokens together do not hold `need`.
-template <typename T, bool kMass>
-__device__ unsigned find_key(const Row<T> &R, const Kept &keep, u64 need, u64 all, u64 *list, u64 *sums, int part,
-                             Exchange &ex)
+// A bracket of the value at which the row's tokens from the largest on hold `count` of them or, with
+// kMass, the part p of their weight; of the tokens >= keep.tau. From a histogram of the tokens by
+// value, kBins bins of (L - l) / T: for counts the bin it is in, for weights, which the bins'
+// middles stand for (to a part in 10^6), that and the bins beside it. Where those hold more than
+// the list, a second histogram of just that span narrows it down further. A guess that the caller
+// checks: sh.lower and sh.upper of every CTA.
+template <bool kMass, typename T>
+__device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, const Room &room, Exchange &ex)
 {
-    constexpr int n = Row<T>::n;
+    constexpr int n = Row<T>::n, kv = 4;
     Shared &sh = ex.sh;
     const int tid = threadIdx.x, cluster = ex.cluster;
-    auto *words = reinterpret_cast<unsigned *>(sums);
-    const float scale = keep.inv * (kBins / kSpan);
-    for (int i = tid; i < kBins / 2; i += kThreads) words[i] = 0;
-    __syncthreads();
-    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-        float f[n];
-        Vec<T>::get(R.vec[j], f);
+    auto *words = reinterpret_cast<unsigned *>(room.peaks);
+    float from = 0.0f, width = kSpan / kBins;  // the bins' first edge and width, as (L - l) / T
+    u64 want = 0, before = 0;                  // (the leader's) what to reach, and what lies before the bins
+    for (int level = 0; level < 2; ++level) {
+        const float scale = keep.inv / width, shift = from / width;
+        for (int i = tid; i < kBins / 2; i += kThreads) words[i] = 0;
+        __syncthreads();
+        R.template each<kv>([&](uint4 (&v)[kv], int m, int) {
 #pragma unroll
-        for (int e = 0; e < n; ++e) {
-            const float at = (keep.L - f[e]) * scale;
-            if (f[e] >= keep.tau && at < static_cast<float>(kBins)) {
-                const int b = static_cast<int>(at);
-                atomicAdd(words + (b >> 1), 1u << (16 * (b & 1)));  // (a CTA holds fewer than 2^16 tokens)
-            }
-        }
-    }
-    cluster_sync();
-    if (ex.rank == 0) {
-        constexpr int q = kBins / kThreads;  // bins of a thread
-        unsigned c[q] = {};
-        for (int k = 0; k < cluster; ++k)
+            for (int i = 0; i < kv; ++i)
+                if (i < m) {
+                    float f[n];
+                    Vec<T>::get(v[i], f);
 #pragma unroll
-            for (int i = 0; i < q / 8; ++i) {
-                const uint4 v = get16(remote(words + tid * (q / 2) + 4 * i, k));
-                const unsigned w[4] = {v.x, v.y, v.z, v.w};
+                    for (int e = 0; e < n; ++e) {
+                        const float at = __fmaf_rn(keep.L - f[e], scale, -shift);
+                        if (f[e] >= keep.tau && at >= 0.0f && at < static_cast<float>(kBins)) {
+                            const int b = static_cast<int>(at);
+                            atomicAdd(words + (b >> 1), 1u << (16 * (b & 1)));  // (an overflow spoils the guess only)
+                        }
+                    }
+                }
+        });
+        cluster_sync();
+        if (ex.rank == 0) {
+            constexpr int q = kBins / kThreads;  // bins of a thread
+            unsigned c[q] = {};
+            for (int k = 0; k < cluster; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    c[8 * i + 2 * e] += w[e] & 0xFFFFu;
-                    c[8 * i + 2 * e + 1] += w[e] >> 16;
+                for (int i = 0; i < q / 8; ++i) {
+                    const uint4 v = get16(remote(words + tid * (q / 2) + 4 * i, k));
+                    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        c[8 * i + 2 * e] += w[e] & 0xFFFFu;
+                        c[8 * i + 2 * e + 1] += w[e] >> 16;
+                    }
+                }
+            auto held = [&](int i) -> u64 {
+                if (!kMass) return c[i];
+                const float middle = from + (static_cast<float>(tid * q + i) + 0.5f) * width;
+                return static_cast<u64>(c[i]) * static_cast<unsigned>(0x1p+31f * sv::ex2_approx(-middle * kLog2e));
+            };
+            u64 own = 0, total, tokens;
+#pragma unroll
+            for (int i = 0; i < q; ++i) own += held(i);
+            const u64 upto = block_scan(own, sh.box, &total);
+            if (level == 0) want = kMass ? share_of(p, total) : count;
+            constexpr int around = kMass ? 1 : 0;
+            if (tid == 0) sh.first = kBins;
+            __syncthreads();
+            u64 run = before + upto;
+            if (run + own >= want && run < want) {
+#pragma unroll
+                for (int i = 0; i < q; ++i) {
+                    run += held(i);
+                    if (run >= want) atomicMin(&sh.first, tid * q + i);
                 }
             }
-        u64 own = 0, total;
-        auto held = [&](int i) -> u64 {
-            if (!kMass) return c[i];
-            const float middle = (static_cast<float>(tid * q + i) + 0.5f) * (kSpan / kBins);
-            return static_cast<u64>(c[i]) * static_cast<unsigned>(0x1p+31f * sv::ex2_approx(-middle * kLog2e));
-        };
-#pragma unroll
-        for (int i = 0; i < q; ++i) own += held(i);
-        u64 run = block_scan(own, sh.box, &total);
-        const u64 want = kMass ? static_cast<u64>(as_sum(need) / as_sum(all) * __ull2float_rn(total)) : need;
-        if (tid == 0) sh.first = kBins;
-        __syncthreads();
-        if (run + own >= want && run < want) {
+            __syncthreads();
+            const int b = sh.first;
+            // what the bracket's bins hold in tokens, and what lies before them
+            u64 in = 0;
+            run = before + upto;
+            if (tid == 0) sh.below = before;
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < q; ++i) {
+                const int at = tid * q + i;
+                if (at >= b - around && at <= b + around) in += c[i];
+                if (at == b - around) sh.below = run;
                 run += held(i);
-                if (run >= want) atomicMin(&sh.first, tid * q + i);
+            }
+            block_scan(in, sh.box, &tokens);
+            before = sh.below;
+            // (in the last bins or beyond them: everything below)
+            const float slack = 4e-6f * fmaxf(fabsf(keep.L), kSpan / keep.inv);
+            const float lo = from + static_cast<float>(max(b - around, 0)) * width, hi = from + static_cast<float>(b + around + 1) * width;
+            const float upper = lo <= 0.0f ? keep.L : keep.L - lo / keep.inv + slack;
+            const float lower = b >= kBins - 2 ? -FLT_MAX : keep.L - hi / keep.inv - slack;
+            if (tid < cluster) {
+                put(remote(&sh.upper, tid), __float_as_uint(upper));
+                put(remote(&sh.lower, tid), __float_as_uint(fmaxf(lower, -FLT_MAX)));
+                put(remote(&sh.from, tid), __float_as_uint(lo));
+                put(remote(&sh.width, tid), __float_as_uint((hi - lo) / kBins));
+                // (of bf16 logits with a distinct value or two there a second look tells nothing more)
+                const bool again = level == 0 && b < kBins - 2 && tokens * (cluster > 1 ? 5 : 3) / 3 > kWideList &&
+                                   (sizeof(T) == 4 || key_of(upper) >> 16 > (key_of(lower) >> 16) + 2);
+                put(remote(&sh.again, tid), static_cast<unsigned>(again));
             }
         }
-        __syncthreads();
-        const int b = sh.first, around = kMass ? 1 : 0;
-        const float width = kSpan / kBins / keep.inv, slack = 4e-6f * fmaxf(fabsf(keep.L), kSpan / keep.inv);
-        // (a row beyond the last bin: everything, which the halving then has to do)
-        const float upper = b - around <= 0 ? keep.L : keep.L - static_cast<float>(b - around) * width + slack;
-        const float lower = b >= kBins - 2 ? -FLT_MAX : keep.L - static_cast<float>(b + around + 1) * width - slack;
-        if (tid < cluster) {
-            put(remote(&sh.upper, tid), __float_as_uint(upper));
-            put(remote(&sh.lower, tid), __float_as_uint(fmaxf(lower, -FLT_MAX)));
-        }
+        cluster_sync();
+        if (!sh.again) return;
+        from = sh.from;
+        width = sh.width;
     }
-    cluster_sync();
-    const float upper = sh.upper, lower = fmaxf(sh.lower, keep.tau);
+}
+
+// One pass over the row for a bracket: the tokens within it go to the leader's list as (key, ~index);
+// *above: this warp's tokens above it or, with kMass, their weight, and *all the weight of all tokens
+// >= keep.tau.
+template <bool kMass, typename T>
+__device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float lower, float upper, const Room &room, int part,
+                                       u64 *above, u64 *all, Exchange &ex)
+{
+    constexpr int n = Row<T>::n, kv = 4;
+    Shared &sh = ex.sh;
+    const int tid = threadIdx.x;
     if (tid == 0) sh.mine = 0;
     __syncthreads();
-    u64 *mine = list + ex.rank * part;
-    WeightSum above;
+    u64 *mine = room.list + ex.rank * part;
+    WeightSum over, total;
     int count = 0;
-#pragma unroll 2
-    for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-        float f[n];
-        Vec<T>::get(R.vec[j], f);
-        bool within = false;
+    R.template each<kv>([&](uint4 (&v)[kv], int m, int c) {
 #pragma unroll
-        for (int e = 0; e < n; e += 2) {
-            if (kMass) {
-                float a, b;
-                parts(kept_weight<true>(f[e], f[e + 1], keep), a, b);
-                above.add(two(f[e] > upper ? a : 0.0f, f[e + 1] > upper ? b : 0.0f));
-            } else {
-                count += f[e] > upper;
-                count += f[e + 1] > upper;
-            }
-            within |= (f[e] >= lower && f[e] <= upper) || (f[e + 1] >= lower && f[e + 1] <= upper);
-        }
-        if (kMass) count += n;
-        if (within)
+        for (int i = 0; i < kv; ++i) {
+            if (i >= m) continue;
+            float f[n];
+            Vec<T>::get(v[i], f);
+            bool within = false;
 #pragma unroll
-            for (int e = 0; e < n; ++e)
-                if (f[e] >= lower && f[e] <= upper) {
-                    const unsigned at = atomicAdd(&sh.mine, 1u);
-                    if (at < static_cast<unsigned>(part)) mine[at] = static_cast<u64>(key_of(f[e])) << 32;
+            for (int e = 0; e < n; e += 2) {
+                if (kMass) {
+                    float a, b;
+                    parts(kept_weight<true>(f[e], f[e + 1], keep), a, b);
+                    total.add(two(f[e] >= keep.tau ? a : 0.0f, f[e + 1] >= keep.tau ? b : 0.0f));
+                    over.add(two(f[e] > upper ? a : 0.0f, f[e + 1] > upper ? b : 0.0f));
+                } else {
+                    count += f[e] > upper;
+                    count += f[e + 1] > upper;
                 }
-    }
-    const u64 over_all = warp_sum(kMass ? above.total(count) : static_cast<u64>(count));
+                within |= (f[e] >= lower && f[e] <= upper) || (f[e + 1] >= lower && f[e + 1] <= upper);
+            }
+            if (within)
+#pragma unroll
+                for (int e = 0; e < n; ++e)
+                    if (f[e] >= lower && f[e] <= upper) {
+                        const unsigned at = atomicAdd(&sh.mine, 1u);
+                        const auto index = static_cast<unsigned>(R.base + (R.lo + R.lane + 32 * (c * kv + i)) * n + e);
+                        if (at < static_cast<unsigned>(part))
+                            mine[at] = (static_cast<u64>(key_of(f[e])) << 32) | static_cast<u64>(~index);
+                    }
+        }
+        if (kMass) count += n * m;
+    });
+    *above = warp_sum(kMass ? over.total(count) : static_cast<u64>(count));
+    *all = kMass ? warp_sum(total.total(count)) : 0;
     __syncthreads();
     const int listed = static_cast<int>(sh.mine);
     if (ex.rank != 0)
         for (int i = tid; i < min(listed, part); i += kThreads) put(remote(mine + i, 0), mine[i]);
-    if (tid < cluster) put(remote(&sh.count[ex.rank], tid), static_cast<unsigned>(listed));
-    const u64 over = ex.sum(over_all);
+    if (tid < ex.cluster) put(remote(&sh.count[ex.rank], tid), static_cast<unsigned>(listed));
+}
+
+// The leader's entries of the list, a thread's share of them, with their weights (kMass) or 1.
+template <bool kMass>
+struct Listed {
+    static constexpr int per = kWideList / kThreads;
+    u64 entry[per], w[per];
+    __device__ __forceinline__ Listed(const u64 *list, int part, int cluster, int total, const Kept &keep, const Shared &sh)
+    {
+#pragma unroll
+        for (int q = 0; q < per; ++q) {
+            const int i = static_cast<int>(threadIdx.x) + q * kThreads;
+            entry[q] = i < total ? listed_entry(list, part, cluster, sh, i) : 0;
+            const auto key = static_cast<unsigned>(entry[q] >> 32);
+            w[q] = key == 0 ? 0 : kMass ? weight(exp_weight(delta(of_key(key), keep.L, keep.inv))) : 1;
+        }
+    }
+    // The largest key in [lo, hi] such that `over` and the entries with keys at least as large hold
+    // `need`, or 0; *held: what they hold.
+    template <typename T>
+    __device__ __forceinline__ unsigned key(u64 over, u64 need, unsigned lo, unsigned hi, u64 *held, Shared &sh) const
+    {
+        constexpr int drop = sizeof(T) == 2 ? 16 : 0;
+        auto from = [&](unsigned bound) {
+            u64 m = 0, sum;
+#pragma unroll
+            for (int q = 0; q < per; ++q) m += static_cast<unsigned>(entry[q] >> 32) >> drop >= bound ? w[q] : 0;
+            block_scan(m, sh.box, &sum);
+            return over + sum;
+        };
+        lo >>= drop;
+        hi >>= drop;
+        *held = from(lo);
+        if (*held < need) return 0;
+        while (lo < hi) {
+            const unsigned mid = lo + (hi - lo) / 2 + 1;
+            const u64 h = from(mid);
+            if (h >= need) {
+                lo = mid;
+                *held = h;
+            } else {
+                hi = mid - 1;
+            }
+        }
+        return max(lo << drop, 1u);
+    }
+};
+
+// The largest key such that the tokens at least as large hold k of them, for a k beyond the list; 0
+// where the row has fewer tokens. Where the bracket holds more than the list, or the guess was wrong,
+// it is found by halving.
+template <typename T>
+__device__ unsigned find_kth(const Row<T> &R, const Kept &keep, u64 k, const Room &room, Exchange &ex)
+{
+    Shared &sh = ex.sh;
+    const int part = kWideList / ex.cluster;
+    bracket<false>(R, keep, k, 0.0f, room, ex);
+    const float upper = sh.upper, lower = sh.lower;
+    u64 above, all;
+    gather<false>(R, keep, lower, upper, room, part, &above, &all, ex);
+    const u64 over = ex.sum(above);
     int total;
     unsigned found = 0;
-    if (over < need) {
-        if (all_listed(sh, cluster, part, &total)) {
+    if (over < k) {
+        if (all_listed(sh, ex.cluster, part, &total)) {
             if (ex.rank == 0) {
-                constexpr int kMine = kList / kThreads, drop = sizeof(T) == 2 ? 16 : 0;
-                unsigned key[kMine];
-                u64 w[kMine];
-#pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                    const int i = tid + q * kThreads;
-                    key[q] = i < total ? static_cast<unsigned>(listed_entry(list, part, cluster, sh, i) >> 32) : 0;
-                    w[q] = key[q] == 0 ? 0 : kMass ? weight(exp_weight(delta(of_key(key[q]), keep.L, keep.inv))) : 1;
-                }
-                auto from = [&](unsigned bound) {
-                    u64 m = 0, sum;
-#pragma unroll
-                    for (int q = 0; q < kMine; ++q) m += key[q] >> drop >= bound ? w[q] : 0;
-                    block_scan(m, sh.box, &sum);
-                    return over + sum;
-                };
-                unsigned lo = key_of(lower) >> drop, hi = key_of(upper) >> drop;
-                if (from(lo) >= need) {
-                    while (lo < hi) {
-                        const unsigned mid = lo + (hi - lo) / 2 + 1;
-                        if (from(mid) >= need) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    found = max(lo << drop, 1u);
-                }
-                if (tid < cluster) put(remote(&sh.fits, tid), found);
+                const Listed<false> mine(room.list, part, ex.cluster, total, keep, sh);
+                found = mine.template key<T>(over, k, key_of(lower), key_of(upper), &all, sh);
+                if (threadIdx.x < ex.cluster) put(remote(&sh.fits, threadIdx.x), found);
             }
             cluster_sync();
             found = sh.fits;
         } else {
-            found = search_key<T, kMass>(R, keep, need, key_of(lower), key_of(upper), ex);
+            found = search_key<false>(R, keep, k, key_of(lower), key_of(upper), ex);
         }
     }
-    if (found == 0) found = search_key<T, kMass>(R, keep, need, 0, key_of(keep.L), ex);
-    return found;
+    return found ? found : search_key<false>(R, keep, k, 0, key_of(keep.L), ex);
 }
 
-// The draw over the whole row: every warp's sum of kept weights goes to every CTA, the CTA that
-// holds the warp's run on which the uniform number falls finds the token in it, and each
-// writes its part of the distribution.
-template <typename T, bool kAll>
-__device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, float u, const Kept &keep, Exchange &ex)
+// Where in the runs of the cluster's warps, whose kept weights are in seg, the target falls: the run
+// and the weight before it. By every warp that calls it.
+__device__ __forceinline__ int find_run(const u64 *seg, int warps, float u, u64 *Z, u64 *below)
 {
-    constexpr int n = Row<T>::n;
-    Shared &sh = ex.sh;
-    const int tid = threadIdx.x, lane = tid & 31, warps = P.cluster * kWarps;
-    const u64 *seg = ex.all(warp_weight<T, kAll>(R, keep));
     constexpr int q = kMaxCluster * kWarps / 32;  // a lane's consecutive runs
+    const int lane = threadIdx.x & 31;
     u64 own = 0;
 #pragma unroll
     for (int i = 0; i < q; ++i)
@@ -1171,47 +1427,190 @@ __device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, fl
         const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, k);
         if (lane >= k) upto += o;
     }
-    const u64 Z = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const Target target(u, Z);
+    *Z = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const Target target(u, *Z);
     const int at = __ffs(__ballot_sync(0xFFFFFFFFu, target.passed(upto))) - 1;
     int s = 0;
-    u64 below = upto - own;
+    u64 b = upto - own;
     if (lane == at) {
         s = lane * q;
-        while (!target.passed(below + seg[s])) below += seg[s++];
+        while (!target.passed(b + seg[s])) b += seg[s++];
     }
-    s = __shfl_sync(0xFFFFFFFFu, s, at);
-    below = __shfl_sync(0xFFFFFFFFu, below, at);
-    if (s / kWarps == static_cast<int>(ex.rank)) {
-        const int mine = max(min(P.split.per_cta, (P.V - R.base + n - 1) / n), 0);
-        const int lo = min((s % kWarps) * P.split.per_warp, mine), hi = min(lo + P.split.per_warp, mine);
+    *below = __shfl_sync(0xFFFFFFFFu, b, at);
+    return __shfl_sync(0xFFFFFFFFu, s, at);
+}
+
+// The CTA's part of the distribution over kept tokens. Where not all are kept the row is 0 before,
+// and only vectors with kept tokens are written. Four probabilities at a time where the rows of
+// logits and probabilities lie alike to 16 bytes, else one by one, neighbours by neighbouring lanes.
+template <bool kAll, typename T>
+__device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const Kept &keep, u64 Z)
+{
+    constexpr int n = Row<T>::n, k = 2;
+    const float scale = inverse_sum(Z);
+    if ((reinterpret_cast<uintptr_t>(probs + R.base) & 15u) != 0) {
+        for (int i = R.first() + static_cast<int>(threadIdx.x); i < R.last(); i += kThreads) {
+            const float l = R.at(i), d = delta(l, keep.L, keep.inv);
+            const bool in = l > -kInf && (kAll || (l >= keep.tau && d >= keep.low));
+            if (kAll || in) probs[i] = in ? sv::exp_f32(d) * scale : 0.0f;
+        }
+        return;
+    }
+    R.template each<k>([&](uint4 (&v)[k], int m, int c) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+            const int j = R.lo + R.lane + 32 * (c * k + i);
+            if (i >= m || j >= R.hi) continue;
+            Largest<T> largest;
+            largest.add(v[i]);
+            if (!kAll && !(largest.get() >= keep.tau)) continue;
+            float f[n];
+            Vec<T>::get(v[i], f);
+#pragma unroll
+            for (int e = 0; e < n; e += 2) {
+                const Two d = (two(f[e], f[e + 1]) + two(-keep.L)) * two(keep.inv);
+                float da, db, a, b;
+                parts(d, da, db);
+                parts(exp_two(d) * two(scale), a, b);
+                // (the comparison also keeps a NaN and -inf out)
+                f[e] = f[e] > -kInf && (kAll || (f[e] >= keep.tau && da >= keep.low)) ? a : 0.0f;
+                f[e + 1] = f[e + 1] > -kInf && (kAll || (f[e + 1] >= keep.tau && db >= keep.low)) ? b : 0.0f;
+            }
+            const int first = R.base + j * n;
+            if (first >= 0 && first + n <= R.V) {
+#pragma unroll
+                for (int e = 0; e < n; e += 4)
+                    *reinterpret_cast<float4 *>(probs + first + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < n; ++e)
+                    if (first + e >= 0 && first + e < R.V) probs[first + e] = f[e];
+            }
+        }
+    });
+}
+
+// Zeros for the CTA's part of a distribution.
+template <typename T>
+__device__ __forceinline__ void write_zeros(const Row<T> &R, float *probs)
+{
+    const int tid = threadIdx.x, first = R.first(), last = R.last();
+    const int head = min(first + static_cast<int>((16u - (reinterpret_cast<uintptr_t>(probs + first) & 15u)) / 4u % 4u), last);
+    const int body = head + max(last - head, 0) / 4 * 4;
+    if (first + tid < head) probs[first + tid] = 0.0f;
+    for (int i = head + 4 * tid; i < body; i += 4 * kThreads) *reinterpret_cast<float4 *>(probs + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (body + tid < last) probs[body + tid] = 0.0f;
+}
+
+// The draw where the run on which the uniform number falls is known: the CTA that holds it finds the
+// token in it, and each writes its part of the distribution.
+template <bool kAll, typename T>
+__device__ void draw_run(const SampleParams &P, const Row<T> &R, long long r, float u, const Kept &keep, int s, u64 below, u64 Z,
+                         unsigned rank, Shared &sh)
+{
+    constexpr int n = Row<T>::n;
+    const int tid = threadIdx.x;
+    if (s / kWarps == static_cast<int>(rank)) {
+        const Target target(u, Z);
+        const int lo = min((s % kWarps) * R.per_warp, R.mine), hi = min(lo + R.per_warp, R.mine);
         const int each = (hi - lo + kThreads - 1) / kThreads;
         const int from = min(lo + tid * each, hi), to = min(from + each, hi);
         u64 sum = 0, all;
         for (int j = from; j < to; ++j) {
             float f[n];
-            Vec<T>::get(R.vec[j], f);
+            Vec<T>::get(R.get(j), f);
 #pragma unroll
             for (int e = 0; e < n; ++e) sum += weight(kept_weight<kAll>(f[e], keep));
         }
         u64 run = below + block_scan(sum, sh.box, &all);
         if (target.passed(run + sum) && !target.passed(run)) {
-            const T *elems = reinterpret_cast<const T *>(R.vec);
-            int i = from * n;
-            float l = as_float(elems[i]);
-            while (!target.passed(run += weight(kept_weight<kAll>(l, keep)))) l = as_float(elems[++i]);
-            P.tokens[r] = R.base + i;
+            int i = R.base + from * n;
+            float l = R.at(i);
+            while (!target.passed(run += weight(kept_weight<kAll>(l, keep)))) l = R.at(++i);
+            P.tokens[r] = i;
             if (P.logprob) P.logprob[r] = log_prob(delta(l, keep.L, keep.inv), Z);
         }
     }
-    if (P.probs) {
-        float *probs = P.probs + r * P.probs_stride;
-        const float z = as_sum(Z);
-        for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) {
-            const float l = R.at(i), d = delta(l, keep.L, keep.inv);
-            probs[i] = l >= keep.tau && l > -kInf && d >= keep.low ? __fdiv_rn(sv::exp_f32(d), z) : 0.0f;
+    if (P.probs) write_probs<kAll>(R, P.probs + r * P.probs_stride, keep, Z);
+}
+
+// The draw over the whole row by one pass of exact sums: every warp's goes to every CTA.
+template <bool kAll, typename T>
+__device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, float u, const Kept &keep, Exchange &ex)
+{
+    const u64 *seg = ex.all(warp_weight<kAll>(R, keep));
+    u64 Z, below;
+    const int s = find_run(seg, P.cluster * kWarps, u, &Z, &below);
+    draw_run<kAll>(P, R, r, u, keep, s, below, Z, ex.rank, ex.sh);
+}
+
+// The draw from a top-p set larger than the list (of the tokens >= keep.tau): a bracket of the least
+// logit in it by the histogram, one pass that sums up all, what lies above the bracket in every
+// warp's run, and lists what lies in it; the leader finds the least logit, adds the listed tokens
+// that are in the set to their runs, and finds the run to draw from.
+template <typename T>
+__device__ void draw_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, Kept keep, const Room &room,
+                          Exchange &ex)
+{
+    constexpr int n = Row<T>::n;
+    Shared &sh = ex.sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cluster = ex.cluster, part = kWideList / cluster;
+    bracket<true>(R, keep, 0, p, room, ex);
+    const float upper = sh.upper, lower = fmaxf(sh.lower, keep.tau);
+    u64 above, all;
+    gather<true>(R, keep, lower, upper, room, part, &above, &all, ex);
+    if (lane < cluster) put(remote(&sh.runs[ex.rank * kWarps + warp], lane), above);  // (as Exchange does)
+    const u64 Z = ex.sum(all);
+    u64 over = 0;
+    for (int i = lane; i < cluster * kWarps; i += 32) over += sh.runs[i];
+    over = warp_sum(over);
+    const u64 need = share_of(p, Z);
+    int total;
+    bool done = false;
+    unsigned key = 0;
+    if (over < need && all_listed(sh, cluster, part, &total)) {
+        if (ex.rank == 0) {
+            const Listed<true> mine(room.list, part, cluster, total, keep, sh);
+            u64 held;
+            key = mine.template key<T>(over, need, key_of(lower), key_of(upper), &held, sh);
+            const float tau = of_key(max(key, 0x00800000u));
+            // (what min-p leaves out of the set is not in these sums)
+            const bool plain = key && !(delta(tau, keep.L, keep.inv) < keep.low);
+            if (plain) {
+                const int off = static_cast<int>((reinterpret_cast<uintptr_t>(R.row) & 15u) / sizeof(T));
+#pragma unroll
+                for (int q = 0; q < mine.per; ++q)
+                    if (static_cast<unsigned>(mine.entry[q] >> 32) >= key) {
+                        const int j = (static_cast<int>(~static_cast<unsigned>(mine.entry[q])) + off) / n;
+                        const int at = j / P.split.per_cta * kWarps + j % P.split.per_cta / P.split.per_warp;
+                        atomicAdd(&sh.runs[at], mine.w[q]);
+                    }
+            }
+            __syncthreads();
+            if (plain && warp == 0) {
+                u64 kept, below;
+                const int s = find_run(sh.runs, cluster * kWarps, u, &kept, &below);
+                if (lane < cluster) {
+                    put(remote(&sh.kept, lane), kept);
+                    put(remote(&sh.below, lane), below);
+                    put(remote(&sh.run, lane), static_cast<unsigned>(s));
+                }
+            }
+            if (tid < cluster) {
+                put(remote(&sh.tau, tid), key);
+                put(remote(&sh.fits, tid), static_cast<unsigned>(plain));
+            }
         }
+        cluster_sync();
+        key = sh.tau;
+        done = sh.fits != 0;
+    } else if (over < need) {
+        key = search_key<true>(R, keep, need, key_of(lower), key_of(upper), ex);
     }
+    if (key == 0) key = search_key<true>(R, keep, need, 0, key_of(keep.L), ex);
+    keep.tau = of_key(key);
+    if (done) draw_run<false>(P, R, r, u, keep, sh.run, sh.below, sh.kept, ex.rank, sh);
+    else draw_row<false>(P, R, r, u, keep, ex);
 }
 
 template <typename T>
@@ -1222,11 +1621,9 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     const int tid = threadIdx.x, cluster = P.cluster;
     const unsigned rank = cluster_rank();
     const long long r = blockIdx.x / cluster;
-    const T *row = logits + r * P.stride;
-    u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
-    u64 *sums = list + kList;
-    Row<T> R = start_row(row, P.V, P.split, store, rank);
+    const Room room(store);
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
+    Row<T> R = start_row(logits + r * P.stride, P.V, P.split, rank, sh);
     const int part = kList / cluster;
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const int k0 = P.top_k ? __ldg(P.top_k + r) : 0;
@@ -1237,11 +1634,10 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     const int k = k0 >= 1 && k0 < P.V ? k0 : 0;
     const bool open = !greedy && !k && !(p < 1.0f) && !(m > 0.0f);
     float *probs = P.probs ? P.probs + r * P.probs_stride : nullptr;
-    if (probs && !open)  // zeros while the logits come; what is kept goes over them
-        for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
-    // (in binary64, by one thread, while the logits come)
+    if (probs && !open) write_zeros(R, probs);  // what is kept goes over them
+    // (in binary64, by one thread, while the others read)
     if (m > 0.0f && tid == 0) sh.d = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
-    float peak = lane_max(R);
+    float peak = lane_max(R, room.peaks);
     const float largest = block_max(peak, sh);
     cluster_wait();
 
@@ -1251,10 +1647,10 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         if (peak == largest && peak > -kInf) {
             int best = INT_MAX;
             for (int j = R.lo + R.lane; j < R.hi && best == INT_MAX; j += 32) {
-                float f[Row<T>::n];
-                Vec<T>::get(R.vec[j], f);
-                for (int e = Row<T>::n - 1; e >= 0; --e)
-                    if (f[e] == largest) best = R.base + j * Row<T>::n + e;
+                float f[R.n];
+                Vec<T>::get(R.get(j), f);
+                for (int e = R.n - 1; e >= 0; --e)
+                    if (f[e] == largest) best = R.base + j * R.n + e;
             }
             atomicMin(&sh.first, best);
         }
@@ -1285,7 +1681,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         // the k largest: of every CTA at least its own k largest, or as many as find place
         const int most = part / 8 * 5;
         const float cut = cut_for(peak, largest, min(k, most), sh);
-        collect<T, false>(R, peak, cut, list, part, rank, cluster, keep, true, sh);
+        collect<false>(R, cut, room, part, rank, cluster, keep, true, sh);
         cluster_sync();
         if (all_listed(sh, cluster, part, &total)) {
             if (total == 0) {  // nothing to keep
@@ -1296,11 +1692,11 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
                 return;
             }
             if (k <= most) {
-                if (rank == 0) finish_list<T>(P, r, list, sums, part, total, k, true, p, 0, u, keep, sh);
+                if (rank == 0) finish_list<T>(P, r, room.list, room.work, part, total, k, true, p, Share{}, u, keep, sh);
                 return;
             }
             if (rank == 0) {
-                const bool done = finish_list<T>(P, r, list, sums, part, total, k, false, p, 0, u, keep, sh);
+                const bool done = finish_list<T>(P, r, room.list, room.work, part, total, k, false, p, Share{}, u, keep, sh);
                 if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
             }
             cluster_sync();
@@ -1325,56 +1721,64 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
             P.tokens[r] = -1;
             if (P.logprob) P.logprob[r] = -kInf;
         }
-        if (probs && open)
-            for (int i = R.first() + tid; i < R.last(P.split.per_cta); i += kThreads) probs[i] = 0.0f;
+        if (probs && open) write_zeros(R, probs);
         return;
     }
-    if (L == kInf) {  // the tokens at +inf share the row: 0 for them, -inf for the others
-        for (int j = R.lo + R.lane; j < R.hi; j += 32) {
-            T *e = reinterpret_cast<T *>(store + j);
-            for (int i = 0; i < Row<T>::n; ++i) e[i] = as_float(e[i]) == kInf ? T(0) : Low<T>::value();
-        }
-        peak = peak == kInf ? 0.0f : -kInf;
+    if (L == kInf) {  // the tokens at +inf share the row
+        R.inf = true;
         L = cut = 0.0f;
         __syncthreads();
+        for (int g = 0; g < kGroups; ++g) {
+            float *at = room.peaks + g * kThreads + tid;
+            *at = *at == kInf ? 0.0f : -kInf;
+        }
     }
     keep.L = L;
     Exchange ex{sh, rank, cluster, 0};
     if (open) {
-        draw_row<T, true>(P, R, r, u, keep, ex);
+        draw_row<true>(P, R, r, u, keep, ex);
         return;
     }
-    u64 Z = 0;
-    if (k == 0) {
-        if (mass) {
-            collect<T, true>(R, peak, cut, list, part, rank, cluster, keep, false, sh);
-            Z = ex.sum(warp_weight<T, true>(R, keep));
-        } else {
-            const float span = keep.low / keep.inv;
-            cut = fmaxf(L + span - 4e-6f * (fabsf(L) + fabsf(span)), -FLT_MAX);
-            collect<T, false>(R, peak, cut, list, part, rank, cluster, keep, false, sh);
+    if (mass) {
+        // the row's weight, to a part in kSure, and the candidates' exactly: where these reach the share
+        // for sure, the leader draws from the list, unless a border between its tokens lies so near to
+        // the share that this precision does not tell
+        collect<true>(R, cut, room, part, rank, cluster, keep, false, sh);
+        float sum = 0.0f;
+        const float scale = fminf(keep.inv * kLog2e, FLT_MAX);
+        R.template each<kAhead>([&](uint4 (&v)[kAhead], int n, int) { sum += fast_sum<T>(v, n, L, scale); });
+#pragma unroll
+        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
+        const u64 near = ex.sum(__float2ull_rn(sum * 0x1p+40f));
+        Share share{true, share_of(p, near - near / kSure), share_of(p, near + near / kSure + 1)};
+        u64 listed = 0;
+        for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
+        if (cut == -FLT_MAX) share.least = share.most = share_of(p, listed);  // (the whole row is listed)
+        if (all_listed(sh, cluster, part, &total) && listed >= share.most) {
+            if (rank == 0) {
+                const bool done = finish_list<T>(P, r, room.list, room.work, part, total, 0, true, p, share, u, keep, sh);
+                if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
+            }
             cluster_sync();
+            if (sh.fits) return;
         }
-        bool fits = all_listed(sh, cluster, part, &total);
-        if (fits && mass && cut > -FLT_MAX) {  // do the listed tokens reach P of the whole?
-            u64 listed = 0;
-            for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
-            fits = listed >= share_of(p, Z);
-        }
-        if (fits) {
-            if (rank == 0) finish_list<T>(P, r, list, sums, part, total, 0, true, p, Z, u, keep, sh);
-            return;
-        }
+        draw_wide(P, R, r, p, u, keep, room, ex);
+        return;
     }
     if (k > 0) {
-        const unsigned key = find_key<T, false>(R, keep, static_cast<u64>(k), 0, list, sums, part, ex);
+        const unsigned key = find_kth(R, keep, static_cast<u64>(k), room, ex);
         if (key) keep.tau = of_key(key);
+        if (p < 1.0f) draw_wide(P, R, r, p, u, keep, room, ex);
+        else draw_row<false>(P, R, r, u, keep, ex);
+        return;
     }
-    if (p < 1.0f) {
-        if (!mass) Z = held_from<T, true>(R, keep, -FLT_MAX, ex);
-        keep.tau = of_key(find_key<T, true>(R, keep, share_of(p, Z), Z, list, sums, part, ex));
-    }
-    draw_row<T, false>(P, R, r, u, keep, ex);
+    // min-p alone
+    const float span = keep.low / keep.inv;
+    cut = fmaxf(L + span - 4e-6f * (fabsf(L) + fabsf(span)), -FLT_MAX);
+    collect<false>(R, cut, room, part, rank, cluster, keep, false, sh);
+    cluster_sync();
+    if (!all_listed(sh, cluster, part, &total)) draw_row<false>(P, R, r, u, keep, ex);
+    else if (rank == 0) finish_list<T>(P, r, room.list, room.work, part, total, 0, true, p, Share{}, u, keep, sh);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1417,15 +1821,14 @@ __device__ __forceinline__ u64 pack(float a, float b)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logits, LogprobParams P)
 {
-    constexpr int n = Row<T>::n;
+    constexpr int n = Vec<T>::n;
     extern __shared__ uint4 store[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, cluster = P.cluster, top = P.num_top;
     const unsigned rank = cluster_rank();
     const long long r = blockIdx.x / cluster;
     const T *row = logits + r * P.stride;
-    u64 *list = reinterpret_cast<u64 *>(store + P.split.per_cta);
-    u64 *work = list + kList;
+    const Room room(store);
     const int token = P.tokens ? row_token(P, r) : 0;
     const bool wanted = token >= 0 && token < P.V;
     if (!wanted) {
@@ -1438,52 +1841,33 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
         }
         return;
     }
-    const Row<T> R = start_row(row, P.V, P.split, store, rank);
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
+    const Row<T> R = start_row(row, P.V, P.split, rank, sh);
     const float lt = fmaxf(as_float(__ldg(row + token)), -kInf);  // (NaN as -inf)
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
     const float scale = fminf(inv * kLog2e, FLT_MAX);
-    // every portion of a lane's vectors against the largest so far
+    // some vectors at a time, against the largest logit so far
     float peak = -kInf, s = 0.0f;
     Above<T> above(lt);
-    by_portions(R, [&](int first, int end) {
-        Largest<T> m;
-#pragma unroll 4
-        for (int j = first; j < end; j += 32) m.add(R.vec[j]);
-        const float ref = fmaxf(peak, m.get());
+    R.template each<kAhead>([&](uint4 (&v)[kAhead], int m, int c) {
+        Largest<T> largest;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) largest.add(v[i]);
+        const float own = largest.get(), ref = fmaxf(peak, own);
+        if (top > 0) {
+            float *at = room.peaks + (c % kGroups) * kThreads + tid;
+            *at = c < kGroups ? own : fmaxf(*at, own);
+        }
         if (ref > peak) {
             if (peak > -kInf) s *= sv::ex2_approx((peak - ref) * scale);
             peak = ref;
         }
-        Two sum = two(0.0f);
-#pragma unroll 4
-        for (int j = first; j < end; j += 32) {
-            const uint4 v = R.vec[j];
-            above.add(v);
-            float f[n];
-            Vec<T>::get(v, f);
 #pragma unroll
-            for (int e = 0; e < n; e += 2) {
-                const Two x = (two(f[e], f[e + 1]) + two(-ref)) * two(scale);
-                float a, b;
-                parts(x, a, b);
-                sum = sum + two(sv::ex2_approx(a), sv::ex2_approx(b));
-            }
-        }
-        float a, b;
-        parts(sum, a, b);
-        a += b;
-        if (a != a) {  // a NaN among them, or logits of +inf (those share the row) or -inf alone
-            a = 0.0f;
-            for (int j = first; j < end; j += 32) {
-                float f[n];
-                Vec<T>::get(R.vec[j], f);
-                for (int e = 0; e < n; ++e)
-                    if (f[e] > -kInf) a += f[e] == ref ? 1.0f : sv::ex2_approx((f[e] - ref) * scale);
-            }
-        }
-        s += a;
+        for (int i = 0; i < kAhead; ++i)
+            if (i < m) above.add(v[i]);
+        above.flush();
+        s += fast_sum<T>(v, m, ref, scale);
     });
     const float top_of_warp = warp_max(peak);
     if (peak < top_of_warp && s > 0.0f) s *= sv::ex2_approx((peak - top_of_warp) * scale);
@@ -1499,7 +1883,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
     if (top > 0) {
         const float largest = block_max(peak, sh);
         const float cut = largest > -kInf && largest < kInf ? cut_for(peak, largest, min(top, part / 8 * 5), sh) : -FLT_MAX;
-        collect<T, false>(R, peak, cut, list, part, rank, cluster, Kept{}, true, sh);
+        collect<false>(R, cut, room, part, rank, cluster, Kept{}, true, sh);
     }
     cluster_sync();
     float L = -kInf;
@@ -1547,16 +1931,16 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
             u64 mine[kList / kThreads];
 #pragma unroll
             for (int q = 0; q < kList / kThreads; ++q)
-                mine[q] = tid + q * kThreads < total ? listed_entry(list, part, cluster, sh, tid + q * kThreads) : 0;
+                mine[q] = tid + q * kThreads < total ? listed_entry(room.list, part, cluster, sh, tid + q * kThreads) : 0;
 #pragma unroll
             for (int q = 0; q < kList / kThreads; ++q)
-                if (mine[q]) work[tid + q * kThreads] = mine[q];
+                if (mine[q]) room.work[tid + q * kThreads] = mine[q];
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < kList / kThreads; ++q)
                 if (mine[q]) {
                     int place = 0;
-                    for (int j = 0; j < total; ++j) place += work[j] > mine[q];
+                    for (int j = 0; j < total; ++j) place += room.work[j] > mine[q];
                     if (place < top) {
                         write(place, mine[q]);
                         done &= of_key(static_cast<unsigned>(mine[q] >> 32)) >= high;
@@ -1574,12 +1958,12 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
     // more ties than the list holds: one token after the other
     cluster_sync();  // (the leader has read what the warps sent)
     Exchange ex{sh, rank, cluster, 0};
-    u64 last = kNone64;
+    u64 last = ~0ull;
     for (int i = 0; i < top; ++i) {
         u64 best = 0;
         for (int j = R.lo + R.lane; j < R.hi; j += 32) {
             float f[n];
-            Vec<T>::get(R.vec[j], f);
+            Vec<T>::get(R.get(j), f);
 #pragma unroll
             for (int e = 0; e < n; ++e) {
                 const unsigned key = key_of(f[e]);
@@ -1633,7 +2017,6 @@ struct DeviceGuard {
 };
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxStore = 232448 - static_cast<int>(sizeof(Shared)) - 1024;  // dynamic shared memory of a CTA
 std::mutex g_rows_mutex;
 bool g_rows_ready[kMaxDevices];
 
@@ -1657,8 +2040,7 @@ int rows_device(int dev)
                           reinterpret_cast<const void *>(sv_sample_kernel<float>),
                           reinterpret_cast<const void *>(sv_logprobs_kernel<uint16_t>),
                           reinterpret_cast<const void *>(sv_logprobs_kernel<float>)})
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStore) != cudaSuccess ||
-            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Room::bytes)) != cudaSuccess) {
             cudaGetLastError();
             return SV_ECUDA;
         }
@@ -1666,40 +2048,36 @@ int rows_device(int dev)
     return SV_OK;
 }
 
-// How a launch splits its rows: CTAs per row, vectors of 16 bytes per CTA and per warp.
+// How a launch splits its rows: CTAs per row, vectors of 16 bytes per CTA and per warp. As many CTAs
+// for a row as the device holds at once (two on each of its 152 SMs) over the rows, in powers of
+// two, and at least a vector for each of their threads.
 struct Shape {
     int cluster;
     Split split;
-    size_t smem;
 };
 
-Shape shape_of(int rows, int V, int elem_bytes, bool lists)
+Shape shape_of(int rows, int V, int elem_bytes, bool wide)
 {
     const int vectors = V / (16 / elem_bytes) + 2;  // (a row may start and end within one)
     int c = 1;
-    // at most 80 KB of a row in a CTA: two or more CTAs on an SM, one computing while another loads
-    while (c < kMaxCluster && (vectors + c - 1) / c > 80 * 1024 / 16) c *= 2;
-    // few rows: more CTAs for each, down to 8 KB in a CTA
-    while (c < kMaxCluster && 2ll * rows * c <= 152 && vectors / (2 * c) >= 512) c *= 2;
+    while (c < kMaxCluster && 2ll * rows * c <= (wide ? 8 : 1) * 304 && vectors >= 2 * c * kThreads) c *= 2;
     Shape s;
     s.cluster = c;
     s.split.per_warp = ((vectors + c - 1) / c + kWarps - 1) / kWarps;
     s.split.per_cta = s.split.per_warp * kWarps;
-    s.smem = static_cast<size_t>(s.split.per_cta) * 16 + (lists ? 2 * kList * 8 : 0);
     return s;
 }
 
 template <typename T, typename Params>
-int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, bool lists, cudaStream_t stream)
+int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, bool lists, bool wide, cudaStream_t stream)
 {
-    const Shape s = shape_of(rows, P.V, sizeof(T), lists);
-    if (s.smem > static_cast<size_t>(kMaxStore)) return SV_ECAPACITY;
+    const Shape s = shape_of(rows, P.V, sizeof(T), wide);
     P.cluster = s.cluster;
     P.split = s.split;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * static_cast<unsigned>(s.cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = s.smem;
+    cfg.dynamicSmemBytes = lists ? Room::bytes : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1754,8 +2132,8 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
     P.probs = a->probs;
     P.V = a->vocab_size;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, true, stream)
-                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, true, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, true, P.top_p && !P.top_k, stream)
+                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, true, P.top_p && !P.top_k, stream);
 }
 
 extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cuda_stream)
@@ -1791,6 +2169,6 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, a->num_top > 0, stream)
-                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, a->num_top > 0, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, a->num_top > 0, false, stream)
+                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, a->num_top > 0, false, stream);
 }
