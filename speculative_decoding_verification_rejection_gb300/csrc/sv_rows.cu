@@ -37,6 +37,7 @@ constexpr int kHits = 2048;       // groups a CTA looks through for candidates
 constexpr int kPairs = 256;       // most entries that are compared each with each
 constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
+constexpr int kBeside = 64;       // tokens on each side of a guess
 constexpr int kBins = 8192;       // bins of the value histogram, two to a word
 constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr float kInf = __builtin_huge_valf();
@@ -1170,19 +1171,22 @@ __device__ unsigned search_key(const RowT &R, const Kept &keep, u64 need, unsign
 
 // A bracket of the value at which the row's tokens from the largest on hold `count` of them or, with
 // kMass, the part p of their weight; of the tokens >= keep.tau. From a histogram of the tokens by
-// value, kBins bins of (L - l) / T: for counts the bin it is in, for weights, which the bins'
-// middles stand for (to a part in 10^6), that and the bins beside it. Where those hold more than
-// the list, a second histogram of just that span narrows it down further. A guess that the caller
-// checks: sh.lower and sh.upper of every CTA.
+// value, kBins bins of (L - l) / T: for counts the bin it is in; for weights, which the bins'
+// middles stand for, that and the bins beside it until they hold kBeside tokens on each side (the
+// error is that of a few tokens: the heaviest, those from `ceiling` on, are not in the histogram, and
+// their weight `above` is exact). Where the bracket holds more than the list, a second histogram of
+// just that span narrows it down further. A guess that the caller checks: sh.lower and sh.upper of
+// every CTA.
 template <bool kMass, typename T>
-__device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, const Room &room, Exchange &ex)
+__device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, float ceiling, u64 above, const Room &room,
+                        Exchange &ex)
 {
     constexpr int n = Row<T>::n, kv = 4;
     Shared &sh = ex.sh;
     const int tid = threadIdx.x, cluster = ex.cluster;
     auto *words = reinterpret_cast<unsigned *>(room.peaks);
     float from = 0.0f, width = kSpan / kBins;  // the bins' first edge and width, as (L - l) / T
-    u64 want = 0, before = 0;                  // (the leader's) what to reach, and what lies before the bins
+    u64 want = 0, before = above >> 9;         // (the leader's, 2^31 to 1) what to reach, and what lies before the bins
     for (int level = 0; level < 2; ++level) {
         const float scale = keep.inv / width, shift = from / width;
         for (int i = tid; i < kBins / 2; i += kThreads) words[i] = 0;
@@ -1196,7 +1200,7 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, c
 #pragma unroll
                     for (int e = 0; e < n; ++e) {
                         const float at = __fmaf_rn(keep.L - f[e], scale, -shift);
-                        if (f[e] >= keep.tau && at >= 0.0f && at < static_cast<float>(kBins)) {
+                        if (f[e] >= keep.tau && f[e] < ceiling && at >= 0.0f && at < static_cast<float>(kBins)) {
                             const int b = static_cast<int>(at);
                             atomicAdd(words + (b >> 1), 1u << (16 * (b & 1)));  // (an overflow spoils the guess only)
                         }
@@ -1227,8 +1231,7 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, c
 #pragma unroll
             for (int i = 0; i < q; ++i) own += held(i);
             const u64 upto = block_scan(own, sh.box, &total);
-            if (level == 0) want = kMass ? share_of(p, total) : count;
-            constexpr int around = kMass ? 1 : 0;
+            if (level == 0) want = kMass ? share_of(p, before + total) : count;
             if (tid == 0) sh.first = kBins;
             __syncthreads();
             u64 run = before + upto;
@@ -1241,32 +1244,59 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, c
             }
             __syncthreads();
             const int b = sh.first;
-            // what the bracket's bins hold in tokens, and what lies before them
-            u64 in = 0;
-            run = before + upto;
-            if (tid == 0) sh.below = before;
+            // the bracket's first and last bin, what it holds in tokens, and what lies before it
+            u64 mine = 0;
+#pragma unroll
+            for (int i = 0; i < q; ++i) mine += c[i];
+            u64 passed = block_scan(mine, sh.box, &tokens);
+            if (tid == 0) {
+                sh.kept = tokens;
+                sh.run = 0;
+                sh.found = kBins - 1;
+                sh.below = before;
+            }
             __syncthreads();
+            u64 at_count = passed;
+#pragma unroll
+            for (int i = 0; i < q; ++i) {
+                if (tid * q + i == b) sh.kept = at_count;
+                at_count += c[i];
+            }
+            __syncthreads();
+            const u64 here = sh.kept;
+            at_count = passed;
 #pragma unroll
             for (int i = 0; i < q; ++i) {
                 const int at = tid * q + i;
-                if (at >= b - around && at <= b + around) in += c[i];
-                if (at == b - around) sh.below = run;
+                if (at < b && at_count + (kMass ? kBeside : 0) <= here) atomicMax(&sh.run, at);
+                at_count += c[i];
+                if (at > b && at_count >= here + 2 * kBeside) atomicMin(&sh.found, at);
+            }
+            __syncthreads();
+            const int head = kMass ? sh.run : min(b, kBins - 1), tail = kMass ? max(sh.found, min(b + 1, kBins - 1)) : min(b, kBins - 1);
+            u64 in = 0;
+            run = before + upto;
+#pragma unroll
+            for (int i = 0; i < q; ++i) {
+                const int at = tid * q + i;
+                if (at >= head && at <= tail) in += c[i];
+                if (at == head) sh.below = run;
                 run += held(i);
             }
             block_scan(in, sh.box, &tokens);
             before = sh.below;
             // (in the last bins or beyond them: everything below)
             const float slack = 4e-6f * fmaxf(fabsf(keep.L), kSpan / keep.inv);
-            const float lo = from + static_cast<float>(max(b - around, 0)) * width, hi = from + static_cast<float>(b + around + 1) * width;
+            const float lo = from + static_cast<float>(head) * width, hi = from + static_cast<float>(tail + 1) * width;
             const float upper = lo <= 0.0f ? keep.L : keep.L - lo / keep.inv + slack;
-            const float lower = b >= kBins - 2 ? -FLT_MAX : keep.L - hi / keep.inv - slack;
+            const float lower = level == 0 && tail == kBins - 1 ? -FLT_MAX : keep.L - hi / keep.inv - slack;
             if (tid < cluster) {
                 put(remote(&sh.upper, tid), __float_as_uint(upper));
                 put(remote(&sh.lower, tid), __float_as_uint(fmaxf(lower, -FLT_MAX)));
                 put(remote(&sh.from, tid), __float_as_uint(lo));
                 put(remote(&sh.width, tid), __float_as_uint((hi - lo) / kBins));
                 // (of bf16 logits with a distinct value or two there a second look tells nothing more)
-                const bool again = level == 0 && b < kBins - 2 && tokens * (cluster > 1 ? 5 : 3) / 3 > kWideList &&
+                const bool again = level == 0 && b < kBins && tokens * (cluster > 1 ? 5 : 3) / 3 > kWideList &&
                                    (sizeof(T) == 4 || key_of(upper) >> 16 > (key_of(lower) >> 16) + 2);
                 put(remote(&sh.again, tid), static_cast<unsigned>(again));
             }
@@ -1384,11 +1414,11 @@ struct Listed {
 // where the row has fewer tokens. Where the bracket holds more than the list, or the guess was wrong,
 // it is found by halving.
 template <typename T>
-__device__ unsigned find_kth(const Row<T> &R, const Kept &keep, u64 k, const Room &room, Exchange &ex)
+__device__ __noinline__ unsigned find_kth(const Row<T> &R, const Kept &keep, u64 k, const Room &room, Exchange &ex)
 {
     Shared &sh = ex.sh;
     const int part = kWideList / ex.cluster;
-    bracket<false>(R, keep, k, 0.0f, room, ex);
+    bracket<false>(R, keep, k, 0.0f, kInf, 0, room, ex);
     const float upper = sh.upper, lower = sh.lower;
     u64 above, all;
     gather<false>(R, keep, lower, upper, room, part, &above, &all, ex);
@@ -1547,15 +1577,16 @@ __device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, fl
 // The draw from a top-p set larger than the list (of the tokens >= keep.tau): a bracket of the least
 // logit in it by the histogram, one pass that sums up all, what lies above the bracket in every
 // warp's run, and lists what lies in it; the leader finds the least logit, adds the listed tokens
-// that are in the set to their runs, and finds the run to draw from.
+// that are in the set to their runs, and finds the run to draw from. (`heavy` is the weight of the
+// tokens >= ceiling, which is below the bracket's tokens' values or +inf with 0.)
 template <typename T>
-__device__ void draw_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, Kept keep, const Room &room,
-                          Exchange &ex)
+__device__ __noinline__ void draw_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, Kept keep, float ceiling,
+                          u64 heavy, const Room &room, Exchange &ex)
 {
     constexpr int n = Row<T>::n;
     Shared &sh = ex.sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cluster = ex.cluster, part = kWideList / cluster;
-    bracket<true>(R, keep, 0, p, room, ex);
+    bracket<true>(R, keep, 0, p, ceiling, heavy, room, ex);
     const float upper = sh.upper, lower = fmaxf(sh.lower, keep.tau);
     u64 above, all;
     gather<true>(R, keep, lower, upper, room, part, &above, &all, ex);
@@ -1754,21 +1785,30 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         u64 listed = 0;
         for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
         if (cut == -FLT_MAX) share.least = share.most = share_of(p, listed);  // (the whole row is listed)
-        if (all_listed(sh, cluster, part, &total) && listed >= share.most) {
+        const bool fits = all_listed(sh, cluster, part, &total);
+        if (fits && listed >= share.most) {
             if (rank == 0) {
                 const bool done = finish_list<T>(P, r, room.list, room.work, part, total, 0, true, p, share, u, keep, sh);
                 if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
             }
             cluster_sync();
             if (sh.fits) return;
+            if (rank == 0 && tid < cluster) sh.count[tid] = tid == 0 ? static_cast<unsigned>(total) : 0;  // (it closed the list up)
         }
-        draw_wide(P, R, r, p, u, keep, room, ex);
+        if (fits && listed >= share.least) {  // too near to tell: exactly, then
+            share.least = share.most = share_of(p, ex.sum(warp_weight<true>(R, keep)));
+            if (listed >= share.least) {
+                if (rank == 0) finish_list<T>(P, r, room.list, room.work, part, total, 0, true, p, share, u, keep, sh);
+                return;
+            }
+        }
+        draw_wide(P, R, r, p, u, keep, fits ? cut : kInf, fits ? listed : 0, room, ex);
         return;
     }
     if (k > 0) {
         const unsigned key = find_kth(R, keep, static_cast<u64>(k), room, ex);
         if (key) keep.tau = of_key(key);
-        if (p < 1.0f) draw_wide(P, R, r, p, u, keep, room, ex);
+        if (p < 1.0f) draw_wide(P, R, r, p, u, keep, kInf, 0, room, ex);
         else draw_row<false>(P, R, r, u, keep, ex);
         return;
     }
