@@ -38,7 +38,7 @@ constexpr int kPairs = 256;       // most entries that are compared each with ea
 constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
 constexpr int kBeside = 64;       // tokens on each side of a guess
-constexpr int kBins = 8192;       // bins of the value histogram, two to a word
+constexpr int kBins = 4096;       // bins of the value histogram
 constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
@@ -351,6 +351,25 @@ struct WeightSum {
     }
 };
 
+// Two such sums at once: of all weights added, and of those that are marked.
+struct WeightSums {
+    unsigned a = 0, b = 0, ma = 0, mb = 0;
+    __device__ __forceinline__ void add(Two t, bool first, bool second)
+    {
+        const Two x = t + two(12.0f);
+        const Two y = fma(x + two(-12.0f), two(-1.0f), t) + two(0x1.8p-17f);
+        float p, q;
+        parts(x, p, q);
+        a += __float_as_uint(p) + __float_as_uint(q);
+        ma += (first ? __float_as_uint(p) : __float_as_uint(12.0f)) + (second ? __float_as_uint(q) : __float_as_uint(12.0f));
+        parts(y, p, q);
+        b += __float_as_uint(p) + __float_as_uint(q);
+        mb += (first ? __float_as_uint(p) : __float_as_uint(0x1.8p-17f)) + (second ? __float_as_uint(q) : __float_as_uint(0x1.8p-17f));
+    }
+    __device__ __forceinline__ u64 total(int n) const { return WeightSum{a, b}.total(n); }
+    __device__ __forceinline__ u64 total_marked(int n) const { return WeightSum{ma, mb}.total(n); }
+};
+
 __device__ __forceinline__ u64 weight(float t)
 {
     WeightSum s;
@@ -459,6 +478,42 @@ __device__ u64 block_scan(u64 v, u64 *box, u64 *all)
     return before + s - v;
 }
 
+// The same for a float and a whole number, totals in *all and *count (`box` takes both).
+__device__ __forceinline__ void block_scan(float &v, unsigned &c, u64 *box, float *all, unsigned *count)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float s = v;
+    unsigned t = c;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const float o = __shfl_up_sync(0xFFFFFFFFu, s, k);
+        const unsigned p = __shfl_up_sync(0xFFFFFFFFu, t, k);
+        if (lane >= k) {
+            s += o;
+            t += p;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) box[warp] = (static_cast<u64>(t) << 32) | __float_as_uint(s);
+    __syncthreads();
+    float before = 0.0f, total = 0.0f;
+    unsigned fewer = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const u64 x = box[w];
+        if (w < warp) {
+            before += __uint_as_float(static_cast<unsigned>(x));
+            fewer += static_cast<unsigned>(x >> 32);
+        }
+        total += __uint_as_float(static_cast<unsigned>(x));
+        sum += static_cast<unsigned>(x >> 32);
+    }
+    *all = total;
+    *count = sum;
+    v = before + s - v;
+    c = fewer + t - c;
+}
+
 // ---------------------------------------------------------------------------------------
 // a row over a cluster
 // ---------------------------------------------------------------------------------------
@@ -505,7 +560,7 @@ struct Room {
         : list(static_cast<u64 *>(p)), work(list + kList), peaks(reinterpret_cast<float *>(work + kList)),
           hits(reinterpret_cast<unsigned *>(peaks + kGroups * kThreads)) {}
 };
-static_assert(kBins / 2 == kGroups * kThreads && kWideList == 2 * kList, "what shares a room");
+static_assert(kBins == kGroups * kThreads && kWideList == 2 * kList, "what shares a room");
 
 template <typename T>
 struct Row {
@@ -610,24 +665,6 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     return R;
 }
 
-// The largest of this lane's logits, and of each group of them (times c of kAhead vectors with the
-// same c mod kGroups) into `peaks`.
-template <typename T>
-__device__ __forceinline__ float lane_max(const Row<T> &R, float *peaks)
-{
-    float all = -kInf;
-    R.template each<kAhead>([&](uint4 (&v)[kAhead], int, int c) {
-        Largest<T> m;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) m.add(v[i]);
-        float *at = peaks + (c % kGroups) * kThreads + threadIdx.x;
-        const float own = m.get();
-        *at = c < kGroups ? own : fmaxf(*at, own);
-        all = fmaxf(all, own);
-    });
-    return all;
-}
-
 // Sum of 2^((l - ref) scale) over v[0, m), in binary32, ref the largest logit or more; a NaN and -inf
 // add nothing, and where ref is +inf each logit of +inf adds 1.
 template <typename T, int k>
@@ -664,6 +701,29 @@ __device__ __forceinline__ float fast_sum(const uint4 (&v)[k], int m, float ref,
     return a;
 }
 
+// The largest of this lane's logits, and of each group of them (times c of kAhead vectors with the
+// same c mod kGroups) into `peaks`; with kSum also *sum, the sum of 2^((l - largest) scale) over them.
+template <bool kSum, typename T>
+__device__ __forceinline__ float lane_max(const Row<T> &R, float *peaks, float scale, float *sum)
+{
+    float all = -kInf, s = 0.0f;
+    R.template each<kAhead>([&](uint4 (&v)[kAhead], int n, int c) {
+        Largest<T> m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) m.add(v[i]);
+        float *at = peaks + (c % kGroups) * kThreads + threadIdx.x;
+        const float own = m.get(), ref = fmaxf(all, own);
+        *at = c < kGroups ? own : fmaxf(*at, own);
+        if (kSum) {
+            if (ref > all && all > -kInf) s *= sv::ex2_approx((all - ref) * scale);
+            s += fast_sum<T>(v, n, ref, scale);
+        }
+        all = ref;
+    });
+    if (kSum) *sum = s;
+    return all;
+}
+
 // The largest of a value over the block.
 __device__ __forceinline__ float block_max(float v, Shared &sh)
 {
@@ -677,12 +737,14 @@ __device__ __forceinline__ float block_max(float v, Shared &sh)
 // A cut that at least `want` of this CTA's lane maxima reach and at most a quarter more, or what
 // twenty halvings of the span of keys from the least to the largest of them give; the lowest
 // finite number where there are not so many. The CTA's tokens at or above it hold its `want` largest, and are few more than that.
+template <typename T>
 __device__ float cut_for(float peak, float largest, int want, Shared &sh)
 {
-    const unsigned key = key_of(peak);
+    constexpr int drop = sizeof(T) == 2 ? 16 : 0;  // (of bf16 logits the upper half of the key says all)
+    const unsigned key = key_of(peak) >> drop;
     int reach = __syncthreads_count(key != 0);
     if (reach < want) return -FLT_MAX;
-    unsigned lo = key_of(-block_max(key ? -peak : -kInf, sh)), hi = key_of(largest);
+    unsigned lo = key_of(-block_max(key ? -peak : -kInf, sh)) >> drop, hi = key_of(largest) >> drop;
     for (int i = 0; i < 20 && lo < hi && reach > want + (want >> 2); ++i) {
         const unsigned mid = lo + (hi - lo) / 2 + 1;
         const int c = __syncthreads_count(key >= mid);
@@ -693,7 +755,7 @@ __device__ float cut_for(float peak, float largest, int want, Shared &sh)
             hi = mid - 1;
         }
     }
-    return of_key(lo);
+    return of_key(lo << drop);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -709,11 +771,14 @@ struct SampleParams {
     Split split;
 };
 
-// The row's weight by fast_sum is off by less than one part in kSure: the 2^x by 2^-22, its argument,
-// at most 42, by three roundings (42 3 2^-24 ln 2 = 2^-17.5), a chain of at most 32 + 16 additions by
-// as many, the joining of lanes and warps by a dozen more, the weights' own exp by 2^-23 and their
-// rounding to 2^-40 by V 2^-41: together below 2^-16.
-constexpr u64 kSure = 1 << 16;
+// The row's weight by the lanes' sums is off by less than one part in kSure: a term's 2^x by 2^-22,
+// its argument, at most 42, by three roundings (42 3 2^-24 ln 2 < 2^-17.5); the same again where a
+// lane's sum is taken from one largest logit to another, which happens to a sum at most 33 times (once
+// for each of up to 32 times it is added to, and to the row's), each time by 2^-22 and the rounding
+// of a difference that these 33 add up to at most 42; a chain of at most 32 + 32 additions by as many
+// roundings; the weights' own exp by 2^-23 and their rounding to 2^-40 by V 2^-41. Together below
+// 2^-17.5 + 2^-17.5 + 33 2^-22 + 64 2^-24 + 2^-21 < 2^-15.
+constexpr u64 kSure = 1 << 15;
 
 // What is kept, besides key_of(l) != 0: l >= tau and d >= low.
 struct Kept {
@@ -1169,27 +1234,36 @@ __device__ unsigned search_key(const RowT &R, const Kept &keep, u64 need, unsign
     return max(lo << drop, least);
 }
 
+// What is known of a row before its bracket is looked for: the weight `heavy` (2^40 to 1) of the
+// tokens >= ceiling (+inf and 0: nothing is), the -d beyond which it does not lie, and about the weight
+// of the whole (1 to 1; 0: nothing is).
+struct Known {
+    float ceiling, lowest, whole;
+    u64 heavy;
+};
+
 // A bracket of the value at which the row's tokens from the largest on hold `count` of them or, with
 // kMass, the part p of their weight; of the tokens >= keep.tau. From a histogram of the tokens by
-// value, kBins bins of (L - l) / T: for counts the bin it is in; for weights, which the bins'
-// middles stand for, that and the bins beside it until they hold kBeside tokens on each side (the
-// error is that of a few tokens: the heaviest, those from `ceiling` on, are not in the histogram, and
-// their weight `above` is exact). Where the bracket holds more than the list, a second histogram of
-// just that span narrows it down further. A guess that the caller checks: sh.lower and sh.upper of
-// every CTA.
+// d, kBins bins: for counts the bin it is in; for weights, which the bins' middles stand for, that and
+// the bins beside it until they hold kBeside tokens on each side (the error is that of a few tokens:
+// the heaviest, those from known.ceiling on, are not in the histogram, and their weight is exact).
+// Where the bracket holds more than the list, a second histogram of just that span narrows it down
+// further. A guess that the caller checks: sh.lower and sh.upper of every CTA.
 template <bool kMass, typename T>
-__device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, float ceiling, u64 above, const Room &room,
+__device__ void bracket(const Row<T> &R, const Kept &keep, unsigned count, float p, const Known &known, const Room &room,
                         Exchange &ex)
 {
     constexpr int n = Row<T>::n, kv = 4;
     Shared &sh = ex.sh;
     const int tid = threadIdx.x, cluster = ex.cluster;
-    auto *words = reinterpret_cast<unsigned *>(room.peaks);
-    float from = 0.0f, width = kSpan / kBins;  // the bins' first edge and width, as (L - l) / T
-    u64 want = 0, before = above >> 9;         // (the leader's, 2^31 to 1) what to reach, and what lies before the bins
+    auto *bins = reinterpret_cast<unsigned *>(room.peaks);
+    // the bins' first edge and width, in -d
+    float from = known.ceiling < kInf ? (keep.L - known.ceiling) * keep.inv * 1.000001f : 0.0f;
+    float width = fmaxf(fminf(known.lowest, kSpan) - from, 1e-3f) / kBins;
+    float before = static_cast<float>(known.heavy >> 20) * 0x1p-20f, want = 0.0f;  // (the leader's)
     for (int level = 0; level < 2; ++level) {
         const float scale = keep.inv / width, shift = from / width;
-        for (int i = tid; i < kBins / 2; i += kThreads) words[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
         __syncthreads();
         R.template each<kv>([&](uint4 (&v)[kv], int m, int) {
 #pragma unroll
@@ -1199,96 +1273,101 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, f
                     Vec<T>::get(v[i], f);
 #pragma unroll
                     for (int e = 0; e < n; ++e) {
-                        const float at = __fmaf_rn(keep.L - f[e], scale, -shift);
-                        if (f[e] >= keep.tau && f[e] < ceiling && at >= 0.0f && at < static_cast<float>(kBins)) {
-                            const int b = static_cast<int>(at);
-                            atomicAdd(words + (b >> 1), 1u << (16 * (b & 1)));  // (an overflow spoils the guess only)
-                        }
+                        const int b = __float2int_rd(__fmaf_rn(keep.L - f[e], scale, -shift));
+                        if (static_cast<unsigned>(b) < kBins && f[e] >= keep.tau) atomicAdd(bins + b, 1u);
                     }
                 }
         });
         cluster_sync();
         if (ex.rank == 0) {
             constexpr int q = kBins / kThreads;  // bins of a thread
+            static_assert(q == 8, "two 16-byte reads");
             unsigned c[q] = {};
             for (int k = 0; k < cluster; ++k)
 #pragma unroll
-                for (int i = 0; i < q / 8; ++i) {
-                    const uint4 v = get16(remote(words + tid * (q / 2) + 4 * i, k));
-                    const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        c[8 * i + 2 * e] += w[e] & 0xFFFFu;
-                        c[8 * i + 2 * e + 1] += w[e] >> 16;
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 v = get16(remote(bins + tid * q + 4 * i, k));
+                    c[4 * i] += v.x;
+                    c[4 * i + 1] += v.y;
+                    c[4 * i + 2] += v.z;
+                    c[4 * i + 3] += v.w;
                 }
-            auto held = [&](int i) -> u64 {
-                if (!kMass) return c[i];
-                const float middle = from + (static_cast<float>(tid * q + i) + 0.5f) * width;
-                return static_cast<u64>(c[i]) * static_cast<unsigned>(0x1p+31f * sv::ex2_approx(-middle * kLog2e));
-            };
-            u64 own = 0, total, tokens;
+            float w[q], mass = 0.0f, total;
+            unsigned tokens = 0, all;
 #pragma unroll
-            for (int i = 0; i < q; ++i) own += held(i);
-            const u64 upto = block_scan(own, sh.box, &total);
-            if (level == 0) want = kMass ? share_of(p, before + total) : count;
-            if (tid == 0) sh.first = kBins;
+            for (int i = 0; i < q; ++i) {
+                float middle = from + (static_cast<float>(tid * q + i) + 0.5f) * width;
+                if (kMass && sizeof(T) == 2) {
+                    // (a bin that holds one bf16 value: that, or the bins of evenly spaced values would all
+                    // be off to one side)
+                    const unsigned near = __float_as_uint(keep.L - middle / keep.inv) + 0x8000u;
+                    const float value = __uint_as_float(near & 0xFFFF0000u);
+                    if (__float2int_rd(__fmaf_rn(keep.L - value, scale, -shift)) == tid * q + i) middle = (keep.L - value) * keep.inv;
+                }
+                w[i] = kMass ? static_cast<float>(c[i]) * sv::ex2_approx(-middle * kLog2e) : static_cast<float>(c[i]);
+                mass += w[i];
+                tokens += c[i];
+            }
+            float run = mass;
+            unsigned passed = tokens;
+            block_scan(run, passed, sh.box, &total, &all);
+            if (level == 0) want = kMass ? p * (known.whole > 0.0f ? known.whole : before + total) : static_cast<float>(count);
+            // the bin in which it lies, and the number of tokens before it
+            if (tid == 0) {
+                sh.first = before < want ? kBins : 0;
+                sh.mine = before < want ? all : 0;
+                sh.run = 0;
+                sh.found = kBins - 1;
+            }
             __syncthreads();
-            u64 run = before + upto;
-            if (run + own >= want && run < want) {
+            run += before;
+            if (run < want && run + mass >= want) {
+                int i = 0;
+                unsigned t = passed;
+                float m = run;
 #pragma unroll
-                for (int i = 0; i < q; ++i) {
-                    run += held(i);
-                    if (run >= want) atomicMin(&sh.first, tid * q + i);
-                }
+                for (int j = 0; j < q - 1; ++j)
+                    if (i == j && m + w[j] < want) {
+                        m += w[j];
+                        t += c[j];
+                        ++i;
+                    }
+                if (atomicMin(&sh.first, tid * q + i) > tid * q + i) sh.mine = t;
             }
             __syncthreads();
             const int b = sh.first;
-            // the bracket's first and last bin, what it holds in tokens, and what lies before it
-            u64 mine = 0;
+            const unsigned here = sh.mine, beside = kMass ? kBeside : 0;
+            // the bracket's first bin: the last one below b before which `beside` fewer tokens lie; its
+            // last: the first one above b up to which as many more lie
+            if (kMass && b < kBins) {
+                unsigned t = passed;
 #pragma unroll
-            for (int i = 0; i < q; ++i) mine += c[i];
-            u64 passed = block_scan(mine, sh.box, &tokens);
-            if (tid == 0) {
-                sh.kept = tokens;
-                sh.run = 0;
-                sh.found = kBins - 1;
-                sh.below = before;
+                for (int i = 0; i < q; ++i) {
+                    const int at = tid * q + i;
+                    if (at < b && t + beside <= here) atomicMax(&sh.run, at);
+                    t += c[i];
+                    if (at > b && t >= here + 2 * beside) atomicMin(&sh.found, at);
+                }
             }
             __syncthreads();
-            u64 at_count = passed;
-#pragma unroll
-            for (int i = 0; i < q; ++i) {
-                if (tid * q + i == b) sh.kept = at_count;
-                at_count += c[i];
-            }
-            __syncthreads();
-            const u64 here = sh.kept;
-            at_count = passed;
-#pragma unroll
-            for (int i = 0; i < q; ++i) {
-                const int at = tid * q + i;
-                if (at < b && at_count + (kMass ? kBeside : 0) <= here) atomicMax(&sh.run, at);
-                at_count += c[i];
-                if (at > b && at_count >= here + 2 * kBeside) atomicMin(&sh.found, at);
-            }
-            __syncthreads();
-            const int head = kMass ? sh.run : min(b, kBins - 1), tail = kMass ? max(sh.found, min(b + 1, kBins - 1)) : min(b, kBins - 1);
-            u64 in = 0;
-            run = before + upto;
+            const int head = kMass && b < kBins ? sh.run : min(b, kBins - 1);
+            const int tail = kMass && b < kBins ? max(sh.found, min(b + 1, kBins - 1)) : min(b, kBins - 1);
+            // what the bracket holds in tokens, and what lies before it
+            unsigned in = 0;
+            float m = run, none = 0.0f, unused;
 #pragma unroll
             for (int i = 0; i < q; ++i) {
                 const int at = tid * q + i;
                 if (at >= head && at <= tail) in += c[i];
-                if (at == head) sh.below = run;
-                run += held(i);
+                if (at == head) sh.d = m;
+                m += w[i];
             }
-            block_scan(in, sh.box, &tokens);
-            before = sh.below;
-            // (in the last bins or beyond them: everything below)
+            block_scan(none, in, sh.box, &unused, &all);
+            before = sh.d;
+            // (in the last bin or beyond it: everything below)
             const float slack = 4e-6f * fmaxf(fabsf(keep.L), kSpan / keep.inv);
             const float lo = from + static_cast<float>(head) * width, hi = from + static_cast<float>(tail + 1) * width;
-            const float upper = lo <= 0.0f ? keep.L : keep.L - lo / keep.inv + slack;
+            const float upper = head == 0 && level == 0 ? (known.ceiling < kInf ? known.ceiling : keep.L) : keep.L - lo / keep.inv + slack;
             const float lower = level == 0 && tail == kBins - 1 ? -FLT_MAX : keep.L - hi / keep.inv - slack;
             if (tid < cluster) {
                 put(remote(&sh.upper, tid), __float_as_uint(upper));
@@ -1296,7 +1375,7 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, f
                 put(remote(&sh.from, tid), __float_as_uint(lo));
                 put(remote(&sh.width, tid), __float_as_uint((hi - lo) / kBins));
                 // (of bf16 logits with a distinct value or two there a second look tells nothing more)
-                const bool again = level == 0 && b < kBins && tokens * (cluster > 1 ? 5 : 3) / 3 > kWideList &&
+                const bool again = level == 0 && b < kBins && all * (cluster > 1 ? 5 : 3) / 3 > kWideList &&
                                    (sizeof(T) == 4 || key_of(upper) >> 16 > (key_of(lower) >> 16) + 2);
                 put(remote(&sh.again, tid), static_cast<unsigned>(again));
             }
@@ -1310,8 +1389,8 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, u64 count, float p, f
 
 // One pass over the row for a bracket: the tokens within it go to the leader's list as (key, ~index);
 // *above: this warp's tokens above it or, with kMass, their weight, and *all the weight of all tokens
-// >= keep.tau.
-template <bool kMass, typename T>
+// >= keep.tau (kAll: of all).
+template <bool kMass, bool kAll, typename T>
 __device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float lower, float upper, const Room &room, int part,
                                        u64 *above, u64 *all, Exchange &ex)
 {
@@ -1321,7 +1400,7 @@ __device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float 
     if (tid == 0) sh.mine = 0;
     __syncthreads();
     u64 *mine = room.list + ex.rank * part;
-    WeightSum over, total;
+    WeightSums sums;
     int count = 0;
     R.template each<kv>([&](uint4 (&v)[kv], int m, int c) {
 #pragma unroll
@@ -1333,10 +1412,7 @@ __device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float 
 #pragma unroll
             for (int e = 0; e < n; e += 2) {
                 if (kMass) {
-                    float a, b;
-                    parts(kept_weight<true>(f[e], f[e + 1], keep), a, b);
-                    total.add(two(f[e] >= keep.tau ? a : 0.0f, f[e + 1] >= keep.tau ? b : 0.0f));
-                    over.add(two(f[e] > upper ? a : 0.0f, f[e + 1] > upper ? b : 0.0f));
+                    sums.add(kept_weight<kAll>(f[e], f[e + 1], keep), f[e] > upper, f[e + 1] > upper);
                 } else {
                     count += f[e] > upper;
                     count += f[e + 1] > upper;
@@ -1355,8 +1431,8 @@ __device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float 
         }
         if (kMass) count += n * m;
     });
-    *above = warp_sum(kMass ? over.total(count) : static_cast<u64>(count));
-    *all = kMass ? warp_sum(total.total(count)) : 0;
+    *above = warp_sum(kMass ? sums.total_marked(count) : static_cast<u64>(count));
+    *all = kMass ? warp_sum(sums.total(count)) : 0;
     __syncthreads();
     const int listed = static_cast<int>(sh.mine);
     if (ex.rank != 0)
@@ -1418,10 +1494,10 @@ __device__ __noinline__ unsigned find_kth(const Row<T> &R, const Kept &keep, u64
 {
     Shared &sh = ex.sh;
     const int part = kWideList / ex.cluster;
-    bracket<false>(R, keep, k, 0.0f, kInf, 0, room, ex);
+    bracket<false>(R, keep, static_cast<unsigned>(k), 0.0f, Known{kInf, kSpan, 0.0f, 0}, room, ex);
     const float upper = sh.upper, lower = sh.lower;
     u64 above, all;
-    gather<false>(R, keep, lower, upper, room, part, &above, &all, ex);
+    gather<false, true>(R, keep, lower, upper, room, part, &above, &all, ex);
     const u64 over = ex.sum(above);
     int total;
     unsigned found = 0;
@@ -1577,19 +1653,21 @@ __device__ void draw_row(const SampleParams &P, const Row<T> &R, long long r, fl
 // The draw from a top-p set larger than the list (of the tokens >= keep.tau): a bracket of the least
 // logit in it by the histogram, one pass that sums up all, what lies above the bracket in every
 // warp's run, and lists what lies in it; the leader finds the least logit, adds the listed tokens
-// that are in the set to their runs, and finds the run to draw from. (`heavy` is the weight of the
-// tokens >= ceiling, which is below the bracket's tokens' values or +inf with 0.)
+// that are in the set to their runs, and finds the run to draw from.
 template <typename T>
-__device__ __noinline__ void draw_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, Kept keep, float ceiling,
-                          u64 heavy, const Room &room, Exchange &ex)
+__device__ __noinline__ void draw_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, Kept keep,
+                                      const Known &known, const Room &room, Exchange &ex)
 {
     constexpr int n = Row<T>::n;
     Shared &sh = ex.sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cluster = ex.cluster, part = kWideList / cluster;
-    bracket<true>(R, keep, 0, p, ceiling, heavy, room, ex);
+    bracket<true>(R, keep, 0, p, known, room, ex);
     const float upper = sh.upper, lower = fmaxf(sh.lower, keep.tau);
     u64 above, all;
-    gather<true>(R, keep, lower, upper, room, part, &above, &all, ex);
+    Kept whole = keep;
+    whole.low = -kInf;
+    if (keep.tau == -FLT_MAX) gather<true, true>(R, whole, lower, upper, room, part, &above, &all, ex);
+    else gather<true, false>(R, whole, lower, upper, room, part, &above, &all, ex);
     if (lane < cluster) put(remote(&sh.runs[ex.rank * kWarps + warp], lane), above);  // (as Exchange does)
     const u64 Z = ex.sum(all);
     u64 over = 0;
@@ -1644,6 +1722,30 @@ __device__ __noinline__ void draw_wide(const SampleParams &P, const Row<T> &R, l
     else draw_row<false>(P, R, r, u, keep, ex);
 }
 
+// The calls of the two functions that stay functions (in line, their registers would be taken from
+// the common rows): with copies, so that what the caller keeps in registers stays there.
+template <typename T>
+__device__ __forceinline__ void call_wide(const SampleParams &P, const Row<T> &R, long long r, float p, float u, const Kept &keep,
+                                          const Known &known, const Room &room, const Exchange &ex)
+{
+    const Row<T> row = R;
+    const Known k = known;
+    const Room m = room;
+    Exchange e = ex;
+    draw_wide(P, row, r, p, u, keep, k, m, e);
+}
+template <typename T>
+__device__ __forceinline__ unsigned call_kth(const Row<T> &R, const Kept &keep, u64 k, const Room &room, Exchange &ex)
+{
+    const Row<T> row = R;
+    const Kept kept = keep;
+    const Room m = room;
+    Exchange e = ex;
+    const unsigned key = find_kth(row, kept, k, m, e);
+    ex.turn = e.turn;
+    return key;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits, SampleParams P)
 {
@@ -1668,7 +1770,10 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     if (probs && !open) write_zeros(R, probs);  // what is kept goes over them
     // (in binary64, by one thread, while the others read)
     if (m > 0.0f && tid == 0) sh.d = __double2float_rn(log(static_cast<double>(fminf(m, 1.0f))));
-    float peak = lane_max(R, room.peaks);
+    const bool mass = p < 1.0f && k == 0 && !greedy;  // the top-p set's total is the whole row's
+    const float scale = fminf(inverse(temp) * kLog2e, FLT_MAX);
+    float sum = 0.0f;
+    const float peak = mass ? lane_max<true>(R, room.peaks, scale, &sum) : lane_max<false>(R, room.peaks, scale, &sum);
     const float largest = block_max(peak, sh);
     cluster_wait();
 
@@ -1711,7 +1816,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
     if (k > 0) {
         // the k largest: of every CTA at least its own k largest, or as many as find place
         const int most = part / 8 * 5;
-        const float cut = cut_for(peak, largest, min(k, most), sh);
+        const float cut = cut_for<T>(peak, largest, min(k, most), sh);
         collect<false>(R, cut, room, part, rank, cluster, keep, true, sh);
         cluster_sync();
         if (all_listed(sh, cluster, part, &total)) {
@@ -1735,8 +1840,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         }
     }
     // the row's largest logit
-    const bool mass = p < 1.0f && k == 0;  // the top-p set's total is the whole row's
-    const float own_cut = mass ? cut_for(peak, largest, kTopP, sh) : 0.0f;
+    const float own_cut = mass ? cut_for<T>(peak, largest, kTopP, sh) : 0.0f;
     if (tid < cluster) {
         put(remote(&sh.peak[rank], tid), __float_as_uint(largest));
         put(remote(&sh.cut[rank], tid), __float_as_uint(own_cut));
@@ -1775,12 +1879,9 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
         // for sure, the leader draws from the list, unless a border between its tokens lies so near to
         // the share that this precision does not tell
         collect<true>(R, cut, room, part, rank, cluster, keep, false, sh);
-        float sum = 0.0f;
-        const float scale = fminf(keep.inv * kLog2e, FLT_MAX);
-        R.template each<kAhead>([&](uint4 (&v)[kAhead], int n, int) { sum += fast_sum<T>(v, n, L, scale); });
-#pragma unroll
-        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
-        const u64 near = ex.sum(__float2ull_rn(sum * 0x1p+40f));
+        // the lanes' sums against the row's largest (a lane of tokens at +inf holds their number)
+        const float own = R.inf ? (peak == kInf ? sum : 0.0f) : peak > -kInf ? sum * sv::ex2_approx((peak - L) * scale) : 0.0f;
+        const u64 near = ex.sum(warp_sum(__float2ull_rn(own * 0x1p+40f)));
         Share share{true, share_of(p, near - near / kSure), share_of(p, near + near / kSure + 1)};
         u64 listed = 0;
         for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
@@ -1802,13 +1903,16 @@ __global__ void __launch_bounds__(kThreads, 2) sv_sample_kernel(const T *logits,
                 return;
             }
         }
-        draw_wide(P, R, r, p, u, keep, fits ? cut : kInf, fits ? listed : 0, room, ex);
+        // (what lies so low that V tokens there hold no more than the rest is not looked through)
+        const float lowest = sv::log_f32(static_cast<float>(P.V) / ((1.0f - p) * as_sum(near))) + 0.1f;
+        const Known known{fits ? cut : kInf, lowest, as_sum(near), fits ? listed : 0};
+        call_wide(P, R, r, p, u, keep, known, room, ex);
         return;
     }
     if (k > 0) {
-        const unsigned key = find_kth(R, keep, static_cast<u64>(k), room, ex);
+        const unsigned key = call_kth(R, keep, static_cast<u64>(k), room, ex);
         if (key) keep.tau = of_key(key);
-        if (p < 1.0f) draw_wide(P, R, r, p, u, keep, kInf, 0, room, ex);
+        if (p < 1.0f) call_wide(P, R, r, p, u, keep, Known{kInf, kSpan, 0.0f, 0}, room, ex);
         else draw_row<false>(P, R, r, u, keep, ex);
         return;
     }
@@ -1922,7 +2026,7 @@ __global__ void __launch_bounds__(kThreads, 2) sv_logprobs_kernel(const T *logit
     const int part = kList / cluster;
     if (top > 0) {
         const float largest = block_max(peak, sh);
-        const float cut = largest > -kInf && largest < kInf ? cut_for(peak, largest, min(top, part / 8 * 5), sh) : -FLT_MAX;
+        const float cut = largest > -kInf && largest < kInf ? cut_for<T>(peak, largest, min(top, part / 8 * 5), sh) : -FLT_MAX;
         collect<false>(R, cut, room, part, rank, cluster, Kept{}, true, sh);
     }
     cluster_sync();
@@ -2096,11 +2200,11 @@ struct Shape {
     Split split;
 };
 
-Shape shape_of(int rows, int V, int elem_bytes, bool wide)
+Shape shape_of(int rows, int V, int elem_bytes)
 {
     const int vectors = V / (16 / elem_bytes) + 2;  // (a row may start and end within one)
     int c = 1;
-    while (c < kMaxCluster && 2ll * rows * c <= (wide ? 8 : 1) * 304 && vectors >= 2 * c * kThreads) c *= 2;
+    while (c < kMaxCluster && 2ll * rows * c <= 304 && vectors >= 2 * c * kThreads) c *= 2;
     Shape s;
     s.cluster = c;
     s.split.per_warp = ((vectors + c - 1) / c + kWarps - 1) / kWarps;
@@ -2109,9 +2213,9 @@ Shape shape_of(int rows, int V, int elem_bytes, bool wide)
 }
 
 template <typename T, typename Params>
-int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, bool lists, bool wide, cudaStream_t stream)
+int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, bool lists, cudaStream_t stream)
 {
-    const Shape s = shape_of(rows, P.V, sizeof(T), wide);
+    const Shape s = shape_of(rows, P.V, sizeof(T));
     P.cluster = s.cluster;
     P.split = s.split;
     cudaLaunchConfig_t cfg = {};
@@ -2172,8 +2276,8 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
     P.probs = a->probs;
     P.V = a->vocab_size;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, true, P.top_p && !P.top_k, stream)
-                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, true, P.top_p && !P.top_k, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_sample_kernel<uint16_t>, a->logits, P, a->num_rows, true, stream)
+                                      : launch(sv_sample_kernel<float>, a->logits, P, a->num_rows, true, stream);
 }
 
 extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cuda_stream)
@@ -2209,6 +2313,6 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, a->num_top > 0, false, stream)
-                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, a->num_top > 0, false, stream);
+    return a->logits_dtype == SV_BF16 ? launch(sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, a->num_top > 0, stream)
+                                      : launch(sv_logprobs_kernel<float>, a->logits, P, a->num_rows, a->num_top > 0, stream);
 }
