@@ -34,7 +34,8 @@ constexpr int kAhead = 8;         // vectors a lane reads before it uses the fir
 constexpr int kGroups = 8;        // groups of a lane's vectors whose maxima are kept
 constexpr int kList = 1024;       // entries of the leader's candidate list
 constexpr int kHits = 2048;       // groups a CTA looks through for candidates
-constexpr int kPairs = 256;       // most entries that are compared each with each
+constexpr int kPairs = 256;       // most entries that are compared each with each, and the threads that do it
+constexpr int kFewPairs = 128;    // most that are so before the k largest are picked out
 constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
 constexpr int kBeside = 64;       // tokens on each side of a guess
@@ -657,6 +658,7 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     R.edge = sh.edge;
     R.front = off != 0 && rank == 0 ? 0 : -1;
     R.back = (off + V) % n != 0 && vectors - 1 - v0 < R.mine ? vectors - 1 - v0 : -1;
+    if (off == 0 && (off + V) % n == 0) return R;
     if (threadIdx.x < 2 * n) {
         const int k = threadIdx.x / n, e = threadIdx.x % n, i = (k == 0 ? 0 : vectors - 1) * n - off + e;
         reinterpret_cast<T *>(&sh.edge[k])[e] = i >= 0 && i < V ? __ldg(row + i) : Low<T>::value();
@@ -956,46 +958,87 @@ struct Share {
     u64 least, most;
 };
 
-// The draw from `count` entries of work[0, count) with their weights in wts, at most kPairs of them:
-// what lies above each in value, and then before each in index, is summed over all pairs, several
-// threads to an entry.
-__device__ bool draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums, int count, const Share &share, float u,
-                           Shared &sh)
+// Among the first kPairs threads of the block, by a barrier of their own.
+__device__ __forceinline__ void pairs_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPairs) : "memory"); }
+__device__ __forceinline__ u64 pairs_sum(u64 v, u64 *box)
+{
+    v = warp_sum(v);
+    pairs_sync();
+    if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
+    pairs_sync();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kPairs / 32; ++w) v += box[w];
+    return v;
+}
+
+// The draw from `count` entries of work[0, count) with their weights in wts, at most kPairs of them
+// (with k > 0 from the k largest and their equals): what lies above each in value, and then before
+// each in index, is counted and summed over all pairs, several threads to an entry. By half the
+// block: more warps would wait on one another's instructions longer than they save.
+__device__ bool draw_pairs(const Drawn &out, const u64 *work, u64 *wts, int count, int k, float p, Share share, u64 *part,
+                           u64 *box, float u, Shared &sh)
 {
     const int tid = threadIdx.x;
-    int each = 32;  // threads side by side, one for each entry
+    if (tid >= kPairs) return true;
+    int each = 64;  // threads side by side, one for each entry
     while (each < count) each *= 2;
-    const int ways = kThreads / each, i = tid & (each - 1), way = tid / each;
+    const int ways = kPairs / each, i = tid & (each - 1), way = tid / each;
     const int from = way * ((count + ways - 1) / ways), to = min(from + (count + ways - 1) / ways, count);
+    const bool first = way == 0;
     const u64 entry = i < count ? work[i] : 0;
     const auto key = static_cast<unsigned>(entry >> 32);
+    u64 w = i < count ? wts[i] : 0;
     bool keep = i < count && listed_delta(key, out.keep) >= out.keep.low;
-    if (share.on) {
+    const bool within = k > 0 && p < 1.0f;  // the share is of what top-k keeps
+    if (k > 0 || share.on || within) {
         u64 above = 0;
+        unsigned larger = 0;
+#pragma unroll 4
         for (int j = from; j < to; ++j)
-            if (static_cast<unsigned>(work[j] >> 32) > key) above += wts[j];
-        part_sums[tid] = above;
-        __syncthreads();
-        above = 0;
-        for (int w = 0; w < ways; ++w) above += part_sums[w * each + i];
-        if (__syncthreads_or(i < count && above >= share.least && above < share.most)) return false;
-        keep = keep && above < share.least;
+            if (static_cast<unsigned>(work[j] >> 32) > key) {
+                above += wts[j];
+                ++larger;
+            }
+        if (ways > 1) {  // (the number goes above the weight: 2^40 times 2^8 entries)
+            part[tid] = (static_cast<u64>(larger) << 48) + above;
+            pairs_sync();
+            above = 0;
+            for (int v = 0; v < ways; ++v) above += part[v * each + i];
+            larger = static_cast<unsigned>(above >> 48);
+            above &= (1ull << 48) - 1;
+        }
+        const bool among = k == 0 || larger < static_cast<unsigned>(k);
+        if (within) {
+            share.on = true;
+            share.least = share.most = share_of(p, pairs_sum(first && among ? w : 0, box));
+        }
+        keep = keep && among;
+        if (share.on) {
+            if (share.least != share.most) {
+                const u64 doubt = pairs_sum(i < count && above >= share.least && above < share.most ? 1 : 0, box);
+                if (doubt) return false;
+            }
+            keep = keep && above < share.least;
+        }
     }
-    const bool first = way == 0;
-    const u64 w = keep ? wts[i] : 0;
-    u64 kept;
-    block_scan(first ? w : 0, sh.box, &kept);  // (its barriers also stand between the uses of wts)
+    w = keep ? w : 0;
+    const u64 kept = pairs_sum(first ? w : 0, box);  // (its barriers also stand between the uses of wts)
     if (first && i < count) wts[i] = w;
-    __syncthreads();
-    const auto index = static_cast<unsigned>(~static_cast<unsigned>(entry));
+    pairs_sync();
+    const auto index = ~static_cast<unsigned>(entry);
     u64 upto = 0;
+#pragma unroll 4
     for (int j = from; j < to; ++j)
         if (~static_cast<unsigned>(work[j]) <= index) upto += wts[j];
-    part_sums[tid] = upto;
-    __syncthreads();
-    if (first && keep) {
+    if (ways > 1) {
+        part[tid] = upto;
+        pairs_sync();
         upto = 0;
-        for (int v = 0; v < ways; ++v) upto += part_sums[v * each + i];
+        if (first)
+            for (int v = 0; v < ways; ++v) upto += part[v * each + i];
+    }
+    if (first && keep) {
         const Target target(u, kept);
         if (target.passed(upto) && !target.passed(upto - w)) out.token(entry, kept);
         if (out.P.probs) out.prob(entry, inverse_sum(kept));
@@ -1005,7 +1048,8 @@ __device__ bool draw_pairs(const Drawn &out, u64 *work, u64 *wts, u64 *part_sums
 
 // The same for more entries, `size` (a power of two, the rest filled with zeros) of them: sorted by
 // value and summed up, cut off, sorted by index and summed up again.
-__device__ bool draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, const Share &share, float u, Shared &sh)
+__device__ bool draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, bool within, float p, Share share, float u,
+                            Shared &sh)
 {
     const int tid = threadIdx.x;
     sort_down(list, size);
@@ -1016,6 +1060,10 @@ __device__ bool draw_sorted(const Drawn &out, u64 *list, u64 *sums, int size, co
     };
     for (int i = tid * q; i < min(tid * q + q, size); ++i) own += weight_of(list[i]);
     u64 run = block_scan(own, sh.box, &all);
+    if (within) {  // the share is of what is listed
+        share.on = true;
+        share.least = share.most = share_of(p, all);
+    }
     for (int i = tid * q; i < min(tid * q + q, size); ++i) {
         run += weight_of(list[i]);
         sums[i] = run;  // up to and with entry i
@@ -1091,16 +1139,25 @@ __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *
             for (int q = 0; q < kMine; ++q) c += __syncthreads_count(static_cast<unsigned>(mine[q] >> 32) >= key_of(high));
             if (c < k) return false;
         }
-        if (k < total) {
+        if (k < total && total > kFewPairs) {
             const unsigned kth = kth_key<T>(mine, (total + kThreads - 1) / kThreads, k, key_of(low), top);
 #pragma unroll
             for (int q = 0; q < kMine; ++q)
                 if (static_cast<unsigned>(mine[q] >> 32) < kth) mine[q] = 0;
         }
     }
+    const Drawn out{P, r, keep};
+    if (total <= kFewPairs) {
+        u64 *wts = sums, *part = sums + kPairs;
+        if (tid < total) {
+            list[tid] = mine[0];  // (all entries have been read)
+            wts[tid] = weight(exp_weight(listed_delta(static_cast<unsigned>(mine[0] >> 32), keep)));
+        }
+        __syncthreads();
+        return draw_pairs(out, list, wts, total, k, p, share, part, sh.box, u, sh);
+    }
     // the entries left, in any order, closed up
-    u64 w = 0;
-    u64 *work = list, *wts = sums;
+    u64 *wts = sums;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
         const unsigned some = __ballot_sync(0xFFFFFFFFu, mine[q] != 0);
@@ -1108,26 +1165,18 @@ __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *
         if ((tid & 31) == 0 && some) at = static_cast<int>(atomicAdd(&sh.mine, __popc(some)));
         at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(some & ((1u << (tid & 31)) - 1));
         if (mine[q]) {
-            const u64 x = weight(exp_weight(listed_delta(static_cast<unsigned>(mine[q] >> 32), keep)));
-            w += x;
-            work[at] = mine[q];
-            wts[at] = x;
+            list[at] = mine[q];
+            wts[at] = weight(exp_weight(listed_delta(static_cast<unsigned>(mine[q] >> 32), keep)));
         }
     }
-    u64 all;
-    block_scan(w, sh.box, &all);
+    __syncthreads();
     const int count = static_cast<int>(sh.mine);
-    if (k > 0 && p < 1.0f) {
-        share.on = true;
-        share.least = share.most = share_of(p, all);
-    }
-    const Drawn out{P, r, keep};
-    if (count <= kPairs) return draw_pairs(out, work, wts, sums + kPairs, count, share, u, sh);
+    if (count <= kPairs) return draw_pairs(out, list, wts, count, k, p, share, sums + kPairs, sh.box, u, sh);
     int size = 1;
     while (size < count) size *= 2;
     for (int i = count + tid; i < size; i += kThreads) list[i] = 0;
     __syncthreads();
-    return draw_sorted(out, list, sums, size, share, u, sh);
+    return draw_sorted(out, list, sums, size, k > 0 && p < 1.0f, p, share, u, sh);
 }
 
 template <bool kAll>
@@ -1940,15 +1989,18 @@ struct LogprobParams {
 
 // The token wanted of row r: tokens[r], or with prefix sums of the draft lengths the entry of the
 // verification output [num_reqs, token_stride] that row r is the logits of (row cu[i] + i + j is
-// position j of request i). The search stays in [0, num_reqs) whatever cu holds.
-__device__ int row_token(const LogprobParams &P, long long r)
+// position j of request i). A search by every warp, 32 places at a time; it stays in [0, num_reqs)
+// whatever cu holds.
+__device__ __forceinline__ int row_token(const LogprobParams &P, long long r)
 {
     if (!P.cu) return __ldg(P.tokens + r);
+    const int lane = threadIdx.x & 31;
     int lo = 0, hi = P.num_reqs;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<long long>(__ldg(P.cu + mid)) + mid <= r) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+        const bool before = lane == 0 || (at < hi && static_cast<long long>(__ldg(P.cu + at)) + at <= r);
+        lo += (31 - __clz(static_cast<int>(__ballot_sync(0xFFFFFFFFu, before)))) * step;
+        hi = min(hi, lo + step);
     }
     const long long j = r - __ldg(P.cu + lo) - lo;
     return j >= 0 && j < P.token_stride ? __ldg(P.tokens + static_cast<long long>(lo) * P.token_stride + j) : -1;

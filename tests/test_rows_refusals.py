@@ -112,7 +112,7 @@ def test_python_refuses_wrong_tensors(monkeypatch):
     called = []
     monkeypatch.setattr(sv, "spec_verify_sample", lambda *a: called.append(a))
     monkeypatch.setattr(sv, "spec_verify_logprobs", lambda *a: called.append(a))
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: None)
+    monkeypatch.setattr(sv, "_current_stream", lambda index: 0)
     T = FakeTensor
     l, u, out = T((4, 10), f32), T((4,), f32), [T((4,), i32)]
     sv.sample(l, u, out=out)                                           # the good call
