@@ -21,7 +21,8 @@ _ROOT = os.path.dirname(_PKG)
 _INCLUDE = os.path.join(_ROOT, "include")
 _HEADER = os.path.join(_INCLUDE, "spec_verify.h")
 _UNITS = [os.path.join(_PKG, "csrc", f) for f in ("spec_verify.cu", "sv_rows.cu")]
-_SOURCES = [*_UNITS, os.path.join(_PKG, "csrc", "sv_device.cuh")]
+_SOURCES = [*_UNITS, *(os.path.join(_PKG, "csrc", f) for f in ("sv_device.cuh", "sv_rows.cuh",
+                                                                "sv_rows_block.cuh"))]
 # SPEC_VERIFY_DEBUG_BOUNDS=1 in the environment selects the checked build (-DSV_DEBUG_BOUNDS): every
 # global load and store of the kernels is checked against the call's arrays, and an access
 # outside them is skipped and reported as SV_ERR_BOUNDS in the error word. For tests only.
