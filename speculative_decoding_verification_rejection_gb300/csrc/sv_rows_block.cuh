@@ -138,6 +138,7 @@ struct Row {
     int V;
     int lane, warp;
     bool inf;             // read through only_inf()
+    bool plain;           // this warp's run has neither of these vectors, and not inf
 
     static __device__ __forceinline__ uint4 read(const uint4 *p)
     {
@@ -175,12 +176,22 @@ struct Row {
         }
         return min((hi - (j - lane) + 31) / 32, k);
     }
-    // Calls f(v, m, c) for this lane's vectors, k at a time: v[0, m) of the c-th time.
-    template <int k, typename F>
+    // Calls f(v, m, c) for this lane's vectors, k at a time: v[0, m) of the c-th time. With kTwice f is
+    // there twice, once for the times when there is nothing to look at: for passes that compute more
+    // than they wait for memory (a pass of exact sums 31 against 34 us with two rows of 151936 bf16
+    // logits on an SM; in the first pass the registers it takes cost more, 68 against 76 us).
+    template <int k, bool kTwice = false, typename F>
     __device__ __forceinline__ void each(F f) const
     {
-        int c = 0;
-        for (int j = lo + lane; j - lane < hi; j += 32 * k, ++c) {
+        int c = 0, j = lo + lane;
+        if (kTwice && plain)
+            for (; j - lane + 32 * k <= hi; j += 32 * k, ++c) {
+                uint4 v[k];
+#pragma unroll
+                for (int i = 0; i < k; ++i) v[i] = read(vec + j + 32 * i);
+                f(v, k, c);
+            }
+        for (; j - lane < hi; j += 32 * k, ++c) {
             uint4 v[k];
             const int m = load<k>(j, v);
             f(v, m, c);
@@ -219,6 +230,7 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     R.edge = sh.edge;
     R.front = off != 0 && rank == 0 ? 0 : -1;
     R.back = (off + V) % n != 0 && vectors - 1 - v0 < R.mine ? vectors - 1 - v0 : -1;
+    R.plain = !(R.front >= R.lo && R.front < R.hi) && !(R.back >= R.lo && R.back < R.hi);
     if (off == 0 && (off + V) % n == 0) return R;
     if (threadIdx.x < 2 * n) {
         const int k = threadIdx.x / n, e = threadIdx.x % n, i = (k == 0 ? 0 : vectors - 1) * n - off + e;
@@ -756,7 +768,7 @@ __device__ __forceinline__ u64 warp_weight(const RowT &R, const Kept &keep)
     constexpr int n = RowT::n, k = 4;
     WeightSum s;
     int count = 0;
-    R.template each<k>([&](uint4 (&v)[k], int m, int) {
+    R.template each<k, true>([&](uint4 (&v)[k], int m, int) {
 #pragma unroll
         for (int i = 0; i < k; ++i)
             if (i < m) {
@@ -865,7 +877,7 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, unsigned count, float
         const float scale = keep.inv / width, shift = from / width;
         for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
         __syncthreads();
-        R.template each<kv>([&](uint4 (&v)[kv], int m, int) {
+        R.template each<kv, true>([&](uint4 (&v)[kv], int m, int) {
 #pragma unroll
             for (int i = 0; i < kv; ++i)
                 if (i < m) {
@@ -1001,7 +1013,7 @@ __device__ __forceinline__ void gather(const Row<T> &R, const Kept &keep, float 
     u64 *mine = room.list + ex.rank * part;
     WeightSums sums;
     int count = 0;
-    R.template each<kv>([&](uint4 (&v)[kv], int m, int c) {
+    R.template each<kv, true>([&](uint4 (&v)[kv], int m, int c) {
 #pragma unroll
         for (int i = 0; i < kv; ++i) {
             if (i >= m) continue;
@@ -1161,7 +1173,7 @@ __device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const
         }
         return;
     }
-    R.template each<k>([&](uint4 (&v)[k], int m, int c) {
+    R.template each<k, true>([&](uint4 (&v)[k], int m, int c) {
 #pragma unroll
         for (int i = 0; i < k; ++i) {
             const int j = R.lo + R.lane + 32 * (c * k + i);
@@ -1460,6 +1472,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     }
     if (L == kInf) {  // the tokens at +inf share the row
         R.inf = true;
+        R.plain = false;
         L = cut = 0.0f;
         __syncthreads();
         for (int g = 0; g < kGroups; ++g) {
