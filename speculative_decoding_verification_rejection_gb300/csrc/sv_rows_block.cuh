@@ -1564,6 +1564,8 @@ __device__ __forceinline__ u64 pack(float a, float b)
     return (static_cast<u64>(__float_as_uint(a)) << 32) | __float_as_uint(b);
 }
 
+static_assert(SV_MAX_TOP <= kList / kMaxCluster / 8 * 5, "every CTA can list its own best tokens");
+
 // Each warp sums 2^((l - m) / T log2 e) over its logits against its own largest, m, and counts the
 // logits above the token's; the leader joins the warps' sums. The best tokens come from the list
 // of those above the cut that num_top lane maxima reach, sorted by the leader.
@@ -1631,7 +1633,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_logprobs_kernel(const T *l
     const int part = kList / cluster;
     if (top > 0) {
         const float largest = block_max(peak, sh);
-        const float cut = largest > -kInf && largest < kInf ? cut_for<T>(peak, largest, min(top, part / 8 * 5), sh) : -FLT_MAX;
+        const float cut = largest > -kInf && largest < kInf ? cut_for<T>(peak, largest, top, sh) : -FLT_MAX;
         collect<false>(R, cut, room, part, rank, cluster, Kept{}, true, sh);
     }
     cluster_sync();
@@ -1670,39 +1672,24 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_logprobs_kernel(const T *l
     };
     int total;
     if (all_listed(sh, cluster, part, &total)) {
-        const bool sure = top <= part / 8 * 5;  // every CTA listed its own `top` largest
-        if (rank == 0) {
-            // an entry's place is the number of larger ones; past the row's tokens nothing is left
-            bool done = true;
-            float high = -FLT_MAX;
-            for (int c = 0; c < cluster; ++c) high = fmaxf(high, sh.cut[c]);
-            for (int i = total + tid; i < top; i += kThreads) write(i, 0);
-            u64 mine[kList / kThreads];
+        if (rank != 0) return;
+        // an entry's place is the number of larger ones; past the row's tokens nothing is left
+        for (int i = total + tid; i < top; i += kThreads) write(i, 0);
+        u64 mine[kList / kThreads];
 #pragma unroll
-            for (int q = 0; q < kList / kThreads; ++q)
-                mine[q] = tid + q * kThreads < total ? listed_entry(room.list, part, cluster, sh, tid + q * kThreads) : 0;
-#pragma unroll
-            for (int q = 0; q < kList / kThreads; ++q)
-                if (mine[q]) room.work[tid + q * kThreads] = mine[q];
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < kList / kThreads; ++q)
-                if (mine[q]) {
-                    int place = 0;
-                    for (int j = 0; j < total; ++j) place += room.work[j] > mine[q];
-                    if (place < top) {
-                        write(place, mine[q]);
-                        done &= of_key(static_cast<unsigned>(mine[q] >> 32)) >= high;
-                    }
-                }
-            if (!sure) {
-                done = __syncthreads_and(done && (total >= top || high == -FLT_MAX));
-                if (tid < cluster) put(remote(&sh.fits, tid), static_cast<unsigned>(done));
-            }
+        for (int q = 0; q < kList / kThreads; ++q) {
+            mine[q] = tid + q * kThreads < total ? listed_entry(room.list, part, cluster, sh, tid + q * kThreads) : 0;
+            if (mine[q]) room.work[tid + q * kThreads] = mine[q];
         }
-        if (sure) return;
-        cluster_sync();
-        if (sh.fits) return;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kList / kThreads; ++q)
+            if (mine[q]) {
+                int place = 0;
+                for (int j = 0; j < total; ++j) place += room.work[j] > mine[q];
+                if (place < top) write(place, mine[q]);
+            }
+        return;
     }
     // more ties than the list holds: one token after the other
     cluster_sync();  // (the leader has read what the warps sent)

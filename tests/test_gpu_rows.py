@@ -174,6 +174,61 @@ def test_sample_strides(V, stride, probs_stride, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1500, 9001])
+def test_sample_more_rows_than_the_device_holds(V, dtype):
+    """Over 600 rows take the smaller blocks; every kind of row is among them."""
+    R = 640
+    rng = np.random.default_rng(V)
+    l = rows_of(V, R, V, dtype)
+    l[::7] = rows_of(V + 1, l[::7].shape[0], V, dtype, sigma=1.0, n_peak=0)
+    special = special_rows(V, V + 2, -1e30)
+    l[300:300 + special.shape[0]] = special
+    if dtype == "bf16":
+        from _util import bf16_bits_to_f32, to_bf16_bits
+
+        l = bf16_bits_to_f32(to_bf16_bits(l)).reshape(R, V)
+    kw = dict(T=rng.choice([0.0, 0.5, 1.0, 1.4], R), k=rng.choice([0, 0, 0, 1, 20, 200, 700, V - 2], R),
+              P=rng.choice([1.0, 0.95, 0.5], R), M=rng.choice([0.0, 0.0, 0.05], R), u=rng.random(R))
+    got = run_sample(l, dtype, **kw)
+    check_sample(l, got, **kw)
+    same_tokens_without_probs(l, dtype, got, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [2, 40, 200])
+def test_favoured_tokens_side_by_side(R, dtype):
+    """The largest logits stand next to one another, so that one part of the row holds them all."""
+    V, n = 70001, 400
+    rng = np.random.default_rng(R)
+    l = rows_of(R, R, V, dtype, n_peak=0)
+    at = rng.integers(0, V - n, R)
+    for r in range(R):
+        l[r, at[r]:at[r] + n] = 12.0 + rng.permutation(n) / 64.0
+    if dtype == "bf16":                                      # what the GPU gets
+        from _util import bf16_bits_to_f32, to_bf16_bits
+
+        l = bf16_bits_to_f32(to_bf16_bits(l)).reshape(R, V)
+    k = rng.choice([0, 30, 90, 150, 399, 401, 900], R)
+    kw = dict(k=k, P=rng.choice([1.0, 0.9], R), u=rng.random(R))
+    check_sample(l, run_sample(l, dtype, **kw), **kw)
+    tokens = at + rng.integers(0, n, R)
+    check_logprobs(l, run_logprobs(l, dtype, tokens, 64), tokens, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(3, 151936), (170, 20011), (2, 524288)])
+def test_sample_wide_top_p(R, V, dtype):
+    """Top-p sets of thousands of tokens: flat, steep and tied rows, with and without min-p and k."""
+    rng = np.random.default_rng(V)
+    l = rows_of(V, R, V, dtype, sigma=2.0, n_peak=8, peak=(6.0, 12.0))
+    l[1] = np.round(l[1])
+    kw = dict(T=rng.uniform(0.8, 2.0, R), P=rng.choice([0.9, 0.99, 0.6, 0.9999], R), u=rng.random(R))
+    check_sample(l, run_sample(l, dtype, **kw), **kw)
+    kw.update(M=rng.choice([0.0, 1e-3, 1e-2], R), k=rng.choice([0, V // 2, 5000], R))
+    check_sample(l, run_sample(l, dtype, **kw), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kw", [{}, {"k": 7}, {"P": 0.8}, {"M": 0.03}, {"k": 40, "P": 0.95, "M": 0.01}])
 def test_evenly_spaced_uniforms_draw_the_distribution(dtype, kw):
     """N uniforms (i + 1/2) / N on N copies of a row: token v is drawn N p_v times, to within one
