@@ -443,7 +443,7 @@ def spec_verify_status_string(status: int) -> str:
 
 def _row_matrix(name, t, dtypes, shape, device):
     """A 2-d device tensor whose rows are contiguous (any row stride), checked."""
-    if t.dim() != 2 or tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
@@ -459,15 +459,15 @@ def _row_array(name, t, dtype, shape, device):
     """Address of a contiguous device tensor of this shape (None stays None), checked."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_of(logits):

@@ -149,6 +149,14 @@ int launch_sample(const void *logits, const SampleParams &P, int rows, cudaStrea
                             : launch(b512::sv_sample_kernel<T>, logits, P, rows, 512, P.top_p != nullptr, b512::Room::bytes, stream);
 }
 
+template <typename T>
+int launch_logprobs(const void *logits, const LogprobParams &P, int rows, cudaStream_t stream)
+{
+    return P.num_top > 0
+               ? launch(b256::sv_logprobs_kernel<T, true>, logits, P, rows, 256, false, b256::Room::bytes, stream)
+               : launch(b256::sv_logprobs_kernel<T, false>, logits, P, rows, 256, false, 0, stream);
+}
+
 bool misaligned(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 // What both entry points ask of the rows themselves.
@@ -229,8 +237,6 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
-    const size_t room = a->num_top > 0 ? b256::Room::bytes : 0;
-    return a->logits_dtype == SV_BF16
-               ? launch(b256::sv_logprobs_kernel<uint16_t>, a->logits, P, a->num_rows, 256, false, room, stream)
-               : launch(b256::sv_logprobs_kernel<float>, a->logits, P, a->num_rows, 256, false, room, stream);
+    return a->logits_dtype == SV_BF16 ? launch_logprobs<uint16_t>(a->logits, P, a->num_rows, stream)
+                                      : launch_logprobs<float>(a->logits, P, a->num_rows, stream);
 }
