@@ -894,6 +894,7 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, unsigned count, float
         if (ex.rank == 0) {
             constexpr int q = kBins / kThreads;  // bins of a thread
             unsigned c[q] = {};
+#pragma unroll 4
             for (int k = 0; k < cluster; ++k)
 #pragma unroll
                 for (int i = 0; i < q / 4; ++i) {
@@ -1072,15 +1073,29 @@ struct Listed {
     __device__ __forceinline__ unsigned key(u64 over, u64 need, unsigned lo, unsigned hi, u64 *held, Shared &sh) const
     {
         constexpr int drop = sizeof(T) == 2 ? 16 : 0;
+        // (in halves of 20 bits, which the warp's own addition takes, and one barrier a step)
+        int turn = 0;
         auto from = [&](unsigned bound) {
-            u64 m = 0, sum;
+            unsigned a = 0, b = 0;
 #pragma unroll
-            for (int q = 0; q < per; ++q) m += static_cast<unsigned>(entry[q] >> 32) >> drop >= bound ? w[q] : 0;
-            block_scan(m, sh.box, &sum);
-            return over + sum;
+            for (int q = 0; q < per; ++q)
+                if (static_cast<unsigned>(entry[q] >> 32) >> drop >= bound) {
+                    a += static_cast<unsigned>(w[q]) & 0xFFFFFu;
+                    b += static_cast<unsigned>(w[q] >> 20);
+                }
+            a = __reduce_add_sync(0xFFFFFFFFu, a);
+            b = __reduce_add_sync(0xFFFFFFFFu, b);
+            u64 *box = sh.seg[turn ^= 1];
+            const int lane = threadIdx.x & 31;
+            if (lane == 0) box[threadIdx.x >> 5] = (static_cast<u64>(b) << 32) | a;
+            __syncthreads();
+            const u64 x = lane < kWarps ? box[lane] : 0;
+            return over + __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(x)) +
+                   (static_cast<u64>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(x >> 32))) << 20);
         };
         lo >>= drop;
         hi >>= drop;
+        __syncthreads();  // (what was in these boxes has been read)
         *held = from(lo);
         if (*held < need) return 0;
         while (lo < hi) {
