@@ -460,8 +460,9 @@ int spec_verify_noalloc_last_error(uint32_t *err_word);
  * log-probabilities of tokens. They use no context and no scratch memory: the arguments are one
  * struct, everything a call needs is in it, and calls may overlap on any streams. All pointers
  * are device pointers of `device` (a CUDA ordinal; the stream belongs to it too), owned by the
- * caller and valid until the stream reaches the end of the call. No allocation, no host
- * synchronisation, capturable in a CUDA graph; the first call on a device looks the device up.
+ * caller and valid until the stream reaches the end of the call; outputs share no memory with
+ * inputs or with each other. No allocation, no host synchronisation, capturable in a CUDA graph;
+ * the first call on a device looks the device up.
  * Problems visible on the host return a status and launch nothing; 0 rows are SV_OK.
  *   logits        num_rows rows of vocab_size elements of logits_dtype (SV_F32 / SV_BF16), row r
  *                 at logits + r * logits_stride elements, logits_stride >= vocab_size; aligned to
@@ -495,7 +496,8 @@ int spec_verify_noalloc_last_error(uint32_t *err_word);
  *   probs          row r at probs + r * probs_stride, vocab_size binary32 each (out) or NULL:
  *                  the distribution drawn from, exp(d_v) 2^40 / Z of kept tokens, 0 elsewhere (a
  *                  greedy row: 1 at its token); with probs_stride = vocab_size the draft_probs
- *                  of spec_verify_run
+ *                  of spec_verify_run. SV_EINVAL where the memory from its first row's start to
+ *                  its last one's end meets that of the logits
  */
 typedef struct spec_verify_sample_args {
     const void *logits;

@@ -493,11 +493,15 @@ def _current_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _row_outputs(out, want, device):
-    """The output tensors (name, dtype, shape): those given, one for each, or new ones."""
+def _row_outputs(out, want, device, stream):
+    """The output tensors (name, dtype, shape): those given, one for each, or new ones, of the
+    memory that belongs to the stream that writes them."""
     import torch
 
     if out is None:
+        if stream is not None and _stream_handle(stream) != _current_stream(device.index):
+            with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device)):
+                return _row_outputs(None, want, device, None)
         return [torch.empty(shape, dtype=dtype, device=device) for _, dtype, shape in want]
     if len(out) != len(want):
         raise ValueError("out must hold " + ", ".join(name for name, _, _ in want))
@@ -528,7 +532,7 @@ def sample(logits, uniforms, temperature=None, *, top_k=None, top_p=None, min_p=
         want.append(("logprob", f32, (rows,)))
     if probs:
         want.append(("probs", f32, (rows, vocab)))
-    got = _row_outputs(out, want, dev)
+    got = _row_outputs(out, want, dev, stream)
     pp, pstride = _row_matrix("probs", got[-1], (f32,), (rows, vocab), dev) if probs else (None, 0)
     args = SampleArgs(ptr, stride, _row_array("temperature", temperature, f32, (rows,), dev),
                       _row_array("top_k", top_k, i32, (rows,), dev),
@@ -567,7 +571,7 @@ def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_
     want = [("logprob", f32, (rows,)), ("rank", i32, (rows,))] if tokens is not None else []
     if num_top:
         want += [("top_ids", i32, (rows, num_top)), ("top_logprobs", f32, (rows, num_top))]
-    got = _row_outputs(out, want, dev)
+    got = _row_outputs(out, want, dev, stream)
     at = [_row_array(name, t, d, shape, dev) for t, (name, d, shape) in zip(got, want)]
     if tokens is None:
         at = [None, None, *at]

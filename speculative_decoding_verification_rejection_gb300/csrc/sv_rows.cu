@@ -132,7 +132,9 @@ int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), P) == cudaSuccess ? SV_OK : SV_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), P) == cudaSuccess) return SV_OK;
+    cudaGetLastError();
+    return SV_ECUDA;
 }
 
 // Sampling by blocks of 512 threads, two on an SM, or, with more rows than four blocks on every SM,
@@ -159,6 +161,17 @@ int launch_logprobs(const void *logits, const LogprobParams &P, int rows, cudaSt
 
 bool misaligned(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
+// Whether the memory from the first row's start to the last one's end is shared by two matrices of
+// `rows` rows of V elements (of a and b bytes; strides in elements).
+bool spans_meet(const void *p, int64_t p_stride, unsigned a, const void *q, int64_t q_stride, unsigned b, int rows, int V)
+{
+    using wide = unsigned __int128;
+    const wide p0 = reinterpret_cast<uintptr_t>(p), q0 = reinterpret_cast<uintptr_t>(q);
+    const wide p1 = p0 + (static_cast<wide>(rows - 1) * static_cast<wide>(p_stride) + static_cast<wide>(V)) * a;
+    const wide q1 = q0 + (static_cast<wide>(rows - 1) * static_cast<wide>(q_stride) + static_cast<wide>(V)) * b;
+    return p0 < q1 && q0 < p1;
+}
+
 // What both entry points ask of the rows themselves.
 int check_rows(const void *logits, int64_t stride, int dtype, int num_rows, int vocab)
 {
@@ -183,6 +196,10 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
                           static_cast<const void *>(a->uniforms), static_cast<const void *>(a->tokens),
                           static_cast<const void *>(a->token_logprob), static_cast<const void *>(a->probs)})
         if (misaligned(p, 4)) return SV_EINVAL;
+    // (the distributions are set to 0 before the logits are read a second time)
+    if (a->probs && spans_meet(a->logits, a->logits_stride, a->logits_dtype == SV_BF16 ? 2 : 4, a->probs, a->probs_stride, 4,
+                               a->num_rows, a->vocab_size))
+        return SV_EINVAL;
     const int rd = rows_device(a->device);
     if (rd != SV_OK) return rd;
     const DeviceGuard guard(a->device);

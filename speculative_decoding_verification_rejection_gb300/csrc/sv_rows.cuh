@@ -50,7 +50,7 @@ struct LogprobParams {
 };
 
 // ---------------------------------------------------------------------------------------
-// thread-block clusters and asynchronous copies
+// thread-block clusters
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ unsigned smem_addr(const void *p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
 

@@ -86,7 +86,8 @@ __device__ __forceinline__ void block_scan(float &v, unsigned &c, u64 *box, floa
 // The 16-byte vectors that hold the row are split evenly over the cluster's CTAs and then over
 // their warps, both in contiguous runs, so that the warps in order hold the row in index order; a
 // lane has the vectors lane, lane + 32, ... of its warp's run. Every pass reads them from global
-// memory: the first one from HBM, those after it from the L2 cache, which holds all rows in work.
+// memory: the first one from HBM, those after it from the L2 cache as far as that holds the rows in
+// work (of 256 rows of 151936 bf16 logits, 78 MB, about a third of the reads hit it).
 // (Rows copied to shared memory once were as fast where few are in work and slower where many
 // are, since then the 227 KB of an SM bounds how many: 64 rows of 151936 bf16 logits 18 against 20 us,
 // 1024 rows with top-k 157 against 108.) What of the first and last vector lies outside the row is
@@ -1256,9 +1257,10 @@ __device__ void draw_run(const SampleParams &P, const Row<T> &R, long long r, fl
         }
         u64 run = below + block_scan(sum, sh.box, &all);
         if (target.passed(run + sum) && !target.passed(run)) {
+            const int last = R.base + to * n - 1;  // (it ends before this, unless the row changes meanwhile)
             int i = R.base + from * n;
             float l = R.at(i);
-            while (!target.passed(run += weight(kept_weight<kAll>(l, keep)))) l = R.at(++i);
+            while (!target.passed(run += weight(kept_weight<kAll>(l, keep))) && i < last) l = R.at(++i);
             P.tokens[r] = i;
             if (P.logprob) P.logprob[r] = log_prob(delta(l, keep.L, keep.inv), Z);
         }
@@ -1583,7 +1585,8 @@ static_assert(SV_MAX_TOP <= kList / kMaxCluster / 8 * 5, "every CTA can list its
 
 // Each warp sums 2^((l - m) / T log2 e) over its logits against its own largest, m, and counts the
 // logits above the token's; the leader joins the warps' sums. The best tokens come from the list
-// of those above the cut that num_top lane maxima reach, sorted by the leader.
+// of those from the cut on that num_top lane maxima reach, each put by the leader in the place that
+// the number of larger ones gives it.
 // Without best tokens no row is read again, and a fifth block on an SM, with half the vectors read
 // ahead, hides more than the second look at rows that no longer fit the L2 cache costs (640x40003
 // float32 21 against 27 us; with 5 best of 1536x151936 bf16 77 against 68).

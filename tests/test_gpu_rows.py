@@ -1,4 +1,8 @@
 """The row operators on the GPU against the plain implementation of tests/_rows.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -474,3 +478,54 @@ def test_wrong_arguments_on_the_device_are_refused():
         sv.logprobs(l, torch.zeros(4, dtype=torch.int64, device="cuda"))
     assert sv.sample(l[:0], u[:0])[0].shape == (0,)
     assert sv.logprobs(l[:0], torch.zeros(0, dtype=torch.int32, device="cuda"))[0].shape == (0,)
+
+
+def test_new_outputs_belong_to_the_stream_that_writes_them():
+    """Of a call on another stream than the current one the allocator knows the writer: their
+    memory is reused in that stream's order."""
+    import torch
+
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    gen = torch.Generator().manual_seed(5)
+    logits = torch.randn(3, 5000, generator=gen).cuda()
+    u = torch.rand(3, generator=gen).cuda()
+    here = sv.sample(logits, u, logprob=True, probs=True)
+    best = sv.logprobs(logits, here[0], num_top=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        there = sv.sample(logits, u, logprob=True, probs=True, stream=stream)
+        there += sv.logprobs(logits, there[0], num_top=3, stream=stream)
+        owner = {}
+        for seg in torch.cuda.memory_snapshot():
+            for t in there:
+                if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                    owner[t.data_ptr()] = seg["stream"]
+        assert [owner[t.data_ptr()] for t in there] == [side.cuda_stream] * len(there)
+        torch.cuda.synchronize()
+        for a, b in zip(here + best, there):
+            assert torch.equal(a, b)
+
+
+def test_a_process_may_capture_its_first_calls():
+    code = """
+import torch
+import speculative_decoding_verification_rejection_gb300 as sv
+torch.cuda.init()
+gen = torch.Generator().manual_seed(6)
+logits = torch.randn(5, 3001, generator=gen).cuda()
+u = torch.rand(5, generator=gen).cuda()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = sv.sample(logits, u, logprob=True)
+    got += sv.logprobs(logits, got[0], num_top=2)
+graph.replay()
+torch.cuda.synchronize()
+want = sv.sample(logits, u, logprob=True)
+want += sv.logprobs(logits, want[0], num_top=2)
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))

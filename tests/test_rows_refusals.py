@@ -39,6 +39,18 @@ def test_sample_refuses(change, status):
     assert sv.lib().spec_verify_sample(ctypes.byref(sample_args(**change)), None) == status
 
 
+# 4 rows of 1000 float32 logits 1000 apart: 16000 bytes; no device has this ordinal, so a call that
+# is not refused for its memory ends there
+@pytest.mark.parametrize("at,stride,status", [
+    (P, 1000, sv.SV_EINVAL), (P + 16000 - 4, 1000, sv.SV_EINVAL), (P + 16000, 1000, sv.SV_EDEVICE),
+    (P - 16000 + 4, 1000, sv.SV_EINVAL), (P - 16000, 1000, sv.SV_EDEVICE),
+    (P - 16000, 1001, sv.SV_EINVAL), (4, (1 << 62) - 1, sv.SV_EINVAL), (P + 16000, (1 << 62) - 1, sv.SV_EDEVICE),
+])
+def test_distributions_over_the_logits_are_refused(at, stride, status):
+    args = sample_args(probs=at, probs_stride=stride, device=1000)
+    assert sv.lib().spec_verify_sample(ctypes.byref(args), None) == status
+
+
 @pytest.mark.parametrize("change,status", ROWS + [
     (dict(num_top=-1), sv.SV_EINVAL), (dict(num_top=3), sv.SV_EINVAL),
     (dict(num_top=3, top_ids=P), sv.SV_EINVAL),
