@@ -15,6 +15,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "spec_verify.h"
 #include "sv_rows.cuh"
@@ -113,6 +114,17 @@ Shape shape_of(int rows, int V, int elem_bytes, int threads, bool wide)
     return s;
 }
 
+// Sampling by blocks of 512 threads, two on an SM, or, with more rows than four blocks on every SM,
+// of 256: four rows in work on an SM hide one another's waits better than two (1024 rows of 151936
+// bf16 logits with top-k and top-p 80 against 93 us, of 32000 35 against 45), while up to that a row's
+// own time counts, which is shorter with more threads (256 rows 25 against 30 us; where a top-p set is
+// wide, 512 rows of 129280 float32 logits, 170 against 254).
+// The smaller number of rows, where the device does not hold them at once, starts with those that may
+// take long if it may be of both kinds, which top-k and top-p given together say: the look at all rows'
+// limits costs a CTA 1.5 us (256 mixed rows of 151936 bf16 logits 74 against 89 us, all with top-k and
+// top-p 38.5 against 37).
+constexpr int kManyRows = 4 * 152;
+
 template <typename T, typename Params>
 int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, int threads, bool wide, size_t room,
            cudaStream_t stream)
@@ -120,6 +132,8 @@ int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int 
     const Shape s = shape_of(rows, P.V, sizeof(T), threads, wide);
     P.cluster = s.cluster;
     P.split = s.split;
+    if constexpr (std::is_same_v<Params, SampleParams>)
+        P.ordered = P.top_p && P.top_k && rows <= 2 * threads && rows * s.cluster > 152 * (1024 / threads) ? rows : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * static_cast<unsigned>(s.cluster));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -136,13 +150,6 @@ int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int 
     cudaGetLastError();
     return SV_ECUDA;
 }
-
-// Sampling by blocks of 512 threads, two on an SM, or, with more rows than four blocks on every SM,
-// of 256: four rows in work on an SM hide one another's waits better than two (1024 rows of 151936
-// bf16 logits with top-k and top-p 80 against 93 us, of 32000 35 against 45), while up to that a row's
-// own time counts, which is shorter with more threads (256 rows 25 against 30 us; where a top-p set is
-// wide, 512 rows of 129280 float32 logits, 196 against 254).
-constexpr int kManyRows = 4 * 152;
 
 template <typename T>
 int launch_sample(const void *logits, const SampleParams &P, int rows, cudaStream_t stream)

@@ -36,7 +36,7 @@ struct SampleParams {
     const int32_t *top_k;
     int32_t *tokens;
     float *logprob, *probs;
-    int V, cluster;
+    int V, cluster, ordered;  // ordered: the rows, where those that may take long come first, else 0
     Split split;
 };
 struct LogprobParams {

@@ -1374,6 +1374,47 @@ __device__ __forceinline__ unsigned call_kth(const Row<T> &R, const Kept &keep, 
     return key;
 }
 
+// The row of the cluster at place `at`, where those whose top-p set or k may be beyond the list come
+// first (each kind in order): they take three times as long as the others, and where the device does not
+// hold all rows at once the last to start decides how long the call takes. For up to 2 kThreads rows
+// (more than that go to the smaller blocks, without an order).
+__device__ __forceinline__ int long_first(const SampleParams &P, int at, Shared &sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = P.ordered;
+    bool is_long[2];
+    unsigned same[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int row = tid + q * kThreads;
+        is_long[q] = false;
+        if (row < rows) {
+            const int k = P.top_k ? __ldg(P.top_k + row) : 0;
+            const bool limited = k >= 1 && k < P.V;
+            is_long[q] = limited ? k > kList / 2 : P.top_p && __ldg(P.top_p + row) < 1.0f;
+            is_long[q] = is_long[q] && (!P.temperature || __ldg(P.temperature + row) > 0.0f);
+        }
+        same[q] = __ballot_sync(0xFFFFFFFFu, is_long[q]);
+    }
+    if (lane == 0) sh.box[warp] = (static_cast<u64>(__popc(same[1])) << 32) | static_cast<u64>(__popc(same[0]));
+    __syncthreads();
+    u64 before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh.box[w];
+        all += sh.box[w];
+    }
+    const int first = static_cast<int>(all & 0xFFFFFFFFu), total = first + static_cast<int>(all >> 32);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int row = tid + q * kThreads;
+        const int n = (q ? first + static_cast<int>(before >> 32) : static_cast<int>(before & 0xFFFFFFFFu)) +
+                      __popc(same[q] & ((1u << lane) - 1));
+        if (row < rows && (is_long[q] ? n : total + row - n) == at) sh.first = row;
+    }
+    __syncthreads();
+    return sh.first;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *logits, SampleParams P)
 {
@@ -1381,9 +1422,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     __shared__ Shared sh;
     const int tid = threadIdx.x, cluster = P.cluster;
     const unsigned rank = cluster_rank();
-    const long long r = blockIdx.x / cluster;
+    const int place = static_cast<int>(blockIdx.x) / cluster;
     const Room room(store);
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
+    const long long r = P.ordered ? long_first(P, place, sh) : place;
     Row<T> R = start_row(logits + r * P.stride, P.V, P.split, rank, sh);
     const int part = kList / cluster;
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;

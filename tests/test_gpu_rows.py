@@ -198,6 +198,23 @@ def test_sample_more_rows_than_the_device_holds(V, dtype):
     same_tokens_without_probs(l, dtype, got, **kw)
 
 
+@pytest.mark.parametrize("R", [305, 512, 513, 608])
+@pytest.mark.parametrize("kinds", ["both", "long", "short"])
+def test_rows_of_both_kinds_in_any_number(R, kinds):
+    """Where the device does not hold all rows at once those with large top-p sets or k may start
+    first; each row is drawn once, by its own limits."""
+    V = 1300
+    rng = np.random.default_rng(R)
+    l = rows_of(R, R, V, "f32", sigma=1.0, n_peak=4)
+    k = {"both": [0, 0, 1, 30, 511, 512, 513, 900, V], "long": [0, 513, 1200], "short": [1, 20, 512]}[kinds]
+    P = {"both": [1.0, 0.9, 0.3], "long": [0.99, 0.9], "short": [1.0, 0.8]}[kinds]
+    kw = dict(k=rng.choice(k, R), P=rng.choice(P, R), u=rng.random(R))
+    for more in ({}, {"T": rng.choice([0.0, 1.0, 0.7] if kinds == "both" else [0.9, 1.1], R)}):
+        got = run_sample(l, "f32", **kw, **more)
+        check_sample(l, got, **kw, **more)
+    same_tokens_without_probs(l, "f32", got, **kw, **more)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("R", [2, 40, 200])
 def test_favoured_tokens_side_by_side(R, dtype):
