@@ -94,7 +94,7 @@ int rows_device(int dev)
 // for a row as the device holds at once (1024 threads on each of its 152 SMs) over the rows, in powers of
 // two, and at least a vector for each of their threads. Where one CTA is a row's share and top-p may
 // keep more than the list (`wide`), yet two: one wide row then decides how long the call takes
-// (256 rows of 151936 bf16 logits, one in seven wide, 96 against 143 us; none wide 41 against 24).
+// (256 rows of 151936 bf16 logits, one in seven wide, 74 against 127 us; none wide 38 against 24).
 struct Shape {
     int cluster;
     Split split;
