@@ -198,6 +198,19 @@ def test_sample_more_rows_than_the_device_holds(V, dtype):
     same_tokens_without_probs(l, dtype, got, **kw)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [6, 24, 70, 160, 620])
+def test_k_from_small_to_beyond_the_list(R, dtype):
+    """Every k between what a CTA lists for sure and what no list holds, by rows split over many CTAs
+    to rows of one small block."""
+    V = 40003 if R < 100 else 6007
+    rng = np.random.default_rng(R)
+    l = rows_of(R, R, V, dtype, sigma=2.0, n_peak=0)
+    for low, high in ((60, 200), (200, 520), (500, 1100)):
+        kw = dict(k=rng.integers(low, high, R), P=rng.choice([1.0, 0.9], R), u=rng.random(R))
+        check_sample(l, run_sample(l, dtype, **kw), **kw)
+
+
 @pytest.mark.parametrize("R", [305, 512, 513, 608])
 @pytest.mark.parametrize("kinds", ["both", "long", "short"])
 def test_rows_of_both_kinds_in_any_number(R, kinds):
