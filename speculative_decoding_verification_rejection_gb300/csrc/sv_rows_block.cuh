@@ -870,7 +870,13 @@ __device__ void bracket(const Row<T> &R, const Kept &keep, unsigned count, float
     const int tid = threadIdx.x, cluster = ex.cluster;
     auto *bins = reinterpret_cast<unsigned *>(room.peaks);
     // the bins' first edge and width, in -d
-    float from = known.ceiling < kInf ? (keep.L - known.ceiling) * keep.inv * 1.000001f : 0.0f;
+    float from = 0.0f;
+    if (known.ceiling < kInf) {
+        // (between the last value that is known and the next: of bf16 logits half-way, whose ceiling is a
+        // key with zeros below; a token there in neither part, or in both, would be missed by the guess)
+        const unsigned key = key_of(known.ceiling);
+        from = (keep.L - (sizeof(T) == 4 ? known.ceiling : of_key(key & 0x80000000u ? key - 0x8000u : key + 0x7FFFu))) * keep.inv;
+    }
     float width = fmaxf(fminf(known.lowest, kSpan) - from, 1e-3f) / kBins;
     float before = static_cast<float>(known.heavy >> 20) * 0x1p-20f, want = 0.0f;  // (the leader's)
     for (int level = 0; level < 2; ++level) {
@@ -1514,7 +1520,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
         }
     }
     // the row's largest logit
-    const float own_cut = mass ? cut_for<T>(peak, largest, kTopP, kTopP / 4 * 5, sh) : 0.0f;
+    // (a list of all CTAs that is still compared each with each: a row of 151936 bf16 logits whose set is
+    // small 13 us, where eight CTAs list 64 each 27)
+    const int few = kTopP / max(cluster / 2, 1);
+    const float own_cut = mass ? cut_for<T>(peak, largest, few, few + (few >> 2), sh) : 0.0f;
     if (tid < cluster) {
         put(remote(&sh.peak[rank], tid), __float_as_uint(largest));
         put(remote(&sh.cut[rank], tid), __float_as_uint(own_cut));

@@ -199,6 +199,29 @@ def test_sample_more_rows_than_the_device_holds(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [4, 30, 160, 620])
+def test_heavy_tailed_rows(R, dtype):
+    """Probabilities that fall as a power of the rank: top-p sets of all sizes from one token to most
+    of the row, with many equal bf16 logits at their borders; positive, mixed and negative logits."""
+    V = 30011 if R < 100 else 5003
+    rng = np.random.default_rng(V + R)
+    l = np.empty((R, V))
+    for r in range(R):
+        l[r] = rng.permutation(-rng.uniform(0.9, 2.0) * np.log(np.arange(1, V + 1))) + rng.choice([0.0, 4.0, 30.0])
+    l = (l + 0.3 * rng.standard_normal((R, V))).astype(np.float32)
+    if dtype == "bf16":                                      # what the GPU gets
+        from _util import bf16_bits_to_f32, to_bf16_bits
+
+        l = bf16_bits_to_f32(to_bf16_bits(l)).reshape(R, V)
+    kw = dict(P=rng.choice([0.5, 0.9, 0.99], R), u=rng.random(R))
+    check_sample(l, run_sample(l, dtype, **kw), **kw)
+    kw["T"] = rng.choice([0.6, 1.0, 1.5], R)
+    got = run_sample(l, dtype, **kw)
+    check_sample(l, got, **kw)
+    same_tokens_without_probs(l, dtype, got, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("R", [6, 24, 70, 160, 620])
 def test_k_from_small_to_beyond_the_list(R, dtype):
     """Every k between what a CTA lists for sure and what no list holds, by rows split over many CTAs
