@@ -460,9 +460,9 @@ int spec_verify_noalloc_last_error(uint32_t *err_word);
  * log-probabilities of tokens. They use no context and no scratch memory: the arguments are one
  * struct, everything a call needs is in it, and calls may overlap on any streams. All pointers
  * are device pointers of `device` (a CUDA ordinal; the stream belongs to it too), owned by the
- * caller and valid until the stream reaches the end of the call; outputs share no memory with
- * inputs or with each other. No allocation, no host synchronisation, capturable in a CUDA graph;
- * the first call on a device looks the device up.
+ * caller and valid until the stream reaches the end of the call; inputs stay as they are until
+ * then, and outputs share no memory with inputs or with each other. No allocation, no host
+ * synchronisation, capturable in a CUDA graph; the first call on a device looks the device up.
  * Problems visible on the host return a status and launch nothing; 0 rows are SV_OK.
  *   logits        num_rows rows of vocab_size elements of logits_dtype (SV_F32 / SV_BF16), row r
  *                 at logits + r * logits_stride elements, logits_stride >= vocab_size; aligned to

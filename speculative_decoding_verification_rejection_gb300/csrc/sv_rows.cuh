@@ -18,7 +18,7 @@ constexpr int kList = 1024;       // entries of the leader's candidate list
 constexpr int kHits = 2048;       // groups a CTA looks through for candidates
 constexpr int kPairs = 256;       // most entries that are compared each with each, and the threads that do it
 constexpr int kFewPairs = 128;    // most that are so before the k largest are picked out
-constexpr int kTopP = 64;         // lane maxima of a CTA that the cut for top-p alone is to reach
+constexpr int kTopP = 64;         // lane maxima that the cut for top-p alone is to reach, of a CTA of two at most
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
 constexpr int kBeside = 64;       // tokens on each side of a guess
 constexpr int kBins = 4096;       // bins of the value histogram

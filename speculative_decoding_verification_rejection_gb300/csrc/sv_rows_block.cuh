@@ -1401,6 +1401,7 @@ __device__ __forceinline__ int long_first(const SampleParams &P, int at, Shared 
         }
         same[q] = __ballot_sync(0xFFFFFFFFu, is_long[q]);
     }
+    if (tid == 0) sh.first = at;  // (a row in any case, also where the limits change meanwhile)
     if (lane == 0) sh.box[warp] = (static_cast<u64>(__popc(same[1])) << 32) | static_cast<u64>(__popc(same[0]));
     __syncthreads();
     u64 before = 0, all = 0;
