@@ -22,6 +22,7 @@ constexpr int kTopP = 64;         // lane maxima that the cut for top-p alone is
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
 constexpr int kBeside = 64;       // tokens on each side of a guess
 constexpr int kBins = 4096;       // bins of the value histogram
+constexpr float kRise = 4.0f;     // doublings that a log-probability's logits pass their reference by before it moves
 constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;

@@ -241,8 +241,8 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     return R;
 }
 
-// Sum of 2^((l - ref) scale) over v[0, m), in binary32, ref the largest logit or more; a NaN and -inf
-// add nothing, and where ref is +inf each logit of +inf adds 1.
+// Sum of 2^((l - ref) scale) over v[0, m), in binary32, no logit more than kRise / scale above ref; a NaN
+// and -inf add nothing, and where ref is +inf each logit of +inf adds 1.
 template <typename T, int k>
 __device__ __forceinline__ float fast_sum(const uint4 (&v)[k], int m, float ref, float scale)
 {
@@ -1639,10 +1639,10 @@ __device__ __forceinline__ u64 pack(float a, float b)
 
 static_assert(SV_MAX_TOP <= kList / kMaxCluster / 8 * 5, "every CTA can list its own best tokens");
 
-// Each warp sums 2^((l - m) / T log2 e) over its logits against its own largest, m, and counts the
-// logits above the token's; the leader joins the warps' sums. The best tokens come from the list
-// of those from the cut on that num_top lane maxima reach, each put by the leader in the place that
-// the number of larger ones gives it.
+// Each lane sums 2^((l - m) / T log2 e) over its logits against a reference m and counts the logits above
+// the token's; a warp joins its lanes' sums against its largest logit, the leader the warps'. The best
+// tokens come from the list of those from the cut on that num_top lane maxima reach, each put by the
+// leader in the place that the number of larger ones gives it.
 // Without best tokens no row is read again, and a fifth block on an SM, with half the vectors read
 // ahead, hides more than the second look at rows that no longer fit the L2 cache costs (640x40003
 // float32 21 against 27 us; with 5 best of 1536x151936 bf16 77 against 68).
@@ -1675,30 +1675,42 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
     const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
     const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
     const float scale = fminf(inv * kLog2e, FLT_MAX);
-    // some vectors at a time, against the largest logit so far
-    float peak = -kInf, s = 0.0f;
+    // Some vectors at a time, against a reference that moves to the largest logit only once that is kRise
+    // above it: each move rounds what was added before, and where logits rise a little all along the row
+    // those errors would add up (moved each time, -13.1639 was off by 6.8e-6 after 128 moves). Batches
+    // are added with what the addition loses (Knuth's two-sum): a batch far smaller than the sum
+    // would otherwise round it the same way each time (-0.0257 off by 3.1e-6). (The two cost 1.7 of 22 us
+    // where rows are short and float32, 640x40003, and 1 of 66 with 5 best of 1536x151936 bf16.)
+    float peak = -kInf, ref = -kInf, s = 0.0f, lost = 0.0f;
     Above<T> above(lt);
     R.template each<ahead>([&](uint4 (&v)[ahead], int m, int c) {
         Largest<T> largest;
 #pragma unroll
         for (int i = 0; i < ahead; ++i) largest.add(v[i]);
-        const float own = largest.get(), ref = fmaxf(peak, own);
+        const float own = largest.get();
         if (kTop) {
             float *at = room.peaks + (c % kGroups) * kThreads + tid;
             *at = c < kGroups ? own : fmaxf(*at, own);
         }
-        if (ref > peak) {
-            if (peak > -kInf) s *= sv::ex2_approx((peak - ref) * scale);
-            peak = ref;
+        peak = fmaxf(peak, own);
+        if ((own - ref) * scale > kRise) {
+            const float f = sv::ex2_approx((ref - own) * scale);  // (of the first reference, -inf, 0)
+            s *= f;
+            lost *= f;
+            ref = own;
         }
+        const float batch = fast_sum<T>(v, m, ref, scale);
 #pragma unroll
         for (int i = 0; i < ahead; ++i)
             if (i < m) above.add(v[i]);
         above.flush();
-        s += fast_sum<T>(v, m, ref, scale);
+        const float sum = __fadd_rn(s, batch), added = __fsub_rn(sum, s);
+        lost += __fadd_rn(__fsub_rn(s, __fsub_rn(sum, added)), __fsub_rn(batch, added));
+        s = sum;
     });
+    s += lost;
     const float top_of_warp = warp_max(peak);
-    if (peak < top_of_warp && s > 0.0f) s *= sv::ex2_approx((peak - top_of_warp) * scale);
+    if (ref < top_of_warp && s > 0.0f) s *= sv::ex2_approx((ref - top_of_warp) * scale);
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
     const unsigned larger = __reduce_add_sync(0xFFFFFFFFu, above.get());
