@@ -25,7 +25,8 @@ _SOURCES = [*_UNITS, *(os.path.join(_PKG, "csrc", f) for f in ("sv_device.cuh", 
                                                                 "sv_rows_block.cuh"))]
 # SPEC_VERIFY_DEBUG_BOUNDS=1 in the environment selects the checked build (-DSV_DEBUG_BOUNDS): every
 # global load and store of the kernels is checked against the call's arrays, and an access
-# outside them is skipped and reported as SV_ERR_BOUNDS in the error word. For tests only.
+# outside them is skipped and reported as SV_ERR_BOUNDS in the error word (by the row operators in the
+# one that spec_verify_rows_outside of that build reads). For tests only.
 DEBUG_BOUNDS = os.environ.get("SPEC_VERIFY_DEBUG_BOUNDS", "0") not in ("", "0")
 RELEASE_LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libspecverify_debug.so")

@@ -13,7 +13,9 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 
@@ -125,6 +127,54 @@ Shape shape_of(int rows, int V, int elem_bytes, int threads, bool wide)
 // top-p 38.5 against 37).
 constexpr int kManyRows = 4 * 152;
 
+#ifdef SV_DEBUG_BOUNDS
+// The arrays of one call, registered in g_spans (in stream order) before its launch. The environment
+// variable SV_DEBUG_SHRINK leaves that many bytes of the end of every row of the first (the logits) out, so
+// that tests can check that the check fires on memory that is there.
+struct SpanList {
+    Spans l{};
+    void add(const void *p, bool out, size_t bytes, size_t rows = 1, size_t stride = 1)
+    {
+        if (p && bytes && rows && l.n < kSpans) l.s[l.n++] = Span{reinterpret_cast<u64>(p), stride, bytes, rows, out};
+    }
+    int push(cudaStream_t stream)
+    {
+        if (const char *e = getenv("SV_DEBUG_SHRINK")) l.s[0].bytes -= std::min<u64>(strtoull(e, nullptr, 10), l.s[0].bytes);
+        return cudaMemcpyToSymbolAsync(g_spans, &l, sizeof(l), 0, cudaMemcpyHostToDevice, stream) == cudaSuccess ? SV_OK : SV_ECUDA;
+    }
+};
+
+int push_spans(const spec_verify_sample_args &a, cudaStream_t stream)
+{
+    const size_t R = static_cast<size_t>(a.num_rows), V = static_cast<size_t>(a.vocab_size), e = a.logits_dtype == SV_BF16 ? 2 : 4;
+    SpanList s;
+    s.add(a.logits, false, V * e, R, static_cast<size_t>(a.logits_stride) * e);
+    for (const void *p : {static_cast<const void *>(a.temperature), static_cast<const void *>(a.top_k), static_cast<const void *>(a.top_p),
+                          static_cast<const void *>(a.min_p), static_cast<const void *>(a.uniforms)})
+        s.add(p, false, R * 4);
+    s.add(a.tokens, true, R * 4);
+    s.add(a.token_logprob, true, R * 4);
+    s.add(a.probs, true, V * 4, R, static_cast<size_t>(a.probs_stride) * 4);
+    return s.push(stream);
+}
+
+int push_spans(const spec_verify_logprobs_args &a, cudaStream_t stream)
+{
+    const size_t R = static_cast<size_t>(a.num_rows), V = static_cast<size_t>(a.vocab_size), e = a.logits_dtype == SV_BF16 ? 2 : 4;
+    const size_t n = static_cast<size_t>(a.num_reqs), top = static_cast<size_t>(a.num_top);
+    SpanList s;
+    s.add(a.logits, false, V * e, R, static_cast<size_t>(a.logits_stride) * e);
+    s.add(a.temperature, false, R * 4);
+    s.add(a.tokens, false, a.cu_num_draft ? n * static_cast<size_t>(a.token_stride) * 4 : R * 4);
+    s.add(a.cu_num_draft, false, (n + 1) * 4);
+    s.add(a.token_logprob, true, R * 4);
+    s.add(a.token_rank, true, R * 4);
+    s.add(a.top_ids, true, R * top * 4);
+    s.add(a.top_logprobs, true, R * top * 4);
+    return s.push(stream);
+}
+#endif
+
 template <typename T, typename Params>
 int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int rows, int threads, bool wide, size_t room,
            cudaStream_t stream)
@@ -224,6 +274,9 @@ extern "C" int spec_verify_sample(const spec_verify_sample_args *a, void *cuda_s
     P.probs = a->probs;
     P.V = a->vocab_size;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
+#ifdef SV_DEBUG_BOUNDS
+    if (push_spans(*a, stream) != SV_OK) return SV_ECUDA;
+#endif
     return a->logits_dtype == SV_BF16 ? launch_sample<uint16_t>(a->logits, P, a->num_rows, stream)
                                       : launch_sample<float>(a->logits, P, a->num_rows, stream);
 }
@@ -261,6 +314,23 @@ extern "C" int spec_verify_logprobs(const spec_verify_logprobs_args *a, void *cu
     P.top_ids = a->top_ids;
     P.top_logprob = a->top_logprobs;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
+#ifdef SV_DEBUG_BOUNDS
+    if (push_spans(*a, stream) != SV_OK) return SV_ECUDA;
+#endif
     return a->logits_dtype == SV_BF16 ? launch_logprobs<uint16_t>(a->logits, P, a->num_rows, stream)
                                       : launch_logprobs<float>(a->logits, P, a->num_rows, stream);
 }
+
+#ifdef SV_DEBUG_BOUNDS
+// Of the checked build only: SV_ERR_BOUNDS in *word if a kernel of a row operator that has ended tried an
+// access outside its call's arrays (the current device's; read and cleared).
+extern "C" int spec_verify_rows_outside(uint32_t *word)
+{
+    const unsigned zero = 0;
+    if (!word) return SV_EINVAL;
+    return cudaMemcpyFromSymbol(word, g_outside, sizeof(*word)) == cudaSuccess &&
+                   cudaMemcpyToSymbol(g_outside, &zero, sizeof(zero)) == cudaSuccess
+               ? SV_OK
+               : SV_ECUDA;
+}
+#endif

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "spec_verify.h"
 #include "sv_device.cuh"
 
 namespace sv_rows {
@@ -49,6 +50,69 @@ struct LogprobParams {
     int32_t *rank, *top_ids;
     Split split;
 };
+
+// ---------------------------------------------------------------------------------------
+// global memory
+// ---------------------------------------------------------------------------------------
+// Every global load and store of the row operators goes through these. Built with -DSV_DEBUG_BOUNDS
+// each is checked against the rows of the call's arrays (loads against its inputs, stores against its
+// outputs; what lies between the rows of a strided array is outside), which the host registers before
+// the launch: one that is outside is skipped (a load gives 0) and leaves a mark that
+// spec_verify_rows_outside() reads. In a normal build they are plain accesses.
+#ifdef SV_DEBUG_BOUNDS
+struct Span {
+    u64 at, stride, bytes, rows;  // rows of `bytes` bytes, `stride` apart
+    bool out;
+};
+constexpr int kSpans = 12;
+struct Spans {
+    Span s[kSpans];
+    int n;
+};
+__device__ Spans g_spans;
+__device__ unsigned g_outside;
+
+__device__ __noinline__ bool inside(const void *p, unsigned bytes, bool out)
+{
+    const u64 a = reinterpret_cast<u64>(p);
+    for (int k = 0; k < g_spans.n; ++k) {
+        const Span &s = g_spans.s[k];
+        if (a < s.at || s.out != out) continue;
+        const u64 off = a - s.at, row = s.rows > 1 ? off / s.stride : 0;
+        if (row < s.rows && off - row * s.stride + bytes <= s.bytes) return true;
+    }
+    atomicOr(&g_outside, SV_ERR_BOUNDS);
+    return false;
+}
+#define SV_INSIDE(p, bytes, out) inside((p), (bytes), (out))
+#else
+#define SV_INSIDE(p, bytes, out) true
+#endif
+
+template <typename T>
+__device__ __forceinline__ T ld(const T *p)
+{
+    if (!SV_INSIDE(p, sizeof(T), false)) return T{};
+    return __ldg(p);
+}
+// A vector of a row of logits, read once a pass: not kept in L1.
+__device__ __forceinline__ uint4 ld_row(const uint4 *p)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (SV_INSIDE(p, 16, false))
+        asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+template <typename T, typename U>
+__device__ __forceinline__ void st(T *p, const U &v)
+{
+    if (SV_INSIDE(p, sizeof(T), true)) *p = v;
+}
+// Four floats that leave the L2 cache first.
+__device__ __forceinline__ void st_leaving(float4 *p, const float4 &v)
+{
+    if (SV_INSIDE(p, sizeof(float4), true)) __stcs(p, v);
+}
 
 // ---------------------------------------------------------------------------------------
 // thread-block clusters

@@ -141,18 +141,12 @@ struct Row {
     bool inf;             // read through only_inf()
     bool plain;           // this warp's run has neither of these vectors, and not inf
 
-    static __device__ __forceinline__ uint4 read(const uint4 *p)
-    {
-        uint4 v;
-        asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-        return v;
-    }
     __device__ __forceinline__ uint4 get(int j) const
     {
         uint4 v;
         if (j == front) v = edge[0];
         else if (j == back) v = edge[1];
-        else v = read(vec + j);
+        else v = ld_row(vec + j);
         return inf ? only_inf<T>(v) : v;
     }
     // Vectors j, j + 32, ... of this lane, k of them, those past the run's end all -inf. Returns how
@@ -164,7 +158,7 @@ struct Row {
         for (int i = 0; i < k; ++i) {  // the reads first, then the rare vectors that are something else
             const int a = j + 32 * i;
             v[i] = make_uint4(Low<T>::word, Low<T>::word, Low<T>::word, Low<T>::word);
-            if (a < hi && a != front && a != back) v[i] = read(vec + a);
+            if (a < hi && a != front && a != back) v[i] = ld_row(vec + a);
         }
 #pragma unroll
         for (int i = 0; i < k; ++i) {
@@ -189,7 +183,7 @@ struct Row {
             for (; j - lane + 32 * k <= hi; j += 32 * k, ++c) {
                 uint4 v[k];
 #pragma unroll
-                for (int i = 0; i < k; ++i) v[i] = read(vec + j + 32 * i);
+                for (int i = 0; i < k; ++i) v[i] = ld_row(vec + j + 32 * i);
                 f(v, k, c);
             }
         for (; j - lane < hi; j += 32 * k, ++c) {
@@ -200,7 +194,7 @@ struct Row {
     }
     __device__ __forceinline__ float at(int i) const  // element i of the row; -inf outside
     {
-        const float l = i >= 0 && i < V ? as_float(__ldg(row + i)) : -kInf;
+        const float l = i >= 0 && i < V ? as_float(ld(row + i)) : -kInf;
         return !inf ? l : l == kInf ? 0.0f : -kInf;
     }
     __device__ __forceinline__ int first() const { return max(base, 0); }
@@ -235,7 +229,7 @@ __device__ __forceinline__ Row<T> start_row(const T *row, int V, const Split &sp
     if (off == 0 && (off + V) % n == 0) return R;
     if (threadIdx.x < 2 * n) {
         const int k = threadIdx.x / n, e = threadIdx.x % n, i = (k == 0 ? 0 : vectors - 1) * n - off + e;
-        reinterpret_cast<T *>(&sh.edge[k])[e] = i >= 0 && i < V ? __ldg(row + i) : Low<T>::value();
+        reinterpret_cast<T *>(&sh.edge[k])[e] = i >= 0 && i < V ? ld(row + i) : Low<T>::value();
     }
     __syncthreads();
     return R;
@@ -481,13 +475,13 @@ struct Drawn {
     const Kept &keep;
     __device__ __forceinline__ void token(u64 entry, u64 Z) const
     {
-        P.tokens[r] = static_cast<int>(~static_cast<unsigned>(entry));
-        if (P.logprob) P.logprob[r] = log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z);
+        st(P.tokens + r, static_cast<int>(~static_cast<unsigned>(entry)));
+        if (P.logprob) st(P.logprob + r, log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z));
     }
     __device__ __forceinline__ void prob(u64 entry, float scale) const
     {
-        P.probs[r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry))] =
-            sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)) * scale;
+        st(P.probs + r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry)),
+           sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)) * scale);
     }
 };
 
@@ -1190,7 +1184,7 @@ __device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const
         for (int i = R.first() + static_cast<int>(threadIdx.x); i < R.last(); i += kThreads) {
             const float l = R.at(i), d = delta(l, keep.L, keep.inv);
             const bool in = l > -kInf && (kAll || (l >= keep.tau && d >= keep.low));
-            if (kAll || in) probs[i] = in ? sv::exp_f32(d) * scale : 0.0f;
+            if (kAll || in) st(probs + i, in ? sv::exp_f32(d) * scale : 0.0f);
         }
         return;
     }
@@ -1218,11 +1212,11 @@ __device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const
             if (first >= 0 && first + n <= R.V) {
 #pragma unroll
                 for (int e = 0; e < n; e += 4)
-                    *reinterpret_cast<float4 *>(probs + first + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                    st(reinterpret_cast<float4 *>(probs + first + e), make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
             } else {
 #pragma unroll
                 for (int e = 0; e < n; ++e)
-                    if (first + e >= 0 && first + e < R.V) probs[first + e] = f[e];
+                    if (first + e >= 0 && first + e < R.V) st(probs + first + e, f[e]);
             }
         }
     });
@@ -1236,9 +1230,9 @@ __device__ __forceinline__ void write_zeros(const Row<T> &R, float *probs)
     const int tid = threadIdx.x, first = R.first(), last = R.last();
     const int head = min(first + static_cast<int>((16u - (reinterpret_cast<uintptr_t>(probs + first) & 15u)) / 4u % 4u), last);
     const int body = head + max(last - head, 0) / 4 * 4;
-    if (first + tid < head) probs[first + tid] = 0.0f;
-    for (int i = head + 4 * tid; i < body; i += 4 * kThreads) __stcs(reinterpret_cast<float4 *>(probs + i), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-    if (body + tid < last) probs[body + tid] = 0.0f;
+    if (first + tid < head) st(probs + first + tid, 0.0f);
+    for (int i = head + 4 * tid; i < body; i += 4 * kThreads) st_leaving(reinterpret_cast<float4 *>(probs + i), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    if (body + tid < last) st(probs + body + tid, 0.0f);
 }
 
 // The draw where the run on which the uniform number falls is known: the CTA that holds it finds the
@@ -1267,8 +1261,8 @@ __device__ void draw_run(const SampleParams &P, const Row<T> &R, long long r, fl
             int i = R.base + from * n;
             float l = R.at(i);
             while (!target.passed(run += weight(kept_weight<kAll>(l, keep))) && i < last) l = R.at(++i);
-            P.tokens[r] = i;
-            if (P.logprob) P.logprob[r] = log_prob(delta(l, keep.L, keep.inv), Z);
+            st(P.tokens + r, i);
+            if (P.logprob) st(P.logprob + r, log_prob(delta(l, keep.L, keep.inv), Z));
         }
     }
     if (P.probs) write_probs<kAll>(R, P.probs + r * P.probs_stride, keep, Z);
@@ -1394,10 +1388,10 @@ __device__ __forceinline__ int long_first(const SampleParams &P, int at, Shared 
         const int row = tid + q * kThreads;
         is_long[q] = false;
         if (row < rows) {
-            const int k = P.top_k ? __ldg(P.top_k + row) : 0;
+            const int k = P.top_k ? ld(P.top_k + row) : 0;
             const bool limited = k >= 1 && k < P.V;
-            is_long[q] = limited ? k > kList / 2 : P.top_p && __ldg(P.top_p + row) < 1.0f;
-            is_long[q] = is_long[q] && (!P.temperature || __ldg(P.temperature + row) > 0.0f);
+            is_long[q] = limited ? k > kList / 2 : P.top_p && ld(P.top_p + row) < 1.0f;
+            is_long[q] = is_long[q] && (!P.temperature || ld(P.temperature + row) > 0.0f);
         }
         same[q] = __ballot_sync(0xFFFFFFFFu, is_long[q]);
     }
@@ -1435,11 +1429,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     const long long r = P.ordered ? long_first(P, place, sh) : place;
     Row<T> R = start_row(logits + r * P.stride, P.V, P.split, rank, sh);
     const int part = kList / cluster;
-    const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
-    const int k0 = P.top_k ? __ldg(P.top_k + r) : 0;
-    const float p = P.top_p ? __ldg(P.top_p + r) : 1.0f;
-    const float m = P.min_p ? __ldg(P.min_p + r) : 0.0f;
-    const float u = __ldg(P.uniforms + r);
+    const float temp = P.temperature ? ld(P.temperature + r) : 1.0f;
+    const int k0 = P.top_k ? ld(P.top_k + r) : 0;
+    const float p = P.top_p ? ld(P.top_p + r) : 1.0f;
+    const float m = P.min_p ? ld(P.min_p + r) : 0.0f;
+    const float u = ld(P.uniforms + r);
     const bool greedy = !(temp > 0.0f) || k0 == 1;
     const int k = k0 >= 1 && k0 < P.V ? k0 : 0;
     const bool open = !greedy && !k && !(p < 1.0f) && !(m > 0.0f);
@@ -1481,9 +1475,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
                     L = sh.peak[c];
                     best = static_cast<int>(sh.count[c]);
                 }
-            P.tokens[r] = best;
-            if (P.logprob) P.logprob[r] = best < 0 ? -kInf : 0.0f;
-            if (probs && best >= 0) probs[best] = 1.0f;
+            st(P.tokens + r, best);
+            if (P.logprob) st(P.logprob + r, best < 0 ? -kInf : 0.0f);
+            if (probs && best >= 0) st(probs + best, 1.0f);
         }
         return;
     }
@@ -1503,8 +1497,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
         if (all_listed(sh, cluster, part, &total)) {
             if (total == 0) {  // nothing to keep
                 if (rank == 0 && tid == 0) {
-                    P.tokens[r] = -1;
-                    if (P.logprob) P.logprob[r] = -kInf;
+                    st(P.tokens + r, -1);
+                    if (P.logprob) st(P.logprob + r, -kInf);
                 }
                 return;
             }
@@ -1537,8 +1531,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     }
     if (!(L > -kInf)) {
         if (rank == 0 && tid == 0) {
-            P.tokens[r] = -1;
-            if (P.logprob) P.logprob[r] = -kInf;
+            st(P.tokens + r, -1);
+            if (P.logprob) st(P.logprob + r, -kInf);
         }
         if (probs && open) write_zeros(R, probs);
         return;
@@ -1619,17 +1613,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
 // whatever cu holds.
 __device__ __forceinline__ int row_token(const LogprobParams &P, long long r)
 {
-    if (!P.cu) return __ldg(P.tokens + r);
+    if (!P.cu) return ld(P.tokens + r);
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = P.num_reqs;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
-        const bool before = lane == 0 || (at < hi && static_cast<long long>(__ldg(P.cu + at)) + at <= r);
+        const bool before = lane == 0 || (at < hi && static_cast<long long>(ld(P.cu + at)) + at <= r);
         lo += (31 - __clz(static_cast<int>(__ballot_sync(0xFFFFFFFFu, before)))) * step;
         hi = min(hi, lo + step);
     }
-    const long long j = r - __ldg(P.cu + lo) - lo;
-    return j >= 0 && j < P.token_stride ? __ldg(P.tokens + static_cast<long long>(lo) * P.token_stride + j) : -1;
+    const long long j = r - ld(P.cu + lo) - lo;
+    return j >= 0 && j < P.token_stride ? ld(P.tokens + static_cast<long long>(lo) * P.token_stride + j) : -1;
 }
 
 __device__ __forceinline__ u64 pack(float a, float b)
@@ -1661,18 +1655,18 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
     const bool wanted = token >= 0 && token < P.V;
     if (!wanted) {
         if (rank != 0) return;
-        if (tid == 0 && P.logprob) P.logprob[r] = -kInf;
-        if (tid == 0 && P.rank) P.rank[r] = 0;
+        if (tid == 0 && P.logprob) st(P.logprob + r, -kInf);
+        if (tid == 0 && P.rank) st(P.rank + r, 0);
         for (int i = tid; i < top; i += kThreads) {
-            P.top_ids[r * top + i] = -1;
-            P.top_logprob[r * top + i] = -kInf;
+            st(P.top_ids + r * top + i, -1);
+            st(P.top_logprob + r * top + i, -kInf);
         }
         return;
     }
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
     const Row<T> R = start_row(row, P.V, P.split, rank, sh);
-    const float lt = fmaxf(as_float(__ldg(row + token)), -kInf);  // (NaN as -inf)
-    const float temp = P.temperature ? __ldg(P.temperature + r) : 1.0f;
+    const float lt = fmaxf(as_float(ld(row + token)), -kInf);  // (NaN as -inf)
+    const float temp = P.temperature ? ld(P.temperature + r) : 1.0f;
     const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
     const float scale = fminf(inv * kLog2e, FLT_MAX);
     // Some vectors at a time, against a reference that moves to the largest logit only once that is kRise
@@ -1747,8 +1741,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
         norm = sv::log_f32(sum);
         if (tid == 0) {
             const float d = lt == L ? 0.0f : (lt - L) * inv;
-            if (P.logprob) P.logprob[r] = lt > -kInf ? d - norm : -kInf;
-            if (P.rank) P.rank[r] = 1 + static_cast<int>(rank_sum);
+            if (P.logprob) st(P.logprob + r, lt > -kInf ? d - norm : -kInf);
+            if (P.rank) st(P.rank + r, 1 + static_cast<int>(rank_sum));
         }
     }
     if (!kTop) return;
@@ -1756,8 +1750,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
         const auto index = static_cast<int>(~static_cast<unsigned>(entry));
         const float l = entry ? of_key(static_cast<unsigned>(entry >> 32)) : -kInf;
         const float d = l == L ? 0.0f : (l - L) * inv;
-        P.top_ids[r * top + i] = entry ? index : -1;
-        P.top_logprob[r * top + i] = entry ? d - norm : -kInf;
+        st(P.top_ids + r * top + i, entry ? index : -1);
+        st(P.top_logprob + r * top + i, entry ? d - norm : -kInf);
     };
     int total;
     if (all_listed(sh, cluster, part, &total)) {
