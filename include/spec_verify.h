@@ -524,7 +524,8 @@ int spec_verify_sample(const spec_verify_sample_args *args, void *cuda_stream);
  * best tokens, over the whole vocabulary: ln p_v = (l_v - L) / T - ln sum exp((l_v - L) / T),
  * computed in binary32. Its error is at most 2^-16 + 2^-22 |ln p_v| for any row of any length (1e-6
  * is usual); a value near 0 has this absolute precision, not a relative one.
- *   temperature    [num_rows] binary32 or NULL (1); a value that is not above 0 counts as 1
+ *   temperature    [num_rows] binary32 or NULL (1); a value that is not above 0 counts as 1, one below
+ *                  2^-126 (a subnormal number) as 2^-126
  *   tokens         [num_rows] int32; or, with cu_num_draft, the `sampled` of a verification,
  *                  [num_reqs, token_stride] int32 with token_stride = max_spec_len_this_batch + 1:
  *                  row cu_num_draft[i] + i + j is then the row of sampled[i, j]; or NULL (only

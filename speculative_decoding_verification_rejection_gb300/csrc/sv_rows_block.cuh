@@ -1562,6 +1562,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
         const float own = R.inf ? (peak == kInf ? sum : 0.0f) : peak > -kInf ? sum * sv::ex2_approx((peak - L) * scale) : 0.0f;
         const u64 near = ex.sum(warp_sum(__float2ull_rn(own * 0x1p+40f)));
         Share share{true, share_of(p, near - near / kSure), share_of(p, near + near / kSure + 1)};
+        if (scale == FLT_MAX) {  // (log2 e / T beyond that: the sums are of other powers)
+            share.least = 0;
+            share.most = ~0ull;
+        }
         u64 listed = 0;
         for (int c = 0; c < cluster; ++c) listed += sh.listed[c];
         if (cut == -FLT_MAX) share.least = share.most = share_of(p, listed);  // (the whole row is listed)
@@ -1667,8 +1671,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
     const Row<T> R = start_row(row, P.V, P.split, rank, sh);
     const float lt = fmaxf(as_float(ld(row + token)), -kInf);  // (NaN as -inf)
     const float temp = P.temperature ? ld(P.temperature + r) : 1.0f;
-    const float inv = temp > 0.0f ? inverse(temp) : 1.0f;
-    const float scale = fminf(inv * kLog2e, FLT_MAX);
+    const float inv = temp > 0.0f ? inverse(fmaxf(temp, FLT_MIN)) : 1.0f;
+    const float scale = inv * kLog2e;
     // Some vectors at a time, against a reference that moves to the largest logit only once that is kRise
     // above it: each move rounds what was added before, and where logits rise a little all along the row
     // those errors would add up (moved each time, -13.1639 was off by 6.8e-6 after 128 moves). Batches
