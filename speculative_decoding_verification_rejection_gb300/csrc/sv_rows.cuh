@@ -23,10 +23,12 @@ constexpr int kTopP = 64;         // lane maxima that the cut for top-p alone is
 constexpr int kWideList = 2048;   // the same of a bracket's tokens
 constexpr int kBeside = 64;       // tokens on each side of a guess
 constexpr int kBins = 4096;       // bins of the value histogram
-constexpr float kRise = 4.0f;     // doublings that a log-probability's logits pass their reference by before it moves
 constexpr float kSpan = 28.5f;    // the d they cover: below -28.43 a weight is 0
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 0x1.715476p+0f;
+constexpr float kRise = 4.0f;     // doublings that a log-probability's logits pass their reference by before it moves
+static_assert(kPairs <= 256, "a sum of weights below 2^48, and a number above it, in 64 bits");
+static_assert(kWideList < 4096, "sums of the weights' upper 20 bits in 32");
 
 // What a launch is told.
 struct Split {
@@ -393,8 +395,9 @@ __device__ __forceinline__ Two exp_two(Two d)
 // 2^-20, whose count the low mantissa bits then hold; what that left, at most 2^-21, is rounded to
 // a multiple of 2^-40 by adding 1.5 2^-17 in the same way. Together they are rint(t 2^40), ties as
 // rint's. The words add the bit patterns; the constant parts come off at the end. Good for up to
-// 4095 weights. (Nothing here is done in binary64, nor by conversions to 64-bit integers: this
+// kMostWeights weights. (Nothing here is done in binary64, nor by conversions to 64-bit integers: this
 // part runs those at a sixtieth of the binary32 rate.)
+constexpr int kMostWeights = 4095;  // (each adds up to 2^20 to the first word)
 struct WeightSum {
     unsigned a = 0, b = 0;
     __device__ __forceinline__ void add(float t)

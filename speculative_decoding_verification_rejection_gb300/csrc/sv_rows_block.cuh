@@ -330,14 +330,34 @@ __device__ float cut_for(float peak, float largest, int want, int most, Shared &
 // ---------------------------------------------------------------------------------------
 // sampling
 // ---------------------------------------------------------------------------------------
-// The row's weight by the lanes' sums is off by less than one part in kSure: a term's 2^x by 2^-22,
-// its argument, at most 42, by three roundings (42 3 2^-24 ln 2 < 2^-17.5); the same again where a
-// lane's sum is taken from one largest logit to another, which happens to a sum at most 65 times (once
-// for each of up to 64 times it is added to, and to the row's), each time by 2^-22 and the rounding
-// of a difference that these add up to at most 42; a chain of at most 32 + 64 additions by as many
-// roundings; the weights' own exp by 2^-23 and their rounding to 2^-40 by V 2^-41. Together below
-// 2^-17.5 + 2^-17.5 + 65 2^-22 + 96 2^-24 + 2^-21 < 2^-14.
+// A lane's most vectors of a row: the largest vocabulary, by one CTA.
+template <typename T>
+constexpr int most_vectors()
+{
+    const int per_warp = (SV_ROWS_MAX_VOCAB / Vec<T>::n + 2 + kWarps - 1) / kWarps;
+    return (per_warp + 31) / 32;
+}
+template <typename T>
+constexpr int most_batches = (most_vectors<T>() + kAhead - 1) / kAhead;
+static_assert(most_vectors<uint16_t>() * Vec<uint16_t>::n <= kMostWeights && most_vectors<float>() * Vec<float>::n <= kMostWeights,
+              "a lane's weights go into one sum");
+static_assert(SV_ROWS_MAX_VOCAB < 1 << 23, "a row's weights, 2^40 each at most, go into 64 bits");
+
+// The row's weight by the lanes' sums is off by less than one part in kSure. In units of 2^-24, a rounding:
+//   arguments  a term that is not 0 has a d of at most 29.2 (42 doublings). Its argument is a difference
+//              times fl(fl(log2 e) / T): log2 e off by 0.25, two products and the difference, each
+//              relative to the difference, also where the sum goes from one largest logit to another
+//              (the differences then add up to that d); and the d that the weight is made from has two
+//              roundings of its own: 29.2 * 5.25 < 154
+//   moves      a lane's sum goes from one largest logit to another at most once a batch after the first,
+//              and then to the row's: a 2^x of 4 and a product, 5 a batch
+//   additions  at most 32 pairs in a batch, its halves, and one a batch
+//   the rest   a term's 2^x 4, the weight's exp 2, its rounding to 2^-40 and the terms that are 0 there, over
+//              a sum of at least 1, V 2^-41 each: 4 and 4, and the sum as a whole number 1: below 16
+// (kRise is not in this: here the reference is the largest logit so far.)
 constexpr u64 kSure = 1 << 14;
+constexpr int kSumError = 154 + (5 + 1) * (most_batches<float> > most_batches<uint16_t> ? most_batches<float> : most_batches<uint16_t>) + 33 + 16;
+static_assert(static_cast<u64>(kSumError) * kSure <= 1 << 24, "the row's weight is known to a part in kSure");
 
 // What is kept, besides key_of(l) != 0: l >= tau and d >= low.
 struct Kept {
