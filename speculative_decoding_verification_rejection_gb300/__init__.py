@@ -581,7 +581,8 @@ def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_
     num_reqs = width = 0
     if cu_num_draft is not None:
         num_reqs = cu_num_draft.numel() - 1
-        if tokens.dim() != 2 or tokens.shape[0] != num_reqs or num_reqs < 1 or tokens.shape[1] < 1:
+        if (tokens.dim() != 2 or tokens.shape[0] != num_reqs or (num_reqs == 0 and rows)
+                or tokens.shape[1] < 1):
             raise ValueError("with cu_num_draft, tokens must be [num_reqs, max_spec_len + 1]")
         width = tokens.shape[1]
     args = LogprobsArgs(ptr, stride, _row_array("temperature", temperature, f32, (rows,), dev),
