@@ -183,7 +183,7 @@ int launch(void (*kernel)(const T *, Params), const void *logits, Params P, int 
     P.cluster = s.cluster;
     P.split = s.split;
     if constexpr (std::is_same_v<Params, SampleParams>)
-        P.ordered = P.top_p && P.top_k && rows <= 2 * threads && rows * s.cluster > 152 * (1024 / threads) ? rows : 0;
+        P.ordered = P.top_p && P.top_k && threads == 512 && rows <= 2 * threads && rows * s.cluster > 152 * (1024 / threads) ? rows : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * static_cast<unsigned>(s.cluster));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));

@@ -4,6 +4,7 @@ constexpr int kThreads = SV_ROWS_THREADS;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = kBins / kThreads;  // groups of a lane's vectors whose maxima are kept
 constexpr int kCtas = 1024 / kThreads;     // CTAs on an SM: 64 registers for each thread
+constexpr bool kOrdered = kThreads == 512;  // whether rows may be put in order (the smaller blocks take too many)
 
 // ---------------------------------------------------------------------------------------
 // warp and block reductions (block-wide ones by every thread)
@@ -554,7 +555,7 @@ __device__ __forceinline__ u64 pairs_sum(u64 v, u64 *box)
 // each in index, is counted and summed over all pairs, several threads to an entry. By half the
 // block: more warps would wait on one another's instructions longer than they save.
 __device__ bool draw_pairs(const Drawn &out, const u64 *work, u64 *wts, int count, int k, float p, Share share, u64 *part,
-                           u64 *box, float u, Shared &sh)
+                           u64 *box, float u)
 {
     const int tid = threadIdx.x;
     if (tid >= kPairs) return true;
@@ -568,7 +569,7 @@ __device__ bool draw_pairs(const Drawn &out, const u64 *work, u64 *wts, int coun
     u64 w = i < count ? wts[i] : 0;
     bool keep = i < count && listed_delta(key, out.keep) >= out.keep.low;
     const bool within = k > 0 && p < 1.0f;  // the share is of what top-k keeps
-    if (k > 0 || share.on || within) {
+    if (k > 0 || share.on) {
         u64 above = 0;
         unsigned larger = 0;
 #pragma unroll 4
@@ -731,7 +732,7 @@ __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *
             wts[tid] = weight(exp_weight(listed_delta(static_cast<unsigned>(mine[0] >> 32), keep)));
         }
         __syncthreads();
-        return draw_pairs(out, list, wts, total, k, p, share, part, sh.box, u, sh);
+        return draw_pairs(out, list, wts, total, k, p, share, part, sh.box, u);
     }
     // the entries left, in any order, closed up
     u64 *wts = sums;
@@ -748,7 +749,7 @@ __device__ bool finish_list(const SampleParams &P, long long r, u64 *list, u64 *
     }
     __syncthreads();
     const int count = static_cast<int>(sh.mine);
-    if (count <= kPairs) return draw_pairs(out, list, wts, count, k, p, share, sums + kPairs, sh.box, u, sh);
+    if (count <= kPairs) return draw_pairs(out, list, wts, count, k, p, share, sums + kPairs, sh.box, u);
     int size = 1;
     while (size < count) size *= 2;
     for (int i = count + tid; i < size; i += kThreads) list[i] = 0;
@@ -1446,7 +1447,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     const int place = static_cast<int>(blockIdx.x) / cluster;
     const Room room(store);
     cluster_announce();  // (waited for before the first write to another CTA: that it runs by then)
-    const long long r = P.ordered ? long_first(P, place, sh) : place;
+    const long long r = kOrdered && P.ordered ? long_first(P, place, sh) : place;
     Row<T> R = start_row(logits + r * P.stride, P.V, P.split, rank, sh);
     const int part = kList / cluster;
     const float temp = P.temperature ? ld(P.temperature + r) : 1.0f;
