@@ -496,12 +496,12 @@ struct Drawn {
     const Kept &keep;
     __device__ __forceinline__ void token(u64 entry, u64 Z) const
     {
-        st(P.tokens + r, static_cast<int>(~static_cast<unsigned>(entry)));
-        if (P.logprob) st(P.logprob + r, log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z));
+        st(&P.tokens[r], static_cast<int>(~static_cast<unsigned>(entry)));
+        if (P.logprob) st(&P.logprob[r], log_prob(listed_delta(static_cast<unsigned>(entry >> 32), keep), Z));
     }
     __device__ __forceinline__ void prob(u64 entry, float scale) const
     {
-        st(P.probs + r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry)),
+        st(&P.probs[r * P.probs_stride + static_cast<int>(~static_cast<unsigned>(entry))],
            sv::exp_f32(listed_delta(static_cast<unsigned>(entry >> 32), keep)) * scale);
     }
 };
@@ -1205,7 +1205,7 @@ __device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const
         for (int i = R.first() + static_cast<int>(threadIdx.x); i < R.last(); i += kThreads) {
             const float l = R.at(i), d = delta(l, keep.L, keep.inv);
             const bool in = l > -kInf && (kAll || (l >= keep.tau && d >= keep.low));
-            if (kAll || in) st(probs + i, in ? sv::exp_f32(d) * scale : 0.0f);
+            if (kAll || in) st(&probs[i], in ? sv::exp_f32(d) * scale : 0.0f);
         }
         return;
     }
@@ -1237,7 +1237,7 @@ __device__ __forceinline__ void write_probs(const Row<T> &R, float *probs, const
             } else {
 #pragma unroll
                 for (int e = 0; e < n; ++e)
-                    if (first + e >= 0 && first + e < R.V) st(probs + first + e, f[e]);
+                    if (first + e >= 0 && first + e < R.V) st(&probs[first + e], f[e]);
             }
         }
     });
@@ -1251,9 +1251,9 @@ __device__ __forceinline__ void write_zeros(const Row<T> &R, float *probs)
     const int tid = threadIdx.x, first = R.first(), last = R.last();
     const int head = min(first + static_cast<int>((16u - (reinterpret_cast<uintptr_t>(probs + first) & 15u)) / 4u % 4u), last);
     const int body = head + max(last - head, 0) / 4 * 4;
-    if (first + tid < head) st(probs + first + tid, 0.0f);
+    if (first + tid < head) st(&probs[first + tid], 0.0f);
     for (int i = head + 4 * tid; i < body; i += 4 * kThreads) st_leaving(reinterpret_cast<float4 *>(probs + i), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-    if (body + tid < last) st(probs + body + tid, 0.0f);
+    if (body + tid < last) st(&probs[body + tid], 0.0f);
 }
 
 // The draw where the run on which the uniform number falls is known: the CTA that holds it finds the
@@ -1282,8 +1282,8 @@ __device__ void draw_run(const SampleParams &P, const Row<T> &R, long long r, fl
             int i = R.base + from * n;
             float l = R.at(i);
             while (!target.passed(run += weight(kept_weight<kAll>(l, keep))) && i < last) l = R.at(++i);
-            st(P.tokens + r, i);
-            if (P.logprob) st(P.logprob + r, log_prob(delta(l, keep.L, keep.inv), Z));
+            st(&P.tokens[r], i);
+            if (P.logprob) st(&P.logprob[r], log_prob(delta(l, keep.L, keep.inv), Z));
         }
     }
     if (P.probs) write_probs<kAll>(R, P.probs + r * P.probs_stride, keep, Z);
@@ -1496,9 +1496,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
                     L = sh.peak[c];
                     best = static_cast<int>(sh.count[c]);
                 }
-            st(P.tokens + r, best);
-            if (P.logprob) st(P.logprob + r, best < 0 ? -kInf : 0.0f);
-            if (probs && best >= 0) st(probs + best, 1.0f);
+            st(&P.tokens[r], best);
+            if (P.logprob) st(&P.logprob[r], best < 0 ? -kInf : 0.0f);
+            if (probs && best >= 0) st(&probs[best], 1.0f);
         }
         return;
     }
@@ -1518,8 +1518,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
         if (all_listed(sh, cluster, part, &total)) {
             if (total == 0) {  // nothing to keep
                 if (rank == 0 && tid == 0) {
-                    st(P.tokens + r, -1);
-                    if (P.logprob) st(P.logprob + r, -kInf);
+                    st(&P.tokens[r], -1);
+                    if (P.logprob) st(&P.logprob[r], -kInf);
                 }
                 return;
             }
@@ -1552,8 +1552,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sv_sample_kernel(const T *log
     }
     if (!(L > -kInf)) {
         if (rank == 0 && tid == 0) {
-            st(P.tokens + r, -1);
-            if (P.logprob) st(P.logprob + r, -kInf);
+            st(&P.tokens[r], -1);
+            if (P.logprob) st(&P.logprob[r], -kInf);
         }
         if (probs && open) write_zeros(R, probs);
         return;
@@ -1680,11 +1680,11 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
     const bool wanted = token >= 0 && token < P.V;
     if (!wanted) {
         if (rank != 0) return;
-        if (tid == 0 && P.logprob) st(P.logprob + r, -kInf);
-        if (tid == 0 && P.rank) st(P.rank + r, 0);
+        if (tid == 0 && P.logprob) st(&P.logprob[r], -kInf);
+        if (tid == 0 && P.rank) st(&P.rank[r], 0);
         for (int i = tid; i < top; i += kThreads) {
-            st(P.top_ids + r * top + i, -1);
-            st(P.top_logprob + r * top + i, -kInf);
+            st(&P.top_ids[r * top + i], -1);
+            st(&P.top_logprob[r * top + i], -kInf);
         }
         return;
     }
@@ -1766,8 +1766,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
         norm = sv::log_f32(sum);
         if (tid == 0) {
             const float d = lt == L ? 0.0f : (lt - L) * inv;
-            if (P.logprob) st(P.logprob + r, lt > -kInf ? d - norm : -kInf);
-            if (P.rank) st(P.rank + r, 1 + static_cast<int>(rank_sum));
+            if (P.logprob) st(&P.logprob[r], lt > -kInf ? d - norm : -kInf);
+            if (P.rank) st(&P.rank[r], 1 + static_cast<int>(rank_sum));
         }
     }
     if (!kTop) return;
@@ -1775,8 +1775,8 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
         const auto index = static_cast<int>(~static_cast<unsigned>(entry));
         const float l = entry ? of_key(static_cast<unsigned>(entry >> 32)) : -kInf;
         const float d = l == L ? 0.0f : (l - L) * inv;
-        st(P.top_ids + r * top + i, entry ? index : -1);
-        st(P.top_logprob + r * top + i, entry ? d - norm : -kInf);
+        st(&P.top_ids[r * top + i], entry ? index : -1);
+        st(&P.top_logprob[r * top + i], entry ? d - norm : -kInf);
     };
     int total;
     if (all_listed(sh, cluster, part, &total)) {

@@ -34,6 +34,6 @@ def test_every_global_access_is_a_checked_one():
     with open(os.path.join(os.path.dirname(sv._UNITS[0]), "sv_rows_block.cuh"), encoding="utf-8") as f:
         code = re.sub(r"//.*", "", f.read())
     arrays = r"(?:row|vec|probs|logits|P\.[a-z_]+)\b"
-    for plain in (r"__ldg|__stcs|[a-z]+\.global", rf"(?<![\w.]){arrays}\s*\[", rf"(?:[=(,{{;]|return)\s*\*\s*\(?{arrays}",
+    for plain in (r"__ldg|__stcs|[a-z]+\.global", rf"(?<![\w.&]){arrays}\s*\[", rf"(?:[=(,{{;]|return)\s*\*\s*\(?{arrays}",
                   r"(?:[=(,{;]|return)\s*\*\s*reinterpret_cast"):
         assert not (found := re.findall(plain, code)), found
