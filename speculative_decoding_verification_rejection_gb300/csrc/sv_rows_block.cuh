@@ -1664,7 +1664,7 @@ static_assert(SV_MAX_TOP <= kList / kMaxCluster / 8 * 5, "every CTA can list its
 // leader in the place that the number of larger ones gives it.
 // Without best tokens no row is read again, and a fifth block on an SM, with half the vectors read
 // ahead, hides more than the second look at rows that no longer fit the L2 cache costs (640x40003
-// float32 21 against 27 us; with 5 best of 1536x151936 bf16 77 against 68).
+// float32 23 against 30 us; with 5 best of 1536x151936 bf16 78 against 69).
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprobs_kernel(const T *logits, LogprobParams P)
 {
@@ -1700,7 +1700,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? kCtas : kCtas + 1) sv_logprob
     // are added by Kahan's compensated summation: a batch far smaller than the sum would otherwise
     // round it the same way each time (-0.0257 off by 3.1e-6). Together they cost 2 to 4 %. The logit from
     // which the reference moves is held in a register where float32 rows are read once and found anew for
-    // each batch elsewhere: 512x128256 float32 50 against 58 us, 640x151936 bf16 47 against 44.5, with 5
+    // each batch elsewhere: 512x128256 float32 50 against 58 us, 640x151936 bf16 46 against 44.5, with 5
     // best tokens 65 against 57.
     constexpr bool held = !kTop && sizeof(T) == 4;
     float peak = -kInf, ref = -kInf, limit = -kInf, s = 0.0f, lost = 0.0f;
