@@ -80,13 +80,15 @@ extern "C" {
 #define SV_OK 0
 #define SV_EINVAL (-1)    /* NULL or misaligned pointer, negative size, bad argument */
 #define SV_ECAPACITY (-2) /* a size above the capacity given to spec_verify_init */
-#define SV_EDTYPE (-3)    /* logits dtype not SV_F32 / SV_BF16 */
+#define SV_EDTYPE (-3)    /* an element type that the call does not take */
 #define SV_ECUDA (-4)     /* a CUDA runtime call failed */
 #define SV_EDEVICE (-5)   /* no usable device, or not an sm_103 device */
 
-/* logits element types */
+/* element types (logits: the first two; cache operators: the last three) */
 #define SV_F32 0  /* IEEE binary32 */
 #define SV_BF16 1 /* bfloat16 (upper half of a binary32) */
+#define SV_F16 2  /* IEEE binary16 */
+#define SV_E4M3 3 /* 8 bits: 4 of exponent, 3 of mantissa, no infinity, largest value 448 */
 
 /* draft inputs a context accepts (bits of spec_verify_init's draft_input) */
 #define SV_DRAFT_PROBS 1  /* draft_probs may be given to spec_verify_run */
@@ -560,6 +562,140 @@ typedef struct spec_verify_logprobs_args {
 } spec_verify_logprobs_args;
 
 int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_stream);
+
+/*
+ * Cache operators: what the rows of a step do with the paged cache of keys and values before their
+ * logits are there. The rows are the verification's: row cu_num_draft[i] + i + j, 0 <= j <= K_i,
+ * is the j-th new token of request i (cu_num_draft NULL: one row a request), and its place in the
+ * sequence is x = lengths[i] + j, lengths[i] the tokens that the cache holds of the request
+ * before the step. A step appends its rows (spec_verify_cache_append), attends over the cache
+ * (spec_verify_cache_attention, the same lengths), verifies, and then adds num_sampled to lengths:
+ * of the appended tokens the accepted ones stay, and the next step overwrites the others.
+ *
+ * Place x of request i is slot x % page_size of page page_table[i, x / page_size]. Which pages a
+ * request has is the caller's; entries behind its last place are not read. All pointers are
+ * device pointers of `device` except `axes`, owned by the caller and valid until the stream reaches
+ * the end of the call; inputs stay as they are until then, and outputs share no memory with
+ * inputs or with each other. No context, no allocation, no host synchronisation, capturable in a CUDA
+ * graph; calls may overlap on any streams. Problems visible on the host return a status and launch
+ * nothing; 0 rows or 0 requests are SV_OK.
+ *   Left out, with nothing written for them: rows behind the last request's; a request whose rows
+ *   are not all within num_rows (an inconsistent cu_num_draft). A request of negative length takes no
+ *   part (a padded batch): nothing is appended and its queries are not turned; its attention
+ *   outputs are those of rows that see no key. A key whose page is outside [0, num_pages), or whose
+ *   place is not within pages_per_req pages, is not written, and not seen.
+ *   A head's head_dim elements are contiguous; strides are in elements, multiples of 16 bytes
+ *   (any sign-free layout: pages of tokens or of heads, views of a fused projection); addresses
+ *   of q, k, v, out and the caches are 16-byte aligned. An element of an SV_E4M3 cache stands for
+ *   itself times its head's scale; without scales (NULL) for itself.
+ */
+#define SV_MAX_HEAD_DIM 256
+#define SV_MAX_AXES 4
+#define SV_MAX_PAGE 65536
+
+/*
+ * spec_verify_cache_append: k and v of every row into the cache, k turned by its position and so
+ * the queries. Pair m < rotary_dim / 2 of a head, elements (m, m + rotary_dim / 2) or with
+ * interleaved (2 m, 2 m + 1), is turned by the angle a = pos * inv_freq[m]:
+ * (y1, y2) = (x1 cos a - x2 sin a, x1 sin a + x2 cos a); elements from rotary_dim on stay as they
+ * are. a is taken modulo a turn in fixed point (steps of 2^-64 of a turn; its error is below
+ * 2^-52 |a| + 2^-29), so far positions lose nothing; sums and products are binary32, rounded once to the
+ * element type. Values beyond 448 of an SV_E4M3 cache become 448, NaN stays NaN.
+ *   q, q_out        [num_rows, num_q_heads, head_dim] of dtype (num_q_heads 0: none); q_out may be q
+ *                   itself with the same strides
+ *   k, v            [num_rows, num_kv_heads, head_dim] of dtype (SV_BF16 / SV_F16)
+ *   k_cache, v_cache [num_pages, page_size, num_kv_heads, head_dim] of cache_dtype: dtype, or SV_E4M3
+ *   page_table      [num_reqs, pages_per_req] int32, rows table_stride apart
+ *   lengths         [num_reqs] int32;  cu_num_draft [num_reqs + 1] int32 or NULL
+ *   inv_freq        [rotary_dim / 2] binary32, radians a position; NULL with rotary_dim 0
+ *   positions       NULL (pos = x), or [num_axes, num_rows] int32, rows positions_stride apart: pos
+ *                   of pair m is that of axis axes[m] (axes a HOST array of rotary_dim / 2 bytes below
+ *                   num_axes, read during the call; NULL: axis 0)
+ *   k_scale, v_scale [num_kv_heads] binary32 or NULL, with SV_E4M3 only: what is stored is the
+ *                   value divided by the scale
+ *   head_dim a multiple of 16 up to SV_MAX_HEAD_DIM, rotary_dim one up to head_dim
+ */
+typedef struct spec_verify_cache_append_args {
+    const void *q;
+    const void *k;
+    const void *v;
+    void *q_out;
+    void *k_cache;
+    void *v_cache;
+    int64_t q_row_stride, q_head_stride;
+    int64_t k_row_stride, k_head_stride;
+    int64_t v_row_stride, v_head_stride;
+    int64_t q_out_row_stride, q_out_head_stride;
+    int64_t k_page_stride, k_slot_stride, k_cache_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_cache_head_stride;
+    const int32_t *page_table;
+    int64_t table_stride;
+    const int32_t *lengths;
+    const int32_t *cu_num_draft;
+    const int32_t *positions;
+    int64_t positions_stride;
+    const float *inv_freq;
+    const float *k_scale;
+    const float *v_scale;
+    const uint8_t *axes;
+    int32_t num_rows, num_reqs, num_q_heads, num_kv_heads;
+    int32_t head_dim, rotary_dim, interleaved, num_axes;
+    int32_t num_pages, page_size, pages_per_req;
+    int32_t dtype, cache_dtype, device;
+} spec_verify_cache_append_args;
+
+int spec_verify_cache_append(const spec_verify_cache_append_args *args, void *cuda_stream);
+
+/*
+ * spec_verify_cache_attention: softmax attention of every row over the keys of its request's cache
+ * up to its own place (the rows' own keys have been appended before): with
+ * s_t = scale * (q . k_t) for the places t <= x, and t > x - window if window > 0,
+ * out = sum exp(s_t) v_t / Z, lse = ln Z, Z = sum exp(s_t). Query head g reads key head
+ * g / (num_q_heads / num_kv_heads). A row that sees no key (or only keys of score -inf) gets out 0 and
+ * lse -inf. Keys and values that a row does not see do not reach it, whatever they hold. Products of
+ * elements are exact, sums, maxima and Z binary32; weights are rounded to the products' 16-bit type
+ * relative to a maximum of their row.
+ *   q, out          [num_rows, num_q_heads, head_dim] of dtype (SV_BF16 / SV_F16)
+ *   lse             [num_rows, num_q_heads] binary32 (out) or NULL
+ *   k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale: as above
+ *   scale           finite;  window 0: none
+ *   head_dim        64, 128 or 256
+ *   workspace       device memory of workspace_bytes, at least what
+ *                   spec_verify_cache_attention_workspace says (of the same arguments; it may be 0),
+ *                   16-byte aligned; its contents matter neither before nor after. Calls that may
+ *                   overlap need one each
+ * Any number of new rows a request; the kernels are made for the few of a draft or verification step.
+ */
+typedef struct spec_verify_cache_attention_args {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    void *out;
+    float *lse;
+    int64_t q_row_stride, q_head_stride;
+    int64_t out_row_stride, out_head_stride;
+    int64_t k_page_stride, k_slot_stride, k_cache_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_cache_head_stride;
+    const int32_t *page_table;
+    int64_t table_stride;
+    const int32_t *lengths;
+    const int32_t *cu_num_draft;
+    const float *k_scale;
+    const float *v_scale;
+    void *workspace;
+    int64_t workspace_bytes;
+    float scale;
+    int32_t window;
+    int32_t num_rows, num_reqs, num_q_heads, num_kv_heads, head_dim;
+    int32_t num_pages, page_size, pages_per_req;
+    int32_t dtype, cache_dtype, device;
+} spec_verify_cache_attention_args;
+
+int spec_verify_cache_attention(const spec_verify_cache_attention_args *args, void *cuda_stream);
+
+/* Bytes of workspace that spec_verify_cache_attention needs for these arguments (pointers are not looked
+ * at); they follow from the sizes and types alone. Launches nothing. */
+int spec_verify_cache_attention_workspace(const spec_verify_cache_attention_args *args, int64_t *bytes);
 
 /* Release the context and its device memory. NULL is a no-op. */
 void spec_verify_free(spec_verify_ctx *ctx);

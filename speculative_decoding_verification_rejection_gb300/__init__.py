@@ -20,26 +20,27 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
 _INCLUDE = os.path.join(_ROOT, "include")
 _HEADER = os.path.join(_INCLUDE, "spec_verify.h")
-_UNITS = [os.path.join(_PKG, "csrc", f) for f in ("spec_verify.cu", "sv_rows.cu")]
+_UNITS = [os.path.join(_PKG, "csrc", f) for f in ("spec_verify.cu", "sv_rows.cu", "sv_cache.cu")]
 _SOURCES = [*_UNITS, *(os.path.join(_PKG, "csrc", f) for f in ("sv_device.cuh", "sv_rows.cuh",
-                                                                "sv_rows_block.cuh"))]
+                                                                "sv_rows_block.cuh", "sv_cache.cuh"))]
 # SPEC_VERIFY_DEBUG_BOUNDS=1 in the environment selects the checked build (-DSV_DEBUG_BOUNDS): every
 # global load and store of the kernels is checked against the call's arrays, and an access
-# outside them is skipped and reported as SV_ERR_BOUNDS in the error word (by the row operators in the
-# one that spec_verify_rows_outside of that build reads). For tests only.
+# outside them is skipped and reported as SV_ERR_BOUNDS in the error word (by the row and cache operators in
+# those that spec_verify_rows_outside and spec_verify_cache_outside of that build read). For tests only.
 DEBUG_BOUNDS = os.environ.get("SPEC_VERIFY_DEBUG_BOUNDS", "0") not in ("", "0")
 RELEASE_LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libspecverify_debug.so")
 LIB_PATH = DEBUG_LIB_PATH if DEBUG_BOUNDS else RELEASE_LIB_PATH
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-shared", "-Xcompiler", "-fPIC", "--threads", "2", "-I" + _INCLUDE]
+              "-shared", "-Xcompiler", "-fPIC", "--threads", "3", "-I" + _INCLUDE]
 
 SV_OK, SV_EINVAL, SV_ECAPACITY, SV_EDTYPE, SV_ECUDA, SV_EDEVICE = 0, -1, -2, -3, -4, -5
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 1, 2
 SV_MAX_SYNTHETIC = 64
 SV_ROWS_MAX_VOCAB, SV_MAX_TOP = 524288, 64
+SV_MAX_HEAD_DIM, SV_MAX_AXES, SV_MAX_PAGE = 256, 4, 65536
 
 
 class Batch(ctypes.Structure):
@@ -86,6 +87,38 @@ class LogprobsArgs(ctypes.Structure):
                 ("num_reqs", ctypes.c_int32), ("num_top", ctypes.c_int32),
                 ("num_rows", ctypes.c_int32), ("vocab_size", ctypes.c_int32),
                 ("logits_dtype", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
+_VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """spec_verify_cache_append_args of include/spec_verify.h."""
+    _fields_ = [*((f, _VP) for f in ("q", "k", "v", "q_out", "k_cache", "v_cache")),
+                *((f, _I64) for f in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                      "v_row_stride", "v_head_stride", "q_out_row_stride", "q_out_head_stride",
+                                      "k_page_stride", "k_slot_stride", "k_cache_head_stride",
+                                      "v_page_stride", "v_slot_stride", "v_cache_head_stride")),
+                ("page_table", _VP), ("table_stride", _I64), ("lengths", _VP), ("cu_num_draft", _VP),
+                ("positions", _VP), ("positions_stride", _I64), ("inv_freq", _VP), ("k_scale", _VP),
+                ("v_scale", _VP), ("axes", ctypes.c_char_p),
+                *((f, _I32) for f in ("num_rows", "num_reqs", "num_q_heads", "num_kv_heads", "head_dim",
+                                      "rotary_dim", "interleaved", "num_axes", "num_pages", "page_size",
+                                      "pages_per_req", "dtype", "cache_dtype", "device"))]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    """spec_verify_cache_attention_args of include/spec_verify.h."""
+    _fields_ = [*((f, _VP) for f in ("q", "k_cache", "v_cache", "out", "lse")),
+                *((f, _I64) for f in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride",
+                                      "k_page_stride", "k_slot_stride", "k_cache_head_stride",
+                                      "v_page_stride", "v_slot_stride", "v_cache_head_stride")),
+                ("page_table", _VP), ("table_stride", _I64), ("lengths", _VP), ("cu_num_draft", _VP),
+                ("k_scale", _VP), ("v_scale", _VP), ("workspace", _VP), ("workspace_bytes", _I64),
+                ("scale", ctypes.c_float),
+                *((f, _I32) for f in ("window", "num_rows", "num_reqs", "num_q_heads", "num_kv_heads",
+                                      "head_dim", "num_pages", "page_size", "pages_per_req", "dtype",
+                                      "cache_dtype", "device"))]
 
 
 SV_ERR_BATCH, SV_ERR_COUNTS, SV_ERR_BOUNDS, SV_ERR_SELECT = 1, 2, 4, 8
@@ -201,6 +234,10 @@ def lib():
     L.spec_verify_noalloc_last_error.argtypes = [ctypes.POINTER(u32)]
     L.spec_verify_sample.argtypes = [ctypes.POINTER(SampleArgs), vp]
     L.spec_verify_logprobs.argtypes = [ctypes.POINTER(LogprobsArgs), vp]
+    L.spec_verify_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), vp]
+    L.spec_verify_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), vp]
+    L.spec_verify_cache_attention_workspace.argtypes = [ctypes.POINTER(CacheAttentionArgs),
+                                                        ctypes.POINTER(i64)]
     L.spec_verify_reserve_host_io.argtypes = [vp]
     L.spec_verify_last_error.argtypes = [vp, ctypes.POINTER(u32)]
     L.spec_verify_set_profiling.argtypes = [vp, i32]
@@ -215,7 +252,8 @@ def lib():
               "spec_verify_run_batch", "spec_verify_set_synthetic", "spec_verify_synthetic_rates",
               "spec_verify_shard_stats", "spec_verify_shard_race", "spec_verify_shard_finish",
               "spec_verify_run_host", "spec_verify_run_noalloc", "spec_verify_noalloc_last_error",
-              "spec_verify_sample", "spec_verify_logprobs",
+              "spec_verify_sample", "spec_verify_logprobs", "spec_verify_cache_append",
+              "spec_verify_cache_attention", "spec_verify_cache_attention_workspace",
               "spec_verify_reserve_host_io", "spec_verify_last_error", "spec_verify_set_profiling",
               "spec_verify_get_profile", "spec_verify_set_chunks", "spec_verify_launches_per_run"):
         getattr(L, f).restype = i32
@@ -400,6 +438,24 @@ def spec_verify_sample(args: SampleArgs, cuda_stream=None) -> None:
 def spec_verify_logprobs(args: LogprobsArgs, cuda_stream=None) -> None:
     _check(lib().spec_verify_logprobs(ctypes.byref(args), _stream_handle(cuda_stream)),
            "spec_verify_logprobs")
+
+
+def spec_verify_cache_append(args: CacheAppendArgs, cuda_stream=None) -> None:
+    _check(lib().spec_verify_cache_append(ctypes.byref(args), _stream_handle(cuda_stream)),
+           "spec_verify_cache_append")
+
+
+def spec_verify_cache_attention(args: CacheAttentionArgs, cuda_stream=None) -> None:
+    _check(lib().spec_verify_cache_attention(ctypes.byref(args), _stream_handle(cuda_stream)),
+           "spec_verify_cache_attention")
+
+
+def spec_verify_cache_attention_workspace(args: CacheAttentionArgs) -> int:
+    """Bytes of workspace that spec_verify_cache_attention needs for arguments of these sizes and types."""
+    n = ctypes.c_int64()
+    _check(lib().spec_verify_cache_attention_workspace(ctypes.byref(args), ctypes.byref(n)),
+           "spec_verify_cache_attention_workspace")
+    return n.value
 
 
 def spec_verify_reserve_host_io(ctx) -> None:
@@ -590,6 +646,201 @@ def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_
                         _row_array("cu_num_draft", cu_num_draft, i32, (num_reqs + 1,), dev),
                         *at, width, num_reqs, num_top, rows, vocab, dtype, dev.index)
     spec_verify_logprobs(args, _current_stream(dev.index) if stream is None else stream)
+    return tuple(got)
+
+
+# ---- cache operators -----------------------------------------------------------------------
+
+_CODES = {}  # element types of the cache operators and their codes
+
+
+def _code(name, t) -> int:
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3})
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has the unsupported dtype {t.dtype}")
+    return code
+
+
+def _head_rows(name, t, shape, dtype, device):
+    """(address, row stride, head stride) of a [rows, heads, head_dim] device tensor whose heads are
+    contiguous, checked."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    row, head, one = t.stride()
+    at = t.data_ptr()
+    if one != 1 or at & 15 or (row & 7 and shape[0] > 1) or (head & 7 and shape[1] > 1):
+        raise ValueError(f"{name}'s heads must be contiguous, its address and strides multiples of 16 bytes")
+    return at, row, head
+
+
+def _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale, rows, heads, dim, dtype,
+             device):
+    """The arguments that the cache operators share, checked: (addresses of the caches, their strides, the
+    page table and what follows it, sizes of the pool, type codes)."""
+    import torch
+
+    i32 = torch.int32
+    if k_cache.dim() != 4 or k_cache.shape[3] != dim or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim], head_dim that of the rows")
+    if k_cache.dtype is not v_cache.dtype or (k_cache.dtype is not dtype and k_cache.dtype is not torch.float8_e4m3fn):
+        raise ValueError(f"caches have dtype {k_cache.dtype} and {v_cache.dtype}, expected {dtype} or torch.float8_e4m3fn")
+    if k_cache.device != device or v_cache.device != device:
+        raise ValueError(f"caches are on {k_cache.device} and {v_cache.device}, expected {device}")
+    strides = (*k_cache.stride(), *v_cache.stride())
+    if strides[3] != 1 or strides[7] != 1:
+        raise ValueError("the caches' heads must be contiguous")
+    if heads is not None and k_cache.shape[2] != heads:
+        raise ValueError(f"the caches hold {k_cache.shape[2]} heads, the rows {heads}")
+    n = lengths.shape[0] if lengths.dim() == 1 else -1
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError("page_table must be [num_reqs, pages], lengths [num_reqs]")
+    width = page_table.shape[1]
+    if page_table.dtype is not i32 or page_table.device != device:
+        raise ValueError(f"page_table must be int32 on {device}")
+    table_stride = page_table.stride(0) if n > 1 else width
+    if (width > 1 and page_table.stride(1) != 1) or table_stride < width:
+        raise ValueError("page_table's rows must be contiguous and must not overlap")
+    cu = None
+    if cu_num_draft is not None:
+        cu = _row_array("cu_num_draft", cu_num_draft, i32, (n + 1,), device)
+    elif rows < n:
+        raise ValueError(f"without cu_num_draft every request has a row: {n} requests, {rows} rows")
+    cache_code = _code("k_cache", k_cache)
+    if cache_code != SV_E4M3 and (k_scale is not None or v_scale is not None):
+        raise ValueError("scales belong to float8_e4m3fn caches")
+    scale_shape, f32 = (k_cache.shape[2],), torch.float32
+    return (strides[:3] + strides[4:7],
+            (page_table.data_ptr(), table_stride, _row_array("lengths", lengths, i32, (n,), device), cu),
+            (None if k_scale is None else _row_array("k_scale", k_scale, f32, scale_shape, device),
+             None if v_scale is None else _row_array("v_scale", v_scale, f32, scale_shape, device)),
+            (k_cache.shape[0], k_cache.shape[1], width), cache_code, n)
+
+
+def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_freq=None, cu_num_draft=None,
+                 positions=None, axes=None, interleaved: bool = False, k_scale=None, v_scale=None, out=None,
+                 stream=None):
+    """Append the keys and values of a step's rows to the paged cache, the keys turned by their
+    positions, and turn the queries.
+
+    k, v: [rows, kv_heads, head_dim] bfloat16 or float16 (views of one projection, say); row
+    cu_num_draft[i] + i + j is the j-th new token of request i (cu_num_draft [num_reqs + 1] int32, the
+    verification's; None: one row a request) at place lengths[i] + j ([num_reqs] int32, the tokens cached
+    before; negative: the request takes no part). k_cache, v_cache: [pages, page_size, kv_heads, head_dim]
+    in any layout whose heads are contiguous, of the rows' dtype, or float8_e4m3fn with k_scale and v_scale
+    ([kv_heads] float32: what is stored is the value divided by its head's scale) or without. page_table:
+    [num_reqs, pages_of_a_request] int32.
+
+    inv_freq ([rotary_dim / 2] float32, None: nothing is turned): the rotation of the first rotary_dim
+    elements of q's and k's heads, pair m by the angle position * inv_freq[m]; pairs are half of rotary_dim
+    apart, or neighbours with interleaved=True. The position is the row's place, or with positions
+    ([num_axes, rows] int32, or [rows]) that of axis axes[m] (a sequence of rotary_dim / 2 axis numbers;
+    None: axis 0).
+
+    Returns the turned queries [rows, q_heads, head_dim] (None without q): a new tensor, or `out`, which
+    may be q itself. Runs on k's device, on `stream` or that device's current stream. The exact rules stand
+    at spec_verify_cache_append in include/spec_verify.h."""
+    import torch
+
+    if k.dim() != 3:
+        raise ValueError("k must be [rows, kv_heads, head_dim]")
+    if not k.is_cuda:
+        raise ValueError("k must be on a CUDA device")
+    rows, hk, dim = k.shape
+    dev, dtype = k.device, k.dtype
+    code = _code("k", k)
+    if code == SV_E4M3:
+        raise ValueError(f"k has the unsupported dtype {dtype}")
+    strides, step, scales, pool, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+                                                          k_scale, v_scale, rows, hk, dim, dtype, dev)
+    kp = _head_rows("k", k, (rows, hk, dim), dtype, dev)
+    vp = _head_rows("v", v, (rows, hk, dim), dtype, dev)
+    qp = op = (None, 0, 0)
+    hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [rows, q_heads, head_dim]")
+        hq = q.shape[1]
+        qp = _head_rows("q", q, (rows, hq, dim), dtype, dev)
+        if out is None:
+            (out,) = _row_outputs(None, [("out", dtype, (rows, hq, dim))], dev, stream)
+        op = _head_rows("out", out, (rows, hq, dim), dtype, dev)
+    elif out is not None:
+        raise ValueError("out without q")
+    half = 0
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        inv_freq = _row_array("inv_freq", inv_freq, torch.float32, (half,), dev)
+    num_axes, pos, pos_stride, axis_bytes = 0, None, 0, None
+    if positions is not None:
+        if positions.dim() == 1:
+            positions = positions[None]
+        num_axes, pos_stride = positions.shape[0], rows
+        pos = _row_array("positions", positions, torch.int32, (num_axes, rows), dev)
+    if axes is not None:
+        if len(axes) != half:
+            raise ValueError(f"axes must name the axis of each of the {half} pairs")
+        axis_bytes = bytes(axes)
+    spec_verify_cache_append(
+        CacheAppendArgs(qp[0], kp[0], vp[0], op[0], k_cache.data_ptr(), v_cache.data_ptr(), qp[1], qp[2], kp[1], kp[2],
+                        vp[1], vp[2], op[1], op[2], *strides, *step, pos, pos_stride, inv_freq, *scales,
+                        axis_bytes, rows, n, hq, hk, dim, 2 * half, bool(interleaved), num_axes, *pool, code,
+                        cache_code, dev.index), _current_stream(dev.index) if stream is None else stream)
+    return out
+
+
+def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=None, scale=None, window: int = 0,
+                    k_scale=None, v_scale=None, lse: bool = False, out=None, stream=None):
+    """Attention of a step's rows over the paged cache: q [rows, q_heads, head_dim] (bfloat16 or float16,
+    head_dim 64, 128 or 256), laid out as for :func:`cache_append`, which has appended the rows' own keys
+    under the same page_table, lengths and cu_num_draft. The row at place x = lengths[i] + j sees the keys at
+    places 0 to x of its request, with window > 0 the last `window` of them; query head g reads key head
+    g // (q_heads // kv_heads). scale: the factor of q . k, head_dim ** -0.5 by default. A row that sees no key
+    (a request of negative length) gets 0.
+
+    Returns (out [rows, q_heads, head_dim] of q's dtype,), with lse=True also the logarithm of the sum of
+    exponentials, [rows, q_heads] float32 (-inf where no key is seen), with which parts of an attention can be
+    joined. out: tensors to write instead of new ones, in that order. Rows behind the last request's are left
+    as they are. Runs on q's device, on `stream` or that device's current stream; the workspace is the call's own, so
+    calls may overlap. The exact rules stand at spec_verify_cache_attention in include/spec_verify.h."""
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    if not q.is_cuda:
+        raise ValueError("q must be on a CUDA device")
+    rows, hq, dim = q.shape
+    dev, dtype = q.device, q.dtype
+    code = _code("q", q)
+    if code == SV_E4M3:
+        raise ValueError(f"q has the unsupported dtype {dtype}")
+    strides, step, scales, pool, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+                                                          k_scale, v_scale, rows, None, dim, dtype, dev)
+    hk = k_cache.shape[2]
+    if hk < 1 or hq < 1 or hq % hk:
+        raise ValueError(f"{hq} query heads are not a multiple of the caches' {hk} heads")
+    qp = _head_rows("q", q, (rows, hq, dim), dtype, dev)
+    want = [("out", dtype, (rows, hq, dim))]
+    if lse:
+        want.append(("lse", torch.float32, (rows, hq)))
+    got = _row_outputs(out, want, dev, stream)
+    op = _head_rows("out", got[0], (rows, hq, dim), dtype, dev)
+    lp = _row_array("lse", got[1], torch.float32, (rows, hq), dev) if lse else None
+    args = CacheAttentionArgs(qp[0], k_cache.data_ptr(), v_cache.data_ptr(), op[0], lp, qp[1], qp[2], op[1], op[2],
+                              *strides, *step, *scales, None, 0, dim ** -0.5 if scale is None else scale, window, rows, n,
+                              hq, hk, dim, *pool, code, cache_code, dev.index)
+    need = spec_verify_cache_attention_workspace(args)
+    if need:
+        (space,) = _row_outputs(None, [("workspace", torch.uint8, (need,))], dev, stream)
+        args.workspace, args.workspace_bytes = space.data_ptr(), need
+    spec_verify_cache_attention(args, _current_stream(dev.index) if stream is None else stream)
     return tuple(got)
 
 

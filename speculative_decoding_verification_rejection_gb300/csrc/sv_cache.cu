@@ -1,0 +1,621 @@
+// Cache operators (spec_verify_cache_append, spec_verify_cache_attention of include/spec_verify.h): the rows
+// of a step are appended to the paged cache of keys and values, turned by their positions, and attend
+// over it.
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+
+#include "sv_cache.cuh"
+
+namespace {
+
+using namespace sv_cache;
+
+// ---------------------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------------------
+// Every element is read once and written once; what is computed is a sine and cosine a pair and row (not
+// a head: a block turns all heads of a row by the same table in shared memory) and six operations a
+// pair and head, so memory bounds it.
+//
+// The angle in turns, modulo one: pos * frac(inv_freq / 2 pi) with the fraction in steps of 2^-64, one
+// 64-bit product whose upper bits wrap away exactly the whole turns. A binary32 angle of position 10^6
+// would be off by 0.03 radians.
+struct AppendParams {
+    Step s;
+    const unsigned char *q, *k, *v;
+    unsigned char *q_out;
+    i64 q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;  // bytes
+    Cache kc, vc;
+    const float *inv_freq, *k_scale, *v_scale;
+    const int32_t *positions;
+    i64 positions_stride;
+    int hq, hk, dim, half, interleaved;
+    uint32_t axes[SV_MAX_HEAD_DIM / 2 / 16];  // two bits a pair
+};
+
+constexpr int kAppendThreads = 256;
+
+// The 16 elements that a thread turns: two runs of 8 where the pairs are half a rotary dimension apart, else one run.
+struct Item {
+    int first, second;  // element of the first 8 and of the second 8
+    int pair;           // the first one's pair, -1: not turned
+};
+__device__ __forceinline__ Item item_of(int c, int half, int interleaved)
+{
+    const int e = c * 16;
+    if (e >= 2 * half) return Item{e, e + 8, -1};
+    return interleaved ? Item{e, e + 8, c * 8} : Item{c * 8, half + c * 8, c * 8};
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &w, float *x)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 p = pair_of<T>(u[k]);
+        x[2 * k] = p.x;
+        x[2 * k + 1] = p.y;
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float *x)
+{
+    return make_uint4(pack<T>(x[0], x[1]), pack<T>(x[2], x[3]), pack<T>(x[4], x[5]), pack<T>(x[6], x[7]));
+}
+// 8 values divided by their head's scale, rounded once.
+__device__ __forceinline__ uint2 pack8_e4m3(const float *x, float scale)
+{
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = e4m3_of(x[2 * k] / scale, x[2 * k + 1] / scale);
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads) sv_cache_append_kernel(const AppendParams P)
+{
+    __shared__ float2 table[2][SV_MAX_HEAD_DIM / 2];
+    const int per_head = P.dim / 16, items = (P.hq + 2 * P.hk) * per_head;
+    // this thread's pair: its share of a turn a position, in steps of 2^-64
+    u64 turn = 0;
+    bool odd = false;
+    if (threadIdx.x < P.half) {
+        const double f = static_cast<double>(ld(P.inv_freq + threadIdx.x)) * 0.15915494309189533577;  // / 2 pi
+        odd = !(fabs(f) < 1e300);
+        turn = __double2ull_rn(odd ? 0.0 : (f - floor(f)) * 18446744073709551616.0);
+    }
+    int flip = 0;
+    for (int r = blockIdx.x; r < P.s.rows; r += gridDim.x) {
+        const int i = request_of(P.s, r);
+        const int length = i < 0 ? -1 : ld(P.s.lengths + i);
+        if (length < 0) continue;  // (all threads agree)
+        int first;
+        request_rows(P.s, i, first);
+        const i64 x = static_cast<i64>(length) + (r - first);
+        i64 page = 0;
+        int slot = 0;
+        const bool kept = place(P.s, i, x, page, slot);
+        if (threadIdx.x < P.half) {
+            const int axis = P.axes[threadIdx.x / 16] >> (threadIdx.x % 16 * 2) & 3;
+            const i64 pos = P.positions ? static_cast<i64>(ld(P.positions + axis * P.positions_stride + r)) : x;
+            const int half_turns = static_cast<int>((static_cast<u64>(pos) * turn) >> 32);  // of 2^-31
+            float2 cs;
+            sincospif(static_cast<float>(half_turns) * 0x1p-31f, &cs.y, &cs.x);
+            table[flip][threadIdx.x] = odd ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)) : cs;
+        }
+        __syncthreads();  // (one a row that is turned: the next one's table is the other)
+        const float2 *turns = table[flip];
+        flip ^= 1;
+        for (int at = blockIdx.y * kAppendThreads + threadIdx.x; at < items; at += gridDim.y * kAppendThreads) {
+            const int head = at / per_head, h = head < P.hq ? head : head < P.hq + P.hk ? head - P.hq : head - P.hq - P.hk;
+            const bool is_q = head < P.hq, is_v = head >= P.hq + P.hk;
+            if (!is_q && !kept) continue;
+            Item m = item_of(at - head * per_head, P.half, P.interleaved);
+            if (is_v && m.pair >= 0) m = Item{(at - head * per_head) * 16, (at - head * per_head) * 16 + 8, -1};
+            const unsigned char *src = is_q ? P.q + r * P.q_row + h * P.q_head : is_v ? P.v + r * P.v_row + h * P.v_head : P.k + r * P.k_row + h * P.k_head;
+            const uint4 a = ld_own(reinterpret_cast<const uint4 *>(src + m.first * 2)), b = ld_own(reinterpret_cast<const uint4 *>(src + m.second * 2));
+            float u[8], w[8];
+            unpack8<T>(a, u);
+            unpack8<T>(b, w);
+            if (m.pair >= 0) {
+                const float2 *t = turns + m.pair;
+                if (P.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 c = t[e], d = t[e + 4];
+                        const float u0 = u[2 * e], u1 = u[2 * e + 1], w0 = w[2 * e], w1 = w[2 * e + 1];
+                        u[2 * e] = u0 * c.x - u1 * c.y;
+                        u[2 * e + 1] = u0 * c.y + u1 * c.x;
+                        w[2 * e] = w0 * d.x - w1 * d.y;
+                        w[2 * e + 1] = w0 * d.y + w1 * d.x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 c = t[e];
+                        const float u0 = u[e], w0 = w[e];
+                        u[e] = u0 * c.x - w0 * c.y;
+                        w[e] = u0 * c.y + w0 * c.x;
+                    }
+                }
+            }
+            if (is_q) {
+                unsigned char *to = P.q_out + r * P.out_row + h * P.out_head;
+                st(reinterpret_cast<uint4 *>(to + m.first * 2), pack8<T>(u));
+                st(reinterpret_cast<uint4 *>(to + m.second * 2), pack8<T>(w));
+                continue;
+            }
+            const Cache &c = is_v ? P.vc : P.kc;
+            unsigned char *to = c.at + page * c.page + slot * c.slot + h * c.head;
+            if constexpr (E4M3) {
+                const float *scales = is_v ? P.v_scale : P.k_scale;
+                const float scale = scales ? ld(scales + h) : 1.0f;
+                st(reinterpret_cast<uint2 *>(to + m.first), pack8_e4m3(u, scale));
+                st(reinterpret_cast<uint2 *>(to + m.second), pack8_e4m3(w, scale));
+            } else {
+                st(reinterpret_cast<uint4 *>(to + m.first * 2), pack8<T>(u));
+                st(reinterpret_cast<uint4 *>(to + m.second * 2), pack8<T>(w));
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------------------
+struct AttentionParams {
+    Step s;
+    const unsigned char *q;
+    unsigned char *out;
+    i64 q_row, q_head, out_row, out_head;  // bytes
+    Cache kc, vc;
+    const float *k_scale, *v_scale;
+    float *lse;
+    float scale;
+    int window, hq, group;
+};
+
+// One CTA a row and head, its warps every fourth key each, a running maximum and sum a warp, joined at the end.
+template <typename T, typename C, int D>
+__global__ void __launch_bounds__(128) sv_cache_attention_kernel(const AttentionParams P)
+{
+    constexpr int E = D / 32;
+    __shared__ float shared[4][D + 2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int r = blockIdx.x, head = blockIdx.y, h = head / P.group;
+    const int i = request_of(P.s, r);
+    if (i < 0) return;
+    int first;
+    request_rows(P.s, i, first);
+    const int length = ld(P.s.lengths + i);
+    const i64 x = length < 0 ? -1 : static_cast<i64>(length) + (r - first);
+    float q[E], o[E] = {}, top = -kInf, sum = 0;
+    for (int e = 0; e < E; ++e)
+        q[e] = static_cast<float>(ld(reinterpret_cast<const T *>(P.q + r * P.q_row + head * P.q_head) + lane * E + e));
+    const float scale = P.scale * (P.k_scale ? ld(P.k_scale + h) : 1.0f);
+    const i64 from = P.window > 0 && x - P.window + 1 > 0 ? x - P.window + 1 : 0;
+    for (i64 t = from + warp; t <= x && t < static_cast<i64>(P.s.width) * P.s.page; t += 4) {
+        i64 page;
+        int slot;
+        if (!place(P.s, i, t, page, slot)) continue;
+        const C *k = reinterpret_cast<const C *>(P.kc.at + page * P.kc.page + slot * P.kc.slot + h * P.kc.head) + lane * E;
+        const C *v = reinterpret_cast<const C *>(P.vc.at + page * P.vc.page + slot * P.vc.slot + h * P.vc.head) + lane * E;
+        float dot = 0;
+        for (int e = 0; e < E; ++e) dot = fmaf(q[e], static_cast<float>(ld_own(k + e)), dot);
+        for (int d = 16; d; d /= 2) dot += __shfl_xor_sync(~0u, dot, d);
+        dot *= scale;
+        if (dot == -kInf) continue;
+        const float up = fmaxf(top, dot), keep = expf(top - up), p = expf(dot - up);
+        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * static_cast<float>(ld_own(v + e));
+        sum = sum * keep + p;
+        top = up;
+    }
+    for (int e = 0; e < E; ++e) shared[warp][lane * E + e] = o[e];
+    shared[warp][D] = top;
+    shared[warp][D + 1] = sum;
+    __syncthreads();
+    float most = -kInf, z = 0;
+    for (int w = 0; w < 4; ++w) most = fmaxf(most, shared[w][D]);
+    for (int w = 0; w < 4; ++w)
+        if (shared[w][D + 1] != 0) z += shared[w][D + 1] * expf(shared[w][D] - most);
+    for (int d = threadIdx.x; d < D; d += 128) {
+        float y = 0;
+        for (int w = 0; w < 4; ++w)
+            if (shared[w][D + 1] != 0) y += shared[w][d] * expf(shared[w][D] - most);
+        y = z == 0 ? 0.0f : y / z * (P.v_scale ? ld(P.v_scale + h) : 1.0f);
+        st(reinterpret_cast<T *>(P.out + r * P.out_row + head * P.out_head) + d, static_cast<T>(y));
+    }
+    if (P.lse && threadIdx.x == 0) st(P.lse + static_cast<i64>(r) * P.hq + head, z == 0 ? -kInf : most + logf(z));
+}
+
+// ---------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------
+struct NvtxRange {
+    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+    NvtxRange(const NvtxRange &) = delete;
+    NvtxRange &operator=(const NvtxRange &) = delete;
+};
+
+// Makes `dev` current for the call.
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = true, moved = false;
+    explicit DeviceGuard(int dev)
+    {
+        if (cudaGetDevice(&prev) != cudaSuccess) {
+            ok = false;
+            return;
+        }
+        if (prev != dev) {
+            ok = cudaSetDevice(dev) == cudaSuccess;
+            moved = ok;
+        }
+    }
+    ~DeviceGuard()
+    {
+        if (moved) cudaSetDevice(prev);
+    }
+    DeviceGuard(const DeviceGuard &) = delete;
+    DeviceGuard &operator=(const DeviceGuard &) = delete;
+};
+
+constexpr int kMaxDevices = 64;
+std::mutex g_cache_mutex;
+bool g_cache_ready[kMaxDevices];
+
+// Whether `dev` is a device the kernels run on; looked up once per device.
+int cache_device(int dev)
+{
+    if (dev < 0 || dev >= kMaxDevices) return SV_EDEVICE;
+    std::lock_guard<std::mutex> lock(g_cache_mutex);
+    if (g_cache_ready[dev]) return SV_OK;
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SV_EDEVICE;
+    }
+    if (major != 10 || minor != 3) return SV_EDEVICE;  // built for sm_103a only
+    g_cache_ready[dev] = true;
+    return SV_OK;
+}
+
+bool misaligned(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+using wide = __int128;
+
+// An array of up to three strided dimensions of whole heads.
+struct View {
+    const void *at;
+    int64_t size[3], stride[3];  // elements
+    int inner, elem;
+
+    // Strides that are whole vectors, none negative, and no offset beyond 2^62 bytes.
+    bool sound() const
+    {
+        wide last = inner;
+        for (int d = 0; d < 3; ++d) {
+            if (size[d] <= 1) continue;
+            if (stride[d] < 0 || stride[d] % (16 / elem) != 0) return false;
+            last += static_cast<wide>(size[d] - 1) * stride[d];
+        }
+        return last * elem < (static_cast<wide>(1) << 62);
+    }
+    int64_t bytes() const
+    {
+        int64_t last = inner;
+        for (int d = 0; d < 3; ++d)
+            if (size[d] > 1) last += (size[d] - 1) * stride[d];
+        return last * elem;
+    }
+    // No two elements share memory (each stride reaches over all that is within it).
+    bool distinct() const
+    {
+        int order[3] = {0, 1, 2};
+        std::sort(order, order + 3, [this](int a, int b) { return stride[a] < stride[b]; });
+        wide extent = inner;
+        for (int d : order) {
+            if (size[d] <= 1) continue;
+            if (stride[d] < extent) return false;
+            extent += static_cast<wide>(size[d] - 1) * stride[d];
+        }
+        return true;
+    }
+};
+
+// The first address of a dimension is all there is where its size is 1: its stride is not looked at.
+int64_t stride_of(int64_t size, int64_t stride, int elem) { return size > 1 ? stride * elem : 0; }
+
+int elem_bytes(int dtype) { return dtype == SV_E4M3 ? 1 : 2; }
+
+#ifdef SV_DEBUG_BOUNDS
+// The arrays of one call, registered in g_spans (in stream order) before its launch. The environment
+// variable SV_DEBUG_SHRINK leaves that many bytes of the end of the first (the cached keys) out, so
+// that tests can check that the check fires on memory that is there.
+struct SpanList {
+    Spans l{};
+    void add(const void *p, bool in, bool out, int64_t bytes)
+    {
+        if (p && bytes > 0 && l.n < kSpans) l.s[l.n++] = Span{reinterpret_cast<u64>(p), static_cast<u64>(bytes), in, out};
+    }
+    int push(cudaStream_t stream)
+    {
+        if (const char *e = getenv("SV_DEBUG_SHRINK")) l.s[0].bytes -= std::min<u64>(strtoull(e, nullptr, 10), l.s[0].bytes);
+        return cudaMemcpyToSymbolAsync(g_spans, &l, sizeof(l), 0, cudaMemcpyHostToDevice, stream) == cudaSuccess ? SV_OK : SV_ECUDA;
+    }
+};
+
+template <typename Args>
+void add_step(SpanList &s, const Args &a)
+{
+    s.add(a.page_table, true, false, ((a.num_reqs - 1) * (a.num_reqs > 1 ? a.table_stride : 0) + a.pages_per_req) * 4);
+    s.add(a.lengths, true, false, a.num_reqs * 4ll);
+    s.add(a.cu_num_draft, true, false, (a.num_reqs + 1) * 4ll);
+    s.add(a.k_scale, true, false, a.num_kv_heads * 4ll);
+    s.add(a.v_scale, true, false, a.num_kv_heads * 4ll);
+}
+#endif
+
+// What both entry points ask of the step and the caches. head_dim is checked by the caller.
+template <typename Args>
+int check_step(const Args &a, View &k, View &v)
+{
+    if (a.dtype != SV_BF16 && a.dtype != SV_F16) return SV_EDTYPE;
+    if (a.cache_dtype != a.dtype && a.cache_dtype != SV_E4M3) return SV_EDTYPE;
+    if (a.num_rows < 0 || a.num_reqs < 0 || a.num_kv_heads < 1 || a.num_pages < 0 || a.page_size < 1 || a.pages_per_req < 0) return SV_EINVAL;
+    if (a.page_size > SV_MAX_PAGE) return SV_ECAPACITY;
+    if (a.cache_dtype != SV_E4M3 && (a.k_scale || a.v_scale)) return SV_EINVAL;
+    const int elem = elem_bytes(a.cache_dtype);
+    k = View{a.k_cache, {a.num_pages, a.page_size, a.num_kv_heads}, {a.k_page_stride, a.k_slot_stride, a.k_cache_head_stride}, a.head_dim, elem};
+    v = View{a.v_cache, {a.num_pages, a.page_size, a.num_kv_heads}, {a.v_page_stride, a.v_slot_stride, a.v_cache_head_stride}, a.head_dim, elem};
+    if (!k.sound() || !v.sound()) return SV_EINVAL;
+    if (a.num_rows == 0 || a.num_reqs == 0) return SV_OK;
+    if (!a.lengths || (a.pages_per_req > 0 && !a.page_table) || (a.num_pages > 0 && (!a.k_cache || !a.v_cache))) return SV_EINVAL;
+    if (a.num_reqs > 1 && (a.table_stride < a.pages_per_req || a.table_stride > (1ll << 40))) return SV_EINVAL;
+    for (const void *p : {static_cast<const void *>(a.page_table), static_cast<const void *>(a.lengths), static_cast<const void *>(a.cu_num_draft),
+                          static_cast<const void *>(a.k_scale), static_cast<const void *>(a.v_scale)})
+        if (misaligned(p, 4)) return SV_EINVAL;
+    if (misaligned(a.k_cache, 16) || misaligned(a.v_cache, 16)) return SV_EINVAL;
+    return SV_OK;
+}
+
+template <typename Args>
+Step step_of(const Args &a)
+{
+    return Step{a.page_table, a.lengths, a.cu_num_draft, a.num_reqs > 1 ? a.table_stride : 0, a.num_reqs, a.num_rows, a.num_pages, a.page_size,
+                a.pages_per_req, ((u64{1} << 42) + static_cast<u64>(a.page_size) - 1) / static_cast<u64>(a.page_size)};
+}
+
+Cache cache_of(const View &v)
+{
+    return Cache{static_cast<unsigned char *>(const_cast<void *>(v.at)), stride_of(v.size[0], v.stride[0], v.elem),
+                 stride_of(v.size[1], v.stride[1], v.elem), stride_of(v.size[2], v.stride[2], v.elem)};
+}
+
+// Rows of heads: [rows, heads, head_dim] of 16-bit elements.
+View rows_of(const void *at, int rows, int heads, int64_t row, int64_t head, int dim) { return View{at, {rows, heads, 1}, {row, head, 0}, dim, 2}; }
+
+int status_of(cudaError_t e)
+{
+    if (e == cudaSuccess) return SV_OK;
+    cudaGetLastError();
+    return SV_ECUDA;
+}
+
+template <typename T, typename C>
+void launch_attention(const AttentionParams &P, int dim, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(P.s.rows), static_cast<unsigned>(P.hq));
+    if (dim == 64)
+        sv_cache_attention_kernel<T, C, 64><<<grid, 128, 0, stream>>>(P);
+    else if (dim == 128)
+        sv_cache_attention_kernel<T, C, 128><<<grid, 128, 0, stream>>>(P);
+    else
+        sv_cache_attention_kernel<T, C, 256><<<grid, 128, 0, stream>>>(P);
+}
+
+// What an attention call asks beyond its step; the workspace it needs.
+int check_attention(const spec_verify_cache_attention_args &a, View &k, View &v, int64_t &workspace)
+{
+    workspace = 0;
+    if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return SV_EINVAL;
+    const int rc = check_step(a, k, v);
+    if (rc != SV_OK) return rc;
+    if (a.num_q_heads < 1 || a.num_q_heads % a.num_kv_heads != 0 || a.num_q_heads > 65535 || a.window < 0 || !std::isfinite(a.scale)) return SV_EINVAL;
+    return SV_OK;
+}
+
+}  // namespace
+
+extern "C" int spec_verify_cache_append(const spec_verify_cache_append_args *a, void *cuda_stream)
+{
+    const NvtxRange nvtx("spec_verify_cache_append");
+    if (!a) return SV_EINVAL;
+    if (a->head_dim < 16 || a->head_dim % 16 != 0 || a->rotary_dim < 0 || a->rotary_dim % 16 != 0 || a->rotary_dim > a->head_dim) return SV_EINVAL;
+    if (a->head_dim > SV_MAX_HEAD_DIM) return SV_ECAPACITY;
+    View kc, vc;
+    const int rc = check_step(*a, kc, vc);
+    if (rc != SV_OK) return rc;
+    if (!kc.distinct() || !vc.distinct() || a->num_q_heads < 0) return SV_EINVAL;
+    if (a->num_pages > 0 && a->k_cache == a->v_cache) return SV_EINVAL;
+    if (a->rotary_dim > 0 && (!a->inv_freq || misaligned(a->inv_freq, 4))) return SV_EINVAL;
+    if (a->positions && (a->num_axes < 1 || misaligned(a->positions, 4) || (a->num_axes > 1 && a->positions_stride < a->num_rows))) return SV_EINVAL;
+    if (a->positions && a->num_axes > SV_MAX_AXES) return SV_ECAPACITY;
+    if (a->axes && !a->positions) return SV_EINVAL;
+    AppendParams P;
+    memset(P.axes, 0, sizeof(P.axes));
+    for (int m = 0; a->axes && m < a->rotary_dim / 2; ++m) {
+        if (a->axes[m] >= a->num_axes) return SV_EINVAL;
+        P.axes[m / 16] |= static_cast<uint32_t>(a->axes[m]) << (m % 16 * 2);
+    }
+    const int D = a->head_dim;
+    const View q = rows_of(a->q, a->num_rows, a->num_q_heads, a->q_row_stride, a->q_head_stride, D);
+    const View out = rows_of(a->q_out, a->num_rows, a->num_q_heads, a->q_out_row_stride, a->q_out_head_stride, D);
+    const View k = rows_of(a->k, a->num_rows, a->num_kv_heads, a->k_row_stride, a->k_head_stride, D);
+    const View v = rows_of(a->v, a->num_rows, a->num_kv_heads, a->v_row_stride, a->v_head_stride, D);
+    if (!q.sound() || !out.sound() || (a->num_q_heads > 0 && !out.distinct()) || !k.sound() || !v.sound()) return SV_EINVAL;
+    if (a->num_rows == 0 || a->num_reqs == 0) return SV_OK;
+    if (!a->k || !a->v || (a->num_q_heads > 0 && (!a->q || !a->q_out))) return SV_EINVAL;
+    for (const void *p : {a->q, a->k, a->v, static_cast<const void *>(a->q_out)})
+        if (misaligned(p, 16)) return SV_EINVAL;
+    // in place means every element in its own place
+    if (a->q == a->q_out && ((a->num_rows > 1 && a->q_row_stride != a->q_out_row_stride) || (a->num_q_heads > 1 && a->q_head_stride != a->q_out_head_stride)))
+        return SV_EINVAL;
+    const int rd = cache_device(a->device);
+    if (rd != SV_OK) return rd;
+    const DeviceGuard guard(a->device);
+    if (!guard.ok) return SV_EDEVICE;
+    P.s = step_of(*a);
+    P.q = static_cast<const unsigned char *>(a->q);
+    P.k = static_cast<const unsigned char *>(a->k);
+    P.v = static_cast<const unsigned char *>(a->v);
+    P.q_out = static_cast<unsigned char *>(a->q_out);
+    P.q_row = stride_of(a->num_rows, a->q_row_stride, 2);
+    P.q_head = stride_of(a->num_q_heads, a->q_head_stride, 2);
+    P.k_row = stride_of(a->num_rows, a->k_row_stride, 2);
+    P.k_head = stride_of(a->num_kv_heads, a->k_head_stride, 2);
+    P.v_row = stride_of(a->num_rows, a->v_row_stride, 2);
+    P.v_head = stride_of(a->num_kv_heads, a->v_head_stride, 2);
+    P.out_row = stride_of(a->num_rows, a->q_out_row_stride, 2);
+    P.out_head = stride_of(a->num_q_heads, a->q_out_head_stride, 2);
+    P.kc = cache_of(kc);
+    P.vc = cache_of(vc);
+    P.inv_freq = a->inv_freq;
+    P.k_scale = a->k_scale;
+    P.v_scale = a->v_scale;
+    P.positions = a->positions;
+    P.positions_stride = a->num_axes > 1 ? a->positions_stride : 0;
+    P.hq = a->num_q_heads;
+    P.hk = a->num_kv_heads;
+    P.dim = D;
+    P.half = a->rotary_dim / 2;
+    P.interleaved = a->interleaved;
+    const auto stream = static_cast<cudaStream_t>(cuda_stream);
+#ifdef SV_DEBUG_BOUNDS
+    SpanList s;
+    s.add(a->k_cache, false, true, kc.bytes());
+    s.add(a->v_cache, false, true, vc.bytes());
+    if (a->num_q_heads) {
+        s.add(a->q, true, false, q.bytes());
+        s.add(a->q_out, false, true, out.bytes());
+    }
+    s.add(a->k, true, false, k.bytes());
+    s.add(a->v, true, false, v.bytes());
+    s.add(a->inv_freq, true, false, a->rotary_dim * 2ll);
+    s.add(a->positions, true, false, ((a->num_axes - 1) * P.positions_stride + a->num_rows) * 4);
+    add_step(s, *a);
+    if (s.push(stream) != SV_OK) return SV_ECUDA;
+#endif
+    const int items = (P.hq + 2 * P.hk) * (D / 16), parts = (items + kAppendThreads - 1) / kAppendThreads;
+    const int per_row = a->num_rows < 2 * 152 ? parts : 1;
+    const dim3 grid(static_cast<unsigned>(std::min(a->num_rows, 8 * 152)), static_cast<unsigned>(std::min(per_row, 65535)));
+    if (a->dtype == SV_BF16) {
+        if (a->cache_dtype == SV_E4M3)
+            sv_cache_append_kernel<__nv_bfloat16, true><<<grid, kAppendThreads, 0, stream>>>(P);
+        else
+            sv_cache_append_kernel<__nv_bfloat16, false><<<grid, kAppendThreads, 0, stream>>>(P);
+    } else {
+        if (a->cache_dtype == SV_E4M3)
+            sv_cache_append_kernel<__half, true><<<grid, kAppendThreads, 0, stream>>>(P);
+        else
+            sv_cache_append_kernel<__half, false><<<grid, kAppendThreads, 0, stream>>>(P);
+    }
+    return status_of(cudaGetLastError());
+}
+
+extern "C" int spec_verify_cache_attention_workspace(const spec_verify_cache_attention_args *a, int64_t *bytes)
+{
+    if (!a || !bytes) return SV_EINVAL;
+    spec_verify_cache_attention_args sizes = *a;  // (the sizes alone: no address is looked at)
+    sizes.num_rows = 0;
+    View k, v;
+    int64_t none;
+    const int rc = a->num_rows < 0 ? SV_EINVAL : check_attention(sizes, k, v, none);
+    *bytes = 0;
+    return rc;
+}
+
+extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_args *a, void *cuda_stream)
+{
+    const NvtxRange nvtx("spec_verify_cache_attention");
+    if (!a) return SV_EINVAL;
+    View kc, vc;
+    int64_t workspace;
+    const int rc = check_attention(*a, kc, vc, workspace);
+    if (rc != SV_OK) return rc;
+    const View q = rows_of(a->q, a->num_rows, a->num_q_heads, a->q_row_stride, a->q_head_stride, a->head_dim);
+    const View out = rows_of(a->out, a->num_rows, a->num_q_heads, a->out_row_stride, a->out_head_stride, a->head_dim);
+    if (!q.sound() || !out.sound() || !out.distinct()) return SV_EINVAL;
+    if (a->num_rows == 0 || a->num_reqs == 0) return SV_OK;
+    if (!a->q || !a->out || a->q == a->out || misaligned(a->q, 16) || misaligned(a->out, 16) || misaligned(a->lse, 4)) return SV_EINVAL;
+    if (a->workspace_bytes < workspace || (workspace > 0 && !a->workspace) || misaligned(a->workspace, 16)) return SV_EINVAL;
+    const int rd = cache_device(a->device);
+    if (rd != SV_OK) return rd;
+    const DeviceGuard guard(a->device);
+    if (!guard.ok) return SV_EDEVICE;
+    AttentionParams P;
+    P.s = step_of(*a);
+    P.q = static_cast<const unsigned char *>(a->q);
+    P.out = static_cast<unsigned char *>(a->out);
+    P.q_row = stride_of(a->num_rows, a->q_row_stride, 2);
+    P.q_head = stride_of(a->num_q_heads, a->q_head_stride, 2);
+    P.out_row = stride_of(a->num_rows, a->out_row_stride, 2);
+    P.out_head = stride_of(a->num_q_heads, a->out_head_stride, 2);
+    P.kc = cache_of(kc);
+    P.vc = cache_of(vc);
+    P.k_scale = a->k_scale;
+    P.v_scale = a->v_scale;
+    P.lse = a->lse;
+    P.scale = a->scale;
+    P.window = a->window;
+    P.hq = a->num_q_heads;
+    P.group = a->num_q_heads / a->num_kv_heads;
+    const auto stream = static_cast<cudaStream_t>(cuda_stream);
+#ifdef SV_DEBUG_BOUNDS
+    SpanList s;
+    s.add(a->k_cache, true, false, kc.bytes());
+    s.add(a->v_cache, true, false, vc.bytes());
+    s.add(a->q, true, false, q.bytes());
+    s.add(a->out, false, true, out.bytes());
+    s.add(a->lse, false, true, static_cast<int64_t>(a->num_rows) * a->num_q_heads * 4);
+    s.add(a->workspace, true, true, a->workspace_bytes);
+    add_step(s, *a);
+    if (s.push(stream) != SV_OK) return SV_ECUDA;
+#endif
+    if (a->dtype == SV_BF16) {
+        if (a->cache_dtype == SV_E4M3)
+            launch_attention<__nv_bfloat16, __nv_fp8_e4m3>(P, a->head_dim, stream);
+        else
+            launch_attention<__nv_bfloat16, __nv_bfloat16>(P, a->head_dim, stream);
+    } else {
+        if (a->cache_dtype == SV_E4M3)
+            launch_attention<__half, __nv_fp8_e4m3>(P, a->head_dim, stream);
+        else
+            launch_attention<__half, __half>(P, a->head_dim, stream);
+    }
+    return status_of(cudaGetLastError());
+}
+
+#ifdef SV_DEBUG_BOUNDS
+// Of the checked build only: SV_ERR_BOUNDS in *word if a kernel of a cache operator that has ended tried an
+// access outside its call's arrays (the current device's; read and cleared).
+extern "C" int spec_verify_cache_outside(uint32_t *word)
+{
+    const unsigned zero = 0;
+    if (!word) return SV_EINVAL;
+    return cudaMemcpyFromSymbol(word, g_outside, sizeof(*word)) == cudaSuccess &&
+                   cudaMemcpyToSymbol(g_outside, &zero, sizeof(zero)) == cudaSuccess
+               ? SV_OK
+               : SV_ECUDA;
+}
+#endif
