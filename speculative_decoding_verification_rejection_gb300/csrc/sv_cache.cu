@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "sv_cache.cuh"
+#include "sv_cache_attention.cuh"
 
 namespace {
 
@@ -169,74 +170,6 @@ __global__ void __launch_bounds__(kAppendThreads) sv_cache_append_kernel(const A
 }
 
 // ---------------------------------------------------------------------------------------
-// attention
-// ---------------------------------------------------------------------------------------
-struct AttentionParams {
-    Step s;
-    const unsigned char *q;
-    unsigned char *out;
-    i64 q_row, q_head, out_row, out_head;  // bytes
-    Cache kc, vc;
-    const float *k_scale, *v_scale;
-    float *lse;
-    float scale;
-    int window, hq, group;
-};
-
-// One CTA a row and head, its warps every fourth key each, a running maximum and sum a warp, joined at the end.
-template <typename T, typename C, int D>
-__global__ void __launch_bounds__(128) sv_cache_attention_kernel(const AttentionParams P)
-{
-    constexpr int E = D / 32;
-    __shared__ float shared[4][D + 2];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int r = blockIdx.x, head = blockIdx.y, h = head / P.group;
-    const int i = request_of(P.s, r);
-    if (i < 0) return;
-    int first;
-    request_rows(P.s, i, first);
-    const int length = ld(P.s.lengths + i);
-    const i64 x = length < 0 ? -1 : static_cast<i64>(length) + (r - first);
-    float q[E], o[E] = {}, top = -kInf, sum = 0;
-    for (int e = 0; e < E; ++e)
-        q[e] = static_cast<float>(ld(reinterpret_cast<const T *>(P.q + r * P.q_row + head * P.q_head) + lane * E + e));
-    const float scale = P.scale * (P.k_scale ? ld(P.k_scale + h) : 1.0f);
-    const i64 from = P.window > 0 && x - P.window + 1 > 0 ? x - P.window + 1 : 0;
-    for (i64 t = from + warp; t <= x && t < static_cast<i64>(P.s.width) * P.s.page; t += 4) {
-        i64 page;
-        int slot;
-        if (!place(P.s, i, t, page, slot)) continue;
-        const C *k = reinterpret_cast<const C *>(P.kc.at + page * P.kc.page + slot * P.kc.slot + h * P.kc.head) + lane * E;
-        const C *v = reinterpret_cast<const C *>(P.vc.at + page * P.vc.page + slot * P.vc.slot + h * P.vc.head) + lane * E;
-        float dot = 0;
-        for (int e = 0; e < E; ++e) dot = fmaf(q[e], static_cast<float>(ld_own(k + e)), dot);
-        for (int d = 16; d; d /= 2) dot += __shfl_xor_sync(~0u, dot, d);
-        dot *= scale;
-        if (dot == -kInf) continue;
-        const float up = fmaxf(top, dot), keep = expf(top - up), p = expf(dot - up);
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * static_cast<float>(ld_own(v + e));
-        sum = sum * keep + p;
-        top = up;
-    }
-    for (int e = 0; e < E; ++e) shared[warp][lane * E + e] = o[e];
-    shared[warp][D] = top;
-    shared[warp][D + 1] = sum;
-    __syncthreads();
-    float most = -kInf, z = 0;
-    for (int w = 0; w < 4; ++w) most = fmaxf(most, shared[w][D]);
-    for (int w = 0; w < 4; ++w)
-        if (shared[w][D + 1] != 0) z += shared[w][D + 1] * expf(shared[w][D] - most);
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float y = 0;
-        for (int w = 0; w < 4; ++w)
-            if (shared[w][D + 1] != 0) y += shared[w][d] * expf(shared[w][D] - most);
-        y = z == 0 ? 0.0f : y / z * (P.v_scale ? ld(P.v_scale + h) : 1.0f);
-        st(reinterpret_cast<T *>(P.out + r * P.out_row + head * P.out_head) + d, static_cast<T>(y));
-    }
-    if (P.lse && threadIdx.x == 0) st(P.lse + static_cast<i64>(r) * P.hq + head, z == 0 ? -kInf : most + logf(z));
-}
-
-// ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
 struct NvtxRange {
@@ -269,6 +202,42 @@ struct DeviceGuard {
     DeviceGuard &operator=(const DeviceGuard &) = delete;
 };
 
+// One kernel of the attention: what it needs, and how it is launched.
+struct Kernel {
+    const void *run, *join;
+    int rows, tokens, threads, resident, bytes, dim;
+    float offset;
+};
+
+template <bool BF16, int ES, int D, int RG, int MT>
+Kernel kernel_of()
+{
+    using S = Tile<ES, D, RG, MT>;
+    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<BF16, ES, D, RG, MT>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>),
+                  S::rows, S::tokens, S::threads, S::resident, S::bytes, D, BF16 ? 0.0f : 15.0f};
+}
+
+template <bool BF16, int ES, int D>
+Kernel kernel_of(int tiles)
+{
+    if constexpr (D == 256)
+        return tiles == 1 ? kernel_of<BF16, ES, D, 1, 1>() : kernel_of<BF16, ES, D, 2, 1>();
+    else
+        return tiles == 1 ? kernel_of<BF16, ES, D, 1, 1>() : tiles == 2 ? kernel_of<BF16, ES, D, 2, 1>()
+             : tiles == 3 ? kernel_of<BF16, ES, D, 3, 1>() : kernel_of<BF16, ES, D, 2, 2>();
+}
+
+template <bool BF16, int ES>
+Kernel kernel_of(int dim, int tiles)
+{
+    return dim == 64 ? kernel_of<BF16, ES, 64>(tiles) : dim == 128 ? kernel_of<BF16, ES, 128>(tiles) : kernel_of<BF16, ES, 256>(tiles);
+}
+
+Kernel kernel_of(int cache_dtype, int dim, int tiles)
+{
+    return cache_dtype == SV_BF16 ? kernel_of<true, 2>(dim, tiles) : cache_dtype == SV_F16 ? kernel_of<false, 2>(dim, tiles) : kernel_of<false, 1>(dim, tiles);
+}
+
 constexpr int kMaxDevices = 64;
 std::mutex g_cache_mutex;
 bool g_cache_ready[kMaxDevices];
@@ -286,6 +255,17 @@ int cache_device(int dev)
         return SV_EDEVICE;
     }
     if (major != 10 || minor != 3) return SV_EDEVICE;  // built for sm_103a only
+    const DeviceGuard guard(dev);
+    if (!guard.ok) return SV_EDEVICE;
+    for (int cache : {SV_BF16, SV_F16, SV_E4M3})
+        for (int dim : {64, 128, 256})
+            for (int tiles = 1; tiles <= 4; ++tiles) {
+                const Kernel k = kernel_of(cache, dim, tiles);
+                if (cudaFuncSetAttribute(k.run, cudaFuncAttributeMaxDynamicSharedMemorySize, k.bytes) != cudaSuccess) {
+                    cudaGetLastError();
+                    return SV_ECUDA;
+                }
+            }
     g_cache_ready[dev] = true;
     return SV_OK;
 }
@@ -311,6 +291,7 @@ struct View {
         }
         return last * elem < (static_cast<wide>(1) << 62);
     }
+#ifdef SV_DEBUG_BOUNDS
     int64_t bytes() const
     {
         int64_t last = inner;
@@ -318,6 +299,7 @@ struct View {
             if (size[d] > 1) last += (size[d] - 1) * stride[d];
         return last * elem;
     }
+#endif
     // No two elements share memory (each stride reaches over all that is within it).
     bool distinct() const
     {
@@ -412,26 +394,40 @@ int status_of(cudaError_t e)
     return SV_ECUDA;
 }
 
-template <typename T, typename C>
-void launch_attention(const AttentionParams &P, int dim, cudaStream_t stream)
+// The kernel for a call. Query rows of a key head of one request (on average: the rows of each are known on the device
+// only) in tiles of 16: as few tiles over the keys as there can be, of as few rows.
+Kernel kernel_for(const spec_verify_cache_attention_args &a)
 {
-    const dim3 grid(static_cast<unsigned>(P.s.rows), static_cast<unsigned>(P.hq));
-    if (dim == 64)
-        sv_cache_attention_kernel<T, C, 64><<<grid, 128, 0, stream>>>(P);
-    else if (dim == 128)
-        sv_cache_attention_kernel<T, C, 128><<<grid, 128, 0, stream>>>(P);
-    else
-        sv_cache_attention_kernel<T, C, 256><<<grid, 128, 0, stream>>>(P);
+    const int most = a.head_dim == 256 ? 2 : 4;
+    const i64 rows = (static_cast<i64>(a.num_rows) + std::max(a.num_reqs, 1) - 1) / std::max(a.num_reqs, 1) * (a.num_q_heads / a.num_kv_heads);
+    const i64 tiles = std::max<i64>(1, (rows + 15) / 16), passes = (tiles + most - 1) / most;
+    return kernel_of(a.cache_dtype, a.head_dim, static_cast<int>((tiles + passes - 1) / passes));
 }
 
-// What an attention call asks beyond its step; the workspace it needs.
-int check_attention(const spec_verify_cache_attention_args &a, View &k, View &v, int64_t &workspace)
+// How many CTAs a call has: those that the device holds at once, or as many as there can be tiles.
+i64 ctas_for(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
-    workspace = 0;
+    const i64 groups = (a.num_reqs + static_cast<i64>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) / k.rows) * a.num_kv_heads;
+    const i64 tiles = std::max<i64>(1, (static_cast<i64>(a.pages_per_req) * a.page_size + k.tokens - 1) / k.tokens);
+    return std::min<i64>(152 * k.resident, groups > (1 << 20) || tiles > (1 << 20) ? 1 << 20 : groups * tiles);
+}
+
+// Whether groups may have to be joined: not where each has one tile.
+bool joins(const spec_verify_cache_attention_args &a, const Kernel &k) { return static_cast<i64>(a.pages_per_req) * a.page_size > k.tokens; }
+
+int64_t workspace_of(const spec_verify_cache_attention_args &a, const Kernel &k)
+{
+    return joins(a, k) ? ctas_for(a, k) * (2ll * k.rows * (k.dim + 2) * 4 + static_cast<int64_t>(sizeof(Part))) : 0;
+}
+
+// What an attention call asks beyond its step.
+int check_attention(const spec_verify_cache_attention_args &a, View &k, View &v)
+{
     if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return SV_EINVAL;
     const int rc = check_step(a, k, v);
     if (rc != SV_OK) return rc;
-    if (a.num_q_heads < 1 || a.num_q_heads % a.num_kv_heads != 0 || a.num_q_heads > 65535 || a.window < 0 || !std::isfinite(a.scale)) return SV_EINVAL;
+    if (a.num_q_heads < 1 || a.num_q_heads % a.num_kv_heads != 0 || a.window < 0 || !std::isfinite(a.scale)) return SV_EINVAL;
+    if (static_cast<int64_t>(a.pages_per_req) * a.page_size > kMaxPlace) return SV_ECAPACITY;
     return SV_OK;
 }
 
@@ -539,9 +535,8 @@ extern "C" int spec_verify_cache_attention_workspace(const spec_verify_cache_att
     spec_verify_cache_attention_args sizes = *a;  // (the sizes alone: no address is looked at)
     sizes.num_rows = 0;
     View k, v;
-    int64_t none;
-    const int rc = a->num_rows < 0 ? SV_EINVAL : check_attention(sizes, k, v, none);
-    *bytes = 0;
+    const int rc = a->num_rows < 0 ? SV_EINVAL : check_attention(sizes, k, v);
+    *bytes = rc == SV_OK && a->num_rows > 0 && a->num_reqs > 0 ? workspace_of(*a, kernel_for(*a)) : 0;
     return rc;
 }
 
@@ -550,14 +545,15 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     const NvtxRange nvtx("spec_verify_cache_attention");
     if (!a) return SV_EINVAL;
     View kc, vc;
-    int64_t workspace;
-    const int rc = check_attention(*a, kc, vc, workspace);
+    const int rc = check_attention(*a, kc, vc);
     if (rc != SV_OK) return rc;
     const View q = rows_of(a->q, a->num_rows, a->num_q_heads, a->q_row_stride, a->q_head_stride, a->head_dim);
     const View out = rows_of(a->out, a->num_rows, a->num_q_heads, a->out_row_stride, a->out_head_stride, a->head_dim);
     if (!q.sound() || !out.sound() || !out.distinct()) return SV_EINVAL;
     if (a->num_rows == 0 || a->num_reqs == 0) return SV_OK;
     if (!a->q || !a->out || a->q == a->out || misaligned(a->q, 16) || misaligned(a->out, 16) || misaligned(a->lse, 4)) return SV_EINVAL;
+    const Kernel kernel = kernel_for(*a);
+    const int64_t workspace = workspace_of(*a, kernel);
     if (a->workspace_bytes < workspace || (workspace > 0 && !a->workspace) || misaligned(a->workspace, 16)) return SV_EINVAL;
     const int rd = cache_device(a->device);
     if (rd != SV_OK) return rd;
@@ -576,10 +572,16 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     P.k_scale = a->k_scale;
     P.v_scale = a->v_scale;
     P.lse = a->lse;
-    P.scale = a->scale;
+    P.scale = a->scale * kLog2e;
     P.window = a->window;
     P.hq = a->num_q_heads;
+    P.hk = a->num_kv_heads;
     P.group = a->num_q_heads / a->num_kv_heads;
+    P.bf16 = a->dtype == SV_BF16;
+    const i64 ctas = ctas_for(*a, kernel);
+    P.sums = static_cast<float *>(workspace ? a->workspace : nullptr);
+    P.stats = workspace ? reinterpret_cast<float2 *>(P.sums + ctas * 2 * kernel.rows * kernel.dim) : nullptr;
+    P.parts = workspace ? reinterpret_cast<Part *>(P.stats + ctas * 2 * kernel.rows) : nullptr;
     const auto stream = static_cast<cudaStream_t>(cuda_stream);
 #ifdef SV_DEBUG_BOUNDS
     SpanList s;
@@ -592,18 +594,25 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     add_step(s, *a);
     if (s.push(stream) != SV_OK) return SV_ECUDA;
 #endif
-    if (a->dtype == SV_BF16) {
-        if (a->cache_dtype == SV_E4M3)
-            launch_attention<__nv_bfloat16, __nv_fp8_e4m3>(P, a->head_dim, stream);
-        else
-            launch_attention<__nv_bfloat16, __nv_bfloat16>(P, a->head_dim, stream);
-    } else {
-        if (a->cache_dtype == SV_E4M3)
-            launch_attention<__half, __nv_fp8_e4m3>(P, a->head_dim, stream);
-        else
-            launch_attention<__half, __half>(P, a->head_dim, stream);
-    }
-    return status_of(cudaGetLastError());
+    void *params[] = {&P};
+    if (cudaLaunchKernel(kernel.run, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(kernel.threads)), params,
+                         static_cast<size_t>(kernel.bytes), stream) != cudaSuccess)
+        return status_of(cudaErrorLaunchFailure);
+    if (!workspace) return SV_OK;
+    // the join's CTAs start while the attention's end, and wait for them on the device
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int rows = kernel.rows;
+    float offset = kernel.offset;
+    void *join[] = {&P, &rows, &offset};
+    return status_of(cudaLaunchKernelExC(&cfg, kernel.join, join));
 }
 
 #ifdef SV_DEBUG_BOUNDS
