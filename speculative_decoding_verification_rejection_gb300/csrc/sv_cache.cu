@@ -13,6 +13,7 @@
 
 #include "sv_cache.cuh"
 #include "sv_cache_attention.cuh"
+#include "sv_cache_tensor.cuh"
 
 namespace {
 
@@ -207,6 +208,7 @@ struct Kernel {
     const void *run, *join;
     int rows, tokens, threads, resident, bytes, dim;
     float offset;
+    bool tensor;  // (with tensor maps)
 };
 
 template <bool BF16, int ES, int D, int RG, int MT>
@@ -214,7 +216,7 @@ Kernel kernel_of()
 {
     using S = Tile<ES, D, RG, MT>;
     return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<BF16, ES, D, RG, MT>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>),
-                  S::rows, S::tokens, S::threads, S::resident, S::bytes, D, BF16 ? 0.0f : 15.0f};
+                  S::rows, S::tokens, S::threads, S::resident, S::bytes, D, BF16 ? 0.0f : 15.0f, false};
 }
 
 template <bool BF16, int ES, int D>
@@ -227,20 +229,41 @@ Kernel kernel_of(int tiles)
              : tiles == 3 ? kernel_of<BF16, ES, D, 3, 1>() : kernel_of<BF16, ES, D, 2, 2>();
 }
 
-template <bool BF16, int ES>
-Kernel kernel_of(int dim, int tiles)
+template <bool BF16, int D, int N>
+Kernel tensor_kernel_of()
 {
-    return dim == 64 ? kernel_of<BF16, ES, 64>(tiles) : dim == 128 ? kernel_of<BF16, ES, 128>(tiles) : kernel_of<BF16, ES, 256>(tiles);
+    using S = Tensor<D, N>;
+    return Kernel{reinterpret_cast<const void *>(sv_cache_tensor_kernel<BF16, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>),
+                  S::rows, S::tokens, S::threads, 1, S::bytes, D, Weights<BF16>::offset, true};
+}
+
+template <bool BF16, int D>
+Kernel tensor_kernel_of(int tiles)
+{
+    if constexpr (D == 256)
+        return tiles == 1 ? tensor_kernel_of<BF16, D, 16>() : tensor_kernel_of<BF16, D, 32>();
+    else
+        return tiles == 1 ? tensor_kernel_of<BF16, D, 16>() : tiles == 2 ? tensor_kernel_of<BF16, D, 32>()
+             : tiles == 3 ? tensor_kernel_of<BF16, D, 48>() : tensor_kernel_of<BF16, D, 64>();
+}
+
+template <bool BF16>
+Kernel tensor_kernel_of(int dim, int tiles)
+{
+    return dim == 64 ? tensor_kernel_of<BF16, 64>(tiles) : dim == 128 ? tensor_kernel_of<BF16, 128>(tiles) : tensor_kernel_of<BF16, 256>(tiles);
 }
 
 Kernel kernel_of(int cache_dtype, int dim, int tiles)
 {
-    return cache_dtype == SV_BF16 ? kernel_of<true, 2>(dim, tiles) : cache_dtype == SV_F16 ? kernel_of<false, 2>(dim, tiles) : kernel_of<false, 1>(dim, tiles);
+    if (cache_dtype == SV_BF16) return tensor_kernel_of<true>(dim, tiles);
+    if (cache_dtype == SV_F16) return tensor_kernel_of<false>(dim, tiles);
+    return dim == 64 ? kernel_of<false, 1, 64>(tiles) : dim == 128 ? kernel_of<false, 1, 128>(tiles) : kernel_of<false, 1, 256>(tiles);
 }
 
 constexpr int kMaxDevices = 64;
 std::mutex g_cache_mutex;
 bool g_cache_ready[kMaxDevices];
+decltype(&cuTensorMapEncodeTiled) g_encode;
 
 // Whether `dev` is a device the kernels run on; looked up once per device.
 int cache_device(int dev)
@@ -266,6 +289,15 @@ int cache_device(int dev)
                     return SV_ECUDA;
                 }
             }
+    if (!g_encode) {
+        cudaDriverEntryPointQueryResult found;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess || found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return SV_ECUDA;
+        }
+        g_encode = reinterpret_cast<decltype(g_encode)>(f);
+    }
     g_cache_ready[dev] = true;
     return SV_OK;
 }
@@ -386,6 +418,29 @@ Cache cache_of(const View &v)
 
 // Rows of heads: [rows, heads, head_dim] of 16-bit elements.
 View rows_of(const void *at, int rows, int heads, int64_t row, int64_t head, int dim) { return View{at, {rows, heads, 1}, {row, head, 0}, dim, 2}; }
+
+// The tensor map of an array of heads, [size2][size1][size0][inner] of 16-bit elements, for copies of boxes of 64 elements
+// by `box` of the first dimension.
+int map_of(CUtensorMap &map, bool bf16, const View &v, int box)
+{
+    const cuuint64_t sizes[4] = {static_cast<cuuint64_t>(v.inner), static_cast<cuuint64_t>(v.size[0]), static_cast<cuuint64_t>(v.size[1]), static_cast<cuuint64_t>(v.size[2])};
+    cuuint64_t strides[3];
+    for (int d = 0; d < 3; ++d) strides[d] = static_cast<cuuint64_t>(v.size[d] > 1 ? v.stride[d] : v.inner) * 2;
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+    return g_encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(v.at), sizes, strides, boxes, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SV_OK
+               : SV_ECUDA;
+}
+
+// Whether copies by tensor map can walk it: every stride in use above 0 and below 2^40 bytes.
+bool walkable(const View &v)
+{
+    for (int d = 0; d < 3; ++d)
+        if (v.size[d] > 1 && (v.stride[d] < 1 || v.stride[d] * v.elem >= (1ll << 40))) return false;
+    return true;
+}
 
 int status_of(cudaError_t e)
 {
@@ -549,7 +604,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     if (rc != SV_OK) return rc;
     const View q = rows_of(a->q, a->num_rows, a->num_q_heads, a->q_row_stride, a->q_head_stride, a->head_dim);
     const View out = rows_of(a->out, a->num_rows, a->num_q_heads, a->out_row_stride, a->out_head_stride, a->head_dim);
-    if (!q.sound() || !out.sound() || !out.distinct()) return SV_EINVAL;
+    if (!q.sound() || !out.sound() || !out.distinct() || !walkable(q) || !walkable(kc) || !walkable(vc)) return SV_EINVAL;
     if (a->num_rows == 0 || a->num_reqs == 0) return SV_OK;
     if (!a->q || !a->out || a->q == a->out || misaligned(a->q, 16) || misaligned(a->out, 16) || misaligned(a->lse, 4)) return SV_EINVAL;
     const Kernel kernel = kernel_for(*a);
@@ -594,7 +649,21 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     add_step(s, *a);
     if (s.push(stream) != SV_OK) return SV_ECUDA;
 #endif
-    void *params[] = {&P};
+    TensorMaps maps;
+    int box = 1;
+    if (kernel.tensor) {
+        while (box < kernel.tokens && a->page_size % (2 * box) == 0) box *= 2;
+        const bool bf16 = a->cache_dtype == SV_BF16;
+        // (sizes of the map: slots, heads, pages; of the queries heads, rows. Without a page nothing of the map is looked at)
+        auto turned = [&](const View &c) {
+            View v{a->num_pages ? c.at : a->q, {c.size[1], c.size[2], c.size[0]}, {c.stride[1], c.stride[2], c.stride[0]}, c.inner, 2};
+            if (!a->num_pages) v.size[0] = v.size[1] = v.size[2] = 1;
+            return v;
+        };
+        const View queries{a->q, {a->num_q_heads, a->num_rows, 1}, {a->q_head_stride, a->q_row_stride, 0}, a->head_dim, 2};
+        if (map_of(maps.k, bf16, turned(kc), box) != SV_OK || map_of(maps.v, bf16, turned(vc), box) != SV_OK || map_of(maps.q, bf16, queries, 1) != SV_OK) return SV_ECUDA;
+    }
+    void *params[] = {&P, &maps, &box};
     if (cudaLaunchKernel(kernel.run, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(kernel.threads)), params,
                          static_cast<size_t>(kernel.bytes), stream) != cudaSuccess)
         return status_of(cudaErrorLaunchFailure);

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(Tile<ES, D, RG, MT>::threads, Tile<ES, D, RG, 
     // Weights are rounded to the products' type relative to 1 (bf16) or 2^15 (binary16, whose smallest step
     // is then 2^-39 of the largest weight: without it 60000 weights of 2^-26 would be lost).
     constexpr float kOffset = BF16 ? 0.0f : 15.0f;
-    extern __shared__ __align__(128) unsigned char room[];
+    extern __shared__ __align__(1024) unsigned char room[];
     auto &sh = *reinterpret_cast<typename S::Shared *>(room + S::stages * S::stage + S::q_bytes);
     const uint32_t stages_at = shared_address(room);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;

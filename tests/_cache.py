@@ -150,8 +150,9 @@ def ref_attention(s: Step, *, scale=None, window=0):
             out[r, o], lse[r, o] = y, z
             many = (n / 8 + 32) * 2.0**-22
             oe[r, o] = size * (weight + 2 * off[:, None] + 2 * many) * 1.01 + y.abs() * HALF[s.dtype] * 1.01 + smallest(s.dtype)
-            # weights below the smallest step of binary16, 2^-39 of the row's largest
-            oe[r, o] += v.abs().sum(0) * abs(vs) * 2.0**-38 * p.amax(1, keepdim=True)
+            # binary16 weights are held 11 doublings above the reference, itself at most the row's largest: half their
+            # smallest step, 2^-24, is 2^-36 of that
+            oe[r, o] += v.abs().sum(0) * abs(vs) * 2.0**-36 * p.amax(1, keepdim=True)
             le[r, o] = off + many + 2.0**-22 * z.abs()
     return (out, lse), (oe, le)
 

@@ -70,7 +70,7 @@ def test_append_refuses(change, status):
     (dict(num_q_heads=0), sv.SV_EINVAL), (dict(window=-1), sv.SV_EINVAL), (dict(scale=float("nan")), sv.SV_EINVAL),
     (dict(scale=float("inf")), sv.SV_EINVAL), (dict(out=None), sv.SV_EINVAL), (dict(out=P), sv.SV_EINVAL), (dict(out=P + 4), sv.SV_EINVAL),
     (dict(lse=P + 2), sv.SV_EINVAL), (dict(lse=None), sv.SV_EDEVICE), (dict(workspace=P + 8), sv.SV_EINVAL),
-    (dict(out_head_stride=32), sv.SV_EINVAL), (dict(out_row_stride=0), sv.SV_EINVAL), (dict(k_page_stride=0), sv.SV_EDEVICE),
+    (dict(out_head_stride=32), sv.SV_EINVAL), (dict(out_row_stride=0), sv.SV_EINVAL), (dict(k_page_stride=0), sv.SV_EINVAL), (dict(q_row_stride=0), sv.SV_EINVAL),
 ])
 def test_attention_refuses(change, status):
     assert sv.lib().spec_verify_cache_attention(ctypes.byref(attention_args(**change)), None) == status
