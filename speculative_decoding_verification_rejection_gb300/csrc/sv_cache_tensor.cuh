@@ -11,8 +11,8 @@ namespace sv_cache {
 // A tile is 128 keys. Both products have the keys or the elements in the 128 rows of the tensor cores' memory and
 // the query rows (N, 16 to 64) in its columns: scores^T = K Q^T, and out^T += V^T weights^T. So few query rows
 // waste nothing, and every key is read from shared memory once for all of them. Roles: four warps for the weights (a
-// thread has one key's scores of all rows), one thread that issues the products, one warp that reads the page
-// table and issues the copies.
+// thread has one key's scores of all rows), one thread that issues the products, one warp that goes through the tiles
+// and the page table ahead of the others, one that copies keys and queries and one that copies values.
 template <int D, int N>
 struct Tensor {
     static constexpr int tokens = 128;
@@ -21,22 +21,24 @@ struct Tensor {
     static constexpr int slot = tokens * D * 2;      // keys or values of a tile
     static constexpr int q_bytes = N * D * 2;
     static constexpr int weights = tokens * N * 2;
-    static constexpr int q_buffers = D == 256 && N > 16 ? 1 : 2;
-    static constexpr int fit = (229376 - q_buffers * q_bytes - 2 * weights) / slot;
-    static constexpr int slots = fit > 10 ? 10 : fit;
-    static constexpr int heads = 8;                  // descriptions of tiles that are kept
+    static constexpr int q_buffers = D == 256 && N > 16 || N == 64 ? 1 : 2;
+    static constexpr int heads = D == 256 && N > 16 ? 3 : 8;  // descriptions of tiles that are kept
+    static constexpr int fit = (heads == 8 ? 225800 : 229376) - q_buffers * q_bytes - 2 * weights;
+    static constexpr int slots = fit / slot > 12 ? 12 : fit / slot;
+    static constexpr int k_slots = slots / 2, v_slots = slots - slots / 2;  // rings of their own: each has one warp that fills it
     static constexpr int blocks = D == 256 ? 2 : 1;  // of 128 elements
     static constexpr int columns_used = (2 + blocks) * N;
     static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
-    static constexpr int threads = 192;
-    static_assert(slots >= 3 && columns_used <= 256 && slots / 2 + 3 <= heads, "room");
+    static constexpr int threads = 256;
+    static_assert(slots >= 2 && columns_used <= 256, "room");
     struct Head {
         int p0, first, count, from, row0, head, length, flags;
-        int part_first, part_last, part_slot, q_buffer;
+        int part_first, part_last, part_slot, segment;
         uint32_t seen[4];
+        int page[tokens];  // of each box
     };
     struct Shared {
-        u64 full[slots], empty[slots], scores[2], weighed[2], done[2], q_empty[2];
+        u64 k_full[k_slots], k_empty[k_slots], v_full[v_slots], v_empty[v_slots], scores[2], weighed[2], done[2], q_empty[2], told[heads], used[heads];
         Head head[heads];
         alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
         alignas(16) float top[N];     // the reference, times log2 e
@@ -178,7 +180,7 @@ struct Weights {
 };
 
 template <bool BF16, int D, int N>
-__global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps, const int box)
+__global__ void __launch_bounds__(256, 1) sv_cache_tensor_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps, const int box)
 {
     using S = Tensor<D, N>;
     using E = std::conditional_t<BF16, __nv_bfloat16, __half>;
@@ -193,8 +195,10 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
 
     // -- this CTA's tiles, barriers, memory
     if (tid == 0) {
-        for (int k = 0; k < S::slots; ++k) barrier_init(sh.full + k, 1), barrier_init(sh.empty + k, 1);
+        for (int k = 0; k < S::k_slots; ++k) barrier_init(sh.k_full + k, 1), barrier_init(sh.k_empty + k, 1);
+        for (int k = 0; k < S::v_slots; ++k) barrier_init(sh.v_full + k, 1), barrier_init(sh.v_empty + k, 1);
         for (int k = 0; k < 2; ++k) barrier_init(sh.scores + k, 1), barrier_init(sh.weighed + k, 128), barrier_init(sh.done + k, 1), barrier_init(sh.q_empty + k, 1);
+        for (int k = 0; k < S::heads; ++k) barrier_init(sh.told + k, 1), barrier_init(sh.used + k, 1);
         sh.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         shared_to_async();
@@ -246,112 +250,115 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
     int *const lost = &sh.lost;
 
     if (warp == 5) {
-        // -- copies: descriptions of the tiles, keys and values by boxes of `box` places (which divides the page), queries
+        // -- descriptions of the tiles: this lane has places lane, 32 + lane, ... of each
         walk.seek(static_cast<int>(sh.start[0]), sh.start[1], u0);
         int segment = -1;
-        for (int it = 0; it < n; ++it) {
-            const Range range = walk.range;
-            const int p0 = walk.t * S::tokens, boxes = S::tokens / box;
-            // this lane's boxes, at most four
-            int page[4], slot[4];
-            uint32_t whole = 0;  // of the 128 places those in a page that is there and seen by some row: bits of this lane's boxes
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int p = p0 + (x * 32 + lane) * box;
-                page[x] = P.s.pages;
-                slot[x] = 0;
-                if (x * 32 + lane < boxes && walk.rows && p < range.end && p + box > range.start) {
-                    const int c = p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * P.s.page_magic) >> 42) : p / P.s.page;
-                    slot[x] = p - c * P.s.page;
-                    int pg = ld(P.s.table + walk.i * P.s.table_stride + c);
-#ifdef SV_DEBUG_BOUNDS
-                    for (int r = 0; r < box && pg >= 0 && pg < P.s.pages; ++r)
-                        if (!inside(P.kc.at + pg * P.kc.page + (slot[x] + r) * P.kc.slot + walk.head * P.kc.head, D * 2, false) ||
-                            !inside(P.vc.at + pg * P.vc.page + (slot[x] + r) * P.vc.slot + walk.head * P.vc.head, D * 2, false))
-                            pg = -1;
-#endif
-                    if (pg >= 0 && pg < P.s.pages) page[x] = pg, whole |= 1u << x;
-                }
-            }
-            const bool opens = walk.t == range.t0, ends = walk.t + 1 == range.t1;
-            const bool first = it == 0 || opens, last = it == n - 1 || ends;
-            // places of the tile that some row sees: those of the boxes that are there, from start to end
-            uint32_t seen[4];
+        int page[4];
+        auto look_up = [&] {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t bits = 0;
-                if (box >= 32) {
-                    const int b = w * 32 / box;  // (one box or less in 32 places)
-                    bits = __shfl_sync(~0u, whole, b & 31) >> (b >> 5) & 1 ? ~0u : 0;
-                } else {
-                    const int in = 32 / box;  // boxes in 32 places
-                    for (int b = 0; b < in; ++b) {
-                        const int all = w * in + b;
-                        if (__shfl_sync(~0u, whole, all & 31) >> (all >> 5) & 1) bits |= ((1u << box) - 1) << (b * box);
-                    }
+                const int p = walk.t * S::tokens + w * 32 + lane;
+                // (all places of a box that some row sees a place of)
+                const int in = p & ~(box - 1);
+                page[w] = -1;
+                if (walk.rows && in < walk.range.end && in + box > walk.range.start) {
+                    const int c = p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * P.s.page_magic) >> 42) : p / P.s.page;
+                    page[w] = ld(P.s.table + walk.i * P.s.table_stride + c);
+#ifdef SV_DEBUG_BOUNDS
+                    const int pg = page[w], slot = p - c * P.s.page;
+                    if (pg >= 0 && pg < P.s.pages)
+                        inside(P.kc.at + pg * P.kc.page + slot * P.kc.slot + walk.head * P.kc.head, D * 2, false),
+                            inside(P.vc.at + pg * P.vc.page + slot * P.vc.slot + walk.head * P.vc.head, D * 2, false);
+#endif
                 }
-                const int lo = range.start - p0 - w * 32, hi = range.end - p0 - w * 32;  // bits lo to hi - 1
-                const uint32_t from = lo <= 0 ? ~0u : lo >= 32 ? 0u : ~0u << lo, to = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
-                seen[w] = bits & from & to;
             }
+        };
+        look_up();
+        for (int it = 0; it < n; ++it) {
+            const int k = it % S::heads;
+            if (it >= S::heads) barrier_wait(sh.used + k, (it / S::heads - 1) & 1, lost);
+            auto &h = sh.head[k];
+            const int p0 = walk.t * S::tokens;
+            bool all = true;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int p = p0 + w * 32 + lane;
+                const bool there = page[w] >= 0 && page[w] < P.s.pages;
+                const uint32_t seen = __ballot_sync(~0u, there && p >= walk.range.start && p < walk.range.end);
+                all = all && seen == ~0u;
+                if (lane == 0) h.seen[w] = seen;
+                if ((p & (box - 1)) == 0) h.page[(w * 32 + lane) / box] = there ? page[w] : P.s.pages;  // (a page behind the last: zeros)
+            }
+            const bool opens = walk.t == walk.range.t0, ends = walk.t + 1 == walk.range.t1;
+            const bool first = it == 0 || opens, last = it == n - 1 || ends;
             if (first) ++segment;
-            const int qb = segment % S::q_buffers;
-            // room for the keys (what frees it also frees this tile's description)
-            const int o = 2 * it, ks = o % S::slots, vs = (o + 1) % S::slots;
-            if (o >= S::slots) barrier_wait(sh.empty + ks, (o / S::slots - 1) & 1, lost);
             if (lane == 0) {
-                auto &h = sh.head[it % S::heads];
                 const int j0 = walk.from / P.group, j1 = (walk.from + walk.count - 1) / P.group;
                 const bool part = walk.base < u0 || walk.base + walk.tiles() > u1;
-                const bool all = (seen[0] & seen[1] & seen[2] & seen[3]) == ~0u && static_cast<i64>(p0) + S::tokens - 1 <= static_cast<i64>(walk.length) + j0 &&
-                                 (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
+                all = all && static_cast<i64>(p0) + S::tokens - 1 <= static_cast<i64>(walk.length) + j0 &&
+                      (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
                 h.p0 = p0;
                 h.first = walk.first;
                 h.count = walk.count;
                 h.from = walk.from;
                 h.head = walk.head;
                 h.length = walk.length;
-                h.q_buffer = qb;
+                h.segment = segment;
                 h.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (part ? kPartial : 0) | (walk.base > u0 ? kSlot : 0) | (last && !ends ? kOpen : 0) | (all ? 0 : kEdge);
                 if (last && !ends) {  // the CTAs that have tiles of the group
                     h.part_first = static_cast<int>(((walk.base + 1) * ctas - 1) / total);
                     h.part_last = static_cast<int>(((walk.base + walk.tiles()) * ctas - 1) / total);
                     h.part_slot = total * h.part_first / ctas < walk.base;
                 }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) h.seen[w] = seen[w];
-                barrier_expect(sh.full + ks, S::slot + (first ? S::q_bytes : 0));
             }
             __syncwarp();
-            auto boxes_to = [&](const CUtensorMap *map, int s) {
-                for (int x = 0; x * 32 < boxes; ++x) {
-                    const int b = x * 32 + lane;
-                    const int pg = x == 0 ? page[0] : x == 1 ? page[1] : x == 2 ? page[2] : page[3], sl = x == 0 ? slot[0] : x == 1 ? slot[1] : x == 2 ? slot[2] : slot[3];
-                    if (b < boxes)
-                        for (int e = 0; e < S::halves; ++e)
-                            copy_box(room_at + s * S::slot + e * (S::tokens * 128) + b * box * 128, map, sh.full + s, e * 64, sl, walk.head, pg);
-                }
-            };
-            boxes_to(&maps.k, ks);
-            if (first) {
+            if (lane == 0) barrier_arrive(sh.told + k);
+            walk.next();
+            if (it + 1 < n) look_up();
+        }
+    } else if (warp >= 6) {
+        // -- copies: keys (and queries) or values, by boxes of `box` places, a power of two that divides the page
+        const bool values = warp == 7;
+        const CUtensorMap *const map = values ? &maps.v : &maps.k;
+        const int boxes = S::tokens / box;
+        const int slots = values ? S::v_slots : S::k_slots;
+        u64 *const fulls = values ? sh.v_full : sh.k_full, *const empties = values ? sh.v_empty : sh.k_empty;
+        const uint32_t ring = room_at + (values ? S::k_slots * S::slot : 0);
+        int s = 0;
+        uint32_t turn = 0;  // times the ring has been gone round, as the parity waited for
+        for (int it = 0; it < n; ++it) {
+            const int k = it % S::heads;
+            u64 *const full = fulls + s;
+            barrier_wait(sh.told + k, it / S::heads & 1, lost);
+            const auto &h = sh.head[k];
+            const int flags = h.flags, head = h.head, p0 = h.p0;
+            if (it >= slots) barrier_wait(empties + s, turn ^ 1, lost);
+            if (lane == 0) barrier_expect(full, S::slot + (flags & kFirst && !values ? S::q_bytes : 0));
+            __syncwarp();
+            for (int b = lane; b < boxes; b += 32) {
+                const int p = p0 + b * box, c = p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * P.s.page_magic) >> 42) : p / P.s.page;
+                const int page = h.page[b];
+#pragma unroll
+                for (int e = 0; e < S::halves; ++e)
+                    copy_box(ring + s * S::slot + e * (S::tokens * 128) + b * box * 128, map, full, e * 64, p - c * P.s.page, head, page);
+            }
+            if (flags & kFirst && !values) {
+                const int segment = h.segment, qb = segment % S::q_buffers, from = h.from, count = h.count, first = h.first;
                 if (segment >= S::q_buffers) barrier_wait(sh.q_empty + qb, (segment / S::q_buffers - 1) & 1, lost);
                 __syncwarp();
                 for (int r = lane; r < N; r += 32) {
-                    const int at_row = walk.from + r, j = at_row / P.group;
-                    const int row = r < walk.count ? walk.first + j : P.s.rows;  // (a row behind the last: zeros)
+                    const int at_row = from + r, j = at_row / P.group;
+                    const int row = r < count ? first + j : P.s.rows;  // (a row behind the last: zeros)
+#pragma unroll
                     for (int e = 0; e < S::halves; ++e)
-                        copy_row(q_at + qb * S::q_bytes + e * (N * 128) + r * 128, &maps.q, sh.full + ks, e * 64, walk.head * P.group + at_row - j * P.group, row);
+                        copy_row(q_at + qb * S::q_bytes + e * (N * 128) + r * 128, &maps.q, full, e * 64, head * P.group + at_row - j * P.group, row);
                 }
             }
-            if (o + 1 >= S::slots) barrier_wait(sh.empty + vs, ((o + 1) / S::slots - 1) & 1, lost);
-            if (lane == 0) barrier_expect(sh.full + vs, S::slot);
-            __syncwarp();
-            boxes_to(&maps.v, vs);
-            walk.next();
+            if (++s == slots) s = 0, turn ^= 1;
         }
         if (*reinterpret_cast<volatile int *>(lost))  // copies in flight end before the block does
-            for (int o = max(0, 2 * n - S::slots); o < 2 * n; ++o)
-                for (int k = 0; k < kPatience && !barrier_try(sh.full + o % S::slots, o / S::slots & 1); ++k) {
+            for (int it = max(0, n - slots); it < n; ++it)
+                for (int k = 0; k < kPatience && !barrier_try(fulls + it % slots, it / slots & 1); ++k) {
                 }
     } else if (warp == 4) {
         // -- products
@@ -359,30 +366,30 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
             constexpr uint32_t kScores = product_of(BF16, N, false), kOut = product_of(BF16, N, true);
             int qb = 0;
             auto scores = [&](int it) {
-                const int o = 2 * it, s = o % S::slots;
-                barrier_wait(sh.full + s, o / S::slots & 1, lost);
+                const int s = it % S::k_slots;
+                barrier_wait(sh.k_full + s, it / S::k_slots & 1, lost);
                 tensor_after();
                 const auto &h = sh.head[it % S::heads];
                 const int flags = h.flags;
-                qb = h.q_buffer;
+                qb = h.segment % S::q_buffers;
                 const uint32_t k_at = room_at + s * S::slot, qa = q_at + qb * S::q_bytes;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     product(tensor + (it & 1) * N, matrix_at(k_at + k / 4 * (S::tokens * 128) + k % 4 * 32, 16, 1024, 2),
                             matrix_at(qa + k / 4 * (N * 128) + k % 4 * 32, 16, 1024, 2), kScores, k > 0);
                 products_close(sh.scores + (it & 1));
-                products_close(sh.empty + s);
+                products_close(sh.k_empty + s);
                 if (flags & kLast) products_close(sh.q_empty + qb);
             };
             scores(0);
             for (int it = 0; it < n; ++it) {
                 if (it + 1 < n) scores(it + 1);
-                const int o = 2 * it + 1, s = o % S::slots, b = it & 1;
+                const int s = it % S::v_slots, b = it & 1;
                 barrier_wait(sh.weighed + b, it >> 1 & 1, lost);
-                barrier_wait(sh.full + s, o / S::slots & 1, lost);
+                barrier_wait(sh.v_full + s, it / S::v_slots & 1, lost);
                 tensor_after();
                 const bool first = sh.head[it % S::heads].flags & kFirst;
-                const uint32_t v_at = room_at + s * S::slot, wa = w_at + b * S::weights;
+                const uint32_t v_at = room_at + (S::k_slots + s) * S::slot, wa = w_at + b * S::weights;
                 // 64 elements of 8 keys are 1024 bytes; the next 64 elements are a piece further (with 64 in all: the same again,
                 // into rows of the memory that nobody reads)
 #pragma unroll
@@ -392,7 +399,8 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
                         product(tensor + (2 + e) * N, matrix_at(v_at + e * 2 * (S::tokens * 128) + k * 2048, D == 64 ? 0 : S::tokens * 128, 1024, 2),
                                 matrix_at(wa + k * 256, 128, 2048, 0), kOut, k > 0 || !first);
                 products_close(sh.done + b);
-                products_close(sh.empty + s);
+                products_close(sh.v_empty + s);
+                products_close(sh.used + it % S::heads);
             }
         }
         __syncwarp();
@@ -403,6 +411,7 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
         float scale = 0;
         for (int it = 0; it < n; ++it) {
             const int b = it & 1;
+            barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
             barrier_wait(sh.scores + b, it >> 1 & 1, lost);
             tensor_after();
             const auto &h = sh.head[it % S::heads];
@@ -425,9 +434,9 @@ __global__ void __launch_bounds__(192, 1) sv_cache_tensor_kernel(const Attention
                 if (!(h.seen[tid / 32] >> (tid & 31) & 1)) r_hi = 0;
                 // A weight of 0 times a value that is not finite would be NaN. Such elements, if any, are set to 0 in shared
                 // memory, and what they make of the rows that see them is added by hand.
-                const int vo = 2 * it + 1, vslot = vo % S::slots;
-                barrier_wait(sh.full + vslot, vo / S::slots & 1, lost);
-                unsigned char *const v = room + vslot * S::slot;
+                const int vslot = it % S::v_slots;
+                barrier_wait(sh.v_full + vslot, it / S::v_slots & 1, lost);
+                unsigned char *const v = room + (S::k_slots + vslot) * S::slot;
                 auto chunk = [&](int key, int c) { return reinterpret_cast<uint4 *>(v + c / 8 * (S::tokens * 128) + key * 128 + ((c & 7 ^ key & 7) << 4)); };
                 constexpr uint32_t mask = BF16 ? 0x7f80u : 0x7c00u;
                 bool odd = false;

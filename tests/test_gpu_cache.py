@@ -154,6 +154,34 @@ def test_attention_many_requests(n):
     check_attention(s)
 
 
+@pytest.mark.parametrize("dim,hq,hk", ((256, 8, 1), (256, 16, 1), (128, 8, 1), (128, 12, 1), (128, 16, 1), (64, 24, 1)))
+@pytest.mark.parametrize("cache", ("bf16", "e4m3"))
+def test_attention_long_runs_of_tiles(dim, hq, hk, cache):
+    """Hundreds of tiles of many requests for every CTA: rings of copies that go round many times."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    n, page, width = 96, 32, 100
+    g = torch.Generator(device="cuda").manual_seed(dim + hq)
+    pages = torch.randn(300, page, hk, dim, generator=g, device="cuda")
+    k, v = pages.to(TYPES[cache]), pages.flip(0).to(TYPES[cache])
+    table = torch.randint(0, 300, (n, width), generator=g, device="cuda").int()
+    lengths = torch.randint(0, 3100, (n,), generator=g, device="cuda").int()
+    lengths[::7] = torch.arange(14, device="cuda").int()
+    new = 4
+    cu = torch.arange(n + 1, device="cuda").int() * (new - 1)
+    q = torch.randn(n * new, hq, dim, generator=g, device="cuda").bfloat16()
+    for _ in range(3):
+        out, lse = sv.cache_attention(q, k, v, table, lengths, cu_num_draft=cu, lse=True)
+    kk, vv = (c[table.long()].float().view(n, -1, dim).double() for c in (k, v))
+    score = torch.einsum("nrhd,ntd->nrht", q.view(n, new, hq, dim).double(), kk) * dim ** -0.5
+    seen = torch.arange(width * page, device="cuda") <= lengths[:, None, None].long() + torch.arange(new, device="cuda")[:, None]
+    score.masked_fill_(~seen[:, :, None], -float("inf"))
+    want = torch.einsum("nrht,ntd->nrhd", torch.softmax(score, -1), vv)
+    # the largest value's weights off by one rounding of 16 bits (2^-8), the output's likewise
+    assert float((out.view(n, new, hq, dim).double() - want).abs().max()) <= float(vv.abs().max()) * 2.0**-7
+    assert float((lse.view(n, new, hq).double() - torch.logsumexp(score, -1)).abs().max()) <= 1e-4   # (scores up to 10, 2^-22 each of 128 products)
+
+
 @pytest.mark.parametrize("scale", (0.0, -0.3, 1e-20, 2.0))
 def test_attention_scale(scale):
     check_attention(Step(5, [100, 3], [2, 5], dim=128), scale=scale)
