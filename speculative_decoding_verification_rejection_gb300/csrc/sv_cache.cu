@@ -13,7 +13,6 @@
 
 #include "sv_cache.cuh"
 #include "sv_cache_attention.cuh"
-#include "sv_cache_tensor.cuh"
 
 namespace {
 
@@ -206,58 +205,36 @@ struct DeviceGuard {
 // One kernel of the attention: what it needs, and how it is launched.
 struct Kernel {
     const void *run, *join;
-    int rows, tokens, threads, resident, bytes, dim;
+    int rows, bytes, dim;
     float offset;
-    bool tensor;  // (with tensor maps)
 };
 
-template <bool BF16, int ES, int D, int RG, int MT>
+template <int KIND, int D, int N>
 Kernel kernel_of()
 {
-    using S = Tile<ES, D, RG, MT>;
-    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<BF16, ES, D, RG, MT>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>),
-                  S::rows, S::tokens, S::threads, S::resident, S::bytes, D, BF16 ? 0.0f : 15.0f, false};
+    using S = Tile<KIND, D, N>;
+    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<KIND, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>), N, S::bytes, D,
+                  Weights<S::bf16>::offset};
 }
 
-template <bool BF16, int ES, int D>
-Kernel kernel_of(int tiles)
+template <int KIND, int D>
+Kernel kernel_of(int rows)
 {
     if constexpr (D == 256)
-        return tiles == 1 ? kernel_of<BF16, ES, D, 1, 1>() : kernel_of<BF16, ES, D, 2, 1>();
+        return rows == 16 ? kernel_of<KIND, D, 16>() : kernel_of<KIND, D, 32>();
     else
-        return tiles == 1 ? kernel_of<BF16, ES, D, 1, 1>() : tiles == 2 ? kernel_of<BF16, ES, D, 2, 1>()
-             : tiles == 3 ? kernel_of<BF16, ES, D, 3, 1>() : kernel_of<BF16, ES, D, 2, 2>();
+        return rows == 16 ? kernel_of<KIND, D, 16>() : rows == 32 ? kernel_of<KIND, D, 32>() : rows == 48 ? kernel_of<KIND, D, 48>() : kernel_of<KIND, D, 64>();
 }
 
-template <bool BF16, int D, int N>
-Kernel tensor_kernel_of()
+template <int KIND>
+Kernel kernel_of(int dim, int rows)
 {
-    using S = Tensor<D, N>;
-    return Kernel{reinterpret_cast<const void *>(sv_cache_tensor_kernel<BF16, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>),
-                  S::rows, S::tokens, S::threads, 1, S::bytes, D, Weights<BF16>::offset, true};
+    return dim == 64 ? kernel_of<KIND, 64>(rows) : dim == 128 ? kernel_of<KIND, 128>(rows) : kernel_of<KIND, 256>(rows);
 }
 
-template <bool BF16, int D>
-Kernel tensor_kernel_of(int tiles)
+Kernel kernel_of(int cache_dtype, int dim, int rows)
 {
-    if constexpr (D == 256)
-        return tiles == 1 ? tensor_kernel_of<BF16, D, 16>() : tensor_kernel_of<BF16, D, 32>();
-    else
-        return tiles == 1 ? tensor_kernel_of<BF16, D, 16>() : tiles == 2 ? tensor_kernel_of<BF16, D, 32>()
-             : tiles == 3 ? tensor_kernel_of<BF16, D, 48>() : tensor_kernel_of<BF16, D, 64>();
-}
-
-template <bool BF16>
-Kernel tensor_kernel_of(int dim, int tiles)
-{
-    return dim == 64 ? tensor_kernel_of<BF16, 64>(tiles) : dim == 128 ? tensor_kernel_of<BF16, 128>(tiles) : tensor_kernel_of<BF16, 256>(tiles);
-}
-
-Kernel kernel_of(int cache_dtype, int dim, int tiles)
-{
-    if (cache_dtype == SV_BF16) return tensor_kernel_of<true>(dim, tiles);
-    if (cache_dtype == SV_F16) return tensor_kernel_of<false>(dim, tiles);
-    return dim == 64 ? kernel_of<false, 1, 64>(tiles) : dim == 128 ? kernel_of<false, 1, 128>(tiles) : kernel_of<false, 1, 256>(tiles);
+    return cache_dtype == SV_BF16 ? kernel_of<SV_BF16>(dim, rows) : cache_dtype == SV_F16 ? kernel_of<SV_F16>(dim, rows) : kernel_of<SV_E4M3>(dim, rows);
 }
 
 constexpr int kMaxDevices = 64;
@@ -282,8 +259,8 @@ int cache_device(int dev)
     if (!guard.ok) return SV_EDEVICE;
     for (int cache : {SV_BF16, SV_F16, SV_E4M3})
         for (int dim : {64, 128, 256})
-            for (int tiles = 1; tiles <= 4; ++tiles) {
-                const Kernel k = kernel_of(cache, dim, tiles);
+            for (int rows = 16; rows <= 64; rows += 16) {
+                const Kernel k = kernel_of(cache, dim, rows);
                 if (cudaFuncSetAttribute(k.run, cudaFuncAttributeMaxDynamicSharedMemorySize, k.bytes) != cudaSuccess) {
                     cudaGetLastError();
                     return SV_ECUDA;
@@ -456,23 +433,62 @@ Kernel kernel_for(const spec_verify_cache_attention_args &a)
     const int most = a.head_dim == 256 ? 2 : 4;
     const i64 rows = (static_cast<i64>(a.num_rows) + std::max(a.num_reqs, 1) - 1) / std::max(a.num_reqs, 1) * (a.num_q_heads / a.num_kv_heads);
     const i64 tiles = std::max<i64>(1, (rows + 15) / 16), passes = (tiles + most - 1) / most;
-    return kernel_of(a.cache_dtype, a.head_dim, static_cast<int>((tiles + passes - 1) / passes));
+    return kernel_of(a.cache_dtype, a.head_dim, 16 * static_cast<int>((tiles + passes - 1) / passes));
+}
+
+// Tiles of whole pages, or of parts of a page above 128 places, by tensor map; 8-bit caches and pages below kSmallPage places
+// by loads (a copy costs its warp 40 to 90 cycles, whatever its size).
+constexpr int kSmallPage = 16;
+
+Cut cut_of(const spec_verify_cache_attention_args &a, const Kernel &k)
+{
+    const int page = a.page_size, group = a.num_q_heads / a.num_kv_heads;
+    int q_box = k.rows;
+    while (group % q_box != 0) --q_box;  // a divisor of the group ...
+    while (k.rows % q_box != 0) {        // ... and of the tile
+        --q_box;
+        while (group % q_box != 0) --q_box;
+    }
+    if (a.cache_dtype == SV_E4M3 || page < kSmallPage) return Cut{kTile, 0, 1, kTile, q_box};
+    if (page <= kTile) return Cut{kTile / page * page, page, 1, kTile / page, q_box};
+    const int parts = (page + kTile - 1) / kTile, box = (page + parts - 1) / parts;
+    return Cut{box, box, parts, 1, q_box};
 }
 
 // How many CTAs a call has: those that the device holds at once, or as many as there can be tiles.
+i64 most_tiles(const spec_verify_cache_attention_args &a, const Kernel &k)
+{
+    const Cut cut = cut_of(a, k);
+    return std::max<i64>(1, cut.parts > 1 ? static_cast<i64>(a.pages_per_req) * cut.parts : (static_cast<i64>(a.pages_per_req) * a.page_size + cut.span - 1) / cut.span);
+}
+
 i64 ctas_for(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
-    const i64 groups = (a.num_reqs + static_cast<i64>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) / k.rows) * a.num_kv_heads;
-    const i64 tiles = std::max<i64>(1, (static_cast<i64>(a.pages_per_req) * a.page_size + k.tokens - 1) / k.tokens);
-    return std::min<i64>(152 * k.resident, groups > (1 << 20) || tiles > (1 << 20) ? 1 << 20 : groups * tiles);
+    const i64 groups = (a.num_reqs + static_cast<i64>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) / k.rows) * a.num_kv_heads, tiles = most_tiles(a, k);
+    return groups >= 152 || tiles >= 152 ? 152 : std::min<i64>(152, groups * tiles);
 }
 
 // Whether groups may have to be joined: not where each has one tile.
-bool joins(const spec_verify_cache_attention_args &a, const Kernel &k) { return static_cast<i64>(a.pages_per_req) * a.page_size > k.tokens; }
+bool joins(const spec_verify_cache_attention_args &a, const Kernel &k) { return most_tiles(a, k) > 1; }
 
 int64_t workspace_of(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
     return joins(a, k) ? ctas_for(a, k) * (2ll * k.rows * (k.dim + 2) * 4 + static_cast<int64_t>(sizeof(Part))) : 0;
+}
+
+int launch_after(const void *kernel, unsigned grid, unsigned block, int bytes, cudaStream_t stream, void **params)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return status_of(cudaLaunchKernelExC(&cfg, kernel, params));
 }
 
 // What an attention call asks beyond its step.
@@ -633,6 +649,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     P.hk = a->num_kv_heads;
     P.group = a->num_q_heads / a->num_kv_heads;
     P.bf16 = a->dtype == SV_BF16;
+    P.cut = cut_of(*a, kernel);
     const i64 ctas = ctas_for(*a, kernel);
     P.sums = static_cast<float *>(workspace ? a->workspace : nullptr);
     P.stats = workspace ? reinterpret_cast<float2 *>(P.sums + ctas * 2 * kernel.rows * kernel.dim) : nullptr;
@@ -650,38 +667,29 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     if (s.push(stream) != SV_OK) return SV_ECUDA;
 #endif
     TensorMaps maps;
-    int box = 1;
-    if (kernel.tensor) {
-        while (box < kernel.tokens && a->page_size % (2 * box) == 0) box *= 2;
+    memset(&maps, 0, sizeof(maps));
+    if (a->cache_dtype != SV_E4M3) {
         const bool bf16 = a->cache_dtype == SV_BF16;
-        // (sizes of the map: slots, heads, pages; of the queries heads, rows. Without a page nothing of the map is looked at)
-        auto turned = [&](const View &c) {
-            View v{a->num_pages ? c.at : a->q, {c.size[1], c.size[2], c.size[0]}, {c.stride[1], c.stride[2], c.stride[0]}, c.inner, 2};
-            if (!a->num_pages) v.size[0] = v.size[1] = v.size[2] = 1;
-            return v;
-        };
         const View queries{a->q, {a->num_q_heads, a->num_rows, 1}, {a->q_head_stride, a->q_row_stride, 0}, a->head_dim, 2};
-        if (map_of(maps.k, bf16, turned(kc), box) != SV_OK || map_of(maps.v, bf16, turned(vc), box) != SV_OK || map_of(maps.q, bf16, queries, 1) != SV_OK) return SV_ECUDA;
+        if (map_of(maps.q, bf16, queries, P.cut.q_box) != SV_OK) return SV_ECUDA;
+        if (P.cut.box) {
+            // (sizes of the map: slots, heads, pages. Without a page only zeros come of it, whatever it names)
+            auto turned = [&](const View &c) {
+                View v{a->num_pages ? c.at : a->q, {c.size[1], c.size[2], c.size[0]}, {c.stride[1], c.stride[2], c.stride[0]}, c.inner, 2};
+                if (!a->num_pages) v.size[0] = v.size[1] = v.size[2] = 1;
+                return v;
+            };
+            if (map_of(maps.k, bf16, turned(kc), P.cut.box) != SV_OK || map_of(maps.v, bf16, turned(vc), P.cut.box) != SV_OK) return SV_ECUDA;
+        }
     }
-    void *params[] = {&P, &maps, &box};
-    if (cudaLaunchKernel(kernel.run, dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(kernel.threads)), params,
-                         static_cast<size_t>(kernel.bytes), stream) != cudaSuccess)
-        return status_of(cudaErrorLaunchFailure);
-    if (!workspace) return SV_OK;
-    // the join's CTAs start while the attention's end, and wait for them on the device
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    // Each kernel may start while the one before it ends; it waits for that on the device before it looks at memory.
+    void *params[] = {&P, &maps};
+    int rc_launch = launch_after(kernel.run, static_cast<unsigned>(ctas), 512, kernel.bytes, stream, params);
+    if (rc_launch != SV_OK || !workspace) return rc_launch;
     int rows = kernel.rows;
     float offset = kernel.offset;
     void *join[] = {&P, &rows, &offset};
-    return status_of(cudaLaunchKernelExC(&cfg, kernel.join, join));
+    return launch_after(kernel.join, static_cast<unsigned>(ctas), 256, 0, stream, join);
 }
 
 #ifdef SV_DEBUG_BOUNDS

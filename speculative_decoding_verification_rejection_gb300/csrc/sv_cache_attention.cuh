@@ -1,5 +1,7 @@
-// Attention of a step's rows over the paged cache. See sv_cache_attention.cu for the mathematics.
+// Attention of a step's rows over the paged cache. See sv_cache.cu for the mathematics.
 #pragma once
+
+#include <cuda.h>
 
 #include <type_traits>
 
@@ -9,13 +11,20 @@ namespace sv_cache {
 
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kLn2 = 0x1.62e430p-1f;
-constexpr int kSlices = 4;             // warps that share a tile's tokens
-constexpr int kMaxPlace = 1 << 30;     // places of a request
+constexpr int kMaxPlace = 1 << 30;  // places of a request
+constexpr int kTile = 128;          // keys of a tile, at most
 
 // A part of a group that ends at a CTA's last tile, to be joined with those of the CTAs behind: the CTAs that
 // hold parts of the group, the first one's slot, and the group's rows. first < 0: none.
 struct Part {
     int first, last, slot, row0, from, count, head, unused;
+};
+
+// How places are cut into tiles: `span` places each, whole pages where a page has at most 128 places (parts 1), or
+// each page in `parts` tiles of `box` places (the last may have fewer). Copies by tensor map bring boxes of `box` places
+// that lie in one page; box 0: keys are loaded one by one, whatever the pages are.
+struct Cut {
+    int span, box, parts, boxes, q_box;
 };
 
 struct AttentionParams {
@@ -29,167 +38,183 @@ struct AttentionParams {
     float scale;  // times log2 e
     int window, hq, hk, group;
     bool bf16;            // type of the rows
+    Cut cut;
     float *sums;          // workspace: [ctas][2][rows of a tile][dim], then [ctas][2][rows of a tile][2], then Part [ctas]
     float2 *stats;
     Part *parts;
 };
 
-// What a kernel's tile is. ES bytes of a cached element, D elements of a head, RG groups of warps, each with MT
-// tiles of 16 rows.
-template <int ES, int D, int RG, int MT>
-struct Tile {
-    static constexpr int row = D * ES;                              // bytes of a key
-    static constexpr int chunks = row / 16;
-    static constexpr int tokens = row <= 128 ? 128 : 64;
-    static constexpr int sub = tokens / (16 * kSlices);             // groups of 16 tokens a warp
-    static constexpr int rows = 16 * RG * MT;
-    static constexpr int threads = 32 * kSlices * RG;
-    static constexpr int kv = tokens * row;
-    static constexpr int stage = 2 * kv + rows * D * 2;
-    static constexpr int resident = RG == 1 && stage <= 37000 ? 2 : 1;  // CTAs on an SM
-    static constexpr bool q_held = MT == 1;                         // the queries' fragments stay in registers,
-    static constexpr int q_bytes = q_held ? 0 : rows * D * 2;       // or the queries in shared memory
-    static constexpr int fit = ((tokens == 128 ? 220000 : 226000) - q_bytes) / stage;
-    static constexpr int stages = resident == 2 ? (stage > 30000 ? 3 : 5) : fit > 6 ? 6 : fit;
-    static constexpr int buffers = 2 * rows * D * 4 <= 2 * kv ? 2 : 1;
-    static_assert(stages >= 2 && rows * D * 4 <= 2 * kv, "room");
-    // shared memory behind the stages
-    struct Head {
-        int p0, first, count, from, row0, head, length, flags;      // see describe()
-        int part_first, part_last, part_slot, unused;
-        uint32_t seen[tokens / 32];
-    };
-    struct Shared {
-        int2 place[stages + 1][tokens];  // page, slot
-        Head head[stages + 1];
-        float2 stat[kSlices][rows];
-        float2 joined[rows];
-        i64 scan[threads / 32 + 1];
-        i64 start[2];
-    };
-    static constexpr int bytes = stages * stage + q_bytes + static_cast<int>(sizeof(Shared));
-    static_assert(bytes <= (resident == 2 ? 115712 : 232448), "shared memory");
+struct TensorMaps {
+    CUtensorMap q, k, v;
 };
 
-enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16 };
+enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge = 32 };
+
+// A tile is up to 128 keys. Both products have the keys or the elements in the 128 rows of the tensor cores' memory and
+// the query rows (N, 16 to 64) in its columns: scores^T = K Q^T, and out^T += V^T weights^T. So few query rows
+// waste nothing, and every key is read from shared memory once for all of them. Roles, each a warp or more: weights
+// (four warps; a thread has one key's scores of all rows), the first product, the second, a plan (the tiles and their
+// pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are 8 bits or
+// the pages small, by eight warps that load, widen and store them.
+template <int KIND, int D, int N>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
+struct Tile {
+    static constexpr bool bf16 = KIND == SV_BF16;    // type of the products
+    static constexpr int bytes_of = KIND == SV_E4M3 ? 1 : 2;
+    static constexpr int rows = N;
+    static constexpr int halves = D / 64;            // pieces of 64 elements, 128 bytes a key: the copies' swizzle
+    static constexpr int piece = kTile * 128;
+    static constexpr int slot = halves * piece;      // keys or values of a tile
+    static constexpr int q_bytes = N * D * 2;
+    static constexpr int weights = kTile * N * 2;
+    static constexpr int q_buffers = (D == 256 && N > 16) || N == 64 ? 1 : 2;
+    static constexpr int heads = D == 256 && N > 16 ? 2 : 8;  // descriptions of tiles that are kept
+    static constexpr int fit = ((heads == 8 ? 224800 : 229376) - q_buffers * q_bytes - 2 * weights) / slot;
+    static constexpr int slots = fit > 12 ? 12 : fit;
+    static constexpr int k_slots = slots / 2, v_slots = slots - slots / 2;  // rings of their own: each is filled in turn
+    static constexpr int blocks = D == 256 ? 2 : 1;  // of 128 elements
+    static constexpr int columns_used = (2 + blocks) * N;
+    static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
+    static constexpr int threads = 512;
+    static_assert(slots >= 2 && columns_used <= 256, "room");
+    struct Head {
+        int p0, first, count, from, head, length, flags, segment;
+        int part_first, part_last, part_slot, slot, started;
+        uint32_t seen[4];
+        int page[kTile];  // of each box, or of each key
+    };
+    struct Shared {
+        u64 k_full[k_slots], k_empty[k_slots], v_full[v_slots], v_empty[v_slots], scores[2], weighed[2], done[2], q_full[2], q_empty[2], told[heads],
+            used[heads];
+        Head head[heads];
+        alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
+        alignas(16) float factor[N];  // what a new reference makes of the old sums; of the result
+        alignas(16) float scale[N];   // of the scores
+        alignas(16) float most[4][N];
+        float top[N];                 // the reference, times log2 e
+        float sum[N];
+        float q_scale[2][N];          // of queries held in binary16
+        u64 scan[threads / 32];
+        u64 start[2];
+        uint32_t tensor_at;
+        int lost;
+    };
+    static constexpr int bytes = slots * slot + q_buffers * q_bytes + 2 * weights + static_cast<int>(sizeof(Shared));
+    static_assert(bytes <= 232448, "shared memory");
+};
+
+// Weights relative to a reference that is the row's largest score when it is set, and is set anew when some score is
+// `slack` doublings above it: in bf16 (range of binary32) rarely, in binary16 so that weights stay below 2^15, held
+// `offset` doublings up, so that the smallest step of a weight is 2^-35.
+template <bool BF16>
+struct Weights {
+    static constexpr float offset = BF16 ? 0.0f : 11.0f, slack = BF16 ? 8.0f : 4.0f;
+};
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void copy16(uint32_t to, const unsigned char *from, bool there)
-{
-    there = there && SV_CACHE_INSIDE(from, 16, false);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void matrices(uint32_t *r, uint32_t at)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void matrices_turned(uint32_t *r, uint32_t at)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ void multiply(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
-{
-    if constexpr (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// The tiles of a group (rows `from` to from + count - 1 of request i with one key head): [t0, t1), at least one; keys
-// at places [start, end) are seen by one of its rows.
-struct Range {
-    int t0, t1, start, end;
-};
-__device__ __forceinline__ Range range_of(const AttentionParams &P, int tokens, int length, int j0, int j1)
+// The larger number; NaN if one is.
+__device__ __forceinline__ float larger(float a, float b)
 {
-    const i64 cap = static_cast<i64>(P.s.width) * P.s.page;
-    i64 end = length < 0 ? 0 : min(static_cast<i64>(length) + j1 + 1, cap);
-    i64 start = P.window > 0 && length >= 0 ? max(0ll, static_cast<i64>(length) + j0 + 1 - P.window) : 0;
-    if (start >= end) start = end = 0;
-    Range r;
-    r.start = static_cast<int>(start);
-    r.end = static_cast<int>(end);
-    r.t0 = r.start / tokens;
-    r.t1 = max(r.t0 + 1, (r.end + tokens - 1) / tokens);
-    return r;
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+    return c;
 }
 
+// ---------------------------------------------------------------------------------------
+// which tiles there are
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ int page_of(const Step &s, int p)
+{
+    return p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * s.page_magic) >> 42) : p / s.page;
+}
+__device__ __forceinline__ int tile_of(const AttentionParams &P, int p)
+{
+    if (P.cut.parts == 1) return static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(P.cut.span));
+    const int c = page_of(P.s, p);
+    return c * P.cut.parts + (p - c * P.s.page) / P.cut.box;
+}
+// total k / of, rounded down (k <= of < 2^10)
+__device__ __forceinline__ u64 share_of(u64 total, int k, int of)
+{
+    return total < (1u << 22) ? static_cast<uint32_t>(total) * static_cast<uint32_t>(k) / static_cast<uint32_t>(of) : total * static_cast<u64>(k) / static_cast<u64>(of);
+}
+// the last k with share_of(total, k, of) <= number
+__device__ __forceinline__ int sharer_of(u64 total, u64 number, int of) { return static_cast<int>(((number + 1) * static_cast<u64>(of) - 1) / total); }
+
 // All tiles of the step in order: request, rows of a tile, key head, tokens. CTA c takes those from c W / ctas
-// to (c + 1) W / ctas, so every CTA gets as many whatever the lengths are.
-template <typename Shape>
+// to (c + 1) W / ctas, so every CTA gets as many whatever the lengths are. A group is the tiles of a request's N query
+// rows and a key head: at least one tile; keys at places [start, end) are seen by one of its rows.
+template <int N>
 struct Walk {
     const AttentionParams &P;
     int i, first, rows, length;  // the request: its first row, its rows times the group, its length
     int from, count, head, t;    // the group: its first row within the request, its rows; the tile
-    Range range;
-    i64 base;                    // number of the group's first tile
+    int t0, t1, start, end;
+    u64 base;                    // number of the group's first tile
 
-    __device__ Walk(const AttentionParams &P) : P(P) {}
-    __device__ void request(int k)
+    __device__ __forceinline__ Walk(const AttentionParams &P) : P(P) {}
+    __device__ __forceinline__ void request(int k)
     {
         i = k;
         rows = i < P.s.n ? request_rows(P.s, i, first) * P.group : 0;
         length = rows ? ld(P.s.lengths + i) : 0;
     }
-    __device__ void group(int at)
+    __device__ __forceinline__ void group(int at)
     {
         from = at;
-        count = min(Shape::rows, rows - at);
-        range = range_of(P, Shape::tokens, length, at / P.group, (at + count - 1) / P.group);
-        t = range.t0;
+        count = min(N, rows - at);
+        const int cap = P.s.width * P.s.page;  // (at most kMaxPlace)
+        // places up to that of the last row
+        end = length < 0 ? 0 : static_cast<int>(min(static_cast<i64>(length) + (rows <= N ? rows / P.group : (at + count - 1) / P.group + 1), static_cast<i64>(cap)));
+        start = 0;
+        if (P.window > 0 && length >= 0) start = static_cast<int>(min(max(0ll, static_cast<i64>(length) + at / P.group + 1 - P.window), static_cast<i64>(cap)));
+        if (start >= end) start = end = 0;
+        t0 = start ? tile_of(P, start) : 0;
+        t1 = end ? tile_of(P, end - 1) + 1 : 1;
+        t = t0;
     }
-    __device__ int tiles() const { return range.t1 - range.t0; }
-    __device__ i64 request_tiles(int k)
+    __device__ __forceinline__ int tiles() const { return t1 - t0; }
+    __device__ u64 request_tiles(int k)
     {
         request(k);
-        i64 sum = 0;
-        for (int at = 0; at < rows; at += Shape::rows) {
+        u64 sum = 0;
+#pragma unroll 1
+        for (int at = 0; at < rows; at += N) {
             group(at);
-            sum += static_cast<i64>(tiles()) * P.hk;
+            sum += static_cast<u64>(tiles()) * static_cast<u64>(P.hk);
         }
         return sum;
     }
-    // To tile `skip` of request k.
-    __device__ void seek(int k, i64 skip, i64 number)
+    // To tile `skip` of request k, the step's tile `number`.
+    __device__ void seek(int k, u64 skip, u64 number)
     {
         request(k);
         base = number - skip;
-        for (int at = 0; at < rows; at += Shape::rows) {
+#pragma unroll 1
+        for (int at = 0; at < rows; at += N) {
             group(at);
-            const i64 here = static_cast<i64>(tiles()) * P.hk;
+            const u64 here = static_cast<u64>(tiles()) * static_cast<u64>(P.hk);
             if (skip < here) break;
             skip -= here;
             base += here;
         }
-        head = static_cast<int>(skip / tiles());
-        t += static_cast<int>(skip - static_cast<i64>(head) * tiles());
-        base += static_cast<i64>(head) * tiles();
+        head = static_cast<int>(skip < (1u << 31) ? static_cast<uint32_t>(skip) / static_cast<uint32_t>(tiles()) : skip / static_cast<u64>(tiles()));
+        t += static_cast<int>(skip - static_cast<u64>(head) * static_cast<u64>(tiles()));
+        base += static_cast<u64>(head) * static_cast<u64>(tiles());
     }
-    __device__ void next()
+    __device__ __forceinline__ void next()
     {
-        if (++t < range.t1) return;
+        if (++t < t1) return;
         base += tiles();
-        t = range.t0;
+        t = t0;
         if (++head < P.hk) return;
         head = 0;
-        if (from + Shape::rows < rows) return group(from + Shape::rows);
+        if (from + N < rows) return group(from + N);
         do
             request(i + 1);
         while (rows == 0 && i < P.s.n);
@@ -197,510 +222,782 @@ struct Walk {
     }
 };
 
-// Address of a 16-byte chunk of a key in a stage: chunks of eight keys in a row fall into different banks.
-template <int CHUNKS>
-__device__ __forceinline__ uint32_t swizzled(int token, int chunk)
+// ---------------------------------------------------------------------------------------
+// barriers, copies, products
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void barrier_init(u64 *b, int count) { asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(shared_address(b)), "r"(count) : "memory"); }
+__device__ __forceinline__ void barrier_expect(u64 *b, int bytes)
 {
-    return CHUNKS >= 8 ? token * (CHUNKS * 16) + ((chunk ^ (token & 7)) << 4) : token * (CHUNKS * 16) + ((chunk ^ (token >> 1 & 3)) << 4);
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(u64 *b) { asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(shared_address(b)) : "memory"); }
+// Waits for a phase to end, not for ever: after kPatience looks (seconds) the call is given up (`lost`), every later
+// wait returns at once, and the rows get NaN. Whoever waits has seen the phase before end, so that a parity names one phase.
+constexpr int kPatience = 1 << 22;
+__device__ __forceinline__ bool barrier_try(u64 *b, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(shared_address(b)), "r"(parity) : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ void barrier_wait(u64 *b, uint32_t parity, int *lost)
+{
+    if (barrier_try(b, parity)) return;
+    for (int k = 0; k < kPatience; ++k) {
+        if (barrier_try(b, parity)) return;
+        if (*reinterpret_cast<volatile int *>(lost)) return;
+    }
+    *reinterpret_cast<volatile int *>(lost) = 1;
+}
+// A box of an array of heads, [1][1][box][64 elements], to shared memory (swizzled by 128 bytes).
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap *map, u64 *b, int element, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(to), "l"(map),
+                 "r"(shared_address(b)), "r"(element), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// Description of a matrix in shared memory: address, the two strides in bytes, and the swizzle (2: 128 bytes, 0: none). The
+// address is in the lower word, in steps of 16 bytes.
+__device__ __forceinline__ u64 matrix_at(uint32_t at, uint32_t lead, uint32_t stride, u64 swizzle)
+{
+    return static_cast<u64>((at & 0x3ffff) >> 4) | static_cast<u64>(lead >> 4) << 16 | static_cast<u64>(stride >> 4) << 32 | u64{1} << 46 | swizzle << 61;
+}
+// Shape of a product of 16-bit elements, 128 x N, into binary32; whether A and B have their rows contiguous.
+__host__ __device__ constexpr uint32_t product_of(bool bf16, int n, bool turned)
+{
+    return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (turned ? 3u : 0u) << 15 | static_cast<uint32_t>(n >> 3) << 17 | 8u << 24;
+}
+// One lane of a warp, always the same.
+__device__ __forceinline__ uint32_t elected()
+{
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
+}
+// d (+)= A B, issued by the elected lane of a warp whose lanes all call it: with operands that are the same in the whole warp
+// a product is issued every 40 to 50 cycles, by a lane on its own path (and descriptions put together anew) every 75 to 115.
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t shape, bool add, uint32_t leader)
+{
+    asm volatile(
+        "{\n.reg .pred p, q;\n.reg .b64 x, y;\nmov.b64 x, {%1, %2};\nmov.b64 y, {%3, %4};\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}" ::"r"(d),
+        "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(shape), "r"(static_cast<int>(add)), "r"(leader)
+        : "memory");
+}
+// An arrival at b when all products that the elected lane has issued so far have ended.
+__device__ __forceinline__ void products_close(u64 *b, uint32_t leader)
+{
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"l"(
+                     static_cast<u64>(shared_address(b))),
+                 "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void tensor_load16(float *v, uint32_t at)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
+__device__ __forceinline__ void tensor_store16(uint32_t at, const float *v)
+{
+    uint32_t r[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(v[k]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]),
+        "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tensor_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tensor_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tensor_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tensor_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The four warps of the weights among themselves.
+__device__ __forceinline__ void weights_meet() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool weights_any(bool x)
+{
+    int any;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, 2, 128, p;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(any) : "r"(static_cast<int>(x)) : "memory");
+    return any != 0;
 }
 
-// The fragments of a 16 x 16 piece of the queries. For 16-bit caches as the product wants them; for e4m3, whose
-// bytes come four neighbours to a lane, with the elements of a piece in that order (4 t to 4 t + 3 in lane t of
-// four), and bf16 queries as binary16 times their row's factor.
-template <int ES, int D>
-__device__ __forceinline__ void query_fragment(uint32_t *a, uint32_t q_at, int row0, int ks, int lane, bool convert, const float *factor)
+// The boxes of a tile's keys or values, by a warp, once the slot is free.
+template <typename S>
+__device__ __forceinline__ void boxes_to(const CUtensorMap *map, u64 *full, u64 *empty, bool wait, uint32_t parity, uint32_t to, const Cut &cut, int slot, int head,
+                                         const int *page, int lane, int *lost)
 {
-    if constexpr (ES == 2) {
-        const int r = row0 + (lane & 15), c = ks * 2 + (lane >> 4);
-        matrices(a, q_at + swizzled<D / 8>(r, c));
-    } else {
-        const int t = lane & 3;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = row0 + lane / 4 + half * 8, e = ks * 16 + 4 * t;
-            uint32_t lo, hi;
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(q_at + swizzled<D / 8>(r, e / 8) + (e & 7) * 2) : "memory");
-            if (convert) {
-                const float2 x = pair_of<__nv_bfloat16>(lo), y = pair_of<__nv_bfloat16>(hi);
-                lo = pack<__half>(x.x * factor[half], x.y * factor[half]);
-                hi = pack<__half>(y.x * factor[half], y.y * factor[half]);
-            }
-            a[half] = lo;
-            a[2 + half] = hi;
-        }
+    if (wait) barrier_wait(empty, parity, lost);
+    if (lane == 0) barrier_expect(full, cut.boxes * cut.box * 128 * S::halves);
+    __syncwarp();
+#pragma unroll 1
+    for (int k = lane; k < cut.boxes * S::halves; k += 32) {
+        const int b = k / S::halves, e = k % S::halves;
+        copy_box(to + e * S::piece + b * cut.box * 128, map, full, e * 64, slot, head, page[b]);
     }
 }
-
-template <bool BF16, int ES, int D, int RG, int MT>
-__global__ void __launch_bounds__(Tile<ES, D, RG, MT>::threads, Tile<ES, D, RG, MT>::resident) sv_cache_attention_kernel(const AttentionParams P)
+template <typename E, typename T>
+__device__ __forceinline__ E from_bits(T v)
 {
-    using S = Tile<ES, D, RG, MT>;
-    // Weights are rounded to the products' type relative to 1 (bf16) or 2^15 (binary16, whose smallest step
-    // is then 2^-39 of the largest weight: without it 60000 weights of 2^-26 would be lost).
-    constexpr float kOffset = BF16 ? 0.0f : 15.0f;
+    static_assert(sizeof(E) == 2 && sizeof(T) == 2);
+    E e;
+    memcpy(&e, &v, 2);
+    return e;
+}
+
+// The largest of 16 columns' numbers over a warp: lane l gets that of column l % 16 (NaN if one is).
+__device__ __forceinline__ float columns_largest(float *v, int lane)
+{
+#pragma unroll
+    for (int half = 8; half; half /= 2)
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const bool upper = lane & half;
+            const float other = __shfl_xor_sync(~0u, upper ? v[k] : v[k + half], half);
+            v[k] = larger(upper ? v[k + half] : v[k], other);
+        }
+    return larger(v[0], __shfl_xor_sync(~0u, v[0], 16));
+}
+
+// Registers of a warp's roles: 216 + 72 + 2 x 112 of four warps each make the 4 x 128 of the launch. (The checked build
+// spills instead: its calls in these loops need more than there are.)
+#ifdef SV_DEBUG_BOUNDS
+#define SV_CACHE_REGISTERS(way, count)
+#else
+#define SV_CACHE_REGISTERS(way, count) asm volatile("setmaxnreg." way ".sync.aligned.u32 " #count ";")
+#endif
+
+template <int KIND, int D, int N>
+__global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
+{
+    using S = Tile<KIND, D, N>;
+    constexpr bool kBf16 = S::bf16, kWide = KIND == SV_E4M3;  // 8 bits are widened to binary16
+    using E = std::conditional_t<kBf16, __nv_bfloat16, __half>;
+    using W = Weights<kBf16>;
     extern __shared__ __align__(1024) unsigned char room[];
-    auto &sh = *reinterpret_cast<typename S::Shared *>(room + S::stages * S::stage + S::q_bytes);
-    const uint32_t stages_at = shared_address(room);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t4 = lane & 3;
-    const int slice = warp % kSlices, rg = warp / kSlices;
+    unsigned char *const q_room = room + S::slots * S::slot, *const w_room = q_room + S::q_buffers * S::q_bytes;
+    auto &sh = *reinterpret_cast<typename S::Shared *>(w_room + 2 * S::weights);
+    const uint32_t room_at = shared_address(room), q_at = shared_address(q_room), w_at = shared_address(w_room);
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid & 31;
     const int cta = blockIdx.x;
+    const bool loads = kWide || P.cut.box == 0;  // keys by loads, not by tensor map
+
+    // -- barriers and memory, while the work before this call ends
+    if (warp == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&sh.tensor_at)), "n"(S::columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        const int filled = loads ? 8 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
+#pragma unroll 1
+        for (int k = 0; k < S::v_slots; ++k) {
+            if (k < S::k_slots) barrier_init(sh.k_full + k, filled), barrier_init(sh.k_empty + k, 1);
+            barrier_init(sh.v_full + k, filled), barrier_init(sh.v_empty + k, 1);
+        }
+#pragma unroll 1
+        for (int k = 0; k < S::heads; ++k) barrier_init(sh.told + k, 1), barrier_init(sh.used + k, 2);  // (used: by the second product, and by the warp of the queries)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k)
+            barrier_init(sh.scores + k, 1), barrier_init(sh.weighed + k, 128), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, kWide ? 2 : 1);
+        sh.lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 32 && !loads) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
+        if (!kWide) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q) : "memory");
+    }
+    if (!loads) {  // places of a slot that no copy writes: zeros for good
+        const int filled = P.cut.boxes * P.cut.box, piece = (kTile - filled) * 8;
+#pragma unroll 1
+        for (int x = tid; x < S::slots * S::halves * piece; x += S::threads)
+            *reinterpret_cast<uint4 *>(room + x / piece * S::piece + filled * 128 + x % piece * 16) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // -- this CTA's tiles
-    Walk<S> walk(P);
+    Walk<N> walk(P);
     const int per = (P.s.n + S::threads - 1) / S::threads;
-    i64 mine = 0;
+    u64 mine = 0;
+#pragma unroll 1
     for (int k = tid * per; k < min(P.s.n, (tid + 1) * per); ++k) mine += walk.request_tiles(k);
-    i64 before = mine;
+    u64 before = mine;
+#pragma unroll 1
     for (int d = 1; d < 32; d *= 2) {
-        const i64 up = __shfl_up_sync(~0u, before, d);
+        const u64 up = __shfl_up_sync(~0u, before, d);
         if (lane >= d) before += up;
     }
     if (lane == 31) sh.scan[warp] = before;
+    tensor_before();
     __syncthreads();
-    i64 total = 0, ahead = 0;
+    tensor_after();
+    u64 total = 0, ahead = 0;
+#pragma unroll 1
     for (int w = 0; w < S::threads / 32; ++w) {
         if (w == warp) ahead = total;
         total += sh.scan[w];
     }
     before += ahead - mine;
-    const int ctas = static_cast<int>(min(total, static_cast<i64>(gridDim.x)));  // (each with a tile at least)
-    if (cta >= ctas) {
-        if (P.parts && tid == 0) st(&P.parts[cta].first, -1);
-        return;
-    }
-    const i64 u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-    const int n = static_cast<int>(u1 - u0);
-    if (u0 >= before && u0 < before + mine) {
-        i64 at = before;
-        for (int k = tid * per; k < min(P.s.n, (tid + 1) * per); ++k) {
-            const i64 here = walk.request_tiles(k);
-            if (u0 < at + here) {
-                sh.start[0] = k;
-                sh.start[1] = u0 - at;
-                break;
-            }
-            at += here;
-        }
-    }
-    __syncthreads();
-    walk.seek(static_cast<int>(sh.start[0]), sh.start[1], u0);
-
-    // -- a tile's description: what is in it, and where its keys are
-    int page = -1, slot = 0;
-    auto look_up = [&](int) {  // this thread's key (its page arrives while a tile is computed)
-        const int p = walk.t * S::tokens + tid;
-        page = -1;
-        if (walk.rows && tid < S::tokens && p >= walk.range.start && p < walk.range.end) {
-            const int c = p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * P.s.page_magic) >> 42) : p / P.s.page;
-            slot = p - c * P.s.page;
-            page = ld(P.s.table + walk.i * P.s.table_stride + c);
-        }
-    };
-    auto describe = [&](int d) {
-        const int k = d % (S::stages + 1);
-        if (tid < S::tokens) {
-            const bool seen = page >= 0 && page < P.s.pages;
-            sh.place[k][tid] = make_int2(seen ? page : -1, slot);
-            const uint32_t all = __ballot_sync(~0u, seen);
-            if (lane == 0) sh.head[k].seen[warp] = all;
-        }
-        if (tid == 0) {
-            auto &h = sh.head[k];
-            const bool opens = walk.t == walk.range.t0, ends = walk.t + 1 == walk.range.t1;
-            // (a segment: the tiles of one group that this CTA has)
-            const bool first = d == 0 || opens, last = d == n - 1 || ends;
-            const bool part = walk.base < u0 || walk.base + walk.tiles() > u1;
-            h.p0 = walk.t * S::tokens;
-            h.first = walk.first;
-            h.count = walk.count;
-            h.from = walk.from;
-            h.head = walk.head;
-            h.length = walk.length;
-            h.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (part ? kPartial : 0) | (walk.base > u0 ? kSlot : 0) | (last && !ends ? kOpen : 0);
-            if (last && !ends) {  // the CTAs that have tiles of the group
-                h.part_first = static_cast<int>(((walk.base + 1) * ctas - 1) / total);
-                h.part_last = static_cast<int>(((walk.base + walk.tiles()) * ctas - 1) / total);
-                h.part_slot = total * h.part_first / ctas < walk.base;
-            }
-        }
-        walk.next();
-    };
-    auto issue = [&](int d) {
-        const int k = d % (S::stages + 1);
-        const uint32_t at = stages_at + (d % S::stages) * S::stage;
-        const auto &h = sh.head[k];
-        const i64 head = h.head;
-        const unsigned char *keys = P.kc.at + head * P.kc.head, *values = P.vc.at + head * P.vc.head;
-#pragma unroll 4
-        for (int x = tid; x < S::tokens * S::chunks; x += S::threads) {
-            const int token = x / S::chunks, c = x % S::chunks;
-            const int2 w = sh.place[k][token];
-            const bool there = w.x >= 0;
-            const i64 pg = there ? w.x : 0, sl = there ? w.y : 0;
-            const uint32_t to = at + swizzled<S::chunks>(token, c);
-            copy16(to, keys + pg * P.kc.page + sl * P.kc.slot + c * 16, there);
-            copy16(to + S::kv, values + pg * P.vc.page + sl * P.vc.slot + c * 16, there);
-        }
-        if (h.flags & kFirst)
-            for (int x = tid; x < S::rows * (D / 8); x += S::threads) {
-                const int r = x / (D / 8), c = x % (D / 8);
-                const bool there = r < h.count;
-                const int at_row = h.from + (there ? r : 0), j = at_row / P.group, qh = static_cast<int>(head) * P.group + at_row - j * P.group;
-                copy16(at + 2 * S::kv + swizzled<D / 8>(r, c), P.q + (h.first + j) * P.q_row + qh * P.q_head + c * 16, there);
-            }
-    };
-
-    for (int d = 0; d < S::stages && d < n; ++d) {
-        look_up(d);
-        describe(d);
-    }
-    __syncthreads();
-    for (int d = 0; d < S::stages - 1; ++d) {
-        if (d < n) issue(d);
-        copies_close();
-    }
-
-    // -- the tiles
-    uint32_t q[S::q_held ? D / 16 : 1][4];
-    float o[MT][D / 8][4], top[MT][2], sum[MT][2], scale[MT][2], factor[MT][2];
-    int hi[MT][2], lo[MT][2];
-    bool part_written = false;
-    for (int it = 0; it < n; ++it) {
-        copies_wait<S::stages - 2>();
-        __syncthreads();
-        if (it + S::stages - 1 < n) issue(it + S::stages - 1);
-        copies_close();
-        const bool more = it + S::stages < n;
-        if (more) look_up(it + S::stages);
-
-        const auto &h = sh.head[it % (S::stages + 1)];
-        const uint32_t at = stages_at + (it % S::stages) * S::stage, q_at = S::q_held ? at + 2 * S::kv : stages_at + S::stages * S::stage;
-        const int flags = h.flags, p0 = h.p0, row_base = rg * MT * 16;
-        if (flags & kFirst) {
-            if constexpr (!S::q_held) {  // (the stage will hold other keys before the segment ends)
-                const uint4 *from = reinterpret_cast<const uint4 *>(room + (it % S::stages) * S::stage + 2 * S::kv);
-                for (int x = tid; x < S::q_bytes / 16; x += S::threads) reinterpret_cast<uint4 *>(room + S::stages * S::stage)[x] = from[x];
-                __syncthreads();
-            }
-            const float ks = P.scale * (P.k_scale ? ld(P.k_scale + h.head) : 1.0f);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int e = 0; e < D / 8; ++e) o[m][e][0] = o[m][e][1] = o[m][e][2] = o[m][e][3] = 0;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = row_base + m * 16 + g + half * 8, j = (h.from + min(r, h.count - 1)) / P.group;
-                    const i64 x = h.length < 0 ? -1 : static_cast<i64>(h.length) + j;
-                    hi[m][half] = static_cast<int>(min(x, static_cast<i64>(kMaxPlace)));
-                    lo[m][half] = P.window > 0 ? static_cast<int>(max(-1ll, min(x - P.window, static_cast<i64>(kMaxPlace)))) : -1;
-                    top[m][half] = -kInf;
-                    sum[m][half] = 0;
-                    factor[m][half] = 1.0f;
-                    scale[m][half] = ks;
-                    if constexpr (ES == 1) {
-                        if (P.bf16) {
-                            // bf16 queries as binary16 times a power of two that takes the row's largest to [2^13, 2^14):
-                            // exact down to 2^-28 of it
-                            float most = 0;
-#pragma unroll 4
-                            for (int e = t4 * 4; e < D; e += 16) {
-                                uint32_t x0, x1;
-                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x0), "=r"(x1) : "r"(q_at + swizzled<D / 8>(r, e / 8) + (e & 7) * 2) : "memory");
-                                const float2 a = pair_of<__nv_bfloat16>(x0), b = pair_of<__nv_bfloat16>(x1);
-                                most = fmaxf(fmaxf(most, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-                            }
-                            most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-                            most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-                            const int up = min(110, 13 - (static_cast<int>(__float_as_uint(most) >> 23) - 127));
-                            factor[m][half] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-                            scale[m][half] = ks * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                        }
-                    }
-                }
-                if constexpr (S::q_held) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) query_fragment<ES, D>(q[k], q_at, row_base + m * 16, k, lane, P.bf16, factor[m]);
-                }
-            }
-        }
-
-        // the tile's keys that this warp has
-        const int token0 = slice * 16 * S::sub;
-        uint32_t seen = h.seen[token0 / 32];
-        if constexpr (S::sub == 1) seen = seen >> (token0 & 31) & 0xffffu;
-        constexpr uint32_t kAll = S::sub == 1 ? 0xffffu : ~0u;
-        if (seen) {
-            float s[MT][S::sub][2][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int b = 0; b < S::sub; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[m][b][0][e] = s[m][b][1][e] = 0;
-            if constexpr (ES == 2) {
-                const int token = token0 + (lane >> 4) * 8 + (lane & 7), c = lane >> 3 & 1;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t b[S::sub][4];
-#pragma unroll
-                    for (int x = 0; x < S::sub; ++x) matrices(b[x], at + swizzled<S::chunks>(token + x * 16, k * 2 + c));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t a[4];
-                        if constexpr (!S::q_held) query_fragment<ES, D>(a, q_at, row_base + m * 16, k, lane, false, factor[m]);
-                        const uint32_t *f = S::q_held ? q[S::q_held ? k : 0] : a;
-#pragma unroll
-                        for (int x = 0; x < S::sub; ++x) {
-                            multiply<BF16>(s[m][x][0], f, b[x][0], b[x][1]);
-                            multiply<BF16>(s[m][x][1], f, b[x][2], b[x][3]);
-                        }
-                    }
-                }
-            } else {
-                const int token = token0 + (lane >> 3 & 1) * 8 + (lane & 7), c = lane >> 4;
-#pragma unroll
-                for (int k = 0; k < D / 16; k += 2) {
-                    uint32_t b[S::sub][4];
-#pragma unroll
-                    for (int x = 0; x < S::sub; ++x) matrices(b[x], at + swizzled<S::chunks>(token + x * 16, k + c));
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        uint32_t w[S::sub][4];
-#pragma unroll
-                        for (int x = 0; x < S::sub; ++x) {
-                            w[x][0] = half2_of_e4m3(b[x][2 * kk]);
-                            w[x][1] = half2_of_e4m3(b[x][2 * kk] >> 16);
-                            w[x][2] = half2_of_e4m3(b[x][2 * kk + 1]);
-                            w[x][3] = half2_of_e4m3(b[x][2 * kk + 1] >> 16);
-                        }
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            uint32_t a[4];
-                            if constexpr (!S::q_held) query_fragment<ES, D>(a, q_at, row_base + m * 16, k + kk, lane, P.bf16, factor[m]);
-                            const uint32_t *f = S::q_held ? q[S::q_held ? k + kk : 0] : a;
-#pragma unroll
-                            for (int x = 0; x < S::sub; ++x) {
-                                multiply<BF16>(s[m][x][0], f, w[x][0], w[x][1]);
-                                multiply<BF16>(s[m][x][1], f, w[x][2], w[x][3]);
-                            }
-                        }
-                    }
-                }
-            }
-
-            // which keys a row does not see: looked at in the tiles where some row may not see all
-            const int first_key = p0 + token0, last_key = first_key + 16 * S::sub - 1;
-            bool edge = seen != kAll;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) edge |= last_key > hi[m][half] || first_key <= lo[m][half];
-            edge = __any_sync(~0u, edge);
-            uint32_t w[MT][S::sub][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float up[2] = {top[m][0], top[m][1]};
-#pragma unroll
-                for (int x = 0; x < S::sub; ++x)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = s[m][x][b][e] * scale[m][e / 2];
-                            if (edge) {
-                                const int key = x * 16 + b * 8 + t4 * 2 + (e & 1), place = first_key + key;
-                                if (!(seen >> key & 1) || place > hi[m][e / 2] || place <= lo[m][e / 2]) v = -kInf;
-                            }
-                            s[m][x][b][e] = v;
-                            up[e / 2] = fmaxf(up[e / 2], v);
-                        }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    up[half] = fmaxf(up[half], __shfl_xor_sync(~0u, up[half], 1));
-                    up[half] = fmaxf(up[half], __shfl_xor_sync(~0u, up[half], 2));
-                }
-                if (__any_sync(~0u, up[0] > top[m][0] || up[1] > top[m][1])) {
-                    float keep[2];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        keep[half] = up[half] == top[m][half] ? 1.0f : exp2_fast(top[m][half] - up[half]);
-                        sum[m][half] *= keep[half];
-                        top[m][half] = up[half];
-                    }
-#pragma unroll
-                    for (int e = 0; e < D / 8; ++e)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) o[m][e][c] *= keep[c / 2];
-                }
-                const float from[2] = {(up[0] == -kInf ? 0.0f : up[0]) - kOffset, (up[1] == -kInf ? 0.0f : up[1]) - kOffset};
-#pragma unroll
-                for (int x = 0; x < S::sub; ++x)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const float e0 = exp2_fast(s[m][x][b][2 * half] - from[half]), e1 = exp2_fast(s[m][x][b][2 * half + 1] - from[half]);
-                            sum[m][half] += e0 + e1;
-                            w[m][x][b * 2 + half] = BF16 ? pack<__nv_bfloat16>(e0, e1) : pack<__half>(e0, e1);
-                        }
-            }
-
-            // weights times values
-            const uint32_t v_at = at + S::kv;
-            auto both = [&](int x, int n8, const uint32_t *b) {  // two pieces of eight elements
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (edge) {
-                        // A weight of 0 times a value that is not finite is NaN in a product: such pieces, if any, by hand.
-                        bool odd = false;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t mask = BF16 ? 0x7f80u : 0x7c00u;
-                            odd |= (b[c] & mask) == mask || (b[c] >> 16 & mask) == mask;
-                        }
-                        if (__any_sync(~0u, odd)) {
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
+    const uint32_t tensor = __shfl_sync(~0u, sh.tensor_at, 0);
+    const int ctas = static_cast<int>(min(total, static_cast<u64>(gridDim.x)));  // (each with a tile at least)
+    int n = 0;
+    u64 u0 = 0, u1 = 0;
+    if (cta < ctas) {
+        u0 = share_of(total, cta, ctas), u1 = share_of(total, cta + 1, ctas);
+        n = __shfl_sync(~0u, static_cast<int>(u1 - u0), 0);
+        if (u0 >= before && u0 < before + mine) {
+            u64 at = before;
+            int k = tid * per;
+            if (per > 1)
 #pragma unroll 1
-                                for (int key = 0; key < 8; ++key) {
-                                    // weights of the rows g and g + 8: in lane key / 2 of the four; values of the
-                                    // elements 2 t4 and 2 t4 + 1: in the lanes 8 t4 + key / 2 and 4 behind
-                                    const int in = key / 2, high = key & 1;
-                                    using E = std::conditional_t<BF16, __nv_bfloat16, __half>;
-                                    auto part = [&](uint32_t v, int from) {
-                                        const float2 f = pair_of<E>(__shfl_sync(~0u, v, from));
-                                        return high ? f.y : f.x;
-                                    };
-                                    const float w0 = part(w[m][x][kk * 2], (lane & ~3) | in), w1 = part(w[m][x][kk * 2 + 1], (lane & ~3) | in);
+                for (; k < min(P.s.n, (tid + 1) * per) - 1; ++k) {
+                    const u64 here = walk.request_tiles(k);
+                    if (u0 < at + here) break;
+                    at += here;
+                }
+            sh.start[0] = static_cast<u64>(k);
+            sh.start[1] = u0 - at;
+        }
+    } else if (P.parts && tid == 0) {
+        st(&P.parts[cta].first, -1);
+    }
+    __syncthreads();
+    int *const lost = &sh.lost;
+
+    if (warp < 4) {
+        SV_CACHE_REGISTERS("inc", 216);
+        // -- weights: this thread has the key `tid` of every tile, and the elements tid and tid + 128 of the outputs
+        const uint32_t lanes = tensor + (static_cast<uint32_t>(warp) << 21);  // (lane 32 * warp of the tensor memory, in bits 16 and up)
+        float sum[N];
+        float scale = 0;
+#pragma unroll 1
+        for (int it = 0; it < n; ++it) {
+            const int b = it & 1;
+            const uint32_t turn = it >> 1 & 1;
+            auto &h = sh.head[it % S::heads];
+            barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+            const int flags = h.flags;
+            if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, lost);  // (the weights' room is free, and the values before the last have come)
+            int r_lo = 0, r_hi = N;  // the rows that see this thread's key
+            if (flags & kFirst) {
+                const int head = h.head;
+                scale = P.scale * (P.k_scale ? ld(P.k_scale + head) : 1.0f);
 #pragma unroll
-                                    for (int piece = 0; piece < 2; ++piece) {
-                                        const float b0 = part(b[piece * 2 + kk], t4 * 8 + in), b1 = part(b[piece * 2 + kk], t4 * 8 + 4 + in);
-                                        float *c = o[m][n8 + piece];
-                                        if (w0 != 0) c[0] = fmaf(w0, b0, c[0]), c[1] = fmaf(w0, b1, c[1]);
-                                        if (w1 != 0) c[2] = fmaf(w1, b0, c[2]), c[3] = fmaf(w1, b1, c[3]);
-                                    }
-                                }
-                            continue;
+                for (int r = 0; r < N; ++r) sum[r] = 0;
+                if constexpr (kWide) {
+                    const int segment = h.segment;
+                    barrier_wait(sh.q_full + segment % S::q_buffers, segment / S::q_buffers & 1, lost);
+                    if (tid < N) sh.scale[tid] = scale * sh.q_scale[segment % S::q_buffers][tid];
+                    weights_meet();
+                    if (tid == 0) barrier_arrive(sh.q_empty + segment % S::q_buffers);  // (the factors have been read; the first product adds its arrival)
+                }
+            }
+            if (flags & kEdge) {
+                const i64 d = static_cast<i64>(h.p0) + tid - h.length;  // it is the d-th new token's place
+                const i64 lo = d <= 0 ? 0 : d * P.group - h.from, hi = P.window > 0 ? (d + P.window) * P.group - h.from : N;
+                r_lo = static_cast<int>(min(max(lo, 0ll), static_cast<i64>(N)));
+                r_hi = static_cast<int>(min(max(hi, 0ll), static_cast<i64>(N)));
+                if (!(h.seen[tid / 32] >> (tid & 31) & 1)) r_hi = 0;
+                // A weight of 0 times a value that is not finite would be NaN. Such elements, if any, are set to 0 in shared
+                // memory, and what they make of the rows that see them is added by hand.
+                const int vslot = it % S::v_slots;
+                barrier_wait(sh.v_full + vslot, it / S::v_slots & 1, lost);
+                unsigned char *const v = room + (S::k_slots + vslot) * S::slot;
+                auto chunk = [&](int key, int c) { return reinterpret_cast<uint4 *>(v + c / 8 * S::piece + key * 128 + (((c & 7) ^ (key & 7)) << 4)); };
+                constexpr uint32_t mask = kBf16 ? 0x7f80u : 0x7c00u;
+                bool odd = false;
+#pragma unroll 2
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = *chunk(tid, c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+                        odd |= (w & mask) == mask || (w >> 16 & mask) == mask;
+                    }
+                }
+                if (weights_any(odd)) {
+                    // (rare: one row at a time, every element over all keys)
+                    if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
+                    tensor_after();
+#pragma unroll 1
+                    for (int e = 0; e < S::blocks; ++e)
+#pragma unroll 1
+                        for (int r = 0; r < N; ++r) {
+                            const uint32_t at = lanes + (2 + e) * N + r;
+                            uint32_t w;
+                            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(at) : "memory");
+                            tensor_loaded();
+                            float x = flags & kFirst ? 0.0f : __uint_as_float(w);
+                            const int element = e * 128 + tid;
+#pragma unroll 1
+                            for (int key = 0; key < kTile && element < D; ++key) {
+                                const i64 dk = static_cast<i64>(h.p0) + key - h.length;
+                                if (!(h.seen[key / 32] >> (key & 31) & 1) || (dk > 0 && r < dk * P.group - h.from) || (P.window > 0 && r >= (dk + P.window) * P.group - h.from)) continue;
+                                const float y = static_cast<float>(reinterpret_cast<const E *>(chunk(key, element / 8))[element & 7]);
+                                if (!(fabsf(y) < kInf)) x += y;
+                            }
+                            __syncwarp();
+                            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(__float_as_uint(x)) : "memory");
+                        }
+                    tensor_stored();
+                    tensor_before();
+                    weights_meet();
+#pragma unroll 1
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint32_t *x = reinterpret_cast<uint32_t *>(chunk(tid, c));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((x[k] & mask) == mask) x[k] &= 0xffff0000u;
+                            if ((x[k] >> 16 & mask) == mask) x[k] &= 0xffffu;
                         }
                     }
-                    multiply<BF16>(o[m][n8], w[m][x], b[0], b[1]);
-                    multiply<BF16>(o[m][n8 + 1], w[m][x], b[2], b[3]);
+                    shared_to_async();
+                    if (tid == 0) h.started = 1;
+                }
+            }
+
+            // -- the scores relative to the reference; a new one where some score is too far above it
+            barrier_wait(sh.scores + b, turn, lost);
+            tensor_after();
+            const uint32_t scores_at = lanes + b * N;
+            float s[N];
+            auto relative = [&] {
+#pragma unroll
+                for (int c = 0; c < N; c += 16) tensor_load16(s + c, scores_at + c);
+                tensor_loaded();
+#pragma unroll
+                for (int r = 0; r < N; r += 4) {
+                    const float4 less = *reinterpret_cast<const float4 *>(sh.less + r);
+                    const float4 by = kWide ? *reinterpret_cast<const float4 *>(sh.scale + r) : make_float4(scale, scale, scale, scale);
+                    s[r] = fmaf(s[r], by.x, less.x), s[r + 1] = fmaf(s[r + 1], by.y, less.y);
+                    s[r + 2] = fmaf(s[r + 2], by.z, less.z), s[r + 3] = fmaf(s[r + 3], by.w, less.w);
+                }
+                if (flags & kEdge) {
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        if (r < r_lo || r >= r_hi) s[r] = -kInf;
                 }
             };
-            const int token = token0 + (lane >> 3 & 1) * 8 + (lane & 7);
+            bool renew = flags & kFirst;
+            if (!renew) {
+                relative();
+                float far[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-            for (int x = 0; x < S::sub; ++x) {
-                if constexpr (ES == 2) {
+                for (int r = 0; r < N; ++r) far[r & 3] = fmaxf(far[r & 3], s[r]);
+                renew = weights_any(fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) > W::offset + W::slack);
+            }
+            if (renew) {
+#pragma unroll 1
+                for (int c = 0; c < N; c += 16) {
+                    float v[16];
+                    tensor_load16(v, scores_at + c);
+                    tensor_loaded();
 #pragma unroll
-                    for (int e = 0; e < D / 16; ++e) {
-                        uint32_t b[4];
-                        matrices_turned(b, v_at + swizzled<S::chunks>(token + x * 16, e * 2 + (lane >> 4)));
-                        both(x, 2 * e, b);
+                    for (int r = 0; r < 16; ++r) v[r] = c + r < r_lo || c + r >= r_hi ? -kInf : v[r] * (kWide ? sh.scale[c + r] : scale);
+                    const float most = columns_largest(v, lane);
+                    if (lane < 16) sh.most[warp][c + lane] = most;
+                }
+                weights_meet();
+                if (tid < N) {
+                    const float old = flags & kFirst ? -kInf : sh.top[tid];
+                    const float top = larger(larger(larger(sh.most[0][tid], sh.most[1][tid]), larger(sh.most[2][tid], sh.most[3][tid])), old);
+                    sh.factor[tid] = top == old ? 1.0f : exp2_fast(old - top);
+                    sh.top[tid] = top;
+                    sh.less[tid] = top == -kInf ? 0x1p120f : W::offset - top;  // (no key yet: any score is far above)
+                }
+                weights_meet();
+                if (!(flags & kFirst)) {
+                    barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
+                    tensor_after();
+#pragma unroll 1
+                    for (int c = 0; c < S::blocks * N; c += 16) {
+                        float o[16];
+                        tensor_load16(o, lanes + 2 * N + c);
+                        tensor_loaded();
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) o[r] *= sh.factor[(c % N) + r];
+                        tensor_store16(lanes + 2 * N + c, o);
                     }
-                } else {
+                    tensor_stored();
+                    tensor_before();
 #pragma unroll
-                    for (int e = 0; e < D / 16; e += 2) {
-                        uint32_t r[4];
-                        matrices_turned(r, v_at + swizzled<S::chunks>(token + x * 16, e + (lane >> 4)));
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            // two keys, two neighbouring elements in each register: first both keys of the even element
-                            const uint32_t a0 = __byte_perm(r[2 * c], 0, 0x3120), a1 = __byte_perm(r[2 * c + 1], 0, 0x3120);
-                            const uint32_t b[4] = {half2_of_e4m3(a0), half2_of_e4m3(a1), half2_of_e4m3(a0 >> 16), half2_of_e4m3(a1 >> 16)};
-                            both(x, 2 * (e + c), b);
-                        }
+                    for (int r = 0; r < N; r += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sh.factor + r);
+                        sum[r] *= f.x, sum[r + 1] *= f.y, sum[r + 2] *= f.z, sum[r + 3] *= f.w;
                     }
+                }
+                relative();
+            }
+            // -- weights, to shared memory as the product wants them: eight rows of a key side by side
+            unsigned char *const to = w_room + b * S::weights + tid * 16;
+#pragma unroll
+            for (int r = 0; r < N; r += 8) {
+                float e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    e[k] = exp2_fast(s[r + k]);
+                    sum[r + k] += e[k];
+                }
+                *reinterpret_cast<uint4 *>(to + r / 8 * (kTile * 16)) = make_uint4(pack<E>(e[0], e[1]), pack<E>(e[2], e[3]), pack<E>(e[4], e[5]), pack<E>(e[6], e[7]));
+            }
+            shared_to_async();
+            tensor_before();
+            const int head = h.head, from = h.from, count = h.count, first_row = h.first;
+            const int part_first = h.part_first, part_last = h.part_last, part_slot = h.part_slot;  // (before others may take the description's room)
+            barrier_arrive(sh.weighed + b);
+            if (!(flags & kLast)) continue;
+
+            // -- a segment's end: the sums over the keys, and the result or the part written
+            barrier_wait(sh.done + b, turn, lost);
+            if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
+            tensor_after();
+            float *const all = reinterpret_cast<float *>(w_room);  // (both rooms for weights are free)
+#pragma unroll
+            for (int r = 0; r < N; ++r) all[r * kTile + tid] = sum[r];
+            weights_meet();
+            const float vs = P.v_scale ? ld(P.v_scale + head) : 1.0f;
+            const float sound = *reinterpret_cast<volatile int *>(lost) ? __int_as_float(0x7fffffff) : 1.0f;
+#pragma unroll 1
+            for (int r = warp; r < N; r += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(all + r * kTile + lane * 4);
+                float z = (x.x + x.y) + (x.z + x.w);
+#pragma unroll
+                for (int d = 16; d; d /= 2) z += __shfl_xor_sync(~0u, z, d);
+                if (lane == 0) {
+                    const bool none = sh.top[r] == -kInf;
+                    sh.sum[r] = none ? 0.0f : z * sound;
+                    sh.factor[r] = none ? 0.0f : sound * (flags & kPartial ? 1.0f : vs / z);
                 }
             }
-        }
-
-        // -- a segment's end: the slices joined, and the result or the part written
-        if (flags & kLast) {
+            weights_meet();
+            const i64 part = (static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0)) * N;
+#pragma unroll 1
+            for (int c = 0; c < S::blocks * N; c += 16) {
+                float o[16];
+                tensor_load16(o, lanes + 2 * N + c);
+                tensor_loaded();
+                const int e = (c < N ? 0 : 128) + tid, r0 = c % N;
+                int j = (from + r0) / P.group, g = from + r0 - j * P.group;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    sum[m][half] += __shfl_xor_sync(~0u, sum[m][half], 1);
-                    sum[m][half] += __shfl_xor_sync(~0u, sum[m][half], 2);
-                    if (t4 == 0) sh.stat[slice][row_base + m * 16 + g + half * 8] = make_float2(top[m][half], sum[m][half]);
-                }
-            __syncthreads();  // (and every warp is through with the stage)
-            float *buffer = reinterpret_cast<float *>(room + (it % S::stages) * S::stage);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = row_base + m * 16 + g + half * 8;
-                    float most = -kInf, z = 0;
-#pragma unroll
-                    for (int w = 0; w < kSlices; ++w) most = fmaxf(most, sh.stat[w][r].x);
-                    const float from = most == -kInf ? 0.0f : most;
-#pragma unroll
-                    for (int w = 0; w < kSlices; ++w) {
-                        const float2 x = sh.stat[w][r];
-                        z += x.y * (x.x == most ? 1.0f : exp2_fast(x.x - from));
+                for (int k = 0; k < 16; ++k) {
+                    const int r = r0 + k;
+                    if (r < count && (D >= 128 || e < D)) {
+                        const float f = sh.factor[r], y = f == 0 ? 0.0f : o[k] * f;
+                        if (flags & kPartial)
+                            st(P.sums + (part + r) * D + e, y);
+                        else
+                            st(reinterpret_cast<E *>(P.out + static_cast<i64>(first_row + j) * P.out_row + static_cast<i64>(head * P.group + g) * P.out_head) + e,
+                               kWide && P.bf16 ? from_bits<E>(__float2bfloat16_rn(y)) : from_bits<E>(static_cast<E>(y)));
                     }
-                    const float keep = top[m][half] == most ? 1.0f : exp2_fast(top[m][half] - from);
-#pragma unroll
-                    for (int e = 0; e < D / 8; ++e) o[m][e][2 * half] *= keep, o[m][e][2 * half + 1] *= keep;
-                    if (slice == 0 && t4 == 0) sh.joined[r] = make_float2(most, z);
+                    if (++g == P.group) g = 0, ++j;
                 }
-            constexpr int kTurns = kSlices / S::buffers;
+            }
+            if (tid < count) {
+                const float top = sh.top[tid], z = sh.sum[tid];
+                const int at_row = from + tid, j = at_row / P.group;
+                if (flags & kPartial)
+                    st(P.stats + part + tid, make_float2(top, z));
+                else if (P.lse)
+                    st(P.lse + static_cast<i64>(first_row + j) * P.hq + head * P.group + at_row - j * P.group, z == 0 ? -kInf : (top - W::offset + log2f(z)) * kLn2);
+            }
+            if (tid == 0 && P.parts && it == n - 1) {
+                const bool open = flags & kOpen;
+                st(reinterpret_cast<int4 *>(P.parts + cta), make_int4(open ? part_first : -1, part_last, part_slot, first_row));
+                st(reinterpret_cast<int4 *>(P.parts + cta) + 1, make_int4(from, count, head, 0));
+            }
+            tensor_before();
+            weights_meet();  // (the sums' room takes weights again)
+        }
+    } else if (warp < 8) {
+        SV_CACHE_REGISTERS("dec", 72);
+        if (warp == 4) {
+            // -- scores^T = K Q^T
+            const uint32_t leader = elected();
+            constexpr uint32_t kShape = product_of(kBf16, N, false);
+#pragma unroll 1
+            for (int it = 0; it < n; ++it) {
+                const int s = it % S::k_slots;
+                if (it >= 2) barrier_wait(sh.weighed + (it & 1), (it >> 1 & 1) ^ 1, lost);  // (its scores have been read)
+                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                const auto &h = sh.head[it % S::heads];
+                const int flags = __shfl_sync(~0u, h.flags, 0), segment = __shfl_sync(~0u, h.segment, 0), qb = segment % S::q_buffers;
+                if (flags & kFirst) barrier_wait(sh.q_full + qb, segment / S::q_buffers & 1, lost);
+                barrier_wait(sh.k_full + s, it / S::k_slots & 1, lost);
+                tensor_after();
+                const u64 a = matrix_at(room_at + s * S::slot, 16, 1024, 2), q = matrix_at(q_at + qb * S::q_bytes, 16, 1024, 2);
 #pragma unroll
-            for (int turn = 0; turn < kTurns; ++turn) {
-                if (slice / S::buffers == turn) {
-                    float *to = buffer + slice % S::buffers * S::rows * D;
+                for (int k = 0; k < D / 16; ++k)
+                    product(tensor + (it & 1) * N, static_cast<uint32_t>(a) + (k / 4 * S::piece + k % 4 * 32) / 16, static_cast<uint32_t>(a >> 32),
+                            static_cast<uint32_t>(q) + (k / 4 * (N * 128) + k % 4 * 32) / 16, static_cast<uint32_t>(q >> 32), kShape, k > 0, leader);
+                products_close(sh.scores + (it & 1), leader);
+                products_close(sh.k_empty + s, leader);
+                if (flags & kLast) products_close(sh.q_empty + qb, leader);
+            }
+        } else if (warp == 5) {
+            // -- out^T += V^T weights^T
+            const uint32_t leader = elected();
+            constexpr uint32_t kShape = product_of(kBf16, N, true);
+#pragma unroll 1
+            for (int it = 0; it < n; ++it) {
+                const int s = it % S::v_slots, b = it & 1;
+                barrier_wait(sh.v_full + s, it / S::v_slots & 1, lost);
+                barrier_wait(sh.weighed + b, it >> 1 & 1, lost);
+                tensor_after();
+                const auto &h = sh.head[it % S::heads];
+                const bool first = __shfl_sync(~0u, h.flags & kFirst && !h.started, 0);
+                // 64 elements of 8 keys are 1024 bytes; the next 64 elements are a piece further (with 64 in all: the same again,
+                // into rows of the memory that nobody reads)
+                const u64 a = matrix_at(room_at + (S::k_slots + s) * S::slot, D == 64 ? 0 : S::piece, 1024, 2), w = matrix_at(w_at + b * S::weights, 128, kTile * 16, 0);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                for (int e = 0; e < S::blocks; ++e)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int r = row_base + m * 16 + g + half * 8;
+                    for (int k = 0; k < kTile / 16; ++k)
+                        product(tensor + (2 + e) * N, static_cast<uint32_t>(a) + (e * 2 * S::piece + k * 2048) / 16, static_cast<uint32_t>(a >> 32),
+                                static_cast<uint32_t>(w) + k * 256 / 16, static_cast<uint32_t>(w >> 32), kShape, k > 0 || !first, leader);
+                products_close(sh.done + b, leader);
+                products_close(sh.v_empty + s, leader);
+                products_close(sh.used + it % S::heads, leader);
+            }
+        } else if (warp == 6 && n > 0) {
+            // -- plan: this lane has places lane, 32 + lane, ... of each tile
+            walk.seek(static_cast<int>(sh.start[0]), sh.start[1], u0);
+            int segment = -1;
+#pragma unroll 1
+            for (int it = 0; it < n; ++it) {
+                // the tile's places: p0 and `places` more; a tile in parts of a page starts at its slot `slot0`
+                int p0 = walk.t * P.cut.span, places = P.cut.span, c0 = walk.t * P.cut.boxes, slot0 = 0;
+                if (P.cut.parts > 1) {
+                    c0 = walk.t / P.cut.parts;
+                    slot0 = (walk.t - c0 * P.cut.parts) * P.cut.box;
+                    p0 = c0 * P.s.page + slot0;
+                    places = min(P.cut.box, P.s.page - slot0);
+                }
+                int page[4], in[4];
 #pragma unroll
-                            for (int e = 0; e < D / 8; ++e) {
-                                // (for e4m3 two pieces are the even and the odd elements of 16)
-                                const int c0 = ES == 2 ? e * 8 + 2 * t4 : e / 2 * 16 + 4 * t4 + e % 2;
-                                float *x = to + r * D + (c0 ^ (r & 7) << 3), *y = x + (ES == 2 ? 1 : 2);
-                                *x = o[m][e][2 * half] + (turn ? *x : 0.0f);
-                                *y = o[m][e][2 * half + 1] + (turn ? *y : 0.0f);
+                for (int w = 0; w < 4; ++w) {
+                    const int k = w * 32 + lane, p = p0 + k, c = page_of(P.s, p);
+                    page[w] = -1;
+                    in[w] = loads ? k : P.cut.parts > 1 ? 0 : c - c0;  // its box, and the box's places
+                    const int lo = loads ? p : P.cut.parts > 1 ? p0 : c * P.s.page, hi = loads ? p + 1 : P.cut.parts > 1 ? p0 + places : lo + P.s.page;
+                    if (walk.rows && k < places && lo < walk.end && hi > walk.start) page[w] = ld(P.s.table + walk.i * P.s.table_stride + c);
+                    if (!loads && p != lo) in[w] = -1;  // (the box's first place speaks for it)
+                }
+                const int k = it % S::heads;
+                if (it >= S::heads) barrier_wait(sh.used + k, (it / S::heads - 1) & 1, lost);
+                auto &h = sh.head[k];
+                bool all = true;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int p = p0 + w * 32 + lane;
+                    bool there = page[w] >= 0 && page[w] < P.s.pages;
+#ifdef SV_DEBUG_BOUNDS
+                    const int sl = p - page_of(P.s, p) * P.s.page;
+                    if (there && w * 32 + lane < places)
+                        there = inside(P.kc.at + page[w] * P.kc.page + sl * P.kc.slot + walk.head * P.kc.head, D * S::bytes_of, false) &&
+                                inside(P.vc.at + page[w] * P.vc.page + sl * P.vc.slot + walk.head * P.vc.head, D * S::bytes_of, false);
+#endif
+                    const uint32_t seen = __ballot_sync(~0u, there && w * 32 + lane < places && p >= walk.start && p < walk.end);
+                    all = all && seen == ~0u;
+                    if (lane == 0) h.seen[w] = seen;
+                    if (in[w] >= 0 && w * 32 + lane < places) h.page[in[w]] = there ? page[w] : loads ? -1 : P.s.pages;  // (a page behind the last: zeros)
+                }
+                const bool opens = walk.t == walk.t0, ends = walk.t + 1 == walk.t1;
+                const bool first = it == 0 || opens, last = it == n - 1 || ends;
+                if (first) ++segment;
+                if (lane == 0) {
+                    const int j0 = walk.from / P.group, j1 = (walk.from + walk.count - 1) / P.group;
+                    const bool part = walk.base < u0 || walk.base + static_cast<u64>(walk.tiles()) > u1;
+                    all = all && static_cast<i64>(p0) + kTile - 1 <= static_cast<i64>(walk.length) + j0 &&
+                          (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
+                    h.p0 = p0;
+                    h.first = walk.first;
+                    h.count = walk.count;
+                    h.from = walk.from;
+                    h.head = walk.head;
+                    h.length = walk.length;
+                    h.segment = segment;
+                    h.slot = slot0;
+                    h.started = 0;  // (1: sums of the segment are there before its first product)
+                    h.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (part ? kPartial : 0) | (walk.base > u0 ? kSlot : 0) | (last && !ends ? kOpen : 0) | (all ? 0 : kEdge);
+                    if (last && !ends) {  // the CTAs that have tiles of the group
+                        h.part_first = sharer_of(total, walk.base, ctas);
+                        h.part_last = sharer_of(total, walk.base + static_cast<u64>(walk.tiles()) - 1, ctas);
+                        h.part_slot = share_of(total, h.part_first, ctas) < walk.base;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) barrier_arrive(sh.told + k);
+                walk.next();
+            }
+        } else if (warp == 7) {
+            // -- keys by boxes, and queries
+            int s = 0;
+            uint32_t turn = 0;  // times the ring has been gone round, as the parity waited for
+#pragma unroll 1
+            for (int it = 0; it < n; ++it) {
+                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                const auto &h = sh.head[it % S::heads];
+                const int flags = h.flags, head = h.head;
+                if (!loads) {
+                    boxes_to<S>(&maps.k, sh.k_full + s, sh.k_empty + s, it >= S::k_slots, turn ^ 1, room_at + s * S::slot, P.cut, h.slot, head, h.page, lane, lost);
+                    if (++s == S::k_slots) s = 0, turn ^= 1;
+                }
+                if (flags & kFirst) {
+                const int segment = h.segment, qb = segment % S::q_buffers, from = h.from, count = h.count, first = h.first;
+                if (segment >= S::q_buffers) barrier_wait(sh.q_empty + qb, (segment / S::q_buffers - 1) & 1, lost);
+                if constexpr (!kWide) {
+                    if (lane == 0) barrier_expect(sh.q_full + qb, S::q_bytes);
+                    __syncwarp();
+                    const int box = P.cut.q_box;  // rows of one token side by side, so that no box has two tokens
+#pragma unroll 1
+                    for (int r = lane * box; r < N; r += 32 * box) {
+                        const int at_row = from + r, j = at_row / P.group;
+                        const int row = r < count ? first + j : P.s.rows;  // (a row behind the last: zeros)
+#pragma unroll 1
+                        for (int e = 0; e < S::halves; ++e)
+                            copy_box(q_at + qb * S::q_bytes + e * (N * 128) + r * 128, &maps.q, sh.q_full + qb, e * 64, head * P.group + at_row - j * P.group, row, 0);
+                    }
+                } else {
+                    // queries in binary16: bf16 ones times a power of two that takes the row's largest to [2^13, 2^14), exact down
+                    // to 2^-28 of it
+                    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at once
+                    const int c = lane % kLanes;
+#pragma unroll 1
+                    for (int r = lane / kLanes; r < N; r += 4 * kAtOnce) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int rr = r + k * kAtOnce, at_row = from + min(rr, count - 1), j = at_row / P.group;
+                            x[k] = make_uint4(0, 0, 0, 0);
+                            if (rr < count)
+                                x[k] = ld(reinterpret_cast<const uint4 *>(P.q + static_cast<i64>(first + j) * P.q_row + static_cast<i64>(head * P.group + at_row - j * P.group) * P.q_head) + c);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int rr = r + k * kAtOnce;
+                            float less = 1.0f;
+                            if (P.bf16) {
+                                uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                                float most = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = pair_of<__nv_bfloat16>(w[e]);
+                                    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+                                }
+#pragma unroll
+                                for (int d = kLanes / 2; d; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+                                const int up = min(110, 13 - (static_cast<int>(__float_as_uint(most) >> 23) - 127));
+                                const float more = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                                less = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = pair_of<__nv_bfloat16>(w[e]);
+                                    w[e] = pack<__half>(f.x * more, f.y * more);
+                                }
+                                x[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            if (rr < N) {
+                                *reinterpret_cast<uint4 *>(q_room + qb * S::q_bytes + c / 8 * (N * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[k];
+                                if (c == 0) sh.q_scale[qb][rr] = less;
                             }
                         }
+                    }
+                    shared_to_async();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(sh.q_full + qb);
                 }
-                __syncthreads();
-            }
-            const float vs = P.v_scale ? ld(P.v_scale + h.head) : 1.0f;
-            const i64 part = static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0);
-            for (int x = tid; x < h.count * (D / 4); x += S::threads) {
-                const int r = x / (D / 4), c = x % (D / 4) * 4, at_row = h.from + r, j = at_row / P.group;
-                float4 v = *reinterpret_cast<const float4 *>(buffer + r * D + (c ^ (r & 7) << 3));
-                if constexpr (S::buffers == 2) {
-                    const float4 u = *reinterpret_cast<const float4 *>(buffer + (S::rows + r) * D + (c ^ (r & 7) << 3));
-                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
                 }
-                const float2 stat = sh.joined[r];
-                if (flags & kPartial) {
-                    st(reinterpret_cast<float4 *>(P.sums + (part * S::rows + r) * D + c), v);
-                    if (c == 0) st(P.stats + part * S::rows + r, stat);
-                } else {
-                    const int qh = h.head * P.group + at_row - j * P.group;
-                    const float f = stat.y == 0 ? 0.0f : vs / stat.y;
-                    const float4 y = stat.y == 0 ? make_float4(0, 0, 0, 0) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-                    const bool bf16 = BF16 || P.bf16;
-                    const uint2 w = bf16 ? make_uint2(pack<__nv_bfloat16>(y.x, y.y), pack<__nv_bfloat16>(y.z, y.w)) : make_uint2(pack<__half>(y.x, y.y), pack<__half>(y.z, y.w));
-                    st(reinterpret_cast<uint2 *>(P.out + (h.first + j) * P.out_row + qh * P.out_head + c * 2), w);
-                    if (c == 0 && P.lse) st(P.lse + static_cast<i64>(h.first + j) * P.hq + qh, stat.y == 0 ? -kInf : (stat.x - kOffset + log2f(stat.y)) * kLn2);
-                }
+                __syncwarp();
+                if (lane == 0) barrier_arrive(sh.used + it % S::heads);
             }
-            if (flags & kOpen && tid == 0) {
-                const Part x{h.part_first, h.part_last, h.part_slot, h.first, h.from, h.count, h.head, 0};
-                st(reinterpret_cast<int4 *>(P.parts + cta), make_int4(x.first, x.last, x.slot, x.row0));
-                st(reinterpret_cast<int4 *>(P.parts + cta) + 1, make_int4(x.from, x.count, x.head, 0));
-            }
-            part_written = flags & kOpen;
         }
-        if (more) describe(it + S::stages);
+    } else {
+        SV_CACHE_REGISTERS("dec", 112);
+        if (!loads) {
+            if (warp == 8) {
+                // -- values by boxes
+                int s = 0;
+                uint32_t turn = 0;
+#pragma unroll 1
+                for (int it = 0; it < n; ++it) {
+                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                    const auto &h = sh.head[it % S::heads];
+                    boxes_to<S>(&maps.v, sh.v_full + s, sh.v_empty + s, it >= S::v_slots, turn ^ 1, room_at + (S::k_slots + s) * S::slot, P.cut, h.slot, h.head, h.page, lane, lost);
+                    if (++s == S::v_slots) s = 0, turn ^= 1;
+                }
+            }
+        } else {
+            // -- keys and values by loads: pieces (a tile's keys, its values, the next tile's keys, ...) of which `kAhead` are on
+            // the way to registers
+            constexpr int kRow = D * S::bytes_of / 16, kEvery = 256 / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's
+            constexpr int kAhead = 16 / kEach < 1 ? 1 : 16 / kEach > 4 ? 4 : 16 / kEach;
+            const int x = tid - 256, c = x % kRow, key0 = x / kRow;
+            uint4 data[kAhead][kEach];
+            auto load = [&](int u, uint4 *to) {
+                const int it = u >> 1;
+                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                const auto &h = sh.head[it % S::heads];
+                const Cache &from = u & 1 ? P.vc : P.kc;
+                const unsigned char *const at = from.at + static_cast<i64>(h.head) * from.head + c * 16;
+                const int p0 = h.p0;
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int key = key0 + k * kEvery, page = h.page[key], p = p0 + key, slot = p - page_of(P.s, p) * P.s.page;
+                    to[k] = make_uint4(0, 0, 0, 0);
+                    if (page >= 0) to[k] = ld_stream(reinterpret_cast<const uint4 *>(at + page * from.page + slot * from.slot));
+                }
+            };
+            auto store = [&](int u, const uint4 *from) {
+                const int it = u >> 1, slots = u & 1 ? S::v_slots : S::k_slots, s = it % slots;
+                u64 *const full = (u & 1 ? sh.v_full : sh.k_full) + s, *const empty = (u & 1 ? sh.v_empty : sh.k_empty) + s;
+                if (it >= slots) barrier_wait(empty, (it / slots - 1) & 1, lost);
+                unsigned char *const to = room + ((u & 1 ? S::k_slots : 0) + s) * S::slot;
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int key = key0 + k * kEvery;
+                    auto put = [&](int chunk, const uint4 &w) { *reinterpret_cast<uint4 *>(to + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4)) = w; };
+                    if constexpr (kWide) {
+                        put(2 * c, make_uint4(half2_of_e4m3(from[k].x), half2_of_e4m3(from[k].x >> 16), half2_of_e4m3(from[k].y), half2_of_e4m3(from[k].y >> 16)));
+                        put(2 * c + 1, make_uint4(half2_of_e4m3(from[k].z), half2_of_e4m3(from[k].z >> 16), half2_of_e4m3(from[k].w), half2_of_e4m3(from[k].w >> 16)));
+                    } else {
+                        put(c, from[k]);
+                    }
+                }
+                shared_to_async();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(full);
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k < 2 * n) load(k, data[k]);
+#pragma unroll 1
+            for (int u = 0; u < 2 * n; u += kAhead)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (u + k < 2 * n) {
+                        store(u + k, data[k]);
+                        if (u + k + kAhead < 2 * n) load(u + k + kAhead, data[k]);
+                    }
+        }
     }
-    if (!part_written && P.parts && tid == 0) st(&P.parts[cta].first, -1);
+    if (*reinterpret_cast<volatile int *>(lost) && !loads && (warp == 7 || warp == 8)) {  // copies in flight end before the block does
+        const int slots = warp == 8 ? S::v_slots : S::k_slots;
+        for (int it = max(0, n - slots); it < n; ++it)
+            for (int k = 0; k < kPatience && !barrier_try((warp == 8 ? sh.v_full : sh.k_full) + it % slots, it / slots & 1); ++k) {
+            }
+    }
+    tensor_before();
+    __syncthreads();
+    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(S::columns) : "memory");
 }
 
 // Joins the parts of the groups that more than one CTA has. A group over k + 1 CTAs has k CTAs here, which share its
