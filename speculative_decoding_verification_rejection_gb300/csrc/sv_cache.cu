@@ -684,7 +684,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     }
     // Each kernel may start while the one before it ends; it waits for that on the device before it looks at memory.
     void *params[] = {&P, &maps};
-    int rc_launch = launch_after(kernel.run, static_cast<unsigned>(ctas), 512, kernel.bytes, stream, params);
+    int rc_launch = launch_after(kernel.run, static_cast<unsigned>(ctas), 640, kernel.bytes, stream, params);
     if (rc_launch != SV_OK || !workspace) return rc_launch;
     int rows = kernel.rows;
     float offset = kernel.offset;

@@ -53,9 +53,9 @@ enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge =
 // A tile is up to 128 keys. Both products have the keys or the elements in the 128 rows of the tensor cores' memory and
 // the query rows (N, 16 to 64) in its columns: scores^T = K Q^T, and out^T += V^T weights^T. So few query rows
 // waste nothing, and every key is read from shared memory once for all of them. Roles, each a warp or more: weights
-// (four warps; a thread has one key's scores of all rows), the first product, the second, a plan (the tiles and their
-// pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are 8 bits or
-// the pages small, by eight warps that load, widen and store them.
+// (twice four warps; a thread has one key's scores of half of the rows), the first product, the second, a plan (the tiles
+// and their pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are
+// 8 bits or the pages small, by eight warps that load, widen and store them.
 template <int KIND, int D, int N>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
 struct Tile {
     static constexpr bool bf16 = KIND == SV_BF16;    // type of the products
@@ -74,7 +74,8 @@ struct Tile {
     static constexpr int blocks = D == 256 ? 2 : 1;  // of 128 elements
     static constexpr int columns_used = (2 + blocks) * N;
     static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
-    static constexpr int threads = 512;
+    static constexpr int threads = 640;
+    static constexpr int mine = N / 2;                // rows of a weights warp
     static_assert(slots >= 2 && columns_used <= 256, "room");
     struct Head {
         int p0, first, count, from, head, length, flags, segment;
@@ -89,9 +90,9 @@ struct Tile {
         alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
         alignas(16) float factor[N];  // what a new reference makes of the old sums; of the result
         alignas(16) float scale[N];   // of the scores
-        alignas(16) float most[4][N];
+        alignas(16) float most[4][N];  // by warps: largest scores, sums of weights
         float top[N];                 // the reference, times log2 e
-        float sum[N];
+        i64 row_at[N];                // where a row's result goes, in bytes from its array's start; -1: nowhere
         float q_scale[2][N];          // of queries held in binary16
         u64 scan[threads / 32];
         u64 start[2];
@@ -292,40 +293,36 @@ __device__ __forceinline__ void products_close(u64 *b, uint32_t leader)
                  "r"(leader)
                  : "memory");
 }
-__device__ __forceinline__ void tensor_load16(float *v, uint32_t at)
+__device__ __forceinline__ void tensor_load8(float *v, uint32_t at)
 {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at)
-        : "memory");
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at)
+                 : "memory");
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r[k]);
 }
-__device__ __forceinline__ void tensor_store16(uint32_t at, const float *v)
+__device__ __forceinline__ void tensor_store8(uint32_t at, const float *v)
 {
-    uint32_t r[16];
+    uint32_t r[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(v[k]);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]),
-        "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(at)
-        : "memory");
+    for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(v[k]);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+                 "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
+                 : "memory");
 }
 __device__ __forceinline__ void tensor_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tensor_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tensor_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tensor_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// The four warps of the weights among themselves.
-__device__ __forceinline__ void weights_meet() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The eight warps of the weights among themselves.
+__device__ __forceinline__ void weights_meet() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool weights_any(bool x)
 {
     int any;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, 2, 128, p;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(any) : "r"(static_cast<int>(x)) : "memory");
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, 2, 256, p;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(any) : "r"(static_cast<int>(x)) : "memory");
     return any != 0;
 }
 
@@ -352,22 +349,25 @@ __device__ __forceinline__ E from_bits(T v)
     return e;
 }
 
-// The largest of 16 columns' numbers over a warp: lane l gets that of column l % 16 (NaN if one is).
-__device__ __forceinline__ float columns_largest(float *v, int lane)
+// The largest of 8 columns' numbers over a warp, or their sums: lane l gets that of column l % 8 (a NaN stays one).
+template <bool SUM>
+__device__ __forceinline__ float columns_joined(float *v, int lane)
 {
+    auto join = [](float a, float b) { return SUM ? a + b : larger(a, b); };
 #pragma unroll
-    for (int half = 8; half; half /= 2)
+    for (int half = 4; half; half /= 2)
 #pragma unroll
         for (int k = 0; k < half; ++k) {
             const bool upper = lane & half;
             const float other = __shfl_xor_sync(~0u, upper ? v[k] : v[k + half], half);
-            v[k] = larger(upper ? v[k + half] : v[k], other);
+            v[k] = join(upper ? v[k + half] : v[k], other);
         }
-    return larger(v[0], __shfl_xor_sync(~0u, v[0], 16));
+    v[0] = join(v[0], __shfl_xor_sync(~0u, v[0], 8));
+    return join(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
-// Registers of a warp's roles: 216 + 72 + 2 x 112 of four warps each make the 4 x 128 of the launch. (The checked build
-// spills instead: its calls in these loops need more than there are.)
+// Registers of a warp's roles: 2 x 112 + 56 + 2 x 96 of four warps each are within the 5 x 96 of the launch. (The checked
+// build spills instead: its calls in these loops need more than there are.)
 #ifdef SV_DEBUG_BOUNDS
 #define SV_CACHE_REGISTERS(way, count)
 #else
@@ -375,7 +375,7 @@ __device__ __forceinline__ float columns_largest(float *v, int lane)
 #endif
 
 template <int KIND, int D, int N>
-__global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
+__global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
 {
     using S = Tile<KIND, D, N>;
     constexpr bool kBf16 = S::bf16, kWide = KIND == SV_E4M3;  // 8 bits are widened to binary16
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
     const bool loads = kWide || P.cut.box == 0;  // keys by loads, not by tensor map
 
     // -- barriers and memory, while the work before this call ends
-    if (warp == 4) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&sh.tensor_at)), "n"(S::columns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -405,11 +405,11 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
         for (int k = 0; k < S::heads; ++k) barrier_init(sh.told + k, 1), barrier_init(sh.used + k, 2);  // (used: by the second product, and by the warp of the queries)
 #pragma unroll 1
         for (int k = 0; k < 2; ++k)
-            barrier_init(sh.scores + k, 1), barrier_init(sh.weighed + k, 128), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, kWide ? 2 : 1);
+            barrier_init(sh.scores + k, 1), barrier_init(sh.weighed + k, 256), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, kWide ? 2 : 1);
         sh.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid == 32 && !loads) {
+    if (tid == 12 * 32 && !loads) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
         if (!kWide) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q) : "memory");
@@ -473,11 +473,13 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
     __syncthreads();
     int *const lost = &sh.lost;
 
-    if (warp < 4) {
-        SV_CACHE_REGISTERS("inc", 216);
-        // -- weights: this thread has the key `tid` of every tile, and the elements tid and tid + 128 of the outputs
-        const uint32_t lanes = tensor + (static_cast<uint32_t>(warp) << 21);  // (lane 32 * warp of the tensor memory, in bits 16 and up)
-        float sum[N];
+    if (warp < 8) {
+        SV_CACHE_REGISTERS("inc", 112);
+        // -- weights: this thread has key `key0` of every tile, the elements key0 and key0 + 128 of the outputs, and rows r0 to r0 + M - 1
+        constexpr int M = S::mine;
+        const int key0 = tid & 127, r0 = warp / 4 * M;
+        const uint32_t lanes = tensor + (static_cast<uint32_t>(warp & 3) << 21);  // (lane 32 * (warp % 4) of the tensor memory, in bits 16 and up)
+        float sum[M];
         float scale = 0;
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
@@ -487,12 +489,12 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
             barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
             const int flags = h.flags;
             if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, lost);  // (the weights' room is free, and the values before the last have come)
-            int r_lo = 0, r_hi = N;  // the rows that see this thread's key
+            int r_lo = 0, r_hi = M;  // the rows, from r0 on, that see this thread's key
             if (flags & kFirst) {
                 const int head = h.head;
                 scale = P.scale * (P.k_scale ? ld(P.k_scale + head) : 1.0f);
 #pragma unroll
-                for (int r = 0; r < N; ++r) sum[r] = 0;
+                for (int r = 0; r < M; ++r) sum[r] = 0;
                 if constexpr (kWide) {
                     const int segment = h.segment;
                     barrier_wait(sh.q_full + segment % S::q_buffers, segment / S::q_buffers & 1, lost);
@@ -502,11 +504,11 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 }
             }
             if (flags & kEdge) {
-                const i64 d = static_cast<i64>(h.p0) + tid - h.length;  // it is the d-th new token's place
-                const i64 lo = d <= 0 ? 0 : d * P.group - h.from, hi = P.window > 0 ? (d + P.window) * P.group - h.from : N;
-                r_lo = static_cast<int>(min(max(lo, 0ll), static_cast<i64>(N)));
-                r_hi = static_cast<int>(min(max(hi, 0ll), static_cast<i64>(N)));
-                if (!(h.seen[tid / 32] >> (tid & 31) & 1)) r_hi = 0;
+                const i64 d = static_cast<i64>(h.p0) + key0 - h.length;  // it is the d-th new token's place
+                const i64 lo = d <= 0 ? 0 : d * P.group - h.from - r0, hi = P.window > 0 ? (d + P.window) * P.group - h.from - r0 : M;
+                r_lo = static_cast<int>(min(max(lo, 0ll), static_cast<i64>(M)));
+                r_hi = static_cast<int>(min(max(hi, 0ll), static_cast<i64>(M)));
+                if (!(h.seen[key0 / 32] >> (key0 & 31) & 1)) r_hi = 0;
                 // A weight of 0 times a value that is not finite would be NaN. Such elements, if any, are set to 0 in shared
                 // memory, and what they make of the rows that see them is added by hand.
                 const int vslot = it % S::v_slots;
@@ -516,8 +518,8 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 constexpr uint32_t mask = kBf16 ? 0x7f80u : 0x7c00u;
                 bool odd = false;
 #pragma unroll 2
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = *chunk(tid, c);
+                for (int c = warp / 4; c < D / 8; c += 2) {
+                    const uint4 x = *chunk(key0, c);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t w = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
@@ -531,13 +533,13 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
 #pragma unroll 1
                     for (int e = 0; e < S::blocks; ++e)
 #pragma unroll 1
-                        for (int r = 0; r < N; ++r) {
+                        for (int r = r0; r < r0 + M; ++r) {
                             const uint32_t at = lanes + (2 + e) * N + r;
                             uint32_t w;
                             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(at) : "memory");
                             tensor_loaded();
                             float x = flags & kFirst ? 0.0f : __uint_as_float(w);
-                            const int element = e * 128 + tid;
+                            const int element = e * 128 + key0;
 #pragma unroll 1
                             for (int key = 0; key < kTile && element < D; ++key) {
                                 const i64 dk = static_cast<i64>(h.p0) + key - h.length;
@@ -552,8 +554,8 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                     tensor_before();
                     weights_meet();
 #pragma unroll 1
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint32_t *x = reinterpret_cast<uint32_t *>(chunk(tid, c));
+                    for (int c = warp / 4; c < D / 8; c += 2) {
+                        uint32_t *x = reinterpret_cast<uint32_t *>(chunk(key0, c));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if ((x[k] & mask) == mask) x[k] &= 0xffff0000u;
@@ -568,22 +570,22 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
             // -- the scores relative to the reference; a new one where some score is too far above it
             barrier_wait(sh.scores + b, turn, lost);
             tensor_after();
-            const uint32_t scores_at = lanes + b * N;
-            float s[N];
+            const uint32_t scores_at = lanes + b * N + r0;
+            float s[M];
             auto relative = [&] {
 #pragma unroll
-                for (int c = 0; c < N; c += 16) tensor_load16(s + c, scores_at + c);
+                for (int c = 0; c < M; c += 8) tensor_load8(s + c, scores_at + c);
                 tensor_loaded();
 #pragma unroll
-                for (int r = 0; r < N; r += 4) {
-                    const float4 less = *reinterpret_cast<const float4 *>(sh.less + r);
-                    const float4 by = kWide ? *reinterpret_cast<const float4 *>(sh.scale + r) : make_float4(scale, scale, scale, scale);
+                for (int r = 0; r < M; r += 4) {
+                    const float4 less = *reinterpret_cast<const float4 *>(sh.less + r0 + r);
+                    const float4 by = kWide ? *reinterpret_cast<const float4 *>(sh.scale + r0 + r) : make_float4(scale, scale, scale, scale);
                     s[r] = fmaf(s[r], by.x, less.x), s[r + 1] = fmaf(s[r + 1], by.y, less.y);
                     s[r + 2] = fmaf(s[r + 2], by.z, less.z), s[r + 3] = fmaf(s[r + 3], by.w, less.w);
                 }
                 if (flags & kEdge) {
 #pragma unroll
-                    for (int r = 0; r < N; ++r)
+                    for (int r = 0; r < M; ++r)
                         if (r < r_lo || r >= r_hi) s[r] = -kInf;
                 }
             };
@@ -592,19 +594,19 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 relative();
                 float far[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
-                for (int r = 0; r < N; ++r) far[r & 3] = fmaxf(far[r & 3], s[r]);
+                for (int r = 0; r < M; ++r) far[r & 3] = fmaxf(far[r & 3], s[r]);
                 renew = weights_any(fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) > W::offset + W::slack);
             }
             if (renew) {
 #pragma unroll 1
-                for (int c = 0; c < N; c += 16) {
-                    float v[16];
-                    tensor_load16(v, scores_at + c);
+                for (int c = 0; c < M; c += 8) {
+                    float v[8];
+                    tensor_load8(v, scores_at + c);
                     tensor_loaded();
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) v[r] = c + r < r_lo || c + r >= r_hi ? -kInf : v[r] * (kWide ? sh.scale[c + r] : scale);
-                    const float most = columns_largest(v, lane);
-                    if (lane < 16) sh.most[warp][c + lane] = most;
+                    for (int r = 0; r < 8; ++r) v[r] = c + r < r_lo || c + r >= r_hi ? -kInf : v[r] * (kWide ? sh.scale[r0 + c + r] : scale);
+                    const float most = columns_joined<false>(v, lane);
+                    if (lane < 8) sh.most[warp & 3][r0 + c + lane] = most;
                 }
                 weights_meet();
                 if (tid < N) {
@@ -619,28 +621,30 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                     barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
                     tensor_after();
 #pragma unroll 1
-                    for (int c = 0; c < S::blocks * N; c += 16) {
-                        float o[16];
-                        tensor_load16(o, lanes + 2 * N + c);
-                        tensor_loaded();
+                    for (int e = 0; e < S::blocks; ++e)
+#pragma unroll 1
+                        for (int c = 0; c < M; c += 8) {
+                            float o[8];
+                            tensor_load8(o, lanes + (2 + e) * N + r0 + c);
+                            tensor_loaded();
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) o[r] *= sh.factor[(c % N) + r];
-                        tensor_store16(lanes + 2 * N + c, o);
-                    }
+                            for (int r = 0; r < 8; ++r) o[r] *= sh.factor[r0 + c + r];
+                            tensor_store8(lanes + (2 + e) * N + r0 + c, o);
+                        }
                     tensor_stored();
                     tensor_before();
 #pragma unroll
-                    for (int r = 0; r < N; r += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sh.factor + r);
+                    for (int r = 0; r < M; r += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sh.factor + r0 + r);
                         sum[r] *= f.x, sum[r + 1] *= f.y, sum[r + 2] *= f.z, sum[r + 3] *= f.w;
                     }
                 }
                 relative();
             }
             // -- weights, to shared memory as the product wants them: eight rows of a key side by side
-            unsigned char *const to = w_room + b * S::weights + tid * 16;
+            unsigned char *const to = w_room + b * S::weights + r0 / 8 * (kTile * 16) + key0 * 16;
 #pragma unroll
-            for (int r = 0; r < N; r += 8) {
+            for (int r = 0; r < M; r += 8) {
                 float e[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -657,69 +661,60 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
             if (!(flags & kLast)) continue;
 
             // -- a segment's end: the sums over the keys, and the result or the part written
-            barrier_wait(sh.done + b, turn, lost);
-            if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
-            tensor_after();
-            float *const all = reinterpret_cast<float *>(w_room);  // (both rooms for weights are free)
 #pragma unroll
-            for (int r = 0; r < N; ++r) all[r * kTile + tid] = sum[r];
-            weights_meet();
-            const float vs = P.v_scale ? ld(P.v_scale + head) : 1.0f;
-            const float sound = *reinterpret_cast<volatile int *>(lost) ? __int_as_float(0x7fffffff) : 1.0f;
-#pragma unroll 1
-            for (int r = warp; r < N; r += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(all + r * kTile + lane * 4);
-                float z = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-                for (int d = 16; d; d /= 2) z += __shfl_xor_sync(~0u, z, d);
-                if (lane == 0) {
-                    const bool none = sh.top[r] == -kInf;
-                    sh.sum[r] = none ? 0.0f : z * sound;
-                    sh.factor[r] = none ? 0.0f : sound * (flags & kPartial ? 1.0f : vs / z);
-                }
+            for (int c = 0; c < M; c += 8) {
+                const float z = columns_joined<true>(sum + c, lane);
+                if (lane < 8) sh.most[warp & 3][r0 + c + lane] = z;
             }
             weights_meet();
-            const i64 part = (static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0)) * N;
-#pragma unroll 1
-            for (int c = 0; c < S::blocks * N; c += 16) {
-                float o[16];
-                tensor_load16(o, lanes + 2 * N + c);
-                tensor_loaded();
-                const int e = (c < N ? 0 : 128) + tid, r0 = c % N;
-                int j = (from + r0) / P.group, g = from + r0 - j * P.group;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int r = r0 + k;
-                    if (r < count && (D >= 128 || e < D)) {
-                        const float f = sh.factor[r], y = f == 0 ? 0.0f : o[k] * f;
-                        if (flags & kPartial)
-                            st(P.sums + (part + r) * D + e, y);
-                        else
-                            st(reinterpret_cast<E *>(P.out + static_cast<i64>(first_row + j) * P.out_row + static_cast<i64>(head * P.group + g) * P.out_head) + e,
-                               kWide && P.bf16 ? from_bits<E>(__float2bfloat16_rn(y)) : from_bits<E>(static_cast<E>(y)));
-                    }
-                    if (++g == P.group) g = 0, ++j;
+            const bool partial = flags & kPartial;
+            if (tid < N) {
+                const float top = sh.top[tid], sound = *reinterpret_cast<volatile int *>(lost) ? __int_as_float(0x7fffffff) : 1.0f;
+                const float z = top == -kInf ? 0.0f : ((sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid])) * sound;
+                const int at_row = from + tid, j = at_row / P.group, qh = head * P.group + at_row - j * P.group;
+                const i64 part = (static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0)) * N + tid;
+                sh.factor[tid] = z == 0 ? 0.0f : partial ? sound : (P.v_scale ? ld(P.v_scale + head) : 1.0f) / z;
+                sh.row_at[tid] = tid >= count ? -1 : partial ? part * (D * 4) : static_cast<i64>(first_row + j) * P.out_row + static_cast<i64>(qh) * P.out_head;
+                if (tid < count) {
+                    if (partial)
+                        st(P.stats + part, make_float2(top, z));
+                    else if (P.lse)
+                        st(P.lse + static_cast<i64>(first_row + j) * P.hq + qh, z == 0 ? -kInf : (top - W::offset + log2f(z)) * kLn2);
                 }
             }
-            if (tid < count) {
-                const float top = sh.top[tid], z = sh.sum[tid];
-                const int at_row = from + tid, j = at_row / P.group;
-                if (flags & kPartial)
-                    st(P.stats + part + tid, make_float2(top, z));
-                else if (P.lse)
-                    st(P.lse + static_cast<i64>(first_row + j) * P.hq + head * P.group + at_row - j * P.group, z == 0 ? -kInf : (top - W::offset + log2f(z)) * kLn2);
-            }
-            if (tid == 0 && P.parts && it == n - 1) {
-                const bool open = flags & kOpen;
-                st(reinterpret_cast<int4 *>(P.parts + cta), make_int4(open ? part_first : -1, part_last, part_slot, first_row));
+            if (tid == 128 && P.parts && it == n - 1) {
+                st(reinterpret_cast<int4 *>(P.parts + cta), make_int4(flags & kOpen ? part_first : -1, part_last, part_slot, first_row));
                 st(reinterpret_cast<int4 *>(P.parts + cta) + 1, make_int4(from, count, head, 0));
             }
+            weights_meet();
+            barrier_wait(sh.done + b, turn, lost);
+            tensor_after();
+            if (D >= 128 || key0 < D) {
+                unsigned char *const array = partial ? reinterpret_cast<unsigned char *>(P.sums) : P.out;
+#pragma unroll 1
+                for (int e = 0; e < S::blocks; ++e)
+#pragma unroll 1
+                    for (int c = 0; c < M; c += 8) {
+                        float o[8];
+                        tensor_load8(o, lanes + (2 + e) * N + r0 + c);
+                        tensor_loaded();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const i64 at = sh.row_at[r0 + c + k];
+                            const float f = sh.factor[r0 + c + k], y = f == 0 ? 0.0f : o[k] * f;
+                            if (at < 0) continue;
+                            if (partial)
+                                st(reinterpret_cast<float *>(array + at) + e * 128 + key0, y);
+                            else
+                                st(reinterpret_cast<E *>(array + at) + e * 128 + key0, kWide && P.bf16 ? from_bits<E>(__float2bfloat16_rn(y)) : from_bits<E>(static_cast<E>(y)));
+                        }
+                    }
+            }
             tensor_before();
-            weights_meet();  // (the sums' room takes weights again)
         }
-    } else if (warp < 8) {
-        SV_CACHE_REGISTERS("dec", 72);
-        if (warp == 4) {
+    } else if (warp < 12) {
+        SV_CACHE_REGISTERS("dec", 56);
+        if (warp == 8) {
             // -- scores^T = K Q^T
             const uint32_t leader = elected();
             constexpr uint32_t kShape = product_of(kBf16, N, false);
@@ -742,7 +737,7 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 products_close(sh.k_empty + s, leader);
                 if (flags & kLast) products_close(sh.q_empty + qb, leader);
             }
-        } else if (warp == 5) {
+        } else if (warp == 9) {
             // -- out^T += V^T weights^T
             const uint32_t leader = elected();
             constexpr uint32_t kShape = product_of(kBf16, N, true);
@@ -767,7 +762,7 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 products_close(sh.v_empty + s, leader);
                 products_close(sh.used + it % S::heads, leader);
             }
-        } else if (warp == 6 && n > 0) {
+        } else if (warp == 10 && n > 0) {
             // -- plan: this lane has places lane, 32 + lane, ... of each tile
             walk.seek(static_cast<int>(sh.start[0]), sh.start[1], u0);
             int segment = -1;
@@ -838,7 +833,7 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                 if (lane == 0) barrier_arrive(sh.told + k);
                 walk.next();
             }
-        } else if (warp == 7) {
+        } else if (warp == 11) {
             // -- keys by boxes, and queries
             int s = 0;
             uint32_t turn = 0;  // times the ring has been gone round, as the parity waited for
@@ -921,9 +916,8 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
             }
         }
     } else {
-        SV_CACHE_REGISTERS("dec", 112);
         if (!loads) {
-            if (warp == 8) {
+            if (warp == 12) {
                 // -- values by boxes
                 int s = 0;
                 uint32_t turn = 0;
@@ -939,8 +933,8 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
             // -- keys and values by loads: pieces (a tile's keys, its values, the next tile's keys, ...) of which `kAhead` are on
             // the way to registers
             constexpr int kRow = D * S::bytes_of / 16, kEvery = 256 / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's
-            constexpr int kAhead = 16 / kEach < 1 ? 1 : 16 / kEach > 4 ? 4 : 16 / kEach;
-            const int x = tid - 256, c = x % kRow, key0 = x / kRow;
+            constexpr int kAhead = 12 / kEach < 1 ? 1 : 12 / kEach > 4 ? 4 : 12 / kEach;
+            const int x = tid - 384, c = x % kRow, key0 = x / kRow;
             uint4 data[kAhead][kEach];
             auto load = [&](int u, uint4 *to) {
                 const int it = u >> 1;
@@ -952,8 +946,7 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
                     const int key = key0 + k * kEvery, page = h.page[key], p = p0 + key, slot = p - page_of(P.s, p) * P.s.page;
-                    to[k] = make_uint4(0, 0, 0, 0);
-                    if (page >= 0) to[k] = ld_stream(reinterpret_cast<const uint4 *>(at + page * from.page + slot * from.slot));
+                    ld_stream(to[k], reinterpret_cast<const uint4 *>(at + page * from.page + slot * from.slot), page >= 0);
                 }
             };
             auto store = [&](int u, const uint4 *from) {
@@ -989,15 +982,15 @@ __global__ void __launch_bounds__(512, 1) sv_cache_attention_kernel(const Attent
                     }
         }
     }
-    if (*reinterpret_cast<volatile int *>(lost) && !loads && (warp == 7 || warp == 8)) {  // copies in flight end before the block does
-        const int slots = warp == 8 ? S::v_slots : S::k_slots;
+    if (*reinterpret_cast<volatile int *>(lost) && !loads && (warp == 11 || warp == 12)) {  // copies in flight end before the block does
+        const int slots = warp == 12 ? S::v_slots : S::k_slots;
         for (int it = max(0, n - slots); it < n; ++it)
-            for (int k = 0; k < kPatience && !barrier_try((warp == 8 ? sh.v_full : sh.k_full) + it % slots, it / slots & 1); ++k) {
+            for (int k = 0; k < kPatience && !barrier_try((warp == 12 ? sh.v_full : sh.k_full) + it % slots, it / slots & 1); ++k) {
             }
     }
     tensor_before();
     __syncthreads();
-    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(S::columns) : "memory");
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(S::columns) : "memory");
 }
 
 // Joins the parts of the groups that more than one CTA has. A group over k + 1 CTAs has k CTAs here, which share its
