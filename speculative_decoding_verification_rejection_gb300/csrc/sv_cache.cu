@@ -411,11 +411,11 @@ int map_of(CUtensorMap &map, bool bf16, const View &v, int box)
                : SV_ECUDA;
 }
 
-// Whether copies by tensor map can walk it: every stride in use above 0 and below 2^40 bytes.
+// Whether copies by tensor map can walk it: every stride in use above 0 (and below 2^36 bytes, which 32 bits hold in vectors).
 bool walkable(const View &v)
 {
     for (int d = 0; d < 3; ++d)
-        if (v.size[d] > 1 && (v.stride[d] < 1 || v.stride[d] * v.elem >= (1ll << 40))) return false;
+        if (v.size[d] > 1 && (v.stride[d] < 1 || v.stride[d] * v.elem >= (1ll << 36))) return false;
     return true;
 }
 
@@ -462,9 +462,14 @@ i64 most_tiles(const spec_verify_cache_attention_args &a, const Kernel &k)
     return std::max<i64>(1, cut.parts > 1 ? static_cast<i64>(a.pages_per_req) * cut.parts : (static_cast<i64>(a.pages_per_req) * a.page_size + cut.span - 1) / cut.span);
 }
 
+i64 most_groups(const spec_verify_cache_attention_args &a, const Kernel &k)
+{
+    return (a.num_reqs + static_cast<i64>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) / k.rows) * a.num_kv_heads;
+}
+
 i64 ctas_for(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
-    const i64 groups = (a.num_reqs + static_cast<i64>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) / k.rows) * a.num_kv_heads, tiles = most_tiles(a, k);
+    const i64 groups = most_groups(a, k), tiles = most_tiles(a, k);
     return groups >= 152 || tiles >= 152 ? 152 : std::min<i64>(152, groups * tiles);
 }
 
@@ -624,6 +629,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     if (a->num_rows == 0 || a->num_reqs == 0) return SV_OK;
     if (!a->q || !a->out || a->q == a->out || misaligned(a->q, 16) || misaligned(a->out, 16) || misaligned(a->lse, 4)) return SV_EINVAL;
     const Kernel kernel = kernel_for(*a);
+    if (static_cast<wide>(most_groups(*a, kernel)) * most_tiles(*a, kernel) >= (1ll << 31)) return SV_ECAPACITY;
     const int64_t workspace = workspace_of(*a, kernel);
     if (a->workspace_bytes < workspace || (workspace > 0 && !a->workspace) || misaligned(a->workspace, 16)) return SV_EINVAL;
     const int rd = cache_device(a->device);

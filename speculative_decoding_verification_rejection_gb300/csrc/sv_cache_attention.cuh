@@ -68,12 +68,13 @@ struct Tile {
     static constexpr int weights = kTile * N * 2;
     static constexpr int q_buffers = (D == 256 && N > 16) || N == 64 ? 1 : 2;
     static constexpr int heads = D == 256 && N > 16 ? 2 : 8;  // descriptions of tiles that are kept
-    static constexpr int fit = ((heads == 8 ? 224800 : 229376) - q_buffers * q_bytes - 2 * weights) / slot;
+    static constexpr int fit = ((heads == 8 ? 223400 : 229376) - q_buffers * q_bytes - 2 * weights) / slot;
     static constexpr int slots = fit > 12 ? 12 : fit;
     static constexpr int k_slots = slots / 2, v_slots = slots - slots / 2;  // rings of their own: each is filled in turn
     static constexpr int blocks = D == 256 ? 2 : 1;  // of 128 elements
     static constexpr int columns_used = (2 + blocks) * N;
     static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
+    static constexpr bool slots_told = D < 256;
     static constexpr int threads = 640;
     static constexpr int mine = N / 2;                // rows of a weights warp
     static_assert(slots >= 2 && columns_used <= 256, "room");
@@ -81,7 +82,8 @@ struct Tile {
         int p0, first, count, from, head, length, flags, segment;
         int part_first, part_last, part_slot, slot, started;
         uint32_t seen[4];
-        int page[kTile];  // of each box, or of each key
+        int page[kTile];                            // of each box, or of each key
+        uint16_t key_slot[slots_told ? kTile : 2];  // of each key
     };
     struct Shared {
         u64 k_full[k_slots], k_empty[k_slots], v_full[v_slots], v_empty[v_slots], scores[2], weighed[2], done[2], q_full[2], q_empty[2], told[heads],
@@ -94,8 +96,7 @@ struct Tile {
         float top[N];                 // the reference, times log2 e
         i64 row_at[N];                // where a row's result goes, in bytes from its array's start; -1: nowhere
         float q_scale[2][N];          // of queries held in binary16
-        u64 scan[threads / 32];
-        u64 start[2];
+        uint32_t scan[32], start[2];
         uint32_t tensor_at;
         int lost;
     };
@@ -139,13 +140,10 @@ __device__ __forceinline__ int tile_of(const AttentionParams &P, int p)
     const int c = page_of(P.s, p);
     return c * P.cut.parts + (p - c * P.s.page) / P.cut.box;
 }
-// total k / of, rounded down (k <= of < 2^10)
-__device__ __forceinline__ u64 share_of(u64 total, int k, int of)
-{
-    return total < (1u << 22) ? static_cast<uint32_t>(total) * static_cast<uint32_t>(k) / static_cast<uint32_t>(of) : total * static_cast<u64>(k) / static_cast<u64>(of);
-}
-// the last k with share_of(total, k, of) <= number
-__device__ __forceinline__ int sharer_of(u64 total, u64 number, int of) { return static_cast<int>(((number + 1) * static_cast<u64>(of) - 1) / total); }
+// CTA k's first tile of `total` (below 2^31): total k / ctas, rounded down.
+__device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t k, uint32_t ctas) { return total / ctas * k + total % ctas * k / ctas; }
+// The last CTA whose first tile is not behind this one.
+__device__ __forceinline__ int sharer_of(uint32_t total, uint32_t number, uint32_t ctas) { return static_cast<int>((static_cast<u64>(number) * ctas + ctas - 1) / total); }
 
 // All tiles of the step in order: request, rows of a tile, key head, tokens. CTA c takes those from c W / ctas
 // to (c + 1) W / ctas, so every CTA gets as many whatever the lengths are. A group is the tiles of a request's N query
@@ -156,7 +154,7 @@ struct Walk {
     int i, first, rows, length;  // the request: its first row, its rows times the group, its length
     int from, count, head, t;    // the group: its first row within the request, its rows; the tile
     int t0, t1, start, end;
-    u64 base;                    // number of the group's first tile
+    uint32_t base;               // number of the group's first tile
 
     __device__ __forceinline__ Walk(const AttentionParams &P) : P(P) {}
     __device__ __forceinline__ void request(int k)
@@ -180,33 +178,33 @@ struct Walk {
         t = t0;
     }
     __device__ __forceinline__ int tiles() const { return t1 - t0; }
-    __device__ u64 request_tiles(int k)
+    __device__ __forceinline__ uint32_t request_tiles(int k)
     {
         request(k);
-        u64 sum = 0;
+        uint32_t sum = 0;
 #pragma unroll 1
         for (int at = 0; at < rows; at += N) {
             group(at);
-            sum += static_cast<u64>(tiles()) * static_cast<u64>(P.hk);
+            sum += tiles() * P.hk;
         }
         return sum;
     }
     // To tile `skip` of request k, the step's tile `number`.
-    __device__ void seek(int k, u64 skip, u64 number)
+    __device__ __forceinline__ void seek(int k, uint32_t skip, uint32_t number)
     {
         request(k);
         base = number - skip;
 #pragma unroll 1
         for (int at = 0; at < rows; at += N) {
             group(at);
-            const u64 here = static_cast<u64>(tiles()) * static_cast<u64>(P.hk);
+            const uint32_t here = tiles() * P.hk;
             if (skip < here) break;
             skip -= here;
             base += here;
         }
-        head = static_cast<int>(skip < (1u << 31) ? static_cast<uint32_t>(skip) / static_cast<uint32_t>(tiles()) : skip / static_cast<u64>(tiles()));
-        t += static_cast<int>(skip - static_cast<u64>(head) * static_cast<u64>(tiles()));
-        base += static_cast<u64>(head) * static_cast<u64>(tiles());
+        head = static_cast<int>(skip / static_cast<uint32_t>(tiles()));
+        t += static_cast<int>(skip) - head * tiles();
+        base += head * tiles();
     }
     __device__ __forceinline__ void next()
     {
@@ -427,44 +425,42 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
     // -- this CTA's tiles
     Walk<N> walk(P);
     const int per = (P.s.n + S::threads - 1) / S::threads;
-    u64 mine = 0;
+    uint32_t mine = 0;
 #pragma unroll 1
     for (int k = tid * per; k < min(P.s.n, (tid + 1) * per); ++k) mine += walk.request_tiles(k);
-    u64 before = mine;
-#pragma unroll 1
-    for (int d = 1; d < 32; d *= 2) {
-        const u64 up = __shfl_up_sync(~0u, before, d);
-        if (lane >= d) before += up;
-    }
+    auto running = [lane](uint32_t x) {
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t up = __shfl_up_sync(~0u, x, d);
+            if (lane >= d) x += up;
+        }
+        return x;
+    };
+    uint32_t before = running(mine);
     if (lane == 31) sh.scan[warp] = before;
     tensor_before();
     __syncthreads();
     tensor_after();
-    u64 total = 0, ahead = 0;
-#pragma unroll 1
-    for (int w = 0; w < S::threads / 32; ++w) {
-        if (w == warp) ahead = total;
-        total += sh.scan[w];
-    }
-    before += ahead - mine;
+    const uint32_t warps = running(lane < S::threads / 32 ? sh.scan[lane] : 0u), total = __shfl_sync(~0u, warps, 31);
+    before += (warp ? __shfl_sync(~0u, warps, (warp - 1) & 31) : 0u) - mine;
     const uint32_t tensor = __shfl_sync(~0u, sh.tensor_at, 0);
-    const int ctas = static_cast<int>(min(total, static_cast<u64>(gridDim.x)));  // (each with a tile at least)
+    const uint32_t ctas = min(total, gridDim.x);  // (each with a tile at least)
     int n = 0;
-    u64 u0 = 0, u1 = 0;
-    if (cta < ctas) {
+    uint32_t u0 = 0, u1 = 0;
+    if (cta < static_cast<int>(ctas)) {
         u0 = share_of(total, cta, ctas), u1 = share_of(total, cta + 1, ctas);
         n = __shfl_sync(~0u, static_cast<int>(u1 - u0), 0);
         if (u0 >= before && u0 < before + mine) {
-            u64 at = before;
+            uint32_t at = before;
             int k = tid * per;
             if (per > 1)
 #pragma unroll 1
                 for (; k < min(P.s.n, (tid + 1) * per) - 1; ++k) {
-                    const u64 here = walk.request_tiles(k);
+                    const uint32_t here = walk.request_tiles(k);
                     if (u0 < at + here) break;
                     at += here;
                 }
-            sh.start[0] = static_cast<u64>(k);
+            sh.start[0] = static_cast<uint32_t>(k);
             sh.start[1] = u0 - at;
         }
     } else if (P.parts && tid == 0) {
@@ -776,12 +772,13 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     p0 = c0 * P.s.page + slot0;
                     places = min(P.cut.box, P.s.page - slot0);
                 }
-                int page[4], in[4];
+                int page[4], in[4], at[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int k = w * 32 + lane, p = p0 + k, c = page_of(P.s, p);
                     page[w] = -1;
                     in[w] = loads ? k : P.cut.parts > 1 ? 0 : c - c0;  // its box, and the box's places
+                    at[w] = p - c * P.s.page;
                     const int lo = loads ? p : P.cut.parts > 1 ? p0 : c * P.s.page, hi = loads ? p + 1 : P.cut.parts > 1 ? p0 + places : lo + P.s.page;
                     if (walk.rows && k < places && lo < walk.end && hi > walk.start) page[w] = ld(P.s.table + walk.i * P.s.table_stride + c);
                     if (!loads && p != lo) in[w] = -1;  // (the box's first place speaks for it)
@@ -805,12 +802,16 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     if (lane == 0) h.seen[w] = seen;
                     if (in[w] >= 0 && w * 32 + lane < places) h.page[in[w]] = there ? page[w] : loads ? -1 : P.s.pages;  // (a page behind the last: zeros)
                 }
+                if constexpr (S::slots_told) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) h.key_slot[w * 32 + lane] = static_cast<uint16_t>(at[w]);
+                }
                 const bool opens = walk.t == walk.t0, ends = walk.t + 1 == walk.t1;
                 const bool first = it == 0 || opens, last = it == n - 1 || ends;
                 if (first) ++segment;
                 if (lane == 0) {
                     const int j0 = walk.from / P.group, j1 = (walk.from + walk.count - 1) / P.group;
-                    const bool part = walk.base < u0 || walk.base + static_cast<u64>(walk.tiles()) > u1;
+                    const bool part = walk.base < u0 || walk.base + walk.tiles() > u1;
                     all = all && static_cast<i64>(p0) + kTile - 1 <= static_cast<i64>(walk.length) + j0 &&
                           (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
                     h.p0 = p0;
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     h.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (part ? kPartial : 0) | (walk.base > u0 ? kSlot : 0) | (last && !ends ? kOpen : 0) | (all ? 0 : kEdge);
                     if (last && !ends) {  // the CTAs that have tiles of the group
                         h.part_first = sharer_of(total, walk.base, ctas);
-                        h.part_last = sharer_of(total, walk.base + static_cast<u64>(walk.tiles()) - 1, ctas);
+                        h.part_last = sharer_of(total, walk.base + walk.tiles() - 1, ctas);
                         h.part_slot = share_of(total, h.part_first, ctas) < walk.base;
                     }
                 }
@@ -941,12 +942,14 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
                 const auto &h = sh.head[it % S::heads];
                 const Cache &from = u & 1 ? P.vc : P.kc;
-                const unsigned char *const at = from.at + static_cast<i64>(h.head) * from.head + c * 16;
-                const int p0 = h.p0;
+                // (strides in vectors of 16 bytes, below 2^32)
+                const uint32_t by_page = static_cast<uint32_t>(from.page >> 4), by_slot = static_cast<uint32_t>(from.slot >> 4);
+                const uint4 *const at = reinterpret_cast<const uint4 *>(from.at + static_cast<i64>(h.head) * from.head) + c;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
-                    const int key = key0 + k * kEvery, page = h.page[key], p = p0 + key, slot = p - page_of(P.s, p) * P.s.page;
-                    ld_stream(to[k], reinterpret_cast<const uint4 *>(at + page * from.page + slot * from.slot), page >= 0);
+                    const int key = key0 + k * kEvery, page = h.page[key], p = h.p0 + key;
+                    const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
+                    ld_stream(to[k], at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot), page >= 0);
                 }
             };
             auto store = [&](int u, const uint4 *from) {
