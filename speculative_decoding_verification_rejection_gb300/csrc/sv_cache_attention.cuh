@@ -364,7 +364,7 @@ __device__ __forceinline__ float columns_joined(float *v, int lane)
     return join(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
-// Registers of a warp's roles: 2 x 112 + 56 + 2 x 96 of four warps each are within the 5 x 96 of the launch. (The checked
+// Registers of a warp's roles: 4 x 104 + 56 of four warps each are within the 5 x 96 of the launch. (The checked
 // build spills instead: its calls in these loops need more than there are.)
 #ifdef SV_DEBUG_BOUNDS
 #define SV_CACHE_REGISTERS(way, count)
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        const int filled = loads ? 8 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
+        const int filled = loads ? 4 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
 #pragma unroll 1
         for (int k = 0; k < S::v_slots; ++k) {
             if (k < S::k_slots) barrier_init(sh.k_full + k, filled), barrier_init(sh.k_empty + k, 1);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
     int *const lost = &sh.lost;
 
     if (warp < 8) {
-        SV_CACHE_REGISTERS("inc", 112);
+        SV_CACHE_REGISTERS("inc", 104);
         // -- weights: this thread has key `key0` of every tile, the elements key0 and key0 + 128 of the outputs, and rows r0 to r0 + M - 1
         constexpr int M = S::mine;
         const int key0 = tid & 127, r0 = warp / 4 * M;
@@ -917,6 +917,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
             }
         }
     } else {
+        SV_CACHE_REGISTERS("inc", 104);
         if (!loads) {
             if (warp == 12) {
                 // -- values by boxes
@@ -931,35 +932,36 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 }
             }
         } else {
-            // -- keys and values by loads: pieces (a tile's keys, its values, the next tile's keys, ...) of which `kAhead` are on
-            // the way to registers
-            constexpr int kRow = D * S::bytes_of / 16, kEvery = 256 / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's
-            constexpr int kAhead = 12 / kEach < 1 ? 1 : 12 / kEach > 4 ? 4 : 12 / kEach;
-            const int x = tid - 384, c = x % kRow, key0 = x / kRow;
+            // -- keys (four warps) and values (four warps) by loads: steps of up to kEach vectors a thread, of which kAhead are
+            // on the way to registers; a tile is kSteps steps
+            const bool values = warp >= 16;
+            constexpr int kRow = D * S::bytes_of / 16, kEvery = 128 / kRow, kAll = kTile / kEvery;  // vectors of a key; keys at once; a thread's
+            constexpr int kEach = kAll < 8 ? kAll : 8, kSteps = kAll / kEach, kAhead = 16 / kEach;
+            const int x = tid & 127, c = x % kRow, key0 = x / kRow, slots = values ? S::v_slots : S::k_slots, steps = n * kSteps;
+            const Cache &cache = values ? P.vc : P.kc;
+            // (strides in vectors of 16 bytes, below 2^32)
+            const uint32_t by_page = static_cast<uint32_t>(cache.page >> 4), by_slot = static_cast<uint32_t>(cache.slot >> 4);
             uint4 data[kAhead][kEach];
-            auto load = [&](int u, uint4 *to) {
-                const int it = u >> 1;
-                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
-                const auto &h = sh.head[it % S::heads];
-                const Cache &from = u & 1 ? P.vc : P.kc;
-                // (strides in vectors of 16 bytes, below 2^32)
-                const uint32_t by_page = static_cast<uint32_t>(from.page >> 4), by_slot = static_cast<uint32_t>(from.slot >> 4);
-                const uint4 *const at = reinterpret_cast<const uint4 *>(from.at + static_cast<i64>(h.head) * from.head) + c;
+            int loading = 0, storing = 0, slot_at = 0;  // tiles; the slot of the one that is stored
+            uint32_t turn = 0;
+            auto load = [&](int step, uint4 *to) {
+                const auto &h = sh.head[loading % S::heads];
+                if (step == 0) barrier_wait(sh.told + loading % S::heads, loading / S::heads & 1, lost);
+                const uint4 *const at = reinterpret_cast<const uint4 *>(cache.at + static_cast<i64>(h.head) * cache.head) + c;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
-                    const int key = key0 + k * kEvery, page = h.page[key], p = h.p0 + key;
+                    const int key = key0 + (step * kEach + k) * kEvery, page = h.page[key], p = h.p0 + key;
                     const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
                     ld_stream(to[k], at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot), page >= 0);
                 }
+                if (step == kSteps - 1) ++loading;
             };
-            auto store = [&](int u, const uint4 *from) {
-                const int it = u >> 1, slots = u & 1 ? S::v_slots : S::k_slots, s = it % slots;
-                u64 *const full = (u & 1 ? sh.v_full : sh.k_full) + s, *const empty = (u & 1 ? sh.v_empty : sh.k_empty) + s;
-                if (it >= slots) barrier_wait(empty, (it / slots - 1) & 1, lost);
-                unsigned char *const to = room + ((u & 1 ? S::k_slots : 0) + s) * S::slot;
+            auto store = [&](int step, const uint4 *from) {
+                if (step == 0 && storing >= slots) barrier_wait((values ? sh.v_empty : sh.k_empty) + slot_at, turn ^ 1, lost);
+                unsigned char *const to = room + ((values ? S::k_slots : 0) + slot_at) * S::slot;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
-                    const int key = key0 + k * kEvery;
+                    const int key = key0 + (step * kEach + k) * kEvery;
                     auto put = [&](int chunk, const uint4 &w) { *reinterpret_cast<uint4 *>(to + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4)) = w; };
                     if constexpr (kWide) {
                         put(2 * c, make_uint4(half2_of_e4m3(from[k].x), half2_of_e4m3(from[k].x >> 16), half2_of_e4m3(from[k].y), half2_of_e4m3(from[k].y >> 16)));
@@ -968,20 +970,25 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                         put(c, from[k]);
                     }
                 }
+                if (step < kSteps - 1) return;
                 shared_to_async();
                 __syncwarp();
-                if (lane == 0) barrier_arrive(full);
+                if (lane == 0) barrier_arrive((values ? sh.v_full : sh.k_full) + slot_at);
+                ++storing;
+                if (++slot_at == slots) slot_at = 0, turn ^= 1;
             };
+            static_assert(kAhead % kSteps == 0 || kSteps % kAhead == 0, "steps of a tile go round with the registers");
+            constexpr int kRound = kAhead > kSteps ? kAhead : kSteps;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (k < 2 * n) load(k, data[k]);
+                if (k < steps) load(k % kSteps, data[k]);
 #pragma unroll 1
-            for (int u = 0; u < 2 * n; u += kAhead)
+            for (int u = 0; u < steps; u += kRound)
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (u + k < 2 * n) {
-                        store(u + k, data[k]);
-                        if (u + k + kAhead < 2 * n) load(u + k + kAhead, data[k]);
+                for (int k = 0; k < kRound; ++k)
+                    if (u + k < steps) {
+                        store(k % kSteps, data[k % kAhead]);
+                        if (u + k + kAhead < steps) load((k + kAhead) % kSteps, data[k % kAhead]);
                     }
         }
     }
