@@ -79,15 +79,6 @@ __device__ __forceinline__ T ld_own(const T *p)
     if (!SV_CACHE_INSIDE(p, sizeof(T), false)) return T{};
     return *p;
 }
-// A vector that is read once (not kept in L1), or zeros. (In place, so that nothing waits for it before it is used.)
-__device__ __forceinline__ void ld_stream(uint4 &v, const uint4 *p, bool there)
-{
-    there = there && SV_CACHE_INSIDE(p, 16, false);
-    v = make_uint4(0, 0, 0, 0);
-    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
-                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-                 : "l"(p), "r"(static_cast<int>(there)));
-}
 template <typename T>
 __device__ __forceinline__ void st(T *p, const T &v)
 {

@@ -55,7 +55,7 @@ enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge =
 // waste nothing, and every key is read from shared memory once for all of them. Roles, each a warp or more: weights
 // (twice four warps; a thread has one key's scores of half of the rows), the first product, the second, a plan (the tiles
 // and their pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are
-// 8 bits or the pages small, by eight warps that load, widen and store them.
+// 8 bits or the pages small, by eight warps that copy (and widen) them vector by vector.
 template <int KIND, int D, int N>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
 struct Tile {
     static constexpr bool bf16 = KIND == SV_BF16;    // type of the products
@@ -68,7 +68,9 @@ struct Tile {
     static constexpr int weights = kTile * N * 2;
     static constexpr int q_buffers = (D == 256 && N > 16) || N == 64 ? 1 : 2;
     static constexpr int heads = D == 256 && N > 16 ? 2 : 8;  // descriptions of tiles that are kept
-    static constexpr int fit = ((heads == 8 ? 223400 : 229376) - q_buffers * q_bytes - 2 * weights) / slot;
+    // 8-bit keys and values are copied to `staged` rooms of a tile before they are widened
+    static constexpr int staged = bytes_of == 2 ? 0 : D == 64 ? 4 : D == 128 ? 2 : 1, staging = staged * 2 * kTile * D;
+    static constexpr int fit = ((heads == 8 ? 223400 : 229376) - q_buffers * q_bytes - 2 * weights - staging) / slot;
     static constexpr int slots = fit > 12 ? 12 : fit;
     static constexpr int k_slots = slots / 2, v_slots = slots - slots / 2;  // rings of their own: each is filled in turn
     static constexpr int blocks = D == 256 ? 2 : 1;  // of 128 elements
@@ -100,7 +102,7 @@ struct Tile {
         uint32_t tensor_at;
         int lost;
     };
-    static constexpr int bytes = slots * slot + q_buffers * q_bytes + 2 * weights + static_cast<int>(sizeof(Shared));
+    static constexpr int bytes = slots * slot + staging + q_buffers * q_bytes + 2 * weights + static_cast<int>(sizeof(Shared));
     static_assert(bytes <= 232448, "shared memory");
 };
 
@@ -113,6 +115,18 @@ struct Weights {
 };
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(void *to, const void *from, bool there)
+{
+    there = there && SV_CACHE_INSIDE(from, 16, false);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_address(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
     using E = std::conditional_t<kBf16, __nv_bfloat16, __half>;
     using W = Weights<kBf16>;
     extern __shared__ __align__(1024) unsigned char room[];
-    unsigned char *const q_room = room + S::slots * S::slot, *const w_room = q_room + S::q_buffers * S::q_bytes;
+    unsigned char *const staging = room + S::slots * S::slot, *const q_room = staging + S::staging, *const w_room = q_room + S::q_buffers * S::q_bytes;
     auto &sh = *reinterpret_cast<typename S::Shared *>(w_room + 2 * S::weights);
     const uint32_t room_at = shared_address(room), q_at = shared_address(q_room), w_at = shared_address(w_room);
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid & 31;
@@ -508,6 +522,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 // A weight of 0 times a value that is not finite would be NaN. Such elements, if any, are set to 0 in shared
                 // memory, and what they make of the rows that see them is added by hand.
                 const int vslot = it % S::v_slots;
+                if (S::v_slots == 1 && it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
                 barrier_wait(sh.v_full + vslot, it / S::v_slots & 1, lost);
                 unsigned char *const v = room + (S::k_slots + vslot) * S::slot;
                 auto chunk = [&](int key, int c) { return reinterpret_cast<uint4 *>(v + c / 8 * S::piece + key * 128 + (((c & 7) ^ (key & 7)) << 4)); };
@@ -932,64 +947,57 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 }
             }
         } else {
-            // -- keys (four warps) and values (four warps) by loads: steps of up to kEach vectors a thread, of which kAhead are
-            // on the way to registers; a tile is kSteps steps
+            // -- keys (four warps) and values (four warps) vector by vector: copied to their slot, or to a room of the thread's
+            // own and widened from there. A tile is given on when kLag more have been asked for.
             const bool values = warp >= 16;
-            constexpr int kRow = D * S::bytes_of / 16, kEvery = 128 / kRow, kAll = kTile / kEvery;  // vectors of a key; keys at once; a thread's
-            constexpr int kEach = kAll < 8 ? kAll : 8, kSteps = kAll / kEach, kAhead = 16 / kEach;
-            const int x = tid & 127, c = x % kRow, key0 = x / kRow, slots = values ? S::v_slots : S::k_slots, steps = n * kSteps;
+            constexpr int kRow = D * S::bytes_of / 16, kEvery = 128 / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's vectors
+            constexpr int kLag = kWide ? S::staged - 1 : S::k_slots > 2 ? S::k_slots - 2 : S::k_slots - 1;
+            const int x = tid & 127, c = x % kRow, key0 = x / kRow, slots = values ? S::v_slots : S::k_slots;
             const Cache &cache = values ? P.vc : P.kc;
             // (strides in vectors of 16 bytes, below 2^32)
             const uint32_t by_page = static_cast<uint32_t>(cache.page >> 4), by_slot = static_cast<uint32_t>(cache.slot >> 4);
-            uint4 data[kAhead][kEach];
-            int loading = 0, storing = 0, slot_at = 0;  // tiles; the slot of the one that is stored
-            uint32_t turn = 0;
-            auto load = [&](int step, uint4 *to) {
-                const auto &h = sh.head[loading % S::heads];
-                if (step == 0) barrier_wait(sh.told + loading % S::heads, loading / S::heads & 1, lost);
-                const uint4 *const at = reinterpret_cast<const uint4 *>(cache.at + static_cast<i64>(h.head) * cache.head) + c;
-#pragma unroll
-                for (int k = 0; k < kEach; ++k) {
-                    const int key = key0 + (step * kEach + k) * kEvery, page = h.page[key], p = h.p0 + key;
-                    const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
-                    ld_stream(to[k], at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot), page >= 0);
+            u64 *const fulls = values ? sh.v_full : sh.k_full, *const empties = values ? sh.v_empty : sh.k_empty;
+            unsigned char *const ring = room + (values ? S::k_slots * S::slot : 0);
+            auto place_of = [&](unsigned char *slot, int chunk, int key) { return slot + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4); };
+            auto own = [&](int it, int k) { return staging + ((((it % (S::staged ? S::staged : 1)) * 2 + values) * kEach + k) * 128 + x) * 16; };
+            int asked = 0, given = 0;  // slots
+            uint32_t asked_turn = 0, given_turn = 0;
+#pragma unroll 1
+            for (int it = 0; it < n + kLag; ++it) {
+                if (it < n) {
+                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                    if (!kWide && it >= slots) barrier_wait(empties + asked, asked_turn ^ 1, lost);
+                    const auto &h = sh.head[it % S::heads];
+                    const uint4 *const at = reinterpret_cast<const uint4 *>(cache.at + static_cast<i64>(h.head) * cache.head) + c;
+#pragma unroll 8
+                    for (int k = 0; k < kEach; ++k) {
+                        const int key = key0 + k * kEvery, page = h.page[key], p = h.p0 + key;
+                        const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
+                        const uint4 *const from = page >= 0 ? at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot) : at;
+                        copy16(kWide ? own(it, k) : place_of(ring + asked * S::slot, c, key), from, page >= 0);
+                    }
+                    if (++asked == slots) asked = 0, asked_turn ^= 1;
                 }
-                if (step == kSteps - 1) ++loading;
-            };
-            auto store = [&](int step, const uint4 *from) {
-                if (step == 0 && storing >= slots) barrier_wait((values ? sh.v_empty : sh.k_empty) + slot_at, turn ^ 1, lost);
-                unsigned char *const to = room + ((values ? S::k_slots : 0) + slot_at) * S::slot;
-#pragma unroll
-                for (int k = 0; k < kEach; ++k) {
-                    const int key = key0 + (step * kEach + k) * kEvery;
-                    auto put = [&](int chunk, const uint4 &w) { *reinterpret_cast<uint4 *>(to + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4)) = w; };
-                    if constexpr (kWide) {
-                        put(2 * c, make_uint4(half2_of_e4m3(from[k].x), half2_of_e4m3(from[k].x >> 16), half2_of_e4m3(from[k].y), half2_of_e4m3(from[k].y >> 16)));
-                        put(2 * c + 1, make_uint4(half2_of_e4m3(from[k].z), half2_of_e4m3(from[k].z >> 16), half2_of_e4m3(from[k].w), half2_of_e4m3(from[k].w >> 16)));
-                    } else {
-                        put(c, from[k]);
+                copies_close();
+                if (it < kLag) continue;
+                copies_wait<kLag>();
+                if constexpr (kWide) {
+                    if (it - kLag >= slots) barrier_wait(empties + given, given_turn ^ 1, lost);
+#pragma unroll 4
+                    for (int k = 0; k < kEach; ++k) {
+                        const int key = key0 + k * kEvery;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(own(it - kLag, k));
+                        *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c, key)) =
+                            make_uint4(half2_of_e4m3(v.x), half2_of_e4m3(v.x >> 16), half2_of_e4m3(v.y), half2_of_e4m3(v.y >> 16));
+                        *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + 1, key)) =
+                            make_uint4(half2_of_e4m3(v.z), half2_of_e4m3(v.z >> 16), half2_of_e4m3(v.w), half2_of_e4m3(v.w >> 16));
                     }
                 }
-                if (step < kSteps - 1) return;
                 shared_to_async();
                 __syncwarp();
-                if (lane == 0) barrier_arrive((values ? sh.v_full : sh.k_full) + slot_at);
-                ++storing;
-                if (++slot_at == slots) slot_at = 0, turn ^= 1;
-            };
-            static_assert(kAhead % kSteps == 0 || kSteps % kAhead == 0, "steps of a tile go round with the registers");
-            constexpr int kRound = kAhead > kSteps ? kAhead : kSteps;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (k < steps) load(k % kSteps, data[k]);
-#pragma unroll 1
-            for (int u = 0; u < steps; u += kRound)
-#pragma unroll
-                for (int k = 0; k < kRound; ++k)
-                    if (u + k < steps) {
-                        store(k % kSteps, data[k % kAhead]);
-                        if (u + k + kAhead < steps) load((k + kAhead) % kSteps, data[k % kAhead]);
-                    }
+                if (lane == 0) barrier_arrive(fulls + given);
+                if (++given == slots) given = 0, given_turn ^= 1;
+            }
         }
     }
     if (*reinterpret_cast<volatile int *>(lost) && !loads && (warp == 11 || warp == 12)) {  // copies in flight end before the block does
