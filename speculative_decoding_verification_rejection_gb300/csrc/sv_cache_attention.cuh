@@ -969,12 +969,21 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     if (!kWide && it >= slots) barrier_wait(empties + asked, asked_turn ^ 1, lost);
                     const auto &h = sh.head[it % S::heads];
                     const uint4 *const at = reinterpret_cast<const uint4 *>(cache.at + static_cast<i64>(h.head) * cache.head) + c;
-#pragma unroll 8
-                    for (int k = 0; k < kEach; ++k) {
-                        const int key = key0 + k * kEvery, page = h.page[key], p = h.p0 + key;
-                        const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
-                        const uint4 *const from = page >= 0 ? at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot) : at;
-                        copy16(kWide ? own(it, k) : place_of(ring + asked * S::slot, c, key), from, page >= 0);
+                    constexpr int kPart = kEach < 8 ? kEach : 8;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kEach; k0 += kPart) {
+                        const uint4 *from[kPart];
+                        uint32_t there = 0;
+#pragma unroll
+                        for (int k = 0; k < kPart; ++k) {
+                            const int key = key0 + (k0 + k) * kEvery, page = h.page[key], p = h.p0 + key;
+                            const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
+                            from[k] = page >= 0 ? at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot) : at;
+                            there |= static_cast<uint32_t>(page >= 0) << k;
+                        }
+#pragma unroll
+                        for (int k = 0; k < kPart; ++k)
+                            copy16(kWide ? own(it, k0 + k) : place_of(ring + asked * S::slot, c, key0 + (k0 + k) * kEvery), from[k], there >> k & 1);
                     }
                     if (++asked == slots) asked = 0, asked_turn ^= 1;
                 }
@@ -983,14 +992,22 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 copies_wait<kLag>();
                 if constexpr (kWide) {
                     if (it - kLag >= slots) barrier_wait(empties + given, given_turn ^ 1, lost);
-#pragma unroll 4
-                    for (int k = 0; k < kEach; ++k) {
-                        const int key = key0 + k * kEvery;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(own(it - kLag, k));
-                        *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c, key)) =
-                            make_uint4(half2_of_e4m3(v.x), half2_of_e4m3(v.x >> 16), half2_of_e4m3(v.y), half2_of_e4m3(v.y >> 16));
-                        *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + 1, key)) =
-                            make_uint4(half2_of_e4m3(v.z), half2_of_e4m3(v.z >> 16), half2_of_e4m3(v.w), half2_of_e4m3(v.w >> 16));
+                    // (of the lanes of a key those of the upper half write their second vector first: eight lanes, eight banks)
+                    const bool second = kRow == 8 ? c >> 2 : kRow == 4 ? 0 : c >> 2 & 1;
+                    constexpr int kPart = 4;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kEach; k0 += kPart) {
+                        uint4 v[kPart];
+#pragma unroll
+                        for (int k = 0; k < kPart; ++k) v[k] = *reinterpret_cast<const uint4 *>(own(it - kLag, k0 + k));
+#pragma unroll
+                        for (int k = 0; k < kPart; ++k) {
+                            const uint4 lo = make_uint4(half2_of_e4m3(v[k].x), half2_of_e4m3(v[k].x >> 16), half2_of_e4m3(v[k].y), half2_of_e4m3(v[k].y >> 16));
+                            const uint4 hi = make_uint4(half2_of_e4m3(v[k].z), half2_of_e4m3(v[k].z >> 16), half2_of_e4m3(v[k].w), half2_of_e4m3(v[k].w >> 16));
+                            const int key = key0 + (k0 + k) * kEvery;
+                            *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + second, key)) = second ? hi : lo;
+                            *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + !second, key)) = second ? lo : hi;
+                        }
                     }
                 }
                 shared_to_async();
