@@ -384,7 +384,7 @@ template <typename Args>
 Step step_of(const Args &a)
 {
     return Step{a.page_table, a.lengths, a.cu_num_draft, a.num_reqs > 1 ? a.table_stride : 0, a.num_reqs, a.num_rows, a.num_pages, a.page_size,
-                a.pages_per_req, ((u64{1} << 42) + static_cast<u64>(a.page_size) - 1) / static_cast<u64>(a.page_size)};
+                a.pages_per_req, Divider(static_cast<uint32_t>(a.page_size))};
 }
 
 Cache cache_of(const View &v)
@@ -656,6 +656,9 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     P.group = a->num_q_heads / a->num_kv_heads;
     P.bf16 = a->dtype == SV_BF16;
     P.cut = cut_of(*a, kernel);
+    P.by_group = Divider(static_cast<uint32_t>(P.group));
+    P.by_span = Divider(static_cast<uint32_t>(P.cut.span));
+    P.by_parts = Divider(static_cast<uint32_t>(P.cut.parts));
     const i64 ctas = ctas_for(*a, kernel);
     P.sums = static_cast<float *>(workspace ? a->workspace : nullptr);
     P.stats = workspace ? reinterpret_cast<float2 *>(P.sums + ctas * 2 * kernel.rows * kernel.dim) : nullptr;

@@ -16,12 +16,27 @@ using u64 = unsigned long long;
 
 constexpr float kInf = __builtin_huge_valf();
 
+// Division of whole numbers below 2^31 by one of 1 to 2^31 - 1: with 2^l the power of two from the divisor on,
+// by = ceil(2^(31 + l) / divisor) is off by less than 1 in 2^l steps, so x by / 2^(31 + l) is off by less than x / 2^31 < 1.
+struct Divider {
+    uint32_t by;
+    int shift;
+    explicit Divider(uint32_t divisor = 1)
+    {
+        int l = 0;
+        while ((uint64_t{1} << l) < divisor) ++l;
+        shift = 31 + l;
+        by = static_cast<uint32_t>(((uint64_t{1} << shift) + divisor - 1) / divisor);
+    }
+    __device__ __forceinline__ int operator()(int x) const { return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * by) >> shift); }
+};
+
 // The requests of a step and where their keys are.
 struct Step {
     const int32_t *table, *lengths, *cu;  // cu NULL: one row a request
     i64 table_stride;
     int n, rows, pages, page, width;      // requests, rows, pages of the pool, slots of a page, pages of a request at most
-    u64 page_magic;                       // ceil(2^42 / page): x / page = (x * page_magic) >> 42 for x < 2^22 (else divided)
+    Divider by_page;
 };
 
 // One cache: address and strides in bytes.
@@ -125,7 +140,7 @@ __device__ __forceinline__ int request_of(const Step &s, int r)
 __device__ __forceinline__ bool place(const Step &s, int i, i64 x, i64 &page, int &slot)
 {
     if (x < 0 || x >= static_cast<i64>(s.width) * s.page) return false;
-    const i64 c = x < (1 << 22) ? static_cast<i64>((static_cast<u64>(x) * s.page_magic) >> 42) : x / s.page;
+    const i64 c = x < (1ll << 31) ? s.by_page(static_cast<int>(x)) : x / s.page;
     slot = static_cast<int>(x - c * s.page);
     page = ld(s.table + i * s.table_stride + c);
     return page >= 0 && page < s.pages;

@@ -39,6 +39,7 @@ struct AttentionParams {
     int window, hq, hk, group;
     bool bf16;            // type of the rows
     Cut cut;
+    Divider by_group, by_span, by_parts;
     float *sums;          // workspace: [ctas][2][rows of a tile][dim], then [ctas][2][rows of a tile][2], then Part [ctas]
     float2 *stats;
     Part *parts;
@@ -144,15 +145,11 @@ __device__ __forceinline__ float larger(float a, float b)
 // ---------------------------------------------------------------------------------------
 // which tiles there are
 // ---------------------------------------------------------------------------------------
-__device__ __forceinline__ int page_of(const Step &s, int p)
-{
-    return p < (1 << 22) ? static_cast<int>((static_cast<u64>(p) * s.page_magic) >> 42) : p / s.page;
-}
 __device__ __forceinline__ int tile_of(const AttentionParams &P, int p)
 {
-    if (P.cut.parts == 1) return static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(P.cut.span));
-    const int c = page_of(P.s, p);
-    return c * P.cut.parts + (p - c * P.s.page) / P.cut.box;
+    if (P.cut.parts == 1) return P.by_span(p);
+    const int c = P.s.by_page(p);
+    return c * P.cut.parts + P.by_span(p - c * P.s.page);  // (a tile's span is its box)
 }
 // CTA k's first tile of `total` (below 2^31): total k / ctas, rounded down.
 __device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t k, uint32_t ctas) { return total / ctas * k + total % ctas * k / ctas; }
@@ -183,9 +180,9 @@ struct Walk {
         count = min(N, rows - at);
         const int cap = P.s.width * P.s.page;  // (at most kMaxPlace)
         // places up to that of the last row
-        end = length < 0 ? 0 : static_cast<int>(min(static_cast<i64>(length) + (rows <= N ? rows / P.group : (at + count - 1) / P.group + 1), static_cast<i64>(cap)));
+        end = length < 0 ? 0 : static_cast<int>(min(static_cast<i64>(length) + (P.by_group(at + count - 1) + 1), static_cast<i64>(cap)));
         start = 0;
-        if (P.window > 0 && length >= 0) start = static_cast<int>(min(max(0ll, static_cast<i64>(length) + at / P.group + 1 - P.window), static_cast<i64>(cap)));
+        if (P.window > 0 && length >= 0) start = static_cast<int>(min(max(0ll, static_cast<i64>(length) + P.by_group(at) + 1 - P.window), static_cast<i64>(cap)));
         if (start >= end) start = end = 0;
         t0 = start ? tile_of(P, start) : 0;
         t1 = end ? tile_of(P, end - 1) + 1 : 1;
@@ -255,12 +252,12 @@ __device__ __forceinline__ bool barrier_try(u64 *b, uint32_t parity)
 }
 __device__ __forceinline__ void barrier_wait(u64 *b, uint32_t parity, int *lost)
 {
-    if (barrier_try(b, parity)) return;
-    for (int k = 0; k < kPatience; ++k) {
-        if (barrier_try(b, parity)) return;
-        if (*reinterpret_cast<volatile int *>(lost)) return;
-    }
-    *reinterpret_cast<volatile int *>(lost) = 1;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b32 k, l;\nmov.b32 k, %3;\n$AGAIN_%=: mbarrier.try_wait.parity.shared.b64 p, [%0], %1;\n@p bra $DONE_%=;\n"
+        "ld.volatile.shared.b32 l, [%2];\nsetp.ne.b32 p, l, 0;\n@p bra $DONE_%=;\nsub.u32 k, k, 1;\nsetp.ne.b32 p, k, 0;\n@p bra $AGAIN_%=;\n"
+        "mov.b32 l, 1;\nst.volatile.shared.b32 [%2], l;\n$DONE_%=:\n}" ::"r"(shared_address(b)),
+        "r"(parity), "r"(shared_address(lost)), "n"(kPatience)
+        : "memory");
 }
 // A box of an array of heads, [1][1][box][64 elements], to shared memory (swizzled by 128 bytes).
 __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap *map, u64 *b, int element, int x, int y, int z)
@@ -513,7 +510,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     if (tid == 0) barrier_arrive(sh.q_empty + segment % S::q_buffers);  // (the factors have been read; the first product adds its arrival)
                 }
             }
-            if (flags & kEdge) {
+            if (__builtin_expect(flags & kEdge, 0)) {
                 const i64 d = static_cast<i64>(h.p0) + key0 - h.length;  // it is the d-th new token's place
                 const i64 lo = d <= 0 ? 0 : d * P.group - h.from - r0, hi = P.window > 0 ? (d + P.window) * P.group - h.from - r0 : M;
                 r_lo = static_cast<int>(min(max(lo, 0ll), static_cast<i64>(M)));
@@ -537,7 +534,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                         odd |= (w & mask) == mask || (w >> 16 & mask) == mask;
                     }
                 }
-                if (weights_any(odd)) {
+                if (__builtin_expect(weights_any(odd), 0)) {
                     // (rare: one row at a time, every element over all keys)
                     if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
                     tensor_after();
@@ -594,7 +591,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     s[r] = fmaf(s[r], by.x, less.x), s[r + 1] = fmaf(s[r + 1], by.y, less.y);
                     s[r + 2] = fmaf(s[r + 2], by.z, less.z), s[r + 3] = fmaf(s[r + 3], by.w, less.w);
                 }
-                if (flags & kEdge) {
+                if (__builtin_expect(flags & kEdge, 0)) {
 #pragma unroll
                     for (int r = 0; r < M; ++r)
                         if (r < r_lo || r >= r_hi) s[r] = -kInf;
@@ -608,7 +605,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 for (int r = 0; r < M; ++r) far[r & 3] = fmaxf(far[r & 3], s[r]);
                 renew = weights_any(fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) > W::offset + W::slack);
             }
-            if (renew) {
+            if (__builtin_expect(renew, 0)) {
 #pragma unroll 1
                 for (int c = 0; c < M; c += 8) {
                     float v[8];
@@ -669,7 +666,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
             const int head = h.head, from = h.from, count = h.count, first_row = h.first;
             const int part_first = h.part_first, part_last = h.part_last, part_slot = h.part_slot;  // (before others may take the description's room)
             barrier_arrive(sh.weighed + b);
-            if (!(flags & kLast)) continue;
+            if (__builtin_expect(!(flags & kLast), 1)) continue;
 
             // -- a segment's end: the sums over the keys, and the result or the part written
 #pragma unroll
@@ -682,7 +679,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
             if (tid < N) {
                 const float top = sh.top[tid], sound = *reinterpret_cast<volatile int *>(lost) ? __int_as_float(0x7fffffff) : 1.0f;
                 const float z = top == -kInf ? 0.0f : ((sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid])) * sound;
-                const int at_row = from + tid, j = at_row / P.group, qh = head * P.group + at_row - j * P.group;
+                const int at_row = from + tid, j = P.by_group(at_row), qh = head * P.group + at_row - j * P.group;
                 const i64 part = (static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0)) * N + tid;
                 sh.factor[tid] = z == 0 ? 0.0f : partial ? sound : (P.v_scale ? ld(P.v_scale + head) : 1.0f) / z;
                 sh.row_at[tid] = tid >= count ? -1 : partial ? part * (D * 4) : static_cast<i64>(first_row + j) * P.out_row + static_cast<i64>(qh) * P.out_head;
@@ -782,7 +779,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 // the tile's places: p0 and `places` more; a tile in parts of a page starts at its slot `slot0`
                 int p0 = walk.t * P.cut.span, places = P.cut.span, c0 = walk.t * P.cut.boxes, slot0 = 0;
                 if (P.cut.parts > 1) {
-                    c0 = walk.t / P.cut.parts;
+                    c0 = P.by_parts(walk.t);
                     slot0 = (walk.t - c0 * P.cut.parts) * P.cut.box;
                     p0 = c0 * P.s.page + slot0;
                     places = min(P.cut.box, P.s.page - slot0);
@@ -790,7 +787,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 int page[4], in[4], at[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const int k = w * 32 + lane, p = p0 + k, c = page_of(P.s, p);
+                    const int k = w * 32 + lane, p = p0 + k, c = P.s.by_page(p);
                     page[w] = -1;
                     in[w] = loads ? k : P.cut.parts > 1 ? 0 : c - c0;  // its box, and the box's places
                     at[w] = p - c * P.s.page;
@@ -807,7 +804,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     const int p = p0 + w * 32 + lane;
                     bool there = page[w] >= 0 && page[w] < P.s.pages;
 #ifdef SV_DEBUG_BOUNDS
-                    const int sl = p - page_of(P.s, p) * P.s.page;
+                    const int sl = p - P.s.by_page(p) * P.s.page;
                     if (there && w * 32 + lane < places)
                         there = inside(P.kc.at + page[w] * P.kc.page + sl * P.kc.slot + walk.head * P.kc.head, D * S::bytes_of, false) &&
                                 inside(P.vc.at + page[w] * P.vc.page + sl * P.vc.slot + walk.head * P.vc.head, D * S::bytes_of, false);
@@ -825,7 +822,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 const bool first = it == 0 || opens, last = it == n - 1 || ends;
                 if (first) ++segment;
                 if (lane == 0) {
-                    const int j0 = walk.from / P.group, j1 = (walk.from + walk.count - 1) / P.group;
+                    const int j0 = P.by_group(walk.from), j1 = P.by_group(walk.from + walk.count - 1);
                     const bool part = walk.base < u0 || walk.base + walk.tiles() > u1;
                     all = all && static_cast<i64>(p0) + kTile - 1 <= static_cast<i64>(walk.length) + j0 &&
                           (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
@@ -871,7 +868,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     const int box = P.cut.q_box;  // rows of one token side by side, so that no box has two tokens
 #pragma unroll 1
                     for (int r = lane * box; r < N; r += 32 * box) {
-                        const int at_row = from + r, j = at_row / P.group;
+                        const int at_row = from + r, j = P.by_group(at_row);
                         const int row = r < count ? first + j : P.s.rows;  // (a row behind the last: zeros)
 #pragma unroll 1
                         for (int e = 0; e < S::halves; ++e)
@@ -887,7 +884,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                         uint4 x[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int rr = r + k * kAtOnce, at_row = from + min(rr, count - 1), j = at_row / P.group;
+                            const int rr = r + k * kAtOnce, at_row = from + min(rr, count - 1), j = P.by_group(at_row);
                             x[k] = make_uint4(0, 0, 0, 0);
                             if (rr < count)
                                 x[k] = ld(reinterpret_cast<const uint4 *>(P.q + static_cast<i64>(first + j) * P.q_row + static_cast<i64>(head * P.group + at_row - j * P.group) * P.q_head) + c);
@@ -977,7 +974,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
 #pragma unroll
                         for (int k = 0; k < kPart; ++k) {
                             const int key = key0 + (k0 + k) * kEvery, page = h.page[key], p = h.p0 + key;
-                            const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - page_of(P.s, p) * P.s.page);
+                            const uint32_t slot = S::slots_told ? h.key_slot[S::slots_told ? key : 0] : static_cast<uint32_t>(p - P.s.by_page(p) * P.s.page);
                             from[k] = page >= 0 ? at + (static_cast<u64>(static_cast<uint32_t>(page)) * by_page + static_cast<u64>(slot) * by_slot) : at;
                             there |= static_cast<uint32_t>(page >= 0) << k;
                         }
@@ -1071,7 +1068,7 @@ __global__ void __launch_bounds__(256) sv_cache_join_kernel(const AttentionParam
             most = up;
         }
         if (!there || lane != 0) continue;
-        const int at_row = from + r, j = at_row / P.group, qh = head * P.group + at_row - j * P.group;
+        const int at_row = from + r, j = P.by_group(at_row), qh = head * P.group + at_row - j * P.group;
         const float f = z == 0 ? 0.0f : vs / z;
         if (z == 0) y = make_float4(0, 0, 0, 0);
         const uint2 w = P.bf16 ? make_uint2(pack<__nv_bfloat16>(y.x * f, y.y * f), pack<__nv_bfloat16>(y.z * f, y.w * f))
