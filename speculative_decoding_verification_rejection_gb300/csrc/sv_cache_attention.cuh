@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
             barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
             const int flags = h.flags;
             if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, lost);  // (the weights' room is free, and the values before the last have come)
-            int r_lo = 0, r_hi = M;  // the rows, from r0 on, that see this thread's key
+            int r_lo = 0, r_hi = key0 < P.cut.span ? M : 0;  // the rows, from r0 on, that see this thread's key
+            const bool masks = flags & kEdge || (key0 | 31) >= P.cut.span;  // (the same in a warp)
             if (flags & kFirst) {
                 const int head = h.head;
                 scale = P.scale * (P.k_scale ? ld(P.k_scale + head) : 1.0f);
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     s[r] = fmaf(s[r], by.x, less.x), s[r + 1] = fmaf(s[r + 1], by.y, less.y);
                     s[r + 2] = fmaf(s[r + 2], by.z, less.z), s[r + 3] = fmaf(s[r + 3], by.w, less.w);
                 }
-                if (__builtin_expect(flags & kEdge, 0)) {
+                if (__builtin_expect(masks, 0)) {
 #pragma unroll
                     for (int r = 0; r < M; ++r)
                         if (r < r_lo || r >= r_hi) s[r] = -kInf;
@@ -810,7 +811,8 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                                 inside(P.vc.at + page[w] * P.vc.page + sl * P.vc.slot + walk.head * P.vc.head, D * S::bytes_of, false);
 #endif
                     const uint32_t seen = __ballot_sync(~0u, there && w * 32 + lane < places && p >= walk.start && p < walk.end);
-                    all = all && seen == ~0u;
+                    const int in_word = places - w * 32;  // (places of a tile that are none do not count)
+                    all = all && seen == (in_word >= 32 ? ~0u : in_word <= 0 ? 0u : (1u << in_word) - 1);
                     if (lane == 0) h.seen[w] = seen;
                     if (in[w] >= 0 && w * 32 + lane < places) h.page[in[w]] = there ? page[w] : loads ? -1 : P.s.pages;  // (a page behind the last: zeros)
                 }
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 if (lane == 0) {
                     const int j0 = P.by_group(walk.from), j1 = P.by_group(walk.from + walk.count - 1);
                     const bool part = walk.base < u0 || walk.base + walk.tiles() > u1;
-                    all = all && static_cast<i64>(p0) + kTile - 1 <= static_cast<i64>(walk.length) + j0 &&
+                    all = all && places == P.cut.span && static_cast<i64>(p0) + places - 1 <= static_cast<i64>(walk.length) + j0 &&
                           (P.window <= 0 || static_cast<i64>(p0) > static_cast<i64>(walk.length) + j1 - P.window);
                     h.p0 = p0;
                     h.first = walk.first;
