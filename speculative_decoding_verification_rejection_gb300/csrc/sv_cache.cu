@@ -205,7 +205,7 @@ struct DeviceGuard {
 // One kernel of the attention: what it needs, and how it is launched.
 struct Kernel {
     const void *run, *join;
-    int rows, bytes, dim;
+    int rows, threads, bytes, dim;
     float offset;
 };
 
@@ -213,7 +213,7 @@ template <int KIND, int D, int N>
 Kernel kernel_of()
 {
     using S = Tile<KIND, D, N>;
-    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<KIND, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>), N, S::bytes, D,
+    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<KIND, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>), N, S::threads, S::bytes, D,
                   Weights<S::bf16>::offset};
 }
 
@@ -693,7 +693,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     }
     // Each kernel may start while the one before it ends; it waits for that on the device before it looks at memory.
     void *params[] = {&P, &maps};
-    int rc_launch = launch_after(kernel.run, static_cast<unsigned>(ctas), 640, kernel.bytes, stream, params);
+    int rc_launch = launch_after(kernel.run, static_cast<unsigned>(ctas), static_cast<unsigned>(kernel.threads), kernel.bytes, stream, params);
     if (rc_launch != SV_OK || !workspace) return rc_launch;
     int rows = kernel.rows;
     float offset = kernel.offset;

@@ -56,7 +56,7 @@ enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge =
 // waste nothing, and every key is read from shared memory once for all of them. Roles, each a warp or more: weights
 // (twice four warps; a thread has one key's scores of half of the rows), the first product, the second, a plan (the tiles
 // and their pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are
-// 8 bits or the pages small, by eight warps that copy (and widen) them vector by vector.
+// 8 bits or the pages small, by eight or sixteen warps that copy (and widen) them vector by vector.
 template <int KIND, int D, int N>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
 struct Tile {
     static constexpr bool bf16 = KIND == SV_BF16;    // type of the products
@@ -78,7 +78,8 @@ struct Tile {
     static constexpr int columns_used = (2 + blocks) * N;
     static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
     static constexpr bool slots_told = D < 256;
-    static constexpr int threads = 640;
+    static constexpr int loaders = bytes_of == 1 ? 16 : 8;  // warps that copy vector by vector, half of them keys
+    static constexpr int threads = 32 * (12 + loaders);
     static constexpr int mine = N / 2;                // rows of a weights warp
     static_assert(slots >= 2 && columns_used <= 256, "room");
     struct Head {
@@ -375,7 +376,8 @@ __device__ __forceinline__ float columns_joined(float *v, int lane)
     return join(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
-// Registers of a warp's roles: 4 x 104 + 56 of four warps each are within the 5 x 96 of the launch. (The checked
+// Registers of a warp's roles, of four warps each: 2 x 104 + 3 x 56 are within the launch's 5 x 96, 2 x 104 + 5 x 56 within
+// 7 x 72. (The checked
 // build spills instead: its calls in these loops need more than there are.)
 #ifdef SV_DEBUG_BOUNDS
 #define SV_CACHE_REGISTERS(way, count)
@@ -384,7 +386,7 @@ __device__ __forceinline__ float columns_joined(float *v, int lane)
 #endif
 
 template <int KIND, int D, int N>
-__global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
+__global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
 {
     using S = Tile<KIND, D, N>;
     constexpr bool kBf16 = S::bf16, kWide = KIND == SV_E4M3;  // 8 bits are widened to binary16
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        const int filled = loads ? 4 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
+        const int filled = loads ? S::loaders / 2 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
 #pragma unroll 1
         for (int k = 0; k < S::v_slots; ++k) {
             if (k < S::k_slots) barrier_init(sh.k_full + k, filled), barrier_init(sh.k_empty + k, 1);
@@ -931,7 +933,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
             }
         }
     } else {
-        SV_CACHE_REGISTERS("inc", 104);
+        SV_CACHE_REGISTERS("dec", 56);
         if (!loads) {
             if (warp == 12) {
                 // -- values by boxes
@@ -946,19 +948,20 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                 }
             }
         } else {
-            // -- keys (four warps) and values (four warps) vector by vector: copied to their slot, or to a room of the thread's
+            // -- keys (half of the warps) and values vector by vector: copied to their slot, or to a room of the thread's
             // own and widened from there. A tile is given on when kLag more have been asked for.
-            const bool values = warp >= 16;
-            constexpr int kRow = D * S::bytes_of / 16, kEvery = 128 / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's vectors
+            constexpr int kSide = 16 * S::loaders;  // threads
+            const bool values = warp >= 12 + S::loaders / 2;
+            constexpr int kRow = D * S::bytes_of / 16, kEvery = kSide / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's vectors
             constexpr int kLag = kWide ? S::staged - 1 : S::k_slots > 2 ? S::k_slots - 2 : S::k_slots - 1;
-            const int x = tid & 127, c = x % kRow, key0 = x / kRow, slots = values ? S::v_slots : S::k_slots;
+            const int x = (tid - 384) % kSide, c = x % kRow, key0 = x / kRow, slots = values ? S::v_slots : S::k_slots;
             const Cache &cache = values ? P.vc : P.kc;
             // (strides in vectors of 16 bytes, below 2^32)
             const uint32_t by_page = static_cast<uint32_t>(cache.page >> 4), by_slot = static_cast<uint32_t>(cache.slot >> 4);
             u64 *const fulls = values ? sh.v_full : sh.k_full, *const empties = values ? sh.v_empty : sh.k_empty;
             unsigned char *const ring = room + (values ? S::k_slots * S::slot : 0);
             auto place_of = [&](unsigned char *slot, int chunk, int key) { return slot + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4); };
-            auto own = [&](int it, int k) { return staging + ((((it % (S::staged ? S::staged : 1)) * 2 + values) * kEach + k) * 128 + x) * 16; };
+            auto own = [&](int it, int k) { return staging + ((((it % (S::staged ? S::staged : 1)) * 2 + values) * kEach + k) * kSide + x) * 16; };
             int asked = 0, given = 0;  // slots
             uint32_t asked_turn = 0, given_turn = 0;
 #pragma unroll 1
@@ -993,7 +996,7 @@ __global__ void __launch_bounds__(640, 1) sv_cache_attention_kernel(const Attent
                     if (it - kLag >= slots) barrier_wait(empties + given, given_turn ^ 1, lost);
                     // (of the lanes of a key those of the upper half write their second vector first: eight lanes, eight banks)
                     const bool second = kRow == 8 ? c >> 2 : kRow == 4 ? 0 : c >> 2 & 1;
-                    constexpr int kPart = 4;
+                    constexpr int kPart = kEach < 4 ? kEach : 4;
 #pragma unroll 1
                     for (int k0 = 0; k0 < kEach; k0 += kPart) {
                         uint4 v[kPart];
