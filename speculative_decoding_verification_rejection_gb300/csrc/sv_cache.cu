@@ -698,7 +698,7 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     int rows = kernel.rows;
     float offset = kernel.offset;
     void *join[] = {&P, &rows, &offset};
-    return launch_after(kernel.join, static_cast<unsigned>(ctas), 256, 0, stream, join);
+    return launch_after(kernel.join, static_cast<unsigned>(ctas), kJoinThreads, 0, stream, join);
 }
 
 #ifdef SV_DEBUG_BOUNDS

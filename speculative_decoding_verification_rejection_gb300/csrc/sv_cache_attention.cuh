@@ -78,6 +78,9 @@ struct Tile {
     static constexpr int columns_used = (2 + blocks) * N;
     static constexpr int columns = columns_used <= 64 ? 64 : columns_used <= 128 ? 128 : 256;
     static constexpr bool slots_told = D < 256;
+    // Factors of the queries of `kept` segments: when those of a segment are written, the weights of all but the two tiles before
+    // the last scores are done, and so those of the segment whose place they take.
+    static constexpr int kept = q_buffers + 2;
     static constexpr int loaders = bytes_of == 1 ? 16 : 8;  // warps that copy vector by vector, half of them keys
     static constexpr int threads = 32 * (12 + loaders);
     static constexpr int mine = N / 2;                // rows of a weights warp
@@ -95,12 +98,16 @@ struct Tile {
         Head head[heads];
         alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
         alignas(16) float factor[N];  // what a new reference makes of the old sums; of the result
-        alignas(16) float scale[N];   // of the scores
-        alignas(16) float most[4][N];  // by warps: largest scores, sums of weights
+        alignas(16) float scale[bytes_of == 1 ? N : 4];  // of the scores
+        union {
+            alignas(16) float most[4][N];  // by warps: largest scores, sums of weights
+            struct {
+                uint32_t scan[32], start[2];  // before the first tile
+            };
+        };
         float top[N];                 // the reference, times log2 e
         i64 row_at[N];                // where a row's result goes, in bytes from its array's start; -1: nowhere
-        float q_scale[2][N];          // of queries held in binary16
-        uint32_t scan[32], start[2];
+        float q_scale[kept][bytes_of == 1 ? N : 1];  // of queries held in binary16
         uint32_t tensor_at;
         int lost;
     };
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
         for (int k = 0; k < S::heads; ++k) barrier_init(sh.told + k, 1), barrier_init(sh.used + k, 2);  // (used: by the second product, and by the warp of the queries)
 #pragma unroll 1
         for (int k = 0; k < 2; ++k)
-            barrier_init(sh.scores + k, 1), barrier_init(sh.weighed + k, 256), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, kWide ? 2 : 1);
+            barrier_init(sh.scores + k, 2), barrier_init(sh.weighed + k, 256), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, 1);
         sh.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -495,7 +502,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
             const int b = it & 1;
             const uint32_t turn = it >> 1 & 1;
             auto &h = sh.head[it % S::heads];
-            barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+            barrier_wait(sh.scores + b, turn, lost);
+            tensor_after();
             const int flags = h.flags;
             if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, lost);  // (the weights' room is free, and the values before the last have come)
             int r_lo = 0, r_hi = key0 < P.cut.span ? M : 0;  // the rows, from r0 on, that see this thread's key
@@ -507,10 +515,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
                 for (int r = 0; r < M; ++r) sum[r] = 0;
                 if constexpr (kWide) {
                     const int segment = h.segment;
-                    barrier_wait(sh.q_full + segment % S::q_buffers, segment / S::q_buffers & 1, lost);
-                    if (tid < N) sh.scale[tid] = scale * sh.q_scale[segment % S::q_buffers][tid];
+                    if (tid < N) sh.scale[tid] = scale * sh.q_scale[segment % S::kept][tid];
                     weights_meet();
-                    if (tid == 0) barrier_arrive(sh.q_empty + segment % S::q_buffers);  // (the factors have been read; the first product adds its arrival)
                 }
             }
             if (__builtin_expect(flags & kEdge, 0)) {
@@ -579,8 +585,6 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
             }
 
             // -- the scores relative to the reference; a new one where some score is too far above it
-            barrier_wait(sh.scores + b, turn, lost);
-            tensor_after();
             const uint32_t scores_at = lanes + b * N + r0;
             float s[M];
             auto relative = [&] {
@@ -666,8 +670,11 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
             }
             shared_to_async();
             tensor_before();
-            const int head = h.head, from = h.from, count = h.count, first_row = h.first;
-            const int part_first = h.part_first, part_last = h.part_last, part_slot = h.part_slot;  // (before others may take the description's room)
+            int head = 0, from = 0, count = 0, first_row = 0, part_first = 0, part_last = 0, part_slot = 0;
+            if (flags & kLast) {  // (before others may take the description's room)
+                head = h.head, from = h.from, count = h.count, first_row = h.first;
+                part_first = h.part_first, part_last = h.part_last, part_slot = h.part_slot;
+            }
             barrier_arrive(sh.weighed + b);
             if (__builtin_expect(!(flags & kLast), 1)) continue;
 
@@ -745,6 +752,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
                     product(tensor + (it & 1) * N, static_cast<uint32_t>(a) + (k / 4 * S::piece + k % 4 * 32) / 16, static_cast<uint32_t>(a >> 32),
                             static_cast<uint32_t>(q) + (k / 4 * (N * 128) + k % 4 * 32) / 16, static_cast<uint32_t>(q >> 32), kShape, k > 0, leader);
                 products_close(sh.scores + (it & 1), leader);
+                if (leader) barrier_arrive(sh.scores + (it & 1));  // (and with it what this warp has seen: the description, the queries' factors)
                 products_close(sh.k_empty + s, leader);
                 if (flags & kLast) products_close(sh.q_empty + qb, leader);
             }
@@ -919,7 +927,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
                             }
                             if (rr < N) {
                                 *reinterpret_cast<uint4 *>(q_room + qb * S::q_bytes + c / 8 * (N * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[k];
-                                if (c == 0) sh.q_scale[qb][rr] = less;
+                                if (c == 0) sh.q_scale[segment % S::kept][rr] = less;
                             }
                         }
                     }
@@ -1031,40 +1039,55 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
 }
 
 // Joins the parts of the groups that more than one CTA has. A group over k + 1 CTAs has k CTAs here, which share its
-// outputs; a few lanes take the parts of four elements.
+// outputs; a few lanes take the parts of four elements, up to four parts of a lane at once. What it takes is three trips to
+// memory, one after the other.
+constexpr int kJoinThreads = 512;
+
 template <int D>
-__global__ void __launch_bounds__(256) sv_cache_join_kernel(const AttentionParams P, int rows, float offset)
+__global__ void __launch_bounds__(kJoinThreads) sv_cache_join_kernel(const AttentionParams P, int rows, float offset)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 a = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x));
-    const int first = a.x, last = a.y, row0 = a.w;
+    const int4 a = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x)), b = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x) + 1);
+    const int first = a.x, last = a.y, row0 = a.w, from = b.x, count = b.y, head = b.z;
     if (first < 0) return;
-    const int4 b = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x) + 1);
-    const int from = b.x, count = b.y, head = b.z;
     const int share = last - first, mine = static_cast<int>(blockIdx.x) - first, items = count * (D / 4);
-    const int lo = static_cast<int>(static_cast<i64>(items) * mine / share), hi = static_cast<int>(static_cast<i64>(items) * (mine + 1) / share);
+    const int lo = items * mine / share, hi = items * (mine + 1) / share;
+    // as many lanes as there is room for, and no more than there are parts
     int lanes = 1;
-    while (lanes < 32 && lanes * 4 < share + 1) lanes *= 2;
-    const int each = 256 / lanes, lane = threadIdx.x % lanes;
+    while (lanes < 32 && lanes <= share && (hi - lo) * lanes * 2 <= kJoinThreads) lanes *= 2;
+    const int each = kJoinThreads / lanes, lane = threadIdx.x & (lanes - 1), nth = threadIdx.x / lanes;
     const float vs = P.v_scale ? ld(P.v_scale + head) : 1.0f;
+#pragma unroll 1
     for (int base = lo; base < hi; base += each) {
-        const int item = base + threadIdx.x / lanes;
+        const int item = base + nth;
         const bool there = item < hi;
         const int r = there ? item / (D / 4) : 0, c = there ? item % (D / 4) * 4 : 0;
-        auto part = [&](int k) { return (static_cast<i64>(first + k) * 2 + (k == 0 ? a.z : 0)) * rows + r; };
         float most = -kInf, z = 0;
         float4 y = make_float4(0, 0, 0, 0);
-        for (int k = lane; k <= share; k += lanes) {
-            const float2 s = ld_own(P.stats + part(k));
-            const float4 v = ld_own(reinterpret_cast<const float4 *>(P.sums + part(k) * D + c));
-            const float up = fmaxf(most, s.x), at = up == -kInf ? 0.0f : up;
-            const float f = exp2_fast(most - at), g = s.x == up ? 1.0f : exp2_fast(s.x - at);
-            z = z * f + s.y * g;
-            y = make_float4(y.x * f + v.x * g, y.y * f + v.y * g, y.z * f + v.z * g, y.w * f + v.w * g);
-            most = up;
+#pragma unroll 1
+        for (int k0 = lane; k0 <= share; k0 += 4 * lanes) {
+            float2 s[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int q = k0 + k * lanes;
+                const i64 part = (static_cast<i64>(first + q) * 2 + (q == 0 ? a.z : 0)) * rows + r;
+                s[k] = make_float2(-kInf, 0);
+                v[k] = make_float4(0, 0, 0, 0);
+                if (q <= share) s[k] = ld_own(P.stats + part), v[k] = ld_own(reinterpret_cast<const float4 *>(P.sums + part * D + c));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float up = larger(most, s[k].x), at = up == -kInf ? 0.0f : up;
+                const float f = exp2_fast(most - at), g = s[k].x == up ? 1.0f : exp2_fast(s[k].x - at);
+                z = z * f + s[k].y * g;
+                y = make_float4(y.x * f + v[k].x * g, y.y * f + v[k].y * g, y.z * f + v[k].z * g, y.w * f + v[k].w * g);
+                most = up;
+            }
         }
+#pragma unroll 1
         for (int d = lanes / 2; d; d /= 2) {
-            const float up = fmaxf(most, __shfl_xor_sync(~0u, most, d)), at = up == -kInf ? 0.0f : up, f = exp2_fast(most - at);
+            const float up = larger(most, __shfl_xor_sync(~0u, most, d)), at = up == -kInf ? 0.0f : up, f = exp2_fast(most - at);
             auto add = [&](float &v) {
                 v *= f;
                 v += __shfl_xor_sync(~0u, v, d);

@@ -291,7 +291,7 @@ def test_attention_strides_and_rows_behind():
     table = torch.full((s.n, 2 * s.width + 1), -3, dtype=torch.int32, device="cuda")
     table[:, 1:1 + s.width] = s.table.cuda()
     again, = sv.cache_attention(cuda(s.q), k, v, table[:, 1:1 + s.width], cuda(s.lengths), cu_num_draft=cuda(s.cu))
-    torch.testing.assert_close(again, got[0][:s.rows], rtol=0, atol=0)
+    off_by(again, want[0], err[0], "a view of a page table")   # (other sizes may be split otherwise)
 
 
 def test_one_row_a_request_without_prefix_sums():
