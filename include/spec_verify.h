@@ -599,7 +599,7 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  * interleaved (2 m, 2 m + 1), is turned by the angle a = pos * inv_freq[m]:
  * (y1, y2) = (x1 cos a - x2 sin a, x1 sin a + x2 cos a); elements from rotary_dim on stay as they
  * are. a is taken modulo a turn in fixed point (steps of 2^-64 of a turn; its error is below
- * 2^-52 |a| + 2^-29), so far positions lose nothing; sums and products are binary32, rounded once to the
+ * 2^-47 |a| + 2^-29), so far positions lose little; sums and products are binary32, rounded once to the
  * element type. Values beyond 448 of an SV_E4M3 cache become 448, NaN stays NaN.
  *   q, q_out        [num_rows, num_q_heads, head_dim] of dtype (num_q_heads 0: none); q_out may be q
  *                   itself with the same strides
@@ -607,12 +607,13 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  *   k_cache, v_cache [num_pages, page_size, num_kv_heads, head_dim] of cache_dtype: dtype, or SV_E4M3
  *   page_table      [num_reqs, pages_per_req] int32, rows table_stride apart
  *   lengths         [num_reqs] int32;  cu_num_draft [num_reqs + 1] int32 or NULL
- *   inv_freq        [rotary_dim / 2] binary32, radians a position; NULL with rotary_dim 0
+ *   inv_freq        [rotary_dim / 2] binary32, radians a position, below 2^20 (NaN comes of others);
+ *                   NULL with rotary_dim 0
  *   positions       NULL (pos = x), or [num_axes, num_rows] int32, rows positions_stride apart: pos
  *                   of pair m is that of axis axes[m] (axes a HOST array of rotary_dim / 2 bytes below
  *                   num_axes, read during the call; NULL: axis 0)
  *   k_scale, v_scale [num_kv_heads] binary32 or NULL, with SV_E4M3 only: what is stored is the
- *                   value divided by the scale
+ *                   value times the reciprocal of the scale
  *   head_dim a multiple of 16 up to SV_MAX_HEAD_DIM, rotary_dim one up to head_dim
  */
 typedef struct spec_verify_cache_append_args {

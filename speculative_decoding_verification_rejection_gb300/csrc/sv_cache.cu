@@ -22,8 +22,9 @@ using namespace sv_cache;
 // append
 // ---------------------------------------------------------------------------------------
 // Every element is read once and written once; what is computed is a sine and cosine a pair and row (not
-// a head: a block turns all heads of a row by the same table in shared memory) and six operations a
-// pair and head, so memory bounds it.
+// a head: a warp turns all heads that it has of a row by one table in shared memory) and six operations a
+// pair and head, so memory bounds it. A warp has a row, or a part of one where there are few rows, and asks for
+// its first elements before it looks for the row's request, page and position: warps do not wait for one another.
 //
 // The angle in turns, modulo one: pos * frac(inv_freq / 2 pi) with the fraction in steps of 2^-64, one
 // 64-bit product whose upper bits wrap away exactly the whole turns. A binary32 angle of position 10^6
@@ -38,10 +39,15 @@ struct AppendParams {
     const int32_t *positions;
     i64 positions_stride;
     int hq, hk, dim, half, interleaved;
+    int parts, items;  // parts of a row, 16-element items of a part
+    Divider by_parts, by_items_a_head;
     uint32_t axes[SV_MAX_HEAD_DIM / 2 / 16];  // two bits a pair
 };
 
 constexpr int kAppendThreads = 256;
+// Blocks of a call at most, twice what the device holds: those that start later ask for their rows while others write
+// (16001 rows 55 us, with half of them 62).
+constexpr int kAppendBlocks = 152 * 8;
 
 // The 16 elements that a thread turns: two runs of 8 where the pairs are half a rotary dimension apart, else one run.
 struct Item {
@@ -71,99 +77,138 @@ __device__ __forceinline__ uint4 pack8(const float *x)
 {
     return make_uint4(pack<T>(x[0], x[1]), pack<T>(x[2], x[3]), pack<T>(x[4], x[5]), pack<T>(x[6], x[7]));
 }
-// 8 values divided by their head's scale, rounded once.
-__device__ __forceinline__ uint2 pack8_e4m3(const float *x, float scale)
+// 8 values times the reciprocal of their head's scale, rounded once.
+__device__ __forceinline__ uint2 pack8_e4m3(const float *x, float by)
 {
     uint32_t h[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = e4m3_of(x[2 * k] / scale, x[2 * k + 1] / scale);
+    for (int k = 0; k < 4; ++k) h[k] = e4m3_of(x[2 * k] * by, x[2 * k + 1] * by);
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) sv_cache_append_kernel(const AppendParams P)
+constexpr int kAppendAtOnce = 2;  // items of a lane that are on the way at once
+
+// A pair's share of a turn a position, frac(f / 2 pi) in steps of 2^-64. The product with 1 / 2 pi, known to 49 bits as two
+// numbers, is one too: its error is below 2^-48 of it. (Binary64 runs at a sixtieth of the binary32 rate here: 256 x 6 rows
+// took 30 us with it.)
+__device__ __forceinline__ u64 turn_of(float f)
 {
-    __shared__ float2 table[2][SV_MAX_HEAD_DIM / 2];
-    const int per_head = P.dim / 16, items = (P.hq + 2 * P.hk) * per_head;
-    // this thread's pair: its share of a turn a position, in steps of 2^-64
-    u64 turn = 0;
-    bool odd = false;
-    if (threadIdx.x < P.half) {
-        const double f = static_cast<double>(ld(P.inv_freq + threadIdx.x)) * 0.15915494309189533577;  // / 2 pi
-        odd = !(fabs(f) < 1e300);
-        turn = __double2ull_rn(odd ? 0.0 : (f - floor(f)) * 18446744073709551616.0);
+    const float hi = f * 0x1.45f306p-3f, lo = fmaf(f, 0x1.45f306p-3f, -hi) + f * 0x1.b9391p-28f;
+    return (static_cast<u64>(__float2ll_rn((hi - truncf(hi)) * 0x1p63f)) << 1) + static_cast<u64>(__float2ll_rn(lo * 0x1p64f));
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads, 4) sv_cache_append_kernel(const AppendParams P)
+{
+    __shared__ float2 tables[kAppendThreads / 32][SV_MAX_HEAD_DIM / 2];
+    __shared__ u64 turns[SV_MAX_HEAD_DIM / 2];
+    __shared__ bool sound[SV_MAX_HEAD_DIM / 2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, per_head = P.dim / 16, all = (P.hq + 2 * P.hk) * per_head;
+    float2 *const table = tables[warp];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int m = threadIdx.x; m < P.half; m += kAppendThreads) {
+        const float f = ld(P.inv_freq + m);
+        sound[m] = fabsf(f) < 0x1p20f;
+        turns[m] = sound[m] ? turn_of(f) : 0;
     }
-    int flip = 0;
-    for (int r = blockIdx.x; r < P.s.rows; r += gridDim.x) {
-        const int i = request_of(P.s, r);
-        const int length = i < 0 ? -1 : ld(P.s.lengths + i);
-        if (length < 0) continue;  // (all threads agree)
-        int first;
-        request_rows(P.s, i, first);
-        const i64 x = static_cast<i64>(length) + (r - first);
-        i64 page = 0;
+    __syncthreads();
+    struct Where {
+        const unsigned char *from;
+        Item m;
+        int head, kind;  // kind 0: queries, 1: keys, 2: values
+    };
+    auto where = [&](int r, int at) {
+        const int head = P.by_items_a_head(at), c = at - head * per_head;
+        Where w;
+        w.kind = head < P.hq ? 0 : head < P.hq + P.hk ? 1 : 2;
+        w.head = head - (w.kind == 0 ? 0 : w.kind == 1 ? P.hq : P.hq + P.hk);
+        w.m = w.kind == 2 ? Item{c * 16, c * 16 + 8, -1} : item_of(c, P.half, P.interleaved);
+        w.from = w.kind == 0 ? P.q + r * P.q_row + w.head * P.q_head : w.kind == 1 ? P.k + r * P.k_row + w.head * P.k_head : P.v + r * P.v_row + w.head * P.v_head;
+        return w;
+    };
+    const i64 units = static_cast<i64>(P.s.rows) * P.parts;
+#pragma unroll 1
+    for (i64 u = static_cast<i64>(blockIdx.x) * (kAppendThreads / 32) + warp; u < units; u += static_cast<i64>(gridDim.x) * (kAppendThreads / 32)) {
+        const int r = P.parts == 1 ? static_cast<int>(u) : P.by_parts(static_cast<int>(u)), part = P.parts == 1 ? 0 : static_cast<int>(u) - r * P.parts;
+        const int lo = part * P.items, hi = min(lo + P.items, all);
+        i64 page = -1;
         int slot = 0;
-        const bool kept = place(P.s, i, x, page, slot);
-        if (threadIdx.x < P.half) {
-            const int axis = P.axes[threadIdx.x / 16] >> (threadIdx.x % 16 * 2) & 3;
-            const i64 pos = P.positions ? static_cast<i64>(ld(P.positions + axis * P.positions_stride + r)) : x;
-            const int half_turns = static_cast<int>((static_cast<u64>(pos) * turn) >> 32);  // of 2^-31
-            float2 cs;
-            sincospif(static_cast<float>(half_turns) * 0x1p-31f, &cs.y, &cs.x);
-            table[flip][threadIdx.x] = odd ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)) : cs;
-        }
-        __syncthreads();  // (one a row that is turned: the next one's table is the other)
-        const float2 *turns = table[flip];
-        flip ^= 1;
-        for (int at = blockIdx.y * kAppendThreads + threadIdx.x; at < items; at += gridDim.y * kAppendThreads) {
-            const int head = at / per_head, h = head < P.hq ? head : head < P.hq + P.hk ? head - P.hq : head - P.hq - P.hk;
-            const bool is_q = head < P.hq, is_v = head >= P.hq + P.hk;
-            if (!is_q && !kept) continue;
-            Item m = item_of(at - head * per_head, P.half, P.interleaved);
-            if (is_v && m.pair >= 0) m = Item{(at - head * per_head) * 16, (at - head * per_head) * 16 + 8, -1};
-            const unsigned char *src = is_q ? P.q + r * P.q_row + h * P.q_head : is_v ? P.v + r * P.v_row + h * P.v_head : P.k + r * P.k_row + h * P.k_head;
-            const uint4 a = ld_own(reinterpret_cast<const uint4 *>(src + m.first * 2)), b = ld_own(reinterpret_cast<const uint4 *>(src + m.second * 2));
-            float u[8], w[8];
-            unpack8<T>(a, u);
-            unpack8<T>(b, w);
-            if (m.pair >= 0) {
-                const float2 *t = turns + m.pair;
-                if (P.interleaved) {
+#pragma unroll 1
+        for (int at0 = lo; at0 < hi; at0 += 32 * kAppendAtOnce) {
+            uint4 a[kAppendAtOnce], b[kAppendAtOnce];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 c = t[e], d = t[e + 4];
-                        const float u0 = u[2 * e], u1 = u[2 * e + 1], w0 = w[2 * e], w1 = w[2 * e + 1];
-                        u[2 * e] = u0 * c.x - u1 * c.y;
-                        u[2 * e + 1] = u0 * c.y + u1 * c.x;
-                        w[2 * e] = w0 * d.x - w1 * d.y;
-                        w[2 * e + 1] = w0 * d.y + w1 * d.x;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 c = t[e];
-                        const float u0 = u[e], w0 = w[e];
-                        u[e] = u0 * c.x - w0 * c.y;
-                        w[e] = u0 * c.y + w0 * c.x;
-                    }
+            for (int k = 0; k < kAppendAtOnce; ++k) {
+                const int at = at0 + k * 32 + lane;
+                if (at < hi) {
+                    const Where w = where(r, at);
+                    a[k] = ld_own(reinterpret_cast<const uint4 *>(w.from + w.m.first * 2));
+                    b[k] = ld_own(reinterpret_cast<const uint4 *>(w.from + w.m.second * 2));
                 }
             }
-            if (is_q) {
-                unsigned char *to = P.q_out + r * P.out_row + h * P.out_head;
-                st(reinterpret_cast<uint4 *>(to + m.first * 2), pack8<T>(u));
-                st(reinterpret_cast<uint4 *>(to + m.second * 2), pack8<T>(w));
-                continue;
+            if (at0 == lo) {
+                const int i = request_of(P.s, r);
+                const int length = i < 0 ? -1 : ld(P.s.lengths + i);
+                if (length < 0) break;  // (the warp's lanes agree)
+                int first;
+                request_rows(P.s, i, first);
+                const i64 x = static_cast<i64>(length) + (r - first);
+                if (!place(P.s, i, x, page, slot)) page = -1;
+                __syncwarp();  // (the table of the row before has been read)
+#pragma unroll 1
+                for (int m = lane; m < P.half; m += 32) {
+                    const int axis = P.axes[m / 16] >> (m % 16 * 2) & 3;
+                    const i64 pos = P.positions ? static_cast<i64>(ld(P.positions + axis * P.positions_stride + r)) : x;
+                    const int half_turns = static_cast<int>((static_cast<u64>(pos) * turns[m]) >> 32);  // of 2^-31
+                    float2 cs;
+                    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &cs.y, &cs.x);
+                    table[m] = sound[m] ? cs : make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+                }
+                __syncwarp();
             }
-            const Cache &c = is_v ? P.vc : P.kc;
-            unsigned char *to = c.at + page * c.page + slot * c.slot + h * c.head;
-            if constexpr (E4M3) {
-                const float *scales = is_v ? P.v_scale : P.k_scale;
-                const float scale = scales ? ld(scales + h) : 1.0f;
-                st(reinterpret_cast<uint2 *>(to + m.first), pack8_e4m3(u, scale));
-                st(reinterpret_cast<uint2 *>(to + m.second), pack8_e4m3(w, scale));
-            } else {
-                st(reinterpret_cast<uint4 *>(to + m.first * 2), pack8<T>(u));
-                st(reinterpret_cast<uint4 *>(to + m.second * 2), pack8<T>(w));
+#pragma unroll
+            for (int k = 0; k < kAppendAtOnce; ++k) {
+                const int at = at0 + k * 32 + lane;
+                if (at >= hi) continue;
+                const Where x = where(r, at);
+                if (x.kind && page < 0) continue;
+                float y[8], w[8];
+                unpack8<T>(a[k], y);
+                unpack8<T>(b[k], w);
+                if (x.m.pair >= 0) {
+                    const float2 *t = table + x.m.pair;
+                    if (P.interleaved) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 c = t[e], d = t[e + 4];
+                            const float y0 = y[2 * e], y1 = y[2 * e + 1], w0 = w[2 * e], w1 = w[2 * e + 1];
+                            y[2 * e] = y0 * c.x - y1 * c.y;
+                            y[2 * e + 1] = y0 * c.y + y1 * c.x;
+                            w[2 * e] = w0 * d.x - w1 * d.y;
+                            w[2 * e + 1] = w0 * d.y + w1 * d.x;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 c = t[e];
+                            const float y0 = y[e], w0 = w[e];
+                            y[e] = y0 * c.x - w0 * c.y;
+                            w[e] = y0 * c.y + w0 * c.x;
+                        }
+                    }
+                }
+                const Cache &c = x.kind == 2 ? P.vc : P.kc;
+                if (E4M3 && x.kind) {
+                    unsigned char *const to = c.at + page * c.page + slot * c.slot + x.head * c.head;
+                    const float *scales = x.kind == 2 ? P.v_scale : P.k_scale;
+                    const float by = scales ? 1.0f / ld(scales + x.head) : 1.0f;
+                    st(reinterpret_cast<uint2 *>(to + x.m.first), pack8_e4m3(y, by));
+                    st(reinterpret_cast<uint2 *>(to + x.m.second), pack8_e4m3(w, by));
+                } else {
+                    unsigned char *const to = x.kind ? c.at + page * c.page + slot * c.slot + x.head * c.head : P.q_out + r * P.out_row + x.head * P.out_head;
+                    st(reinterpret_cast<uint4 *>(to + x.m.first * 2), pack8<T>(y));
+                    st(reinterpret_cast<uint4 *>(to + x.m.second * 2), pack8<T>(w));
+                }
             }
         }
     }
@@ -519,6 +564,7 @@ extern "C" int spec_verify_cache_append(const spec_verify_cache_append_args *a, 
     const int rc = check_step(*a, kc, vc);
     if (rc != SV_OK) return rc;
     if (!kc.distinct() || !vc.distinct() || a->num_q_heads < 0) return SV_EINVAL;
+    if (static_cast<i64>(a->num_q_heads) + 2ll * a->num_kv_heads > 65536) return SV_ECAPACITY;
     if (a->num_pages > 0 && a->k_cache == a->v_cache) return SV_EINVAL;
     if (a->rotary_dim > 0 && (!a->inv_freq || misaligned(a->inv_freq, 4))) return SV_EINVAL;
     if (a->positions && (a->num_axes < 1 || misaligned(a->positions, 4) || (a->num_axes > 1 && a->positions_stride < a->num_rows))) return SV_EINVAL;
@@ -588,21 +634,21 @@ extern "C" int spec_verify_cache_append(const spec_verify_cache_append_args *a, 
     add_step(s, *a);
     if (s.push(stream) != SV_OK) return SV_ECUDA;
 #endif
-    const int items = (P.hq + 2 * P.hk) * (D / 16), parts = (items + kAppendThreads - 1) / kAppendThreads;
-    const int per_row = a->num_rows < 2 * 152 ? parts : 1;
-    const dim3 grid(static_cast<unsigned>(std::min(a->num_rows, 8 * 152)), static_cast<unsigned>(std::min(per_row, 65535)));
-    if (a->dtype == SV_BF16) {
-        if (a->cache_dtype == SV_E4M3)
-            sv_cache_append_kernel<__nv_bfloat16, true><<<grid, kAppendThreads, 0, stream>>>(P);
-        else
-            sv_cache_append_kernel<__nv_bfloat16, false><<<grid, kAppendThreads, 0, stream>>>(P);
-    } else {
-        if (a->cache_dtype == SV_E4M3)
-            sv_cache_append_kernel<__half, true><<<grid, kAppendThreads, 0, stream>>>(P);
-        else
-            sv_cache_append_kernel<__half, false><<<grid, kAppendThreads, 0, stream>>>(P);
-    }
-    return status_of(cudaGetLastError());
+    // Parts of a row where there are fewer rows than the device holds warps (32 an SM): no more than one a warp, of 32 items
+    // at least.
+    const int items = (P.hq + 2 * P.hk) * (D / 16), most = (items + 31) / 32;
+    P.parts = std::max(1, std::min(most, 152 * 32 / a->num_rows));
+    P.items = (items + P.parts - 1) / P.parts;
+    P.by_parts = Divider(static_cast<uint32_t>(P.parts));
+    P.by_items_a_head = Divider(static_cast<uint32_t>(D / 16));
+    const i64 blocks = (static_cast<i64>(a->num_rows) * P.parts + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+    const void *kernel = a->dtype == SV_BF16
+                             ? a->cache_dtype == SV_E4M3 ? reinterpret_cast<const void *>(sv_cache_append_kernel<__nv_bfloat16, true>)
+                                                         : reinterpret_cast<const void *>(sv_cache_append_kernel<__nv_bfloat16, false>)
+                         : a->cache_dtype == SV_E4M3 ? reinterpret_cast<const void *>(sv_cache_append_kernel<__half, true>)
+                                                     : reinterpret_cast<const void *>(sv_cache_append_kernel<__half, false>);
+    void *params[] = {&P};
+    return launch_after(kernel, static_cast<unsigned>(std::min<i64>(blocks, kAppendBlocks)), kAppendThreads, 0, stream, params);
 }
 
 extern "C" int spec_verify_cache_attention_workspace(const spec_verify_cache_attention_args *a, int64_t *bytes)

@@ -90,7 +90,7 @@ def ref_append(s: Step, inv_freq=None, positions=None, axes=None, interleaved=Fa
         y[:, lo], y[:, hi] = one * cos - two * sin, one * sin + two * cos
         # the angle; sincospi's 2 units of 2^-24 (of values up to 1) and its argument's rounding (pi 2^-24);
         # two products and a sum
-        size = (one.abs() + two.abs()) * (a.abs() * 2.0**-52 + 2.0**-29 + 8 * 2.0**-24)
+        size = (one.abs() + two.abs()) * (a.abs() * 2.0**-47 + 2.0**-29 + 8 * 2.0**-24)
         e[:, lo] = e[:, hi] = size
         return y, e
 
@@ -107,7 +107,7 @@ def ref_append(s: Step, inv_freq=None, positions=None, axes=None, interleaved=Fa
         for name, (y, e), scale in (("k", turn(s.k[r], pos), s.k_scale), ("v", (s.v[r].double(), torch.zeros(s.v[r].shape, dtype=torch.float64)), s.v_scale)):
             if scale is not None:
                 y, e = y / scale.double()[:, None], e / scale.double()[:, None]
-                e = e + y.abs() * 2.0**-24
+                e = (e + y.abs() * 2.0**-23) * 1.01   # (the reciprocal's rounding and the product's)
             most = torch.finfo(s.kind).max
             e = e + (y.abs() + e) * HALF[s.kind] + smallest(s.kind) / 2
             out[name][at] = y.clamp(-most, most) if s.kind is TYPES["e4m3"] else y

@@ -33,7 +33,7 @@ def test_append_pages_and_layouts(page, layout):
 
 
 def test_append_far_positions_and_axes():
-    """Angles of positions up to 2^31: in 64 bits they are known to 2^-22 of a turn there and to 2^-33 at 2^20."""
+    """Angles of positions up to 2^31: they are known to 2^-16 radians there and to 2^-27 at 2^20."""
     s = Step(3, [1000, 0, 77], [4, 9, 3], dim=128, hq=4, hk=1)
     g = torch.Generator().manual_seed(4)
     positions = torch.randint(0, 2**31 - 1, (3, s.rows), generator=g).int()
