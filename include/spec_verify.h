@@ -592,6 +592,7 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
 #define SV_MAX_HEAD_DIM 256
 #define SV_MAX_AXES 4
 #define SV_MAX_PAGE 65536
+#define SV_CACHE_WORKSPACE 10121984 /* bytes of workspace that any spec_verify_cache_attention is content with */
 
 /*
  * spec_verify_cache_append: k and v of every row into the cache, k turned by its position and so
@@ -662,8 +663,8 @@ int spec_verify_cache_append(const spec_verify_cache_append_args *args, void *cu
  *   scale           finite;  window 0: none
  *   head_dim        64, 128 or 256
  *   workspace       device memory of workspace_bytes, at least what
- *                   spec_verify_cache_attention_workspace says (of the same arguments; it may be 0),
- *                   16-byte aligned; its contents matter neither before nor after. Calls that may
+ *                   spec_verify_cache_attention_workspace says (of the same arguments; it may be 0, and
+ *                   is never above SV_CACHE_WORKSPACE), 16-byte aligned; its contents matter neither before nor after. Calls that may
  *                   overlap need one each
  * Any number of new rows a request; the kernels are made for the few of a draft or verification step.
  */

@@ -41,7 +41,7 @@ SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 1, 2
 SV_MAX_SYNTHETIC = 64
 SV_ROWS_MAX_VOCAB, SV_MAX_TOP = 524288, 64
-SV_MAX_HEAD_DIM, SV_MAX_AXES, SV_MAX_PAGE = 256, 4, 65536
+SV_MAX_HEAD_DIM, SV_MAX_AXES, SV_MAX_PAGE, SV_CACHE_WORKSPACE = 256, 4, 65536, 10121984
 
 
 class Batch(ctypes.Structure):
@@ -655,74 +655,102 @@ def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_
 _CODES = {}  # element types of the cache operators and their codes
 
 
-def _code(name, t) -> int:
+def _code(name, dtype) -> int:
     if not _CODES:
         import torch
 
         _CODES.update({torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3})
-    code = _CODES.get(t.dtype)
+    code = _CODES.get(dtype)
     if code is None:
-        raise ValueError(f"{name} has the unsupported dtype {t.dtype}")
+        raise ValueError(f"{name} has the unsupported dtype {dtype}")
     return code
 
 
-def _head_rows(name, t, shape, dtype, device):
-    """(address, row stride, head stride) of a [rows, heads, head_dim] device tensor whose heads are
-    contiguous, checked."""
+def _head_rows(name, t, shape, dtype, index):
+    """(address, row stride, head stride) of a [rows, heads, head_dim] tensor on device `index` whose heads
+    are contiguous, checked."""
+    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    at = t.data_ptr()
+    if (t.shape == shape and t.dtype is dtype and t.get_device() == index and one == 1 and not at & 15
+            and (not row & 7 or shape[0] == 1) and (not head & 7 or shape[1] == 1)):
+        return at, row, head
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    row, head, one = t.stride()
-    at = t.data_ptr()
-    if one != 1 or at & 15 or (row & 7 and shape[0] > 1) or (head & 7 and shape[1] > 1):
-        raise ValueError(f"{name}'s heads must be contiguous, its address and strides multiples of 16 bytes")
-    return at, row, head
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name}'s heads must be contiguous, its address and strides multiples of 16 bytes")
+
+
+def _whole(name, t, dtype, shape, index):
+    """Address of a contiguous tensor of this shape on device `index`, checked."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale, rows, heads, dim, dtype,
-             device):
-    """The arguments that the cache operators share, checked: (addresses of the caches, their strides, the
-    page table and what follows it, sizes of the pool, type codes)."""
+             index):
+    """The arguments that the cache operators share, checked: (strides of the caches, the page table and what
+    follows it, the scales, sizes of the pool, heads, type code, number of requests)."""
     import torch
 
     i32 = torch.int32
-    if k_cache.dim() != 4 or k_cache.shape[3] != dim or v_cache.shape != k_cache.shape:
+    shape, kind = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or shape[3] != dim or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim], head_dim that of the rows")
-    if k_cache.dtype is not v_cache.dtype or (k_cache.dtype is not dtype and k_cache.dtype is not torch.float8_e4m3fn):
-        raise ValueError(f"caches have dtype {k_cache.dtype} and {v_cache.dtype}, expected {dtype} or torch.float8_e4m3fn")
-    if k_cache.device != device or v_cache.device != device:
-        raise ValueError(f"caches are on {k_cache.device} and {v_cache.device}, expected {device}")
-    strides = (*k_cache.stride(), *v_cache.stride())
-    if strides[3] != 1 or strides[7] != 1:
+    if v_cache.dtype is not kind or (kind is not dtype and kind is not torch.float8_e4m3fn):
+        raise ValueError(f"caches have dtype {kind} and {v_cache.dtype}, expected {dtype} or torch.float8_e4m3fn")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError(f"caches are on {k_cache.device} and {v_cache.device}, expected cuda:{index}")
+    k_page, k_slot, k_head, k_one = k_cache.stride()
+    v_page, v_slot, v_head, v_one = v_cache.stride()
+    if k_one != 1 or v_one != 1:
         raise ValueError("the caches' heads must be contiguous")
-    if heads is not None and k_cache.shape[2] != heads:
-        raise ValueError(f"the caches hold {k_cache.shape[2]} heads, the rows {heads}")
+    if heads is not None and shape[2] != heads:
+        raise ValueError(f"the caches hold {shape[2]} heads, the rows {heads}")
+    table = page_table.shape
     n = lengths.shape[0] if lengths.dim() == 1 else -1
-    if page_table.dim() != 2 or page_table.shape[0] != n:
+    if len(table) != 2 or table[0] != n:
         raise ValueError("page_table must be [num_reqs, pages], lengths [num_reqs]")
-    width = page_table.shape[1]
-    if page_table.dtype is not i32 or page_table.device != device:
-        raise ValueError(f"page_table must be int32 on {device}")
-    table_stride = page_table.stride(0) if n > 1 else width
-    if (width > 1 and page_table.stride(1) != 1) or table_stride < width:
+    width = table[1]
+    if page_table.dtype is not i32 or page_table.get_device() != index:
+        raise ValueError(f"page_table must be int32 on cuda:{index}")
+    table_stride, one = page_table.stride()
+    if n <= 1:
+        table_stride = width
+    if (width > 1 and one != 1) or table_stride < width:
         raise ValueError("page_table's rows must be contiguous and must not overlap")
-    cu = None
+    cu = ks = vs = None
     if cu_num_draft is not None:
-        cu = _row_array("cu_num_draft", cu_num_draft, i32, (n + 1,), device)
+        cu = _whole("cu_num_draft", cu_num_draft, i32, (n + 1,), index)
     elif rows < n:
         raise ValueError(f"without cu_num_draft every request has a row: {n} requests, {rows} rows")
-    cache_code = _code("k_cache", k_cache)
-    if cache_code != SV_E4M3 and (k_scale is not None or v_scale is not None):
-        raise ValueError("scales belong to float8_e4m3fn caches")
-    scale_shape, f32 = (k_cache.shape[2],), torch.float32
-    return (strides[:3] + strides[4:7],
-            (page_table.data_ptr(), table_stride, _row_array("lengths", lengths, i32, (n,), device), cu),
-            (None if k_scale is None else _row_array("k_scale", k_scale, f32, scale_shape, device),
-             None if v_scale is None else _row_array("v_scale", v_scale, f32, scale_shape, device)),
-            (k_cache.shape[0], k_cache.shape[1], width), cache_code, n)
+    code = _code("k_cache", kind)
+    if k_scale is not None or v_scale is not None:
+        if code != SV_E4M3:
+            raise ValueError("scales belong to float8_e4m3fn caches")
+        ks = None if k_scale is None else _whole("k_scale", k_scale, torch.float32, (shape[2],), index)
+        vs = None if v_scale is None else _whole("v_scale", v_scale, torch.float32, (shape[2],), index)
+    return ((k_page, k_slot, k_head, v_page, v_slot, v_head),
+            (page_table.data_ptr(), table_stride, _whole("lengths", lengths, i32, (n,), index), cu),
+            (ks, vs), (shape[0], shape[1], width), shape[2], code, n)
+
+
+def _new(shape, dtype, device, stream):
+    """A new tensor, of the memory that belongs to the stream that works on it."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _row_outputs(None, [("", dtype, shape)], device, stream)[0]
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_freq=None, cu_num_draft=None,
@@ -754,46 +782,51 @@ def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_fre
         raise ValueError("k must be [rows, kv_heads, head_dim]")
     if not k.is_cuda:
         raise ValueError("k must be on a CUDA device")
-    rows, hk, dim = k.shape
-    dev, dtype = k.device, k.dtype
-    code = _code("k", k)
+    shape, dtype, index = k.shape, k.dtype, k.get_device()
+    rows, hk, dim = shape
+    code = _code("k", dtype)
     if code == SV_E4M3:
         raise ValueError(f"k has the unsupported dtype {dtype}")
-    strides, step, scales, pool, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
-                                                          k_scale, v_scale, rows, hk, dim, dtype, dev)
-    kp = _head_rows("k", k, (rows, hk, dim), dtype, dev)
-    vp = _head_rows("v", v, (rows, hk, dim), dtype, dev)
+    strides, step, scales, pool, _, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+                                                             k_scale, v_scale, rows, hk, dim, dtype, index)
+    kp = _head_rows("k", k, shape, dtype, index)
+    vp = _head_rows("v", v, shape, dtype, index)
     qp = op = (None, 0, 0)
     hq = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [rows, q_heads, head_dim]")
         hq = q.shape[1]
-        qp = _head_rows("q", q, (rows, hq, dim), dtype, dev)
+        qp = _head_rows("q", q, (rows, hq, dim), dtype, index)
         if out is None:
-            (out,) = _row_outputs(None, [("out", dtype, (rows, hq, dim))], dev, stream)
-        op = _head_rows("out", out, (rows, hq, dim), dtype, dev)
+            out = _new((rows, hq, dim), dtype, k.device, stream)
+        op = qp if out is q else _head_rows("out", out, (rows, hq, dim), dtype, index)
     elif out is not None:
         raise ValueError("out without q")
     half = 0
+    inv = pos = axis_bytes = None
     if inv_freq is not None:
+        import torch
+
         half = inv_freq.numel()
-        inv_freq = _row_array("inv_freq", inv_freq, torch.float32, (half,), dev)
-    num_axes, pos, pos_stride, axis_bytes = 0, None, 0, None
+        inv = _whole("inv_freq", inv_freq, torch.float32, (half,), index)
+    num_axes, pos_stride = 0, 0
     if positions is not None:
+        import torch
+
         if positions.dim() == 1:
             positions = positions[None]
         num_axes, pos_stride = positions.shape[0], rows
-        pos = _row_array("positions", positions, torch.int32, (num_axes, rows), dev)
+        pos = _whole("positions", positions, torch.int32, (num_axes, rows), index)
     if axes is not None:
         if len(axes) != half:
             raise ValueError(f"axes must name the axis of each of the {half} pairs")
         axis_bytes = bytes(axes)
     spec_verify_cache_append(
         CacheAppendArgs(qp[0], kp[0], vp[0], op[0], k_cache.data_ptr(), v_cache.data_ptr(), qp[1], qp[2], kp[1], kp[2],
-                        vp[1], vp[2], op[1], op[2], *strides, *step, pos, pos_stride, inv_freq, *scales,
-                        axis_bytes, rows, n, hq, hk, dim, 2 * half, bool(interleaved), num_axes, *pool, code,
-                        cache_code, dev.index), _current_stream(dev.index) if stream is None else stream)
+                        vp[1], vp[2], op[1], op[2], *strides, *step, pos, pos_stride, inv, *scales, axis_bytes, rows,
+                        n, hq, hk, dim, 2 * half, 1 if interleaved else 0, num_axes, *pool, code, cache_code, index),
+        _current_stream(index) if stream is None else stream)
     return out
 
 
@@ -813,36 +846,37 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=No
     calls may overlap. The exact rules stand at spec_verify_cache_attention in include/spec_verify.h."""
     import torch
 
+    import torch
+
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     if not q.is_cuda:
         raise ValueError("q must be on a CUDA device")
-    rows, hq, dim = q.shape
-    dev, dtype = q.device, q.dtype
-    code = _code("q", q)
+    shape, dtype, index = q.shape, q.dtype, q.get_device()
+    rows, hq, dim = shape
+    code = _code("q", dtype)
     if code == SV_E4M3:
         raise ValueError(f"q has the unsupported dtype {dtype}")
-    strides, step, scales, pool, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
-                                                          k_scale, v_scale, rows, None, dim, dtype, dev)
-    hk = k_cache.shape[2]
+    strides, step, scales, pool, hk, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+                                                              k_scale, v_scale, rows, None, dim, dtype, index)
     if hk < 1 or hq < 1 or hq % hk:
         raise ValueError(f"{hq} query heads are not a multiple of the caches' {hk} heads")
-    qp = _head_rows("q", q, (rows, hq, dim), dtype, dev)
-    want = [("out", dtype, (rows, hq, dim))]
-    if lse:
-        want.append(("lse", torch.float32, (rows, hq)))
-    got = _row_outputs(out, want, dev, stream)
-    op = _head_rows("out", got[0], (rows, hq, dim), dtype, dev)
-    lp = _row_array("lse", got[1], torch.float32, (rows, hq), dev) if lse else None
-    args = CacheAttentionArgs(qp[0], k_cache.data_ptr(), v_cache.data_ptr(), op[0], lp, qp[1], qp[2], op[1], op[2],
-                              *strides, *step, *scales, None, 0, dim ** -0.5 if scale is None else scale, window, rows, n,
-                              hq, hk, dim, *pool, code, cache_code, dev.index)
-    need = spec_verify_cache_attention_workspace(args)
-    if need:
-        (space,) = _row_outputs(None, [("workspace", torch.uint8, (need,))], dev, stream)
-        args.workspace, args.workspace_bytes = space.data_ptr(), need
-    spec_verify_cache_attention(args, _current_stream(dev.index) if stream is None else stream)
-    return tuple(got)
+    qp = _head_rows("q", q, shape, dtype, index)
+    if out is None:
+        out = [_new(shape, dtype, q.device, stream)]
+        if lse:
+            out.append(_new((rows, hq), torch.float32, q.device, stream))
+    elif len(out) != 1 + bool(lse):
+        raise ValueError("out must hold out, lse" if lse else "out must hold out")
+    op = _head_rows("out", out[0], shape, dtype, index)
+    lp = _whole("lse", out[1], torch.float32, (rows, hq), index) if lse else None
+    space = _new((SV_CACHE_WORKSPACE,), torch.uint8, q.device, stream)
+    spec_verify_cache_attention(
+        CacheAttentionArgs(qp[0], k_cache.data_ptr(), v_cache.data_ptr(), op[0], lp, qp[1], qp[2], op[1], op[2],
+                           *strides, *step, *scales, space.data_ptr(), SV_CACHE_WORKSPACE,
+                           dim ** -0.5 if scale is None else scale, window, rows, n, hq, hk, dim, *pool, code, cache_code,
+                           index), _current_stream(index) if stream is None else stream)
+    return tuple(out)
 
 
 # ---- convenience owner ---------------------------------------------------------------------

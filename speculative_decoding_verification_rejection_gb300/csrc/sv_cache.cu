@@ -521,6 +521,8 @@ i64 ctas_for(const spec_verify_cache_attention_args &a, const Kernel &k)
 // Whether groups may have to be joined: not where each has one tile.
 bool joins(const spec_verify_cache_attention_args &a, const Kernel &k) { return most_tiles(a, k) > 1; }
 
+static_assert(SV_CACHE_WORKSPACE == 152 * (2 * 64 * (128 + 2) * 4 + sizeof(Part)), "the largest of the kernels'");
+
 int64_t workspace_of(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
     return joins(a, k) ? ctas_for(a, k) * (2ll * k.rows * (k.dim + 2) * 4 + static_cast<int64_t>(sizeof(Part))) : 0;

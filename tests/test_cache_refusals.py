@@ -85,8 +85,14 @@ def test_null_arguments():
 
 
 def test_workspace_goes_by_sizes_alone():
-    args = attention_args(q=None, out=None, k_cache=None, v_cache=None, page_table=None, lengths=None, workspace=None, workspace_bytes=0)
-    assert sv.spec_verify_cache_attention_workspace(args) >= 0
+    args = attention_args(q=None, out=None, k_cache=None, v_cache=None, page_table=None, lengths=None, workspace=None, workspace_bytes=0, pages_per_req=100, table_stride=100)
+    assert 0 < sv.spec_verify_cache_attention_workspace(args) <= sv.SV_CACHE_WORKSPACE
+    one_tile = attention_args(pages_per_req=8, page_size=16)
+    assert sv.spec_verify_cache_attention_workspace(one_tile) == 0   # (nothing to join)
+    most = max(sv.spec_verify_cache_attention_workspace(attention_args(head_dim=d, num_q_heads=2 * g, num_rows=3000, num_reqs=300, page_size=64,
+                                                                       pages_per_req=4000, table_stride=4000, cache_dtype=c))
+               for d in (64, 128, 256) for g in (1, 2, 3, 5, 6, 7, 8, 16) for c in (sv.SV_BF16, sv.SV_E4M3))
+    assert most == sv.SV_CACHE_WORKSPACE
     with pytest.raises(sv.SpecVerifyError):
         sv.spec_verify_cache_attention_workspace(attention_args(head_dim=65))
 
@@ -99,7 +105,8 @@ def fake(shape, dtype=torch.bfloat16, device="cuda:0"):
             self.t = t
 
         def __getattr__(self, name):
-            return {"device": torch.device(device), "is_cuda": True}.get(name, None) if name in ("device", "is_cuda") else getattr(self.t, name)
+            told = {"device": torch.device(device), "is_cuda": device != "cpu", "get_device": lambda: torch.device(device).index if device != "cpu" else -1}
+            return told[name] if name in told else getattr(self.t, name)
 
     return On(torch.zeros(shape, dtype=dtype))
 
