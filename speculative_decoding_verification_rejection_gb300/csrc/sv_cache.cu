@@ -551,6 +551,7 @@ int check_attention(const spec_verify_cache_attention_args &a, View &k, View &v)
     if (rc != SV_OK) return rc;
     if (a.num_q_heads < 1 || a.num_q_heads % a.num_kv_heads != 0 || a.window < 0 || !std::isfinite(a.scale)) return SV_EINVAL;
     if (static_cast<int64_t>(a.pages_per_req) * a.page_size > kMaxPlace) return SV_ECAPACITY;
+    if (static_cast<int64_t>(a.num_rows) * (a.num_q_heads / a.num_kv_heads) >= (1ll << 31)) return SV_ECAPACITY;
     return SV_OK;
 }
 

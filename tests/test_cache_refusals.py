@@ -69,6 +69,7 @@ def test_append_refuses(change, status):
     (dict(head_dim=80), sv.SV_EINVAL), (dict(head_dim=512), sv.SV_EINVAL), (dict(num_q_heads=5), sv.SV_EINVAL),
     (dict(num_q_heads=0), sv.SV_EINVAL), (dict(window=-1), sv.SV_EINVAL), (dict(scale=float("nan")), sv.SV_EINVAL),
     (dict(scale=float("inf")), sv.SV_EINVAL), (dict(out=None), sv.SV_EINVAL), (dict(out=P), sv.SV_EINVAL), (dict(out=P + 4), sv.SV_EINVAL),
+    (dict(num_q_heads=1 << 20, num_kv_heads=1, num_rows=1 << 12, num_reqs=1), sv.SV_ECAPACITY), (dict(pages_per_req=1 << 20, page_size=1 << 11, table_stride=1 << 20), sv.SV_ECAPACITY),
     (dict(lse=P + 2), sv.SV_EINVAL), (dict(lse=None), sv.SV_EDEVICE), (dict(workspace=P + 8), sv.SV_EINVAL),
     (dict(out_head_stride=32), sv.SV_EINVAL), (dict(out_row_stride=0), sv.SV_EINVAL), (dict(k_page_stride=0), sv.SV_EINVAL), (dict(q_row_stride=0), sv.SV_EINVAL),
 ])

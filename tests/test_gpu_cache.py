@@ -391,6 +391,58 @@ def test_captured_steps_follow_their_device_side_lengths():
                 off_by(got, w, e, name)
 
 
+def test_captured_behind_copies_and_another_stream():
+    """In a graph a call may follow a copy, a fill, a kernel, and work of another stream that is joined before it."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    s = Step(75, [300, 20], [3, 2], hq=8, hk=2, dim=64, page=16)
+    k, v = s.device_caches()
+    table, lengths, cu, q0 = cuda(s.table), cuda(s.lengths), cuda(s.cu), cuda(s.q)
+    q, ks, vs = torch.zeros_like(q0), torch.zeros_like(cuda(s.k)), cuda(s.v)
+    kk = cuda(s.k)
+    out, lse = torch.empty_like(q), torch.empty(s.rows, s.hq, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            ks.copy_(kk)
+        q.zero_()
+        here.wait_stream(side)
+        sv.cache_append(ks, vs, k, v, table, lengths, cu_num_draft=cu)
+        q.copy_(q0)
+        sv.cache_attention(q, k, v, table, lengths, cu_num_draft=cu, lse=True, out=[out, lse])
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        out.fill_(9)
+        k[s.slot(0, 300)] = 0
+        g.replay()
+    torch.cuda.synchronize()
+    for r, i, x in s.rows_of():
+        s.k_cache[s.slot(i, x)], s.v_cache[s.slot(i, x)] = s.k[r], s.v[r]
+    want, err = ref_attention(s)
+    off_by(out, want[0], err[0], "out")
+    off_by(lse, want[1], err[1], "lse")
+
+
+def test_an_empty_pool():
+    """No page at all: nothing is written, no key is seen."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    s = Step(76, [30, 2], [2, 3], hq=4, hk=2, dim=64)
+    for kind in (torch.bfloat16, torch.float8_e4m3fn):
+        none = torch.zeros(0, 16, 2, 64, dtype=kind, device="cuda")
+        q = sv.cache_append(cuda(s.k), cuda(s.v), none, torch.zeros_like(none), cuda(s.table), cuda(s.lengths), q=cuda(s.q), cu_num_draft=cuda(s.cu))
+        assert torch.equal(q, cuda(s.q))
+        out, lse = sv.cache_attention(cuda(s.q), none, none, cuda(s.table), cuda(s.lengths), cu_num_draft=cuda(s.cu), lse=True)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+
+
 def test_offsets_beyond_32_bits():
     """A pool of 6 GB with the pages in use at its end."""
     import speculative_decoding_verification_rejection_gb300 as sv
