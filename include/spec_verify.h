@@ -656,7 +656,8 @@ int spec_verify_cache_append(const spec_verify_cache_append_args *args, void *cu
  * g / (num_q_heads / num_kv_heads). A row that sees no key (or only keys of score -inf) gets out 0 and
  * lse -inf. Keys and values that a row does not see do not reach it, whatever they hold. Products of
  * elements are exact, sums, maxima and Z binary32; weights are rounded to the products' 16-bit type
- * relative to a maximum of their row.
+ * (binary16 for SV_E4M3 caches) relative to a reference near their row's largest. Results repeat bit for
+ * bit for the same arguments; calls of other sizes may be split otherwise.
  *   q, out          [num_rows, num_q_heads, head_dim] of dtype (SV_BF16 / SV_F16)
  *   lse             [num_rows, num_q_heads] binary32 (out) or NULL
  *   k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale: as above
