@@ -652,35 +652,55 @@ def logprobs(logits, tokens=None, *, num_top: int = 0, temperature=None, cu_num_
 
 # ---- cache operators -----------------------------------------------------------------------
 
-_CODES = {}  # element types of the cache operators and their codes
+_CODES = {}   # element types of the cache operators and their codes
+_torch = None  # what the cache operators take of PyTorch, looked up once: a call's lookups are a good part of its time
 
 
-def _code(name, dtype) -> int:
-    if not _CODES:
+class _Torch:
+    """PyTorch's types and functions that a call of a cache operator uses, and the library's functions."""
+
+    def __init__(self):
         import torch
 
+        self.int32, self.float32, self.uint8, self.e4m3 = torch.int32, torch.float32, torch.uint8, torch.float8_e4m3fn
+        self.empty, self.stream = torch.empty, torch._C._cuda_getCurrentRawStream
         _CODES.update({torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3})
-    code = _CODES.get(dtype)
-    if code is None:
-        raise ValueError(f"{name} has the unsupported dtype {dtype}")
+        self.append, self.attention, self.byref = lib().spec_verify_cache_append, lib().spec_verify_cache_attention, ctypes.byref
+
+
+def _cache_torch():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _rows_code(name, t) -> int:
+    """Type code of a [rows, heads, head_dim] tensor of the rows, checked."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, {name}_heads, head_dim]" if name == "q" else f"{name} must be [rows, kv_heads, head_dim]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    code = _CODES.get(t.dtype)
+    if code is None or code == SV_E4M3:
+        raise ValueError(f"{name} has the unsupported dtype {t.dtype}")
     return code
 
 
 def _head_rows(name, t, shape, dtype, index):
     """(address, row stride, head stride) of a [rows, heads, head_dim] tensor on device `index` whose heads
     are contiguous, checked."""
-    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-    at = t.data_ptr()
-    if (t.shape == shape and t.dtype is dtype and t.get_device() == index and one == 1 and not at & 15
-            and (not row & 7 or shape[0] == 1) and (not head & 7 or shape[1] == 1)):
-        return at, row, head
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index:
+        row, head, one = t.stride()
+        at = t.data_ptr()
+        if not (one != 1 or at & 15 or (row & 7 and shape[0] != 1) or (head & 7 and shape[1] != 1)):
+            return at, row, head
+        raise ValueError(f"{name}'s heads must be contiguous, its address and strides multiples of 16 bytes")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    raise ValueError(f"{name}'s heads must be contiguous, its address and strides multiples of 16 bytes")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def _whole(name, t, dtype, shape, index):
@@ -696,17 +716,14 @@ def _whole(name, t, dtype, shape, index):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale, rows, heads, dim, dtype,
+def _step_of(T, k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_scale, rows, heads, dim, dtype,
              index):
     """The arguments that the cache operators share, checked: (strides of the caches, the page table and what
     follows it, the scales, sizes of the pool, heads, type code, number of requests)."""
-    import torch
-
-    i32 = torch.int32
     shape, kind = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or shape[3] != dim or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim], head_dim that of the rows")
-    if v_cache.dtype is not kind or (kind is not dtype and kind is not torch.float8_e4m3fn):
+    if v_cache.dtype is not kind or (kind is not dtype and kind is not T.e4m3):
         raise ValueError(f"caches have dtype {kind} and {v_cache.dtype}, expected {dtype} or torch.float8_e4m3fn")
     if k_cache.get_device() != index or v_cache.get_device() != index:
         raise ValueError(f"caches are on {k_cache.device} and {v_cache.device}, expected cuda:{index}")
@@ -714,14 +731,14 @@ def _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_sca
     v_page, v_slot, v_head, v_one = v_cache.stride()
     if k_one != 1 or v_one != 1:
         raise ValueError("the caches' heads must be contiguous")
-    if heads is not None and shape[2] != heads:
-        raise ValueError(f"the caches hold {shape[2]} heads, the rows {heads}")
-    table = page_table.shape
-    n = lengths.shape[0] if lengths.dim() == 1 else -1
-    if len(table) != 2 or table[0] != n:
+    pages, page, hk, _ = shape
+    if heads is not None and hk != heads:
+        raise ValueError(f"the caches hold {hk} heads, the rows {heads}")
+    n = lengths.numel()
+    if page_table.dim() != 2 or lengths.dim() != 1 or page_table.shape[0] != n:
         raise ValueError("page_table must be [num_reqs, pages], lengths [num_reqs]")
-    width = table[1]
-    if page_table.dtype is not i32 or page_table.get_device() != index:
+    width = page_table.shape[1]
+    if page_table.dtype is not T.int32 or page_table.get_device() != index:
         raise ValueError(f"page_table must be int32 on cuda:{index}")
     table_stride, one = page_table.stride()
     if n <= 1:
@@ -730,26 +747,24 @@ def _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_sca
         raise ValueError("page_table's rows must be contiguous and must not overlap")
     cu = ks = vs = None
     if cu_num_draft is not None:
-        cu = _whole("cu_num_draft", cu_num_draft, i32, (n + 1,), index)
+        cu = _whole("cu_num_draft", cu_num_draft, T.int32, (n + 1,), index)
     elif rows < n:
         raise ValueError(f"without cu_num_draft every request has a row: {n} requests, {rows} rows")
-    code = _code("k_cache", kind)
+    code = _CODES[kind]
     if k_scale is not None or v_scale is not None:
         if code != SV_E4M3:
             raise ValueError("scales belong to float8_e4m3fn caches")
-        ks = None if k_scale is None else _whole("k_scale", k_scale, torch.float32, (shape[2],), index)
-        vs = None if v_scale is None else _whole("v_scale", v_scale, torch.float32, (shape[2],), index)
+        ks = None if k_scale is None else _whole("k_scale", k_scale, T.float32, (hk,), index)
+        vs = None if v_scale is None else _whole("v_scale", v_scale, T.float32, (hk,), index)
     return ((k_page, k_slot, k_head, v_page, v_slot, v_head),
-            (page_table.data_ptr(), table_stride, _whole("lengths", lengths, i32, (n,), index), cu),
-            (ks, vs), (shape[0], shape[1], width), shape[2], code, n)
+            (page_table.data_ptr(), table_stride, _whole("lengths", lengths, T.int32, (n,), index), cu),
+            (ks, vs), (pages, page, width), hk, code, n)
 
 
-def _new(shape, dtype, device, stream):
+def _new(T, shape, dtype, device, stream):
     """A new tensor, of the memory that belongs to the stream that works on it."""
-    import torch
-
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return T.empty(shape, dtype=dtype, device=device)
     return _row_outputs(None, [("", dtype, shape)], device, stream)[0]
 
 
@@ -778,55 +793,45 @@ def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_fre
     at spec_verify_cache_append in include/spec_verify.h."""
     import torch
 
-    if k.dim() != 3:
-        raise ValueError("k must be [rows, kv_heads, head_dim]")
-    if not k.is_cuda:
-        raise ValueError("k must be on a CUDA device")
+    T = _torch or _cache_torch()
+    code = _rows_code("k", k)
     shape, dtype, index = k.shape, k.dtype, k.get_device()
     rows, hk, dim = shape
-    code = _code("k", dtype)
-    if code == SV_E4M3:
-        raise ValueError(f"k has the unsupported dtype {dtype}")
-    strides, step, scales, pool, _, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+    strides, step, scales, pool, _, cache_code, n = _step_of(T, k_cache, v_cache, page_table, lengths, cu_num_draft,
                                                              k_scale, v_scale, rows, hk, dim, dtype, index)
-    kp = _head_rows("k", k, shape, dtype, index)
-    vp = _head_rows("v", v, shape, dtype, index)
+    k_at, k_row, k_head = _head_rows("k", k, shape, dtype, index)
+    v_at, v_row, v_head = _head_rows("v", v, shape, dtype, index)
     qp = op = (None, 0, 0)
-    hq = 0
+    hq = half = num_axes = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [rows, q_heads, head_dim]")
         hq = q.shape[1]
         qp = _head_rows("q", q, (rows, hq, dim), dtype, index)
         if out is None:
-            out = _new((rows, hq, dim), dtype, k.device, stream)
+            out = _new(T, (rows, hq, dim), dtype, k.device, stream)
         op = qp if out is q else _head_rows("out", out, (rows, hq, dim), dtype, index)
     elif out is not None:
         raise ValueError("out without q")
-    half = 0
     inv = pos = axis_bytes = None
     if inv_freq is not None:
-        import torch
-
         half = inv_freq.numel()
-        inv = _whole("inv_freq", inv_freq, torch.float32, (half,), index)
-    num_axes, pos_stride = 0, 0
+        inv = _whole("inv_freq", inv_freq, T.float32, (half,), index)
     if positions is not None:
-        import torch
-
         if positions.dim() == 1:
             positions = positions[None]
-        num_axes, pos_stride = positions.shape[0], rows
-        pos = _whole("positions", positions, torch.int32, (num_axes, rows), index)
+        num_axes = positions.shape[0]
+        pos = _whole("positions", positions, T.int32, (num_axes, rows), index)
     if axes is not None:
         if len(axes) != half:
             raise ValueError(f"axes must name the axis of each of the {half} pairs")
         axis_bytes = bytes(axes)
-    spec_verify_cache_append(
-        CacheAppendArgs(qp[0], kp[0], vp[0], op[0], k_cache.data_ptr(), v_cache.data_ptr(), qp[1], qp[2], kp[1], kp[2],
-                        vp[1], vp[2], op[1], op[2], *strides, *step, pos, pos_stride, inv, *scales, axis_bytes, rows,
-                        n, hq, hk, dim, 2 * half, 1 if interleaved else 0, num_axes, *pool, code, cache_code, index),
-        _current_stream(index) if stream is None else stream)
+    args = CacheAppendArgs(qp[0], k_at, v_at, op[0], k_cache.data_ptr(), v_cache.data_ptr(), qp[1], qp[2], k_row, k_head,
+                           v_row, v_head, op[1], op[2], *strides, *step, pos, rows, inv, *scales, axis_bytes, rows, n, hq,
+                           hk, dim, 2 * half, 1 if interleaved else 0, num_axes, *pool, code, cache_code, index)
+    status = T.append(T.byref(args), T.stream(index) if stream is None else _stream_handle(stream))
+    if status:
+        _check(status, "spec_verify_cache_append")
     return out
 
 
@@ -846,36 +851,32 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=No
     calls may overlap. The exact rules stand at spec_verify_cache_attention in include/spec_verify.h."""
     import torch
 
-    import torch
-
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, q_heads, head_dim]")
-    if not q.is_cuda:
-        raise ValueError("q must be on a CUDA device")
+    T = _torch or _cache_torch()
+    code = _rows_code("q", q)
     shape, dtype, index = q.shape, q.dtype, q.get_device()
     rows, hq, dim = shape
-    code = _code("q", dtype)
-    if code == SV_E4M3:
-        raise ValueError(f"q has the unsupported dtype {dtype}")
-    strides, step, scales, pool, hk, cache_code, n = _step_of(k_cache, v_cache, page_table, lengths, cu_num_draft,
+    strides, step, scales, pool, hk, cache_code, n = _step_of(T, k_cache, v_cache, page_table, lengths, cu_num_draft,
                                                               k_scale, v_scale, rows, None, dim, dtype, index)
     if hk < 1 or hq < 1 or hq % hk:
         raise ValueError(f"{hq} query heads are not a multiple of the caches' {hk} heads")
-    qp = _head_rows("q", q, shape, dtype, index)
+    q_at, q_row, q_head = _head_rows("q", q, shape, dtype, index)
+    device = q.device
     if out is None:
-        out = [_new(shape, dtype, q.device, stream)]
+        out = [_new(T, shape, dtype, device, stream)]
         if lse:
-            out.append(_new((rows, hq), torch.float32, q.device, stream))
+            out.append(_new(T, (rows, hq), T.float32, device, stream))
     elif len(out) != 1 + bool(lse):
         raise ValueError("out must hold out, lse" if lse else "out must hold out")
-    op = _head_rows("out", out[0], shape, dtype, index)
-    lp = _whole("lse", out[1], torch.float32, (rows, hq), index) if lse else None
-    space = _new((SV_CACHE_WORKSPACE,), torch.uint8, q.device, stream)
-    spec_verify_cache_attention(
-        CacheAttentionArgs(qp[0], k_cache.data_ptr(), v_cache.data_ptr(), op[0], lp, qp[1], qp[2], op[1], op[2],
-                           *strides, *step, *scales, space.data_ptr(), SV_CACHE_WORKSPACE,
-                           dim ** -0.5 if scale is None else scale, window, rows, n, hq, hk, dim, *pool, code, cache_code,
-                           index), _current_stream(index) if stream is None else stream)
+    o_at, o_row, o_head = _head_rows("out", out[0], shape, dtype, index)
+    l_at = _whole("lse", out[1], T.float32, (rows, hq), index) if lse else None
+    space = _new(T, SV_CACHE_WORKSPACE, T.uint8, device, stream)
+    args = CacheAttentionArgs(q_at, k_cache.data_ptr(), v_cache.data_ptr(), o_at, l_at, q_row, q_head, o_row, o_head,
+                              *strides, *step, *scales, space.data_ptr(), SV_CACHE_WORKSPACE,
+                              dim ** -0.5 if scale is None else scale, window, rows, n, hq, hk, dim, *pool, code,
+                              cache_code, index)
+    status = T.attention(T.byref(args), T.stream(index) if stream is None else _stream_handle(stream))
+    if status:
+        _check(status, "spec_verify_cache_attention")
     return tuple(out)
 
 
