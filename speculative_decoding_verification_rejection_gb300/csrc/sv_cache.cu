@@ -254,32 +254,37 @@ struct Kernel {
     float offset;
 };
 
-template <int KIND, int D, int N>
+template <int KIND, int D, int N, bool LOADS>
 Kernel kernel_of()
 {
-    using S = Tile<KIND, D, N>;
-    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<KIND, D, N>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>), N, S::threads, S::bytes, D,
-                  Weights<S::bf16>::offset};
+    using S = Tile<KIND, D, N, LOADS>;
+    return Kernel{reinterpret_cast<const void *>(sv_cache_attention_kernel<KIND, D, N, LOADS>), reinterpret_cast<const void *>(sv_cache_join_kernel<D>), N, S::threads,
+                  S::bytes, D, Weights<S::bf16>::offset};
 }
 
-template <int KIND, int D>
+template <int KIND, int D, bool LOADS>
 Kernel kernel_of(int rows)
 {
     if constexpr (D == 256)
-        return rows == 16 ? kernel_of<KIND, D, 16>() : kernel_of<KIND, D, 32>();
+        return rows == 16 ? kernel_of<KIND, D, 16, LOADS>() : kernel_of<KIND, D, 32, LOADS>();
     else
-        return rows == 16 ? kernel_of<KIND, D, 16>() : rows == 32 ? kernel_of<KIND, D, 32>() : rows == 48 ? kernel_of<KIND, D, 48>() : kernel_of<KIND, D, 64>();
+        return rows == 16   ? kernel_of<KIND, D, 16, LOADS>()
+               : rows == 32 ? kernel_of<KIND, D, 32, LOADS>()
+               : rows == 48 ? kernel_of<KIND, D, 48, LOADS>()
+                            : kernel_of<KIND, D, 64, LOADS>();
 }
 
-template <int KIND>
+template <int KIND, bool LOADS>
 Kernel kernel_of(int dim, int rows)
 {
-    return dim == 64 ? kernel_of<KIND, 64>(rows) : dim == 128 ? kernel_of<KIND, 128>(rows) : kernel_of<KIND, 256>(rows);
+    return dim == 64 ? kernel_of<KIND, 64, LOADS>(rows) : dim == 128 ? kernel_of<KIND, 128, LOADS>(rows) : kernel_of<KIND, 256, LOADS>(rows);
 }
 
-Kernel kernel_of(int cache_dtype, int dim, int rows)
+Kernel kernel_of(int cache_dtype, int dim, int rows, bool loads)
 {
-    return cache_dtype == SV_BF16 ? kernel_of<SV_BF16>(dim, rows) : cache_dtype == SV_F16 ? kernel_of<SV_F16>(dim, rows) : kernel_of<SV_E4M3>(dim, rows);
+    if (cache_dtype == SV_E4M3) return kernel_of<SV_E4M3, true>(dim, rows);
+    if (cache_dtype == SV_BF16) return loads ? kernel_of<SV_BF16, true>(dim, rows) : kernel_of<SV_BF16, false>(dim, rows);
+    return loads ? kernel_of<SV_F16, true>(dim, rows) : kernel_of<SV_F16, false>(dim, rows);
 }
 
 constexpr int kMaxDevices = 64;
@@ -304,8 +309,8 @@ int cache_device(int dev)
     if (!guard.ok) return SV_EDEVICE;
     for (int cache : {SV_BF16, SV_F16, SV_E4M3})
         for (int dim : {64, 128, 256})
-            for (int rows = 16; rows <= 64; rows += 16) {
-                const Kernel k = kernel_of(cache, dim, rows);
+            for (int which = 0; which < 8; ++which) {
+                const Kernel k = kernel_of(cache, dim, 16 + which / 2 * 16, which % 2 != 0);
                 if (cudaFuncSetAttribute(k.run, cudaFuncAttributeMaxDynamicSharedMemorySize, k.bytes) != cudaSuccess) {
                     cudaGetLastError();
                     return SV_ECUDA;
@@ -471,6 +476,12 @@ int status_of(cudaError_t e)
     return SV_ECUDA;
 }
 
+// 8-bit caches and pages below kSmallPage places vector by vector, others by tensor map (a copy costs its warp 40 to 90 cycles,
+// whatever its size: 128 requests with pages of 20 places 95 us against 101 by vectors, 64 requests of 6 rows with pages of 64
+// 352 against 396).
+constexpr int kSmallPage = 16;
+bool by_loads(const spec_verify_cache_attention_args &a) { return a.cache_dtype == SV_E4M3 || a.page_size < kSmallPage; }
+
 // The kernel for a call. Query rows of a key head of one request (on average: the rows of each are known on the device
 // only) in tiles of 16: as few tiles over the keys as there can be, of as few rows.
 Kernel kernel_for(const spec_verify_cache_attention_args &a)
@@ -478,13 +489,10 @@ Kernel kernel_for(const spec_verify_cache_attention_args &a)
     const int most = a.head_dim == 256 ? 2 : 4;
     const i64 rows = (static_cast<i64>(a.num_rows) + std::max(a.num_reqs, 1) - 1) / std::max(a.num_reqs, 1) * (a.num_q_heads / a.num_kv_heads);
     const i64 tiles = std::max<i64>(1, (rows + 15) / 16), passes = (tiles + most - 1) / most;
-    return kernel_of(a.cache_dtype, a.head_dim, 16 * static_cast<int>((tiles + passes - 1) / passes));
+    return kernel_of(a.cache_dtype, a.head_dim, 16 * static_cast<int>((tiles + passes - 1) / passes), by_loads(a));
 }
 
-// Tiles of whole pages, or of parts of a page above 128 places, by tensor map; 8-bit caches and pages below kSmallPage places
-// by loads (a copy costs its warp 40 to 90 cycles, whatever its size).
-constexpr int kSmallPage = 16;
-
+// Tiles of whole pages, or of parts of a page above 128 places, where copies are by tensor map.
 Cut cut_of(const spec_verify_cache_attention_args &a, const Kernel &k)
 {
     const int page = a.page_size, group = a.num_q_heads / a.num_kv_heads;
@@ -494,7 +502,7 @@ Cut cut_of(const spec_verify_cache_attention_args &a, const Kernel &k)
         --q_box;
         while (group % q_box != 0) --q_box;
     }
-    if (a.cache_dtype == SV_E4M3 || page < kSmallPage) return Cut{kTile, 0, 1, kTile, q_box};
+    if (by_loads(a)) return Cut{kTile, 0, 1, kTile, q_box};
     if (page <= kTile) return Cut{kTile / page * page, page, 1, kTile / page, q_box};
     const int parts = (page + kTile - 1) / kTile, box = (page + parts - 1) / parts;
     return Cut{box, box, parts, 1, q_box};

@@ -57,7 +57,7 @@ enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge =
 // (twice four warps; a thread has one key's scores of half of the rows), the first product, the second, a plan (the tiles
 // and their pages, ahead of the others), queries and keys, values. Keys and values come by tensor map, or, where they are
 // 8 bits or the pages small, by eight or sixteen warps that copy (and widen) them vector by vector.
-template <int KIND, int D, int N>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
+template <int KIND, int D, int N, bool LOADS>  // KIND: type of the cache, SV_BF16, SV_F16 or SV_E4M3
 struct Tile {
     static constexpr bool bf16 = KIND == SV_BF16;    // type of the products
     static constexpr int bytes_of = KIND == SV_E4M3 ? 1 : 2;
@@ -81,7 +81,7 @@ struct Tile {
     // Factors of the queries of `kept` segments: when those of a segment are written, the weights of all but the two tiles before
     // the last scores are done, and so those of the segment whose place they take.
     static constexpr int kept = q_buffers + 2;
-    static constexpr int loaders = bytes_of == 1 ? 16 : 8;  // warps that copy vector by vector, half of them keys
+    static constexpr int loaders = !LOADS ? 1 : bytes_of == 1 ? 16 : 8;  // warps that copy vector by vector, half of them keys; or that of the values
     static constexpr int threads = 32 * (12 + loaders);
     static constexpr int mine = N / 2;                // rows of a weights warp
     static_assert(slots >= 2 && columns_used <= 256, "room");
@@ -383,19 +383,20 @@ __device__ __forceinline__ float columns_joined(float *v, int lane)
     return join(v[0], __shfl_xor_sync(~0u, v[0], 16));
 }
 
-// Registers of a warp's roles, of four warps each: 2 x 104 + 3 x 56 are within the launch's 5 x 96, 2 x 104 + 5 x 56 within
-// 7 x 72. (The checked
+// Registers of a warp's roles in the kernels with many warps, of four warps each: 2 x 104 + 3 x 56 are within the launch's
+// 5 x 96, 2 x 104 + 5 x 56 within 7 x 72. (The checked
 // build spills instead: its calls in these loops need more than there are.)
 #ifdef SV_DEBUG_BOUNDS
-#define SV_CACHE_REGISTERS(way, count)
+#define SV_CACHE_REGISTERS(way, count) (void)0
 #else
 #define SV_CACHE_REGISTERS(way, count) asm volatile("setmaxnreg." way ".sync.aligned.u32 " #count ";")
 #endif
 
-template <int KIND, int D, int N>
-__global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
+// (LOADS: keys vector by vector, not by tensor map. Kernels of their own, since the size of the code counts.)
+template <int KIND, int D, int N, bool LOADS>
+__global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
 {
-    using S = Tile<KIND, D, N>;
+    using S = Tile<KIND, D, N, LOADS>;
     constexpr bool kBf16 = S::bf16, kWide = KIND == SV_E4M3;  // 8 bits are widened to binary16
     using E = std::conditional_t<kBf16, __nv_bfloat16, __half>;
     using W = Weights<kBf16>;
@@ -405,7 +406,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
     const uint32_t room_at = shared_address(room), q_at = shared_address(q_room), w_at = shared_address(w_room);
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid & 31;
     const int cta = blockIdx.x;
-    const bool loads = kWide || P.cut.box == 0;  // keys by loads, not by tensor map
+    constexpr bool loads = LOADS;
+    static_assert(LOADS || !kWide, "8 bits are widened by the loading warps");
 
     // -- barriers and memory, while the work before this call ends
     if (warp == 8) {
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
         if (!kWide) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q) : "memory");
     }
-    if (!loads) {  // places of a slot that no copy writes: zeros for good
+    if constexpr (!loads) {  // places of a slot that no copy writes: zeros for good
         const int filled = P.cut.boxes * P.cut.box, piece = (kTile - filled) * 8;
 #pragma unroll 1
         for (int x = tid; x < S::slots * S::halves * piece; x += S::threads)
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
     int *const lost = &sh.lost;
 
     if (warp < 8) {
-        SV_CACHE_REGISTERS("inc", 104);
+        if constexpr (loads) SV_CACHE_REGISTERS("inc", 104);
         // -- weights: this thread has key `key0` of every tile, the elements key0 and key0 + 128 of the outputs, and rows r0 to r0 + M - 1
         constexpr int M = S::mine;
         const int key0 = tid & 127, r0 = warp / 4 * M;
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
             tensor_before();
         }
     } else if (warp < 12) {
-        SV_CACHE_REGISTERS("dec", 56);
+        if constexpr (loads) SV_CACHE_REGISTERS("dec", 56);
         if (warp == 8) {
             // -- scores^T = K Q^T
             const uint32_t leader = elected();
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
                 barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
                 const auto &h = sh.head[it % S::heads];
                 const int flags = h.flags, head = h.head;
-                if (!loads) {
+                if constexpr (!loads) {
                     boxes_to<S>(&maps.k, sh.k_full + s, sh.k_empty + s, it >= S::k_slots, turn ^ 1, room_at + s * S::slot, P.cut, h.slot, head, h.page, lane, lost);
                     if (++s == S::k_slots) s = 0, turn ^= 1;
                 }
@@ -941,8 +943,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N>::threads), 1) sv_cache_atten
             }
         }
     } else {
-        SV_CACHE_REGISTERS("dec", 56);
-        if (!loads) {
+        if constexpr (loads) SV_CACHE_REGISTERS("dec", 56);
+        if constexpr (!loads) {
             if (warp == 12) {
                 // -- values by boxes
                 int s = 0;
