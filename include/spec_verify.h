@@ -580,7 +580,8 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  * graph; calls may overlap on any streams. Problems visible on the host return a status and launch
  * nothing; 0 rows or 0 requests are SV_OK.
  *   Left out, with nothing written for them: rows behind the last request's; a request whose rows
- *   are not all within num_rows (an inconsistent cu_num_draft). A request of negative length takes no
+ *   are not all within num_rows (an inconsistent cu_num_draft; where requests overlap it is open whose
+ *   a row is, and an attention with 2^31 tiles of keys or more for it is left out). A request of negative length takes no
  *   part (a padded batch): nothing is appended and its queries are not turned; its attention
  *   outputs are those of rows that see no key. A key whose page is outside [0, num_pages), or whose
  *   place is not within pages_per_req pages, is not written, and not seen.
@@ -654,7 +655,8 @@ int spec_verify_cache_append(const spec_verify_cache_append_args *args, void *cu
  * s_t = scale * (q . k_t) for the places t <= x, and t > x - window if window > 0,
  * out = sum exp(s_t) v_t / Z, lse = ln Z, Z = sum exp(s_t). Query head g reads key head
  * g / (num_q_heads / num_kv_heads). A row that sees no key (or only keys of score -inf) gets out 0 and
- * lse -inf. Keys and values that a row does not see do not reach it, whatever they hold. Products of
+ * lse -inf. Keys and values that a row does not see do not reach it, whatever they hold; a value that is not finite
+ * under a weight that rounds to 0 gives itself or NaN. Products of
  * elements are exact, sums, maxima and Z binary32; weights are rounded to the products' 16-bit type
  * (binary16 for SV_E4M3 caches) relative to a reference near their row's largest. Results repeat bit for
  * bit for the same arguments; calls of other sizes may be split otherwise.

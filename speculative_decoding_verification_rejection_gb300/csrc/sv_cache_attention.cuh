@@ -164,6 +164,13 @@ __device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t k, uint32_
 // The last CTA whose first tile is not behind this one.
 __device__ __forceinline__ int sharer_of(uint32_t total, uint32_t number, uint32_t ctas) { return static_cast<int>((static_cast<u64>(number) * ctas + ctas - 1) / total); }
 
+// A sum that does not pass 2^32 - 1.
+__device__ __forceinline__ uint32_t sum_of(uint32_t a, uint32_t b)
+{
+    const uint32_t s = a + b;
+    return s < a ? ~0u : s;
+}
+
 // All tiles of the step in order: request, rows of a tile, key head, tokens. CTA c takes those from c W / ctas
 // to (c + 1) W / ctas, so every CTA gets as many whatever the lengths are. A group is the tiles of a request's N query
 // rows and a key head: at least one tile; keys at places [start, end) are seen by one of its rows.
@@ -204,7 +211,7 @@ struct Walk {
 #pragma unroll 1
         for (int at = 0; at < rows; at += N) {
             group(at);
-            sum += tiles() * P.hk;
+            sum += tiles() * P.hk;  // (below 2^31: the host sees to it for the rows that there are)
         }
         return sum;
     }
@@ -449,12 +456,12 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
     const int per = (P.s.n + S::threads - 1) / S::threads;
     uint32_t mine = 0;
 #pragma unroll 1
-    for (int k = tid * per; k < min(P.s.n, (tid + 1) * per); ++k) mine += walk.request_tiles(k);
+    for (int k = tid * per; k < min(P.s.n, (tid + 1) * per); ++k) mine = sum_of(mine, walk.request_tiles(k));
     auto running = [lane](uint32_t x) {
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const uint32_t up = __shfl_up_sync(~0u, x, d);
-            if (lane >= d) x += up;
+            if (lane >= d) x = sum_of(x, up);
         }
         return x;
     };
@@ -463,7 +470,9 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
     tensor_before();
     __syncthreads();
     tensor_after();
-    const uint32_t warps = running(lane < S::threads / 32 ? sh.scan[lane] : 0u), total = __shfl_sync(~0u, warps, 31);
+    const uint32_t warps = running(lane < S::threads / 32 ? sh.scan[lane] : 0u), all = __shfl_sync(~0u, warps, 31);
+    // (2^31 tiles or more come only of requests that overlap, by prefix sums that are none: such a step is left out)
+    const uint32_t total = all < 1u << 31 ? all : 0;
     before += (warp ? __shfl_sync(~0u, warps, (warp - 1) & 31) : 0u) - mine;
     const uint32_t tensor = __shfl_sync(~0u, sh.tensor_at, 0);
     const uint32_t ctas = min(total, gridDim.x);  // (each with a tile at least)

@@ -556,3 +556,24 @@ def test_steps_of_a_verification_over_the_cache():
             size = (kk[:, h // 2].abs() @ q[i, h].double().abs() / 8).max() * 2.0**-8
             tol = float(vv[:, h // 2].abs().max()) * (2 * float(size) + 3 * 2.0**-8)
             assert float((out[i, h].double() - want).abs().max()) <= tol
+
+
+def test_overlapping_requests_of_too_many_tiles_are_left_out():
+    """Prefix sums that are none, by which 1000 requests have the same 2000 rows: 4.4e9 tiles of keys, which no 32 bits
+    hold (the rows that there are have 78 million at most)."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    n, page, width = 2000, 65536, 34
+    pool = torch.zeros(1, page, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(n, width, dtype=torch.int32, device="cuda")
+    lengths = torch.full((n,), page * width - 10, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 2000] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    q = torch.zeros(4100, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((4100, 2), 7.0, device="cuda")
+    sv.cache_attention(q, pool, pool, table, lengths, cu_num_draft=cu, lse=True, out=[out, lse])
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+    # the same arrays with lengths that 32 bits hold
+    lengths.fill_(0)
+    sv.cache_attention(q, pool, pool, table, lengths, cu_num_draft=cu, lse=True, out=[out, lse])
+    assert bool((out[:2001] == 0).all()) and bool((out[4000:] == 7).all())
