@@ -740,6 +740,8 @@ def _step_of(T, k_cache, v_cache, page_table, lengths, cu_num_draft, k_scale, v_
     width = page_table.shape[1]
     if page_table.dtype is not T.int32 or page_table.get_device() != index:
         raise ValueError(f"page_table must be int32 on cuda:{index}")
+    if (pages | page | width | n | rows) >> 31:  # (the library's are 32 bits)
+        raise ValueError("pages, page_size, requests and rows must be below 2^31")
     table_stride, one = page_table.stride()
     if n <= 1:
         table_stride = width
@@ -859,6 +861,8 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=No
                                                               k_scale, v_scale, rows, None, dim, dtype, index)
     if hk < 1 or hq < 1 or hq % hk:
         raise ValueError(f"{hq} query heads are not a multiple of the caches' {hk} heads")
+    if window >> 31:
+        raise ValueError("window must be within 0 and 2^31 - 1")
     q_at, q_row, q_head = _head_rows("q", q, shape, dtype, index)
     device = q.device
     if out is None:

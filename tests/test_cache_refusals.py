@@ -147,3 +147,14 @@ def test_attention_binding_refuses(change):
         a.pop(name)
     with pytest.raises(ValueError):
         sv.cache_attention(a.pop("q"), a.pop("k_cache"), a.pop("v_cache"), a.pop("page_table"), a.pop("lengths"), out=[a.pop("out")], stream=0, **a)
+
+
+def test_binding_refuses_what_32_bits_do_not_hold():
+    many = dict(k_cache=fake((1, 16, 2, 64)), v_cache=fake((1, 16, 2, 64)))
+    many = {name: type(t)(t.t.expand(2**32 + 1, -1, -1, -1)) for name, t in many.items()}
+    table = fake((3, 1), torch.int32)
+    for change in (many, dict(page_table=type(table)(table.t.expand(-1, 2**32 + 1)))):
+        test_append_binding_refuses(change)
+        test_attention_binding_refuses(change)
+    for window in (2**31, 2**32 + 5, -1, 5 - 2**32):
+        test_attention_binding_refuses(dict(window=window))
