@@ -477,8 +477,8 @@ int status_of(cudaError_t e)
 }
 
 // 8-bit caches and pages below kSmallPage places vector by vector, others by tensor map (a copy costs its warp 40 to 90 cycles,
-// whatever its size: 128 requests with pages of 20 places 95 us against 101 by vectors, 64 requests of 6 rows with pages of 64
-// 352 against 396).
+// whatever its size: 128 requests with pages of 20 places 92 us against 101 by vectors, 64 requests of 6 rows with pages of 64
+// 345 against 396).
 constexpr int kSmallPage = 16;
 bool by_loads(const spec_verify_cache_attention_args &a) { return a.cache_dtype == SV_E4M3 || a.page_size < kSmallPage; }
 
