@@ -282,7 +282,7 @@ Kernel kernel_of(int dim, int rows)
 
 Kernel kernel_of(int cache_dtype, int dim, int rows, bool loads)
 {
-    if (cache_dtype == SV_E4M3) return kernel_of<SV_E4M3, true>(dim, rows);
+    if (cache_dtype == SV_E4M3) return loads ? kernel_of<SV_E4M3, true>(dim, rows) : kernel_of<SV_E4M3, false>(dim, rows);
     if (cache_dtype == SV_BF16) return loads ? kernel_of<SV_BF16, true>(dim, rows) : kernel_of<SV_BF16, false>(dim, rows);
     return loads ? kernel_of<SV_F16, true>(dim, rows) : kernel_of<SV_F16, false>(dim, rows);
 }
@@ -446,16 +446,17 @@ Cache cache_of(const View &v)
 // Rows of heads: [rows, heads, head_dim] of 16-bit elements.
 View rows_of(const void *at, int rows, int heads, int64_t row, int64_t head, int dim) { return View{at, {rows, heads, 1}, {row, head, 0}, dim, 2}; }
 
-// The tensor map of an array of heads, [size2][size1][size0][inner] of 16-bit elements, for copies of boxes of 64 elements
-// by `box` of the first dimension.
+// The tensor map of an array of heads, [size2][size1][size0][inner], for copies of boxes of 64 elements of 16 bits, or of whole
+// heads of 8, by `box` of the first dimension.
 int map_of(CUtensorMap &map, bool bf16, const View &v, int box)
 {
     const cuuint64_t sizes[4] = {static_cast<cuuint64_t>(v.inner), static_cast<cuuint64_t>(v.size[0]), static_cast<cuuint64_t>(v.size[1]), static_cast<cuuint64_t>(v.size[2])};
     cuuint64_t strides[3];
-    for (int d = 0; d < 3; ++d) strides[d] = static_cast<cuuint64_t>(v.size[d] > 1 ? v.stride[d] : v.inner) * 2;
-    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
-    return g_encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(v.at), sizes, strides, boxes, steps,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    for (int d = 0; d < 3; ++d) strides[d] = static_cast<cuuint64_t>(v.size[d] > 1 ? v.stride[d] : v.inner) * v.elem;
+    const bool bytes = v.elem == 1;
+    const cuuint32_t boxes[4] = {bytes ? static_cast<cuuint32_t>(v.inner) : 64, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+    return g_encode(&map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(v.at), sizes, strides, boxes, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SV_OK
                : SV_ECUDA;
@@ -480,7 +481,12 @@ int status_of(cudaError_t e)
 // whatever its size: 128 requests with pages of 20 places 92 us against 101 by vectors, 64 requests of 6 rows with pages of 64
 // 345 against 396).
 constexpr int kSmallPage = 16;
-bool by_loads(const spec_verify_cache_attention_args &a) { return a.cache_dtype == SV_E4M3 || a.page_size < kSmallPage; }
+bool by_loads(const spec_verify_cache_attention_args &a)
+{
+    if (a.page_size < kSmallPage) return true;
+    if (a.cache_dtype != SV_E4M3 || a.page_size > kTile) return false;
+    return a.page_size * a.head_dim % 128 != 0 || kTile / a.page_size * a.page_size * 4 < kTile * 3;
+}
 
 // The kernel for a call. Query rows of a key head of one request (on average: the rows of each are known on the device
 // only) in tiles of 16: as few tiles over the keys as there can be, of as few rows.
@@ -734,19 +740,19 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
 #endif
     TensorMaps maps;
     memset(&maps, 0, sizeof(maps));
+    const bool bf16 = a->cache_dtype == SV_BF16;
     if (a->cache_dtype != SV_E4M3) {
-        const bool bf16 = a->cache_dtype == SV_BF16;
         const View queries{a->q, {a->num_q_heads, a->num_rows, 1}, {a->q_head_stride, a->q_row_stride, 0}, a->head_dim, 2};
         if (map_of(maps.q, bf16, queries, P.cut.q_box) != SV_OK) return SV_ECUDA;
-        if (P.cut.box) {
-            // (sizes of the map: slots, heads, pages. Without a page only zeros come of it, whatever it names)
-            auto turned = [&](const View &c) {
-                View v{a->num_pages ? c.at : a->q, {c.size[1], c.size[2], c.size[0]}, {c.stride[1], c.stride[2], c.stride[0]}, c.inner, 2};
-                if (!a->num_pages) v.size[0] = v.size[1] = v.size[2] = 1;
-                return v;
-            };
-            if (map_of(maps.k, bf16, turned(kc), P.cut.box) != SV_OK || map_of(maps.v, bf16, turned(vc), P.cut.box) != SV_OK) return SV_ECUDA;
-        }
+    }
+    if (P.cut.box) {
+        // (sizes of the map: slots, heads, pages. Without a page only zeros come of it, whatever it names)
+        auto turned = [&](const View &c) {
+            View v{a->num_pages ? c.at : a->q, {c.size[1], c.size[2], c.size[0]}, {c.stride[1], c.stride[2], c.stride[0]}, c.inner, c.elem};
+            if (!a->num_pages) v.size[0] = v.size[1] = v.size[2] = 1;
+            return v;
+        };
+        if (map_of(maps.k, bf16, turned(kc), P.cut.box) != SV_OK || map_of(maps.v, bf16, turned(vc), P.cut.box) != SV_OK) return SV_ECUDA;
     }
     // Each kernel may start while the one before it ends; it waits for that on the device before it looks at memory.
     void *params[] = {&P, &maps};

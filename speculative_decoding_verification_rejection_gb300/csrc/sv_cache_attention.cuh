@@ -70,7 +70,7 @@ struct Tile {
     static constexpr int q_buffers = (D == 256 && N > 16) || N == 64 ? 1 : 2;
     static constexpr int heads = D == 256 && N > 16 ? 2 : 8;  // descriptions of tiles that are kept
     // 8-bit keys and values are copied to `staged` rooms of a tile before they are widened
-    static constexpr int staged = bytes_of == 2 ? 0 : D == 64 ? 4 : D == 128 ? 2 : 1, staging = staged * 2 * kTile * D;
+    static constexpr int staged = bytes_of == 2 ? 0 : D == 64 ? 4 : D == 128 ? 2 : 1, rooms = staged ? staged : 1, staging = staged * 2 * kTile * D;
     static constexpr int fit = ((heads == 8 ? 223400 : 229376) - q_buffers * q_bytes - 2 * weights - staging) / slot;
     static constexpr int slots = fit > 12 ? 12 : fit;
     static constexpr int k_slots = slots / 2, v_slots = slots - slots / 2;  // rings of their own: each is filled in turn
@@ -81,7 +81,7 @@ struct Tile {
     // Factors of the queries of `kept` segments: when those of a segment are written, the weights of all but the two tiles before
     // the last scores are done, and so those of the segment whose place they take.
     static constexpr int kept = q_buffers + 2;
-    static constexpr int loaders = !LOADS ? 1 : bytes_of == 1 ? 16 : 8;  // warps that copy vector by vector, half of them keys; or that of the values
+    static constexpr int loaders = bytes_of == 1 ? 16 : LOADS ? 8 : 1;  // warps that widen or copy vector by vector, half of them keys; or that of the values
     static constexpr int threads = 32 * (12 + loaders);
     static constexpr int mine = N / 2;                // rows of a weights warp
     static_assert(slots >= 2 && columns_used <= 256, "room");
@@ -94,7 +94,7 @@ struct Tile {
     };
     struct Shared {
         u64 k_full[k_slots], k_empty[k_slots], v_full[v_slots], v_empty[v_slots], scores[2], weighed[2], done[2], q_full[2], q_empty[2], told[heads],
-            used[heads];
+            used[heads], raw_full[2][rooms], raw_empty[2][rooms];  // (of 8-bit keys and values before they are widened)
         Head head[heads];
         alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
         alignas(16) float factor[N];  // what a new reference makes of the old sums; of the result
@@ -413,8 +413,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
     const uint32_t room_at = shared_address(room), q_at = shared_address(q_room), w_at = shared_address(w_room);
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid & 31;
     const int cta = blockIdx.x;
-    constexpr bool loads = LOADS;
-    static_assert(LOADS || !kWide, "8 bits are widened by the loading warps");
+    constexpr bool loads = LOADS, many = loads || kWide;
 
     // -- barriers and memory, while the work before this call ends
     if (warp == 8) {
@@ -422,12 +421,14 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        const int filled = loads ? S::loaders / 2 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
+        const int filled = many ? S::loaders / 2 : 1;  // arrivals at a slot: of the loading warps, or of the thread that names the bytes
 #pragma unroll 1
         for (int k = 0; k < S::v_slots; ++k) {
             if (k < S::k_slots) barrier_init(sh.k_full + k, filled), barrier_init(sh.k_empty + k, 1);
             barrier_init(sh.v_full + k, filled), barrier_init(sh.v_empty + k, 1);
         }
+#pragma unroll 1
+        for (int k = 0; k < 2 * S::staged; ++k) barrier_init(&sh.raw_full[0][0] + k, 1), barrier_init(&sh.raw_empty[0][0] + k, S::loaders / 2);
 #pragma unroll 1
         for (int k = 0; k < S::heads; ++k) barrier_init(sh.told + k, 1), barrier_init(sh.used + k, 2);  // (used: by the second product, and by the warp of the queries)
 #pragma unroll 1
@@ -442,10 +443,12 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
         if (!kWide) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q) : "memory");
     }
     if constexpr (!loads) {  // places of a slot that no copy writes: zeros for good
-        const int filled = P.cut.boxes * P.cut.box, piece = (kTile - filled) * 8;
+        // (8 bits: of the rooms that they are copied to before they are widened)
+        constexpr int kPieces = kWide ? 2 * S::staged : S::slots * S::halves, kPiece = kWide ? kTile * D : S::piece, kKey = kWide ? D : 128;
+        const int filled = P.cut.boxes * P.cut.box, piece = (kTile - filled) * (kKey / 16);
 #pragma unroll 1
-        for (int x = tid; x < S::slots * S::halves * piece; x += S::threads)
-            *reinterpret_cast<uint4 *>(room + x / piece * S::piece + filled * 128 + x % piece * 16) = make_uint4(0, 0, 0, 0);
+        for (int x = tid; x < kPieces * piece; x += S::threads)
+            *reinterpret_cast<uint4 *>((kWide ? staging : room) + x / piece * kPiece + filled * kKey + x % piece * 16) = make_uint4(0, 0, 0, 0);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
     int *const lost = &sh.lost;
 
     if (warp < 8) {
-        if constexpr (loads) SV_CACHE_REGISTERS("inc", 104);
+        if constexpr (many) SV_CACHE_REGISTERS("inc", 104);
         // -- weights: this thread has key `key0` of every tile, the elements key0 and key0 + 128 of the outputs, and rows r0 to r0 + M - 1
         constexpr int M = S::mine;
         const int key0 = tid & 127, r0 = warp / 4 * M;
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             tensor_before();
         }
     } else if (warp < 12) {
-        if constexpr (loads) SV_CACHE_REGISTERS("dec", 56);
+        if constexpr (many) SV_CACHE_REGISTERS("dec", 56);
         if (warp == 8) {
             // -- scores^T = K Q^T
             const uint32_t leader = elected();
@@ -878,7 +881,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
                 const auto &h = sh.head[it % S::heads];
                 const int flags = h.flags, head = h.head;
-                if constexpr (!loads) {
+                if constexpr (!many) {
                     boxes_to<S>(&maps.k, sh.k_full + s, sh.k_empty + s, it >= S::k_slots, turn ^ 1, room_at + s * S::slot, P.cut, h.slot, head, h.page, lane, lost);
                     if (++s == S::k_slots) s = 0, turn ^= 1;
                 }
@@ -952,8 +955,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             }
         }
     } else {
-        if constexpr (loads) SV_CACHE_REGISTERS("dec", 56);
-        if constexpr (!loads) {
+        if constexpr (many) SV_CACHE_REGISTERS("dec", 56);
+        if constexpr (!many) {
             if (warp == 12) {
                 // -- values by boxes
                 int s = 0;
@@ -968,7 +971,9 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             }
         } else {
             // -- keys (half of the warps) and values vector by vector: copied to their slot, or to a room of the thread's
-            // own and widened from there. A tile is given on when kLag more have been asked for.
+            // own and widened from there. A tile is given on when kLag more have been asked for. 8 bits in pages that boxes can
+            // bring: the first warp of each half has them copied by tensor map, and every thread widens its vectors of the tile.
+            constexpr bool kRaw = kWide && !loads;
             constexpr int kSide = 16 * S::loaders;  // threads
             const bool values = warp >= 12 + S::loaders / 2;
             constexpr int kRow = D * S::bytes_of / 16, kEvery = kSide / kRow, kEach = kTile / kEvery;  // vectors of a key; keys at once; a thread's vectors
@@ -980,12 +985,22 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             u64 *const fulls = values ? sh.v_full : sh.k_full, *const empties = values ? sh.v_empty : sh.k_empty;
             unsigned char *const ring = room + (values ? S::k_slots * S::slot : 0);
             auto place_of = [&](unsigned char *slot, int chunk, int key) { return slot + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4); };
-            auto own = [&](int it, int k) { return staging + ((((it % (S::staged ? S::staged : 1)) * 2 + values) * kEach + k) * kSide + x) * 16; };
+            auto own = [&](int it, int k) { return staging + (((it % S::rooms * 2 + values) * kEach + k) * kSide + x) * 16; };
             int asked = 0, given = 0;  // slots
             uint32_t asked_turn = 0, given_turn = 0;
 #pragma unroll 1
             for (int it = 0; it < n + kLag; ++it) {
-                if (it < n) {
+                if (kRaw && it < n && warp == (values ? 12 + S::loaders / 2 : 12)) {
+                    const int r = it % S::rooms;
+                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                    if (it >= S::rooms) barrier_wait(&sh.raw_empty[values][r], (it / S::rooms - 1) & 1, lost);
+                    const auto &h = sh.head[it % S::heads];
+                    if (lane == 0) barrier_expect(&sh.raw_full[values][r], P.cut.boxes * P.cut.box * D);
+                    __syncwarp();
+                    if (lane < P.cut.boxes)  // (at most 8)
+                        copy_box(shared_address(staging + (r * 2 + values) * (kTile * D) + lane * P.cut.box * D), values ? &maps.v : &maps.k, &sh.raw_full[values][r], 0, h.slot, h.head, h.page[lane]);
+                }
+                if (!kRaw && it < n) {
                     barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
                     if (!kWide && it >= slots) barrier_wait(empties + asked, asked_turn ^ 1, lost);
                     const auto &h = sh.head[it % S::heads];
@@ -1008,9 +1023,11 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     }
                     if (++asked == slots) asked = 0, asked_turn ^= 1;
                 }
-                copies_close();
+                if (!kRaw) copies_close();
                 if (it < kLag) continue;
-                copies_wait<kLag>();
+                if (!kRaw) copies_wait<kLag>();
+                const int raw = kRaw ? (it - kLag) % S::rooms : 0;
+                if (kRaw) barrier_wait(&sh.raw_full[values][raw], (it - kLag) / S::rooms & 1, lost);
                 if constexpr (kWide) {
                     if (it - kLag >= slots) barrier_wait(empties + given, given_turn ^ 1, lost);
                     // (of the lanes of a key those of the upper half write their second vector first: eight lanes, eight banks)
@@ -1020,7 +1037,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     for (int k0 = 0; k0 < kEach; k0 += kPart) {
                         uint4 v[kPart];
 #pragma unroll
-                        for (int k = 0; k < kPart; ++k) v[k] = *reinterpret_cast<const uint4 *>(own(it - kLag, k0 + k));
+                        for (int k = 0; k < kPart; ++k) v[k] = *reinterpret_cast<const uint4 *>(kRaw ? staging + ((raw * 2 + values) * kTile + key0 + (k0 + k) * kEvery) * D + c * 16 : own(it - kLag, k0 + k));
 #pragma unroll
                         for (int k = 0; k < kPart; ++k) {
                             const uint4 lo = make_uint4(half2_of_e4m3(v[k].x), half2_of_e4m3(v[k].x >> 16), half2_of_e4m3(v[k].y), half2_of_e4m3(v[k].y >> 16));
@@ -1033,12 +1050,18 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 }
                 shared_to_async();
                 __syncwarp();
+                if (kRaw && lane == 0) barrier_arrive(&sh.raw_empty[values][raw]);
                 if (lane == 0) barrier_arrive(fulls + given);
                 if (++given == slots) given = 0, given_turn ^= 1;
             }
         }
     }
-    if (*reinterpret_cast<volatile int *>(lost) && !loads && (warp == 11 || warp == 12)) {  // copies in flight end before the block does
+    if (kWide && !loads && *reinterpret_cast<volatile int *>(lost) && (warp == 12 || warp == 12 + S::loaders / 2)) {
+        for (int it = max(0, n - S::rooms); it < n; ++it)
+            for (int k = 0; k < kPatience && !barrier_try(&sh.raw_full[warp != 12][it % S::rooms], it / S::rooms & 1); ++k) {
+            }
+    }
+    if (!many && *reinterpret_cast<volatile int *>(lost) && (warp == 11 || warp == 12)) {  // copies in flight end before the block does
         const int slots = warp == 12 ? S::v_slots : S::k_slots;
         for (int it = max(0, n - slots); it < n; ++it)
             for (int k = 0; k < kPatience && !barrier_try((warp == 12 ? sh.v_full : sh.k_full) + it % slots, it / slots & 1); ++k) {
