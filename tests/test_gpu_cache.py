@@ -127,6 +127,13 @@ def test_attention_pages_and_layouts(page, layout, dtype, cache):
     check_attention(Step(page, LENGTHS, NEW, hq=8, hk=2, dim=128, dtype=dtype, cache=cache, page=page, layout=layout, spare=3))
 
 
+@pytest.mark.parametrize("page", (15, 17, 18, 42, 72, 96, 100, 128, 129, 200))
+@pytest.mark.parametrize("dim", (64, 128, 256))
+def test_attention_8_bits_of_odd_pages(page, dim):
+    """Pages that tensor maps bring to shared memory, and pages too small, beside 128 bytes, or a bad fit for a tile."""
+    check_attention(Step(page + dim, LENGTHS, NEW, hq=6, hk=2, dim=dim, cache="e4m3", page=page, layout="heads", spare=1))
+
+
 @pytest.mark.parametrize("window", (1, 2, 5, 16, 64, 100, 300, 10**9))
 @pytest.mark.parametrize("dim,cache", ((64, "bf16"), (128, "e4m3")))
 def test_attention_window(window, dim, cache):
@@ -155,12 +162,12 @@ def test_attention_many_requests(n):
 
 
 @pytest.mark.parametrize("dim,hq,hk", ((256, 8, 1), (256, 16, 1), (128, 8, 1), (128, 12, 1), (128, 16, 1), (64, 24, 1)))
-@pytest.mark.parametrize("cache", ("bf16", "e4m3"))
-def test_attention_long_runs_of_tiles(dim, hq, hk, cache):
+@pytest.mark.parametrize("cache,page", (("bf16", 32), ("e4m3", 32), ("bf16", 8), ("e4m3", 8)))
+def test_attention_long_runs_of_tiles(dim, hq, hk, cache, page):
     """Hundreds of tiles of many requests for every CTA: rings of copies that go round many times."""
     import speculative_decoding_verification_rejection_gb300 as sv
 
-    n, page, width = 96, 32, 100
+    n, width = 96, 3200 // page
     g = torch.Generator(device="cuda").manual_seed(dim + hq)
     pages = torch.randn(300, page, hk, dim, generator=g, device="cuda")
     k, v = pages.to(TYPES[cache]), pages.flip(0).to(TYPES[cache])
