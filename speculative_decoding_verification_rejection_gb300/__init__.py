@@ -827,7 +827,10 @@ def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_fre
     if axes is not None:
         if len(axes) != half:
             raise ValueError(f"axes must name the axis of each of the {half} pairs")
-        axis_bytes = bytes(axes)
+        try:
+            axis_bytes = bytes(list(axes))  # (its numbers: bytes of an array are the array's memory)
+        except TypeError as e:
+            raise ValueError("axes must be whole numbers") from e
     args = CacheAppendArgs(qp[0], k_at, v_at, op[0], k_cache.data_ptr(), v_cache.data_ptr(), qp[1], qp[2], k_row, k_head,
                            v_row, v_head, op[1], op[2], *strides, *step, pos, rows, inv, *scales, axis_bytes, rows, n, hq,
                            hk, dim, 2 * half, 1 if interleaved else 0, num_axes, *pool, code, cache_code, index)

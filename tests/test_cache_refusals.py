@@ -1,6 +1,8 @@
 """Refusals of the cache operators: host-visible mistakes give a status and need no device."""
+import array
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -158,3 +160,34 @@ def test_binding_refuses_what_32_bits_do_not_hold():
         test_attention_binding_refuses(change)
     for window in (2**31, 2**32 + 5, -1, 5 - 2**32):
         test_attention_binding_refuses(dict(window=window))
+
+
+def axes_sent(axes, monkeypatch):
+    """The axes that a call with these axes hands to the library (which is not called)."""
+    got = []
+
+    def call(ref, stream):
+        args = ref._obj
+        got.append(list(ctypes.string_at(ctypes.c_void_p.from_buffer(args, sv.CacheAppendArgs.axes.offset).value, args.rotary_dim // 2)))
+        return sv.SV_OK
+
+    monkeypatch.setattr(sv._cache_torch(), "append", call)
+    a = dict(good(), positions=fake((3, 9), torch.int32), axes=axes)
+    sv.cache_append(a.pop("k"), a.pop("v"), a.pop("k_cache"), a.pop("v_cache"), a.pop("page_table"), a.pop("lengths"), stream=0, **a)
+    return got[0]
+
+
+@pytest.mark.parametrize("kind", ("list", "tuple", "bytes", "array.array", "int8", "int32", "int64", "uint64", "strided", "tensor32", "tensor64"))
+def test_axes_are_numbers_whatever_holds_them(kind, monkeypatch):
+    want = [m % 3 for m in range(32)] if kind == "strided" else [0] * 8 + [1] * 12 + [2] * 12
+    held = {"list": list, "tuple": tuple, "bytes": bytes, "array.array": lambda a: array.array("l", a),
+            "strided": lambda a: np.array(a + a, dtype=np.int32).reshape(2, 32).T.copy()[:, 0],
+            "tensor32": lambda a: torch.tensor(a, dtype=torch.int32), "tensor64": torch.tensor}
+    make = held.get(kind) or (lambda a: np.array(a, dtype=kind))
+    assert axes_sent(make(want), monkeypatch) == want
+
+
+@pytest.mark.parametrize("axes", (np.full(32, 0.5), np.zeros((32, 2), dtype=np.int64), torch.zeros(32), ["0"] * 32, "0" * 32, np.full(32, -1), np.full(32, 256)))
+def test_axes_that_are_no_axis_numbers_are_refused(axes, monkeypatch):
+    with pytest.raises(ValueError):
+        axes_sent(axes, monkeypatch)
