@@ -4071,7 +4071,7 @@ const char *spec_verify_status_string(int status)
     case SV_OK: return "ok";
     case SV_EINVAL: return "invalid argument";
     case SV_ECAPACITY: return "size above the context capacity";
-    case SV_EDTYPE: return "unsupported element type";
+    case SV_EDTYPE: return "unsupported logits dtype";
     case SV_ECUDA: return "CUDA runtime error";
     case SV_EDEVICE: return "no usable sm_103 device";
     default: return "unknown status";

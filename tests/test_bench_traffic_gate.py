@@ -28,3 +28,11 @@ def test_traffic_follows_the_source_hash(tmp_path, monkeypatch):
     src.write_bytes(b"__global__ void k() { }\n")          # the kernel changed since the capture
     assert bench.recorded_traffic("summary.md")[0] is None
     assert bench.recorded_traffic("absent.md")[0] is None
+
+
+def test_committed_captures_are_of_the_present_source():
+    """A change of the kernel's file goes with new captures, or the benchmark has no traffic to report."""
+    bench = _bench()
+    for summary in ("stats_kernel_workload3.md", "stats_kernel_workload3_draft_logits.md"):
+        traffic, source = bench.recorded_traffic(summary)
+        assert traffic is not None, f"{summary}: {source}"
