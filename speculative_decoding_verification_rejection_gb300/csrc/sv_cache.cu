@@ -738,6 +738,9 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     s.add(a->workspace, true, true, a->workspace_bytes);
     add_step(s, *a);
     if (s.push(stream) != SV_OK) return SV_ECUDA;
+    // SV_DEBUG_PATIENCE: looks of a wait before it is given up
+    P.patience = kPatience;
+    if (const char *e = getenv("SV_DEBUG_PATIENCE")) P.patience = std::max(1, std::min(kPatience, atoi(e)));
 #endif
     TensorMaps maps;
     memset(&maps, 0, sizeof(maps));

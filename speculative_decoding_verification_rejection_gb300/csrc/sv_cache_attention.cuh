@@ -40,6 +40,9 @@ struct AttentionParams {
     bool bf16;            // type of the rows
     Cut cut;
     Divider by_group, by_span, by_parts;
+#ifdef SV_DEBUG_BOUNDS
+    int patience;
+#endif
     float *sums;          // workspace: [ctas][2][rows of a tile][dim], then [ctas][2][rows of a tile][2], then Part [ctas]
     float2 *stats;
     Part *parts;
@@ -47,6 +50,14 @@ struct AttentionParams {
 
 struct TensorMaps {
     CUtensorMap q, k, v;
+};
+
+// Whether the CTA's work has been given up.
+struct Given {
+    int up;        // some wait of the CTA ran out
+#ifdef SV_DEBUG_BOUNDS
+    int patience;  // (the checked build's tests let waits run out)
+#endif
 };
 
 enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge = 32 };
@@ -95,21 +106,22 @@ struct Tile {
     struct Shared {
         u64 k_full[k_slots], k_empty[k_slots], v_full[v_slots], v_empty[v_slots], scores[2], weighed[2], done[2], q_full[2], q_empty[2], told[heads],
             used[heads], raw_full[2][rooms], raw_empty[2][rooms];  // (of 8-bit keys and values before they are widened)
+        u64 ended;  // (of a call that is given up) all products
         Head head[heads];
         alignas(16) float less[N];    // minus the reference of each row's weights (plus the offset)
         alignas(16) float factor[N];  // what a new reference makes of the old sums; of the result
         alignas(16) float scale[bytes_of == 1 ? N : 4];  // of the scores
         union {
             alignas(16) float most[4][N];  // by warps: largest scores, sums of weights
-            struct {
-                uint32_t scan[32], start[2];  // before the first tile
-            };
+            uint32_t scan[32];  // before the first tile
         };
+        uint32_t start[2], total;  // the first tile's request and its number there; tiles of the step
         float top[N];                 // the reference, times log2 e
         i64 row_at[N];                // where a row's result goes, in bytes from its array's start; -1: nowhere
         float q_scale[kept][bytes_of == 1 ? N : 1];  // of queries held in binary16
         uint32_t tensor_at;
-        int lost;
+        Given given;
+        int asked[3];  // tiles of keys, tiles of values, segments of queries asked for by tensor map
     };
     static constexpr int bytes = slots * slot + staging + q_buffers * q_bytes + 2 * weights + static_cast<int>(sizeof(Shared));
     static_assert(bytes <= 232448, "shared memory");
@@ -256,8 +268,11 @@ __device__ __forceinline__ void barrier_expect(u64 *b, int bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(shared_address(b)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void barrier_arrive(u64 *b) { asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(shared_address(b)) : "memory"); }
-// Waits for a phase to end, not for ever: after kPatience looks (seconds) the call is given up (`lost`), every later
-// wait returns at once, and the rows get NaN. Whoever waits has seen the phase before end, so that a parity names one phase.
+// Waits for a phase to end, not for ever: false if after kPatience looks (seconds) it has not, or some other wait of the CTA ran
+// out before. All lanes of a warp get the same answer. Who gets false leaves its work where it is: it arrives
+// at no barrier and writes no description any more, so every phase that does end stands for what it says, and the others come to the
+// end of their work or to a wait that gives up as well. (The weights' warps, which meet, leave together; see there.) Whoever waits has seen
+// the phase before end, so that a parity names one phase.
 constexpr int kPatience = 1 << 22;
 __device__ __forceinline__ bool barrier_try(u64 *b, uint32_t parity)
 {
@@ -265,14 +280,45 @@ __device__ __forceinline__ bool barrier_try(u64 *b, uint32_t parity)
     asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(shared_address(b)), "r"(parity) : "memory");
     return done != 0;
 }
-__device__ __forceinline__ void barrier_wait(u64 *b, uint32_t parity, int *lost)
+#ifndef SV_DEBUG_BOUNDS
+__device__ __forceinline__ bool barrier_wait(u64 *b, uint32_t parity, Given *given)
 {
+    uint32_t there;
     asm volatile(
-        "{\n.reg .pred p;\n.reg .b32 k, l;\nmov.b32 k, %3;\n$AGAIN_%=: mbarrier.try_wait.parity.shared.b64 p, [%0], %1;\n@p bra $DONE_%=;\n"
-        "ld.volatile.shared.b32 l, [%2];\nsetp.ne.b32 p, l, 0;\n@p bra $DONE_%=;\nsub.u32 k, k, 1;\nsetp.ne.b32 p, k, 0;\n@p bra $AGAIN_%=;\n"
-        "mov.b32 l, 1;\nst.volatile.shared.b32 [%2], l;\n$DONE_%=:\n}" ::"r"(shared_address(b)),
-        "r"(parity), "r"(shared_address(lost)), "n"(kPatience)
+        "{\n.reg .pred p;\n.reg .b32 k, l;\nmov.b32 k, %4;\nmov.b32 %0, 1;\n"
+        "$AGAIN_%=: mbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nvote.sync.all.pred p, p, 0xffffffff;\n@p bra $DONE_%=;\n"
+        "ld.volatile.shared.b32 l, [%3];\nsetp.ne.b32 p, l, 0;\nvote.sync.any.pred p, p, 0xffffffff;\n@p bra $LEAVE_%=;\n"
+        "sub.u32 k, k, 1;\nsetp.ne.b32 p, k, 0;\n@p bra $AGAIN_%=;\n"
+        "mov.b32 l, 1;\nst.volatile.shared.b32 [%3], l;\n$LEAVE_%=: mov.b32 %0, 0;\n$DONE_%=:\n}"
+        : "=r"(there)
+        : "r"(shared_address(b)), "r"(parity), "r"(shared_address(&given->up)), "n"(kPatience)
         : "memory");
+    return there != 0;
+}
+#else
+// The same with looks that do not last, as many as the call says.
+__device__ __forceinline__ bool barrier_wait(u64 *b, uint32_t parity, Given *given)
+{
+    volatile Given *const g = given;
+    for (int k = g->patience;;) {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(shared_address(b)), "r"(parity) : "memory");
+        if (__all_sync(~0u, done)) return true;
+        if (__any_sync(~0u, g->up)) return false;
+        if (--k <= 0) break;
+    }
+    g->up = 1;
+    return false;
+}
+#endif
+// The last `slots` phases, at most, of `count` that a ring's barriers were asked for: waits for them on the way out (again not for ever).
+__device__ __forceinline__ void barrier_drain(u64 *b, int slots, int count)
+{
+#pragma unroll 1
+    for (int it = max(0, count - slots); it < count; ++it)
+#pragma unroll 1
+        for (int k = 0; k < kPatience && !barrier_try(b + it % slots, it / slots & 1); ++k) {
+        }
 }
 // A box of an array of heads, [1][1][box][64 elements], to shared memory (swizzled by 128 bytes).
 __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap *map, u64 *b, int element, int x, int y, int z)
@@ -350,12 +396,20 @@ __device__ __forceinline__ bool weights_any(bool x)
     return any != 0;
 }
 
-// The boxes of a tile's keys or values, by a warp, once the slot is free.
-template <typename S>
-__device__ __forceinline__ void boxes_to(const CUtensorMap *map, u64 *full, u64 *empty, bool wait, uint32_t parity, uint32_t to, const Cut &cut, int slot, int head,
-                                         const int *page, int lane, int *lost)
+// They meet, and know whether one of them has given up (behind the one above, which such a warp makes true).
+__device__ __forceinline__ bool weights_gone(bool x)
 {
-    if (wait) barrier_wait(empty, parity, lost);
+    int any;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, 1, 256, p;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(any) : "r"(static_cast<int>(x)) : "memory");
+    return any != 0;
+}
+
+// The boxes of a tile's keys or values, by a warp, once the slot is free; false if that is given up.
+template <typename S>
+__device__ __forceinline__ bool boxes_to(const CUtensorMap *map, u64 *full, u64 *empty, bool wait, uint32_t parity, uint32_t to, const Cut &cut, int slot, int head,
+                                         const int *page, int lane, Given *given)
+{
+    if (wait && !barrier_wait(empty, parity, given)) return false;
     if (lane == 0) barrier_expect(full, cut.boxes * cut.box * 128 * S::halves);
     __syncwarp();
 #pragma unroll 1
@@ -363,6 +417,7 @@ __device__ __forceinline__ void boxes_to(const CUtensorMap *map, u64 *full, u64 
         const int b = k / S::halves, e = k % S::halves;
         copy_box(to + e * S::piece + b * cut.box * 128, map, full, e * 64, slot, head, page[b]);
     }
+    return true;
 }
 template <typename E, typename T>
 __device__ __forceinline__ E from_bits(T v)
@@ -399,6 +454,44 @@ __device__ __forceinline__ float columns_joined(float *v, int lane)
 #define SV_CACHE_REGISTERS(way, count) asm volatile("setmaxnreg." way ".sync.aligned.u32 " #count ";")
 #endif
 
+// NaN for the rows of a CTA that gave up, or for their parts (told as those of a CTA that did not), by its first 256 threads.
+template <int N, int D, typename E>
+__device__ __forceinline__ void rows_lost(const AttentionParams &P, const uint32_t *start, uint32_t total)
+{
+    const uint32_t ctas = min(total, gridDim.x), cta = blockIdx.x, u0 = share_of(total, cta, ctas), u1 = share_of(total, cta + 1, ctas);
+    const int n = static_cast<int>(u1 - u0);  // (some: who has no tile waits for nothing)
+    Walk<N> walk(P);
+    const float nan = __int_as_float(0x7fffffff);
+    walk.seek(static_cast<int>(start[0]), start[1], u0);
+    int here = 0;  // tiles of the group
+#pragma unroll 1
+    for (int it = 0; it < n; it += here) {
+        here = min(walk.t1 - walk.t, n - it);
+        const bool open = here < walk.t1 - walk.t, partial = walk.base < u0 || walk.base + walk.tiles() > u1;
+        const i64 part = (static_cast<i64>(cta) * 2 + (walk.base > u0 ? 1 : 0)) * N;
+#pragma unroll 1
+        for (int x = threadIdx.x; x < walk.count * D; x += 256) {
+            const int r = x / D, e = x % D, at_row = walk.from + r, j = P.by_group(at_row), qh = walk.head * P.group + at_row - j * P.group;
+            const i64 row = static_cast<i64>(walk.first) + j;
+            if (partial) {
+                st(P.sums + (part + r) * D + e, nan);
+                if (e == 0) st(P.stats + part + r, make_float2(nan, nan));
+            } else {
+                st(reinterpret_cast<E *>(P.out + row * P.out_row + qh * P.out_head) + e, from_bits<E>(static_cast<uint16_t>(0x7fff)));  // (a NaN in either type)
+                if (e == 0 && P.lse) st(P.lse + row * P.hq + qh, nan);
+            }
+        }
+        if (P.parts && threadIdx.x == 0 && it + here == n) {
+            const uint32_t k = sharer_of(total, walk.base, ctas);
+            st(reinterpret_cast<int4 *>(P.parts + cta),
+               make_int4(open ? static_cast<int>(k) : -1, sharer_of(total, walk.base + walk.tiles() - 1, ctas), share_of(total, k, ctas) < walk.base, walk.first));
+            st(reinterpret_cast<int4 *>(P.parts + cta) + 1, make_int4(walk.from, walk.count, walk.head, 0));
+        }
+        walk.t = walk.t1 - 1;
+        walk.next();
+    }
+}
+
 // (LOADS: keys vector by vector, not by tensor map. Kernels of their own, since the size of the code counts.)
 template <int KIND, int D, int N, bool LOADS>
 __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cache_attention_kernel(const AttentionParams P, const __grid_constant__ TensorMaps maps)
@@ -434,7 +527,11 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
 #pragma unroll 1
         for (int k = 0; k < 2; ++k)
             barrier_init(sh.scores + k, 2), barrier_init(sh.weighed + k, 256), barrier_init(sh.done + k, 1), barrier_init(sh.q_full + k, 1), barrier_init(sh.q_empty + k, 1);
-        sh.lost = 0;
+        barrier_init(&sh.ended, 2);
+        sh.given.up = 0;
+#ifdef SV_DEBUG_BOUNDS
+        sh.given.patience = P.patience;
+#endif
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 12 * 32 && !loads) {
@@ -476,6 +573,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
     const uint32_t warps = running(lane < S::threads / 32 ? sh.scan[lane] : 0u), all = __shfl_sync(~0u, warps, 31);
     // (2^31 tiles or more come only of requests that overlap, by prefix sums that are none: such a step is left out)
     const uint32_t total = all < 1u << 31 ? all : 0;
+    if (tid == 0) sh.total = total;
     before += (warp ? __shfl_sync(~0u, warps, (warp - 1) & 31) : 0u) - mine;
     const uint32_t tensor = __shfl_sync(~0u, sh.tensor_at, 0);
     const uint32_t ctas = min(total, gridDim.x);  // (each with a tile at least)
@@ -501,7 +599,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
         st(&P.parts[cta].first, -1);
     }
     __syncthreads();
-    int *const lost = &sh.lost;
+    Given *const given = &sh.given;
 
     if (warp < 8) {
         if constexpr (many) SV_CACHE_REGISTERS("inc", 104);
@@ -511,15 +609,22 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
         const uint32_t lanes = tensor + (static_cast<uint32_t>(warp & 3) << 21);  // (lane 32 * (warp % 4) of the tensor memory, in bits 16 and up)
         float sum[M];
         float scale = 0;
+        // A warp whose wait for scores is given up says so at the tile's first meeting, whatever the tile is: that is `weights_any`, and the
+        // meeting behind it where that is true, `weights_gone`, tells the others to leave with it. Whether a wait within a tile was given up does not
+        // matter: what the tile makes is overwritten at the kernel's end, and its weights are in their room all the same.
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
             const int b = it & 1;
             const uint32_t turn = it >> 1 & 1;
             auto &h = sh.head[it % S::heads];
-            barrier_wait(sh.scores + b, turn, lost);
+            if (__builtin_expect(!barrier_wait(sh.scores + b, turn, given), 0)) {
+                weights_any(true);
+                weights_gone(true);
+                break;
+            }
             tensor_after();
             const int flags = h.flags;
-            if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, lost);  // (the weights' room is free, and the values before the last have come)
+            if (it >= 2) barrier_wait(sh.done + b, turn ^ 1, given);  // (the weights' room is free, and the values before the last have come)
             int r_lo = 0, r_hi = key0 < P.cut.span ? M : 0;  // the rows, from r0 on, that see this thread's key
             const bool masks = flags & kEdge || (key0 | 31) >= P.cut.span;  // (the same in a warp)
             if (flags & kFirst) {
@@ -530,7 +635,10 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 if constexpr (kWide) {
                     const int segment = h.segment;
                     if (tid < N) sh.scale[tid] = scale * sh.q_scale[segment % S::kept][tid];
-                    weights_meet();
+                    if (__builtin_expect(weights_any(false), 0)) {
+                        weights_gone(false);
+                        break;
+                    }
                 }
             }
             if (__builtin_expect(flags & kEdge, 0)) {
@@ -542,8 +650,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 // A weight of 0 times a value that is not finite would be NaN. Such elements, if any, are set to 0 in shared
                 // memory, and what they make of the rows that see them is added by hand.
                 const int vslot = it % S::v_slots;
-                if (S::v_slots == 1 && it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
-                barrier_wait(sh.v_full + vslot, it / S::v_slots & 1, lost);
+                if (S::v_slots == 1 && it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, given);
+                barrier_wait(sh.v_full + vslot, it / S::v_slots & 1, given);
                 unsigned char *const v = room + (S::k_slots + vslot) * S::slot;
                 auto chunk = [&](int key, int c) { return reinterpret_cast<uint4 *>(v + c / 8 * S::piece + key * 128 + (((c & 7) ^ (key & 7)) << 4)); };
                 constexpr uint32_t mask = kBf16 ? 0x7f80u : 0x7c00u;
@@ -559,7 +667,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 }
                 if (__builtin_expect(weights_any(odd), 0)) {
                     // (rare: one row at a time, every element over all keys)
-                    if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
+                    if (it > 0) barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, given);
                     tensor_after();
 #pragma unroll 1
                     for (int e = 0; e < S::blocks; ++e)
@@ -583,7 +691,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                         }
                     tensor_stored();
                     tensor_before();
-                    weights_meet();
+                    if (weights_gone(false)) break;
 #pragma unroll 1
                     for (int c = warp / 4; c < D / 8; c += 2) {
                         uint32_t *x = reinterpret_cast<uint32_t *>(chunk(key0, c));
@@ -637,7 +745,11 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     const float most = columns_joined<false>(v, lane);
                     if (lane < 8) sh.most[warp & 3][r0 + c + lane] = most;
                 }
-                weights_meet();
+                const bool opens = !kWide && (flags & (kFirst | kEdge)) == kFirst;  // (the tile's first meeting)
+                if (opens ? weights_any(false) : weights_gone(false)) {
+                    if (opens) weights_gone(false);
+                    break;
+                }
                 if (tid < N) {
                     const float old = flags & kFirst ? -kInf : sh.top[tid];
                     const float top = larger(larger(larger(sh.most[0][tid], sh.most[1][tid]), larger(sh.most[2][tid], sh.most[3][tid])), old);
@@ -647,7 +759,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 }
                 weights_meet();
                 if (!(flags & kFirst)) {
-                    barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, lost);
+                    barrier_wait(sh.done + (b ^ 1), (it - 1) >> 1 & 1, given);
                     tensor_after();
 #pragma unroll 1
                     for (int e = 0; e < S::blocks; ++e)
@@ -701,11 +813,11 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             weights_meet();
             const bool partial = flags & kPartial;
             if (tid < N) {
-                const float top = sh.top[tid], sound = *reinterpret_cast<volatile int *>(lost) ? __int_as_float(0x7fffffff) : 1.0f;
-                const float z = top == -kInf ? 0.0f : ((sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid])) * sound;
+                const float top = sh.top[tid];
+                const float z = top == -kInf ? 0.0f : (sh.most[0][tid] + sh.most[1][tid]) + (sh.most[2][tid] + sh.most[3][tid]);
                 const int at_row = from + tid, j = P.by_group(at_row), qh = head * P.group + at_row - j * P.group;
                 const i64 part = (static_cast<i64>(cta) * 2 + (flags & kSlot ? 1 : 0)) * N + tid;
-                sh.factor[tid] = z == 0 ? 0.0f : partial ? sound : (P.v_scale ? ld(P.v_scale + head) : 1.0f) / z;
+                sh.factor[tid] = z == 0 ? 0.0f : partial ? 1.0f : (P.v_scale ? ld(P.v_scale + head) : 1.0f) / z;
                 sh.row_at[tid] = tid >= count ? -1 : partial ? part * (D * 4) : static_cast<i64>(first_row + j) * P.out_row + static_cast<i64>(qh) * P.out_head;
                 if (tid < count) {
                     if (partial)
@@ -719,7 +831,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 st(reinterpret_cast<int4 *>(P.parts + cta) + 1, make_int4(from, count, head, 0));
             }
             weights_meet();
-            barrier_wait(sh.done + b, turn, lost);
+            barrier_wait(sh.done + b, turn, given);
             tensor_after();
             if (D >= 128 || key0 < D) {
                 unsigned char *const array = partial ? reinterpret_cast<unsigned char *>(P.sums) : P.out;
@@ -753,12 +865,12 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
 #pragma unroll 1
             for (int it = 0; it < n; ++it) {
                 const int s = it % S::k_slots;
-                if (it >= 2) barrier_wait(sh.weighed + (it & 1), (it >> 1 & 1) ^ 1, lost);  // (its scores have been read)
-                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                if (it >= 2 && !barrier_wait(sh.weighed + (it & 1), (it >> 1 & 1) ^ 1, given)) break;  // (its scores have been read)
+                if (!barrier_wait(sh.told + it % S::heads, it / S::heads & 1, given)) break;
                 const auto &h = sh.head[it % S::heads];
                 const int flags = __shfl_sync(~0u, h.flags, 0), segment = __shfl_sync(~0u, h.segment, 0), qb = segment % S::q_buffers;
-                if (flags & kFirst) barrier_wait(sh.q_full + qb, segment / S::q_buffers & 1, lost);
-                barrier_wait(sh.k_full + s, it / S::k_slots & 1, lost);
+                if (flags & kFirst && !barrier_wait(sh.q_full + qb, segment / S::q_buffers & 1, given)) break;
+                if (!barrier_wait(sh.k_full + s, it / S::k_slots & 1, given)) break;
                 tensor_after();
                 const u64 a = matrix_at(room_at + s * S::slot, 16, 1024, 2), q = matrix_at(q_at + qb * S::q_bytes, 16, 1024, 2);
 #pragma unroll
@@ -777,8 +889,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
 #pragma unroll 1
             for (int it = 0; it < n; ++it) {
                 const int s = it % S::v_slots, b = it & 1;
-                barrier_wait(sh.v_full + s, it / S::v_slots & 1, lost);
-                barrier_wait(sh.weighed + b, it >> 1 & 1, lost);
+                if (!barrier_wait(sh.v_full + s, it / S::v_slots & 1, given)) break;
+                if (!barrier_wait(sh.weighed + b, it >> 1 & 1, given)) break;
                 tensor_after();
                 const auto &h = sh.head[it % S::heads];
                 const bool first = __shfl_sync(~0u, h.flags & kFirst && !h.started, 0);
@@ -821,7 +933,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     if (!loads && p != lo) in[w] = -1;  // (the box's first place speaks for it)
                 }
                 const int k = it % S::heads;
-                if (it >= S::heads) barrier_wait(sh.used + k, (it / S::heads - 1) & 1, lost);
+                if (it >= S::heads && !barrier_wait(sh.used + k, (it / S::heads - 1) & 1, given)) break;
                 auto &h = sh.head[k];
                 bool all = true;
 #pragma unroll
@@ -874,21 +986,23 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             }
         } else if (warp == 11) {
             // -- keys by boxes, and queries
-            int s = 0;
+            int s = 0, asked = 0, asked_q = 0;
             uint32_t turn = 0;  // times the ring has been gone round, as the parity waited for
 #pragma unroll 1
             for (int it = 0; it < n; ++it) {
-                barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                if (!barrier_wait(sh.told + it % S::heads, it / S::heads & 1, given)) break;
                 const auto &h = sh.head[it % S::heads];
                 const int flags = h.flags, head = h.head;
                 if constexpr (!many) {
-                    boxes_to<S>(&maps.k, sh.k_full + s, sh.k_empty + s, it >= S::k_slots, turn ^ 1, room_at + s * S::slot, P.cut, h.slot, head, h.page, lane, lost);
+                    if (!boxes_to<S>(&maps.k, sh.k_full + s, sh.k_empty + s, it >= S::k_slots, turn ^ 1, room_at + s * S::slot, P.cut, h.slot, head, h.page, lane, given)) break;
+                    ++asked;
                     if (++s == S::k_slots) s = 0, turn ^= 1;
                 }
                 if (flags & kFirst) {
                 const int segment = h.segment, qb = segment % S::q_buffers, from = h.from, count = h.count, first = h.first;
-                if (segment >= S::q_buffers) barrier_wait(sh.q_empty + qb, (segment / S::q_buffers - 1) & 1, lost);
+                if (segment >= S::q_buffers && !barrier_wait(sh.q_empty + qb, (segment / S::q_buffers - 1) & 1, given)) break;
                 if constexpr (!kWide) {
+                    ++asked_q;
                     if (lane == 0) barrier_expect(sh.q_full + qb, S::q_bytes);
                     __syncwarp();
                     const int box = P.cut.q_box;  // rows of one token side by side, so that no box has two tokens
@@ -953,21 +1067,27 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 __syncwarp();
                 if (lane == 0) barrier_arrive(sh.used + it % S::heads);
             }
+            if (lane == 0) {
+                if (!many) sh.asked[0] = asked;
+                sh.asked[2] = asked_q;
+            }
         }
     } else {
         if constexpr (many) SV_CACHE_REGISTERS("dec", 56);
         if constexpr (!many) {
             if (warp == 12) {
                 // -- values by boxes
-                int s = 0;
+                int s = 0, asked = 0;
                 uint32_t turn = 0;
 #pragma unroll 1
                 for (int it = 0; it < n; ++it) {
-                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
+                    if (!barrier_wait(sh.told + it % S::heads, it / S::heads & 1, given)) break;
                     const auto &h = sh.head[it % S::heads];
-                    boxes_to<S>(&maps.v, sh.v_full + s, sh.v_empty + s, it >= S::v_slots, turn ^ 1, room_at + (S::k_slots + s) * S::slot, P.cut, h.slot, h.head, h.page, lane, lost);
+                    if (!boxes_to<S>(&maps.v, sh.v_full + s, sh.v_empty + s, it >= S::v_slots, turn ^ 1, room_at + (S::k_slots + s) * S::slot, P.cut, h.slot, h.head, h.page, lane, given)) break;
+                    ++asked;
                     if (++s == S::v_slots) s = 0, turn ^= 1;
                 }
+                if (lane == 0) sh.asked[1] = asked;
             }
         } else {
             // -- keys (half of the warps) and values vector by vector: copied to their slot, or to a room of the thread's
@@ -986,14 +1106,15 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
             unsigned char *const ring = room + (values ? S::k_slots * S::slot : 0);
             auto place_of = [&](unsigned char *slot, int chunk, int key) { return slot + chunk / 8 * S::piece + key * 128 + (((chunk & 7) ^ (key & 7)) << 4); };
             auto own = [&](int it, int k) { return staging + (((it % S::rooms * 2 + values) * kEach + k) * kSide + x) * 16; };
-            int asked = 0, given = 0;  // slots
-            uint32_t asked_turn = 0, given_turn = 0;
+            int asked = 0, passed = 0, boxes = 0;  // slots; tiles asked for by tensor map
+            uint32_t asked_turn = 0, passed_turn = 0;
 #pragma unroll 1
             for (int it = 0; it < n + kLag; ++it) {
                 if (kRaw && it < n && warp == (values ? 12 + S::loaders / 2 : 12)) {
                     const int r = it % S::rooms;
-                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
-                    if (it >= S::rooms) barrier_wait(&sh.raw_empty[values][r], (it / S::rooms - 1) & 1, lost);
+                    if (!barrier_wait(sh.told + it % S::heads, it / S::heads & 1, given)) break;
+                    if (it >= S::rooms && !barrier_wait(&sh.raw_empty[values][r], (it / S::rooms - 1) & 1, given)) break;
+                    ++boxes;
                     const auto &h = sh.head[it % S::heads];
                     if (lane == 0) barrier_expect(&sh.raw_full[values][r], P.cut.boxes * P.cut.box * D);
                     __syncwarp();
@@ -1001,8 +1122,8 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                         copy_box(shared_address(staging + (r * 2 + values) * (kTile * D) + lane * P.cut.box * D), values ? &maps.v : &maps.k, &sh.raw_full[values][r], 0, h.slot, h.head, h.page[lane]);
                 }
                 if (!kRaw && it < n) {
-                    barrier_wait(sh.told + it % S::heads, it / S::heads & 1, lost);
-                    if (!kWide && it >= slots) barrier_wait(empties + asked, asked_turn ^ 1, lost);
+                    if (!barrier_wait(sh.told + it % S::heads, it / S::heads & 1, given)) break;
+                    if (!kWide && it >= slots && !barrier_wait(empties + asked, asked_turn ^ 1, given)) break;
                     const auto &h = sh.head[it % S::heads];
                     const uint4 *const at = reinterpret_cast<const uint4 *>(cache.at + static_cast<i64>(h.head) * cache.head) + c;
                     constexpr int kPart = kEach < 8 ? kEach : 8;
@@ -1027,9 +1148,9 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                 if (it < kLag) continue;
                 if (!kRaw) copies_wait<kLag>();
                 const int raw = kRaw ? (it - kLag) % S::rooms : 0;
-                if (kRaw) barrier_wait(&sh.raw_full[values][raw], (it - kLag) / S::rooms & 1, lost);
+                if (kRaw && !barrier_wait(&sh.raw_full[values][raw], (it - kLag) / S::rooms & 1, given)) break;
                 if constexpr (kWide) {
-                    if (it - kLag >= slots) barrier_wait(empties + given, given_turn ^ 1, lost);
+                    if (it - kLag >= slots && !barrier_wait(empties + passed, passed_turn ^ 1, given)) break;
                     // (of the lanes of a key those of the upper half write their second vector first: eight lanes, eight banks)
                     const bool second = kRow == 8 ? c >> 2 : kRow == 4 ? 0 : c >> 2 & 1;
                     constexpr int kPart = kEach < 4 ? kEach : 4;
@@ -1043,32 +1164,37 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                             const uint4 lo = make_uint4(half2_of_e4m3(v[k].x), half2_of_e4m3(v[k].x >> 16), half2_of_e4m3(v[k].y), half2_of_e4m3(v[k].y >> 16));
                             const uint4 hi = make_uint4(half2_of_e4m3(v[k].z), half2_of_e4m3(v[k].z >> 16), half2_of_e4m3(v[k].w), half2_of_e4m3(v[k].w >> 16));
                             const int key = key0 + (k0 + k) * kEvery;
-                            *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + second, key)) = second ? hi : lo;
-                            *reinterpret_cast<uint4 *>(place_of(ring + given * S::slot, 2 * c + !second, key)) = second ? lo : hi;
+                            *reinterpret_cast<uint4 *>(place_of(ring + passed * S::slot, 2 * c + second, key)) = second ? hi : lo;
+                            *reinterpret_cast<uint4 *>(place_of(ring + passed * S::slot, 2 * c + !second, key)) = second ? lo : hi;
                         }
                     }
                 }
                 shared_to_async();
                 __syncwarp();
                 if (kRaw && lane == 0) barrier_arrive(&sh.raw_empty[values][raw]);
-                if (lane == 0) barrier_arrive(fulls + given);
-                if (++given == slots) given = 0, given_turn ^= 1;
+                if (lane == 0) barrier_arrive(fulls + passed);
+                if (++passed == slots) passed = 0, passed_turn ^= 1;
             }
+            if (kRaw && lane == 0 && warp == (values ? 12 + S::loaders / 2 : 12)) sh.asked[values] = boxes;
         }
-    }
-    if (kWide && !loads && *reinterpret_cast<volatile int *>(lost) && (warp == 12 || warp == 12 + S::loaders / 2)) {
-        for (int it = max(0, n - S::rooms); it < n; ++it)
-            for (int k = 0; k < kPatience && !barrier_try(&sh.raw_full[warp != 12][it % S::rooms], it / S::rooms & 1); ++k) {
-            }
-    }
-    if (!many && *reinterpret_cast<volatile int *>(lost) && (warp == 11 || warp == 12)) {  // copies in flight end before the block does
-        const int slots = warp == 12 ? S::v_slots : S::k_slots;
-        for (int it = max(0, n - slots); it < n; ++it)
-            for (int k = 0; k < kPatience && !barrier_try((warp == 12 ? sh.v_full : sh.k_full) + it % slots, it / slots & 1); ++k) {
-            }
     }
     tensor_before();
     __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<volatile int *>(&given->up), 0)) {  // (all threads see the same: no one waits any more)
+        // -- given up: what is on the way ends before the block does, and the rows that it had get NaN
+        if (loads) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (warp == 8 || warp == 9) products_close(&sh.ended, elected());
+        if (tid == 0) {
+            if constexpr (!loads) {
+                barrier_drain(kWide ? &sh.raw_full[0][0] : sh.k_full, kWide ? S::rooms : S::k_slots, sh.asked[0]);
+                barrier_drain(kWide ? &sh.raw_full[1][0] : sh.v_full, kWide ? S::rooms : S::v_slots, sh.asked[1]);
+            }
+            if constexpr (!kWide) barrier_drain(sh.q_full, S::q_buffers, sh.asked[2]);
+            barrier_drain(&sh.ended, 1, 1);
+        }
+        if (warp < 8) rows_lost<N, D, E>(P, sh.start, sh.total);  // (these have registers for it)
+        __syncthreads();
+    }
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(S::columns) : "memory");
 }
 

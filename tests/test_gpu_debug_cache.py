@@ -23,3 +23,17 @@ def test_cache_operators_stay_inside_their_arrays():
     print(r.stdout[-3000:])
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-3000:]
     assert r.stdout.strip().splitlines()[-1] == "OK"
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_end_the_call():
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    sv.build(debug=True)
+    env = dict(os.environ, SPEC_VERIFY_DEBUG_BOUNDS="1")
+    env.pop("SV_DEBUG_PATIENCE", None)
+    r = subprocess.run([sys.executable, os.path.join(HERE, "debug_cache_waits.py")], env=env,
+                       capture_output=True, text=True, timeout=600)
+    print(r.stdout[-3000:])
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-3000:]
+    assert r.stdout.strip().splitlines()[-1] == "OK"
