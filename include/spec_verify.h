@@ -105,6 +105,8 @@ extern "C" {
 #define SV_ERR_SELECT 8u  /* the top-k / top-p threshold of some row was not found within the
                              selection's pass limit (not expected to happen): that row was
                              left without the constraint */
+#define SV_ERR_WAIT 16u   /* a wait of spec_verify_cache_attention for a copy or a product was given up
+                             after some seconds (not expected to happen): rows got NaN */
 
 typedef struct spec_verify_ctx spec_verify_ctx; /* opaque */
 
@@ -656,7 +658,9 @@ int spec_verify_cache_append(const spec_verify_cache_append_args *args, void *cu
  * out = sum exp(s_t) v_t / Z, lse = ln Z, Z = sum exp(s_t). Query head g reads key head
  * g / (num_q_heads / num_kv_heads). A row that sees no key (or only keys of score -inf) gets out 0 and
  * lse -inf. Keys and values that a row does not see do not reach it, whatever they hold; a value that is not finite
- * under a weight that rounds to 0 gives itself or NaN. Products of
+ * under a weight that rounds to 0 gives itself or NaN. Waits within a kernel (for copies and products) are bounded; should
+ * one run out, the call ends all the same, rows that it may have spoilt get out and lse NaN, and SV_ERR_WAIT is set in the word
+ * that spec_verify_cache_last_error reads. Products of
  * elements are exact, sums, maxima and Z binary32; weights are rounded to the products' 16-bit type
  * (binary16 for SV_E4M3 caches) relative to a reference near their row's largest. Results repeat bit for
  * bit for the same arguments; calls of other sizes may be split otherwise.
@@ -701,6 +705,13 @@ int spec_verify_cache_attention(const spec_verify_cache_attention_args *args, vo
 /* Bytes of workspace that spec_verify_cache_attention needs for these arguments (pointers are not looked
  * at); they follow from the sizes and types alone. Launches nothing. */
 int spec_verify_cache_attention_workspace(const spec_verify_cache_attention_args *args, int64_t *bytes);
+
+/*
+ * Read and clear the error word of the cache operators on the current device (SV_ERR_WAIT, of every
+ * call since the last read), into *err_word. Like spec_verify_last_error it waits for the device
+ * (synchronises it), so call it outside any stream capture. Allocates nothing.
+ */
+int spec_verify_cache_last_error(uint32_t *err_word);
 
 /* Release the context and its device memory. NULL is a no-op. */
 void spec_verify_free(spec_verify_ctx *ctx);

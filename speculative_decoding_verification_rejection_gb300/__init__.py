@@ -122,7 +122,7 @@ class CacheAttentionArgs(ctypes.Structure):
                                       "cache_dtype", "device"))]
 
 
-SV_ERR_BATCH, SV_ERR_COUNTS, SV_ERR_BOUNDS, SV_ERR_SELECT = 1, 2, 4, 8
+SV_ERR_BATCH, SV_ERR_COUNTS, SV_ERR_BOUNDS, SV_ERR_SELECT, SV_ERR_WAIT = 1, 2, 4, 8, 16
 KERNELS = ("stats", "verify", "select")  # profiling slots (select: top-k / top-p calls)
 
 _lib = None
@@ -239,6 +239,7 @@ def lib():
     L.spec_verify_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), vp]
     L.spec_verify_cache_attention_workspace.argtypes = [ctypes.POINTER(CacheAttentionArgs),
                                                         ctypes.POINTER(i64)]
+    L.spec_verify_cache_last_error.argtypes = [ctypes.POINTER(u32)]
     L.spec_verify_reserve_host_io.argtypes = [vp]
     L.spec_verify_last_error.argtypes = [vp, ctypes.POINTER(u32)]
     L.spec_verify_set_profiling.argtypes = [vp, i32]
@@ -255,6 +256,7 @@ def lib():
               "spec_verify_run_host", "spec_verify_run_noalloc", "spec_verify_noalloc_last_error",
               "spec_verify_sample", "spec_verify_logprobs", "spec_verify_cache_append",
               "spec_verify_cache_attention", "spec_verify_cache_attention_workspace",
+              "spec_verify_cache_last_error",
               "spec_verify_reserve_host_io", "spec_verify_last_error", "spec_verify_set_profiling",
               "spec_verify_get_profile", "spec_verify_set_chunks", "spec_verify_launches_per_run"):
         getattr(L, f).restype = i32
@@ -457,6 +459,14 @@ def spec_verify_cache_attention_workspace(args: CacheAttentionArgs) -> int:
     _check(lib().spec_verify_cache_attention_workspace(ctypes.byref(args), ctypes.byref(n)),
            "spec_verify_cache_attention_workspace")
     return n.value
+
+
+def spec_verify_cache_last_error() -> int:
+    """Read and clear the error word of the cache operators on the current device (waits for the
+    device): SV_ERR_WAIT where an attention gave up a wait and wrote NaN."""
+    w = ctypes.c_uint32()
+    _check(lib().spec_verify_cache_last_error(ctypes.byref(w)), "spec_verify_cache_last_error")
+    return w.value
 
 
 def spec_verify_reserve_host_io(ctx) -> None:
@@ -853,7 +863,8 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=No
     exponentials, [rows, q_heads] float32 (-inf where no key is seen), with which parts of an attention can be
     joined. out: tensors to write instead of new ones, in that order. Rows behind the last request's are left
     as they are. Runs on q's device, on `stream` or that device's current stream; the workspace is the call's own, so
-    calls may overlap. The exact rules stand at spec_verify_cache_attention in include/spec_verify.h."""
+    calls may overlap. Should the device lose a copy, rows get NaN and spec_verify_cache_last_error() is not 0. The exact
+    rules stand at spec_verify_cache_attention in include/spec_verify.h."""
     import torch
 
     T = _torch or _cache_torch()

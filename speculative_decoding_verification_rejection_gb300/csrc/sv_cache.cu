@@ -768,6 +768,25 @@ extern "C" int spec_verify_cache_attention(const spec_verify_cache_attention_arg
     return launch_after(kernel.join, static_cast<unsigned>(ctas), kJoinThreads, 0, stream, join);
 }
 
+extern "C" int spec_verify_cache_last_error(uint32_t *err_word)
+{
+    if (!err_word) return SV_EINVAL;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SV_EDEVICE;
+    }
+    const int rc = cache_device(dev);
+    if (rc != SV_OK) return rc;
+    const unsigned zero = 0;
+    unsigned w = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&w, g_cache_error, sizeof(w)) != cudaSuccess ||
+        (w && cudaMemcpyToSymbol(g_cache_error, &zero, sizeof(zero)) != cudaSuccess))
+        return SV_ECUDA;
+    *err_word = w;
+    return SV_OK;
+}
+
 #ifdef SV_DEBUG_BOUNDS
 // Of the checked build only: SV_ERR_BOUNDS in *word if a kernel of a cache operator that has ended tried an
 // access outside its call's arrays (the current device's; read and cleared).

@@ -60,6 +60,9 @@ struct Given {
 #endif
 };
 
+// SV_ERR_WAIT once some CTA of the device has given up.
+static __device__ unsigned g_cache_error;
+
 enum : int { kFirst = 1, kLast = 2, kPartial = 4, kSlot = 8, kOpen = 16, kEdge = 32 };
 
 // A tile is up to 128 keys. Both products have the keys or the elements in the 128 rows of the tensor cores' memory and
@@ -1185,6 +1188,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
         if (loads) asm volatile("cp.async.wait_all;" ::: "memory");
         if (warp == 8 || warp == 9) products_close(&sh.ended, elected());
         if (tid == 0) {
+            atomicOr(&g_cache_error, SV_ERR_WAIT);
             if constexpr (!loads) {
                 barrier_drain(kWide ? &sh.raw_full[0][0] : sh.k_full, kWide ? S::rooms : S::k_slots, sh.asked[0]);
                 barrier_drain(kWide ? &sh.raw_full[1][0] : sh.v_full, kWide ? S::rooms : S::v_slots, sh.asked[1]);

@@ -1,7 +1,8 @@
 """Run by tests/test_gpu_debug_cache.py in a child process whose library is the bounds-checked build
 (SPEC_VERIFY_DEBUG_BOUNDS=1), in which SV_DEBUG_PATIENCE says how often a wait of the cache attention looks
 before it is given up. From one look (nearly every CTA gives up at once) to many (none does) a call has to end, with each row
-and head either as it is in a call of full patience, bit for bit, or all NaN; the next call finds nothing changed.
+and head either as it is in a call of full patience, bit for bit, or all NaN, and an error word that says whether
+waits were given up; the next call finds nothing changed.
 Prints OK at the end."""
 import os
 import sys
@@ -58,12 +59,16 @@ if __name__ == "__main__":
             got = with_patience(looks, s, caches)
             torch.cuda.synchronize()
             lost = torch.isnan(got[1])
+            word = sv.spec_verify_cache_last_error()
+            assert word in (0, sv.SV_ERR_WAIT)
             for t, w in zip(got, want):
                 nan = torch.isnan(t).view(s.rows, s.hq, -1)
                 same = (t.view(torch.uint8) == w).view(s.rows, s.hq, -1).all(-1)
                 assert bool((same | nan.all(-1)).all()), f"{case}, {looks} looks: rows that are neither right nor NaN"
             again = with_patience(0, s, caches)
             assert all(torch.equal(t.view(torch.uint8), w) for t, w in zip(again, want)), f"{case}: the call after one of {looks} looks"
+            assert sv.spec_verify_cache_last_error() == 0
+            assert (word != 0) == bool((lost & ~whole[1]).any()), "every CTA that gives up has rows"
             seen.append(int((lost & ~whole[1]).sum()))
             looks = looks * 9 // 8 + 1
         print(f"{case}: {sorted(set(seen))} of {s.rows * s.hq} rows and heads given up", flush=True)

@@ -191,3 +191,13 @@ def test_axes_are_numbers_whatever_holds_them(kind, monkeypatch):
 def test_axes_that_are_no_axis_numbers_are_refused(axes, monkeypatch):
     with pytest.raises(ValueError):
         axes_sent(axes, monkeypatch)
+
+
+def test_error_word_of_the_cache_operators():
+    assert sv.lib().spec_verify_cache_last_error(None) == sv.SV_EINVAL
+    with open(sv._HEADER, encoding="utf-8") as f:
+        assert f"#define SV_ERR_WAIT {sv.SV_ERR_WAIT}u" in f.read()
+    if not torch.cuda.is_available():
+        with pytest.raises(sv.SpecVerifyError) as e:
+            sv.spec_verify_cache_last_error()
+        assert e.value.status == sv.SV_EDEVICE
