@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) sv_cache_append_kernel(cons
                 const int at = at0 + k * 32 + lane;
                 if (at < hi) {
                     const Where w = where(r, at);
-                    a[k] = ld_own(reinterpret_cast<const uint4 *>(w.from + w.m.first * 2));
-                    b[k] = ld_own(reinterpret_cast<const uint4 *>(w.from + w.m.second * 2));
+                    a[k] = ld(reinterpret_cast<const uint4 *>(w.from + w.m.first * 2));
+                    b[k] = ld(reinterpret_cast<const uint4 *>(w.from + w.m.second * 2));
                 }
             }
             if (at0 == lo) {

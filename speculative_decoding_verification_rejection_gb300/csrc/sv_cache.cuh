@@ -81,15 +81,10 @@ static __device__ __noinline__ bool inside(const void *p, unsigned bytes, bool o
 #define SV_CACHE_INSIDE(p, bytes, out) true
 #endif
 
+// Not by the read-only path: it is for memory that nobody writes while the kernel lives, and these kernels live before the work that
+// writes their inputs (lengths, prefix sums, the queries that an append has turned) has ended; and queries may be turned in place.
 template <typename T>
 __device__ __forceinline__ T ld(const T *p)
-{
-    if (!SV_CACHE_INSIDE(p, sizeof(T), false)) return T{};
-    return __ldg(p);
-}
-// Without the read-only path: memory that the kernel may write as well (queries turned in place).
-template <typename T>
-__device__ __forceinline__ T ld_own(const T *p)
 {
     if (!SV_CACHE_INSIDE(p, sizeof(T), false)) return T{};
     return *p;

@@ -1211,7 +1211,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) sv_cache_join_kernel(const AttentionParams P, int rows, float offset)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 a = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x)), b = ld_own(reinterpret_cast<const int4 *>(P.parts + blockIdx.x) + 1);
+    const int4 a = ld(reinterpret_cast<const int4 *>(P.parts + blockIdx.x)), b = ld(reinterpret_cast<const int4 *>(P.parts + blockIdx.x) + 1);
     const int first = a.x, last = a.y, row0 = a.w, from = b.x, count = b.y, head = b.z;
     if (first < 0) return;
     const int share = last - first, mine = static_cast<int>(blockIdx.x) - first, items = count * (D / 4);
@@ -1238,7 +1238,7 @@ __global__ void __launch_bounds__(kJoinThreads) sv_cache_join_kernel(const Atten
                 const i64 part = (static_cast<i64>(first + q) * 2 + (q == 0 ? a.z : 0)) * rows + r;
                 s[k] = make_float2(-kInf, 0);
                 v[k] = make_float4(0, 0, 0, 0);
-                if (q <= share) s[k] = ld_own(P.stats + part), v[k] = ld_own(reinterpret_cast<const float4 *>(P.sums + part * D + c));
+                if (q <= share) s[k] = ld(P.stats + part), v[k] = ld(reinterpret_cast<const float4 *>(P.sums + part * D + c));
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {

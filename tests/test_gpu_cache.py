@@ -584,3 +584,40 @@ def test_overlapping_requests_of_too_many_tiles_are_left_out():
     lengths.fill_(0)
     sv.cache_attention(q, pool, pool, table, lengths, cu_num_draft=cu, lse=True, out=[out, lse])
     assert bool((out[:2001] == 0).all()) and bool((out[4000:] == 7).all())
+
+
+@pytest.mark.parametrize("cache", ("bf16", "e4m3"))
+def test_steps_right_behind_what_writes_their_inputs(cache):
+    """Lengths, prefix sums and pages moved on by small kernels, queries turned in place, and their attention, one right behind the
+    other: as with a wait for the device after each."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    s = Step(90, [700, 3, 64, 1500], [2, 1, 3, 2], hq=8, hk=2, dim=128, cache=cache, page=16, layout="heads", spare=8)
+    inv = cuda(freqs(64))
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rows = torch.randn(40, 3, s.rows, s.hq, s.dim, generator=g, device="cuda").to(s.dtype)
+    tables = torch.stack([torch.randperm(s.n * s.width, generator=g, device="cuda").view(s.n, s.width) for _ in range(40)]).int()
+    sums = torch.stack((cuda(s.cu), torch.tensor([0, 0, 2, 3, 4], device="cuda"))).int()
+
+    def steps(wait):
+        pool = torch.zeros(s.n * s.width, s.page, s.hk, s.dim, device="cuda").to(s.kind)
+        k, v = pool, pool.clone()
+        lengths, table, cu = cuda(s.lengths), tables[0].clone(), sums[0].clone()
+        q, kk, vv = (torch.empty_like(rows[0, 0]) for _ in range(3))
+        got = []
+        for t in range(40):
+            for to, x in ((q, rows[t, 0]), (kk, rows[t, 1]), (vv, rows[t, 2]), (table, tables[t // 8]), (cu, sums[t % 2])):
+                to.copy_(x)
+                wait()
+            lengths.add_(1)
+            wait()
+            sv.cache_append(kk[:, :s.hk], vv[:, :s.hk], k, v, table, lengths, q=q, inv_freq=inv, cu_num_draft=cu, out=q)
+            wait()
+            got.append((q.clone(), *sv.cache_attention(q, k, v, table, lengths, cu_num_draft=cu, lse=True)))
+            wait()
+        return [x for step in got for x in step] + [k.view(torch.uint8), v.view(torch.uint8)]
+
+    want = steps(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(steps(lambda: None), want):
+            assert torch.equal(a, b)
