@@ -617,7 +617,7 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  *                   of pair m is that of axis axes[m] (axes a HOST array of rotary_dim / 2 bytes below
  *                   num_axes, read during the call; NULL: axis 0)
  *   k_scale, v_scale [num_kv_heads] binary32 or NULL, with SV_E4M3 only: what is stored is the
- *                   value times the reciprocal of the scale
+ *                   value divided by the scale (the binary32 quotient, rounded to 8 bits)
  *   head_dim a multiple of 16 up to SV_MAX_HEAD_DIM, rotary_dim one up to head_dim
  */
 typedef struct spec_verify_cache_append_args {

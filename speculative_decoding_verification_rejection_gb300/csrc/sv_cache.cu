@@ -77,12 +77,13 @@ __device__ __forceinline__ uint4 pack8(const float *x)
 {
     return make_uint4(pack<T>(x[0], x[1]), pack<T>(x[2], x[3]), pack<T>(x[4], x[5]), pack<T>(x[6], x[7]));
 }
-// 8 values times the reciprocal of their head's scale, rounded once.
-__device__ __forceinline__ uint2 pack8_e4m3(const float *x, float by)
+// 8 values, divided by their head's scale. (A product with its reciprocal is 5 % faster, 33.4 against 35.3 us for 4 x 2048 rows of 28 query
+// and 4 key heads of 128, but takes quotients that lie between two steps of 8 bits to the wrong one, and a subnormal scale to infinity.)
+__device__ __forceinline__ uint2 pack8_e4m3(const float *x, float scale)
 {
     uint32_t h[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = e4m3_of(x[2 * k] * by, x[2 * k + 1] * by);
+    for (int k = 0; k < 4; ++k) h[k] = e4m3_of(x[2 * k] / scale, x[2 * k + 1] / scale);
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
@@ -201,9 +202,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) sv_cache_append_kernel(cons
                 if (E4M3 && x.kind) {
                     unsigned char *const to = c.at + page * c.page + slot * c.slot + x.head * c.head;
                     const float *scales = x.kind == 2 ? P.v_scale : P.k_scale;
-                    const float by = scales ? 1.0f / ld(scales + x.head) : 1.0f;
-                    st(reinterpret_cast<uint2 *>(to + x.m.first), pack8_e4m3(y, by));
-                    st(reinterpret_cast<uint2 *>(to + x.m.second), pack8_e4m3(w, by));
+                    const float scale = scales ? ld(scales + x.head) : 1.0f;
+                    st(reinterpret_cast<uint2 *>(to + x.m.first), pack8_e4m3(y, scale));
+                    st(reinterpret_cast<uint2 *>(to + x.m.second), pack8_e4m3(w, scale));
                 } else {
                     unsigned char *const to = x.kind ? c.at + page * c.page + slot * c.slot + x.head * c.head : P.q_out + r * P.out_row + x.head * P.out_head;
                     st(reinterpret_cast<uint4 *>(to + x.m.first * 2), pack8<T>(y));

@@ -621,3 +621,21 @@ def test_steps_right_behind_what_writes_their_inputs(cache):
     for _ in range(3):
         for a, b in zip(steps(lambda: None), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("scale", (7 / 512, 13 / 512, 15 / 512, 61 / 512, 1.0, 0.75, 3e-3, -0.25, 2.0**-140, 1e30))
+def test_append_8_bits_divides_by_the_scale(scale):
+    """Every bfloat16 number as a value: what is stored is its quotient by the scale, rounded to 8 bits (with 7, 13, 15 and 61 / 512
+    some quotients are ties, which a product with the reciprocal misses; 2^-140 has no reciprocal)."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(32, 8, 256)
+    v = torch.where(torch.isnan(v), torch.zeros(()).bfloat16(), v)
+    by = torch.full((8,), scale)
+    k_cache, v_cache = (torch.zeros(4, 16, 8, 256, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    sv.cache_append(cuda(v), cuda(v), k_cache, v_cache, table, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                    cu_num_draft=torch.tensor([0, 31], dtype=torch.int32, device="cuda"), k_scale=cuda(by), v_scale=cuda(by))
+    want = (v.float() / by[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for cache in (k_cache, v_cache):   # (without frequencies nothing is turned)
+        assert torch.equal(torch.cat((cache[2], cache[0])).cpu().view(torch.uint8), want)
