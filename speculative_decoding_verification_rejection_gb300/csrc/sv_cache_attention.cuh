@@ -758,7 +758,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     const float top = larger(larger(larger(sh.most[0][tid], sh.most[1][tid]), larger(sh.most[2][tid], sh.most[3][tid])), old);
                     sh.factor[tid] = top == old ? 1.0f : exp2_fast(old - top);
                     sh.top[tid] = top;
-                    sh.less[tid] = top == -kInf ? 0x1p120f : W::offset - top;  // (no key yet: any score is far above)
+                    sh.less[tid] = top == -kInf ? 0x1.fffffep127f : W::offset - top;  // (no key yet: any score is far above, -1e38 too)
                 }
                 weights_meet();
                 if (!(flags & kFirst)) {
