@@ -478,16 +478,22 @@ int status_of(cudaError_t e)
     return SV_ECUDA;
 }
 
-// Pages below kSmallPage places vector by vector, others by tensor map (a copy costs its warp 40 to 90 cycles,
-// whatever its size: 128 requests with pages of 20 places 92 us against 101 by vectors, 64 requests of 6 rows with pages of 64
-// 345 against 396). 8 bits by tensor map (96 requests of 4 rows 142 against 150 us) where boxes start on 128 bytes and fill three quarters
-// of a tile: every place of a tile is widened, whether it holds a key or not.
-constexpr int kSmallPage = 16;
+// Places that a copy by tensor map brings to a tile: whole pages, or equal parts of a page above kTile.
+int parts_of(int page) { return (page + kTile - 1) / kTile; }
+int places_of(int page) { return page <= kTile ? kTile / page * page : (page + parts_of(page) - 1) / parts_of(page); }
+
+// Copies by tensor map from pages of kSmallPage places on that fill seven eighths of a tile, others vector by vector into whole tiles.
+// Measured, tensor map against vectors, us. 16 bits, 32 requests of 6 rows of heads of 128 over up to 16384 keys: pages of 4 places 300 / 225,
+// 6 239 / 225, 8 205 / 226, 12 216 / 225, 64 194 / 224, 72 299 / 225 and 96 238 / 225, 112 218 / 225, 200 (two parts of 100) 233 / 225,
+// 256 194 / 224; a window and heads of 64: 96 108 / 97, 112 97 / 98; heads of 256: 8 110 / 110, 16 93 / 111. 8 bits, 96 requests of 4 rows of heads of
+// 128: 4 173 / 147, 8 142 / 146, 32 132 / 143, 96 168 / 142, 112 152 / 142, 120 146 / 142, 128 133 / 143; 256 of one row: 96 584 / 552, 112 509 / 550, 128 457 / 549.
+// (Every place of a tile costs its share of the products, whether it holds a key or not, and each box its issue.) 8 bits also need boxes that start
+// on 128 bytes.
+constexpr int kSmallPage = 8;
 bool by_loads(const spec_verify_cache_attention_args &a)
 {
-    if (a.page_size < kSmallPage) return true;
-    if (a.cache_dtype != SV_E4M3 || a.page_size > kTile) return false;
-    return a.page_size * a.head_dim % 128 != 0 || kTile / a.page_size * a.page_size * 4 < kTile * 3;
+    if (a.page_size < kSmallPage || places_of(a.page_size) * 8 < kTile * 7) return true;
+    return a.cache_dtype == SV_E4M3 && a.page_size <= kTile && a.page_size * a.head_dim % 128 != 0;
 }
 
 // The kernel for a call. Query rows of a key head of one request (on average: the rows of each are known on the device
@@ -511,9 +517,8 @@ Cut cut_of(const spec_verify_cache_attention_args &a, const Kernel &k)
         while (group % q_box != 0) --q_box;
     }
     if (by_loads(a)) return Cut{kTile, 0, 1, kTile, q_box};
-    if (page <= kTile) return Cut{kTile / page * page, page, 1, kTile / page, q_box};
-    const int parts = (page + kTile - 1) / kTile, box = (page + parts - 1) / parts;
-    return Cut{box, box, parts, 1, q_box};
+    const int places = places_of(page);
+    return page <= kTile ? Cut{places, page, 1, kTile / page, q_box} : Cut{places, places, parts_of(page), 1, q_box};
 }
 
 // How many CTAs a call has: those that the device holds at once, or as many as there can be tiles.

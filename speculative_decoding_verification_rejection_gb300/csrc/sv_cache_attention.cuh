@@ -1121,7 +1121,7 @@ __global__ void __launch_bounds__((Tile<KIND, D, N, LOADS>::threads), 1) sv_cach
                     const auto &h = sh.head[it % S::heads];
                     if (lane == 0) barrier_expect(&sh.raw_full[values][r], P.cut.boxes * P.cut.box * D);
                     __syncwarp();
-                    if (lane < P.cut.boxes)  // (at most 8)
+                    if (lane < P.cut.boxes)  // (at most 16)
                         copy_box(shared_address(staging + (r * 2 + values) * (kTile * D) + lane * P.cut.box * D), values ? &maps.v : &maps.k, &sh.raw_full[values][r], 0, h.slot, h.head, h.page[lane]);
                 }
                 if (!kRaw && it < n) {

@@ -664,3 +664,13 @@ def test_a_first_key_far_below_after_tiles_without_one(cache, size, scale):
     assert bool(((out.double() - mean).abs() <= mean.abs() * 2.0**-8 + 2.0**-18).all())
     want = score + math.log(seen)
     assert float((lse.double() - want).abs().max()) <= abs(want) * 2.0**-21
+
+
+@pytest.mark.parametrize("page", (7, 8, 9, 11, 14, 15, 37, 111, 112, 125, 130, 223, 224, 249, 255, 500))
+@pytest.mark.parametrize("dim,cache", ((64, "bf16"), (128, "f16"), (256, "bf16"), (64, "e4m3"), (128, "e4m3"), (256, "e4m3")))
+def test_attention_pages_beside_the_border_of_the_two_ways_to_copy(page, dim, cache):
+    """Pages that just fill, or do not fill, seven eighths of a tile, in one part or several, and the smallest that tensor maps bring."""
+    dtype = "bf16" if cache == "e4m3" else cache
+    s = Step(page + dim, LENGTHS + [page * 2 - 1, 1300], NEW + [2, 5], hq=6, hk=2, dim=dim, dtype=dtype, cache=cache, page=page, layout="heads", spare=1)
+    check_attention(s)
+    check_attention(s, window=150)
