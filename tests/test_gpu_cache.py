@@ -643,9 +643,11 @@ def test_append_8_bits_divides_by_the_scale(scale):
         assert torch.equal(torch.cat((cache[2], cache[0])).cpu().view(torch.uint8), want)
 
 
+@pytest.mark.parametrize("group", (2, 16))
 @pytest.mark.parametrize("cache,size,scale", (("bf16", 2.0**60, 1.0), ("bf16", 2.0**60, 2.0**-126), ("e4m3", 2.0**110, 512.0)))
-def test_a_first_key_far_below_after_tiles_without_one(cache, size, scale):
-    """The keys of the first tiles are not there (bad pages); the first that is has a score of -2^126 (or, as little, -1)."""
+def test_a_first_key_far_below_after_tiles_without_one(cache, size, scale, group):
+    """The keys of the first tiles are not there (bad pages); the first that is has a score of -2^126 (or, as little, -1). With 16 query
+    heads to a key head the rows of a tile are all queries (others' scores of 0 would set a reference)."""
     import speculative_decoding_verification_rejection_gb300 as sv
 
     n, page, hk, dim, length = 64, 16, 2, 64, 600
@@ -655,11 +657,11 @@ def test_a_first_key_far_below_after_tiles_without_one(cache, size, scale):
     v = torch.randn(n, page, hk, dim, generator=g, device="cuda").to(TYPES[cache])
     table = torch.full((n, length // page + 1), -1, dtype=torch.int32, device="cuda")
     table[:, -1] = torch.arange(n, device="cuda")
-    q = torch.full((n, 2 * hk, dim), -size, device="cuda").bfloat16()
+    q = torch.full((n, group * hk, dim), -size, device="cuda").bfloat16()
     out, lse = sv.cache_attention(q, k, v, table, torch.full((n,), length, dtype=torch.int32, device="cuda"), scale=scale, lse=True)
     seen = length % page + 1      # all of the same score: their mean, each weight exactly 1
     score = -size * key * dim * scale
-    mean = v[:, :seen].double().mean(1).repeat_interleave(2, 1)
+    mean = v[:, :seen].double().mean(1).repeat_interleave(group, 1)
     # the output's rounding to bfloat16 (8 significant bits: half a step is 2^-8 of the value at most), on top of sums of nine terms below 5 in binary32
     assert bool(((out.double() - mean).abs() <= mean.abs() * 2.0**-8 + 2.0**-18).all())
     want = score + math.log(seen)
