@@ -582,8 +582,8 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  * graph; calls may overlap on any streams. Problems visible on the host return a status and launch
  * nothing; 0 rows or 0 requests are SV_OK.
  *   Left out, with nothing written for them: rows behind the last request's; a request whose rows
- *   are not all within num_rows (an inconsistent cu_num_draft; where requests overlap it is open whose
- *   a row is, and an attention with 2^31 tiles of keys or more for it is left out). A request of negative length takes no
+ *   are not all within num_rows (an inconsistent cu_num_draft; where requests overlap or the sums fall it is open
+ *   whose a row is, and an attention with 2^31 tiles of keys or more for it is left out). A request of negative length takes no
  *   part (a padded batch): nothing is appended and its queries are not turned; its attention
  *   outputs are those of rows that see no key. A key whose page is outside [0, num_pages), or whose
  *   place is not within pages_per_req pages, is not written, and not seen.

@@ -128,7 +128,7 @@ __device__ __forceinline__ int request_of(const Step &s, int r)
     }
     int first;
     const int count = request_rows(s, lo, first);
-    return lo < s.n && r >= first && r - first < count ? lo : -1;
+    return lo < s.n && count > 0 && r >= first && r - first < count ? lo : -1;  // (without rows `first` may be any number)
 }
 
 // Page and slot of place x of request i; false where it has none.

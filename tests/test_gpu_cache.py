@@ -676,3 +676,38 @@ def test_attention_pages_beside_the_border_of_the_two_ways_to_copy(page, dim, ca
     s = Step(page + dim, LENGTHS + [page * 2 - 1, 1300], NEW + [2, 5], hq=6, hk=2, dim=dim, dtype=dtype, cache=cache, page=page, layout="heads", spare=1)
     check_attention(s)
     check_attention(s, window=150)
+
+
+@pytest.mark.parametrize("cu", ([0, 1, 0, 5], [0, -3, 2, 5], [0, 2, 2**31 - 1, 5], [-2**31, 0, 1, 2], [0, 100, 100, 100], [7, 7, 7, 7]))
+def test_requests_that_inconsistent_prefix_sums_leave_are_right(cu):
+    """The requests whose rows are all within the batch are appended and attended for; nothing is written for other rows."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    s = Step(53, [10, 20, 30], [2, 1, 5], dim=64, spare=1)
+    s.table = torch.arange(s.n * s.width).int().view(s.n, s.width)
+    s.pool = s.n * s.width
+    g = torch.Generator().manual_seed(1)
+    s.k_cache, s.v_cache = (torch.randn(s.pool, s.page, s.hk, s.dim, generator=g).to(s.kind) for _ in range(2))
+    rows = s.rows
+    for i in range(s.n):
+        first, count = cu[i] + i, cu[i + 1] - cu[i] + 1
+        s.first[i], s.new[i] = first, count if cu[i] >= 0 and count >= 1 and first + count <= rows else 0
+    valid = [r for r, _, _ in s.rows_of()]
+    assert len(valid) == len(set(valid))
+    k, v = s.device_caches()
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    q = torch.full((rows, s.hq, s.dim), 5.0, dtype=s.dtype, device="cuda")
+    out, lse = torch.full_like(q, 5.0), torch.full((rows, s.hq), 5.0, device="cuda")
+    sv.cache_append(cuda(s.k), cuda(s.v), k, v, cuda(s.table), cuda(s.lengths), q=cuda(s.q), inv_freq=cuda(freqs(32)), cu_num_draft=bad, out=q)
+    others = [r for r in range(rows) if r not in valid]
+    (want_q, want_k, want_v), (qe, ke, ve) = ref_append(s, freqs(32))
+    off_by(k, want_k, ke, "k")     # (slots of no valid row as they were)
+    off_by(v, want_v, ve, "v")
+    off_by(q[valid], want_q[valid], qe[valid], "q")
+    assert bool((q[others] == 5).all())
+    s.k_cache, s.v_cache = k.cpu(), v.cpu()
+    sv.cache_attention(cuda(s.q), k, v, cuda(s.table), cuda(s.lengths), cu_num_draft=bad, lse=True, out=[out, lse])
+    (want, want_lse), (oe, le) = ref_attention(s)
+    off_by(out[valid], want[valid], oe[valid], "out")
+    off_by(lse[valid], want_lse[valid], le[valid], "lse")
+    assert bool((out[others] == 5).all()) and bool((lse[others] == 5).all())
