@@ -678,6 +678,72 @@ def test_attention_pages_beside_the_border_of_the_two_ways_to_copy(page, dim, ca
     check_attention(s, window=150)
 
 
+def long_runs(dim, hq, cache, page, whole):
+    """96 requests of 4 rows over up to 3100 keys (14 of them over fewer than 14) in pages that requests share: arguments of a call,
+    and keys and values as the requests see them, in 64 bits. `whole`: values are whole numbers from -8 to 8."""
+    n, width, new = 96, 3200 // page, 4
+    g = torch.Generator(device="cuda").manual_seed(dim + hq + page)
+    k = torch.randn(300, page, 1, dim, generator=g, device="cuda").to(TYPES[cache])
+    v = (torch.randint(-8, 9, k.shape, generator=g, device="cuda") if whole else torch.randn(k.shape, generator=g, device="cuda")).to(TYPES[cache])
+    table = torch.randint(0, 300, (n, width), generator=g, device="cuda").int()
+    lengths = torch.randint(0, 3100, (n,), generator=g, device="cuda").int()
+    lengths[::7] = torch.arange(14, device="cuda").int()
+    q = torch.randn(n * new, hq, dim, generator=g, device="cuda").bfloat16()
+    keys, values = (c[table.long()].float().view(n, -1, dim).double() for c in (k, v))
+    seen = torch.arange(width * page, device="cuda") <= lengths[:, None, None].long() + torch.arange(new, device="cuda")[:, None]
+    return (q, k, v, table, lengths), dict(cu_num_draft=torch.arange(n + 1, device="cuda").int() * (new - 1), lse=True), keys, values, seen
+
+
+RUNS = pytest.mark.parametrize("dim,hq", ((256, 8), (256, 16), (128, 8), (128, 12), (128, 16), (64, 24)))
+WAYS = pytest.mark.parametrize("cache,page", (("bf16", 32), ("e4m3", 32), ("bf16", 4), ("e4m3", 4)))
+
+
+@RUNS
+@WAYS
+def test_every_value_of_long_runs_of_tiles_counts_once(dim, hq, cache, page):
+    """With a scale of 0 every weight is the same power of two and sums of whole numbers are exact: an output is the mean of the values
+    but for a division and its rounding, and one value too many, too few or of another tile shows (by 1 / 3100 of a unit or more)."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    args, kw, _, values, seen = long_runs(dim, hq, cache, page, whole=True)
+    out, lse = sv.cache_attention(*args, scale=0.0, **kw)
+    count = seen.sum(-1)
+    want = (torch.einsum("nrt,ntd->nrd", seen.double(), values) / count[..., None])[:, :, None]
+    off = (out.view(96, 4, hq, dim).double() - want).abs()
+    # half a step of bfloat16, and a quotient and a product in binary32 before it
+    assert bool((off <= want.abs() * (2.0**-8 + 2.0**-21)).all())
+    assert float((lse.view(96, 4, hq).double() - count.double().log()[..., None]).abs().max()) <= 2.0**-19   # (log2 and a product, of numbers up to 12)
+
+
+@RUNS
+@WAYS
+def test_long_runs_of_tiles_element_by_element(dim, hq, cache, page):
+    """Every output within what its own weights' and scores' roundings allow, and three calls alike bit for bit."""
+    import speculative_decoding_verification_rejection_gb300 as sv
+
+    args, kw, keys, values, seen = long_runs(dim, hq, cache, page, whole=False)
+    out, lse = sv.cache_attention(*args, **kw)
+    for _ in range(2):
+        again = sv.cache_attention(*args, **kw)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    q = args[0].view(96, 4, hq, dim).double()
+    weight = 2.0**-8 if cache == "bf16" else 2.0**-11
+    many = (3200 / 8 + 32) * 2.0**-22
+    for i in range(96):
+        score = (q[i] @ keys[i].T * dim ** -0.5).masked_fill(~seen[i][:, None], -float("inf"))
+        p = torch.softmax(score, -1)
+        want, size, z = p @ values[i], p @ values[i].abs(), torch.logsumexp(score, -1)
+        # as in tests/_cache.py: a score's products added in units that may cut, its factor, the argument of 2^x; and its use in numerator and sum
+        terms = (q[i].abs() @ keys[i].abs().T).masked_fill(~seen[i][:, None], 0)
+        away = (terms * (dim * 2.0**-22) + (q[i].abs().amax(-1, keepdim=True) * keys[i].abs().sum(-1)).masked_fill(~seen[i][:, None], 0) * 2.0**-35).amax(-1) * dim ** -0.5
+        away = away + 3 * 2.0**-24 * torch.where(torch.isfinite(score), score.abs(), 0).amax(-1) + 2.0**-22
+        allowed = size * (weight + 2 * away[..., None] + 2 * many) * 1.01 + want.abs() * 2.0**-8 * 1.01
+        allowed = allowed + (seen[i].double() @ values[i].abs())[:, None] * 2.0**-36 * p.amax(-1, keepdim=True)
+        off = (out.view(96, 4, hq, dim)[i].double() - want).abs()
+        assert bool((off <= allowed).all()), f"request {i}: {float((off / allowed).max())} of the bound"
+        assert bool(((lse.view(96, 4, hq)[i].double() - z).abs() <= away + many + 2.0**-22 * z.abs()).all())
+
+
 @pytest.mark.parametrize("cu", ([0, 1, 0, 5], [0, -3, 2, 5], [0, 2, 2**31 - 1, 5], [-2**31, 0, 1, 2], [0, 100, 100, 100], [7, 7, 7, 7]))
 def test_requests_that_inconsistent_prefix_sums_leave_are_right(cu):
     """The requests whose rows are all within the batch are appended and attended for; nothing is written for other rows."""
