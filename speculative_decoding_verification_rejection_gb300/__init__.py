@@ -803,8 +803,6 @@ def cache_append(k, v, k_cache, v_cache, page_table, lengths, *, q=None, inv_fre
     Returns the turned queries [rows, q_heads, head_dim] (None without q): a new tensor, or `out`, which
     may be q itself. Runs on k's device, on `stream` or that device's current stream. The exact rules stand
     at spec_verify_cache_append in include/spec_verify.h."""
-    import torch
-
     T = _torch or _cache_torch()
     code = _rows_code("k", k)
     shape, dtype, index = k.shape, k.dtype, k.get_device()
@@ -865,8 +863,6 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, *, cu_num_draft=No
     as they are. Runs on q's device, on `stream` or that device's current stream; the workspace is the call's own, so
     calls may overlap. Should the device lose a copy, rows get NaN and spec_verify_cache_last_error() is not 0. The exact
     rules stand at spec_verify_cache_attention in include/spec_verify.h."""
-    import torch
-
     T = _torch or _cache_torch()
     code = _rows_code("q", q)
     shape, dtype, index = q.shape, q.dtype, q.get_device()
