@@ -625,7 +625,8 @@ def test_steps_right_behind_what_writes_their_inputs(cache):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("scale", (7 / 512, 13 / 512, 15 / 512, 61 / 512, 1.0, 0.75, 3e-3, -0.25, 2.0**-140, 1e30))
+@pytest.mark.parametrize("scale", (7 / 512, 13 / 512, 15 / 512, 61 / 512, 1.0, 0.75, 3e-3, -0.25, 2.0**-140, 1e30,
+                                   0.0371, -7 / 512, 1.7 * 2.0**99, 1.2 * 2.0**100, 1.3 * 2.0**-100, 1.7 * 2.0**-101, 2.0**-126, 2.0**126))
 def test_append_8_bits_divides_by_the_scale(scale):
     """Every bfloat16 number as a value: what is stored is its quotient by the scale, rounded to 8 bits (with 7, 13, 15 and 61 / 512
     some quotients are ties, which a product with the reciprocal misses; 2^-140 has no reciprocal)."""
