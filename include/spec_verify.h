@@ -602,8 +602,8 @@ int spec_verify_logprobs(const spec_verify_logprobs_args *args, void *cuda_strea
  * the queries. Pair m < rotary_dim / 2 of a head, elements (m, m + rotary_dim / 2) or with
  * interleaved (2 m, 2 m + 1), is turned by the angle a = pos * inv_freq[m]:
  * (y1, y2) = (x1 cos a - x2 sin a, x1 sin a + x2 cos a); elements from rotary_dim on stay as they
- * are. a is taken modulo a turn in fixed point (steps of 2^-64 of a turn; its error is below
- * 2^-47 |a| + 2^-29), so far positions lose little; sums and products are binary32, rounded once to the
+ * are. a is taken modulo a turn in fixed point (steps of 2^-64 of a turn) and then rounded to binary32 (its
+ * error is below 2^-47 |a| + 2^-23), so far positions lose little; sums and products are binary32, rounded once to the
  * element type. Values beyond 448 of an SV_E4M3 cache become 448, NaN stays NaN.
  *   q, q_out        [num_rows, num_q_heads, head_dim] of dtype (num_q_heads 0: none); q_out may be q
  *                   itself with the same strides

@@ -27,8 +27,8 @@ using namespace sv_cache;
 // its first elements before it looks for the row's request, page and position: warps do not wait for one another.
 //
 // The angle in turns, modulo one: pos * frac(inv_freq / 2 pi) with the fraction in steps of 2^-64, one
-// 64-bit product whose upper bits wrap away exactly the whole turns. A binary32 angle of position 10^6
-// would be off by 0.03 radians.
+// 64-bit product whose upper bits wrap away exactly the whole turns; what is left, 32 bits of a turn, is rounded to binary32 (by up to
+// pi 2^-25) for sine and cosine. A binary32 angle of position 10^6 would be off by 0.03 radians.
 struct AppendParams {
     Step s;
     const unsigned char *q, *k, *v;
